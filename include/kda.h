@@ -387,6 +387,219 @@ KDA_API int kda_decode_step_ex(const kda_dims_t* dims, const kda_prologue_t* pro
                        const void* k, const void* v, const float* log_a, const float* beta,
                        const float* S_in, float* S_out, void* o, void* stream);
 
+/* ------------------------------------------------------------------------- *
+ * Operators around the state layer: what a token-mixing block runs before and
+ * after it.  A block normalises the residual stream (kda_residual_norm), runs
+ * short causal convolutions over its projections (kda_conv), the state layer
+ * or its diagonal relative (kda_scan), and normalises and gates every head's
+ * output (kda_norm_gate).  The pages describe none of them.
+ *
+ * The conventions are those at the top of this file (device pointers owned by
+ * the caller, validation on the host before anything is enqueued, no
+ * allocation, no waiting), with these differences:
+ *   - Widths, head and channel counts are free (no powers of two), and a
+ *     pointer needs the alignment of its element only; a workspace needs 256
+ *     bytes.  Rows of 16-byte multiples at 16-byte addresses run fastest.
+ *   - Inputs that come out of a fused projection may be strided: a *_stride
+ *     is the distance between consecutive tokens in elements (0: contiguous),
+ *     at least the token's own size.  Outputs are contiguous.
+ *   - total_tokens (for kda_norm_gate tokens x heads) and num_seqs go up to
+ *     2147418112, channels up to 16777216; element offsets are 64-bit.
+ *   - With cu_seqlens, tokens at or past cu_seqlens[num_seqs] belong to no
+ *     sequence: they are not read, and their rows of the outputs are left as
+ *     they were.  Offsets outside [0, total_tokens] are clamped into it.
+ *   - Outputs must not overlap inputs or each other except where said.
+ *   - Sums, norms and states are held in fp32; an output is rounded once.
+ *     Reductions run in a fixed order: a call repeats bit for bit.
+ * ------------------------------------------------------------------------- */
+
+/*
+ * Diagonal gated linear recurrence over packed sequences: the state layer's
+ * gate on a state of one value per channel,
+ *     h_t = a_t h_{t-1} + x_t,   a_t = exp(log_a_t),   y_t = h_t.
+ * log_a is <= 0 (not checked; -INFINITY forgets the state).  A non-finite value
+ * stays in its own sequence and channel.
+ */
+typedef struct {
+    int32_t num_seqs;      /* N */
+    int32_t channels;      /* C >= 1 */
+    int64_t total_tokens;  /* T over all sequences (kda_scan_step: T == N) */
+    int32_t dtype;         /* kda_dtype_t of x, y, dy and dx; log_a, dlog_a and the states are float32 */
+    int32_t reserved;      /* 0 */
+    int64_t x_stride, log_a_stride, dy_stride;  /* token strides of the inputs, 0 = C */
+} kda_scan_dims_t;
+
+/* Tokens between two rows of `states` below. */
+#define KDA_SCAN_STATE_EVERY 64
+
+/*
+ *   x          [T, C] dtype;  log_a [T, C] float32
+ *   h0         [N, C] float32 initial states, or NULL for zeros
+ *   cu_seqlens as for kda_chunk_fwd (NULL: N sequences of T / N tokens)
+ *   y          [T, C] dtype
+ *   h_T        [N, C] float32 final states, or NULL to skip (an empty sequence's is its h0)
+ *   states     [ceil(T / 64), C] float32, or NULL: row r is the state before
+ *              token 64 r of the packed axis, i.e. after token 64 r - 1, of
+ *              whichever sequence that token belongs to (row 0 and rows behind
+ *              the last sequence: unspecified).  kda_scan_bwd takes them.
+ *   workspace  kda_scan_workspace_size bytes (0: may be NULL)
+ */
+KDA_API int kda_scan_fwd(const kda_scan_dims_t* dims, const void* x, const float* log_a, const float* h0,
+                         const int32_t* cu_seqlens, void* y, float* h_T, float* states, void* workspace,
+                         size_t workspace_bytes, void* stream);
+
+/*
+ * Gradient of kda_scan_fwd for upstream derivatives dy and dh_T.  With
+ * g_t = dy_t + a_{t+1} g_{t+1} (at a sequence's last token dy_t + dh_T):
+ *     dx_t = g_t,   dlog_a_t = g_t a_t h_{t-1},   dh0 = a_1 g_1.
+ *   x, log_a, h0, cu_seqlens   the forward inputs
+ *   states     as kda_scan_fwd wrote them for these inputs, or NULL: the states
+ *              are computed again (one more pass over x and log_a)
+ *   dy         [T, C] dtype;  dh_T [N, C] float32, or NULL for zeros
+ *   dx         [T, C] dtype;  dlog_a [T, C] float32
+ *   dh0        [N, C] float32, or NULL to skip
+ */
+KDA_API int kda_scan_bwd(const kda_scan_dims_t* dims, const void* x, const float* log_a, const float* h0,
+                         const int32_t* cu_seqlens, const float* states, const void* dy, const float* dh_T,
+                         void* dx, float* dlog_a, float* dh0, void* workspace, size_t workspace_bytes,
+                         void* stream);
+
+/* Workspace of kda_scan_fwd (backward = 0) or kda_scan_bwd (1; enough with or without states). */
+KDA_API int kda_scan_workspace_size(const kda_scan_dims_t* dims, int backward, size_t* bytes);
+
+/* One token per sequence: h_out = exp(log_a) h_in + x, y = h_out.  x, log_a [N, C], h_in and
+ * h_out [N, C] float32; h_out may equal h_in. */
+KDA_API int kda_scan_step(const kda_scan_dims_t* dims, const void* x, const float* log_a, const float* h_in,
+                          float* h_out, void* y, void* stream);
+
+/* Activation of kda_conv and of kda_norm_gate's gate. */
+typedef enum {
+    KDA_ACT_NONE = 0,     /* kda_conv only */
+    KDA_ACT_SILU = 1,     /* z / (1 + e^-z) */
+    KDA_ACT_SIGMOID = 2   /* 1 / (1 + e^-z); kda_norm_gate only */
+} kda_act_t;
+
+/*
+ * Short causal depthwise convolution over packed sequences, the usual step
+ * between the q, k and v projections and the state layer.  With W taps,
+ *     z_t[c] = bias[c] + sum_{j < W} weight[c][j] x_{t - W + 1 + j}[c],   y_t = act(z_t),
+ * where the tokens before a sequence's first are the W - 1 rows of its state
+ * (oldest first).  A sequence's state after it is the last W - 1 rows of its
+ * state followed by its tokens.
+ */
+typedef struct {
+    int32_t num_seqs;      /* N */
+    int32_t channels;      /* C >= 1 */
+    int64_t total_tokens;  /* T (kda_conv_step: T == N) */
+    int32_t dtype;         /* kda_dtype_t of x, y, the states and their derivatives; weight, bias, dweight, dbias: float32 */
+    int32_t width;         /* W: 2, 3 or 4 */
+    int32_t activation;    /* KDA_ACT_NONE or KDA_ACT_SILU */
+    int32_t reserved;      /* 0 */
+    int64_t x_stride, dy_stride;  /* token strides of the inputs, 0 = C */
+} kda_conv_dims_t;
+
+/*
+ *   x          [T, C] dtype
+ *   weight     [C, W] float32;  bias [C] float32, or NULL for zeros
+ *   state      [N, W - 1, C] dtype, or NULL for zeros
+ *   cu_seqlens as for kda_chunk_fwd
+ *   y          [T, C] dtype
+ *   state_T    [N, W - 1, C] dtype, or NULL to skip; must not overlap state
+ */
+KDA_API int kda_conv_fwd(const kda_conv_dims_t* dims, const void* x, const float* weight, const float* bias,
+                         const void* state, const int32_t* cu_seqlens, void* y, void* state_T, void* stream);
+
+/*
+ * Gradient of kda_conv_fwd for upstream derivatives dy [T, C] and dstate_T
+ * [N, W - 1, C] (dtype; NULL for zeros).  Writes dx [T, C] dtype, dweight [C, W]
+ * and dbias [C] float32 (either NULL to skip), dstate [N, W - 1, C] dtype (NULL to
+ * skip).  Needs kda_conv_bwd_workspace_size bytes of workspace.
+ */
+KDA_API int kda_conv_bwd(const kda_conv_dims_t* dims, const void* x, const float* weight, const float* bias,
+                         const void* state, const int32_t* cu_seqlens, const void* dy, const void* dstate_T,
+                         void* dx, float* dweight, float* dbias, void* dstate, void* workspace,
+                         size_t workspace_bytes, void* stream);
+KDA_API int kda_conv_bwd_workspace_size(const kda_conv_dims_t* dims, size_t* bytes);
+
+/* One token per sequence: y [N, C] from x [N, C] and state_in, and the state after it; state_out may
+ * equal state_in. */
+KDA_API int kda_conv_step(const kda_conv_dims_t* dims, const void* x, const float* weight, const float* bias,
+                          const void* state_in, void* state_out, void* y, void* stream);
+
+/*
+ * RMS norm of every (token, head) row times a gate, the usual step after the
+ * state layer:
+ *     y = x / sqrt(mean(x^2) + eps) * weight * act(gate),
+ * the mean over the row's D values.  Without a gate it is a plain RMS norm.
+ */
+typedef struct {
+    int64_t tokens;        /* T */
+    int32_t heads;         /* H >= 1 */
+    int32_t width;         /* D: 1 to 8192 */
+    int32_t dtype;         /* kda_dtype_t of x, gate, y and their derivatives; weight and dweight: float32 */
+    int32_t activation;    /* KDA_ACT_SILU or KDA_ACT_SIGMOID; read only with a gate */
+    float eps;             /* >= 0, finite */
+    int32_t reserved;      /* 0 */
+    int64_t x_stride, gate_stride, dy_stride;  /* token strides of the inputs, 0 = H D (heads are adjacent) */
+} kda_norm_gate_dims_t;
+
+/*   x, gate, y [T, H, D] dtype (gate NULL: none);  weight [D] float32, or NULL for ones.  y may equal x. */
+KDA_API int kda_norm_gate_fwd(const kda_norm_gate_dims_t* dims, const void* x, const float* weight,
+                              const void* gate, void* y, void* stream);
+
+/*
+ * Gradient of kda_norm_gate_fwd for dy [T, H, D]: dx [T, H, D] dtype, dgate
+ * [T, H, D] dtype (NULL exactly if gate is), dweight [D] float32 (NULL to skip; the
+ * sum over tokens and heads).  Needs kda_norm_gate_bwd_workspace_size bytes of
+ * workspace when dweight is given (else it may be NULL).
+ */
+KDA_API int kda_norm_gate_bwd(const kda_norm_gate_dims_t* dims, const void* x, const float* weight,
+                              const void* gate, const void* dy, void* dx, void* dgate, float* dweight,
+                              void* workspace, size_t workspace_bytes, void* stream);
+KDA_API int kda_norm_gate_bwd_workspace_size(const kda_norm_gate_dims_t* dims, size_t* bytes);
+
+/*
+ * Residual sum and the next block's RMS norm in one pass:
+ *     h = residual + scale channel_scale x,   y = h / sqrt(mean(h^2) + eps) * weight,
+ * per token, the mean over its D values.  h is rounded to residual_out; y is
+ * taken from the unrounded sum.
+ */
+typedef struct {
+    int64_t tokens;          /* T */
+    int32_t width;           /* D: 1 to 8192 */
+    int32_t dtype;           /* kda_dtype_t of x, y, dy and dx */
+    int32_t residual_dtype;  /* kda_dtype_t of residual, residual_out and their derivatives:
+                                dtype, or KDA_F32 with a bf16 dtype */
+    float eps;               /* >= 0, finite */
+    float scale;             /* finite */
+    int32_t reserved;        /* 0 */
+    int64_t x_stride, residual_stride, dy_stride, dresidual_stride;  /* of the inputs, 0 = D */
+} kda_residual_norm_dims_t;
+
+/*   x [T, D] dtype;  residual [T, D] residual_dtype;  weight [D] float32;  channel_scale [D] float32,
+ *   or NULL for ones;  residual_out [T, D] residual_dtype, may equal residual;  y [T, D] dtype. */
+KDA_API int kda_residual_norm_fwd(const kda_residual_norm_dims_t* dims, const void* x, const void* residual,
+                                  const float* weight, const float* channel_scale, void* residual_out, void* y,
+                                  void* stream);
+
+/*
+ * Gradient at the stored sum: residual_out as the forward wrote it, upstream
+ * derivatives dy [T, D] dtype and dresidual_out [T, D] residual_dtype (NULL for
+ * zeros; what the stream receives from later blocks).  With dh the sum's
+ * derivative from both, writes
+ *   dx              [T, D] dtype, scale channel_scale dh
+ *   dresidual       [T, D] residual_dtype, dh
+ *   dweight         [D] float32, or NULL to skip
+ *   dchannel_scale  [D] float32, or NULL to skip; needs x (which may be NULL otherwise)
+ * Needs kda_residual_norm_bwd_workspace_size bytes of workspace when dweight or
+ * dchannel_scale is given.
+ */
+KDA_API int kda_residual_norm_bwd(const kda_residual_norm_dims_t* dims, const void* x, const void* residual_out,
+                                  const float* weight, const float* channel_scale, const void* dy,
+                                  const void* dresidual_out, void* dx, void* dresidual, float* dweight,
+                                  float* dchannel_scale, void* workspace, size_t workspace_bytes, void* stream);
+KDA_API int kda_residual_norm_bwd_workspace_size(const kda_residual_norm_dims_t* dims, size_t* bytes);
+
 /* Static text for a status code. */
 KDA_API const char* kda_status_string(int status);
 

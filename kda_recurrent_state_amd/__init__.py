@@ -15,6 +15,10 @@ Shapes (tokens of all sequences packed along the first axis):
     q, k [T, H, dk]; v [T, H, dv]; log_a [T, H, dk] (KDA) or [T, H] (Gated
     DeltaNet); beta [T, H]; states [N, H, dk, dv] float32.  q/k/v are bf16 or
     fp32 (o has the same dtype); log_a, beta and states are fp32.
+
+The operators that a token-mixing block runs around the layer (short
+convolution, diagonal recurrence, gated and residual norms) are in ``block.py``
+and exported here as well.
 """
 from __future__ import annotations
 
@@ -133,6 +137,7 @@ def load_library(build_if_missing: bool = True):
             lib.kda_last_error.restype = ctypes.c_char_p
             lib.kda_last_error.argtypes = []
             lib.kda_version.restype = ctypes.c_int
+            block._declare(lib)
             _lib = lib
         return _lib
 
@@ -537,3 +542,10 @@ def decode_step(q, k, v, log_a, beta, S, *, out=None, S_out=None, order: int = O
                                  _ptr(S), _ptr(So), _ptr(o), _stream_handle(q.device))
     _check(lib, st)
     return o, So
+
+
+# the operators around the state layer (block.py uses the helpers above)
+from . import block  # noqa: E402
+from .block import *  # noqa: E402,F401,F403
+
+__all__ += block.__all__

@@ -8,12 +8,12 @@
 
 #include <math.h>
 #include <mutex>
-#include <stdarg.h>
 #include <stdint.h>
 #include <stdio.h>
 #include <string.h>
 
 #include "../../include/kda.h"
+#include "kda_error.hpp"
 #include "kda_launch.hpp"
 
 // Scratch of kda_chunk_fwd_noalloc (the two-pass workspace of a caller that
@@ -22,23 +22,12 @@
 // only the per-device address from hipGetSymbolAddress, never this name.
 static __device__ __align__(256) uint8_t scratch[KDA_NOALLOC_SCRATCH_BYTES];
 
+using kda::check_ptrs;
+using kda::fail;
+using kda::g_last_error;
+using kda::ok;
+
 namespace {
-
-thread_local char g_last_error[256] = "";
-
-int fail(int status, const char* fmt, ...) __attribute__((format(printf, 2, 3)));
-int fail(int status, const char* fmt, ...) {
-    va_list ap;
-    va_start(ap, fmt);
-    vsnprintf(g_last_error, sizeof(g_last_error), fmt, ap);
-    va_end(ap);
-    return status;
-}
-
-int ok() {
-    g_last_error[0] = '\0';
-    return KDA_OK;
-}
 
 bool aligned16(const void* p) { return ((uintptr_t)p & 15u) == 0; }
 
@@ -59,16 +48,6 @@ int check_dims(const kda_dims_t* d) {
         return fail(KDA_ERR_INVALID_ARGUMENT, "order = %d is not a kda_order_t", d->order);
     if (!width_ok(d->dk) || !width_ok(d->dv))
         return fail(KDA_ERR_UNSUPPORTED, "dk = %d, dv = %d: each must be 16, 32, 64 or 128", d->dk, d->dv);
-    return KDA_OK;
-}
-
-// Non-null pointers with the alignment the kernels' vector accesses need.
-int check_ptrs(const void* const* ptrs, const char* const* names, const int* align, int count) {
-    for (int i = 0; i < count; ++i) {
-        if (!ptrs[i]) return fail(KDA_ERR_INVALID_ARGUMENT, "%s is NULL", names[i]);
-        if ((uintptr_t)ptrs[i] % (uintptr_t)align[i])
-            return fail(KDA_ERR_MISALIGNED, "%s is not %d-byte aligned", names[i], align[i]);
-    }
     return KDA_OK;
 }
 

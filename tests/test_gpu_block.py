@@ -1,0 +1,702 @@
+"""The operators around the state layer on the GPU against their float64
+definitions (tests/block_ref.py, which also derives every tolerance)."""
+import pytest
+import torch
+
+import kda_recurrent_state_amd as kda
+from tests import block_ref as R
+from tests.parity import TOL, log, max_rel_err
+
+pytestmark = pytest.mark.gpu
+DEV = "cuda:0"
+F8, F4, BF = torch.float64, torch.float32, torch.bfloat16
+DTYPES = [F4, BF]
+
+
+def rnd(seed):
+    g = torch.Generator().manual_seed(seed)
+    return lambda *s: torch.randn(*s, generator=g, dtype=F4)
+
+
+def dev(t, dtype=None):
+    return None if t is None else t.to(DEV, dtype or t.dtype)
+
+
+def slice_of(t):
+    """The same values as the middle of a wider tensor (a fused projection)."""
+    wide = torch.full((t.shape[0], 3) + tuple(t.shape[1:]), 7.0, dtype=t.dtype, device=t.device)
+    wide[:, 1] = t
+    return wide[:, 1]
+
+
+def cu_of(lengths, extra=0):
+    return torch.tensor(R.bounds_of(lengths), dtype=torch.int32, device=DEV)
+
+
+LENS = {
+    "one": [1],
+    "short": [1] * 70,
+    "edges": [0, 1, 0, 5, 64, 63, 65, 0, 0, 2, 128, 1, 0],
+    "long": [333],
+    "pair": [192, 192],
+    "ragged": [250, 3, 517, 130],
+}
+
+
+# ------------------------------------------------------------------ diagonal recurrence
+
+def scan_inputs(lengths, C, dtype, seed):
+    r = rnd(seed)
+    T, N = sum(lengths), len(lengths)
+    x = r(T, C).to(dtype)
+    la = -torch.nn.functional.softplus(r(T, C) * 2).clamp(max=8)
+    la[:, ::3] *= 0.01  # long memories
+    return x, la, r(N, C), r(T, C).to(dtype), r(N, C)
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("C", [1, 3, 64, 130, 257])
+@pytest.mark.parametrize("lens", LENS)
+def test_scan_against_reference(lens, C, dtype):
+    lengths = LENS[lens]
+    log(f"scan {lens} C={C} {dtype}")
+    cu, cud = R.bounds_of(lengths), cu_of(lengths)
+    x, la, h0, dy, dhT = scan_inputs(lengths, C, dtype, 11)
+    val, bnd = R.scan(x.double(), la.double(), h0.double(), cu)
+    xd, lad, h0d, dyd, dhTd = map(dev, (x, la, h0, dy, dhT))
+    y, hT, states = kda.scan_fwd_states(xd, lad, h0d, cud)
+    w = [R.check(y, val["y"], bnd["y"], "y"), R.check(hT, val["h"], bnd["h"], "h_T")]
+    y2, hT2 = kda.scan_fwd(slice_of(xd), slice_of(lad), h0d, cud)
+    assert torch.equal(y2, y) and torch.equal(hT2, hT)
+    gval, gbnd = R.scan_grad(x.double(), la.double(), h0.double(), cu, dy.double(), dhT.double())
+    got = kda.scan_bwd(xd, lad, dyd, h0d, cud, dhTd, states=states)
+    w += [R.check(got[k], gval[k], gbnd[k], k) for k in ("dx", "dlog_a", "dh0")]
+    again = kda.scan_bwd(slice_of(xd), slice_of(lad), slice_of(dyd), h0d, cud, dhTd)
+    assert all(torch.equal(again[k], got[k]) for k in got)  # with and without the kept states, bit for bit
+    log("  share of the allowed error: " + " ".join(f"{v:.2f}" for v in w))
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+def test_scan_defaults(dtype):
+    """No initial state, equal lengths without offsets, no final state wanted, no
+    derivative of it, no derivative of the initial one."""
+    log(f"scan defaults {dtype}")
+    C, N, L = 66, 3, 70
+    x, la, _, dy, _ = scan_inputs([L] * N, C, dtype, 12)
+    zero = torch.zeros(N, C, dtype=F8)
+    cu = R.bounds_of([L] * N)
+    val, bnd = R.scan(x.double(), la.double(), zero, cu)
+    y, hT = kda.scan_fwd(dev(x), dev(la), num_seqs=N, final_state=False)
+    assert hT is None
+    R.check(y, val["y"], bnd["y"], "y")
+    gval, gbnd = R.scan_grad(x.double(), la.double(), zero, cu, dy.double(), zero)
+    got = kda.scan_bwd(dev(x), dev(la), dev(dy), num_seqs=N, initial_state_grad=False)
+    assert got["dh0"] is None
+    for k in ("dx", "dlog_a"):
+        R.check(got[k], gval[k], gbnd[k], k)
+    y1, h1 = kda.scan_fwd(dev(x), dev(la))  # one sequence
+    val, bnd = R.scan(x.double(), la.double(), zero[:1], [0, L * N])
+    R.check(y1, val["y"], bnd["y"], "y of one")
+    R.check(h1, val["h"], bnd["h"], "h of one")
+
+
+def test_scan_empty():
+    log("scan empty")
+    z = torch.zeros(0, 5, device=DEV)
+    h0 = torch.randn(3, 5, device=DEV)
+    cu = torch.zeros(4, dtype=torch.int32, device=DEV)
+    y, hT = kda.scan_fwd(z, z, h0, cu)
+    assert y.shape == (0, 5) and torch.equal(hT, h0)
+    g = kda.scan_bwd(z, z, z, None, cu, h0)
+    assert torch.equal(g["dh0"], h0)
+    assert torch.equal(kda.scan_bwd(z, z, z, None, cu)["dh0"], torch.zeros_like(h0))
+    y, hT = kda.scan_fwd(z, z, torch.zeros(0, 5, device=DEV), cu[:1])
+    assert hT.shape == (0, 5)
+
+
+@pytest.mark.parametrize("bad", [float("inf"), float("nan")])
+def test_scan_sequences_stay_apart(bad):
+    """A non-finite value reaches nothing but the rest of its own sequence and channel."""
+    log(f"scan isolation {bad}")
+    lengths = [40, 30, 0, 100, 70]
+    cu = R.bounds_of(lengths)
+    x, la, h0, dy, dhT = scan_inputs(lengths, 8, F4, 13)
+    ok_y, ok_h = kda.scan_fwd(*map(dev, (x, la, h0)), cu_of(lengths))
+    ok_g = kda.scan_bwd(*map(dev, (x, la, dy, h0)), cu_of(lengths), dev(dhT))
+    x2, dy2, h02 = x.clone(), dy.clone(), h0.clone()
+    x2[20, 3] = bad          # sequence 0, channel 3
+    dy2[cu[3] + 50, 5] = bad  # sequence 3, channel 5
+    h02[4, 6] = bad          # sequence 4, channel 6
+    y, h = kda.scan_fwd(*map(dev, (x2, la, h02)), cu_of(lengths))
+    touched = torch.zeros_like(y, dtype=torch.bool)
+    touched[20:40, 3] = True
+    touched[cu[4]:cu[5], 6] = True
+    assert torch.equal(y[~touched], ok_y[~touched]) and not torch.isfinite(y[20:40, 3]).any()
+    hm = torch.zeros_like(h, dtype=torch.bool)
+    hm[0, 3] = hm[4, 6] = True
+    assert torch.equal(h[~hm], ok_h[~hm])
+    g = kda.scan_bwd(*map(dev, (x, la, dy2, h0)), cu_of(lengths), dev(dhT))
+    touched = torch.zeros_like(y, dtype=torch.bool)
+    touched[cu[3]:cu[3] + 51, 5] = True
+    assert torch.equal(g["dx"][~touched], ok_g["dx"][~touched])
+    assert torch.equal(g["dlog_a"][~touched], ok_g["dlog_a"][~touched])
+
+
+def test_scan_forgets_at_minus_infinity():
+    log("scan -inf")
+    x, la, h0, dy, dhT = scan_inputs([150], 6, F4, 14)
+    la[77, 2] = float("-inf")
+    la[0, 1] = float("-inf")
+    cu = [0, 150]
+    val, bnd = R.scan(x.double(), la.double(), h0.double(), cu)
+    y, hT, st = kda.scan_fwd_states(*map(dev, (x, la, h0)))
+    R.check(y, val["y"], bnd["y"], "y")
+    gval, gbnd = R.scan_grad(x.double(), la.double(), h0.double(), cu, dy.double(), dhT.double())
+    got = kda.scan_bwd(*map(dev, (x, la, dy, h0)), None, dev(dhT), states=st)
+    for k in ("dx", "dlog_a", "dh0"):
+        R.check(got[k], gval[k], gbnd[k], k)
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("rows", [1, 90])
+def test_rows_behind_the_last_sequence(dtype, rows):
+    """Tokens past the last offset are neither read nor written."""
+    log(f"tail rows {dtype} {rows}")
+    lengths, C = [30, 41], 9
+    T = 71 + rows
+    x, la, h0, dy, dhT = scan_inputs([T], C, dtype, 15)
+    h0, dhT = h0.repeat(2, 1), dhT.repeat(2, 1)
+    x[71:], la[71:], dy[71:] = float("nan"), float("nan"), float("nan")
+    cu = cu_of(lengths)
+    out = torch.full((T, C), 3.0, dtype=dtype, device=DEV)
+    y, hT = kda.scan_fwd(*map(dev, (x, la, h0)), cu, out=out)
+    y0, h00 = kda.scan_fwd(dev(x[:71]), dev(la[:71]), dev(h0), cu)
+    assert torch.equal(y[:71], y0) and torch.equal(hT, h00) and bool((out[71:] == 3.0).all())
+    g = kda.scan_bwd(*map(dev, (x, la, dy, h0)), cu, dev(dhT))
+    g0 = kda.scan_bwd(dev(x[:71]), dev(la[:71]), dev(dy[:71]), dev(h0), cu, dev(dhT))
+    assert torch.equal(g["dx"][:71], g0["dx"]) and torch.equal(g["dlog_a"][:71], g0["dlog_a"])
+    assert torch.equal(g["dh0"], g0["dh0"])
+    r = rnd(16)
+    w, b, st, dst = r(C, 4), r(C), r(2, 3, C).to(dtype), r(2, 3, C).to(dtype)
+    out.fill_(3.0)
+    y, sT = kda.conv_fwd(dev(x), dev(w), dev(b), dev(st), cu, out=out)
+    y0, sT0 = kda.conv_fwd(dev(x[:71]), dev(w), dev(b), dev(st), cu)
+    assert torch.equal(y[:71], y0) and torch.equal(sT, sT0) and bool((out[71:] == 3.0).all())
+    g = kda.conv_bwd(dev(x), dev(w), dev(dy), dev(b), dev(st), cu, dev(dst))
+    g0 = kda.conv_bwd(dev(x[:71]), dev(w), dev(dy[:71]), dev(b), dev(st), cu, dev(dst))
+    assert torch.equal(g["dx"][:71], g0["dx"]) and torch.equal(g["dstate"], g0["dstate"])
+    vals = R.conv_grad(x[:71].double(), w.double(), b.double(), st.double(), R.bounds_of(lengths), True,
+                       dy[:71].double(), dst.double())
+    for k in ("dweight", "dbias"):
+        R.check(g[k], vals[0][k], vals[1][k], k)
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+def test_scan_step_chain(dtype):
+    """A chain of steps is the recurrence of one packed call; in place and not."""
+    log(f"scan step {dtype}")
+    N, C, L = 5, 77, 9
+    x, la, h0, _, _ = scan_inputs([L] * N, C, dtype, 17)
+    h0 = h0[:N]
+    val, bnd = R.scan(x.double(), la.double(), h0.double(), R.bounds_of([L] * N))
+    xs, las = x.view(N, L, C), la.view(N, L, C)
+    h, ys = dev(h0), []
+    for t in range(L):
+        xt, lt = slice_of(dev(xs[:, t].contiguous())), dev(las[:, t].contiguous())
+        if t % 2:
+            y, h2 = kda.scan_step(xt, lt, h, h_out=torch.empty_like(h))
+            assert h2.data_ptr() != h.data_ptr()
+            h = h2
+        else:
+            y, h = kda.scan_step(xt, lt, h)
+        ys.append(y)
+    R.check(torch.stack(ys, 1).reshape(N * L, C), val["y"], bnd["y"], "y")
+    R.check(h, val["h"], bnd["h"], "h")
+
+
+def test_scan_continues_from_its_final_state():
+    log("scan continuation")
+    x, la, h0, _, _ = scan_inputs([700], 40, F4, 18)
+    val, bnd = R.scan(x.double(), la.double(), h0.double(), [0, 700])
+    h, parts = dev(h0), []
+    for a, b in ((0, 100), (100, 101), (101, 640), (640, 700)):
+        y, h = kda.scan_fwd(dev(x[a:b]), dev(la[a:b]), h)
+        parts.append(y)
+    R.check(torch.cat(parts), val["y"], bnd["y"], "y")
+    R.check(h, val["h"], bnd["h"], "h")
+
+
+# ------------------------------------------------------------------ short convolution
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("W", [2, 3, 4])
+@pytest.mark.parametrize("C,silu", [(1, True), (7, False), (64, True), (130, False), (521, True)])
+@pytest.mark.parametrize("lens", LENS)
+def test_conv_against_reference(lens, C, silu, W, dtype):
+    lengths = LENS[lens]
+    log(f"conv {lens} C={C} W={W} silu={silu} {dtype}")
+    r = rnd(21)
+    T, N = sum(lengths), len(lengths)
+    cu, cud = R.bounds_of(lengths), cu_of(lengths)
+    x, w, b, st = r(T, C).to(dtype), r(C, W), r(C), r(N, W - 1, C).to(dtype)
+    dy, dst = r(T, C).to(dtype), r(N, W - 1, C).to(dtype)
+    act = "silu" if silu else None
+    f8 = [t.double() for t in (x, w, b, st)]
+    val, bnd = R.conv(*f8, cu, silu)
+    xd, wd, bd, sd, dyd, dsd = map(dev, (x, w, b, st, dy, dst))
+    y, sT = kda.conv_fwd(xd, wd, bd, sd, cud, activation=act)
+    worst = [R.check(y, val["y"], bnd["y"], "y")]
+    assert torch.equal(sT.cpu().double(), val["state"])
+    y2, sT2 = kda.conv_fwd(slice_of(xd), wd, bd, sd, cud, activation=act)
+    assert torch.equal(y2, y) and torch.equal(sT2, sT)
+    gval, gbnd = R.conv_grad(*f8, cu, silu, dy.double(), dst.double())
+    g = kda.conv_bwd(xd, wd, dyd, bd, sd, cud, dsd, activation=act)
+    worst += [R.check(g[k], gval[k], gbnd[k], k) for k in ("dx", "dweight", "dbias", "dstate")]
+    g2 = kda.conv_bwd(slice_of(xd), wd, slice_of(dyd), bd, sd, cud, dsd, activation=act)
+    assert all(torch.equal(g2[k], g[k]) for k in g)
+    log("  share of the allowed error: " + " ".join(f"{v:.2f}" for v in worst))
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+def test_conv_defaults_and_step(dtype):
+    """No bias, no states, equal lengths; then the steps from the final state."""
+    log(f"conv defaults {dtype}")
+    r = rnd(22)
+    N, L, C, W = 3, 50, 66, 4
+    x, w = r(N, L + 6, C).to(dtype), r(C, W)
+    zero, zst = torch.zeros(C, dtype=F8), torch.zeros(N, W - 1, C, dtype=F8)
+    full = x.reshape(-1, C)
+    val, bnd = R.conv(full.double(), w.double(), zero, zst, R.bounds_of([L + 6] * N), True)
+    yv, yb = val["y"].view(N, L + 6, C), bnd["y"].view(N, L + 6, C)
+    y, none = kda.conv_fwd(dev(x[:, :L].reshape(-1, C)), dev(w), num_seqs=N, final_state=False)
+    assert none is None
+    y, st = kda.conv_fwd(dev(x[:, :L].reshape(-1, C)), dev(w), num_seqs=N)
+    R.check(y.view(N, L, C), yv[:, :L], yb[:, :L], "y")
+    for t in range(L, L + 6):
+        xt = slice_of(dev(x[:, t].contiguous()))
+        if t % 2:
+            y, st = kda.conv_step(xt, dev(w), st, state_out=torch.empty_like(st))
+        else:
+            y, st = kda.conv_step(xt, dev(w), st)
+        R.check(y, yv[:, t], yb[:, t], f"step {t}")
+    assert torch.equal(st.cpu(), x[:, -3:])
+    dy = r(N * L, C).to(dtype)
+    gval, gbnd = R.conv_grad(x[:, :L].reshape(-1, C).double(), w.double(), zero, zst, R.bounds_of([L] * N), True,
+                             dy.double(), zst)
+    g = kda.conv_bwd(dev(x[:, :L].reshape(-1, C)), dev(w), dev(dy), num_seqs=N, initial_state_grad=False)
+    assert g["dstate"] is None
+    for k in ("dx", "dweight", "dbias"):
+        R.check(g[k], gval[k], gbnd[k], k)
+
+
+def test_conv_empty():
+    log("conv empty")
+    C, W = 6, 3
+    z, w = torch.zeros(0, C, device=DEV), torch.randn(C, W, device=DEV)
+    st = torch.randn(2, W - 1, C, device=DEV)
+    cu = torch.zeros(3, dtype=torch.int32, device=DEV)
+    y, sT = kda.conv_fwd(z, w, None, st, cu)
+    assert y.shape == (0, C) and torch.equal(sT, st)
+    g = kda.conv_bwd(z, w, z, None, st, cu, st)
+    assert torch.equal(g["dstate"], st) and not g["dweight"].any() and not g["dbias"].any()
+    g = kda.conv_bwd(z, w, z, None, st[:0], cu[:1])
+    assert g["dstate"].shape == (0, W - 1, C) and not g["dweight"].any()
+
+
+def test_conv_sequences_stay_apart():
+    log("conv isolation")
+    r = rnd(23)
+    lengths, C, W = [40, 2, 30, 1, 60], 8, 4
+    cu, cud = R.bounds_of(lengths), cu_of(lengths)
+    x, w, b, st, dy = r(133, C), r(C, W), r(C), r(5, W - 1, C), r(133, C)
+    args = [dev(t) for t in (x, w, b, st)]
+    ok, _ = kda.conv_fwd(*args, cud)
+    okg = kda.conv_bwd(args[0], args[1], dev(dy), args[2], args[3], cud)
+    x[39] = float("nan")  # the last token of sequence 0
+    y, _ = kda.conv_fwd(dev(x), *args[1:], cud)
+    assert torch.equal(y[:39], ok[:39]) and torch.equal(y[40:], ok[40:]) and torch.isnan(y[39]).all()
+    g = kda.conv_bwd(dev(x), args[1], dev(dy), args[2], args[3], cud)
+    assert torch.equal(g["dx"][:36], okg["dx"][:36]) and torch.equal(g["dx"][40:], okg["dx"][40:])
+
+
+# ------------------------------------------------------------------ norms
+
+WIDTHS = [1, 3, 16, 17, 32, 64, 83, 128, 200, 256, 300, 512, 600, 1024, 1500, 2048, 4100, 8192]
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("D", WIDTHS)
+@pytest.mark.parametrize("act", ["sigmoid", "silu", None])
+def test_norm_gate_against_reference(D, act, dtype):
+    log(f"norm_gate D={D} {act} {dtype}")
+    r = rnd(31)
+    T, H = (37, 3) if D <= 300 else (5, 1 if D > 2048 else 2)
+    eps = 1e-6
+    x = (r(T, H, D) * torch.exp(r(T, H, 1))).to(dtype)
+    x[1, 0] = 0  # a row of zeros
+    w, dy = 1 + 0.3 * r(D), r(T, H, D).to(dtype)
+    gt = None if act is None else (r(T, H, D) * 3).to(dtype)
+    kw = dict(activation=act or "sigmoid", eps=eps)
+    g8 = None if gt is None else gt.double()
+    yv, yb = R.norm_gate(x.double(), w.double(), g8, act, eps)
+    xd, wd, gd, dyd = map(dev, (x, w, gt, dy))
+    y = kda.norm_gate_fwd(xd, wd, gd, **kw)
+    worst = [R.check(y, yv, yb, "y")]
+    sg = None if gd is None else slice_of(gd)
+    assert torch.equal(kda.norm_gate_fwd(slice_of(xd), wd, sg, **kw), y)
+    inplace = xd.clone()
+    assert kda.norm_gate_fwd(inplace, wd, gd, out=inplace, **kw) is inplace and torch.equal(inplace, y)
+    val, bnd = R.norm_gate_grad(x.double(), w.double(), g8, act, eps, dy.double())
+    g = kda.norm_gate_bwd(xd, wd, dyd, gd, **kw)
+    assert (g["dgate"] is None) == (act is None)
+    worst += [R.check(g[k], val[k], bnd[k], k) for k in val]
+    g2 = kda.norm_gate_bwd(slice_of(xd), wd, slice_of(dyd), sg, **kw)
+    assert all(g[k] is None or torch.equal(g2[k], g[k]) for k in g)
+    log("  share of the allowed error: " + " ".join(f"{v:.2f}" for v in worst))
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+def test_norm_gate_without_weight_many_rows(dtype):
+    log(f"norm_gate rows {dtype}")
+    r = rnd(32)
+    x, gt, dy = r(700, 9, 24).to(dtype), r(700, 9, 24).to(dtype), r(700, 9, 24).to(dtype)
+    one = torch.ones(24)
+    y = kda.norm_gate_fwd(dev(x), None, dev(gt), activation="silu")
+    assert torch.equal(y, kda.norm_gate_fwd(dev(x), dev(one), dev(gt), activation="silu"))
+    g = kda.norm_gate_bwd(dev(x), None, dev(dy), dev(gt), activation="silu")
+    h = kda.norm_gate_bwd(dev(x), dev(one), dev(dy), dev(gt), activation="silu")
+    assert g["dweight"] is None and torch.equal(g["dx"], h["dx"]) and torch.equal(g["dgate"], h["dgate"])
+    val, bnd = R.norm_gate_grad(x.double(), one.double(), gt.double(), "silu", 1e-6, dy.double())
+    for k in val:
+        R.check(h[k], val[k], bnd[k], k)
+    z = torch.zeros(0, 9, 24, dtype=dtype, device=DEV)
+    assert kda.norm_gate_fwd(z, dev(one)).shape == z.shape
+    assert not kda.norm_gate_bwd(z, dev(one), z)["dweight"].any()
+
+
+@pytest.mark.parametrize("dtype,rdtype", [(F4, F4), (BF, BF), (BF, F4)])
+@pytest.mark.parametrize("D", WIDTHS)
+def test_residual_norm_against_reference(D, dtype, rdtype):
+    log(f"residual_norm D={D} {dtype} {rdtype}")
+    r = rnd(41)
+    T = 37 if D <= 300 else 5
+    x, res, w, cs = r(T, D).to(dtype), (3 * r(T, D)).to(rdtype), 1 + 0.3 * r(D), 0.7 + 0.2 * r(D)
+    dy, dres = r(T, D).to(dtype), r(T, D).to(rdtype)
+    xd, rd, wd, cd, dyd, drd = map(dev, (x, res, w, cs, dy, dres))
+    for c, cdev in ((None, None), (cs, cd)):
+        kw = dict(scale=0.5, channel_scale=cdev, eps=1e-5)
+        c8 = None if c is None else c.double()
+        val, bnd = R.residual_norm(x.double(), res.double(), w.double(), 0.5, c8, 1e-5)
+        y, h = kda.residual_norm_fwd(xd, rd, wd, **kw)
+        R.check(y, val["y"], bnd["y"], "y")
+        R.check(h, val["residual"], bnd["residual"], "residual")
+        inplace = rd.clone()
+        y2, h2 = kda.residual_norm_fwd(slice_of(xd), inplace, wd, residual_out=inplace, **kw)
+        assert h2 is inplace and torch.equal(h2, h) and torch.equal(y2, y)
+        y3, h3 = kda.residual_norm_fwd(xd, slice_of(rd), wd, **kw)
+        assert torch.equal(h3, h) and torch.equal(y3, y)
+        h8 = h.cpu().double()
+        gv, gb = R.residual_norm_grad(x.double(), h8, w.double(), 0.5, c8, 1e-5, dy.double(), dres.double())
+        g = kda.residual_norm_bwd(xd, h, wd, dyd, drd, **kw)
+        worst = [R.check(g[k], gv[k], gb[k], k) for k in gv]
+        assert (g["dchannel_scale"] is None) == (c is None)
+        g2 = kda.residual_norm_bwd(slice_of(xd), slice_of(h), wd, slice_of(dyd), slice_of(drd), **kw)
+        assert all(g[k] is None or torch.equal(g2[k], g[k]) for k in g)
+        log("  share of the allowed error: " + " ".join(f"{v:.2f}" for v in worst))
+    zero = torch.zeros_like(res)
+    g = kda.residual_norm_bwd(None, rd, wd, dyd, scale=2.0)
+    gv, gb = R.residual_norm_grad(x.double(), res.double(), w.double(), 2.0, None, 1e-6, dy.double(), zero.double())
+    for k in gv:
+        R.check(g[k], gv[k], gb[k], k)
+
+
+def test_norms_many_rows_column_sums():
+    """More rows than the backward has row groups: every group sums several."""
+    log("norm column sums")
+    r = rnd(42)
+    T, D = 9000, 40
+    x, h, w, dy = r(T, D), r(T, D), r(D), r(T, D)
+    gv, gb = R.residual_norm_grad(x.double(), h.double(), w.double(), 1.0, w.double(), 1e-6, dy.double(),
+                                  torch.zeros(T, D, dtype=F8))
+    g = kda.residual_norm_bwd(dev(x), dev(h), dev(w), dev(dy), channel_scale=dev(w))
+    for k in gv:
+        R.check(g[k], gv[k], gb[k], k)
+    z = torch.zeros(0, D, device=DEV)
+    g = kda.residual_norm_bwd(z, z, dev(w), z, channel_scale=dev(w))
+    assert not g["dweight"].any() and not g["dchannel_scale"].any()
+
+
+# ------------------------------------------------------------------ one tree of calls
+
+def calls(dtype=BF):
+    """Every operator once, on one set of inputs: a list of functions returning tensors."""
+    r = rnd(51)
+    lengths, C, H = [300, 0, 77, 130], 96, 3
+    T, N = sum(lengths), len(lengths)
+    cu = cu_of(lengths)
+    x, dy = dev(r(T, C), dtype), dev(r(T, C), dtype)
+    la = dev(-r(T, C).abs())
+    h0, dh = dev(r(N, C)), dev(r(N, C))
+    w4, b, st = dev(r(C, 4)), dev(r(C)), dev(r(N, 3, C), dtype)
+    x3, g3, d3, w3 = x.view(T, H, 32), dev(r(T, H, 32), dtype), dy.view(T, H, 32), dev(r(32))
+    w, cs = dev(r(C)), dev(r(C))
+    flat = lambda o: [t for t in (o.values() if isinstance(o, dict) else o if isinstance(o, tuple) else [o])]
+    return [
+        lambda: flat(kda.scan_fwd_states(x, la, h0, cu)),
+        lambda: flat(kda.scan_bwd(x, la, dy, h0, cu, dh)),
+        lambda: flat(kda.scan_step(x[:N], la[:N], h0, h_out=torch.empty_like(h0))),
+        lambda: flat(kda.conv_fwd(x, w4, b, st, cu)),
+        lambda: flat(kda.conv_bwd(x, w4, dy, b, st, cu, st)),
+        lambda: flat(kda.conv_step(x[:N], w4, st, b, state_out=torch.empty_like(st))),
+        lambda: flat(kda.norm_gate_fwd(x3, w3, g3)),
+        lambda: flat(kda.norm_gate_bwd(x3, w3, d3, g3)),
+        lambda: flat(kda.residual_norm_fwd(x, dy, w, channel_scale=cs)),
+        lambda: flat(kda.residual_norm_bwd(x, dy, w, x, dy, channel_scale=cs)),
+    ]
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+def test_calls_repeat_bit_for_bit(dtype):
+    log(f"determinism {dtype}")
+    for i, f in enumerate(calls(dtype)):
+        first = f()
+        for _ in range(3):
+            assert all(torch.equal(a, b) for a, b in zip(first, f())), i
+
+
+def test_calls_captured_and_replayed():
+    """Each call captured in a graph replays bit-identical to the eager call, with
+    eager work between the replays; two graphs hold the same operator."""
+    log("graphs")
+    for i, f in enumerate(calls()):
+        want = [t.clone() for t in f()]
+        s = torch.cuda.Stream()
+        s.wait_stream(torch.cuda.current_stream())
+        graphs = []
+        with torch.cuda.stream(s):
+            for _ in range(2):
+                g = torch.cuda.CUDAGraph()
+                with torch.cuda.graph(g, stream=s):
+                    out = f()
+                graphs.append((g, out))
+        torch.cuda.current_stream().wait_stream(s)
+        for _ in range(3):
+            for g, out in graphs:
+                for t in out:
+                    t.fill_(5)
+                junk = f()
+                torch.cuda.synchronize()
+                g.replay()
+                torch.cuda.synchronize()
+                assert all(torch.equal(a, b) for a, b in zip(want, out)), i
+                del junk
+
+
+def test_calls_on_two_streams():
+    log("streams")
+    fs = calls()
+    want = [[t.clone() for t in f()] for f in fs]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    got = []
+    for _ in range(3):
+        for s in streams:
+            with torch.cuda.stream(s):
+                got.append([f() for f in fs])
+    torch.cuda.synchronize()
+    for run in got:
+        for i, (a, b) in enumerate(zip(want, run)):
+            assert all(torch.equal(p, q) for p, q in zip(a, b)), i
+
+
+def test_offsets_past_32_bits():
+    """More than 2^31 elements: the last sequence's rows equal those of the
+    sequence by itself."""
+    log("64-bit offsets")
+    C, L = 4096, 256
+    T = (1 << 31) // C + 2 * L
+    g = torch.Generator(device=DEV).manual_seed(3)
+    x = torch.randn(T, C, generator=g, device=DEV, dtype=BF)
+    la = -torch.rand(T, C, generator=g, device=DEV)
+    cu = torch.tensor([0, T - L, T], dtype=torch.int32, device=DEV)
+    one = torch.tensor([0, L], dtype=torch.int32, device=DEV)
+    y, hT = kda.scan_fwd(x, la, None, cu)
+    y1, h1 = kda.scan_fwd(x[-L:], la[-L:], None, one)
+    assert torch.equal(y[-L:], y1) and torch.equal(hT[1], h1[0])
+    del y
+    got = kda.scan_bwd(x, la, x, None, cu)
+    g1 = kda.scan_bwd(x[-L:], la[-L:], x[-L:], None, one)
+    assert torch.equal(got["dx"][-L:], g1["dx"]) and torch.equal(got["dlog_a"][-L:], g1["dlog_a"])
+    assert torch.equal(got["dh0"][1], g1["dh0"][0])
+    del got, la
+    w = torch.randn(C, 4, generator=g, device=DEV)
+    y, sT = kda.conv_fwd(x, w, None, None, cu)
+    y1, s1 = kda.conv_fwd(x[-L:], w, None, None, one)
+    assert torch.equal(y[-L:], y1) and torch.equal(sT[1], s1[0])
+    got = kda.conv_bwd(x, w, x, None, None, cu)["dx"]
+    g1 = kda.conv_bwd(x[-L:], w, x[-L:], None, None, one)["dx"]
+    assert torch.equal(got[-L:], g1)
+    wn = torch.randn(128, generator=g, device=DEV)
+    x3 = x.view(T, 32, 128)
+    y = kda.norm_gate_fwd(x3, wn, x3)
+    assert torch.equal(y[-L:], kda.norm_gate_fwd(x3[-L:], wn, x3[-L:]))
+    got = kda.norm_gate_bwd(x3, wn, x3, x3)
+    g1 = kda.norm_gate_bwd(x3[-L:], wn, x3[-L:], x3[-L:])
+    assert torch.equal(got["dx"][-L:], g1["dx"]) and torch.equal(got["dgate"][-L:], g1["dgate"])
+    wr = torch.randn(C, generator=g, device=DEV)
+    y, h = kda.residual_norm_fwd(x, x, wr)
+    y1, h1 = kda.residual_norm_fwd(x[-L:], x[-L:], wr)
+    assert torch.equal(y[-L:], y1) and torch.equal(h[-L:], h1)
+
+
+# ------------------------------------------------------------------ the operators together
+
+def rel(a, b):
+    return float((a.detach().cpu().double() - b).norm() / b.norm())
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+def test_a_block_forward_and_backward(dtype):
+    """One token-mixing block as a user runs it: residual norm, convolutions on the
+    projections, the state layer with its prologue, the gated norm, the output
+    projection; then its gradient back to the residual stream, against autograd of
+    the same block in float64, and every new operator on the tensors it met there
+    against its own definition.
+
+    End to end, max|error| / max|value|: the state layer's bar b (TOL) bounds its
+    output's error; the gated norm's gradient reads that output twice (its scale
+    and its direction), which may double the share; the state layer's backward
+    adds another b; six more tensors are stored in between, half a step each.
+    Together 3 b + 6 half steps."""
+    log(f"block {dtype}")
+    from kda_recurrent_state_amd import METHOD_AUTO
+    r = rnd(61)
+    lengths, H, d, D = [70, 1, 45], 2, 32, 48
+    T, N, C = sum(lengths), len(lengths), 64
+    cud, cu = cu_of(lengths), R.bounds_of(lengths)
+    q = lambda t: t.to(dtype)
+    x, res = q(r(T, D)), r(T, D)
+    wn, wg, cs = 1 + 0.1 * r(D), 1 + 0.1 * r(d), 0.5 + 0.1 * r(D)
+    Wp, Wo = q(r(D, 4 * C) * D ** -0.5), q(r(C, D) * C ** -0.5)
+    wc, bc = [r(C, 4) * 0.5 for _ in range(3)], [0.1 * r(C) for _ in range(3)]
+    la, beta = r(T, H, d), r(T, H)
+    dout = q(r(T, D))
+    pro = dict(normalize_k=True, beta_logits=True, log_a_raw=True, log_a_min=-8.0)
+
+    # float64, by definition
+    leaf = lambda t: t.double().requires_grad_(True)
+    X, RS, WN, WG, CS, WP, WO, LA, BE = map(leaf, (x, res, wn, wg, cs, Wp, Wo, la, beta))
+    WC, BC = list(map(leaf, wc)), list(map(leaf, bc))
+    h = RS + 0.7 * CS * X
+    n = h / torch.sqrt((h * h).mean(-1, keepdim=True) + 1e-6) * WN
+    p = (n @ WP).view(T, 4, C)
+    qkv = []
+    for i in range(3):
+        seqs = []
+        for s, e in zip(cu[:-1], cu[1:]):
+            ext = torch.cat([torch.zeros(3, C, dtype=F8), p[s:e, i]])
+            z = sum(WC[i][:, j] * ext[j:j + e - s] for j in range(4)) + BC[i]
+            seqs.append(z / (1 + torch.exp(-z)))
+        qkv.append(torch.cat(seqs).view(T, H, d))
+    Q, K, V = qkv
+    K = K / torch.sqrt((K * K).sum(-1, keepdim=True) + 1e-6)
+    A = torch.exp((-torch.nn.functional.softplus(LA)).clamp(min=-8.0))
+    B = torch.sigmoid(BE)
+    rows = []
+    for s, e in zip(cu[:-1], cu[1:]):
+        S = torch.zeros(H, d, d, dtype=F8)
+        for t in range(s, e):
+            k, v = K[t][:, :, None], V[t][:, None, :]
+            S = A[t][:, :, None] * (S - B[t][:, None, None] * k @ (k.transpose(1, 2) @ S)) \
+                + B[t][:, None, None] * k @ v
+            rows.append((Q[t][:, None, :] @ S)[:, 0])
+    O = torch.stack(rows)
+    G = p[:, 3].view(T, H, d)
+    Y = O / torch.sqrt((O * O).mean(-1, keepdim=True) + 1e-6) * WG * torch.sigmoid(G)
+    OUT = Y.reshape(T, C) @ WO
+    leaves = [X, RS, WN, WG, CS, LA, BE, *WC, *BC]
+    want = torch.autograd.grad(OUT, leaves, dout.double())
+
+    # the kernels
+    xd, rd, wnd, wgd, csd, Wpd, Wod, lad, bed, dod = map(dev, (x, res, wn, wg, cs, Wp, Wo, la, beta, dout))
+    wcd, bcd = list(map(dev, wc)), list(map(dev, bc))
+    nd, hd = kda.residual_norm_fwd(xd, rd, wnd, scale=0.7, channel_scale=csd)
+    pd = nd @ Wpd  # one fused projection, its parts read in place
+    part = [pd[:, i * C:(i + 1) * C] for i in range(4)]
+    qkvd = [kda.conv_fwd(part[i], wcd[i], bcd[i], cu_seqlens=cud)[0].view(T, H, d) for i in range(3)]
+    od, _ = kda.chunk_fwd(*qkvd, lad, bed, cu_seqlens=cud, prologue=pro, method=METHOD_AUTO)
+    gd = part[3].unflatten(1, (H, d))
+    yd = kda.norm_gate_fwd(od, wgd, gd)
+    outd = yd.view(T, C) @ Wod
+    tol = 3 * TOL[dtype] + 6 * R.HALF[dtype]
+    assert max_rel_err(outd, OUT.detach()) <= tol
+    dyd = (dod @ Wod.t()).view(T, H, d)
+    gn = kda.norm_gate_bwd(od, wgd, dyd, gd)
+    gk = kda.chunk_bwd(*qkvd, lad, bed, gn["dx"], cu_seqlens=cud, prologue=pro, initial_state_grad=False)
+    gc = [kda.conv_bwd(part[i], wcd[i], gk[k].view(T, C), bcd[i], cu_seqlens=cud) for i, k in
+          enumerate(("dq", "dk", "dv"))]
+    dp = torch.cat([g["dx"] for g in gc] + [gn["dgate"].view(T, C)], 1)
+    gr = kda.residual_norm_bwd(xd, hd, wnd, dp @ Wpd.t(), None, scale=0.7, channel_scale=csd)
+    got = [gr["dx"], gr["dresidual"], gr["dweight"], gn["dweight"], gr["dchannel_scale"], gk["dlog_a"], gk["dbeta"],
+           *[g["dweight"] for g in gc], *[g["dbias"] for g in gc]]
+    for i, (a, b) in enumerate(zip(got, want)):
+        e = max_rel_err(a, b)
+        log(f"  gradient {i}: {e:.2e}")
+        assert e <= tol, (i, e)
+
+    # stage by stage, on what each stage was given
+    f8 = lambda t: t.detach().cpu().double()
+    v, bd = R.residual_norm(f8(xd), f8(rd), f8(wnd), 0.7, f8(csd), 1e-6)
+    R.check(nd, v["y"], bd["y"], "residual norm")
+    R.check(hd, v["residual"], bd["residual"], "residual sum")
+    zero = torch.zeros(N, 3, C, dtype=F8)
+    for i, k in enumerate(("dq", "dk", "dv")):
+        a = (f8(part[i]), f8(wcd[i]), f8(bcd[i]), zero, cu, True)
+        v, bd = R.conv(*a)
+        R.check(qkvd[i].view(T, C), v["y"], bd["y"], "convolution")
+        v, bd = R.conv_grad(*a, f8(gk[k].view(T, C)), zero)
+        for j in v:
+            R.check(gc[i][j], v[j], bd[j], "convolution " + j)
+    R.check(yd, *R.norm_gate(f8(od), f8(wgd), f8(gd), "sigmoid", 1e-6), "gated norm")
+    v, bd = R.norm_gate_grad(f8(od), f8(wgd), f8(gd), "sigmoid", 1e-6, f8(dyd))
+    for j in v:
+        R.check(gn[j], v[j], bd[j], "gated norm " + j)
+    v, bd = R.residual_norm_grad(f8(xd), f8(hd), f8(wnd), 0.7, f8(csd), 1e-6, f8(dp @ Wpd.t()),
+                                 torch.zeros(T, D, dtype=F8))
+    for j in v:
+        R.check(gr[j], v[j], bd[j], "residual norm " + j)
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+def test_a_recurrent_block_prefill_then_steps(dtype):
+    """Norm, convolution, diagonal recurrence and gated norm: a prefill followed by
+    single tokens from the states it leaves equals one prefill over all tokens."""
+    log(f"recurrent block {dtype}")
+    r = rnd(62)
+    N, L, C, H = 3, 90, 64, 2
+    x, la, g = r(N, L, C).to(dtype), -r(N, L, C).abs() * 0.3, r(N, L, C).to(dtype)
+    w, wc, b, wg = 1 + 0.1 * r(C), r(C, 4) * 0.5, r(C), 1 + 0.1 * r(32)
+    wd, wcd, bd, wgd = map(dev, (w, wc, b, wg))
+
+    def prefill(a, e):
+        n = kda.norm_gate_fwd(dev(x[:, a:e].reshape(-1, 1, C)), wd).view(-1, C)
+        c, cs = kda.conv_fwd(n, wcd, bd, num_seqs=N)
+        h, hT = kda.scan_fwd(c, dev(la[:, a:e].reshape(-1, C)), num_seqs=N)
+        y = kda.norm_gate_fwd(h.view(-1, H, 32), wgd, dev(g[:, a:e].reshape(-1, H, 32)), activation="silu")
+        return y.view(N, e - a, C), cs, hT
+
+    full, cs_full, hT_full = prefill(0, L)
+    y, cs, hT = prefill(0, L - 5)
+    # the recurrence joins its tokens in tiles of the packed axis, where the shorter
+    # sequences lie elsewhere: fp32 sums in another order, and a stored value that may
+    # round the other way (a whole step of its type, relative) in two tensors
+    step = 4 * R.HALF[BF] if dtype is BF else 2 ** -18
+    assert rel(y, full[:, :L - 5].cpu().double()) <= step
+    for t in range(L - 5, L):
+        n = kda.norm_gate_fwd(dev(x[:, t].reshape(N, 1, C)), wd).view(N, C)
+        c, cs = kda.conv_step(n, wcd, cs, bd)
+        h, hT = kda.scan_step(c, dev(la[:, t].contiguous()), hT)
+        y = kda.norm_gate_fwd(h.view(N, H, 32), wgd, dev(g[:, t].reshape(N, H, 32).contiguous()), activation="silu")
+        assert rel(y.view(N, C), full[:, t].cpu().double()) <= step
+    assert torch.equal(cs, cs_full)
+    assert rel(hT, hT_full.cpu().double()) <= step
