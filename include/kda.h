@@ -406,8 +406,8 @@ KDA_API int kda_decode_step_ex(const kda_dims_t* dims, const kda_prologue_t* pro
  *   - total_tokens (for kda_norm_gate tokens x heads) and num_seqs go up to
  *     2147418112, channels up to 16777216; element offsets are 64-bit.
  *   - With cu_seqlens, tokens at or past cu_seqlens[num_seqs] belong to no
- *     sequence: they are not read, and their rows of the outputs are left as
- *     they were.  Offsets outside [0, total_tokens] are clamped into it.
+ *     sequence: what they hold does not matter, and their rows of the outputs
+ *     are left as they were.  Offsets outside [0, total_tokens] are clamped into it.
  *   - Outputs must not overlap inputs or each other except where said.
  *   - Sums, norms and states are held in fp32; an output is rounded once.
  *     Reductions run in a fixed order: a call repeats bit for bit.
@@ -442,7 +442,9 @@ typedef struct {
  *              token 64 r of the packed axis, i.e. after token 64 r - 1, of
  *              whichever sequence that token belongs to (row 0 and rows behind
  *              the last sequence: unspecified).  kda_scan_bwd takes them.
- *   workspace  kda_scan_workspace_size bytes (0: may be NULL)
+ *   workspace  kda_scan_workspace_size bytes (0: may be NULL).  Calls that share
+ *              a workspace must be ordered on one stream: two at once give
+ *              wrong values (NaN where one waits for a state in vain).
  */
 KDA_API int kda_scan_fwd(const kda_scan_dims_t* dims, const void* x, const float* log_a, const float* h0,
                          const int32_t* cu_seqlens, void* y, float* h_T, float* states, void* workspace,

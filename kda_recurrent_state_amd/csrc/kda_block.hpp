@@ -66,7 +66,7 @@ struct ConvArgs {
 };
 hipError_t launch_conv_fwd(const ConvArgs& a, hipStream_t st);
 hipError_t launch_conv_bwd(const ConvArgs& a, hipStream_t st);
-int conv_bwd_parts(int dtype, int T, int N, int C);  // partial rows of the backward
+int conv_bwd_parts(int T, int N, int C);  // partial rows of the backward
 hipError_t launch_conv_step(const ConvArgs& a, hipStream_t st);
 
 struct LinScanArgs {
@@ -79,17 +79,20 @@ struct LinScanArgs {
     void* y;              // forward: y; backward: dx
     float* dla;
     float* hT;            // forward: may be null; backward: dh0, may be null
-    float* states;        // [tiles][C]: state before every 64th token
-    float* agg;           // scratch: [tiles][2][C] tile products and ends
-    float* rcarry;        // backward scratch: [tiles][C] derivative entering a tile from behind
+    float* states;        // state before every 64th token, [ceil(T / 64)][C]; forward: may be null
+    uint64_t* word;       // scratch: linscan_chain_bytes
     int32_t N, T, eq, C;
     int64_t xs, ls, ds;
     int32_t dtype;
 };
-constexpr int LINSCAN_TILE = 64;
-hipError_t launch_linscan_states(const LinScanArgs& a, hipStream_t st);  // fills states
-hipError_t launch_linscan_fwd(const LinScanArgs& a, hipStream_t st);     // y, hT from states
-hipError_t launch_linscan_bwd(const LinScanArgs& a, hipStream_t st);     // dx, dla, dh0 from states
+constexpr int LINSCAN_TILE = 128;
+// The chain between tiles: one word per tile and channel, and a counter.
+inline size_t linscan_chain_bytes(int64_t T, int64_t C) {
+    const size_t tiles = (size_t)((T + LINSCAN_TILE - 1) / LINSCAN_TILE);
+    return tiles > 1 ? tiles * C * 8 + 8 : 0;
+}
+hipError_t launch_linscan_fwd(const LinScanArgs& a, bool out, hipStream_t st);  // out: y, hT; states where given
+hipError_t launch_linscan_bwd(const LinScanArgs& a, hipStream_t st);            // dx, dla, dh0 from states
 hipError_t launch_linscan_step(const LinScanArgs& a, hipStream_t st);
 
 }  // namespace kda

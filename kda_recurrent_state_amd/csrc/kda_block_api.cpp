@@ -103,11 +103,18 @@ int plan_scan(const kda_scan_dims_t* d, kda::LinScanArgs* a) {
     return KDA_OK;
 }
 
-int64_t scan_tiles(int64_t T) { return (T + kda::LINSCAN_TILE - 1) / kda::LINSCAN_TILE; }
-size_t scan_agg_bytes(const kda::LinScanArgs& a) { return round256((size_t)scan_tiles(a.T) * 2 * a.C * 4); }
-size_t scan_state_bytes(const kda::LinScanArgs& a) { return round256((size_t)scan_tiles(a.T) * a.C * 4); }
+size_t scan_chain_bytes(const kda::LinScanArgs& a) { return round256(kda::linscan_chain_bytes(a.T, a.C)); }
 size_t scan_workspace(const kda::LinScanArgs& a, int backward) {
-    return scan_agg_bytes(a) + (backward ? 2 : 1) * scan_state_bytes(a);
+    const size_t states = ((size_t)a.T + KDA_SCAN_STATE_EVERY - 1) / KDA_SCAN_STATE_EVERY * a.C * 4;
+    return scan_chain_bytes(a) + (backward ? round256(states) : 0);
+}
+
+// Workgroups of a launch: 512 threads each, fewer than 2^32 in all.
+int check_scan_size(const kda::LinScanArgs& a) {
+    const int64_t tiles = ((int64_t)a.T + kda::LINSCAN_TILE - 1) / kda::LINSCAN_TILE, blocks = (a.C + 63) / 64;
+    if (tiles * blocks > kMaxThreads / 512 - 64)
+        return fail(KDA_ERR_INVALID_ARGUMENT, "total_tokens x channels = %d x %d is too large", a.T, a.C);
+    return KDA_OK;
 }
 
 // ---------------------------------------------------------------- kda_conv
@@ -131,7 +138,7 @@ int plan_conv(const kda_conv_dims_t* d, kda::ConvArgs* a) {
 }
 
 size_t conv_bwd_workspace(const kda::ConvArgs& a) {
-    return round256((size_t)kda::conv_bwd_parts(a.dtype, a.T, a.N, a.C) * a.C * (a.W + 1) * 4);
+    return round256((size_t)kda::conv_bwd_parts(a.T, a.N, a.C) * a.C * (a.W + 1) * 4);
 }
 
 // ---------------------------------------------------------------- norms
@@ -234,13 +241,11 @@ int kda_scan_fwd(const kda_scan_dims_t* d, const void* x, const float* log_a, co
     KDA_TRY(check_optional(states, 4, "states"));
     if (h_T && h_T == h0) return fail(KDA_ERR_INVALID_ARGUMENT, "h_T must not be h0");
     KDA_TRY(check_workspace(workspace, workspace_bytes, scan_workspace(a, 0)));
-    uint8_t* ws = static_cast<uint8_t*>(workspace);
+    KDA_TRY(check_scan_size(a));
     a.x = x; a.la = log_a; a.h0 = h0; a.cu = cu_seqlens; a.eq = cu_seqlens ? 0 : a.T / a.N;
-    a.y = y; a.hT = h_T;
-    a.agg = reinterpret_cast<float*>(ws);
-    a.states = states ? states : reinterpret_cast<float*>(ws + scan_agg_bytes(a));
-    if (a.T > 0) KDA_TRY(hip_status(kda::launch_linscan_states(a, (hipStream_t)stream), "scan"));
-    return hip_status(kda::launch_linscan_fwd(a, (hipStream_t)stream), "scan");
+    a.y = y; a.hT = h_T; a.states = states;
+    a.word = static_cast<uint64_t*>(workspace);
+    return hip_status(kda::launch_linscan_fwd(a, true, (hipStream_t)stream), "scan");
 }
 
 int kda_scan_bwd(const kda_scan_dims_t* d, const void* x, const float* log_a, const float* h0, const int32_t* cu_seqlens,
@@ -263,16 +268,16 @@ int kda_scan_bwd(const kda_scan_dims_t* d, const void* x, const float* log_a, co
     KDA_TRY(check_optional(dh0, 4, "dh0"));
     if (dh0 && (dh0 == dh_T || dh0 == h0)) return fail(KDA_ERR_INVALID_ARGUMENT, "dh0 must not be dh_T or h0");
     KDA_TRY(check_workspace(workspace, workspace_bytes, scan_workspace(a, 1)));
+    KDA_TRY(check_scan_size(a));
     uint8_t* ws = static_cast<uint8_t*>(workspace);
     a.x = x; a.la = log_a; a.h0 = h0; a.cu = cu_seqlens; a.eq = cu_seqlens ? 0 : a.T / a.N;
     a.dy = dy; a.dhT = dh_T; a.y = dx; a.dla = dlog_a; a.hT = dh0;
-    a.agg = reinterpret_cast<float*>(ws);
-    a.rcarry = reinterpret_cast<float*>(ws + scan_agg_bytes(a));
+    a.word = reinterpret_cast<uint64_t*>(ws);
     if (states) {
         a.states = const_cast<float*>(states);
     } else {
-        a.states = reinterpret_cast<float*>(ws + scan_agg_bytes(a) + scan_state_bytes(a));
-        if (a.T > 0) KDA_TRY(hip_status(kda::launch_linscan_states(a, (hipStream_t)stream), "scan"));
+        a.states = reinterpret_cast<float*>(ws + scan_chain_bytes(a));
+        KDA_TRY(hip_status(kda::launch_linscan_fwd(a, false, (hipStream_t)stream), "scan"));
     }
     return hip_status(kda::launch_linscan_bwd(a, (hipStream_t)stream), "scan gradient");
 }
@@ -348,7 +353,7 @@ int kda_conv_bwd(const kda_conv_dims_t* d, const void* x, const float* weight, c
     a.part = static_cast<float*>(workspace);
     if (a.N > 0) KDA_TRY(hip_status(kda::launch_conv_bwd(a, (hipStream_t)stream), "convolution gradient"));
     if (!dweight && !dbias) return ok();
-    return hip_status(kda::launch_colsum(a.part, kda::conv_bwd_parts(a.dtype, a.T, a.N, a.C), (int64_t)a.C * (a.W + 1),
+    return hip_status(kda::launch_colsum(a.part, kda::conv_bwd_parts(a.T, a.N, a.C), (int64_t)a.C * (a.W + 1),
                                          (int64_t)a.C * a.W, dweight, dbias, (hipStream_t)stream),
                       "convolution gradient");
 }

@@ -31,28 +31,39 @@ struct Taps {
     const T* x;      // channel c of token 0
     const T* state;  // channel c of state row 0, or null
     int64_t xs;
-    int C, n_valid;
+    int C;
     // row `pos` (from -(W-1)) of sequence n whose tokens start at beg
     __device__ __forceinline__ void row(int n, int beg, int pos, float (&v)[V]) const {
         if (pos >= 0) {
-            load_n<T, V>(x + (int64_t)(beg + pos) * xs, n_valid, v);
+            get_v<V>(load_v<V>(x + (int64_t)(beg + pos) * xs), v);
         } else if (state) {
-            load_n<T, V>(state + ((int64_t)n * (W - 1) + (W - 1 + pos)) * C, n_valid, v);
+            get_v<V>(load_v<V>(state + ((int64_t)n * (W - 1) + (W - 1 + pos)) * C), v);
         } else {
-#pragma unroll
-            for (int i = 0; i < V; ++i) v[i] = 0.f;
+            zero_v<V>(v);
         }
     }
 };
+
+// Taps and bias of V channels from c.
+template <int V, int W>
+__device__ __forceinline__ void load_weight(const ConvArgs& a, int c, float (&w)[V][W], float (&b)[V]) {
+    const Pack<float, V * W> wr = load_v<V * W>(a.weight + (int64_t)c * W);
+#pragma unroll
+    for (int i = 0; i < V; ++i)
+#pragma unroll
+        for (int j = 0; j < W; ++j) w[i][j] = wr[i * W + j];
+    if (a.bias) get_v<V>(load_v<V>(a.bias + c), b);
+    else zero_v<V>(b);
+}
 
 template <typename T, int V, int W>
 __global__ __launch_bounds__(BT) void conv_fwd_kernel(ConvArgs a, int G, int L, int strip_blocks) {
     const Seqs sq{a.cu, a.N, a.T, a.eq};
     const int cl = threadIdx.x % G, spb = BT / G, sl = threadIdx.x / G;
-    const int c = ((int)blockIdx.y * G + cl) * V;
-    if (c >= a.C) return;
-    const int nv = a.C - c;
-    const Taps<T, V, W> tp{(const T*)a.x + c, a.state ? (const T*)a.state + c : nullptr, a.xs, a.C, nv};
+    const int at = ((int)blockIdx.y * G + cl) * V;
+    if (at >= a.C) return;
+    const int c = column<V>(at, a.C);
+    const Taps<T, V, W> tp{(const T*)a.x + c, a.state ? (const T*)a.state + c : nullptr, a.xs, a.C};
 
     if ((int)blockIdx.x >= strip_blocks) {  // the sequences' final states
         const int64_t rows = (int64_t)a.N * (W - 1);
@@ -62,31 +73,36 @@ __global__ __launch_bounds__(BT) void conv_fwd_kernel(ConvArgs a, int G, int L, 
             const int len = sq.start(n + 1) - beg;
             float v[V];
             tp.row(n, beg, (len > 0 ? len : 0) - (W - 1) + i, v);
-            store_n<T, V>((T*)a.state_T + r * a.C + c, nv, v);
+            store_v<V>((T*)a.state_T + r * a.C + c, v);
         }
         return;
     }
 
     const int tend = sq.end();
-    int64_t t64 = ((int64_t)blockIdx.x * spb + sl) * L;
+    const int64_t t64 = ((int64_t)blockIdx.x * spb + sl) * L;
     if (t64 >= tend) return;
     int t = (int)t64;
     const int stop = (tend - t > L) ? t + L : tend;
 
     float w[V][W], b[V];
-#pragma unroll
-    for (int i = 0; i < V; ++i) {
-        const int ci = i < nv ? c + i : c;
-#pragma unroll
-        for (int j = 0; j < W; ++j) w[i][j] = a.weight[(int64_t)ci * W + j];
-        b[i] = a.bias ? a.bias[ci] : 0.f;
-    }
+    load_weight<V, W>(a, c, w, b);
     int n = sq.find(t), beg = sq.start(n), end = sq.start(n + 1);
     float win[W - 1][V];  // rows t - W + 1 .. t - 1
+    auto refill = [&]() {
+        if (t - beg >= W - 1) {
+            Pack<T, V> r[W - 1];
 #pragma unroll
-    for (int k = 0; k < W - 1; ++k) tp.row(n, beg, t - beg - (W - 1) + k, win[k]);
+            for (int k = 0; k < W - 1; ++k) r[k] = load_v<V>(tp.x + (int64_t)(t - (W - 1) + k) * a.xs);
+#pragma unroll
+            for (int k = 0; k < W - 1; ++k) get_v<V>(r[k], win[k]);
+        } else {
+#pragma unroll
+            for (int k = 0; k < W - 1; ++k) tp.row(n, beg, t - beg - (W - 1) + k, win[k]);
+        }
+    };
+    refill();
 
-    auto step = [&](int u, const float (&xv)[V]) {
+    auto step = [&](int u, const Pack<T, V>& xv) {
         float z[V];
 #pragma unroll
         for (int i = 0; i < V; ++i) {
@@ -99,14 +115,14 @@ __global__ __launch_bounds__(BT) void conv_fwd_kernel(ConvArgs a, int G, int L, 
             for (int j = 0; j < W - 2; ++j) win[j][i] = win[j + 1][i];
             win[W - 2][i] = xv[i];
         }
-        store_n<T, V>((T*)a.y + (int64_t)u * a.C + c, nv, z);
+        store_v<V>((T*)a.y + (int64_t)u * a.C + c, z);
     };
 
     while (t < stop) {
         if (t + GRP <= stop && t + GRP <= end) {
-            float xv[GRP][V];
+            Pack<T, V> xv[GRP];
 #pragma unroll
-            for (int i = 0; i < GRP; ++i) load_n<T, V>(tp.x + (int64_t)(t + i) * a.xs, nv, xv[i]);
+            for (int i = 0; i < GRP; ++i) xv[i] = load_v<V>(tp.x + (int64_t)(t + i) * a.xs);
 #pragma unroll
             for (int i = 0; i < GRP; ++i) step(t + i, xv[i]);
             t += GRP;
@@ -119,23 +135,26 @@ __global__ __launch_bounds__(BT) void conv_fwd_kernel(ConvArgs a, int G, int L, 
                     beg = sq.start(n);
                     end = sq.start(n + 1);
                     if (end <= t) end = t + 1;  // offsets out of order: still one token at a time
-#pragma unroll
-                    for (int k = 0; k < W - 1; ++k) tp.row(n, beg, t - beg - (W - 1) + k, win[k]);
+                    refill();
                 }
-                float xv[V];
-                load_n<T, V>(tp.x + (int64_t)t * a.xs, nv, xv);
-                step(t, xv);
+                step(t, load_v<V>(tp.x + (int64_t)t * a.xs));
             }
         }
     }
+}
+
+// dy and z to dz
+__device__ __forceinline__ float dz_of(float dy, float z, int silu) {
+    if (!silu) return dy;
+    const float s = sigmoid_f(z);
+    return dy * (s * (1.f + z * (1.f - s)));
 }
 
 // dz of token `pos` of sequence n (beg), from its taps
 template <typename T, int V, int W>
 __device__ __forceinline__ void dz_at(const ConvArgs& a, const Taps<T, V, W>& tp, const T* dyp, const float (&w)[V][W],
                                       const float (&b)[V], int n, int beg, int pos, float (&dz)[V]) {
-    load_n<T, V>(dyp + (int64_t)(beg + pos) * a.ds, tp.n_valid, dz);
-    if (!a.silu) return;
+    const Pack<T, V> dy = load_v<V>(dyp + (int64_t)(beg + pos) * a.ds);
     float z[V];
 #pragma unroll
     for (int i = 0; i < V; ++i) z[i] = b[i];
@@ -147,10 +166,7 @@ __device__ __forceinline__ void dz_at(const ConvArgs& a, const Taps<T, V, W>& tp
         for (int i = 0; i < V; ++i) z[i] += w[i][j] * v[i];
     }
 #pragma unroll
-    for (int i = 0; i < V; ++i) {
-        const float s = sigmoid_f(z[i]);
-        dz[i] *= s * (1.f + z[i] * (1.f - s));
-    }
+    for (int i = 0; i < V; ++i) dz[i] = dz_of(dy[i], z[i], a.silu);
 }
 
 // Workgroups [0, strip_blocks) walk strips of tokens; the rest form the rows of
@@ -163,19 +179,12 @@ __global__ __launch_bounds__(BT) void conv_bwd_kernel(ConvArgs a, int G, int L, 
     const int cl = threadIdx.x % G, spb = BT / G, sl = threadIdx.x / G;
     const int c0 = ((int)blockIdx.y * G + cl) * V;
     const bool live = c0 < a.C;  // idle lanes stay for the sums at the end
-    const int c = live ? c0 : 0;
-    const int nv = a.C - c;
-    const Taps<T, V, W> tp{(const T*)a.x + c, a.state ? (const T*)a.state + c : nullptr, a.xs, a.C, nv};
+    const int c = column<V>(c0, a.C);
+    const Taps<T, V, W> tp{(const T*)a.x + c, a.state ? (const T*)a.state + c : nullptr, a.xs, a.C};
     const T* dyp = (const T*)a.dy + c;
 
     float w[V][W], b[V];
-#pragma unroll
-    for (int i = 0; i < V; ++i) {
-        const int ci = i < nv ? c + i : c;
-#pragma unroll
-        for (int j = 0; j < W; ++j) w[i][j] = a.weight[(int64_t)ci * W + j];
-        b[i] = a.bias ? a.bias[ci] : 0.f;
-    }
+    load_weight<V, W>(a, c, w, b);
     float dw[W][V] = {}, db[V] = {};
 
     // row `pos` (state rows from -(W-1)) of sequence n by itself: its derivative
@@ -184,10 +193,9 @@ __global__ __launch_bounds__(BT) void conv_bwd_kernel(ConvArgs a, int G, int L, 
         float xv[V];
         tp.row(n, beg, pos, xv);
         if (pos >= len - (W - 1) && a.dstT) {
-            load_n<T, V>((const T*)a.dstT + ((int64_t)n * (W - 1) + (pos - len + W - 1)) * a.C + c, nv, dx);
+            get_v<V>(load_v<V>((const T*)a.dstT + ((int64_t)n * (W - 1) + (pos - len + W - 1)) * a.C + c), dx);
         } else {
-#pragma unroll
-            for (int i = 0; i < V; ++i) dx[i] = 0.f;
+            zero_v<V>(dx);
         }
 #pragma unroll
         for (int k = 0; k < W; ++k) {
@@ -213,7 +221,7 @@ __global__ __launch_bounds__(BT) void conv_bwd_kernel(ConvArgs a, int G, int L, 
             if (len < 0) len = 0;
             float dx[V];
             alone(n, beg, len, i - (W - 1), dx);
-            if (a.state_T) store_n<T, V>((T*)a.state_T + r * a.C + c, nv, dx);
+            if (a.state_T) store_v<V>((T*)a.state_T + r * a.C + c, dx);
         }
     } else if (live) {
         const int tend = sq.end();
@@ -233,33 +241,40 @@ __global__ __launch_bounds__(BT) void conv_bwd_kernel(ConvArgs a, int G, int L, 
             }
             if (t + GRP <= stop && t - (W - 1) >= beg && t + GRP + (W - 1) <= end) {
                 if (!have) {
+                    Pack<T, V> r[2 * (W - 1)], d[W - 1];  // x rows from t - W + 1, dy rows from t
+#pragma unroll
+                    for (int k = 0; k < 2 * (W - 1); ++k) r[k] = load_v<V>(tp.x + (int64_t)(t - (W - 1) + k) * a.xs);
+#pragma unroll
+                    for (int k = 0; k < W - 1; ++k) d[k] = load_v<V>(dyp + (int64_t)(t + k) * a.ds);
 #pragma unroll
                     for (int k = 0; k < W - 1; ++k) {
-                        load_n<T, V>(tp.x + (int64_t)(t + k) * a.xs, nv, xw[k]);
-                        dz_at<T, V, W>(a, tp, dyp, w, b, n, beg, t - beg + k, dzw[k]);
+                        get_v<V>(r[W - 1 + k], xw[k]);
+#pragma unroll
+                        for (int i = 0; i < V; ++i) {
+                            float z = b[i];
+#pragma unroll
+                            for (int j = 0; j < W; ++j) z += w[i][j] * r[k + j][i];
+                            dzw[k][i] = dz_of(d[k][i], z, a.silu);
+                        }
                     }
                     have = true;
                 }
-                float xv[GRP][V], dv[GRP][V];
+                Pack<T, V> xv[GRP], dv[GRP];
 #pragma unroll
                 for (int i = 0; i < GRP; ++i) {
-                    load_n<T, V>(tp.x + (int64_t)(t + W - 1 + i) * a.xs, nv, xv[i]);
-                    load_n<T, V>(dyp + (int64_t)(t + W - 1 + i) * a.ds, nv, dv[i]);
+                    xv[i] = load_v<V>(tp.x + (int64_t)(t + W - 1 + i) * a.xs);
+                    dv[i] = load_v<V>(dyp + (int64_t)(t + W - 1 + i) * a.ds);
                 }
 #pragma unroll
                 for (int g = 0; g < GRP; ++g) {  // token t + g; the newest row is t + g + W - 1
                     float dx[V];
 #pragma unroll
                     for (int i = 0; i < V; ++i) {
-                        float dz = dv[g][i];
-                        if (a.silu) {
-                            float z = b[i];
+                        float z = b[i];
 #pragma unroll
-                            for (int j = 0; j < W - 1; ++j) z += w[i][j] * xw[j][i];
-                            z += w[i][W - 1] * xv[g][i];
-                            const float s = sigmoid_f(z);
-                            dz *= s * (1.f + z * (1.f - s));
-                        }
+                        for (int j = 0; j < W - 1; ++j) z += w[i][j] * xw[j][i];
+                        z += w[i][W - 1] * xv[g][i];
+                        const float dz = dz_of(dv[g][i], z, a.silu);
                         float v = w[i][0] * dz;
                         dw[0][i] += xw[0][i] * dz;
 #pragma unroll
@@ -277,7 +292,7 @@ __global__ __launch_bounds__(BT) void conv_bwd_kernel(ConvArgs a, int G, int L, 
                         xw[W - 2][i] = xv[g][i];
                         dzw[W - 2][i] = dz;
                     }
-                    store_n<T, V>((T*)a.y + (int64_t)(t + g) * a.C + c, nv, dx);
+                    store_v<V>((T*)a.y + (int64_t)(t + g) * a.C + c, dx);
                 }
                 t += GRP;
             } else {
@@ -288,7 +303,7 @@ __global__ __launch_bounds__(BT) void conv_bwd_kernel(ConvArgs a, int G, int L, 
                 for (; t < until; ++t) {
                     float dx[V];
                     alone(n, beg, end - beg, t - beg, dx);
-                    store_n<T, V>((T*)a.y + (int64_t)t * a.C + c, nv, dx);
+                    store_v<V>((T*)a.y + (int64_t)t * a.C + c, dx);
                 }
             }
         }
@@ -307,36 +322,47 @@ __global__ __launch_bounds__(BT) void conv_bwd_kernel(ConvArgs a, int G, int L, 
             for (int i = 0; i < V; ++i) {
                 float s = 0.f;
                 for (int q = 0; q < spb; ++q) s += lds[(q * G + cl) * V + i];
-                if (i < nv) out[j < W ? (int64_t)(c + i) * W + j : (int64_t)a.C * W + c + i] = s;
+                out[j < W ? (int64_t)(c + i) * W + j : (int64_t)a.C * W + c + i] = s;
             }
         }
     }
 }
 
-// One token per sequence.
+// One token per sequence.  The state may be updated in place, so a lane owns its
+// columns alone: the row's last few go one by one (a vector at the row's end that
+// overlapped its neighbour's could read what that lane has already written).
+template <typename T, int V, int W>
+__device__ __forceinline__ void conv_step_at(const ConvArgs& a, int n, int c) {
+    const T* st = (const T*)a.state + (int64_t)n * (W - 1) * a.C + c;
+    Pack<T, V> r[W];
+#pragma unroll
+    for (int k = 0; k < W - 1; ++k) r[k] = load_v<V>(st + (int64_t)k * a.C);
+    r[W - 1] = load_v<V>((const T*)a.x + (int64_t)n * a.xs + c);
+    float w[V][W], z[V];
+    load_weight<V, W>(a, c, w, z);
+    T* to = (T*)a.state_T + (int64_t)n * (W - 1) * a.C + c;
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+#pragma unroll
+        for (int j = 0; j < W; ++j) z[i] += w[i][j] * r[j][i];
+        z[i] = act_f(z[i], a.silu);
+    }
+#pragma unroll
+    for (int k = 0; k < W - 1; ++k) *reinterpret_cast<Pack<T, V>*>(to + (int64_t)k * a.C) = r[k + 1];
+    store_v<V>((T*)a.y + (int64_t)n * a.C + c, z);
+}
+
 template <typename T, int V, int W>
 __global__ __launch_bounds__(BT) void conv_step_kernel(ConvArgs a) {
     const int ncv = (a.C + V - 1) / V;
     const int64_t id = (int64_t)blockIdx.x * BT + threadIdx.x;
     if (id >= (int64_t)a.N * ncv) return;
-    const int n = (int)(id / ncv), c = (int)(id % ncv) * V, nv = a.C - c;
-    float win[W][V], z[V];
-#pragma unroll
-    for (int k = 0; k < W - 1; ++k)
-        load_n<T, V>((const T*)a.state + ((int64_t)n * (W - 1) + k) * a.C + c, nv, win[k]);
-    load_n<T, V>((const T*)a.x + (int64_t)n * a.xs + c, nv, win[W - 1]);
-#pragma unroll
-    for (int i = 0; i < V; ++i) {
-        const int ci = i < nv ? c + i : c;
-        z[i] = a.bias ? a.bias[ci] : 0.f;
-#pragma unroll
-        for (int j = 0; j < W; ++j) z[i] += a.weight[(int64_t)ci * W + j] * win[j][i];
-        z[i] = act_f(z[i], a.silu);
+    const int n = (int)(id / ncv), c = (int)(id % ncv) * V;
+    if (c + V <= a.C) {
+        conv_step_at<T, V, W>(a, n, c);
+    } else {
+        for (int i = c; i < a.C; ++i) conv_step_at<T, 1, W>(a, n, i);
     }
-#pragma unroll
-    for (int k = 0; k < W - 1; ++k)
-        store_n<T, V>((T*)a.state_T + ((int64_t)n * (W - 1) + k) * a.C + c, nv, win[k + 1]);
-    store_n<T, V>((T*)a.y + (int64_t)n * a.C + c, nv, z);
 }
 
 // Lanes along the channels, strip length and strip workgroups.
@@ -358,7 +384,10 @@ ConvShape conv_shape(int V, int T, int C, int max_blocks) {
 
 constexpr int BWD_STRIP_BLOCKS = 512;
 int state_blocks(int N) { return N < 32 ? N : 32; }
-int bwd_vec(int dtype) { return 4; }
+// Channels per lane: 16 bytes forwards, 4 backwards (twice the rows and the
+// sums in registers); single channels where the row is shorter.
+int fwd_vec(int dtype, int C) { return dtype == 1 ? (C >= 8 ? 8 : 1) : (C >= 4 ? 4 : 1); }
+int bwd_vec(int C) { return C >= 4 ? 4 : 1; }
 
 #define KDA_CONV_RUN(KERNEL, T_, V_, GRID, ...)                                                                       \
     switch (a.W) {                                                                                                    \
@@ -366,37 +395,45 @@ int bwd_vec(int dtype) { return 4; }
         case 3: hipLaunchKernelGGL((KERNEL<T_, V_, 3>), GRID, dim3(BT), 0, st, __VA_ARGS__); break;                   \
         default: hipLaunchKernelGGL((KERNEL<T_, V_, 4>), GRID, dim3(BT), 0, st, __VA_ARGS__); break;                  \
     }
+// V16 channels per lane for bf16, 4 for fp32, 1 where v is 1
+#define KDA_CONV_TYPES(KERNEL, V16, GRID, ...)                                                                        \
+    if (a.dtype == 1) {                                                                                               \
+        if (v == 1) KDA_CONV_RUN(KERNEL, bf16, 1, GRID, __VA_ARGS__)                                                  \
+        else KDA_CONV_RUN(KERNEL, bf16, V16, GRID, __VA_ARGS__)                                                       \
+    } else {                                                                                                          \
+        if (v == 1) KDA_CONV_RUN(KERNEL, float, 1, GRID, __VA_ARGS__)                                                 \
+        else KDA_CONV_RUN(KERNEL, float, 4, GRID, __VA_ARGS__)                                                        \
+    }
 
 }  // namespace
 
 hipError_t launch_conv_fwd(const ConvArgs& a, hipStream_t st) {
-    const ConvShape s = conv_shape(a.dtype == 1 ? 8 : 4, a.T, a.C, 0);
+    const int v = fwd_vec(a.dtype, a.C);
+    const ConvShape s = conv_shape(v, a.T, a.C, 0);
     const int extra = a.state_T ? state_blocks(a.N) : 0;
     if (s.strips + extra == 0) return hipSuccess;
     const dim3 grid(s.strips + extra, s.cblocks);
-    if (a.dtype == 1) { KDA_CONV_RUN(conv_fwd_kernel, bf16, 8, grid, a, s.G, s.L, s.strips) }
-    else { KDA_CONV_RUN(conv_fwd_kernel, float, 4, grid, a, s.G, s.L, s.strips) }
+    KDA_CONV_TYPES(conv_fwd_kernel, 8, grid, a, s.G, s.L, s.strips)
     return hipGetLastError();
 }
 
-int conv_bwd_parts(int dtype, int T, int N, int C) {
-    return conv_shape(bwd_vec(dtype), T, C, BWD_STRIP_BLOCKS).strips + state_blocks(N);
+int conv_bwd_parts(int T, int N, int C) {
+    return conv_shape(bwd_vec(C), T, C, BWD_STRIP_BLOCKS).strips + state_blocks(N);
 }
 
 hipError_t launch_conv_bwd(const ConvArgs& a, hipStream_t st) {
-    const ConvShape s = conv_shape(bwd_vec(a.dtype), a.T, a.C, BWD_STRIP_BLOCKS);
+    const int v = bwd_vec(a.C);
+    const ConvShape s = conv_shape(v, a.T, a.C, BWD_STRIP_BLOCKS);
     const dim3 grid(s.strips + state_blocks(a.N), s.cblocks);
-    if (a.dtype == 1) { KDA_CONV_RUN(conv_bwd_kernel, bf16, 4, grid, a, s.G, s.L, s.strips) }
-    else { KDA_CONV_RUN(conv_bwd_kernel, float, 4, grid, a, s.G, s.L, s.strips) }
+    KDA_CONV_TYPES(conv_bwd_kernel, 4, grid, a, s.G, s.L, s.strips)
     return hipGetLastError();
 }
 
 hipError_t launch_conv_step(const ConvArgs& a, hipStream_t st) {
-    const int V = a.dtype == 1 ? 8 : 4;
-    const int64_t work = (int64_t)a.N * ((a.C + V - 1) / V);
+    const int v = fwd_vec(a.dtype, a.C);
+    const int64_t work = (int64_t)a.N * ((a.C + v - 1) / v);
     const dim3 grid((unsigned)((work + BT - 1) / BT));
-    if (a.dtype == 1) { KDA_CONV_RUN(conv_step_kernel, bf16, 8, grid, a) }
-    else { KDA_CONV_RUN(conv_step_kernel, float, 4, grid, a) }
+    KDA_CONV_TYPES(conv_step_kernel, 8, grid, a)
     return hipGetLastError();
 }
 

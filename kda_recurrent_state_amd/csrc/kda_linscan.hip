@@ -3,23 +3,41 @@
 //   h_t = a_t h_{t-1} + x_t,  a_t = e^{log a_t},  y_t = h_t            per channel
 //   g_t = dy_t + a_{t+1} g_{t+1},  dx_t = g_t,  dlog a_t = g_t a_t h_{t-1}
 //
-// The packed axis is cut into tiles of 64 tokens whatever the sequences'
-// edges; a workgroup holds one tile of 64 V channels, each of its four
-// wavefronts 16 tokens in registers.  A run of tokens maps the state before it
-// to P h + E (P the product of its a, E its end from a zero state), or, if a
-// sequence starts in it, to E alone: that case is marked by P = -1 and chosen,
-// never multiplied, so that nothing of an earlier sequence, infinities
-// included, reaches the next one.  The backward runs the same way from the
-// end, with c_t = a_t g_t as what a token hands to the one before it.
+// HBM-bound, so x and log a are read once.  The packed axis is cut into tiles of
+// 128 tokens whatever the sequences' edges; a workgroup holds one tile of 64 V
+// channels, each of its eight wavefronts 16 tokens in registers.  A run of tokens
+// maps the state before it to P h + E (P the product of its a, E its end from a
+// zero state), or, if a sequence starts in it, to E alone: that case is marked
+// by P = -1 and chosen, never multiplied, so that nothing of an earlier
+// sequence, infinities included, reaches the next one.
+//
+// Tiles of the same channels form a chain: each workgroup publishes its tile's
+// (P, E), takes the state before the tile from the nearest tile behind whose
+// state is known, folding in the (P, E) of those between, publishes its own end
+// state as (-1, h), and only then walks its tokens.  A pair is one 64-bit word,
+// written and read whole at agent scope, so no other ordering is needed; the
+// fold runs oldest to newest with the same operations that formed the published
+// states, so the result does not depend on which of them were there.  Tiles
+// are taken in the order of a ticket counter: a workgroup waits only for tiles
+// whose workgroups have started, so every wait ends.
+//
+// The backward runs the same way from the end, with c_t = a_t g_t as what a
+// token hands to the one before it, and takes the forward states from `states`.
 #include "kda_block.hpp"
 #include "kda_rows.hpp"
 
 namespace kda {
 namespace {
 
-constexpr int TT = LINSCAN_TILE;      // tokens per tile
-constexpr int NW = 4, BT = NW * WAVE;  // wavefronts of a workgroup
-constexpr int TW = TT / NW;           // tokens per wavefront
+constexpr int TT = LINSCAN_TILE;       // tokens per tile
+constexpr int NW = 8, BT = NW * WAVE;  // wavefronts of a workgroup
+constexpr int TW = TT / NW;            // tokens per wavefront
+constexpr int SW = 64 / TW;            // wavefronts between two rows of states
+constexpr int LB = 8;                  // words of the chain read at once
+constexpr uint32_t EMPTY = 0xffffffffu;  // P of a word not yet published
+// Polls before a wait is given up (seconds; reached only if the workspace is
+// written by something else meanwhile): the state is then NaN and the call ends.
+constexpr int MAX_POLLS = 1 << 21;
 
 // One run of tokens followed by another: (p, e) <- (p2, e2) after (p, e).
 __device__ __forceinline__ void then(float& p, float& e, float p2, float e2) {
@@ -27,6 +45,43 @@ __device__ __forceinline__ void then(float& p, float& e, float p2, float e2) {
     p = p2 < 0.f ? -1.f : p < 0.f ? -1.f : p2 * p;
 }
 __device__ __forceinline__ float apply(float p, float e, float h) { return p < 0.f ? e : p * h + e; }
+
+__device__ __forceinline__ void publish(uint64_t* word, float p, float e) {
+    const uint32_t pb = p == p ? __float_as_uint(p) : 0x7fc00000u;  // no NaN reads as EMPTY
+    __hip_atomic_store(word, (uint64_t)__float_as_uint(e) << 32 | pb, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+}
+
+// The state handed over by the tile behind: words at word, word + step, ...,
+// nearest first, `behind` of them (>= 1; the last of them always becomes (-1, h)).
+__device__ __forceinline__ float look_back(const uint64_t* word, int64_t step, int behind) {
+    for (int poll = 0; poll < MAX_POLLS; ++poll) {
+        uint64_t w[LB];
+#pragma unroll
+        for (int d = 0; d < LB; ++d)
+            w[d] = __hip_atomic_load(word + (d < behind ? d : behind - 1) * step, __ATOMIC_RELAXED,
+                                     __HIP_MEMORY_SCOPE_AGENT);
+        bool have = false;
+        float h = 0.f;
+#pragma unroll
+        for (int d = LB - 1; d >= 0; --d) {
+            const uint32_t pb = (uint32_t)w[d];
+            const float p = __uint_as_float(pb), e = __uint_as_float((uint32_t)(w[d] >> 32));
+            if (pb == EMPTY) have = false;
+            else if (p < 0.f) have = true, h = e;
+            else if (d < behind) h = p * h + e;
+        }
+        if (have) return h;
+        __builtin_amdgcn_s_sleep(1);
+    }
+    return __uint_as_float(0x7fc00000u);
+}
+
+__global__ __launch_bounds__(256) void linscan_clear_kernel(uint64_t* word, int64_t count, uint32_t* ticket) {
+    const int64_t i = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 2;
+    if (i == 0) *ticket = 0;
+    if (i < count) word[i] = ~0ull;
+    if (i + 1 < count) word[i + 1] = ~0ull;
+}
 
 // Which of a wavefront's tokens start and end a sequence (uniform over the
 // wavefront): bit i of first / last for token t0 + i.
@@ -49,166 +104,91 @@ __device__ __forceinline__ Edges edges_of(const Seqs& sq, int t0, int tend) {
     return e;
 }
 
-// a and x of a wavefront's tokens; absent tokens are the identity.
-template <typename T, int V>
-__device__ __forceinline__ void load_run(const LinScanArgs& p, int t0, int count, int c, int nv, float (&a)[TW][V],
-                                         float (&x)[TW][V]) {
+// Rows t0 .. t0 + 15 of a [T, C] tensor at this lane's columns (rows past the
+// tensor's end: its last one, unused).  The rows are the wavefront's, so their
+// addresses stay in scalar registers.
+template <int V, typename T>
+__device__ __forceinline__ void load_rows(const T* base, int64_t stride, int t0, int T_, uint32_t c,
+                                          Pack<T, V> (&r)[TW]) {
 #pragma unroll
     for (int i = 0; i < TW; ++i) {
-        if (i < count) {
-            load_n<float, V>(p.la + (int64_t)(t0 + i) * p.ls + c, nv, a[i]);
-            load_n<T, V>((const T*)p.x + (int64_t)(t0 + i) * p.xs + c, nv, x[i]);
-        } else {
-#pragma unroll
-            for (int v = 0; v < V; ++v) a[i][v] = x[i][v] = 0.f;
-        }
+        const T* row = base + (int64_t)(t0 + i < T_ ? t0 + i : T_ - 1) * stride;
+        r[i] = load_v<V>(row + c);
     }
+}
+
+// e^{log a}; tokens that do not exist keep the state (a = 1, and x = 0 below).
+template <int V>
+__device__ __forceinline__ void decays(const Pack<float, V> (&la)[TW], int count, float (&a)[TW][V]) {
 #pragma unroll
     for (int i = 0; i < TW; ++i)
 #pragma unroll
-        for (int v = 0; v < V; ++v) a[i][v] = __expf(a[i][v]);
+        for (int v = 0; v < V; ++v) a[i][v] = __expf(la[i][v]);
+    if (count < TW) {
+#pragma unroll
+        for (int i = 0; i < TW; ++i)
+#pragma unroll
+            for (int v = 0; v < V; ++v) a[i][v] = i < count ? a[i][v] : 1.f;
+    }
+}
+template <int V, typename T>
+__device__ __forceinline__ float value(const Pack<T, V> (&x)[TW], int i, int v, int count) {
+    return i < count ? x[i][v] : 0.f;
 }
 
 template <int V>
-__device__ __forceinline__ void load_h0(const LinScanArgs& p, const float* h0, int n, int c, int nv, float (&h)[V]) {
-    if (h0) {
-        load_n<float, V>(h0 + (int64_t)n * p.C + c, nv, h);
-    } else {
-#pragma unroll
-        for (int v = 0; v < V; ++v) h[v] = 0.f;
-    }
+__device__ __forceinline__ void load_state(const float* h0, int C, int n, int c, float (&h)[V]) {
+    if (h0) get_v<V>(load_v<V>(h0 + (int64_t)n * C + c), h);
+    else zero_v<V>(h);
 }
 
 // (P, E) of a wavefront's run, forwards
-template <int V>
-__device__ __forceinline__ void run_forward(const LinScanArgs& p, const Seqs& sq, const Edges& ed, int t0, int c, int nv,
-                                            const float (&a)[TW][V], const float (&x)[TW][V], float (&P)[V],
+template <int V, typename T>
+__device__ __forceinline__ void run_forward(const LinScanArgs& p, const Seqs& sq, const Edges& ed, int t0, int c,
+                                            const float (&a)[TW][V], const Pack<T, V> (&x)[TW], float (&P)[V],
                                             float (&E)[V]) {
 #pragma unroll
     for (int v = 0; v < V; ++v) P[v] = 1.f, E[v] = 0.f;
 #pragma unroll
     for (int i = 0; i < TW; ++i) {
         if (ed.first >> i & 1) {
-            load_h0<V>(p, p.h0, sq.find(t0 + i), c, nv, E);
+            load_state<V>(p.h0, p.C, sq.find(t0 + i), c, E);
 #pragma unroll
             for (int v = 0; v < V; ++v) P[v] = -1.f;
         }
 #pragma unroll
         for (int v = 0; v < V; ++v) {
-            E[v] = a[i][v] * E[v] + x[i][v];
+            E[v] = a[i][v] * E[v] + value<V>(x, i, v, ed.count);
             P[v] = P[v] < 0.f ? -1.f : P[v] * a[i][v];
         }
     }
 }
 
-// (P, E) of every tile: agg[tile][0][c] = P, agg[tile][1][c] = E
-template <typename T, int V>
-__global__ __launch_bounds__(BT) void linscan_agg_kernel(LinScanArgs p) {
-    __shared__ float sp[NW][WAVE * V], se[NW][WAVE * V];
-    const Seqs sq{p.cu, p.N, p.T, p.eq};
-    const int lane = threadIdx.x % WAVE, wv = __builtin_amdgcn_readfirstlane(threadIdx.x / WAVE);
-    const int c = ((int)blockIdx.y * WAVE + lane) * V, nv = p.C - c;
-    const int t0 = (int)blockIdx.x * TT + wv * TW;
-    const Edges ed = edges_of(sq, t0, sq.end());
-    float a[TW][V], x[TW][V], P[V], E[V];
-    load_run<T, V>(p, t0, ed.count, c, nv, a, x);
-    run_forward<V>(p, sq, ed, t0, c, nv, a, x, P, E);
-#pragma unroll
-    for (int v = 0; v < V; ++v) sp[wv][lane * V + v] = P[v], se[wv][lane * V + v] = E[v];
-    __syncthreads();
-    if (wv == 0) {
-#pragma unroll
-        for (int w = 1; w < NW; ++w)
-#pragma unroll
-            for (int v = 0; v < V; ++v) then(P[v], E[v], sp[w][lane * V + v], se[w][lane * V + v]);
-        store_n<float, V>(p.agg + (int64_t)blockIdx.x * 2 * p.C + c, nv, P);
-        store_n<float, V>(p.agg + ((int64_t)blockIdx.x * 2 + 1) * p.C + c, nv, E);
-    }
-}
-
-// The same from the end: what a tile hands to the token before it, P c + E for
-// c handed to it from behind.  Absent tokens are the identity.
-template <typename T, int V>
+// The same from the end: what a run hands to the token before it, P c + E for c
+// handed to it from behind.
+template <int V, typename T>
 __device__ __forceinline__ void run_backward(const LinScanArgs& p, const Seqs& sq, const Edges& ed, int t0, int c,
-                                             int nv, const float (&a)[TW][V], const float (&dy)[TW][V], float (&P)[V],
+                                             const float (&a)[TW][V], const Pack<T, V> (&dy)[TW], float (&P)[V],
                                              float (&E)[V]) {
 #pragma unroll
     for (int v = 0; v < V; ++v) P[v] = 1.f, E[v] = 0.f;
 #pragma unroll
     for (int i = TW - 1; i >= 0; --i) {
-        if (i >= ed.count) continue;
         if (ed.last >> i & 1) {
-            load_h0<V>(p, p.dhT, sq.find(t0 + i), c, nv, E);
+            load_state<V>(p.dhT, p.C, sq.find(t0 + i), c, E);
 #pragma unroll
             for (int v = 0; v < V; ++v) P[v] = -1.f;
         }
 #pragma unroll
         for (int v = 0; v < V; ++v) {
-            E[v] = a[i][v] * (dy[i][v] + E[v]);
+            E[v] = a[i][v] * (value<V>(dy, i, v, ed.count) + E[v]);
             P[v] = P[v] < 0.f ? -1.f : P[v] * a[i][v];
         }
     }
 }
 
-template <typename T, int V>
-__global__ __launch_bounds__(BT) void linscan_ragg_kernel(LinScanArgs p) {
-    __shared__ float sp[NW][WAVE * V], se[NW][WAVE * V];
-    const Seqs sq{p.cu, p.N, p.T, p.eq};
-    const int lane = threadIdx.x % WAVE, wv = __builtin_amdgcn_readfirstlane(threadIdx.x / WAVE);
-    const int c = ((int)blockIdx.y * WAVE + lane) * V, nv = p.C - c;
-    const int t0 = (int)blockIdx.x * TT + wv * TW;
-    const Edges ed = edges_of(sq, t0, sq.end());
-    LinScanArgs q = p;
-    q.x = p.dy;
-    q.xs = p.ds;
-    float a[TW][V], dy[TW][V], P[V], E[V];
-    load_run<T, V>(q, t0, ed.count, c, nv, a, dy);
-    run_backward<T, V>(p, sq, ed, t0, c, nv, a, dy, P, E);
-#pragma unroll
-    for (int v = 0; v < V; ++v) sp[wv][lane * V + v] = P[v], se[wv][lane * V + v] = E[v];
-    __syncthreads();
-    if (wv == 0) {
-#pragma unroll
-        for (int v = 0; v < V; ++v) P[v] = sp[NW - 1][lane * V + v], E[v] = se[NW - 1][lane * V + v];
-#pragma unroll
-        for (int w = NW - 2; w >= 0; --w)
-#pragma unroll
-            for (int v = 0; v < V; ++v) then(P[v], E[v], sp[w][lane * V + v], se[w][lane * V + v]);
-        store_n<float, V>(p.agg + (int64_t)blockIdx.x * 2 * p.C + c, nv, P);
-        store_n<float, V>(p.agg + ((int64_t)blockIdx.x * 2 + 1) * p.C + c, nv, E);
-    }
-}
-
-// Carries between tiles, one thread per channel: carry[tile] = the state before
-// (reverse: handed from behind to) the tile.
-constexpr int CB = 16;  // tiles read ahead
-__global__ __launch_bounds__(WAVE) void linscan_carry_kernel(const float* agg, float* carry, int tiles, int C,
-                                                             int reverse) {
-    const int c = (int)blockIdx.x * WAVE + threadIdx.x;
-    if (c >= C) return;
-    float h = 0.f;
-    for (int k0 = 0; k0 < tiles; k0 += CB) {
-        float P[CB], E[CB];
-#pragma unroll
-        for (int i = 0; i < CB; ++i) {
-            const int k = k0 + i < tiles ? k0 + i : tiles - 1;
-            const int64_t tile = reverse ? tiles - 1 - k : k;
-            P[i] = agg[tile * 2 * C + c];
-            E[i] = agg[(tile * 2 + 1) * C + c];
-        }
-#pragma unroll
-        for (int i = 0; i < CB; ++i) {
-            if (k0 + i < tiles) {
-                const int64_t tile = reverse ? tiles - 1 - (k0 + i) : k0 + i;
-                carry[tile * C + c] = h;
-                h = apply(P[i], E[i], h);
-            }
-        }
-    }
-}
-
-// The last workgroups of the output kernels: an empty sequence's final state is
-// its initial one (forward: hT from h0, backward: dh0 from dhT).
+// An empty sequence's final state is its initial one (forward: hT from h0,
+// backward: dh0 from dhT).
 __device__ __forceinline__ void empty_seqs(const Seqs& sq, const float* from, float* to, int C, int block, int blocks) {
     for (int n = block; n < sq.N; n += blocks) {
         if (sq.start(n + 1) > sq.start(n)) continue;
@@ -216,167 +196,240 @@ __device__ __forceinline__ void empty_seqs(const Seqs& sq, const float* from, fl
     }
 }
 
-template <typename T, int V>
-__global__ __launch_bounds__(BT) void linscan_fwd_kernel(LinScanArgs p, int tiles) {
-    __shared__ float sp[NW][WAVE * V], se[NW][WAVE * V];
+// A workgroup's job: a tile of the chain by ticket, or (one tile in all) its own
+// number.  Jobs at and past `jobs` look after the empty sequences.
+__device__ __forceinline__ int take_job(uint32_t* ticket, int* lds) {
+    if (!ticket) return (int)blockIdx.x;
+    if (threadIdx.x == 0) *lds = (int)atomicAdd(ticket, 1u);
+    __syncthreads();
+    return __builtin_amdgcn_readfirstlane(*lds);
+}
+
+// The tile's (P, E) from its wavefronts', the state handed to it, and its own
+// published: thread j < 64 V does channel j of the workgroup.  In: sp, se; out:
+// sh, the state handed to the tile.  BACK: from the last wavefront to the first.
+template <int V, bool BACK>
+__device__ __forceinline__ void chain(const LinScanArgs& p, const float (&sp)[NW][WAVE * V],
+                                      const float (&se)[NW][WAVE * V], float (&sh)[WAVE * V], int cb, int tile,
+                                      int tiles) {
+    const int j = threadIdx.x;
+    if (j >= WAVE * V) return;
+    const int at = (cb * WAVE + j / V) * V;
+    if (at >= p.C) return;
+    const int c = column<V>(at, p.C) + j % V;
+    float P = sp[BACK ? NW - 1 : 0][j], E = se[BACK ? NW - 1 : 0][j];
+#pragma unroll
+    for (int w = 1; w < NW; ++w) then(P, E, sp[BACK ? NW - 1 - w : w][j], se[BACK ? NW - 1 - w : w][j]);
+    const int behind = BACK ? tiles - 1 - tile : tile;
+    uint64_t* word = p.word + (int64_t)tile * p.C + c;
+    float h = 0.f;
+    if (tiles > 1) {
+        if (behind > 0) {
+            publish(word, P, E);
+            h = look_back(BACK ? word + p.C : word - p.C, BACK ? (int64_t)p.C : -(int64_t)p.C, behind);
+        }
+        if (P >= 0.f || behind == 0 || P != P) publish(word, -1.f, apply(P, E, h));
+    }
+    sh[j] = h;
+}
+
+// OUT: y and hT too, else the states alone.
+template <typename T, int V, bool OUT>
+__global__ __launch_bounds__(BT) void linscan_fwd_kernel(LinScanArgs p, int tiles, int cblocks, uint32_t* ticket) {
+    __shared__ float sp[NW][WAVE * V], se[NW][WAVE * V], sh[WAVE * V];
+    __shared__ int s_job;
     const Seqs sq{p.cu, p.N, p.T, p.eq};
-    if ((int)blockIdx.x >= tiles) {
-        if (blockIdx.y == 0) empty_seqs(sq, p.h0, p.hT, p.C, blockIdx.x - tiles, gridDim.x - tiles);
+    const int job = take_job(ticket, &s_job), jobs = tiles * cblocks;
+    if (job >= jobs) {
+        if (OUT && p.hT) empty_seqs(sq, p.h0, p.hT, p.C, job - jobs, gridDim.x - jobs);
         return;
     }
+    const int tile = job / cblocks, cb = job - tile * cblocks;
     const int lane = threadIdx.x % WAVE, wv = __builtin_amdgcn_readfirstlane(threadIdx.x / WAVE);
-    const int c = ((int)blockIdx.y * WAVE + lane) * V, nv = p.C - c;
-    const int t0 = (int)blockIdx.x * TT + wv * TW;
+    const int at = (cb * WAVE + lane) * V, c = column<V>(at, p.C);
+    const int t0 = tile * TT + wv * TW;
+    Pack<float, V> la[TW];
+    Pack<T, V> x[TW];
+    load_rows<V>(p.la, p.ls, t0, p.T, c, la);
+    load_rows<V>((const T*)p.x, p.xs, t0, p.T, c, x);
     const Edges ed = edges_of(sq, t0, sq.end());
-    float a[TW][V], x[TW][V], P[V], E[V], h[V];
-    load_n<float, V>(p.states + (int64_t)blockIdx.x * p.C + c, nv, h);
-    load_run<T, V>(p, t0, ed.count, c, nv, a, x);
-    run_forward<V>(p, sq, ed, t0, c, nv, a, x, P, E);
+    float a[TW][V], P[V], E[V], h[V];
+    decays<V>(la, ed.count, a);
+    run_forward<V>(p, sq, ed, t0, c, a, x, P, E);
 #pragma unroll
     for (int v = 0; v < V; ++v) sp[wv][lane * V + v] = P[v], se[wv][lane * V + v] = E[v];
     __syncthreads();
+    chain<V, false>(p, sp, se, sh, cb, tile, tiles);
+    __syncthreads();
+    if (at >= p.C) return;
+#pragma unroll
+    for (int v = 0; v < V; ++v) h[v] = sh[lane * V + v];
     for (int w = 0; w < wv; ++w)
 #pragma unroll
         for (int v = 0; v < V; ++v) h[v] = apply(sp[w][lane * V + v], se[w][lane * V + v], h[v]);
+    if (p.states && wv % SW == 0 && t0 < p.T) store_v<V>(p.states + (int64_t)(t0 / (SW * TW)) * p.C + c, h);
+    if (!OUT) return;
+    T* y = (T*)p.y + (int64_t)t0 * p.C;
 #pragma unroll
     for (int i = 0; i < TW; ++i) {
         if (i >= ed.count) continue;
-        if (ed.first >> i & 1) load_h0<V>(p, p.h0, sq.find(t0 + i), c, nv, h);
+        if (ed.first >> i & 1) load_state<V>(p.h0, p.C, sq.find(t0 + i), c, h);
 #pragma unroll
         for (int v = 0; v < V; ++v) h[v] = a[i][v] * h[v] + x[i][v];
-        store_n<T, V>((T*)p.y + (int64_t)(t0 + i) * p.C + c, nv, h);
-        if ((ed.last >> i & 1) && p.hT) store_n<float, V>(p.hT + (int64_t)sq.find(t0 + i) * p.C + c, nv, h);
+        store_v<V>(y + (int64_t)i * p.C + (uint32_t)c, h);
+        if ((ed.last >> i & 1) && p.hT) store_v<V>(p.hT + (int64_t)sq.find(t0 + i) * p.C + c, h);
     }
 }
 
 template <typename T, int V>
-__global__ __launch_bounds__(BT) void linscan_bwd_kernel(LinScanArgs p, int tiles) {
-    __shared__ float sp[NW][WAVE * V], se[NW][WAVE * V], rp[NW][WAVE * V], re[NW][WAVE * V];
+__global__ __launch_bounds__(BT) void linscan_bwd_kernel(LinScanArgs p, int tiles, int cblocks, uint32_t* ticket) {
+    __shared__ float sp[NW][WAVE * V], se[NW][WAVE * V], rp[NW][WAVE * V], re[NW][WAVE * V], sh[WAVE * V];
+    __shared__ int s_job;
     const Seqs sq{p.cu, p.N, p.T, p.eq};
-    if ((int)blockIdx.x >= tiles) {
-        if (blockIdx.y == 0) empty_seqs(sq, p.dhT, p.hT, p.C, blockIdx.x - tiles, gridDim.x - tiles);
+    const int job = take_job(ticket, &s_job), jobs = tiles * cblocks;
+    if (job >= jobs) {
+        if (p.hT) empty_seqs(sq, p.dhT, p.hT, p.C, job - jobs, gridDim.x - jobs);
         return;
     }
+    const int back = job / cblocks, cb = job - back * cblocks, tile = tiles - 1 - back;
     const int lane = threadIdx.x % WAVE, wv = __builtin_amdgcn_readfirstlane(threadIdx.x / WAVE);
-    const int c = ((int)blockIdx.y * WAVE + lane) * V, nv = p.C - c;
-    const int t0 = (int)blockIdx.x * TT + wv * TW;
+    const int at = (cb * WAVE + lane) * V, c = column<V>(at, p.C);
+    const int t0 = tile * TT + wv * TW;
+    Pack<float, V> la[TW];
+    Pack<T, V> x[TW], dy[TW];
+    load_rows<V>(p.la, p.ls, t0, p.T, c, la);
+    load_rows<V>((const T*)p.dy, p.ds, t0, p.T, c, dy);
+    load_rows<V>((const T*)p.x, p.xs, t0, p.T, c, x);
+    // the state before the 64 tokens that this wavefront's belong to
+    const int row = (tile * TT + wv / SW * SW * TW) / (SW * TW), rows = (p.T + SW * TW - 1) / (SW * TW);
+    float h[V], g[V];
+    get_v<V>(load_v<V>(p.states + (int64_t)(row < rows ? row : rows - 1) * p.C + c), h);
     const Edges ed = edges_of(sq, t0, sq.end());
-    float a[TW][V], x[TW][V], dy[TW][V], P[V], E[V], h[V], g[V];
-    load_n<float, V>(p.states + (int64_t)blockIdx.x * p.C + c, nv, h);
-    load_n<float, V>(p.rcarry + (int64_t)blockIdx.x * p.C + c, nv, g);
-    load_run<T, V>(p, t0, ed.count, c, nv, a, x);
-#pragma unroll
-    for (int i = 0; i < TW; ++i) {
-        if (i < ed.count) load_n<T, V>((const T*)p.dy + (int64_t)(t0 + i) * p.ds + c, nv, dy[i]);
-    }
-    run_forward<V>(p, sq, ed, t0, c, nv, a, x, P, E);
-#pragma unroll
-    for (int v = 0; v < V; ++v) sp[wv][lane * V + v] = P[v], se[wv][lane * V + v] = E[v];
-    run_backward<T, V>(p, sq, ed, t0, c, nv, a, dy, P, E);
+    float a[TW][V], P[V], E[V];
+    decays<V>(la, ed.count, a);
+    run_backward<V>(p, sq, ed, t0, c, a, dy, P, E);
 #pragma unroll
     for (int v = 0; v < V; ++v) rp[wv][lane * V + v] = P[v], re[wv][lane * V + v] = E[v];
+    run_forward<V>(p, sq, ed, t0, c, a, x, P, E);
+#pragma unroll
+    for (int v = 0; v < V; ++v) sp[wv][lane * V + v] = P[v], se[wv][lane * V + v] = E[v];
     __syncthreads();
-    for (int w = 0; w < wv; ++w)
+    chain<V, true>(p, rp, re, sh, cb, tile, tiles);
+    // the state before every token of the run
+    for (int w = wv / SW * SW; w < wv; ++w)
 #pragma unroll
         for (int v = 0; v < V; ++v) h[v] = apply(sp[w][lane * V + v], se[w][lane * V + v], h[v]);
+    float hb[TW][V];
+#pragma unroll
+    for (int i = 0; i < TW; ++i) {
+        if (ed.first >> i & 1) load_state<V>(p.h0, p.C, sq.find(t0 + i), c, h);
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+            hb[i][v] = h[v];
+            h[v] = a[i][v] * h[v] + x[i][v];
+        }
+    }
+    __syncthreads();
+    if (at >= p.C) return;
+#pragma unroll
+    for (int v = 0; v < V; ++v) g[v] = sh[lane * V + v];
     for (int w = NW - 1; w > wv; --w)
 #pragma unroll
         for (int v = 0; v < V; ++v) g[v] = apply(rp[w][lane * V + v], re[w][lane * V + v], g[v]);
-    // x[i] becomes the state before token i
-#pragma unroll
-    for (int i = 0; i < TW; ++i) {
-        if (ed.first >> i & 1) load_h0<V>(p, p.h0, sq.find(t0 + i), c, nv, h);
-#pragma unroll
-        for (int v = 0; v < V; ++v) {
-            const float xi = x[i][v];
-            x[i][v] = h[v];
-            h[v] = a[i][v] * h[v] + xi;
-        }
-    }
+    T* dx = (T*)p.y + (int64_t)t0 * p.C;
+    float* dla = p.dla + (int64_t)t0 * p.C;
 #pragma unroll
     for (int i = TW - 1; i >= 0; --i) {
         if (i >= ed.count) continue;
-        if (ed.last >> i & 1) load_h0<V>(p, p.dhT, sq.find(t0 + i), c, nv, g);
-        float dl[V];
+        if (ed.last >> i & 1) load_state<V>(p.dhT, p.C, sq.find(t0 + i), c, g);
+        float d[V], dl[V];
 #pragma unroll
-        for (int v = 0; v < V; ++v) dy[i][v] += g[v];
-        store_n<T, V>((T*)p.y + (int64_t)(t0 + i) * p.C + c, nv, dy[i]);
+        for (int v = 0; v < V; ++v) d[v] = dy[i][v] + g[v];
+        store_v<V>(dx + (int64_t)i * p.C + (uint32_t)c, d);
 #pragma unroll
         for (int v = 0; v < V; ++v) {
-            g[v] = a[i][v] * dy[i][v];
-            dl[v] = g[v] * x[i][v];
+            g[v] = a[i][v] * d[v];
+            dl[v] = g[v] * hb[i][v];
         }
-        store_n<float, V>(p.dla + (int64_t)(t0 + i) * p.C + c, nv, dl);
-        if ((ed.first >> i & 1) && p.hT) store_n<float, V>(p.hT + (int64_t)sq.find(t0 + i) * p.C + c, nv, g);
+        store_v<V>(dla + (int64_t)i * p.C + (uint32_t)c, dl);
+        if ((ed.first >> i & 1) && p.hT) store_v<V>(p.hT + (int64_t)sq.find(t0 + i) * p.C + c, g);
     }
 }
 
-template <typename T, int V>
-__global__ __launch_bounds__(BT) void linscan_step_kernel(LinScanArgs p) {
-    const int ncv = (p.C + V - 1) / V;
-    const int64_t id = (int64_t)blockIdx.x * BT + threadIdx.x;
-    if (id >= (int64_t)p.N * ncv) return;
-    const int n = (int)(id / ncv), c = (int)(id % ncv) * V, nv = p.C - c;
-    float a[V], x[V], h[V];
-    load_n<float, V>(p.la + (int64_t)n * p.ls + c, nv, a);
-    load_n<T, V>((const T*)p.x + (int64_t)n * p.xs + c, nv, x);
-    load_n<float, V>(p.h0 + (int64_t)n * p.C + c, nv, h);
+// One token per sequence.  In place: a lane owns its columns alone, the row's
+// last few one by one.
+template <int V, typename T>
+__device__ __forceinline__ void step_at(const LinScanArgs& p, int n, int c) {
+    const Pack<float, V> la = load_v<V>(p.la + (int64_t)n * p.ls + c), h0 = load_v<V>(p.h0 + (int64_t)n * p.C + c);
+    const Pack<T, V> x = load_v<V>((const T*)p.x + (int64_t)n * p.xs + c);
+    float h[V];
 #pragma unroll
-    for (int v = 0; v < V; ++v) h[v] = __expf(a[v]) * h[v] + x[v];
-    store_n<float, V>(p.hT + (int64_t)n * p.C + c, nv, h);
-    store_n<T, V>((T*)p.y + (int64_t)n * p.C + c, nv, h);
+    for (int v = 0; v < V; ++v) h[v] = __expf(la[v]) * h0[v] + x[v];
+    store_v<V>(p.hT + (int64_t)n * p.C + c, h);
+    store_v<V>((T*)p.y + (int64_t)n * p.C + c, h);
+}
+constexpr int BS = 256;
+template <typename T, int V>
+__global__ __launch_bounds__(BS) void linscan_step_kernel(LinScanArgs p) {
+    const int ncv = (p.C + V - 1) / V;
+    const int64_t id = (int64_t)blockIdx.x * BS + threadIdx.x;
+    if (id >= (int64_t)p.N * ncv) return;
+    const int n = (int)(id / ncv), c = (int)(id % ncv) * V;
+    if (c + V <= p.C) {
+        step_at<V, T>(p, n, c);
+    } else {
+        for (int i = c; i < p.C; ++i) step_at<1, T>(p, n, i);
+    }
 }
 
 int tiles_of(int T) { return (T + TT - 1) / TT; }
-dim3 tile_grid(int tiles, int C, int V) { return dim3(tiles, (C + WAVE * V - 1) / (WAVE * V)); }
 int empty_blocks(int N) { return N < 64 ? N : 64; }
-constexpr int VF = 4, VB = 2;  // channels per lane, forward and backward
+
+// Clears the chain (more than one tile) and gives the launch its grid.
+template <int V, typename K>
+hipError_t run_chain(K kernel, const LinScanArgs& a, bool empties, hipStream_t st) {
+    const int tiles = tiles_of(a.T), cblocks = (a.C + WAVE * V - 1) / (WAVE * V);
+    const int64_t blocks = (int64_t)tiles * cblocks + (empties ? empty_blocks(a.N) : 0);
+    if (blocks == 0) return hipSuccess;
+    uint32_t* ticket = nullptr;
+    if (tiles > 1) {
+        ticket = reinterpret_cast<uint32_t*>(a.word + (int64_t)tiles * a.C);
+        const int64_t words = (int64_t)tiles * a.C;
+        hipLaunchKernelGGL(linscan_clear_kernel, dim3((unsigned)((words + 511) / 512)), dim3(256), 0, st, a.word, words,
+                           ticket);
+    }
+    hipLaunchKernelGGL(kernel, dim3((unsigned)blocks), dim3(BT), 0, st, a, tiles, cblocks, ticket);
+    return hipGetLastError();
+}
+
+template <typename T, int V>
+hipError_t fwd(const LinScanArgs& a, bool out, hipStream_t st) {
+    return out ? run_chain<V>(linscan_fwd_kernel<T, V, true>, a, a.hT != nullptr, st)
+               : run_chain<V>(linscan_fwd_kernel<T, V, false>, a, false, st);
+}
 
 }  // namespace
 
-hipError_t launch_linscan_states(const LinScanArgs& a, hipStream_t st) {
-    const int tiles = tiles_of(a.T);
-    if (a.dtype == 1) hipLaunchKernelGGL((linscan_agg_kernel<bf16, VF>), tile_grid(tiles, a.C, VF), dim3(BT), 0, st, a);
-    else hipLaunchKernelGGL((linscan_agg_kernel<float, VF>), tile_grid(tiles, a.C, VF), dim3(BT), 0, st, a);
-    hipLaunchKernelGGL(linscan_carry_kernel, dim3((a.C + WAVE - 1) / WAVE), dim3(WAVE), 0, st, a.agg, a.states, tiles,
-                       a.C, 0);
-    return hipGetLastError();
-}
-
-hipError_t launch_linscan_fwd(const LinScanArgs& a, hipStream_t st) {
-    const int tiles = tiles_of(a.T);
-    dim3 grid = tile_grid(tiles, a.C, VF);
-    grid.x += a.hT ? empty_blocks(a.N) : 0;
-    if (grid.x == 0) return hipSuccess;
-    if (a.dtype == 1) hipLaunchKernelGGL((linscan_fwd_kernel<bf16, VF>), grid, dim3(BT), 0, st, a, tiles);
-    else hipLaunchKernelGGL((linscan_fwd_kernel<float, VF>), grid, dim3(BT), 0, st, a, tiles);
-    return hipGetLastError();
+hipError_t launch_linscan_fwd(const LinScanArgs& a, bool out, hipStream_t st) {
+    if (a.C < 4) return a.dtype == 1 ? fwd<bf16, 1>(a, out, st) : fwd<float, 1>(a, out, st);
+    return a.dtype == 1 ? fwd<bf16, 4>(a, out, st) : fwd<float, 2>(a, out, st);
 }
 
 hipError_t launch_linscan_bwd(const LinScanArgs& a, hipStream_t st) {
-    const int tiles = tiles_of(a.T);
-    if (tiles > 0) {
-        if (a.dtype == 1)
-            hipLaunchKernelGGL((linscan_ragg_kernel<bf16, VF>), tile_grid(tiles, a.C, VF), dim3(BT), 0, st, a);
-        else
-            hipLaunchKernelGGL((linscan_ragg_kernel<float, VF>), tile_grid(tiles, a.C, VF), dim3(BT), 0, st, a);
-        hipLaunchKernelGGL(linscan_carry_kernel, dim3((a.C + WAVE - 1) / WAVE), dim3(WAVE), 0, st, a.agg, a.rcarry,
-                           tiles, a.C, 1);
-    }
-    dim3 grid = tile_grid(tiles, a.C, VB);
-    grid.x += a.hT ? empty_blocks(a.N) : 0;
-    if (grid.x == 0) return hipSuccess;
-    if (a.dtype == 1) hipLaunchKernelGGL((linscan_bwd_kernel<bf16, VB>), grid, dim3(BT), 0, st, a, tiles);
-    else hipLaunchKernelGGL((linscan_bwd_kernel<float, VB>), grid, dim3(BT), 0, st, a, tiles);
-    return hipGetLastError();
+    const bool empties = a.hT != nullptr;
+    if (a.C < 2)
+        return a.dtype == 1 ? run_chain<1>(linscan_bwd_kernel<bf16, 1>, a, empties, st)
+                            : run_chain<1>(linscan_bwd_kernel<float, 1>, a, empties, st);
+    return a.dtype == 1 ? run_chain<2>(linscan_bwd_kernel<bf16, 2>, a, empties, st)
+                        : run_chain<2>(linscan_bwd_kernel<float, 2>, a, empties, st);
 }
 
 hipError_t launch_linscan_step(const LinScanArgs& a, hipStream_t st) {
     constexpr int V = 4;
     const int64_t work = (int64_t)a.N * ((a.C + V - 1) / V);
-    const dim3 grid((unsigned)((work + BT - 1) / BT));
-    if (a.dtype == 1) hipLaunchKernelGGL((linscan_step_kernel<bf16, V>), grid, dim3(BT), 0, st, a);
-    else hipLaunchKernelGGL((linscan_step_kernel<float, V>), grid, dim3(BT), 0, st, a);
+    const dim3 grid((unsigned)((work + BS - 1) / BS));
+    if (a.dtype == 1) hipLaunchKernelGGL((linscan_step_kernel<bf16, V>), grid, dim3(BS), 0, st, a);
+    else hipLaunchKernelGGL((linscan_step_kernel<float, V>), grid, dim3(BS), 0, st, a);
     return hipGetLastError();
 }
 

@@ -45,6 +45,20 @@ __device__ __forceinline__ void row_sum(float (&v)[A], float* lds) {
     }
 }
 
+// The columns of a lane's j-th vector: first column c (the row's last V where the
+// vector would pass its end), and how many of them (0 to V) a neighbour or
+// nobody counts; lanes past the row's end have V and store nothing.
+template <int V, int G> struct Cols {
+    int c, skip;
+    bool live;
+    __device__ __forceinline__ Cols(int j, int g, int D) {
+        const int at = (j * G + g) * V;
+        c = column<V>(at, D);
+        skip = at - c < V ? at - c : V;
+        live = at < D;
+    }
+};
+
 // A workgroup's partial column sums: each of its BT / G row groups holds acc for
 // the same columns; summed in group order and written to out[0 .. D).
 template <int G, int VPT, int V>
@@ -52,14 +66,18 @@ __device__ __forceinline__ void block_partial(const float (&acc)[VPT][V], float*
     constexpr int RPB = BT / G, W_ = G * VPT * V;
     const int g = threadIdx.x % G, rg = threadIdx.x / G;
     __syncthreads();
-    if constexpr (RPB == 1) {
 #pragma unroll
-        for (int j = 0; j < VPT; ++j) store_n<float, V>(out + (j * G + g) * V, D - (j * G + g) * V, acc[j]);
-    } else {
+    for (int j = 0; j < VPT; ++j) {
+        const Cols<V, G> cl(j, g, D);
+        if (!cl.live) continue;
+        if constexpr (RPB == 1) {
+            store_v<V>(out + cl.c, acc[j]);
+        } else {
 #pragma unroll
-        for (int j = 0; j < VPT; ++j)
-#pragma unroll
-            for (int i = 0; i < V; ++i) lds[rg * W_ + (j * G + g) * V + i] = acc[j][i];
+            for (int i = 0; i < V; ++i) lds[rg * W_ + cl.c + i] = acc[j][i];
+        }
+    }
+    if constexpr (RPB > 1) {
         __syncthreads();
         for (int c = threadIdx.x; c < D; c += BT) {
             float s = 0.f;
@@ -70,44 +88,56 @@ __device__ __forceinline__ void block_partial(const float (&acc)[VPT][V], float*
     }
 }
 
+// Gate activation and its slope.
+__device__ __forceinline__ float gate_act(float g, int silu) {
+    const float s = sigmoid_f(g);
+    return silu ? g * s : s;
+}
+
 template <typename T, int V, int G, int VPT>
 __global__ __launch_bounds__(BT) void norm_gate_fwd_kernel(NormGateArgs a) {
     constexpr int RPB = BT / G;
     __shared__ float lds[BT / WAVE];
     const int g = threadIdx.x % G, D = a.width;
     const float invD = 1.f / (float)D;
+    const T* x = (const T*)a.x;
+    const T* gate = (const T*)a.gate;
     for (int64_t r = (int64_t)blockIdx.x * RPB + threadIdx.x / G; r < a.rows; r += (int64_t)gridDim.x * RPB) {
         const uint32_t t = (uint32_t)r / (uint32_t)a.heads, h = (uint32_t)r - t * a.heads;
-        const T* xp = (const T*)a.x + (int64_t)t * a.xs + (int64_t)h * D;
-        const T* gp = (const T*)a.gate + (int64_t)t * a.gs + (int64_t)h * D;
-        float x[VPT][V], gt[VPT][V], ss[1] = {0.f};
+        const T* xp = x + (int64_t)t * a.xs + (int64_t)h * D;
+        const T* gp = gate + (int64_t)t * a.gs + (int64_t)h * D;
+        Pack<T, V> xr[VPT], gr[VPT];
+        Pack<float, V> wr[VPT];
+#pragma unroll
+        for (int j = 0; j < VPT; ++j) xr[j] = load_v<V>(xp + Cols<V, G>(j, g, D).c);
+        if (a.gate)
+#pragma unroll
+            for (int j = 0; j < VPT; ++j) gr[j] = load_v<V>(gp + Cols<V, G>(j, g, D).c);
+        if (a.weight)
+#pragma unroll
+            for (int j = 0; j < VPT; ++j) wr[j] = load_v<V>(a.weight + Cols<V, G>(j, g, D).c);
+        float ss[1] = {0.f};
 #pragma unroll
         for (int j = 0; j < VPT; ++j) {
-            const int c = (j * G + g) * V;
-            load_n<T, V>(xp + c, D - c, x[j]);
-            if (a.gate) load_n<T, V>(gp + c, D - c, gt[j]);
+            const Cols<V, G> cl(j, g, D);
+#pragma unroll
+            for (int i = 0; i < V; ++i) ss[0] += i >= cl.skip ? xr[j][i] * xr[j][i] : 0.f;
         }
-#pragma unroll
-        for (int j = 0; j < VPT; ++j)
-#pragma unroll
-            for (int i = 0; i < V; ++i) ss[0] += x[j][i] * x[j][i];
         row_sum<G, 1>(ss, lds);
         const float rn = rsqrtf(ss[0] * invD + a.eps);
 #pragma unroll
         for (int j = 0; j < VPT; ++j) {
-            const int c = (j * G + g) * V;
-            float w[V], y[V];
-            if (a.weight) load_n<float, V>(a.weight + c, D - c, w);
+            const Cols<V, G> cl(j, g, D);
+            float y[V];
 #pragma unroll
-            for (int i = 0; i < V; ++i) {
-                y[i] = x[j][i] * rn;
-                if (a.weight) y[i] *= w[i];
-                if (a.gate) {
-                    const float s = sigmoid_f(gt[j][i]);
-                    y[i] *= a.silu ? gt[j][i] * s : s;
-                }
-            }
-            store_n<T, V>((T*)a.y + r * D + c, D - c, y);
+            for (int i = 0; i < V; ++i) y[i] = xr[j][i] * rn;
+            if (a.weight)
+#pragma unroll
+                for (int i = 0; i < V; ++i) y[i] *= wr[j][i];
+            if (a.gate)
+#pragma unroll
+                for (int i = 0; i < V; ++i) y[i] *= gate_act(gr[j][i], a.silu);
+            if (cl.live) store_v<V>((T*)a.y + r * D + cl.c, y);
         }
     }
 }
@@ -118,34 +148,42 @@ __global__ __launch_bounds__(BT) void norm_gate_bwd_kernel(NormGateArgs a) {
     __shared__ float lds[RPB > 1 ? RPB * G * VPT * V : 2 * BT / WAVE];
     const int g = threadIdx.x % G, D = a.width;
     const float invD = 1.f / (float)D;
-    float dw[VPT][V] = {};
+    const T* x = (const T*)a.x;
+    const T* gate = (const T*)a.gate;
+    const T* dyb = (const T*)a.dy;
+    float w[VPT][V], dw[VPT][V] = {};
+#pragma unroll
+    for (int j = 0; j < VPT; ++j)
+#pragma unroll
+        for (int i = 0; i < V; ++i) w[j][i] = a.weight ? a.weight[Cols<V, G>(j, g, D).c + i] : 1.f;
     for (int64_t r = (int64_t)blockIdx.x * RPB + threadIdx.x / G; r < a.rows; r += (int64_t)gridDim.x * RPB) {
         const uint32_t t = (uint32_t)r / (uint32_t)a.heads, h = (uint32_t)r - t * a.heads;
-        const T* xp = (const T*)a.x + (int64_t)t * a.xs + (int64_t)h * D;
-        const T* gp = (const T*)a.gate + (int64_t)t * a.gs + (int64_t)h * D;
-        const T* dp = (const T*)a.dy + (int64_t)t * a.ds + (int64_t)h * D;
-        float x[VPT][V], gt[VPT][V], dy[VPT][V], sm[2] = {0.f, 0.f};
+        const T* xp = x + (int64_t)t * a.xs + (int64_t)h * D;
+        const T* gp = gate + (int64_t)t * a.gs + (int64_t)h * D;
+        const T* dp = dyb + (int64_t)t * a.ds + (int64_t)h * D;
+        Pack<T, V> xr[VPT], gr[VPT], dr[VPT];
 #pragma unroll
         for (int j = 0; j < VPT; ++j) {
-            const int c = (j * G + g) * V;
-            load_n<T, V>(xp + c, D - c, x[j]);
-            load_n<T, V>(dp + c, D - c, dy[j]);
-            if (a.gate) load_n<T, V>(gp + c, D - c, gt[j]);
+            const int c = Cols<V, G>(j, g, D).c;
+            xr[j] = load_v<V>(xp + c);
+            dr[j] = load_v<V>(dp + c);
         }
+        if (a.gate)
+#pragma unroll
+            for (int j = 0; j < VPT; ++j) gr[j] = load_v<V>(gp + Cols<V, G>(j, g, D).c);
+        float sg[VPT][V], sm[2] = {0.f, 0.f};  // sg: the gate's logistic value
 #pragma unroll
         for (int j = 0; j < VPT; ++j) {
-            const int c = (j * G + g) * V;
-            float w[V];
-            if (a.weight) load_n<float, V>(a.weight + c, D - c, w);
+            const Cols<V, G> cl(j, g, D);
 #pragma unroll
             for (int i = 0; i < V; ++i) {
                 float act = 1.f;
                 if (a.gate) {
-                    const float s = sigmoid_f(gt[j][i]);
-                    act = a.silu ? gt[j][i] * s : s;
+                    sg[j][i] = sigmoid_f(gr[j][i]);
+                    act = a.silu ? gr[j][i] * sg[j][i] : sg[j][i];
                 }
-                sm[0] += x[j][i] * x[j][i];
-                sm[1] += dy[j][i] * act * (a.weight ? w[i] : 1.f) * x[j][i];
+                sm[0] += i >= cl.skip ? xr[j][i] * xr[j][i] : 0.f;
+                sm[1] += i >= cl.skip ? dr[j][i] * act * w[j][i] * xr[j][i] : 0.f;
             }
         }
         row_sum<G, 2>(sm, lds);
@@ -153,24 +191,25 @@ __global__ __launch_bounds__(BT) void norm_gate_bwd_kernel(NormGateArgs a) {
         const float k = rn * rn * sm[1] * invD;  // r mean(d n)
 #pragma unroll
         for (int j = 0; j < VPT; ++j) {
-            const int c = (j * G + g) * V;
-            float w[V], dx[V], dg[V];
-            if (a.weight) load_n<float, V>(a.weight + c, D - c, w);
+            const Cols<V, G> cl(j, g, D);
+            float dx[V], dg[V];
 #pragma unroll
             for (int i = 0; i < V; ++i) {
-                const float wi = a.weight ? w[i] : 1.f, n = x[j][i] * rn;
+                const float n = xr[j][i] * rn, dy = dr[j][i];
                 float act = 1.f, slope = 0.f;
                 if (a.gate) {
-                    const float s = sigmoid_f(gt[j][i]);
-                    act = a.silu ? gt[j][i] * s : s;
-                    slope = a.silu ? s * (1.f + gt[j][i] * (1.f - s)) : s * (1.f - s);
+                    const float s = sg[j][i];
+                    act = a.silu ? gr[j][i] * s : s;
+                    slope = a.silu ? s * (1.f + gr[j][i] * (1.f - s)) : s * (1.f - s);
                 }
-                dx[i] = rn * (dy[j][i] * act * wi - x[j][i] * k);
-                dg[i] = dy[j][i] * n * wi * slope;
-                dw[j][i] += dy[j][i] * act * n;
+                dx[i] = rn * (dy * act * w[j][i] - xr[j][i] * k);
+                dg[i] = dy * n * w[j][i] * slope;
+                dw[j][i] += dy * act * n;
             }
-            store_n<T, V>((T*)a.y + r * D + c, D - c, dx);
-            if (a.gate) store_n<T, V>((T*)a.dgate + r * D + c, D - c, dg);
+            if (cl.live) {
+                store_v<V>((T*)a.y + r * D + cl.c, dx);
+                if (a.gate) store_v<V>((T*)a.dgate + r * D + cl.c, dg);
+            }
         }
     }
     if (a.part) block_partial<G, VPT, V>(dw, lds, a.part + (int64_t)blockIdx.x * D, D);
@@ -183,32 +222,41 @@ __global__ __launch_bounds__(BT) void res_norm_fwd_kernel(ResNormArgs a) {
     const int g = threadIdx.x % G, D = a.width;
     const float invD = 1.f / (float)D;
     for (int64_t r = (int64_t)blockIdx.x * RPB + threadIdx.x / G; r < a.rows; r += (int64_t)gridDim.x * RPB) {
+        Pack<R, V> rr[VPT];
+        Pack<T, V> xr[VPT];
+        Pack<float, V> wr[VPT], cr[VPT];
+#pragma unroll
+        for (int j = 0; j < VPT; ++j) {
+            const int c = Cols<V, G>(j, g, D).c;
+            rr[j] = load_v<V>((const R*)a.res + r * a.rs + c);
+            xr[j] = load_v<V>((const T*)a.x + r * a.xs + c);
+            wr[j] = load_v<V>(a.weight + c);
+        }
+        if (a.cscale)
+#pragma unroll
+            for (int j = 0; j < VPT; ++j) cr[j] = load_v<V>(a.cscale + Cols<V, G>(j, g, D).c);
         float h[VPT][V], ss[1] = {0.f};
 #pragma unroll
         for (int j = 0; j < VPT; ++j) {
-            const int c = (j * G + g) * V;
-            float x[V], cs[V];
-            load_n<R, V>((const R*)a.res + r * a.rs + c, D - c, h[j]);
-            load_n<T, V>((const T*)a.x + r * a.xs + c, D - c, x);
-            if (a.cscale) load_n<float, V>(a.cscale + c, D - c, cs);
+            const Cols<V, G> cl(j, g, D);
 #pragma unroll
-            for (int i = 0; i < V; ++i) h[j][i] += (a.cscale ? a.scale * cs[i] : a.scale) * x[i];
+            for (int i = 0; i < V; ++i) {
+                h[j][i] = rr[j][i] + (a.cscale ? a.scale * cr[j][i] : a.scale) * xr[j][i];
+                ss[0] += i >= cl.skip ? h[j][i] * h[j][i] : 0.f;
+            }
         }
-#pragma unroll
-        for (int j = 0; j < VPT; ++j)
-#pragma unroll
-            for (int i = 0; i < V; ++i) ss[0] += h[j][i] * h[j][i];
         row_sum<G, 1>(ss, lds);
         const float rn = rsqrtf(ss[0] * invD + a.eps);
 #pragma unroll
         for (int j = 0; j < VPT; ++j) {
-            const int c = (j * G + g) * V;
-            float w[V], y[V];
-            load_n<float, V>(a.weight + c, D - c, w);
+            const Cols<V, G> cl(j, g, D);
+            float y[V];
 #pragma unroll
-            for (int i = 0; i < V; ++i) y[i] = h[j][i] * rn * w[i];
-            store_n<R, V>((R*)a.res_out + r * D + c, D - c, h[j]);
-            store_n<T, V>((T*)a.y + r * D + c, D - c, y);
+            for (int i = 0; i < V; ++i) y[i] = h[j][i] * rn * wr[j][i];
+            if (cl.live) {
+                store_v<V>((R*)a.res_out + r * D + cl.c, h[j]);
+                store_v<V>((T*)a.y + r * D + cl.c, y);
+            }
         }
     }
 }
@@ -219,25 +267,38 @@ __global__ __launch_bounds__(BT) void res_norm_bwd_kernel(ResNormArgs a) {
     __shared__ float lds[RPB > 1 ? RPB * G * VPT * V : 2 * BT / WAVE];
     const int g = threadIdx.x % G, D = a.width;
     const float invD = 1.f / (float)D;
-    float dw[VPT][V] = {}, dcs[VPT][V] = {};
-    for (int64_t r = (int64_t)blockIdx.x * RPB + threadIdx.x / G; r < a.rows; r += (int64_t)gridDim.x * RPB) {
-        float h[VPT][V], dy[VPT][V], dr[VPT][V], sm[2] = {0.f, 0.f};
+    float w[VPT][V], cs[VPT][V], dw[VPT][V] = {}, dcs[VPT][V] = {};
 #pragma unroll
-        for (int j = 0; j < VPT; ++j) {
-            const int c = (j * G + g) * V;
-            load_n<R, V>((const R*)a.res + r * a.rs + c, D - c, h[j]);
-            load_n<T, V>((const T*)a.dy + r * a.ds + c, D - c, dy[j]);
-            if (a.dres) load_n<R, V>((const R*)a.dres + r * a.drs + c, D - c, dr[j]);
+    for (int j = 0; j < VPT; ++j)
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+            const int c = Cols<V, G>(j, g, D).c + i;
+            w[j][i] = a.weight[c];
+            cs[j][i] = a.cscale ? a.scale * a.cscale[c] : a.scale;
         }
+    for (int64_t r = (int64_t)blockIdx.x * RPB + threadIdx.x / G; r < a.rows; r += (int64_t)gridDim.x * RPB) {
+        Pack<R, V> hr[VPT], rr[VPT];
+        Pack<T, V> dr[VPT], xr[VPT];
 #pragma unroll
         for (int j = 0; j < VPT; ++j) {
-            const int c = (j * G + g) * V;
-            float w[V];
-            load_n<float, V>(a.weight + c, D - c, w);
+            const int c = Cols<V, G>(j, g, D).c;
+            hr[j] = load_v<V>((const R*)a.res + r * a.rs + c);
+            dr[j] = load_v<V>((const T*)a.dy + r * a.ds + c);
+        }
+        if (a.dres)
+#pragma unroll
+            for (int j = 0; j < VPT; ++j) rr[j] = load_v<V>((const R*)a.dres + r * a.drs + Cols<V, G>(j, g, D).c);
+        if (a.want_dcs)
+#pragma unroll
+            for (int j = 0; j < VPT; ++j) xr[j] = load_v<V>((const T*)a.x + r * a.xs + Cols<V, G>(j, g, D).c);
+        float sm[2] = {0.f, 0.f};
+#pragma unroll
+        for (int j = 0; j < VPT; ++j) {
+            const Cols<V, G> cl(j, g, D);
 #pragma unroll
             for (int i = 0; i < V; ++i) {
-                sm[0] += h[j][i] * h[j][i];
-                sm[1] += dy[j][i] * w[i] * h[j][i];
+                sm[0] += i >= cl.skip ? hr[j][i] * hr[j][i] : 0.f;
+                sm[1] += i >= cl.skip ? dr[j][i] * w[j][i] * hr[j][i] : 0.f;
             }
         }
         row_sum<G, 2>(sm, lds);
@@ -245,21 +306,20 @@ __global__ __launch_bounds__(BT) void res_norm_bwd_kernel(ResNormArgs a) {
         const float k = rn * rn * sm[1] * invD;
 #pragma unroll
         for (int j = 0; j < VPT; ++j) {
-            const int c = (j * G + g) * V;
-            float w[V], cs[V], x[V], dx[V], dh[V];
-            load_n<float, V>(a.weight + c, D - c, w);
-            if (a.cscale) load_n<float, V>(a.cscale + c, D - c, cs);
-            if (a.want_dcs) load_n<T, V>((const T*)a.x + r * a.xs + c, D - c, x);
+            const Cols<V, G> cl(j, g, D);
+            float dx[V], dh[V];
 #pragma unroll
             for (int i = 0; i < V; ++i) {
-                dh[i] = rn * (dy[j][i] * w[i] - h[j][i] * k);
-                if (a.dres) dh[i] += dr[j][i];
-                dx[i] = (a.cscale ? a.scale * cs[i] : a.scale) * dh[i];
-                dw[j][i] += dy[j][i] * h[j][i] * rn;
-                if (a.want_dcs) dcs[j][i] += a.scale * dh[i] * x[i];
+                dh[i] = rn * (dr[j][i] * w[j][i] - hr[j][i] * k);
+                if (a.dres) dh[i] += rr[j][i];
+                dx[i] = cs[j][i] * dh[i];
+                dw[j][i] += dr[j][i] * hr[j][i] * rn;
+                if (a.want_dcs) dcs[j][i] += a.scale * dh[i] * xr[j][i];
             }
-            store_n<R, V>((R*)a.res_out + r * D + c, D - c, dh);
-            store_n<T, V>((T*)a.y + r * D + c, D - c, dx);
+            if (cl.live) {
+                store_v<V>((R*)a.res_out + r * D + cl.c, dh);
+                store_v<V>((T*)a.y + r * D + cl.c, dx);
+            }
         }
     }
     if (a.part) {
@@ -309,10 +369,15 @@ RowShape row_shape(int nv) {
     if (nv <= 1024) return {256, 4};
     return {256, 8};
 }
-int vec_of(int dtype) { return dtype == 1 ? 8 : 4; }
+// Elements per lane and access: 16 bytes of the row's type, single elements in
+// rows shorter than that.
+int vec_of(int dtype, int width) {
+    const int v = dtype == 1 ? 8 : 4;
+    return width >= v ? v : 1;
+}
 
 int blocks_for(int dtype, int width, int64_t rows, int most) {
-    const int v = vec_of(dtype);
+    const int v = vec_of(dtype, width);
     const RowShape s = row_shape((width + v - 1) / v);
     const int64_t rpb = BT / s.g, b = (rows + rpb - 1) / rpb;
     return (int)(b < most ? b : most);
@@ -325,6 +390,10 @@ constexpr int BWD_BLOCKS = 1024;     // four workgroups per compute unit; each w
     switch (s.g * 16 + s.vpt) {                                                                                \
         case 4 * 16 + 1: RUN(V, 4, 1); break;                                                                  \
         case 8 * 16 + 1: RUN(V, 8, 1); break;                                                                  \
+        default: if constexpr (V > 1) KDA_WIDE_CASES(RUN, V) break;                                            \
+    }
+#define KDA_WIDE_CASES(RUN, V)                                                                                 \
+    switch (s.g * 16 + s.vpt) {                                                                                \
         case 16 * 16 + 1: RUN(V, 16, 1); break;                                                                \
         case 32 * 16 + 1: RUN(V, 32, 1); break;                                                                \
         case 64 * 16 + 1: RUN(V, 64, 1); break;                                                                \
@@ -332,7 +401,7 @@ constexpr int BWD_BLOCKS = 1024;     // four workgroups per compute unit; each w
         case 256 * 16 + 1: RUN(V, 256, 1); break;                                                              \
         case 256 * 16 + 2: RUN(V, 256, 2); break;                                                              \
         case 256 * 16 + 4: RUN(V, 256, 4); break;                                                              \
-        default: if constexpr (V == 4) { RUN(V, 256, 8); } break;                                              \
+        default: if constexpr (V == 4) { RUN(V, 256, 8); }                                                     \
     }
 
 template <typename T, int V>
@@ -363,10 +432,12 @@ hipError_t launch_colsum(const float* part, int rows, int64_t cols, int64_t spli
 int norm_gate_blocks(int dtype, int width, int64_t rows) { return blocks_for(dtype, width, rows, BWD_BLOCKS); }
 
 hipError_t launch_norm_gate(const NormGateArgs& a, bool backward, hipStream_t st) {
-    const int v = vec_of(a.dtype);
+    const int v = vec_of(a.dtype, a.width);
     const RowShape s = row_shape((a.width + v - 1) / v);
     const int blocks = blocks_for(a.dtype, a.width, a.rows, backward ? BWD_BLOCKS : FWD_BLOCKS);
-    if (a.dtype == 1) norm_gate_launch<bf16, 8>(a, backward, blocks, s, st);
+    if (a.dtype == 1 && v == 1) norm_gate_launch<bf16, 1>(a, backward, blocks, s, st);
+    else if (a.dtype == 1) norm_gate_launch<bf16, 8>(a, backward, blocks, s, st);
+    else if (v == 1) norm_gate_launch<float, 1>(a, backward, blocks, s, st);
     else norm_gate_launch<float, 4>(a, backward, blocks, s, st);
     return hipGetLastError();
 }
@@ -374,12 +445,18 @@ hipError_t launch_norm_gate(const NormGateArgs& a, bool backward, hipStream_t st
 int res_norm_blocks(int dtype, int width, int64_t rows) { return blocks_for(dtype, width, rows, BWD_BLOCKS); }
 
 hipError_t launch_res_norm(const ResNormArgs& a, bool backward, hipStream_t st) {
-    const int v = vec_of(a.dtype);
+    const int v = vec_of(a.dtype, a.width);
     const RowShape s = row_shape((a.width + v - 1) / v);
     const int blocks = blocks_for(a.dtype, a.width, a.rows, backward ? BWD_BLOCKS : FWD_BLOCKS);
-    if (a.dtype == 1 && a.rdtype == 1) res_norm_launch<bf16, bf16, 8>(a, backward, blocks, s, st);
-    else if (a.dtype == 1) res_norm_launch<bf16, float, 8>(a, backward, blocks, s, st);
-    else res_norm_launch<float, float, 4>(a, backward, blocks, s, st);
+    if (v == 1) {
+        if (a.dtype == 1 && a.rdtype == 1) res_norm_launch<bf16, bf16, 1>(a, backward, blocks, s, st);
+        else if (a.dtype == 1) res_norm_launch<bf16, float, 1>(a, backward, blocks, s, st);
+        else res_norm_launch<float, float, 1>(a, backward, blocks, s, st);
+    } else {
+        if (a.dtype == 1 && a.rdtype == 1) res_norm_launch<bf16, bf16, 8>(a, backward, blocks, s, st);
+        else if (a.dtype == 1) res_norm_launch<bf16, float, 8>(a, backward, blocks, s, st);
+        else res_norm_launch<float, float, 4>(a, backward, blocks, s, st);
+    }
     return hipGetLastError();
 }
 

@@ -12,47 +12,39 @@ namespace kda {
 // memory accesses on gfx950 need no more than the element's alignment, so a
 // row that starts at an odd address takes the same instructions as an aligned
 // one.
-template <typename T, int V> struct Pack;
-template <> struct Pack<bf16, 8> { typedef __bf16 type __attribute__((vector_size(16), aligned(2))); };
-template <> struct Pack<bf16, 4> { typedef __bf16 type __attribute__((vector_size(8), aligned(2))); };
-template <> struct Pack<bf16, 2> { typedef __bf16 type __attribute__((vector_size(4), aligned(2))); };
-template <> struct Pack<float, 4> { typedef float type __attribute__((vector_size(16), aligned(4))); };
-template <> struct Pack<float, 2> { typedef float type __attribute__((vector_size(8), aligned(4))); };
-template <> struct Pack<float, 8> {  // two 16-byte accesses
-    struct type { Pack<float, 4>::type lo, hi; __device__ float operator[](int i) const { return i < 4 ? lo[i] : hi[i - 4]; } };
+//
+// Loading and converting are apart: a conversion waits for its load, so code
+// that has several loads to make makes them all first.  For the same reason a
+// lane whose V columns would pass the row's end does not branch to a shorter
+// load: it takes the row's last V columns instead (column below), of which the
+// first few belong to its neighbour too.  Both compute the same values from the
+// same inputs and store the same bits.
+template <typename T, int V> struct Pack {
+    static constexpr int N = V * sizeof(T) <= 16 ? V : 16 / sizeof(T);  // elements of one access
+    typedef T vec __attribute__((vector_size(N * sizeof(T)), aligned(sizeof(T))));
+    vec part[V / N];
+    __device__ __forceinline__ float operator[](int i) const { return (float)part[i / N][i % N]; }
 };
 
-// The first n (any value; all if n >= V) of V elements at p; the rest are 0.
-template <typename T, int V>
-__device__ __forceinline__ void load_n(const T* p, int n, float (&v)[V]) {
-    if (n >= V) {
-        const typename Pack<T, V>::type r = *reinterpret_cast<const typename Pack<T, V>::type*>(p);
-#pragma unroll
-        for (int i = 0; i < V; ++i) v[i] = (float)r[i];
-    } else {
-#pragma unroll
-        for (int i = 0; i < V; ++i) v[i] = i < n ? (float)p[i] : 0.f;
-    }
+template <int V, typename T> __device__ __forceinline__ Pack<T, V> load_v(const T* p) {
+    return *reinterpret_cast<const Pack<T, V>*>(p);
 }
-
-template <typename T, int V>
-__device__ __forceinline__ void store_n(T* p, int n, const float (&v)[V]) {
-    if (n >= V) {
-        if constexpr (sizeof(T) * V > 16) {
-            store_n<T, V / 2>(p, V / 2, reinterpret_cast<const float (&)[V / 2]>(v[0]));
-            store_n<T, V / 2>(p + V / 2, V / 2, reinterpret_cast<const float (&)[V / 2]>(v[V / 2]));
-        } else {
-            typename Pack<T, V>::type r;
+template <int V, typename T> __device__ __forceinline__ void store_v(T* p, const float (&v)[V]) {
+    Pack<T, V> r;
 #pragma unroll
-            for (int i = 0; i < V; ++i) r[i] = from_f32<T>(v[i]);
-            *reinterpret_cast<typename Pack<T, V>::type*>(p) = r;
-        }
-    } else {
-#pragma unroll
-        for (int i = 0; i < V; ++i)
-            if (i < n) p[i] = from_f32<T>(v[i]);
-    }
+    for (int i = 0; i < V; ++i) r.part[i / Pack<T, V>::N][i % Pack<T, V>::N] = from_f32<T>(v[i]);
+    *reinterpret_cast<Pack<T, V>*>(p) = r;
 }
+template <int V> __device__ __forceinline__ void zero_v(float (&v)[V]) {
+#pragma unroll
+    for (int i = 0; i < V; ++i) v[i] = 0.f;
+}
+template <int V, typename T> __device__ __forceinline__ void get_v(const Pack<T, V>& r, float (&v)[V]) {
+#pragma unroll
+    for (int i = 0; i < V; ++i) v[i] = r[i];
+}
+// First column of the lane whose columns start at c, in a row of C >= V.
+template <int V> __device__ __forceinline__ int column(int c, int C) { return c + V <= C ? c : C - V; }
 
 // Sequences of a packed axis of T tokens: offsets cu[0..N] on the device, or
 // (cu null) N sequences of eq tokens each.  Offsets are clamped to [0, T], so

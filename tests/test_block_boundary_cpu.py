@@ -21,7 +21,7 @@ def lib():
 
 
 def scan_dims(**kw):
-    d = dict(num_seqs=2, channels=8, total_tokens=64, dtype=1, reserved=0, x_stride=0, log_a_stride=0, dy_stride=0)
+    d = dict(num_seqs=2, channels=8, total_tokens=256, dtype=1, reserved=0, x_stride=0, log_a_stride=0, dy_stride=0)
     d.update(kw)
     return block._ScanDims(*d.values())
 
@@ -89,7 +89,7 @@ CASES = [
     *[(f, dict(x_stride=1 << 60), {}, INVALID) for f in ARGS],
     ("kda_scan_bwd", dict(dy_stride=7), {}, INVALID),
     ("kda_scan_fwd", dict(log_a_stride=7), {}, INVALID),
-    ("kda_scan_fwd", dict(num_seqs=3), dict(cu=None), INVALID),       # 64 % 3
+    ("kda_scan_fwd", dict(num_seqs=3), dict(cu=None), INVALID),       # 256 % 3
     ("kda_scan_fwd", dict(num_seqs=0), {}, INVALID),                  # tokens without a sequence
     ("kda_conv_bwd", dict(num_seqs=0), {}, INVALID),
     ("kda_scan_fwd", dict(num_seqs=0, total_tokens=0), {}, OK),
@@ -99,7 +99,7 @@ CASES = [
     ("kda_conv_step", dict(num_seqs=0, total_tokens=0), {}, OK),
     ("kda_norm_gate_fwd", dict(tokens=0), {}, OK),
     ("kda_residual_norm_fwd", dict(tokens=0), {}, OK),
-    ("kda_scan_step", {}, {}, INVALID),                               # 64 tokens, 2 sequences
+    ("kda_scan_step", {}, {}, INVALID),                               # 256 tokens, 2 sequences
     ("kda_conv_step", {}, {}, INVALID),
     ("kda_scan_fwd", {}, dict(x=None), INVALID),
     ("kda_scan_fwd", {}, dict(y=None), INVALID),
@@ -164,12 +164,13 @@ def test_refusals(lib, fn, change, given, expect):
 
 def test_workspace_sizes(lib):
     n = ctypes.c_size_t(0)
-    for T in (1, 64, 65, 1000):
-        tiles = -(-T // 64)
+    for T in (1, 64, 128, 129, 1000):
+        tiles = -(-T // 128) if T > 128 else 0  # one tile passes no state on: no workspace
         assert lib.kda_scan_workspace_size(ctypes.byref(scan_dims(total_tokens=T)), 0, ctypes.byref(n)) == OK
         fwd = n.value
         assert lib.kda_scan_workspace_size(ctypes.byref(scan_dims(total_tokens=T)), 1, ctypes.byref(n)) == OK
-        assert n.value >= fwd >= tiles * 8 * 4 and fwd % 256 == 0
+        assert fwd >= tiles * 8 * 8 and fwd % 256 == 0 and (fwd > 0) == (T > 128)
+        assert n.value >= fwd + -(-T // 64) * 8 * 4
     assert lib.kda_scan_workspace_size(ctypes.byref(scan_dims()), 0, None) == INVALID
     for fn, d in (("kda_conv_bwd_workspace_size", conv_dims()), ("kda_norm_gate_bwd_workspace_size", ng_dims()),
                   ("kda_residual_norm_bwd_workspace_size", rn_dims())):
