@@ -86,10 +86,12 @@ struct LinScanArgs {
     int32_t dtype;
 };
 constexpr int LINSCAN_TILE = 128;
-// The chain between tiles: one word per tile and channel, and a counter.
+constexpr int LINSCAN_LINE = 16;  // words of a 128-byte line
+// The chain between tiles: one word per tile and channel, and a counter per block
+// of 64 channels or more.
 inline size_t linscan_chain_bytes(int64_t T, int64_t C) {
     const size_t tiles = (size_t)((T + LINSCAN_TILE - 1) / LINSCAN_TILE);
-    return tiles > 1 ? tiles * C * 8 + 8 : 0;
+    return tiles > 1 ? (tiles * C + (C + 63) / 64 * LINSCAN_LINE) * 8 : 0;
 }
 hipError_t launch_linscan_fwd(const LinScanArgs& a, bool out, hipStream_t st);  // out: y, hT; states where given
 hipError_t launch_linscan_bwd(const LinScanArgs& a, hipStream_t st);            // dx, dla, dh0 from states

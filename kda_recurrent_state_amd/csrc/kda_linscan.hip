@@ -33,8 +33,8 @@ constexpr int TT = LINSCAN_TILE;       // tokens per tile
 constexpr int NW = 8, BT = NW * WAVE;  // wavefronts of a workgroup
 constexpr int TW = TT / NW;            // tokens per wavefront
 constexpr int SW = 64 / TW;            // wavefronts between two rows of states
-constexpr int LB = 8;                  // words of the chain read at once
 constexpr uint32_t EMPTY = 0xffffffffu;  // P of a word not yet published
+constexpr uint32_t KNOWN = 0xbf800000u;  // P = -1: E is the state itself
 // Polls before a wait is given up (seconds; reached only if the workspace is
 // written by something else meanwhile): the state is then NaN and the call ends.
 constexpr int MAX_POLLS = 1 << 21;
@@ -51,36 +51,47 @@ __device__ __forceinline__ void publish(uint64_t* word, float p, float e) {
     __hip_atomic_store(word, (uint64_t)__float_as_uint(e) << 32 | pb, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
 }
 
+__device__ __forceinline__ uint64_t read_word(const uint64_t* word) {
+    return __hip_atomic_load(word, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+}
+
 // The state handed over by the tile behind: words at word, word + step, ...,
 // nearest first, `behind` of them (>= 1; the last of them always becomes (-1, h)).
+// The nearest LB are read together; after that a poll reads only the farthest
+// again, whose state is the first to become known, and what was not there yet.
+// LB = 4 keeps a chain of 512 tiles ahead of the memory (2 x 32768 x 4096: 409 us;
+// LB = 2: 415, 8: 416, 1: 473); the float32 backward takes 2, for its registers.
+template <int LB>  // words of the chain read at once
 __device__ __forceinline__ float look_back(const uint64_t* word, int64_t step, int behind) {
-    for (int poll = 0; poll < MAX_POLLS; ++poll) {
-        uint64_t w[LB];
+    const int far = (behind < LB ? behind : LB) - 1;
+    uint64_t w[LB];
 #pragma unroll
-        for (int d = 0; d < LB; ++d)
-            w[d] = __hip_atomic_load(word + (d < behind ? d : behind - 1) * step, __ATOMIC_RELAXED,
-                                     __HIP_MEMORY_SCOPE_AGENT);
+    for (int d = 0; d < LB; ++d) w[d] = read_word(word + (d < far ? d : far) * step);
+    for (int poll = 0; poll < MAX_POLLS; ++poll) {
         bool have = false;
         float h = 0.f;
 #pragma unroll
         for (int d = LB - 1; d >= 0; --d) {
             const uint32_t pb = (uint32_t)w[d];
-            const float p = __uint_as_float(pb), e = __uint_as_float((uint32_t)(w[d] >> 32));
-            if (pb == EMPTY) have = false;
-            else if (p < 0.f) have = true, h = e;
-            else if (d < behind) h = p * h + e;
+            if (d > far) continue;
+            have = pb == KNOWN || (have && pb != EMPTY);
+            h = apply(__uint_as_float(pb), __uint_as_float((uint32_t)(w[d] >> 32)), h);
         }
         if (have) return h;
         __builtin_amdgcn_s_sleep(1);
+#pragma unroll
+        for (int d = 0; d < LB; ++d)
+            if (d == far || (d < far && (uint32_t)w[d] == EMPTY)) w[d] = read_word(word + d * step);
     }
     return __uint_as_float(0x7fc00000u);
 }
 
-__global__ __launch_bounds__(256) void linscan_clear_kernel(uint64_t* word, int64_t count, uint32_t* ticket) {
+// No word published, no ticket taken (the counters follow the words).
+__global__ __launch_bounds__(256) void linscan_clear_kernel(uint64_t* word, int64_t words, int64_t counters) {
     const int64_t i = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 2;
-    if (i == 0) *ticket = 0;
-    if (i < count) word[i] = ~0ull;
-    if (i + 1 < count) word[i + 1] = ~0ull;
+#pragma unroll
+    for (int k = 0; k < 2; ++k)
+        if (i + k < words + counters) word[i + k] = i + k < words ? ~0ull : 0ull;
 }
 
 // Which of a wavefront's tokens start and end a sequence (uniform over the
@@ -134,6 +145,23 @@ __device__ __forceinline__ void decays(const Pack<float, V> (&la)[TW], int count
 template <int V, typename T>
 __device__ __forceinline__ float value(const Pack<T, V> (&x)[TW], int i, int v, int count) {
     return i < count ? x[i][v] : 0.f;
+}
+
+// Makes the rows new values to the compiler, which otherwise keeps the converted
+// ones of the first walk for the second: twice the registers of the bf16 rows.
+template <int V, typename T>
+__device__ __forceinline__ void keep_packed(Pack<T, V> (&x)[TW]) {
+    if constexpr (sizeof(T) == 2 && V > 1) {
+        typedef Pack<T, V> XP;
+        struct Words { uint32_t w[V / 2]; };
+#pragma unroll
+        for (int i = 0; i < TW; ++i) {
+            Words r = __builtin_bit_cast(Words, x[i]);
+#pragma unroll
+            for (int k = 0; k < V / 2; ++k) asm volatile("" : "+v"(r.w[k]));
+            x[i] = __builtin_bit_cast(XP, r);
+        }
+    }
 }
 
 template <int V>
@@ -196,19 +224,31 @@ __device__ __forceinline__ void empty_seqs(const Seqs& sq, const float* from, fl
     }
 }
 
-// A workgroup's job: a tile of the chain by ticket, or (one tile in all) its own
-// number.  Jobs at and past `jobs` look after the empty sequences.
-__device__ __forceinline__ int take_job(uint32_t* ticket, int* lds) {
-    if (!ticket) return (int)blockIdx.x;
-    if (threadIdx.x == 0) *lds = (int)atomicAdd(ticket, 1u);
+// A workgroup's column block and tile (counted from the chain's start).  TG
+// neighbouring column blocks share a ticket counter, in a line of its own, and
+// take a tile's columns one after the other: with a counter for each they drift
+// apart and rows are read in pieces (forward, bf16, 2 x 32768 x 4096: 446 us
+// against 409), with one for all a short chain waits for its tickets (4096 x 2048:
+// 27 us against 23).
+// No counters: one tile in all.
+constexpr int TG = 4;
+__device__ __forceinline__ void take_tile(uint64_t* tickets, int cblocks, int* lds, int& tile, int& cb) {
+    cb = (int)blockIdx.x % cblocks;
+    tile = 0;
+    if (!tickets) return;
+    const int group = cb / TG, width = cblocks - group * TG < TG ? cblocks - group * TG : TG;
+    if (threadIdx.x == 0)
+        *lds = (int)atomicAdd(reinterpret_cast<unsigned long long*>(tickets + group * LINSCAN_LINE), 1ull);
     __syncthreads();
-    return __builtin_amdgcn_readfirstlane(*lds);
+    const int ticket = __builtin_amdgcn_readfirstlane(*lds);
+    tile = ticket / width;
+    cb = group * TG + ticket - tile * width;
 }
 
 // The tile's (P, E) from its wavefronts', the state handed to it, and its own
 // published: thread j < 64 V does channel j of the workgroup.  In: sp, se; out:
 // sh, the state handed to the tile.  BACK: from the last wavefront to the first.
-template <int V, bool BACK>
+template <int V, bool BACK, int LB>
 __device__ __forceinline__ void chain(const LinScanArgs& p, const float (&sp)[NW][WAVE * V],
                                       const float (&se)[NW][WAVE * V], float (&sh)[WAVE * V], int cb, int tile,
                                       int tiles) {
@@ -226,7 +266,7 @@ __device__ __forceinline__ void chain(const LinScanArgs& p, const float (&sp)[NW
     if (tiles > 1) {
         if (behind > 0) {
             publish(word, P, E);
-            h = look_back(BACK ? word + p.C : word - p.C, BACK ? (int64_t)p.C : -(int64_t)p.C, behind);
+            h = look_back<LB>(BACK ? word + p.C : word - p.C, BACK ? (int64_t)p.C : -(int64_t)p.C, behind);
         }
         if (P >= 0.f || behind == 0 || P != P) publish(word, -1.f, apply(P, E, h));
     }
@@ -235,16 +275,18 @@ __device__ __forceinline__ void chain(const LinScanArgs& p, const float (&sp)[NW
 
 // OUT: y and hT too, else the states alone.
 template <typename T, int V, bool OUT>
-__global__ __launch_bounds__(BT) void linscan_fwd_kernel(LinScanArgs p, int tiles, int cblocks, uint32_t* ticket) {
+__global__ __launch_bounds__(BT) void linscan_fwd_kernel(LinScanArgs p, int tiles, int cblocks, uint64_t* tickets) {
     __shared__ float sp[NW][WAVE * V], se[NW][WAVE * V], sh[WAVE * V];
-    __shared__ int s_job;
+    __shared__ int s_tile;
     const Seqs sq{p.cu, p.N, p.T, p.eq};
-    const int job = take_job(ticket, &s_job), jobs = tiles * cblocks;
-    if (job >= jobs) {
-        if (OUT && p.hT) empty_seqs(sq, p.h0, p.hT, p.C, job - jobs, gridDim.x - jobs);
+    const int jobs = tiles * cblocks;
+    if ((int)blockIdx.x >= jobs) {
+        if (OUT && p.hT) empty_seqs(sq, p.h0, p.hT, p.C, blockIdx.x - jobs, gridDim.x - jobs);
         return;
     }
-    const int tile = job / cblocks, cb = job - tile * cblocks;
+    int tile, cb;
+    take_tile(tickets, cblocks, &s_tile, tile, cb);
+    if (tile >= tiles) return;
     const int lane = threadIdx.x % WAVE, wv = __builtin_amdgcn_readfirstlane(threadIdx.x / WAVE);
     const int at = (cb * WAVE + lane) * V, c = column<V>(at, p.C);
     const int t0 = tile * TT + wv * TW;
@@ -256,10 +298,11 @@ __global__ __launch_bounds__(BT) void linscan_fwd_kernel(LinScanArgs p, int tile
     float a[TW][V], P[V], E[V], h[V];
     decays<V>(la, ed.count, a);
     run_forward<V>(p, sq, ed, t0, c, a, x, P, E);
+    keep_packed<V>(x);
 #pragma unroll
     for (int v = 0; v < V; ++v) sp[wv][lane * V + v] = P[v], se[wv][lane * V + v] = E[v];
     __syncthreads();
-    chain<V, false>(p, sp, se, sh, cb, tile, tiles);
+    chain<V, false, 4>(p, sp, se, sh, cb, tile, tiles);
     __syncthreads();
     if (at >= p.C) return;
 #pragma unroll
@@ -276,22 +319,25 @@ __global__ __launch_bounds__(BT) void linscan_fwd_kernel(LinScanArgs p, int tile
         if (ed.first >> i & 1) load_state<V>(p.h0, p.C, sq.find(t0 + i), c, h);
 #pragma unroll
         for (int v = 0; v < V; ++v) h[v] = a[i][v] * h[v] + x[i][v];
-        store_v<V>(y + (int64_t)i * p.C + (uint32_t)c, h);
+        store_nt<V>(y + (int64_t)i * p.C + (uint32_t)c, h);
         if ((ed.last >> i & 1) && p.hT) store_v<V>(p.hT + (int64_t)sq.find(t0 + i) * p.C + c, h);
     }
 }
 
 template <typename T, int V>
-__global__ __launch_bounds__(BT) void linscan_bwd_kernel(LinScanArgs p, int tiles, int cblocks, uint32_t* ticket) {
+__global__ __launch_bounds__(BT, 4) void linscan_bwd_kernel(LinScanArgs p, int tiles, int cblocks, uint64_t* tickets) {
     __shared__ float sp[NW][WAVE * V], se[NW][WAVE * V], rp[NW][WAVE * V], re[NW][WAVE * V], sh[WAVE * V];
-    __shared__ int s_job;
+    __shared__ int s_tile;
     const Seqs sq{p.cu, p.N, p.T, p.eq};
-    const int job = take_job(ticket, &s_job), jobs = tiles * cblocks;
-    if (job >= jobs) {
-        if (p.hT) empty_seqs(sq, p.dhT, p.hT, p.C, job - jobs, gridDim.x - jobs);
+    const int jobs = tiles * cblocks;
+    if ((int)blockIdx.x >= jobs) {
+        if (p.hT) empty_seqs(sq, p.dhT, p.hT, p.C, blockIdx.x - jobs, gridDim.x - jobs);
         return;
     }
-    const int back = job / cblocks, cb = job - back * cblocks, tile = tiles - 1 - back;
+    int tile, cb;
+    take_tile(tickets, cblocks, &s_tile, tile, cb);
+    tile = tiles - 1 - tile;
+    if (tile < 0) return;
     const int lane = threadIdx.x % WAVE, wv = __builtin_amdgcn_readfirstlane(threadIdx.x / WAVE);
     const int at = (cb * WAVE + lane) * V, c = column<V>(at, p.C);
     const int t0 = tile * TT + wv * TW;
@@ -311,10 +357,12 @@ __global__ __launch_bounds__(BT) void linscan_bwd_kernel(LinScanArgs p, int tile
 #pragma unroll
     for (int v = 0; v < V; ++v) rp[wv][lane * V + v] = P[v], re[wv][lane * V + v] = E[v];
     run_forward<V>(p, sq, ed, t0, c, a, x, P, E);
+    keep_packed<V>(x);
+    keep_packed<V>(dy);
 #pragma unroll
     for (int v = 0; v < V; ++v) sp[wv][lane * V + v] = P[v], se[wv][lane * V + v] = E[v];
     __syncthreads();
-    chain<V, true>(p, rp, re, sh, cb, tile, tiles);
+    chain<V, true, sizeof(T) == 4 ? 2 : 4>(p, rp, re, sh, cb, tile, tiles);
     // the state before every token of the run
     for (int w = wv / SW * SW; w < wv; ++w)
 #pragma unroll
@@ -345,13 +393,13 @@ __global__ __launch_bounds__(BT) void linscan_bwd_kernel(LinScanArgs p, int tile
         float d[V], dl[V];
 #pragma unroll
         for (int v = 0; v < V; ++v) d[v] = dy[i][v] + g[v];
-        store_v<V>(dx + (int64_t)i * p.C + (uint32_t)c, d);
+        store_nt<V>(dx + (int64_t)i * p.C + (uint32_t)c, d);
 #pragma unroll
         for (int v = 0; v < V; ++v) {
             g[v] = a[i][v] * d[v];
             dl[v] = g[v] * hb[i][v];
         }
-        store_v<V>(dla + (int64_t)i * p.C + (uint32_t)c, dl);
+        store_nt<V>(dla + (int64_t)i * p.C + (uint32_t)c, dl);
         if ((ed.first >> i & 1) && p.hT) store_v<V>(p.hT + (int64_t)sq.find(t0 + i) * p.C + c, g);
     }
 }
@@ -391,14 +439,14 @@ hipError_t run_chain(K kernel, const LinScanArgs& a, bool empties, hipStream_t s
     const int tiles = tiles_of(a.T), cblocks = (a.C + WAVE * V - 1) / (WAVE * V);
     const int64_t blocks = (int64_t)tiles * cblocks + (empties ? empty_blocks(a.N) : 0);
     if (blocks == 0) return hipSuccess;
-    uint32_t* ticket = nullptr;
+    uint64_t* tickets = nullptr;
     if (tiles > 1) {
-        ticket = reinterpret_cast<uint32_t*>(a.word + (int64_t)tiles * a.C);
-        const int64_t words = (int64_t)tiles * a.C;
-        hipLaunchKernelGGL(linscan_clear_kernel, dim3((unsigned)((words + 511) / 512)), dim3(256), 0, st, a.word, words,
-                           ticket);
+        const int64_t words = (int64_t)tiles * a.C, counters = (int64_t)cblocks * LINSCAN_LINE;
+        tickets = a.word + words;
+        hipLaunchKernelGGL(linscan_clear_kernel, dim3((unsigned)((words + counters + 511) / 512)), dim3(256), 0, st,
+                           a.word, words, counters);
     }
-    hipLaunchKernelGGL(kernel, dim3((unsigned)blocks), dim3(BT), 0, st, a, tiles, cblocks, ticket);
+    hipLaunchKernelGGL(kernel, dim3((unsigned)blocks), dim3(BT), 0, st, a, tiles, cblocks, tickets);
     return hipGetLastError();
 }
 
@@ -412,7 +460,7 @@ hipError_t fwd(const LinScanArgs& a, bool out, hipStream_t st) {
 
 hipError_t launch_linscan_fwd(const LinScanArgs& a, bool out, hipStream_t st) {
     if (a.C < 4) return a.dtype == 1 ? fwd<bf16, 1>(a, out, st) : fwd<float, 1>(a, out, st);
-    return a.dtype == 1 ? fwd<bf16, 4>(a, out, st) : fwd<float, 2>(a, out, st);
+    return a.dtype == 1 ? fwd<bf16, 2>(a, out, st) : fwd<float, 2>(a, out, st);
 }
 
 hipError_t launch_linscan_bwd(const LinScanArgs& a, hipStream_t st) {

@@ -43,6 +43,25 @@ template <int V, typename T> __device__ __forceinline__ void get_v(const Pack<T,
 #pragma unroll
     for (int i = 0; i < V; ++i) v[i] = r[i];
 }
+// The same past the caches: for data that is touched once.
+template <int V, typename T> __device__ __forceinline__ Pack<T, V> load_nt(const T* p) {
+    Pack<T, V> r;
+#pragma unroll
+    for (int k = 0; k < V / Pack<T, V>::N; ++k)
+        r.part[k] = __builtin_nontemporal_load(reinterpret_cast<const typename Pack<T, V>::vec*>(p) + k);
+    return r;
+}
+template <int V, typename T> __device__ __forceinline__ void store_nt(T* p, const float (&v)[V]) {
+    typename Pack<T, V>::vec* q = reinterpret_cast<typename Pack<T, V>::vec*>(p);
+#pragma unroll
+    for (int k = 0; k < V / Pack<T, V>::N; ++k) {
+        typename Pack<T, V>::vec r;
+#pragma unroll
+        for (int i = 0; i < Pack<T, V>::N; ++i) r[i] = from_f32<T>(v[k * Pack<T, V>::N + i]);
+        __builtin_nontemporal_store(r, q + k);
+    }
+}
+
 // First column of the lane whose columns start at c, in a row of C >= V.
 template <int V> __device__ __forceinline__ int column(int c, int C) { return c + V <= C ? c : C - V; }
 
