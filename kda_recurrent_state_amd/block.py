@@ -164,6 +164,14 @@ def _apart(out, *inputs):
                 raise ValueError("an output overlaps another tensor of the call")
 
 
+def _new(like):
+    """An uninitialised contiguous tensor of like's shape (empty_like is the
+    quicker call, and keeps the strides it is given)."""
+    if like.is_contiguous():
+        return torch.empty_like(like)
+    return torch.empty(like.shape, dtype=like.dtype, device=like.device)
+
+
 def _p(t):
     return None if t is None else t.data_ptr()
 
@@ -226,7 +234,7 @@ def _scan(x, log_a, h0, cu_seqlens, num_seqs, out, final_state, states, workspac
         _full(final_state, "final_state", torch.float32, (N, C))
     _same_device(x, log_a=log_a, h0=h0, cu_seqlens=cu_seqlens, out=out, states=states,
                  final_state=final_state if given else None, workspace=workspace)
-    y = torch.empty((T, C), dtype=x.dtype, device=x.device) if out is None else out
+    y = _new(x) if out is None else out
     hT = final_state if given else torch.empty((N, C), dtype=torch.float32, device=x.device) if final_state else None
     for o in (out, hT if given else None, states):
         if o is not None:
@@ -280,8 +288,8 @@ def scan_bwd(x, log_a, dy, h0=None, cu_seqlens=None, dh_T=None, *, num_seqs: int
     _full(states, "states", torch.float32, (-(-T // SCAN_STATE_EVERY), C))
     _same_device(x, log_a=log_a, dy=dy, h0=h0, cu_seqlens=cu_seqlens, dh_T=dh_T, states=states, workspace=workspace)
     dev = x.device
-    dx = torch.empty((T, C), dtype=x.dtype, device=dev)
-    dla = torch.empty((T, C), dtype=torch.float32, device=dev)
+    dx = _new(x)
+    dla = _new(log_a)
     dh0 = torch.empty((N, C), dtype=torch.float32, device=dev) if initial_state_grad else None
     ref = ctypes.byref(d)
     ws = _workspace(lib, lib.kda_scan_workspace_size, (ref, 1), workspace, dev)
@@ -307,7 +315,7 @@ def scan_step(x, log_a, h, *, out=None, h_out=None):
     _full(out, "out", x.dtype, (N, C))
     _same_device(x, log_a=log_a, h=h, h_out=h_out, out=out)
     ho = h if h_out is None else h_out
-    y = torch.empty((N, C), dtype=x.dtype, device=x.device) if out is None else out
+    y = _new(x) if out is None else out
     if out is not None:
         _apart(out, x, log_a, h, h_out)
     if h_out is not None and h_out is not h:
@@ -352,7 +360,7 @@ def conv_fwd(x, weight, bias=None, state=None, cu_seqlens=None, *, num_seqs: int
         _full(final_state, "final_state", x.dtype, (N, W - 1, C))
     _same_device(x, weight=weight, bias=bias, state=state, cu_seqlens=cu_seqlens, out=out,
                  final_state=final_state if given else None)
-    y = torch.empty((T, C), dtype=x.dtype, device=x.device) if out is None else out
+    y = _new(x) if out is None else out
     sT = final_state if given else torch.empty((N, W - 1, C), dtype=x.dtype, device=x.device) if final_state else None
     for o in (out, sT if given else None):
         if o is not None:
@@ -377,8 +385,8 @@ def conv_bwd(x, weight, dy, bias=None, state=None, cu_seqlens=None, dstate_T=Non
     _same_device(x, weight=weight, dy=dy, bias=bias, state=state, cu_seqlens=cu_seqlens, dstate_T=dstate_T,
                  workspace=workspace)
     dev = x.device
-    dx = torch.empty((T, C), dtype=x.dtype, device=dev)
-    dw = torch.empty((C, W), dtype=torch.float32, device=dev)
+    dx = _new(x)
+    dw = _new(weight)
     db = torch.empty((C,), dtype=torch.float32, device=dev)
     ds = torch.empty((N, W - 1, C), dtype=x.dtype, device=dev) if initial_state_grad else None
     ref = ctypes.byref(d)
@@ -405,7 +413,7 @@ def conv_step(x, weight, state, bias=None, *, activation: str | None = "silu", o
     _full(out, "out", x.dtype, (N, C))
     _same_device(x, weight=weight, state=state, bias=bias, state_out=state_out, out=out)
     so = state if state_out is None else state_out
-    y = torch.empty((N, C), dtype=x.dtype, device=x.device) if out is None else out
+    y = _new(x) if out is None else out
     if out is not None:
         _apart(out, x, state, state_out)
     if state_out is not None and state_out is not state:
@@ -438,7 +446,7 @@ def norm_gate_fwd(x, weight=None, gate=None, *, activation: str = "sigmoid", eps
     d = _norm_gate_dims(x, weight, gate, activation, eps)
     _full(out, "out", x.dtype, x.shape)
     _same_device(x, weight=weight, gate=gate, out=out)
-    y = torch.empty(x.shape, dtype=x.dtype, device=x.device) if out is None else out
+    y = _new(x) if out is None else out
     if out is not None:
         _apart(out, gate, *(() if out.data_ptr() == x.data_ptr() and x.is_contiguous() else (x,)))
     _launch(lib.kda_norm_gate_fwd, lib, x.device, (ctypes.byref(d), _p(x), _p(weight), _p(gate), _p(y)))
@@ -453,8 +461,8 @@ def norm_gate_bwd(x, weight, dy, gate=None, *, activation: str = "sigmoid", eps:
     d = _norm_gate_dims(x, weight, gate, activation, eps, _given(dy, "dy"))
     _same_device(x, weight=weight, dy=dy, gate=gate, workspace=workspace)
     dev = x.device
-    dx = torch.empty(x.shape, dtype=x.dtype, device=dev)
-    dg = None if gate is None else torch.empty(x.shape, dtype=x.dtype, device=dev)
+    dx = _new(x)
+    dg = None if gate is None else _new(x)
     dw = None if weight is None else torch.empty(x.shape[2], dtype=torch.float32, device=dev)
     ref = ctypes.byref(d)
     ws = None if dw is None else _workspace(lib, lib.kda_norm_gate_bwd_workspace_size, (ref,), workspace, dev)
@@ -497,8 +505,8 @@ def residual_norm_fwd(x, residual, weight, *, scale: float = 1.0, channel_scale=
     _full(out, "out", x.dtype, x.shape)
     _full(residual_out, "residual_out", residual.dtype, x.shape)
     _same_device(x, residual=residual, weight=weight, channel_scale=channel_scale, out=out, residual_out=residual_out)
-    y = torch.empty(x.shape, dtype=x.dtype, device=x.device) if out is None else out
-    r = torch.empty(x.shape, dtype=residual.dtype, device=x.device) if residual_out is None else residual_out
+    y = _new(x) if out is None else out
+    r = _new(residual) if residual_out is None else residual_out
     if out is not None:
         _apart(out, x, residual, residual_out)
     if residual_out is not None:
@@ -524,8 +532,8 @@ def residual_norm_bwd(x, residual_out, weight, dy, dresidual_out=None, *, scale:
     _same_device(residual_out, x=x, weight=weight, channel_scale=channel_scale, dy=dy, dresidual_out=dresidual_out,
                  workspace=workspace)
     dev, shape = residual_out.device, residual_out.shape
-    dx = torch.empty(shape, dtype=like.dtype, device=dev)
-    dr = torch.empty(shape, dtype=residual_out.dtype, device=dev)
+    dx = _new(like)
+    dr = _new(residual_out)
     dw = torch.empty(shape[1], dtype=torch.float32, device=dev)
     dc = None if channel_scale is None else torch.empty(shape[1], dtype=torch.float32, device=dev)
     ref = ctypes.byref(d)

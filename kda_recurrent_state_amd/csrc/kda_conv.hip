@@ -11,7 +11,7 @@
 // HBM-bound: a thread owns V adjacent channels of a strip of consecutive tokens
 // and slides the W-token window along it in registers, so every row is read
 // once and the strip's W - 1 leading rows (backward: 2 (W - 1)) once more,
-// from cache.  Groups of 8 tokens are loaded together ahead of their use.
+// from cache.  Groups of tokens are loaded together ahead of their use.
 // Groups that a sequence's edge crosses take a path of their own, which
 // fetches each tap where the sequence says it is.
 #include "kda_block.hpp"
@@ -21,23 +21,24 @@ namespace kda {
 namespace {
 
 constexpr int BT = 256;
-constexpr int GRP = 8;  // tokens loaded together
+constexpr int GRP = 8, GRB = 4;  // tokens loaded together, forward and backward
 
-__device__ __forceinline__ float act_f(float z, int silu) { return silu ? z * sigmoid_f(z) : z; }
+template <bool SILU> __device__ __forceinline__ float act_f(float z) { return SILU ? z * sigmoid_f(z) : z; }
 
 // One thread's view: V channels from c of the packed rows of x and the states.
 template <typename T, int V, int W>
 struct Taps {
-    const T* x;      // channel c of token 0
-    const T* state;  // channel c of state row 0, or null
+    const T* x;
+    const T* state;  // may be null
     int64_t xs;
     int C;
+    uint32_t c;
     // row `pos` (from -(W-1)) of sequence n whose tokens start at beg
     __device__ __forceinline__ void row(int n, int beg, int pos, float (&v)[V]) const {
         if (pos >= 0) {
-            get_v<V>(load_v<V>(x + (int64_t)(beg + pos) * xs), v);
+            get_v<V>(load_v<V>(x + (int64_t)(beg + pos) * xs + c), v);
         } else if (state) {
-            get_v<V>(load_v<V>(state + ((int64_t)n * (W - 1) + (W - 1 + pos)) * C), v);
+            get_v<V>(load_v<V>(state + ((int64_t)n * (W - 1) + (W - 1 + pos)) * C + c), v);
         } else {
             zero_v<V>(v);
         }
@@ -56,19 +57,21 @@ __device__ __forceinline__ void load_weight(const ConvArgs& a, int c, float (&w)
     else zero_v<V>(b);
 }
 
-template <typename T, int V, int W>
-__global__ __launch_bounds__(BT) void conv_fwd_kernel(ConvArgs a, int G, int L, int strip_blocks) {
+template <typename T, int V, int W, bool SILU, bool UNI>
+__global__ __launch_bounds__(BT) void conv_fwd_kernel(ConvArgs a, int G, int L, int cblocks, int state_blocks) {
     const Seqs sq{a.cu, a.N, a.T, a.eq};
-    const int cl = threadIdx.x % G, spb = BT / G, sl = threadIdx.x / G;
-    const int at = ((int)blockIdx.y * G + cl) * V;
+    const int cl = threadIdx.x % G, spb = BT / G;
+    const int sl = UNI ? __builtin_amdgcn_readfirstlane(threadIdx.x / WAVE) : threadIdx.x / G;
+    // a token's columns by neighbouring workgroups, so that rows are read whole
+    const int bx = (int)blockIdx.x / cblocks - state_blocks, at = ((int)blockIdx.x % cblocks * G + cl) * V;
     if (at >= a.C) return;
     const int c = column<V>(at, a.C);
-    const Taps<T, V, W> tp{(const T*)a.x + c, a.state ? (const T*)a.state + c : nullptr, a.xs, a.C};
+    const Taps<T, V, W> tp{(const T*)a.x, (const T*)a.state, a.xs, a.C, (uint32_t)c};
 
-    if ((int)blockIdx.x >= strip_blocks) {  // the sequences' final states
+    if (bx < 0) {  // the sequences' final states
         const int64_t rows = (int64_t)a.N * (W - 1);
-        for (int64_t r = (int64_t)(blockIdx.x - strip_blocks) * spb + sl; r < rows;
-             r += (int64_t)(gridDim.x - strip_blocks) * spb) {
+        for (int64_t r = (int64_t)(bx + state_blocks) * spb + sl; r < rows;
+             r += (int64_t)state_blocks * spb) {
             const int n = (int)(r / (W - 1)), i = (int)(r % (W - 1)), beg = sq.start(n);
             const int len = sq.start(n + 1) - beg;
             float v[V];
@@ -79,7 +82,7 @@ __global__ __launch_bounds__(BT) void conv_fwd_kernel(ConvArgs a, int G, int L, 
     }
 
     const int tend = sq.end();
-    const int64_t t64 = ((int64_t)blockIdx.x * spb + sl) * L;
+    const int64_t t64 = ((int64_t)bx * spb + sl) * L;
     if (t64 >= tend) return;
     int t = (int)t64;
     const int stop = (tend - t > L) ? t + L : tend;
@@ -92,7 +95,7 @@ __global__ __launch_bounds__(BT) void conv_fwd_kernel(ConvArgs a, int G, int L, 
         if (t - beg >= W - 1) {
             Pack<T, V> r[W - 1];
 #pragma unroll
-            for (int k = 0; k < W - 1; ++k) r[k] = load_v<V>(tp.x + (int64_t)(t - (W - 1) + k) * a.xs);
+            for (int k = 0; k < W - 1; ++k) r[k] = load_v<V>(tp.x + (int64_t)(t - (W - 1) + k) * a.xs + tp.c);
 #pragma unroll
             for (int k = 0; k < W - 1; ++k) get_v<V>(r[k], win[k]);
         } else {
@@ -110,19 +113,19 @@ __global__ __launch_bounds__(BT) void conv_fwd_kernel(ConvArgs a, int G, int L, 
 #pragma unroll
             for (int j = 0; j < W - 1; ++j) z[i] += w[i][j] * win[j][i];
             z[i] += w[i][W - 1] * xv[i];
-            z[i] = act_f(z[i], a.silu);
+            z[i] = act_f<SILU>(z[i]);
 #pragma unroll
             for (int j = 0; j < W - 2; ++j) win[j][i] = win[j + 1][i];
             win[W - 2][i] = xv[i];
         }
-        store_v<V>((T*)a.y + (int64_t)u * a.C + c, z);
+        store_nt<V>((T*)a.y + (int64_t)u * a.C + tp.c, z);
     };
 
     while (t < stop) {
         if (t + GRP <= stop && t + GRP <= end) {
             Pack<T, V> xv[GRP];
 #pragma unroll
-            for (int i = 0; i < GRP; ++i) xv[i] = load_v<V>(tp.x + (int64_t)(t + i) * a.xs);
+            for (int i = 0; i < GRP; ++i) xv[i] = load_v<V>(tp.x + (int64_t)(t + i) * a.xs + tp.c);
 #pragma unroll
             for (int i = 0; i < GRP; ++i) step(t + i, xv[i]);
             t += GRP;
@@ -137,24 +140,28 @@ __global__ __launch_bounds__(BT) void conv_fwd_kernel(ConvArgs a, int G, int L, 
                     if (end <= t) end = t + 1;  // offsets out of order: still one token at a time
                     refill();
                 }
-                step(t, load_v<V>(tp.x + (int64_t)t * a.xs));
+                step(t, load_v<V>(tp.x + (int64_t)t * a.xs + tp.c));
             }
         }
     }
 }
 
+// UNI below: a strip is a whole wavefront's (G = 64), so its position and its rows'
+// addresses stay in scalar registers (the backward issues 38 vector instructions
+// an element otherwise, and these bound it).
+
 // dy and z to dz
-__device__ __forceinline__ float dz_of(float dy, float z, int silu) {
-    if (!silu) return dy;
+template <bool SILU> __device__ __forceinline__ float dz_of(float dy, float z) {
+    if (!SILU) return dy;
     const float s = sigmoid_f(z);
     return dy * (s * (1.f + z * (1.f - s)));
 }
 
 // dz of token `pos` of sequence n (beg), from its taps
-template <typename T, int V, int W>
+template <typename T, int V, int W, bool SILU>
 __device__ __forceinline__ void dz_at(const ConvArgs& a, const Taps<T, V, W>& tp, const T* dyp, const float (&w)[V][W],
                                       const float (&b)[V], int n, int beg, int pos, float (&dz)[V]) {
-    const Pack<T, V> dy = load_v<V>(dyp + (int64_t)(beg + pos) * a.ds);
+    const Pack<T, V> dy = load_v<V>(dyp + (int64_t)(beg + pos) * a.ds + tp.c);
     float z[V];
 #pragma unroll
     for (int i = 0; i < V; ++i) z[i] = b[i];
@@ -166,22 +173,23 @@ __device__ __forceinline__ void dz_at(const ConvArgs& a, const Taps<T, V, W>& tp
         for (int i = 0; i < V; ++i) z[i] += w[i][j] * v[i];
     }
 #pragma unroll
-    for (int i = 0; i < V; ++i) dz[i] = dz_of(dy[i], z[i], a.silu);
+    for (int i = 0; i < V; ++i) dz[i] = dz_of<SILU>(dy[i], z[i]);
 }
 
-// Workgroups [0, strip_blocks) walk strips of tokens; the rest form the rows of
-// dstate.  Both add the products x_s dz_{s+k} of the rows they own to their
+// The first state_blocks rows of workgroups form the rows of dstate, the others
+// walk strips of tokens.  Both add the products x_s dz_{s+k} of the rows they own to their
 // workgroup's partial dweight.
-template <typename T, int V, int W>
-__global__ __launch_bounds__(BT) void conv_bwd_kernel(ConvArgs a, int G, int L, int strip_blocks) {
+template <typename T, int V, int W, bool SILU, bool UNI>
+__global__ __launch_bounds__(BT) void conv_bwd_kernel(ConvArgs a, int G, int L, int cblocks, int state_blocks) {
     __shared__ float lds[BT * V];
     const Seqs sq{a.cu, a.N, a.T, a.eq};
-    const int cl = threadIdx.x % G, spb = BT / G, sl = threadIdx.x / G;
-    const int c0 = ((int)blockIdx.y * G + cl) * V;
+    const int cl = threadIdx.x % G, spb = BT / G;
+    const int sl = UNI ? __builtin_amdgcn_readfirstlane(threadIdx.x / WAVE) : threadIdx.x / G;
+    const int bx = (int)blockIdx.x / cblocks - state_blocks, c0 = ((int)blockIdx.x % cblocks * G + cl) * V;
     const bool live = c0 < a.C;  // idle lanes stay for the sums at the end
     const int c = column<V>(c0, a.C);
-    const Taps<T, V, W> tp{(const T*)a.x + c, a.state ? (const T*)a.state + c : nullptr, a.xs, a.C};
-    const T* dyp = (const T*)a.dy + c;
+    const Taps<T, V, W> tp{(const T*)a.x, (const T*)a.state, a.xs, a.C, (uint32_t)c};
+    const T* dyp = (const T*)a.dy;
 
     float w[V][W], b[V];
     load_weight<V, W>(a, c, w, b);
@@ -202,7 +210,7 @@ __global__ __launch_bounds__(BT) void conv_bwd_kernel(ConvArgs a, int G, int L, 
             const int p = pos + k;
             if (p < 0 || p >= len) continue;
             float dz[V];
-            dz_at<T, V, W>(a, tp, dyp, w, b, n, beg, p, dz);
+            dz_at<T, V, W, SILU>(a, tp, dyp, w, b, n, beg, p, dz);
 #pragma unroll
             for (int i = 0; i < V; ++i) {
                 dx[i] += w[i][W - 1 - k] * dz[i];
@@ -212,20 +220,20 @@ __global__ __launch_bounds__(BT) void conv_bwd_kernel(ConvArgs a, int G, int L, 
         }
     };
 
-    if (live && (int)blockIdx.x >= strip_blocks) {
+    if (live && bx < 0) {
         const int64_t rows = (int64_t)a.N * (W - 1);
-        for (int64_t r = (int64_t)(blockIdx.x - strip_blocks) * spb + sl; r < rows;
-             r += (int64_t)(gridDim.x - strip_blocks) * spb) {
+        for (int64_t r = (int64_t)(bx + state_blocks) * spb + sl; r < rows;
+             r += (int64_t)state_blocks * spb) {
             const int n = (int)(r / (W - 1)), i = (int)(r % (W - 1)), beg = sq.start(n);
             int len = sq.start(n + 1) - beg;
             if (len < 0) len = 0;
             float dx[V];
             alone(n, beg, len, i - (W - 1), dx);
-            if (a.state_T) store_v<V>((T*)a.state_T + r * a.C + c, dx);
+            if (a.state_T) store_v<V>((T*)a.state_T + r * a.C + tp.c, dx);
         }
     } else if (live) {
         const int tend = sq.end();
-        const int64_t t64 = ((int64_t)blockIdx.x * spb + sl) * L;
+        const int64_t t64 = ((int64_t)bx * spb + sl) * L;
         int t = t64 < tend ? (int)t64 : tend;
         const int stop = (tend - t > L) ? t + L : tend;
         int n = 0, beg = 0, end = 0;
@@ -239,13 +247,13 @@ __global__ __launch_bounds__(BT) void conv_bwd_kernel(ConvArgs a, int G, int L, 
                 if (end <= t) end = t + 1;
                 have = false;
             }
-            if (t + GRP <= stop && t - (W - 1) >= beg && t + GRP + (W - 1) <= end) {
+            if (t + GRB <= stop && t - (W - 1) >= beg && t + GRB + (W - 1) <= end) {
                 if (!have) {
                     Pack<T, V> r[2 * (W - 1)], d[W - 1];  // x rows from t - W + 1, dy rows from t
 #pragma unroll
-                    for (int k = 0; k < 2 * (W - 1); ++k) r[k] = load_v<V>(tp.x + (int64_t)(t - (W - 1) + k) * a.xs);
+                    for (int k = 0; k < 2 * (W - 1); ++k) r[k] = load_v<V>(tp.x + (int64_t)(t - (W - 1) + k) * a.xs + tp.c);
 #pragma unroll
-                    for (int k = 0; k < W - 1; ++k) d[k] = load_v<V>(dyp + (int64_t)(t + k) * a.ds);
+                    for (int k = 0; k < W - 1; ++k) d[k] = load_v<V>(dyp + (int64_t)(t + k) * a.ds + tp.c);
 #pragma unroll
                     for (int k = 0; k < W - 1; ++k) {
                         get_v<V>(r[W - 1 + k], xw[k]);
@@ -254,19 +262,19 @@ __global__ __launch_bounds__(BT) void conv_bwd_kernel(ConvArgs a, int G, int L, 
                             float z = b[i];
 #pragma unroll
                             for (int j = 0; j < W; ++j) z += w[i][j] * r[k + j][i];
-                            dzw[k][i] = dz_of(d[k][i], z, a.silu);
+                            dzw[k][i] = dz_of<SILU>(d[k][i], z);
                         }
                     }
                     have = true;
                 }
-                Pack<T, V> xv[GRP], dv[GRP];
+                Pack<T, V> xv[GRB], dv[GRB];
 #pragma unroll
-                for (int i = 0; i < GRP; ++i) {
-                    xv[i] = load_v<V>(tp.x + (int64_t)(t + W - 1 + i) * a.xs);
-                    dv[i] = load_v<V>(dyp + (int64_t)(t + W - 1 + i) * a.ds);
+                for (int i = 0; i < GRB; ++i) {
+                    xv[i] = load_v<V>(tp.x + (int64_t)(t + W - 1 + i) * a.xs + tp.c);
+                    dv[i] = load_v<V>(dyp + (int64_t)(t + W - 1 + i) * a.ds + tp.c);
                 }
 #pragma unroll
-                for (int g = 0; g < GRP; ++g) {  // token t + g; the newest row is t + g + W - 1
+                for (int g = 0; g < GRB; ++g) {  // token t + g; the newest row is t + g + W - 1
                     float dx[V];
 #pragma unroll
                     for (int i = 0; i < V; ++i) {
@@ -274,7 +282,7 @@ __global__ __launch_bounds__(BT) void conv_bwd_kernel(ConvArgs a, int G, int L, 
 #pragma unroll
                         for (int j = 0; j < W - 1; ++j) z += w[i][j] * xw[j][i];
                         z += w[i][W - 1] * xv[g][i];
-                        const float dz = dz_of(dv[g][i], z, a.silu);
+                        const float dz = dz_of<SILU>(dv[g][i], z);
                         float v = w[i][0] * dz;
                         dw[0][i] += xw[0][i] * dz;
 #pragma unroll
@@ -292,25 +300,25 @@ __global__ __launch_bounds__(BT) void conv_bwd_kernel(ConvArgs a, int G, int L, 
                         xw[W - 2][i] = xv[g][i];
                         dzw[W - 2][i] = dz;
                     }
-                    store_v<V>((T*)a.y + (int64_t)(t + g) * a.C + c, dx);
+                    store_nt<V>((T*)a.y + (int64_t)(t + g) * a.C + tp.c, dx);
                 }
-                t += GRP;
+                t += GRB;
             } else {
-                int until = stop - t > GRP ? t + GRP : stop;
+                int until = stop - t > GRB ? t + GRB : stop;
                 if (until > end) until = end;
                 have = false;
 #pragma unroll 1
                 for (; t < until; ++t) {
                     float dx[V];
                     alone(n, beg, end - beg, t - beg, dx);
-                    store_v<V>((T*)a.y + (int64_t)t * a.C + c, dx);
+                    store_v<V>((T*)a.y + (int64_t)t * a.C + tp.c, dx);
                 }
             }
         }
     }
 
     // the workgroup's partial sums, strip by strip in order
-    float* out = a.part + (int64_t)blockIdx.x * a.C * (W + 1);
+    float* out = a.part + (int64_t)(bx + state_blocks) * a.C * (W + 1);
 #pragma unroll
     for (int j = 0; j <= W; ++j) {
         __syncthreads();
@@ -331,7 +339,7 @@ __global__ __launch_bounds__(BT) void conv_bwd_kernel(ConvArgs a, int G, int L, 
 // One token per sequence.  The state may be updated in place, so a lane owns its
 // columns alone: the row's last few go one by one (a vector at the row's end that
 // overlapped its neighbour's could read what that lane has already written).
-template <typename T, int V, int W>
+template <typename T, int V, int W, bool SILU>
 __device__ __forceinline__ void conv_step_at(const ConvArgs& a, int n, int c) {
     const T* st = (const T*)a.state + (int64_t)n * (W - 1) * a.C + c;
     Pack<T, V> r[W];
@@ -345,95 +353,134 @@ __device__ __forceinline__ void conv_step_at(const ConvArgs& a, int n, int c) {
     for (int i = 0; i < V; ++i) {
 #pragma unroll
         for (int j = 0; j < W; ++j) z[i] += w[i][j] * r[j][i];
-        z[i] = act_f(z[i], a.silu);
+        z[i] = act_f<SILU>(z[i]);
     }
 #pragma unroll
     for (int k = 0; k < W - 1; ++k) *reinterpret_cast<Pack<T, V>*>(to + (int64_t)k * a.C) = r[k + 1];
     store_v<V>((T*)a.y + (int64_t)n * a.C + c, z);
 }
 
-template <typename T, int V, int W>
+template <typename T, int V, int W, bool SILU, bool UNI>
 __global__ __launch_bounds__(BT) void conv_step_kernel(ConvArgs a) {
     const int ncv = (a.C + V - 1) / V;
     const int64_t id = (int64_t)blockIdx.x * BT + threadIdx.x;
     if (id >= (int64_t)a.N * ncv) return;
     const int n = (int)(id / ncv), c = (int)(id % ncv) * V;
     if (c + V <= a.C) {
-        conv_step_at<T, V, W>(a, n, c);
+        conv_step_at<T, V, W, SILU>(a, n, c);
     } else {
-        for (int i = c; i < a.C; ++i) conv_step_at<T, 1, W>(a, n, i);
+        for (int i = c; i < a.C; ++i) conv_step_at<T, 1, W, SILU>(a, n, i);
     }
 }
 
 // Lanes along the channels, strip length and strip workgroups.
 struct ConvShape { int G, L, cblocks, strips; };
-ConvShape conv_shape(int V, int T, int C, int max_blocks) {
+ConvShape conv_shape(int V, int C) {
     ConvShape s;
     const int ncv = (C + V - 1) / V;
     s.G = 64;
     while (s.G > 8 && s.G / 2 >= ncv) s.G /= 2;
     s.cblocks = (ncv + s.G - 1) / s.G;
-    const int spb = BT / s.G;
-    s.L = 8;
-    while (s.L < 64 && ((int64_t)T + (int64_t)spb * s.L - 1) / ((int64_t)spb * s.L) * s.cblocks > 2048) s.L *= 2;
-    // a bounded number of workgroups along the tokens (the backward's partial rows)
-    while (max_blocks && ((int64_t)T + (int64_t)spb * s.L - 1) / ((int64_t)spb * s.L) > max_blocks) s.L *= 2;
-    s.strips = (int)(((int64_t)T + (int64_t)spb * s.L - 1) / ((int64_t)spb * s.L));
+    s.L = s.strips = 0;
+    return s;
+}
+void set_strips(ConvShape* s, int T, int64_t L) {
+    const int64_t spb = BT / s->G;
+    s->L = (int)L;
+    s->strips = (int)((T + spb * L - 1) / (spb * L));
+}
+// Forward: strips of up to 32 tokens, shorter ones where that leaves fewer than
+// 2048 workgroups.
+ConvShape fwd_shape(int V, int T, int C) {
+    ConvShape s = conv_shape(V, C);
+    int L = 8;
+    const int64_t spb = BT / s.G;
+    while (L < 32 && (T + spb * L - 1) / (spb * L) * s.cblocks > 2048) L *= 2;
+    set_strips(&s, T, L);
+    return s;
+}
+// Backward: strips of one length that fill the GPU (1024 workgroups, four per
+// compute unit) in as many whole rounds as keep them near 128 tokens; at most
+// 512 along the tokens, each of which leaves a partial row.
+ConvShape bwd_shape(int V, int T, int C) {
+    ConvShape s = conv_shape(V, C);
+    const int64_t spb = BT / s.G, fill = spb * 1024;
+    const int64_t one = ((int64_t)T * s.cblocks + fill - 1) / fill, rounds = (one + 127) / 128;
+    int64_t L = one == 0 ? 1 : (one + rounds - 1) / rounds;
+    const int64_t least = (T + spb * 512 - 1) / (spb * 512);
+    if (L < least) L = least;
+    if (L < 2 * GRB) L = 2 * GRB;
+    set_strips(&s, T, (L + GRB - 1) / GRB * GRB);
     return s;
 }
 
-constexpr int BWD_STRIP_BLOCKS = 512;
 int state_blocks(int N) { return N < 32 ? N : 32; }
-// Channels per lane: 16 bytes forwards, 4 backwards (twice the rows and the
-// sums in registers); single channels where the row is shorter.
+// Channels per lane.  Forward: 16 bytes.  Backward: 4, but 2 for bf16 with four
+// taps, whose windows and sums leave too few wavefronts otherwise (32768 x 4096:
+// 190 us against 200; with two taps 30000 x 1536: 98 against 88, and float32 with
+// four 20011 x 2000: 142 against 132).  Single channels in rows shorter than that.
 int fwd_vec(int dtype, int C) { return dtype == 1 ? (C >= 8 ? 8 : 1) : (C >= 4 ? 4 : 1); }
-int bwd_vec(int C) { return C >= 4 ? 4 : 1; }
+int bwd_vec(int dtype, int C, int W) { return C < 4 ? 1 : dtype == 1 && W == 4 ? 2 : 4; }
 
-#define KDA_CONV_RUN(KERNEL, T_, V_, GRID, ...)                                                                       \
-    switch (a.W) {                                                                                                    \
-        case 2: hipLaunchKernelGGL((KERNEL<T_, V_, 2>), GRID, dim3(BT), 0, st, __VA_ARGS__); break;                   \
-        case 3: hipLaunchKernelGGL((KERNEL<T_, V_, 3>), GRID, dim3(BT), 0, st, __VA_ARGS__); break;                   \
-        default: hipLaunchKernelGGL((KERNEL<T_, V_, 4>), GRID, dim3(BT), 0, st, __VA_ARGS__); break;                  \
+// One instance by the taps, the activation, the type and channels per lane (V16
+// for bf16, V32 for fp32, 1 where v is 1) and whether a strip is a wavefront's.
+#define KDA_CONV_RUN(KERNEL, T_, V_, W_, GRID, ...)                                                              \
+    if (a.silu && uni) hipLaunchKernelGGL((KERNEL<T_, V_, W_, true, true>), GRID, dim3(BT), 0, st, __VA_ARGS__); \
+    else if (a.silu) hipLaunchKernelGGL((KERNEL<T_, V_, W_, true, false>), GRID, dim3(BT), 0, st, __VA_ARGS__);  \
+    else if (uni) hipLaunchKernelGGL((KERNEL<T_, V_, W_, false, true>), GRID, dim3(BT), 0, st, __VA_ARGS__);     \
+    else hipLaunchKernelGGL((KERNEL<T_, V_, W_, false, false>), GRID, dim3(BT), 0, st, __VA_ARGS__);
+#define KDA_CONV_WIDTHS(KERNEL, T_, V_, GRID, ...)                                   \
+    {                                                                                \
+        if (a.W == 2) { KDA_CONV_RUN(KERNEL, T_, V_, 2, GRID, __VA_ARGS__) }         \
+        else if (a.W == 3) { KDA_CONV_RUN(KERNEL, T_, V_, 3, GRID, __VA_ARGS__) }    \
+        else { KDA_CONV_RUN(KERNEL, T_, V_, 4, GRID, __VA_ARGS__) }                  \
     }
-// V16 channels per lane for bf16, 4 for fp32, 1 where v is 1
-#define KDA_CONV_TYPES(KERNEL, V16, GRID, ...)                                                                        \
-    if (a.dtype == 1) {                                                                                               \
-        if (v == 1) KDA_CONV_RUN(KERNEL, bf16, 1, GRID, __VA_ARGS__)                                                  \
-        else KDA_CONV_RUN(KERNEL, bf16, V16, GRID, __VA_ARGS__)                                                       \
-    } else {                                                                                                          \
-        if (v == 1) KDA_CONV_RUN(KERNEL, float, 1, GRID, __VA_ARGS__)                                                 \
-        else KDA_CONV_RUN(KERNEL, float, 4, GRID, __VA_ARGS__)                                                        \
+#define KDA_CONV_TYPES(KERNEL, V16, V32, GRID, ...)                                  \
+    if (a.dtype == 1) {                                                              \
+        if (v == 1) KDA_CONV_WIDTHS(KERNEL, bf16, 1, GRID, __VA_ARGS__)              \
+        else KDA_CONV_WIDTHS(KERNEL, bf16, V16, GRID, __VA_ARGS__)                   \
+    } else {                                                                         \
+        if (v == 1) KDA_CONV_WIDTHS(KERNEL, float, 1, GRID, __VA_ARGS__)             \
+        else KDA_CONV_WIDTHS(KERNEL, float, V32, GRID, __VA_ARGS__)                  \
     }
 
 }  // namespace
 
 hipError_t launch_conv_fwd(const ConvArgs& a, hipStream_t st) {
     const int v = fwd_vec(a.dtype, a.C);
-    const ConvShape s = conv_shape(v, a.T, a.C, 0);
+    const ConvShape s = fwd_shape(v, a.T, a.C);
     const int extra = a.state_T ? state_blocks(a.N) : 0;
+    const bool uni = s.G == WAVE;
     if (s.strips + extra == 0) return hipSuccess;
-    const dim3 grid(s.strips + extra, s.cblocks);
-    KDA_CONV_TYPES(conv_fwd_kernel, 8, grid, a, s.G, s.L, s.strips)
+    const dim3 grid((unsigned)((int64_t)(s.strips + extra) * s.cblocks));
+    KDA_CONV_TYPES(conv_fwd_kernel, 8, 4, grid, a, s.G, s.L, s.cblocks, extra)
     return hipGetLastError();
 }
 
-int conv_bwd_parts(int T, int N, int C) {
-    return conv_shape(bwd_vec(C), T, C, BWD_STRIP_BLOCKS).strips + state_blocks(N);
+int conv_bwd_parts(int dtype, int T, int N, int C, int W) {
+    return bwd_shape(bwd_vec(dtype, C, W), T, C).strips + state_blocks(N);
 }
 
 hipError_t launch_conv_bwd(const ConvArgs& a, hipStream_t st) {
-    const int v = bwd_vec(a.C);
-    const ConvShape s = conv_shape(v, a.T, a.C, BWD_STRIP_BLOCKS);
-    const dim3 grid(s.strips + state_blocks(a.N), s.cblocks);
-    KDA_CONV_TYPES(conv_bwd_kernel, 4, grid, a, s.G, s.L, s.strips)
+    const int v = bwd_vec(a.dtype, a.C, a.W);
+    const ConvShape s = bwd_shape(v, a.T, a.C);
+    const int extra = state_blocks(a.N);
+    const bool uni = s.G == WAVE;
+    const dim3 grid((unsigned)((int64_t)(s.strips + extra) * s.cblocks));
+    if (v == 2) {
+        KDA_CONV_RUN(conv_bwd_kernel, bf16, 2, 4, grid, a, s.G, s.L, s.cblocks, extra)
+    } else {
+        KDA_CONV_TYPES(conv_bwd_kernel, 4, 4, grid, a, s.G, s.L, s.cblocks, extra)
+    }
     return hipGetLastError();
 }
 
 hipError_t launch_conv_step(const ConvArgs& a, hipStream_t st) {
     const int v = fwd_vec(a.dtype, a.C);
     const int64_t work = (int64_t)a.N * ((a.C + v - 1) / v);
+    constexpr bool uni = true;  // (one instance)
     const dim3 grid((unsigned)((work + BT - 1) / BT));
-    KDA_CONV_TYPES(conv_step_kernel, 8, grid, a)
+    KDA_CONV_TYPES(conv_step_kernel, 8, 4, grid, a)
     return hipGetLastError();
 }
 

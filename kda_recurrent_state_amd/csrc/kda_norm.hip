@@ -88,13 +88,17 @@ __device__ __forceinline__ void block_partial(const float (&acc)[VPT][V], float*
     }
 }
 
-// Gate activation and its slope.
-__device__ __forceinline__ float gate_act(float g, int silu) {
-    const float s = sigmoid_f(g);
-    return silu ? g * s : s;
+// The gate: none, a logistic function of it, or it times that.  s is its
+// logistic value.
+enum { GATE_NONE, GATE_SIGMOID, GATE_SILU };
+template <int GATE> __device__ __forceinline__ float gate_act(float g, float s) {
+    return GATE == GATE_SILU ? g * s : GATE == GATE_SIGMOID ? s : 1.f;
+}
+template <int GATE> __device__ __forceinline__ float gate_slope(float g, float s) {
+    return GATE == GATE_SILU ? s * (1.f + g * (1.f - s)) : s * (1.f - s);
 }
 
-template <typename T, int V, int G, int VPT>
+template <typename T, int V, int G, int VPT, int GATE>
 __global__ __launch_bounds__(BT) void norm_gate_fwd_kernel(NormGateArgs a) {
     constexpr int RPB = BT / G;
     __shared__ float lds[BT / WAVE];
@@ -110,7 +114,7 @@ __global__ __launch_bounds__(BT) void norm_gate_fwd_kernel(NormGateArgs a) {
         Pack<float, V> wr[VPT];
 #pragma unroll
         for (int j = 0; j < VPT; ++j) xr[j] = load_v<V>(xp + Cols<V, G>(j, g, D).c);
-        if (a.gate)
+        if (GATE)
 #pragma unroll
             for (int j = 0; j < VPT; ++j) gr[j] = load_v<V>(gp + Cols<V, G>(j, g, D).c);
         if (a.weight)
@@ -134,15 +138,15 @@ __global__ __launch_bounds__(BT) void norm_gate_fwd_kernel(NormGateArgs a) {
             if (a.weight)
 #pragma unroll
                 for (int i = 0; i < V; ++i) y[i] *= wr[j][i];
-            if (a.gate)
+            if (GATE)
 #pragma unroll
-                for (int i = 0; i < V; ++i) y[i] *= gate_act(gr[j][i], a.silu);
+                for (int i = 0; i < V; ++i) y[i] *= gate_act<GATE>(gr[j][i], sigmoid_f(gr[j][i]));
             if (cl.live) store_v<V>((T*)a.y + r * D + cl.c, y);
         }
     }
 }
 
-template <typename T, int V, int G, int VPT>
+template <typename T, int V, int G, int VPT, int GATE>
 __global__ __launch_bounds__(BT) void norm_gate_bwd_kernel(NormGateArgs a) {
     constexpr int RPB = BT / G;
     __shared__ float lds[RPB > 1 ? RPB * G * VPT * V : 2 * BT / WAVE];
@@ -168,7 +172,7 @@ __global__ __launch_bounds__(BT) void norm_gate_bwd_kernel(NormGateArgs a) {
             xr[j] = load_v<V>(xp + c);
             dr[j] = load_v<V>(dp + c);
         }
-        if (a.gate)
+        if (GATE)
 #pragma unroll
             for (int j = 0; j < VPT; ++j) gr[j] = load_v<V>(gp + Cols<V, G>(j, g, D).c);
         float sg[VPT][V], sm[2] = {0.f, 0.f};  // sg: the gate's logistic value
@@ -177,11 +181,8 @@ __global__ __launch_bounds__(BT) void norm_gate_bwd_kernel(NormGateArgs a) {
             const Cols<V, G> cl(j, g, D);
 #pragma unroll
             for (int i = 0; i < V; ++i) {
-                float act = 1.f;
-                if (a.gate) {
-                    sg[j][i] = sigmoid_f(gr[j][i]);
-                    act = a.silu ? gr[j][i] * sg[j][i] : sg[j][i];
-                }
+                sg[j][i] = GATE ? sigmoid_f(gr[j][i]) : 1.f;
+                const float act = GATE ? gate_act<GATE>(gr[j][i], sg[j][i]) : 1.f;
                 sm[0] += i >= cl.skip ? xr[j][i] * xr[j][i] : 0.f;
                 sm[1] += i >= cl.skip ? dr[j][i] * act * w[j][i] * xr[j][i] : 0.f;
             }
@@ -196,19 +197,14 @@ __global__ __launch_bounds__(BT) void norm_gate_bwd_kernel(NormGateArgs a) {
 #pragma unroll
             for (int i = 0; i < V; ++i) {
                 const float n = xr[j][i] * rn, dy = dr[j][i];
-                float act = 1.f, slope = 0.f;
-                if (a.gate) {
-                    const float s = sg[j][i];
-                    act = a.silu ? gr[j][i] * s : s;
-                    slope = a.silu ? s * (1.f + gr[j][i] * (1.f - s)) : s * (1.f - s);
-                }
+                const float act = GATE ? gate_act<GATE>(gr[j][i], sg[j][i]) : 1.f;
                 dx[i] = rn * (dy * act * w[j][i] - xr[j][i] * k);
-                dg[i] = dy * n * w[j][i] * slope;
+                if (GATE) dg[i] = dy * n * w[j][i] * gate_slope<GATE>(gr[j][i], sg[j][i]);
                 dw[j][i] += dy * act * n;
             }
             if (cl.live) {
                 store_v<V>((T*)a.y + r * D + cl.c, dx);
-                if (a.gate) store_v<V>((T*)a.dgate + r * D + cl.c, dg);
+                if (GATE) store_v<V>((T*)a.dgate + r * D + cl.c, dg);
             }
         }
     }
@@ -406,9 +402,13 @@ constexpr int BWD_BLOCKS = 1024;     // four workgroups per compute unit; each w
 
 template <typename T, int V>
 void norm_gate_launch(const NormGateArgs& a, bool backward, int blocks, RowShape s, hipStream_t st) {
-#define RUN_NG(V_, G, VPT)                                                                                     \
-    if (backward) hipLaunchKernelGGL((norm_gate_bwd_kernel<T, V_, G, VPT>), dim3(blocks), dim3(BT), 0, st, a); \
-    else hipLaunchKernelGGL((norm_gate_fwd_kernel<T, V_, G, VPT>), dim3(blocks), dim3(BT), 0, st, a)
+#define RUN_NG1(V_, G, VPT, GATE)                                                                                    \
+    if (backward) hipLaunchKernelGGL((norm_gate_bwd_kernel<T, V_, G, VPT, GATE>), dim3(blocks), dim3(BT), 0, st, a); \
+    else hipLaunchKernelGGL((norm_gate_fwd_kernel<T, V_, G, VPT, GATE>), dim3(blocks), dim3(BT), 0, st, a)
+#define RUN_NG(V_, G, VPT)                               \
+    if (!a.gate) { RUN_NG1(V_, G, VPT, GATE_NONE); }     \
+    else if (a.silu) { RUN_NG1(V_, G, VPT, GATE_SILU); } \
+    else { RUN_NG1(V_, G, VPT, GATE_SIGMOID); }
     KDA_ROW_CASES(RUN_NG, V)
 }
 
