@@ -14,6 +14,8 @@
 // from cache.  Groups of tokens are loaded together ahead of their use.
 // Groups that a sequence's edge crosses take a path of their own, which
 // fetches each tap where the sequence says it is.
+#include <type_traits>
+
 #include "kda_block.hpp"
 #include "kda_rows.hpp"
 
@@ -48,11 +50,17 @@ struct Taps {
 // Taps and bias of V channels from c.
 template <int V, int W>
 __device__ __forceinline__ void load_weight(const ConvArgs& a, int c, float (&w)[V][W], float (&b)[V]) {
-    const Pack<float, V * W> wr = load_v<V * W>(a.weight + (int64_t)c * W);
+    const float* wp = a.weight + (int64_t)c * W;
+    if constexpr (V == 1) {
 #pragma unroll
-    for (int i = 0; i < V; ++i)
+        for (int j = 0; j < W; ++j) w[0][j] = wp[j];
+    } else {
+        const Pack<float, V * W> wr = load_v<V * W>(wp);
 #pragma unroll
-        for (int j = 0; j < W; ++j) w[i][j] = wr[i * W + j];
+        for (int i = 0; i < V; ++i)
+#pragma unroll
+            for (int j = 0; j < W; ++j) w[i][j] = wr[i * W + j];
+    }
     if (a.bias) get_v<V>(load_v<V>(a.bias + c), b);
     else zero_v<V>(b);
 }
@@ -360,7 +368,7 @@ __device__ __forceinline__ void conv_step_at(const ConvArgs& a, int n, int c) {
     store_v<V>((T*)a.y + (int64_t)n * a.C + c, z);
 }
 
-template <typename T, int V, int W, bool SILU, bool UNI>
+template <typename T, int V, int W, bool SILU>
 __global__ __launch_bounds__(BT) void conv_step_kernel(ConvArgs a) {
     const int ncv = (a.C + V - 1) / V;
     const int64_t id = (int64_t)blockIdx.x * BT + threadIdx.x;
@@ -420,40 +428,71 @@ int state_blocks(int N) { return N < 32 ? N : 32; }
 // 190 us against 200; with two taps 30000 x 1536: 98 against 88, and float32 with
 // four 20011 x 2000: 142 against 132).  Single channels in rows shorter than that.
 int fwd_vec(int dtype, int C) { return dtype == 1 ? (C >= 8 ? 8 : 1) : (C >= 4 ? 4 : 1); }
-int bwd_vec(int dtype, int C, int W) { return C < 4 ? 1 : dtype == 1 && W == 4 ? 2 : 4; }
+constexpr int bwd_vec(int dtype, int C, int W) { return C < 4 ? 1 : dtype == 1 && W == 4 ? 2 : 4; }
 
-// One instance by the taps, the activation, the type and channels per lane (V16
-// for bf16, V32 for fp32, 1 where v is 1) and whether a strip is a wavefront's.
-#define KDA_CONV_RUN(KERNEL, T_, V_, W_, GRID, ...)                                                              \
-    if (a.silu && uni) hipLaunchKernelGGL((KERNEL<T_, V_, W_, true, true>), GRID, dim3(BT), 0, st, __VA_ARGS__); \
-    else if (a.silu) hipLaunchKernelGGL((KERNEL<T_, V_, W_, true, false>), GRID, dim3(BT), 0, st, __VA_ARGS__);  \
-    else if (uni) hipLaunchKernelGGL((KERNEL<T_, V_, W_, false, true>), GRID, dim3(BT), 0, st, __VA_ARGS__);     \
-    else hipLaunchKernelGGL((KERNEL<T_, V_, W_, false, false>), GRID, dim3(BT), 0, st, __VA_ARGS__);
-#define KDA_CONV_WIDTHS(KERNEL, T_, V_, GRID, ...)                                   \
-    {                                                                                \
-        if (a.W == 2) { KDA_CONV_RUN(KERNEL, T_, V_, 2, GRID, __VA_ARGS__) }         \
-        else if (a.W == 3) { KDA_CONV_RUN(KERNEL, T_, V_, 3, GRID, __VA_ARGS__) }    \
-        else { KDA_CONV_RUN(KERNEL, T_, V_, 4, GRID, __VA_ARGS__) }                  \
-    }
-#define KDA_CONV_TYPES(KERNEL, V16, V32, GRID, ...)                                  \
-    if (a.dtype == 1) {                                                              \
-        if (v == 1) KDA_CONV_WIDTHS(KERNEL, bf16, 1, GRID, __VA_ARGS__)              \
-        else KDA_CONV_WIDTHS(KERNEL, bf16, V16, GRID, __VA_ARGS__)                   \
-    } else {                                                                         \
-        if (v == 1) KDA_CONV_WIDTHS(KERNEL, float, 1, GRID, __VA_ARGS__)             \
-        else KDA_CONV_WIDTHS(KERNEL, float, V32, GRID, __VA_ARGS__)                  \
-    }
+// f(taps, SiLU or not) for the call's.
+template <typename F> void by_taps(const ConvArgs& a, F f) {
+    auto act = [&](auto w) {
+        if (a.silu) f(w, std::true_type{});
+        else f(w, std::false_type{});
+    };
+    if (a.W == 2) act(std::integral_constant<int, 2>{});
+    else if (a.W == 3) act(std::integral_constant<int, 3>{});
+    else act(std::integral_constant<int, 4>{});
+}
+
+template <typename T, int V> void fwd_launch(const ConvArgs& a, hipStream_t st) {
+    const ConvShape s = fwd_shape(V, a.T, a.C);
+    const int extra = a.state_T ? state_blocks(a.N) : 0;
+    const dim3 grid((unsigned)((int64_t)(s.strips + extra) * s.cblocks));
+    if (grid.x == 0) return;
+    by_taps(a, [&](auto w, auto silu) {
+        constexpr int W = decltype(w)::value;
+        constexpr bool SILU = decltype(silu)::value;
+        if constexpr (V > 1)
+            if (s.G == WAVE) {
+                hipLaunchKernelGGL((conv_fwd_kernel<T, V, W, SILU, true>), grid, dim3(BT), 0, st, a, s.G, s.L, s.cblocks,
+                                   extra);
+                return;
+            }
+        hipLaunchKernelGGL((conv_fwd_kernel<T, V, W, SILU, false>), grid, dim3(BT), 0, st, a, s.G, s.L, s.cblocks, extra);
+    });
+}
+
+template <typename T, int V> void bwd_launch(const ConvArgs& a, hipStream_t st) {
+    const ConvShape s = bwd_shape(V, a.T, a.C);
+    const int extra = state_blocks(a.N);
+    const dim3 grid((unsigned)((int64_t)(s.strips + extra) * s.cblocks));
+    by_taps(a, [&](auto w, auto silu) {
+        constexpr int W = decltype(w)::value;
+        constexpr bool SILU = decltype(silu)::value;
+        if constexpr (V == 1 || V == bwd_vec(sizeof(T) == 2, 4, W)) {  // the widths that bwd_vec gives this V
+            if constexpr (V > 1)
+                if (s.G == WAVE) {
+                    hipLaunchKernelGGL((conv_bwd_kernel<T, V, W, SILU, true>), grid, dim3(BT), 0, st, a, s.G, s.L,
+                                       s.cblocks, extra);
+                    return;
+                }
+            hipLaunchKernelGGL((conv_bwd_kernel<T, V, W, SILU, false>), grid, dim3(BT), 0, st, a, s.G, s.L, s.cblocks,
+                               extra);
+        }
+    });
+}
+
+template <typename T, int V> void step_launch(const ConvArgs& a, hipStream_t st) {
+    const int64_t work = (int64_t)a.N * ((a.C + V - 1) / V);
+    by_taps(a, [&](auto w, auto silu) {
+        hipLaunchKernelGGL((conv_step_kernel<T, V, decltype(w)::value, decltype(silu)::value>),
+                           dim3((unsigned)((work + BT - 1) / BT)), dim3(BT), 0, st, a);
+    });
+}
 
 }  // namespace
 
 hipError_t launch_conv_fwd(const ConvArgs& a, hipStream_t st) {
     const int v = fwd_vec(a.dtype, a.C);
-    const ConvShape s = fwd_shape(v, a.T, a.C);
-    const int extra = a.state_T ? state_blocks(a.N) : 0;
-    const bool uni = s.G == WAVE;
-    if (s.strips + extra == 0) return hipSuccess;
-    const dim3 grid((unsigned)((int64_t)(s.strips + extra) * s.cblocks));
-    KDA_CONV_TYPES(conv_fwd_kernel, 8, 4, grid, a, s.G, s.L, s.cblocks, extra)
+    if (a.dtype == 1) v == 1 ? fwd_launch<bf16, 1>(a, st) : fwd_launch<bf16, 8>(a, st);
+    else v == 1 ? fwd_launch<float, 1>(a, st) : fwd_launch<float, 4>(a, st);
     return hipGetLastError();
 }
 
@@ -463,24 +502,15 @@ int conv_bwd_parts(int dtype, int T, int N, int C, int W) {
 
 hipError_t launch_conv_bwd(const ConvArgs& a, hipStream_t st) {
     const int v = bwd_vec(a.dtype, a.C, a.W);
-    const ConvShape s = bwd_shape(v, a.T, a.C);
-    const int extra = state_blocks(a.N);
-    const bool uni = s.G == WAVE;
-    const dim3 grid((unsigned)((int64_t)(s.strips + extra) * s.cblocks));
-    if (v == 2) {
-        KDA_CONV_RUN(conv_bwd_kernel, bf16, 2, 4, grid, a, s.G, s.L, s.cblocks, extra)
-    } else {
-        KDA_CONV_TYPES(conv_bwd_kernel, 4, 4, grid, a, s.G, s.L, s.cblocks, extra)
-    }
+    if (a.dtype == 1) v == 1 ? bwd_launch<bf16, 1>(a, st) : v == 2 ? bwd_launch<bf16, 2>(a, st) : bwd_launch<bf16, 4>(a, st);
+    else v == 1 ? bwd_launch<float, 1>(a, st) : bwd_launch<float, 4>(a, st);
     return hipGetLastError();
 }
 
 hipError_t launch_conv_step(const ConvArgs& a, hipStream_t st) {
     const int v = fwd_vec(a.dtype, a.C);
-    const int64_t work = (int64_t)a.N * ((a.C + v - 1) / v);
-    constexpr bool uni = true;  // (one instance)
-    const dim3 grid((unsigned)((work + BT - 1) / BT));
-    KDA_CONV_TYPES(conv_step_kernel, 8, 4, grid, a)
+    if (a.dtype == 1) v == 1 ? step_launch<bf16, 1>(a, st) : step_launch<bf16, 8>(a, st);
+    else v == 1 ? step_launch<float, 1>(a, st) : step_launch<float, 4>(a, st);
     return hipGetLastError();
 }
 

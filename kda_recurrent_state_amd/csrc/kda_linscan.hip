@@ -59,8 +59,10 @@ __device__ __forceinline__ uint64_t read_word(const uint64_t* word) {
 // nearest first, `behind` of them (>= 1; the last of them always becomes (-1, h)).
 // The nearest LB are read together; after that a poll reads only the farthest
 // again, whose state is the first to become known, and what was not there yet.
-// LB = 4 keeps a chain of 512 tiles ahead of the memory (2 x 32768 x 4096: 409 us;
-// LB = 2: 415, 8: 416, 1: 473); the float32 backward takes 2, for its registers.
+// Forwards LB = 4 keeps a wide chain ahead of the memory (2 x 32768 x 4096: 409 us;
+// LB = 2: 415, 8: 416, 1: 473); narrow ones (fewer than 32 column blocks), which
+// wait for each other more than for memory, take 8 (4096 x 2048: 21 us, 4: 23, 16:
+// 27; 60000 x 64: 38, 4: 46).  Backwards 4, in float32 2 for its registers.
 template <int LB>  // words of the chain read at once
 __device__ __forceinline__ float look_back(const uint64_t* word, int64_t step, int behind) {
     const int far = (behind < LB ? behind : LB) - 1;
@@ -274,7 +276,7 @@ __device__ __forceinline__ void chain(const LinScanArgs& p, const float (&sp)[NW
 }
 
 // OUT: y and hT too, else the states alone.
-template <typename T, int V, bool OUT>
+template <typename T, int V, bool OUT, int LB>
 __global__ __launch_bounds__(BT) void linscan_fwd_kernel(LinScanArgs p, int tiles, int cblocks, uint64_t* tickets) {
     __shared__ float sp[NW][WAVE * V], se[NW][WAVE * V], sh[WAVE * V];
     __shared__ int s_tile;
@@ -302,7 +304,7 @@ __global__ __launch_bounds__(BT) void linscan_fwd_kernel(LinScanArgs p, int tile
 #pragma unroll
     for (int v = 0; v < V; ++v) sp[wv][lane * V + v] = P[v], se[wv][lane * V + v] = E[v];
     __syncthreads();
-    chain<V, false, 4>(p, sp, se, sh, cb, tile, tiles);
+    chain<V, false, LB>(p, sp, se, sh, cb, tile, tiles);
     __syncthreads();
     if (at >= p.C) return;
 #pragma unroll
@@ -450,16 +452,22 @@ hipError_t run_chain(K kernel, const LinScanArgs& a, bool empties, hipStream_t s
     return hipGetLastError();
 }
 
+template <typename T, int V, bool OUT>
+hipError_t fwd(const LinScanArgs& a, hipStream_t st) {
+    const bool empties = OUT && a.hT;
+    if constexpr (V > 1)
+        if (a.C >= 32 * WAVE * V) return run_chain<V>(linscan_fwd_kernel<T, V, OUT, 4>, a, empties, st);
+    return run_chain<V>(linscan_fwd_kernel<T, V, OUT, 8>, a, empties, st);
+}
 template <typename T, int V>
 hipError_t fwd(const LinScanArgs& a, bool out, hipStream_t st) {
-    return out ? run_chain<V>(linscan_fwd_kernel<T, V, true>, a, a.hT != nullptr, st)
-               : run_chain<V>(linscan_fwd_kernel<T, V, false>, a, false, st);
+    return out ? fwd<T, V, true>(a, st) : fwd<T, V, false>(a, st);
 }
 
 }  // namespace
 
 hipError_t launch_linscan_fwd(const LinScanArgs& a, bool out, hipStream_t st) {
-    if (a.C < 4) return a.dtype == 1 ? fwd<bf16, 1>(a, out, st) : fwd<float, 1>(a, out, st);
+    if (a.C < 2) return a.dtype == 1 ? fwd<bf16, 1>(a, out, st) : fwd<float, 1>(a, out, st);
     return a.dtype == 1 ? fwd<bf16, 2>(a, out, st) : fwd<float, 2>(a, out, st);
 }
 

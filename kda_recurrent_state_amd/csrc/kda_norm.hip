@@ -385,7 +385,7 @@ constexpr int BWD_BLOCKS = 1024;     // four workgroups per compute unit; each w
 #define KDA_ROW_CASES(RUN, V)                                                                                  \
     switch (s.g * 16 + s.vpt) {                                                                                \
         case 4 * 16 + 1: RUN(V, 4, 1); break;                                                                  \
-        case 8 * 16 + 1: RUN(V, 8, 1); break;                                                                  \
+        case 8 * 16 + 1: if constexpr (V > 1 || sizeof(T) == 2) { RUN(V, 8, 1); } break;                       \
         default: if constexpr (V > 1) KDA_WIDE_CASES(RUN, V) break;                                            \
     }
 #define KDA_WIDE_CASES(RUN, V)                                                                                 \

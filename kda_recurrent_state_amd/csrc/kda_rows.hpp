@@ -21,6 +21,7 @@ namespace kda {
 // same inputs and store the same bits.
 template <typename T, int V> struct Pack {
     static constexpr int N = V * sizeof(T) <= 16 ? V : 16 / sizeof(T);  // elements of one access
+    static_assert((N & (N - 1)) == 0 && V % N == 0, "an access is a power of two (a vector of 3 takes the room of 4)");
     typedef T vec __attribute__((vector_size(N * sizeof(T)), aligned(sizeof(T))));
     vec part[V / N];
     __device__ __forceinline__ float operator[](int i) const { return (float)part[i / N][i % N]; }
