@@ -192,11 +192,21 @@ def _launch(fn, lib, device, args):
         _check(lib, status)
 
 
-def _workspace(lib, size_fn, args, workspace, device):
+_sizes = {}  # workspace bytes by entry point and dims, of which a program has few
+
+
+def _workspace(lib, name, dims, more, workspace, device):
+    """The caller's workspace, or one of the size that lib.<name>(dims, *more) says."""
     if workspace is None:
-        need = ctypes.c_size_t(0)
-        _check(lib, size_fn(*args, ctypes.byref(need)))
-        return torch.empty(need.value, dtype=torch.uint8, device=device)
+        key = (name, bytes(dims), more)
+        size = _sizes.get(key)
+        if size is None:
+            need = ctypes.c_size_t(0)
+            _check(lib, getattr(lib, name)(ctypes.byref(dims), *more, ctypes.byref(need)))
+            if len(_sizes) >= 4096:
+                _sizes.clear()
+            size = _sizes[key] = need.value
+        return torch.empty(size, dtype=torch.uint8, device=device)
     if not isinstance(workspace, torch.Tensor) or workspace.dtype is not torch.uint8 or workspace.dim() != 1 \
             or not workspace.is_contiguous():
         raise TypeError("workspace must be a contiguous 1-D uint8 tensor")
@@ -240,7 +250,7 @@ def _scan(x, log_a, h0, cu_seqlens, num_seqs, out, final_state, states, workspac
         if o is not None:
             _apart(o, x, log_a, h0, *(t for t in (out, hT, states) if t is not o))
     ref = ctypes.byref(d)
-    ws = _workspace(lib, lib.kda_scan_workspace_size, (ref, 0), workspace, x.device)
+    ws = _workspace(lib, "kda_scan_workspace_size", d, (0,), workspace, x.device)
     _launch(lib.kda_scan_fwd, lib, x.device, (ref, _p(x), _p(log_a), _p(h0), _p(cu_seqlens), _p(y), _p(hT),
                                               _p(states), _p(ws), ws.numel()))
     return y, hT
@@ -292,7 +302,7 @@ def scan_bwd(x, log_a, dy, h0=None, cu_seqlens=None, dh_T=None, *, num_seqs: int
     dla = _new(log_a)
     dh0 = torch.empty((N, C), dtype=torch.float32, device=dev) if initial_state_grad else None
     ref = ctypes.byref(d)
-    ws = _workspace(lib, lib.kda_scan_workspace_size, (ref, 1), workspace, dev)
+    ws = _workspace(lib, "kda_scan_workspace_size", d, (1,), workspace, dev)
     _launch(lib.kda_scan_bwd, lib, dev, (ref, _p(x), _p(log_a), _p(h0), _p(cu_seqlens), _p(states), _p(dy), _p(dh_T),
                                          _p(dx), _p(dla), _p(dh0), _p(ws), ws.numel()))
     return {"dx": dx, "dlog_a": dla, "dh0": dh0}
@@ -390,7 +400,7 @@ def conv_bwd(x, weight, dy, bias=None, state=None, cu_seqlens=None, dstate_T=Non
     db = torch.empty((C,), dtype=torch.float32, device=dev)
     ds = torch.empty((N, W - 1, C), dtype=x.dtype, device=dev) if initial_state_grad else None
     ref = ctypes.byref(d)
-    ws = _workspace(lib, lib.kda_conv_bwd_workspace_size, (ref,), workspace, dev)
+    ws = _workspace(lib, "kda_conv_bwd_workspace_size", d, (), workspace, dev)
     _launch(lib.kda_conv_bwd, lib, dev, (ref, _p(x), _p(weight), _p(bias), _p(state), _p(cu_seqlens), _p(dy),
                                          _p(dstate_T), _p(dx), _p(dw), _p(db), _p(ds), _p(ws), ws.numel()))
     return {"dx": dx, "dweight": dw, "dbias": db, "dstate": ds}
@@ -465,7 +475,7 @@ def norm_gate_bwd(x, weight, dy, gate=None, *, activation: str = "sigmoid", eps:
     dg = None if gate is None else _new(x)
     dw = None if weight is None else torch.empty(x.shape[2], dtype=torch.float32, device=dev)
     ref = ctypes.byref(d)
-    ws = None if dw is None else _workspace(lib, lib.kda_norm_gate_bwd_workspace_size, (ref,), workspace, dev)
+    ws = None if dw is None else _workspace(lib, "kda_norm_gate_bwd_workspace_size", d, (), workspace, dev)
     _launch(lib.kda_norm_gate_bwd, lib, dev, (ref, _p(x), _p(weight), _p(gate), _p(dy), _p(dx), _p(dg), _p(dw),
                                               _p(ws), 0 if ws is None else ws.numel()))
     return {"dx": dx, "dgate": dg, "dweight": dw}
@@ -537,7 +547,7 @@ def residual_norm_bwd(x, residual_out, weight, dy, dresidual_out=None, *, scale:
     dw = torch.empty(shape[1], dtype=torch.float32, device=dev)
     dc = None if channel_scale is None else torch.empty(shape[1], dtype=torch.float32, device=dev)
     ref = ctypes.byref(d)
-    ws = _workspace(lib, lib.kda_residual_norm_bwd_workspace_size, (ref,), workspace, dev)
+    ws = _workspace(lib, "kda_residual_norm_bwd_workspace_size", d, (), workspace, dev)
     _launch(lib.kda_residual_norm_bwd, lib, dev, (ref, _p(x), _p(residual_out), _p(weight), _p(channel_scale), _p(dy),
                                                   _p(dresidual_out), _p(dx), _p(dr), _p(dw), _p(dc), _p(ws),
                                                   ws.numel()))

@@ -32,20 +32,29 @@ template <typename T, int V, int W>
 struct Taps {
     const T* x;
     const T* state;  // may be null
+    const T* any;    // V readable elements, for a row that does not count
     int64_t xs;
     int C;
     uint32_t c;
-    // row `pos` (from -(W-1)) of sequence n whose tokens start at beg
-    __device__ __forceinline__ void row(int n, int beg, int pos, float (&v)[V]) const {
-        if (pos >= 0) {
-            get_v<V>(load_v<V>(x + (int64_t)(beg + pos) * xs + c), v);
-        } else if (state) {
-            get_v<V>(load_v<V>(state + ((int64_t)n * (W - 1) + (W - 1 + pos)) * C + c), v);
-        } else {
-            zero_v<V>(v);
-        }
+    __device__ __forceinline__ Taps(const ConvArgs& a, int c_)
+        : x((const T*)a.x), state((const T*)a.state), any((const T*)(a.weight + (int64_t)c_ * W)), xs(a.xs), C(a.C),
+          c((uint32_t)c_) {}
+    // row `pos` (from -(W-1)) of sequence n whose tokens start at beg, if it is
+    // there; loaded either way, so that a caller's loads do not wait for each other
+    __device__ __forceinline__ Pack<T, V> row(int n, int beg, int pos, bool there) const {
+        const T* p = any;
+        if (there && pos >= 0) p = x + (int64_t)(beg + pos) * xs + c;
+        if (there && pos < 0 && state) p = state + ((int64_t)n * (W - 1) + (W - 1 + pos)) * C + c;
+        return load_v<V>(p);
     }
+    __device__ __forceinline__ bool counts(int pos) const { return pos >= 0 || state; }
 };
+
+template <int V, typename T>
+__device__ __forceinline__ void get_if(bool there, const Pack<T, V>& r, float (&v)[V]) {
+#pragma unroll
+    for (int i = 0; i < V; ++i) v[i] = there ? r[i] : 0.f;
+}
 
 // Taps and bias of V channels from c.
 template <int V, int W>
@@ -65,6 +74,21 @@ __device__ __forceinline__ void load_weight(const ConvArgs& a, int c, float (&w)
     else zero_v<V>(b);
 }
 
+// UNI: a strip is a whole wavefront's (G = 64), so its position and its rows'
+// addresses stay in scalar registers (the backward issues 38 vector instructions
+// an element otherwise, and these bound it).
+
+// The sequence of token u, the first behind sequence n: the next one unless it is
+// empty.
+__device__ __forceinline__ void next_seq(const Seqs& sq, int u, int& n, int& beg, int& end) {
+    if (n + 1 < sq.N && sq.start(n + 1) <= u && sq.start(n + 2) > u) n = n + 1;
+    else n = sq.find(u);
+    beg = sq.start(n);
+    end = sq.start(n + 1);
+    if (beg > u) beg = u;      // offsets out of order: still inside the tensors,
+    if (end <= u) end = u + 1;  // and one token at a time
+}
+
 template <typename T, int V, int W, bool SILU, bool UNI>
 __global__ __launch_bounds__(BT) void conv_fwd_kernel(ConvArgs a, int G, int L, int cblocks, int state_blocks) {
     const Seqs sq{a.cu, a.N, a.T, a.eq};
@@ -72,9 +96,8 @@ __global__ __launch_bounds__(BT) void conv_fwd_kernel(ConvArgs a, int G, int L, 
     const int sl = UNI ? __builtin_amdgcn_readfirstlane(threadIdx.x / WAVE) : threadIdx.x / G;
     // a token's columns by neighbouring workgroups, so that rows are read whole
     const int bx = (int)blockIdx.x / cblocks - state_blocks, at = ((int)blockIdx.x % cblocks * G + cl) * V;
-    if (at >= a.C) return;
     const int c = column<V>(at, a.C);
-    const Taps<T, V, W> tp{(const T*)a.x, (const T*)a.state, a.xs, a.C, (uint32_t)c};
+    const Taps<T, V, W> tp(a, c);
 
     if (bx < 0) {  // the sequences' final states
         const int64_t rows = (int64_t)a.N * (W - 1);
@@ -82,9 +105,10 @@ __global__ __launch_bounds__(BT) void conv_fwd_kernel(ConvArgs a, int G, int L, 
              r += (int64_t)state_blocks * spb) {
             const int n = (int)(r / (W - 1)), i = (int)(r % (W - 1)), beg = sq.start(n);
             const int len = sq.start(n + 1) - beg;
+            const int pos = (len > 0 ? len : 0) - (W - 1) + i;
             float v[V];
-            tp.row(n, beg, (len > 0 ? len : 0) - (W - 1) + i, v);
-            store_v<V>((T*)a.state_T + r * a.C + c, v);
+            get_if<V>(tp.counts(pos), tp.row(n, beg, pos, true), v);
+            if (at < a.C) store_v<V>((T*)a.state_T + r * a.C + c, v);
         }
         return;
     }
@@ -97,91 +121,66 @@ __global__ __launch_bounds__(BT) void conv_fwd_kernel(ConvArgs a, int G, int L, 
 
     float w[V][W], b[V];
     load_weight<V, W>(a, c, w, b);
-    int n = sq.find(t), beg = sq.start(n), end = sq.start(n + 1);
-    float win[W - 1][V];  // rows t - W + 1 .. t - 1
-    auto refill = [&]() {
-        if (t - beg >= W - 1) {
-            Pack<T, V> r[W - 1];
+    int n = UNI ? wave_find(sq, t) : sq.find(t), beg = sq.start(n), end = sq.start(n + 1);
+    if (beg > t) beg = t;  // (offsets out of order)
+    if (at >= a.C) return;
+    float win[W - 1][V];  // the rows before token u
+    auto refill = [&](int u) {
+        Pack<T, V> r[W - 1];
 #pragma unroll
-            for (int k = 0; k < W - 1; ++k) r[k] = load_v<V>(tp.x + (int64_t)(t - (W - 1) + k) * a.xs + tp.c);
+        for (int k = 0; k < W - 1; ++k) r[k] = tp.row(n, beg, max(u - beg, 0) - (W - 1) + k, true);
 #pragma unroll
-            for (int k = 0; k < W - 1; ++k) get_v<V>(r[k], win[k]);
-        } else {
-#pragma unroll
-            for (int k = 0; k < W - 1; ++k) tp.row(n, beg, t - beg - (W - 1) + k, win[k]);
-        }
+        for (int k = 0; k < W - 1; ++k) get_if<V>(tp.counts(u - beg - (W - 1) + k), r[k], win[k]);
     };
-    refill();
+    refill(t);
 
-    auto step = [&](int u, const Pack<T, V>& xv) {
+    auto step = [&](int u, const Pack<T, V>& xr) {
         float z[V];
 #pragma unroll
         for (int i = 0; i < V; ++i) {
             z[i] = b[i];
 #pragma unroll
             for (int j = 0; j < W - 1; ++j) z[i] += w[i][j] * win[j][i];
-            z[i] += w[i][W - 1] * xv[i];
+            z[i] += w[i][W - 1] * xr[i];
             z[i] = act_f<SILU>(z[i]);
 #pragma unroll
             for (int j = 0; j < W - 2; ++j) win[j][i] = win[j + 1][i];
-            win[W - 2][i] = xv[i];
+            win[W - 2][i] = xr[i];
         }
         store_nt<V>((T*)a.y + (int64_t)u * a.C + tp.c, z);
     };
 
+    auto row = [&](int u) { return load_v<V>(tp.x + (int64_t)(u < a.T ? u : a.T - 1) * a.xs + tp.c); };
     while (t < stop) {
         if (t + GRP <= stop && t + GRP <= end) {
             Pack<T, V> xv[GRP];
 #pragma unroll
-            for (int i = 0; i < GRP; ++i) xv[i] = load_v<V>(tp.x + (int64_t)(t + i) * a.xs + tp.c);
+            for (int i = 0; i < GRP; ++i) xv[i] = row(t + i);
 #pragma unroll
             for (int i = 0; i < GRP; ++i) step(t + i, xv[i]);
             t += GRP;
         } else {
             const int until = stop - t > GRP ? t + GRP : stop;
+            Pack<T, V> ahead = row(t);
 #pragma unroll 1
             for (; t < until; ++t) {
+                const Pack<T, V> xr = ahead;
+                ahead = row(t + 1);
                 if (t >= end) {
-                    n = sq.find(t);
-                    beg = sq.start(n);
-                    end = sq.start(n + 1);
-                    if (end <= t) end = t + 1;  // offsets out of order: still one token at a time
-                    refill();
+                    next_seq(sq, t, n, beg, end);
+                    refill(t);
                 }
-                step(t, load_v<V>(tp.x + (int64_t)t * a.xs + tp.c));
+                step(t, xr);
             }
         }
     }
 }
-
-// UNI below: a strip is a whole wavefront's (G = 64), so its position and its rows'
-// addresses stay in scalar registers (the backward issues 38 vector instructions
-// an element otherwise, and these bound it).
 
 // dy and z to dz
 template <bool SILU> __device__ __forceinline__ float dz_of(float dy, float z) {
     if (!SILU) return dy;
     const float s = sigmoid_f(z);
     return dy * (s * (1.f + z * (1.f - s)));
-}
-
-// dz of token `pos` of sequence n (beg), from its taps
-template <typename T, int V, int W, bool SILU>
-__device__ __forceinline__ void dz_at(const ConvArgs& a, const Taps<T, V, W>& tp, const T* dyp, const float (&w)[V][W],
-                                      const float (&b)[V], int n, int beg, int pos, float (&dz)[V]) {
-    const Pack<T, V> dy = load_v<V>(dyp + (int64_t)(beg + pos) * a.ds + tp.c);
-    float z[V];
-#pragma unroll
-    for (int i = 0; i < V; ++i) z[i] = b[i];
-#pragma unroll
-    for (int j = 0; j < W; ++j) {
-        float v[V];
-        tp.row(n, beg, pos - (W - 1) + j, v);
-#pragma unroll
-        for (int i = 0; i < V; ++i) z[i] += w[i][j] * v[i];
-    }
-#pragma unroll
-    for (int i = 0; i < V; ++i) dz[i] = dz_of<SILU>(dy[i], z[i]);
 }
 
 // The first state_blocks rows of workgroups form the rows of dstate, the others
@@ -196,7 +195,7 @@ __global__ __launch_bounds__(BT) void conv_bwd_kernel(ConvArgs a, int G, int L, 
     const int bx = (int)blockIdx.x / cblocks - state_blocks, c0 = ((int)blockIdx.x % cblocks * G + cl) * V;
     const bool live = c0 < a.C;  // idle lanes stay for the sums at the end
     const int c = column<V>(c0, a.C);
-    const Taps<T, V, W> tp{(const T*)a.x, (const T*)a.state, a.xs, a.C, (uint32_t)c};
+    const Taps<T, V, W> tp(a, c);
     const T* dyp = (const T*)a.dy;
 
     float w[V][W], b[V];
@@ -206,24 +205,39 @@ __global__ __launch_bounds__(BT) void conv_bwd_kernel(ConvArgs a, int G, int L, 
     // row `pos` (state rows from -(W-1)) of sequence n by itself: its derivative
     // and its part of dw and db
     auto alone = [&](int n, int beg, int len, int pos, float (&dx)[V]) {
-        float xv[V];
-        tp.row(n, beg, pos, xv);
-        if (pos >= len - (W - 1) && a.dstT) {
-            get_v<V>(load_v<V>((const T*)a.dstT + ((int64_t)n * (W - 1) + (pos - len + W - 1)) * a.C + c), dx);
-        } else {
-            zero_v<V>(dx);
+        Pack<T, V> xr[2 * W - 1], dr[W];
+#pragma unroll
+        for (int k = 0; k < 2 * W - 1; ++k) {
+            const int q = pos - (W - 1) + k;
+            xr[k] = tp.row(n, beg, q, q >= -(W - 1) && q < len);
         }
 #pragma unroll
         for (int k = 0; k < W; ++k) {
-            const int p = pos + k;
-            if (p < 0 || p >= len) continue;
-            float dz[V];
-            dz_at<T, V, W, SILU>(a, tp, dyp, w, b, n, beg, p, dz);
+            const int q = pos + k;
+            dr[k] = load_v<V>(q >= 0 && q < len ? dyp + (int64_t)(beg + q) * a.ds + tp.c : tp.any);
+        }
+        const bool out = pos >= len - (W - 1) && a.dstT;  // the row is one of the outgoing state's
+        const Pack<T, V> sr =
+            load_v<V>(out ? (const T*)a.dstT + ((int64_t)n * (W - 1) + (pos - len + W - 1)) * a.C + c : tp.any);
+        get_if<V>(out, sr, dx);
+        float xf[2 * W - 1][V];
+#pragma unroll
+        for (int k = 0; k < 2 * W - 1; ++k) {
+            const int q = pos - (W - 1) + k;
+            get_if<V>(q >= -(W - 1) && q < len && tp.counts(q), xr[k], xf[k]);
+        }
+#pragma unroll
+        for (int k = 0; k < W; ++k) {
+            const bool there = pos + k >= 0 && pos + k < len;
 #pragma unroll
             for (int i = 0; i < V; ++i) {
-                dx[i] += w[i][W - 1 - k] * dz[i];
-                dw[W - 1 - k][i] += xv[i] * dz[i];
-                if (k == 0) db[i] += dz[i];
+                float z = b[i];
+#pragma unroll
+                for (int j = 0; j < W; ++j) z += w[i][j] * xf[k + j][i];
+                const float dz = there ? dz_of<SILU>(dr[k][i], z) : 0.f;
+                dx[i] += w[i][W - 1 - k] * dz;
+                dw[W - 1 - k][i] += there ? xf[W - 1][i] * dz : 0.f;
+                if (k == 0) db[i] += dz;
             }
         }
     };
@@ -245,14 +259,16 @@ __global__ __launch_bounds__(BT) void conv_bwd_kernel(ConvArgs a, int G, int L, 
         int t = t64 < tend ? (int)t64 : tend;
         const int stop = (tend - t > L) ? t + L : tend;
         int n = 0, beg = 0, end = 0;
+        if (UNI && t < stop && !~__ballot(1)) {  // all lanes are here
+            n = wave_find(sq, t);
+            beg = min(sq.start(n), t);
+            end = max(sq.start(n + 1), t + 1);
+        }
         bool have = false;  // xw, dzw hold rows t .. t + W - 2
         float xw[W - 1][V], dzw[W - 1][V];
         while (t < stop) {
             if (t >= end) {
-                n = sq.find(t);
-                beg = sq.start(n);
-                end = sq.start(n + 1);
-                if (end <= t) end = t + 1;
+                next_seq(sq, t, n, beg, end);
                 have = false;
             }
             if (t + GRB <= stop && t - (W - 1) >= beg && t + GRB + (W - 1) <= end) {

@@ -96,24 +96,39 @@ __global__ __launch_bounds__(256) void linscan_clear_kernel(uint64_t* word, int6
         if (i + k < words + counters) word[i + k] = i + k < words ? ~0ull : 0ull;
 }
 
-// Which of a wavefront's tokens start and end a sequence (uniform over the
-// wavefront): bit i of first / last for token t0 + i.
+// The sequences of a wavefront's 16 tokens, and which of the tokens start and
+// end one (bit i of first / last for token t0 + i), all uniform over the
+// wavefront.  Every lane has to be active.
 struct Edges {
     uint32_t first, last;
-    int count;  // tokens of the run that exist
+    int count;   // tokens of the run that exist
+    int n0;      // sequence of token t0
+    int next;    // this lane's: where sequence n0 + 1 + lane starts
+    // sequence of token t (t0 <= t < t0 + count)
+    __device__ __forceinline__ int seq(const Seqs& sq, int t) const {
+        const uint64_t started = __ballot(next <= t);
+        return ~started ? n0 + __popcll(started) : sq.find(t);  // more than 64 of them: look it up
+    }
 };
 __device__ __forceinline__ Edges edges_of(const Seqs& sq, int t0, int tend) {
-    Edges e{0u, 0u, tend - t0 < TW ? tend - t0 : TW};
+    Edges e{0u, 0u, tend - t0 < TW ? tend - t0 : TW, 0, 0x7fffffff};
     if (e.count <= 0) { e.count = 0; return e; }
-    int t = t0;
-    while (t < t0 + e.count) {
-        const int n = sq.find(t);
-        if (sq.start(n) == t) e.first |= 1u << (t - t0);
-        int nx = sq.start(n + 1);
-        if (nx <= t) nx = t + 1;
-        if (nx <= t0 + e.count) e.last |= 1u << (nx - 1 - t0);
-        t = nx;
+    e.n0 = wave_find(sq, t0);
+    if (sq.start(e.n0) == t0) e.first = 1u;
+    if (sq.start(e.n0 + 1) > t0 + TW) return e;  // the usual run, inside one sequence
+    const int n = e.n0 + 1 + (int)threadIdx.x % WAVE;
+    if (n <= sq.N) e.next = sq.start(n);
+#pragma unroll
+    for (int i = 1; i <= TW; ++i)
+        if (__ballot(e.next == t0 + i)) e.first |= 1u << i, e.last |= 1u << (i - 1);
+    if (!~__ballot(e.next <= t0 + TW)) {  // more than 64 starts, empty sequences among them
+        for (int i = 1; i <= e.count; ++i)
+            if (sq.start(sq.find(t0 + i < tend ? t0 + i : tend - 1)) == t0 + i || t0 + i == tend)
+                e.first |= 1u << i, e.last |= 1u << (i - 1);
     }
+    const uint32_t there = (1u << e.count) - 1;
+    e.first &= there;
+    e.last &= there;
     return e;
 }
 
@@ -182,7 +197,7 @@ __device__ __forceinline__ void run_forward(const LinScanArgs& p, const Seqs& sq
 #pragma unroll
     for (int i = 0; i < TW; ++i) {
         if (ed.first >> i & 1) {
-            load_state<V>(p.h0, p.C, sq.find(t0 + i), c, E);
+            load_state<V>(p.h0, p.C, ed.seq(sq, t0 + i), c, E);
 #pragma unroll
             for (int v = 0; v < V; ++v) P[v] = -1.f;
         }
@@ -205,7 +220,7 @@ __device__ __forceinline__ void run_backward(const LinScanArgs& p, const Seqs& s
 #pragma unroll
     for (int i = TW - 1; i >= 0; --i) {
         if (ed.last >> i & 1) {
-            load_state<V>(p.dhT, p.C, sq.find(t0 + i), c, E);
+            load_state<V>(p.dhT, p.C, ed.seq(sq, t0 + i), c, E);
 #pragma unroll
             for (int v = 0; v < V; ++v) P[v] = -1.f;
         }
@@ -256,9 +271,7 @@ __device__ __forceinline__ void chain(const LinScanArgs& p, const float (&sp)[NW
                                       int tiles) {
     const int j = threadIdx.x;
     if (j >= WAVE * V) return;
-    const int at = (cb * WAVE + j / V) * V;
-    if (at >= p.C) return;
-    const int c = column<V>(at, p.C) + j % V;
+    const int c = column<V>((cb * WAVE + j / V) * V, p.C) + j % V;
     float P = sp[BACK ? NW - 1 : 0][j], E = se[BACK ? NW - 1 : 0][j];
 #pragma unroll
     for (int w = 1; w < NW; ++w) then(P, E, sp[BACK ? NW - 1 - w : w][j], se[BACK ? NW - 1 - w : w][j]);
@@ -290,7 +303,7 @@ __global__ __launch_bounds__(BT) void linscan_fwd_kernel(LinScanArgs p, int tile
     take_tile(tickets, cblocks, &s_tile, tile, cb);
     if (tile >= tiles) return;
     const int lane = threadIdx.x % WAVE, wv = __builtin_amdgcn_readfirstlane(threadIdx.x / WAVE);
-    const int at = (cb * WAVE + lane) * V, c = column<V>(at, p.C);
+    const int c = column<V>((cb * WAVE + lane) * V, p.C);  // lanes past the row's end: its last, once more
     const int t0 = tile * TT + wv * TW;
     Pack<float, V> la[TW];
     Pack<T, V> x[TW];
@@ -306,7 +319,6 @@ __global__ __launch_bounds__(BT) void linscan_fwd_kernel(LinScanArgs p, int tile
     __syncthreads();
     chain<V, false, LB>(p, sp, se, sh, cb, tile, tiles);
     __syncthreads();
-    if (at >= p.C) return;
 #pragma unroll
     for (int v = 0; v < V; ++v) h[v] = sh[lane * V + v];
     for (int w = 0; w < wv; ++w)
@@ -318,11 +330,11 @@ __global__ __launch_bounds__(BT) void linscan_fwd_kernel(LinScanArgs p, int tile
 #pragma unroll
     for (int i = 0; i < TW; ++i) {
         if (i >= ed.count) continue;
-        if (ed.first >> i & 1) load_state<V>(p.h0, p.C, sq.find(t0 + i), c, h);
+        if (ed.first >> i & 1) load_state<V>(p.h0, p.C, ed.seq(sq, t0 + i), c, h);
 #pragma unroll
         for (int v = 0; v < V; ++v) h[v] = a[i][v] * h[v] + x[i][v];
         store_nt<V>(y + (int64_t)i * p.C + (uint32_t)c, h);
-        if ((ed.last >> i & 1) && p.hT) store_v<V>(p.hT + (int64_t)sq.find(t0 + i) * p.C + c, h);
+        if ((ed.last >> i & 1) && p.hT) store_v<V>(p.hT + (int64_t)ed.seq(sq, t0 + i) * p.C + c, h);
     }
 }
 
@@ -341,7 +353,7 @@ __global__ __launch_bounds__(BT, 4) void linscan_bwd_kernel(LinScanArgs p, int t
     tile = tiles - 1 - tile;
     if (tile < 0) return;
     const int lane = threadIdx.x % WAVE, wv = __builtin_amdgcn_readfirstlane(threadIdx.x / WAVE);
-    const int at = (cb * WAVE + lane) * V, c = column<V>(at, p.C);
+    const int c = column<V>((cb * WAVE + lane) * V, p.C);  // lanes past the row's end: its last, once more
     const int t0 = tile * TT + wv * TW;
     Pack<float, V> la[TW];
     Pack<T, V> x[TW], dy[TW];
@@ -372,7 +384,7 @@ __global__ __launch_bounds__(BT, 4) void linscan_bwd_kernel(LinScanArgs p, int t
     float hb[TW][V];
 #pragma unroll
     for (int i = 0; i < TW; ++i) {
-        if (ed.first >> i & 1) load_state<V>(p.h0, p.C, sq.find(t0 + i), c, h);
+        if (ed.first >> i & 1) load_state<V>(p.h0, p.C, ed.seq(sq, t0 + i), c, h);
 #pragma unroll
         for (int v = 0; v < V; ++v) {
             hb[i][v] = h[v];
@@ -380,7 +392,6 @@ __global__ __launch_bounds__(BT, 4) void linscan_bwd_kernel(LinScanArgs p, int t
         }
     }
     __syncthreads();
-    if (at >= p.C) return;
 #pragma unroll
     for (int v = 0; v < V; ++v) g[v] = sh[lane * V + v];
     for (int w = NW - 1; w > wv; --w)
@@ -391,7 +402,7 @@ __global__ __launch_bounds__(BT, 4) void linscan_bwd_kernel(LinScanArgs p, int t
 #pragma unroll
     for (int i = TW - 1; i >= 0; --i) {
         if (i >= ed.count) continue;
-        if (ed.last >> i & 1) load_state<V>(p.dhT, p.C, sq.find(t0 + i), c, g);
+        if (ed.last >> i & 1) load_state<V>(p.dhT, p.C, ed.seq(sq, t0 + i), c, g);
         float d[V], dl[V];
 #pragma unroll
         for (int v = 0; v < V; ++v) d[v] = dy[i][v] + g[v];
@@ -402,7 +413,7 @@ __global__ __launch_bounds__(BT, 4) void linscan_bwd_kernel(LinScanArgs p, int t
             dl[v] = g[v] * hb[i][v];
         }
         store_nt<V>(dla + (int64_t)i * p.C + (uint32_t)c, dl);
-        if ((ed.first >> i & 1) && p.hT) store_v<V>(p.hT + (int64_t)sq.find(t0 + i) * p.C + c, g);
+        if ((ed.first >> i & 1) && p.hT) store_v<V>(p.hT + (int64_t)ed.seq(sq, t0 + i) * p.C + c, g);
     }
 }
 

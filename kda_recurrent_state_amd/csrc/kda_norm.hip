@@ -334,8 +334,15 @@ __global__ __launch_bounds__(CSW* CSR) void colsum_kernel(const float* part, int
     const int cl = threadIdx.x % CSW, rl = threadIdx.x / CSW;
     const int64_t c = (int64_t)blockIdx.x * CSW + cl;
     float s = 0.f;
-    if (c < cols)
-        for (int r = rl; r < rows; r += CSR) s += part[(int64_t)r * cols + c];
+    if (c < cols) {
+        int r = rl;
+        for (; r + 3 * CSR < rows; r += 4 * CSR) {  // four loads in flight
+            const float* q = part + (int64_t)r * cols + c;
+            const float v0 = q[0], v1 = q[CSR * cols], v2 = q[2 * CSR * cols], v3 = q[3 * CSR * cols];
+            s += (v0 + v1) + (v2 + v3);
+        }
+        for (; r < rows; r += CSR) s += part[(int64_t)r * cols + c];
+    }
     lds[rl][cl] = s;
 #pragma unroll
     for (int k = CSR / 2; k > 0; k >>= 1) {

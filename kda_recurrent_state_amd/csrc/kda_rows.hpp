@@ -93,6 +93,22 @@ struct Seqs {
     }
 };
 
+// The sequence of a token by a whole wavefront (all lanes active, t the same in
+// each): the lanes read 64 offsets at once, where Seqs::find reads them one
+// after the other.  Offsets out of order give some sequence in [0, N).
+__device__ __forceinline__ int wave_find(const Seqs& sq, int t) {
+    if (!sq.cu) return t / sq.eq;
+    const int lane = threadIdx.x % WAVE;
+    int lo = 0, hi = sq.N;
+    while (hi - lo > 1) {
+        const int step = (hi - lo + WAVE - 1) / WAVE, n = lo + (lane + 1) * step;
+        const int below = __popcll(__ballot(n < hi && sq.start(n < hi ? n : lo) <= t));
+        lo += below * step;
+        hi = hi - lo < step ? hi : lo + step;
+    }
+    return lo;
+}
+
 __device__ __forceinline__ float sigmoid_f(float z) { return __builtin_amdgcn_rcpf(1.f + __expf(-z)); }
 
 // Sum over the G (a power of two up to 64) consecutive lanes of a group.
