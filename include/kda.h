@@ -404,7 +404,7 @@ KDA_API int kda_decode_step_ex(const kda_dims_t* dims, const kda_prologue_t* pro
  *     is the distance between consecutive tokens in elements (0: contiguous),
  *     at least the token's own size.  Outputs are contiguous.
  *   - total_tokens (for kda_norm_gate tokens x heads) and num_seqs go up to
- *     2147418112, channels up to 16777216; element offsets are 64-bit.
+ *     2147418112, channels up to 1048576; element offsets are 64-bit.
  *   - With cu_seqlens, tokens at or past cu_seqlens[num_seqs] belong to no
  *     sequence: what they hold does not matter, and their rows of the outputs
  *     are left as they were.  Offsets outside [0, total_tokens] are clamped into it.

@@ -138,7 +138,7 @@ def _seqs(cu_seqlens, num_seqs, T):
         if n < 0:
             raise ValueError(f"num_seqs must not be negative (got {n})")
         return n
-    if cu_seqlens.dtype is not torch.int32 or cu_seqlens.dim() != 1 or not cu_seqlens.is_contiguous() \
+    if not isinstance(cu_seqlens, torch.Tensor) or cu_seqlens.dtype is not torch.int32 or cu_seqlens.dim() != 1 or not cu_seqlens.is_contiguous() \
             or cu_seqlens.shape[0] < 1:
         raise TypeError("cu_seqlens must be a contiguous 1-D int32 tensor [N + 1]")
     n = cu_seqlens.shape[0] - 1

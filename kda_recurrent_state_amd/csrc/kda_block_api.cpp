@@ -17,7 +17,7 @@ using kda::ok;
 namespace {
 
 constexpr int64_t kMaxTokens = 0x7fff0000;
-constexpr int kMaxChannels = 1 << 24;
+constexpr int kMaxChannels = 1 << 20;
 constexpr int kMaxWidth = 8192;
 constexpr int64_t kMaxThreads = 0xffffffffll;  // threads of one launch along an axis
 

@@ -75,8 +75,7 @@ __device__ __forceinline__ void load_weight(const ConvArgs& a, int c, float (&w)
 }
 
 // UNI: a strip is a whole wavefront's (G = 64), so its position and its rows'
-// addresses stay in scalar registers (the backward issues 38 vector instructions
-// an element otherwise, and these bound it).
+// addresses stay in scalar registers and its sequence is found by all lanes.
 
 // The sequence of token u, the first behind sequence n: the next one unless it is
 // empty.
@@ -457,11 +456,19 @@ template <typename F> void by_taps(const ConvArgs& a, F f) {
     else act(std::integral_constant<int, 4>{});
 }
 
-template <typename T, int V> void fwd_launch(const ConvArgs& a, hipStream_t st) {
+// The grid of rows x cblocks workgroups; a launch has fewer than 2^32 threads.
+bool grid_of(const ConvShape& s, int extra, dim3* grid) {
+    const int64_t blocks = ((int64_t)s.strips + extra) * s.cblocks;
+    *grid = dim3((unsigned)blocks);
+    return blocks <= 0xffffffffll / BT;
+}
+
+template <typename T, int V> hipError_t fwd_launch(const ConvArgs& a, hipStream_t st) {
     const ConvShape s = fwd_shape(V, a.T, a.C);
     const int extra = a.state_T ? state_blocks(a.N) : 0;
-    const dim3 grid((unsigned)((int64_t)(s.strips + extra) * s.cblocks));
-    if (grid.x == 0) return;
+    dim3 grid;
+    if (!grid_of(s, extra, &grid)) return hipErrorInvalidConfiguration;
+    if (grid.x == 0) return hipSuccess;
     by_taps(a, [&](auto w, auto silu) {
         constexpr int W = decltype(w)::value;
         constexpr bool SILU = decltype(silu)::value;
@@ -473,12 +480,14 @@ template <typename T, int V> void fwd_launch(const ConvArgs& a, hipStream_t st) 
             }
         hipLaunchKernelGGL((conv_fwd_kernel<T, V, W, SILU, false>), grid, dim3(BT), 0, st, a, s.G, s.L, s.cblocks, extra);
     });
+    return hipGetLastError();
 }
 
-template <typename T, int V> void bwd_launch(const ConvArgs& a, hipStream_t st) {
+template <typename T, int V> hipError_t bwd_launch(const ConvArgs& a, hipStream_t st) {
     const ConvShape s = bwd_shape(V, a.T, a.C);
     const int extra = state_blocks(a.N);
-    const dim3 grid((unsigned)((int64_t)(s.strips + extra) * s.cblocks));
+    dim3 grid;
+    if (!grid_of(s, extra, &grid)) return hipErrorInvalidConfiguration;
     by_taps(a, [&](auto w, auto silu) {
         constexpr int W = decltype(w)::value;
         constexpr bool SILU = decltype(silu)::value;
@@ -493,23 +502,24 @@ template <typename T, int V> void bwd_launch(const ConvArgs& a, hipStream_t st) 
                                extra);
         }
     });
+    return hipGetLastError();
 }
 
-template <typename T, int V> void step_launch(const ConvArgs& a, hipStream_t st) {
+template <typename T, int V> hipError_t step_launch(const ConvArgs& a, hipStream_t st) {
     const int64_t work = (int64_t)a.N * ((a.C + V - 1) / V);
     by_taps(a, [&](auto w, auto silu) {
         hipLaunchKernelGGL((conv_step_kernel<T, V, decltype(w)::value, decltype(silu)::value>),
                            dim3((unsigned)((work + BT - 1) / BT)), dim3(BT), 0, st, a);
     });
+    return hipGetLastError();
 }
 
 }  // namespace
 
 hipError_t launch_conv_fwd(const ConvArgs& a, hipStream_t st) {
     const int v = fwd_vec(a.dtype, a.C);
-    if (a.dtype == 1) v == 1 ? fwd_launch<bf16, 1>(a, st) : fwd_launch<bf16, 8>(a, st);
-    else v == 1 ? fwd_launch<float, 1>(a, st) : fwd_launch<float, 4>(a, st);
-    return hipGetLastError();
+    if (a.dtype == 1) return v == 1 ? fwd_launch<bf16, 1>(a, st) : fwd_launch<bf16, 8>(a, st);
+    return v == 1 ? fwd_launch<float, 1>(a, st) : fwd_launch<float, 4>(a, st);
 }
 
 int conv_bwd_parts(int dtype, int T, int N, int C, int W) {
@@ -518,16 +528,15 @@ int conv_bwd_parts(int dtype, int T, int N, int C, int W) {
 
 hipError_t launch_conv_bwd(const ConvArgs& a, hipStream_t st) {
     const int v = bwd_vec(a.dtype, a.C, a.W);
-    if (a.dtype == 1) v == 1 ? bwd_launch<bf16, 1>(a, st) : v == 2 ? bwd_launch<bf16, 2>(a, st) : bwd_launch<bf16, 4>(a, st);
-    else v == 1 ? bwd_launch<float, 1>(a, st) : bwd_launch<float, 4>(a, st);
-    return hipGetLastError();
+    if (a.dtype == 1)
+        return v == 1 ? bwd_launch<bf16, 1>(a, st) : v == 2 ? bwd_launch<bf16, 2>(a, st) : bwd_launch<bf16, 4>(a, st);
+    return v == 1 ? bwd_launch<float, 1>(a, st) : bwd_launch<float, 4>(a, st);
 }
 
 hipError_t launch_conv_step(const ConvArgs& a, hipStream_t st) {
     const int v = fwd_vec(a.dtype, a.C);
-    if (a.dtype == 1) v == 1 ? step_launch<bf16, 1>(a, st) : step_launch<bf16, 8>(a, st);
-    else v == 1 ? step_launch<float, 1>(a, st) : step_launch<float, 4>(a, st);
-    return hipGetLastError();
+    if (a.dtype == 1) return v == 1 ? step_launch<bf16, 1>(a, st) : step_launch<bf16, 8>(a, st);
+    return v == 1 ? step_launch<float, 1>(a, st) : step_launch<float, 4>(a, st);
 }
 
 }  // namespace kda

@@ -81,7 +81,7 @@ CASES = [
     *[(f, dict(total_tokens=-1), {}, INVALID) for f in ("kda_scan_fwd", "kda_scan_bwd", "kda_conv_fwd", "kda_conv_bwd")],
     *[(f, dict(total_tokens=1 << 31), {}, INVALID) for f in ("kda_scan_fwd", "kda_conv_fwd")],
     *[(f, dict(channels=0), {}, INVALID) for f in ("kda_scan_fwd", "kda_scan_step", "kda_conv_bwd", "kda_conv_step")],
-    *[(f, dict(channels=(1 << 24) + 1), {}, INVALID) for f in ("kda_scan_fwd", "kda_conv_fwd")],
+    *[(f, dict(channels=(1 << 20) + 1), {}, INVALID) for f in ("kda_scan_fwd", "kda_conv_fwd")],
     *[(f, dict(dtype=2), {}, INVALID) for f in ARGS],
     *[(f, dict(reserved=1), {}, INVALID) for f in ARGS],
     *[(f, dict(x_stride=3), {}, INVALID) for f in ARGS],
@@ -190,6 +190,7 @@ BINDING = [
     (TypeError, lambda: kda.scan_fwd(t(4, 3), t(4, 3, dtype=BF))),
     (TypeError, lambda: kda.scan_fwd([1.0], t(4, 3))),
     (TypeError, lambda: kda.scan_fwd(t(4, 3), t(4, 3), cu_seqlens=torch.tensor([0, 4]))),
+    (TypeError, lambda: kda.scan_fwd(t(4, 3), t(4, 3), cu_seqlens=[0, 4])),
     (TypeError, lambda: kda.scan_bwd(t(4, 3), t(4, 3), None)),
     (TypeError, lambda: kda.scan_step(t(4, 3), t(4, 3), None)),
     (TypeError, lambda: kda.conv_step(t(4, 3), t(3, 4), None)),

@@ -40,6 +40,8 @@ LENS = {
     "long": [333],
     "pair": [192, 192],
     "ragged": [250, 3, 517, 130],
+    # more than 64 sequences start within 16 tokens, most of them empty
+    "hollow": [3] + [0] * 150 + [2] + [0] * 70 + [5, 20],
 }
 
 
@@ -98,6 +100,81 @@ def test_scan_defaults(dtype):
     val, bnd = R.scan(x.double(), la.double(), zero[:1], [0, L * N])
     R.check(y1, val["y"], bnd["y"], "y of one")
     R.check(h1, val["h"], bnd["h"], "h of one")
+
+
+def many(n, seed):
+    g = torch.Generator().manual_seed(seed)
+    return torch.randint(0, 4, (n,), generator=g).tolist()
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("lengths,C", [([2500], 130), ([700], 4100), (many(300, 1), 66), (many(5000, 2), 3)],
+                         ids=["chain", "wide", "300", "5000"])
+def test_scan_long_wide_and_many(lengths, C, dtype):
+    """A chain of twenty tiles, more than 32 column blocks, more sequences than lanes."""
+    log(f"scan {len(lengths)} sequences, {sum(lengths)} tokens, C={C} {dtype}")
+    cu, cud = R.bounds_of(lengths), cu_of(lengths)
+    x, la, h0, dy, dhT = scan_inputs(lengths, C, dtype, 19)
+    val, bnd = R.scan(x.double(), la.double(), h0.double(), cu)
+    xd, lad, h0d, dyd, dhTd = map(dev, (x, la, h0, dy, dhT))
+    ws = torch.randint(0, 256, (kda.scan_workspace_size(xd, num_seqs=len(lengths), backward=True) + 64,), device=DEV,
+                       dtype=torch.uint8)  # what it holds before a call does not matter
+    y, hT, states = kda.scan_fwd_states(xd, lad, h0d, cud, workspace=ws)
+    R.check(y, val["y"], bnd["y"], "y")
+    R.check(hT, val["h"], bnd["h"], "h_T")
+    gval, gbnd = R.scan_grad(x.double(), la.double(), h0.double(), cu, dy.double(), dhT.double())
+    got = kda.scan_bwd(xd, lad, dyd, h0d, cud, dhTd, states=states, workspace=ws)
+    for k in ("dx", "dlog_a", "dh0"):
+        R.check(got[k], gval[k], gbnd[k], k)
+    again = kda.scan_bwd(xd, lad, dyd, h0d, cud, dhTd)
+    assert all(torch.equal(again[k], got[k]) for k in got)
+
+
+@pytest.mark.parametrize("lengths,C", [([2500], 130), (many(300, 1), 66), (many(5000, 2), 5)], ids=["long", "300", "5000"])
+def test_conv_long_and_many(lengths, C):
+    log(f"conv {len(lengths)} sequences, {sum(lengths)} tokens, C={C}")
+    r = rnd(24)
+    T, N, W = sum(lengths), len(lengths), 4
+    cu, cud = R.bounds_of(lengths), cu_of(lengths)
+    x, w, b, st, dy, dst = r(T, C), r(C, W), r(C), r(N, W - 1, C), r(T, C), r(N, W - 1, C)
+    f8 = [t.double() for t in (x, w, b, st)]
+    val, bnd = R.conv(*f8, cu, True)
+    xd, wd, bd, sd, dyd, dsd = map(dev, (x, w, b, st, dy, dst))
+    y, sT = kda.conv_fwd(xd, wd, bd, sd, cud)
+    R.check(y, val["y"], bnd["y"], "y")
+    assert torch.equal(sT.cpu().double(), val["state"])
+    gval, gbnd = R.conv_grad(*f8, cu, True, dy.double(), dst.double())
+    ws = torch.randint(0, 256, (kda.conv_bwd_workspace_size(xd, W, num_seqs=N),), device=DEV, dtype=torch.uint8)
+    g = kda.conv_bwd(xd, wd, dyd, bd, sd, cud, dsd, workspace=ws)
+    for k in gval:
+        R.check(g[k], gval[k], gbnd[k], k)
+
+
+def test_workspaces_too_small_are_refused():
+    log("workspaces")
+    x, la = torch.zeros(300, 8, device=DEV), torch.zeros(300, 8, device=DEV)
+    small = torch.zeros(128, device=DEV, dtype=torch.uint8)
+    for f in (lambda: kda.scan_fwd(x, la, workspace=small), lambda: kda.scan_bwd(x, la, x, workspace=small),
+              lambda: kda.conv_bwd(x, torch.zeros(8, 4, device=DEV), x, workspace=small),
+              lambda: kda.norm_gate_bwd(x.view(300, 1, 8), la[0].clone(), x.view(300, 1, 8), workspace=small),
+              lambda: kda.residual_norm_bwd(x, x, la[0].clone(), x, workspace=small),
+              lambda: kda.scan_fwd(x, la, workspace=torch.zeros(1 << 16, device=DEV, dtype=torch.uint8)[1:])):
+        with pytest.raises(kda.KdaError):
+            f()
+
+
+def test_an_offset_past_the_tensor_is_its_end():
+    log("offset past the end")
+    x, la, h0, dy, _ = scan_inputs([40, 33], 12, F4, 20)
+    good, far = cu_of([40, 33]), torch.tensor([0, 40, 1 << 30], dtype=torch.int32, device=DEV)
+    xd, lad, h0d, dyd = map(dev, (x, la, h0, dy))
+    assert all(torch.equal(a, b) for a, b in zip(kda.scan_fwd(xd, lad, h0d, far), kda.scan_fwd(xd, lad, h0d, good)))
+    a, b = (kda.scan_bwd(xd, lad, dyd, h0d, c) for c in (far, good))
+    assert all(torch.equal(a[k], b[k]) for k in a)
+    w = torch.randn(12, 3, device=DEV)
+    assert all(torch.equal(a, b) for a, b in zip(kda.conv_fwd(xd, w, cu_seqlens=far), kda.conv_fwd(xd, w, cu_seqlens=good)))
+    a, b = (kda.conv_bwd(xd, w, dyd, cu_seqlens=c) for c in (far, good))
+    assert all(torch.equal(a[k], b[k]) for k in a)
 
 
 def test_scan_empty():
