@@ -17,9 +17,12 @@ Packed sequences are given as for ``chunk_fwd``; tokens at or past
 from __future__ import annotations
 
 import ctypes
+from functools import lru_cache
+
 import torch
 
-from . import KDA_BF16, KDA_F32, _check, _same_device, load_library
+from . import KDA_BF16, KDA_F32, _check, load_library
+from . import _same_device as _named_devices
 
 __all__ = ["scan_fwd", "scan_fwd_states", "scan_bwd", "scan_step", "scan_workspace_size", "SCAN_STATE_EVERY",
            "conv_fwd", "conv_bwd", "conv_step", "conv_bwd_workspace_size",
@@ -71,6 +74,13 @@ def _declare(lib):
         getattr(lib, name).argtypes = [ctypes.POINTER(dims), ctypes.POINTER(Z)]
     lib.kda_scan_workspace_size.restype = ctypes.c_int
     lib.kda_scan_workspace_size.argtypes = [ctypes.POINTER(_ScanDims), ctypes.c_int, ctypes.POINTER(Z)]
+
+
+@lru_cache(maxsize=4096)
+def _dims(kind, *fields):
+    """A dims structure (only ever read) and a reference to it."""
+    d = kind(*fields)
+    return d, ctypes.byref(d)
 
 
 def _code(t, name="x"):
@@ -138,13 +148,23 @@ def _seqs(cu_seqlens, num_seqs, T):
         if n < 0:
             raise ValueError(f"num_seqs must not be negative (got {n})")
         return n
-    if not isinstance(cu_seqlens, torch.Tensor) or cu_seqlens.dtype is not torch.int32 or cu_seqlens.dim() != 1 or not cu_seqlens.is_contiguous() \
-            or cu_seqlens.shape[0] < 1:
+    if not isinstance(cu_seqlens, torch.Tensor) or cu_seqlens.dtype is not torch.int32 or cu_seqlens.dim() != 1 \
+            or not cu_seqlens.is_contiguous() or cu_seqlens.shape[0] < 1:
         raise TypeError("cu_seqlens must be a contiguous 1-D int32 tensor [N + 1]")
     n = cu_seqlens.shape[0] - 1
     if num_seqs is not None and int(num_seqs) != n:
         raise ValueError(f"cu_seqlens holds {n} sequences, num_seqs says {int(num_seqs)}")
     return n
+
+
+def _same_device(ref, **tensors):
+    """Every tensor on ref's HIP device; the slower check says which is not."""
+    dev = ref.device
+    if dev.type != "cuda":
+        _named_devices(ref)
+    for t in tensors.values():
+        if t is not None and t.device != dev:
+            _named_devices(ref, **tensors)
 
 
 def _extent(t):
@@ -192,32 +212,27 @@ def _launch(fn, lib, device, args):
         _check(lib, status)
 
 
-_sizes = {}  # workspace bytes by entry point and dims, of which a program has few
+@lru_cache(maxsize=4096)
+def _needed(name, kind, fields, more):
+    lib = load_library()
+    need = ctypes.c_size_t(0)
+    d = kind.from_buffer_copy(fields)
+    _check(lib, getattr(lib, name)(ctypes.byref(d), *more, ctypes.byref(need)))
+    return need.value
 
 
-def _workspace(lib, name, dims, more, workspace, device):
-    """The caller's workspace, or one of the size that lib.<name>(dims, *more) says."""
+def _workspace(name, dims, more, workspace, device):
+    """The caller's workspace, or one of the size that the entry point `name` says."""
     if workspace is None:
-        key = (name, bytes(dims), more)
-        size = _sizes.get(key)
-        if size is None:
-            need = ctypes.c_size_t(0)
-            _check(lib, getattr(lib, name)(ctypes.byref(dims), *more, ctypes.byref(need)))
-            if len(_sizes) >= 4096:
-                _sizes.clear()
-            size = _sizes[key] = need.value
-        return torch.empty(size, dtype=torch.uint8, device=device)
+        return torch.empty(_needed(name, type(dims), bytes(dims), more), dtype=torch.uint8, device=device)
     if not isinstance(workspace, torch.Tensor) or workspace.dtype is not torch.uint8 or workspace.dim() != 1 \
             or not workspace.is_contiguous():
         raise TypeError("workspace must be a contiguous 1-D uint8 tensor")
     return workspace
 
 
-def _size(fn, d, *more):
-    lib = load_library()
-    need = ctypes.c_size_t(0)
-    _check(lib, getattr(lib, fn)(ctypes.byref(d), *more, ctypes.byref(need)))
-    return need.value
+def _size(name, dims, *more):
+    return _needed(name, type(dims), bytes(dims), more)
 
 
 # ------------------------------------------------------------------ diagonal recurrence
@@ -228,14 +243,14 @@ def _scan_dims(x, log_a, N, dy=None):
     xs = _tokens(x, "x", x.dtype, (T, C))
     ls = _tokens(log_a, "log_a", torch.float32, (T, C))
     ds = 0 if dy is None else _tokens(dy, "dy", x.dtype, (T, C))
-    return _ScanDims(N, C, T, code, 0, xs, ls, ds)
+    return _dims(_ScanDims, N, C, T, code, 0, xs, ls, ds)
 
 
 def _scan(x, log_a, h0, cu_seqlens, num_seqs, out, final_state, states, workspace):
     lib = load_library()
     T, C = _rank(x, "x", 2)
     N = _seqs(cu_seqlens, num_seqs, T)
-    d = _scan_dims(x, log_a, N)
+    d, ref = _scan_dims(x, log_a, N)
     _full(h0, "h0", torch.float32, (N, C))
     _full(out, "out", x.dtype, (T, C))
     _full(states, "states", torch.float32, (-(-T // SCAN_STATE_EVERY), C))
@@ -249,8 +264,7 @@ def _scan(x, log_a, h0, cu_seqlens, num_seqs, out, final_state, states, workspac
     for o in (out, hT if given else None, states):
         if o is not None:
             _apart(o, x, log_a, h0, *(t for t in (out, hT, states) if t is not o))
-    ref = ctypes.byref(d)
-    ws = _workspace(lib, "kda_scan_workspace_size", d, (0,), workspace, x.device)
+    ws = _workspace("kda_scan_workspace_size", d, (0,), workspace, x.device)
     _launch(lib.kda_scan_fwd, lib, x.device, (ref, _p(x), _p(log_a), _p(h0), _p(cu_seqlens), _p(y), _p(hT),
                                               _p(states), _p(ws), ws.numel()))
     return y, hT
@@ -292,7 +306,7 @@ def scan_bwd(x, log_a, dy, h0=None, cu_seqlens=None, dh_T=None, *, num_seqs: int
     lib = load_library()
     T, C = _rank(x, "x", 2)
     N = _seqs(cu_seqlens, num_seqs, T)
-    d = _scan_dims(x, log_a, N, _given(dy, "dy"))
+    d, ref = _scan_dims(x, log_a, N, _given(dy, "dy"))
     _full(h0, "h0", torch.float32, (N, C))
     _full(dh_T, "dh_T", torch.float32, (N, C))
     _full(states, "states", torch.float32, (-(-T // SCAN_STATE_EVERY), C))
@@ -301,8 +315,7 @@ def scan_bwd(x, log_a, dy, h0=None, cu_seqlens=None, dh_T=None, *, num_seqs: int
     dx = _new(x)
     dla = _new(log_a)
     dh0 = torch.empty((N, C), dtype=torch.float32, device=dev) if initial_state_grad else None
-    ref = ctypes.byref(d)
-    ws = _workspace(lib, "kda_scan_workspace_size", d, (1,), workspace, dev)
+    ws = _workspace("kda_scan_workspace_size", d, (1,), workspace, dev)
     _launch(lib.kda_scan_bwd, lib, dev, (ref, _p(x), _p(log_a), _p(h0), _p(cu_seqlens), _p(states), _p(dy), _p(dh_T),
                                          _p(dx), _p(dla), _p(dh0), _p(ws), ws.numel()))
     return {"dx": dx, "dlog_a": dla, "dh0": dh0}
@@ -319,7 +332,7 @@ def scan_step(x, log_a, h, *, out=None, h_out=None):
     h_out is given; returns (y, state after)."""
     lib = load_library()
     N, C = _rank(x, "x", 2)
-    d = _scan_dims(x, log_a, N)
+    d, ref = _scan_dims(x, log_a, N)
     _full(_given(h, "h"), "h", torch.float32, (N, C))
     _full(h_out, "h_out", torch.float32, (N, C))
     _full(out, "out", x.dtype, (N, C))
@@ -330,7 +343,7 @@ def scan_step(x, log_a, h, *, out=None, h_out=None):
         _apart(out, x, log_a, h, h_out)
     if h_out is not None and h_out is not h:
         _apart(h_out, x, log_a, *(() if h_out.data_ptr() == h.data_ptr() else (h,)))
-    _launch(lib.kda_scan_step, lib, x.device, (ctypes.byref(d), _p(x), _p(log_a), _p(h), _p(ho), _p(y)))
+    _launch(lib.kda_scan_step, lib, x.device, (ref, _p(x), _p(log_a), _p(h), _p(ho), _p(y)))
     return y, ho
 
 
@@ -347,7 +360,7 @@ def _conv_dims(x, weight, bias, N, activation, dy=None):
         raise ValueError(f"activation must be None or 'silu' (got {activation!r})")
     xs = _tokens(x, "x", x.dtype, (T, C))
     ds = 0 if dy is None else _tokens(dy, "dy", x.dtype, (T, C))
-    return _ConvDims(N, C, T, code, W, _ACT[activation], 0, xs, ds), W
+    return *_dims(_ConvDims, N, C, T, code, W, _ACT[activation], 0, xs, ds), W
 
 
 def conv_fwd(x, weight, bias=None, state=None, cu_seqlens=None, *, num_seqs: int | None = None,
@@ -362,7 +375,7 @@ def conv_fwd(x, weight, bias=None, state=None, cu_seqlens=None, *, num_seqs: int
     lib = load_library()
     T, C = _rank(x, "x", 2)
     N = _seqs(cu_seqlens, num_seqs, T)
-    d, W = _conv_dims(x, weight, bias, N, activation)
+    d, ref, W = _conv_dims(x, weight, bias, N, activation)
     _full(state, "state", x.dtype, (N, W - 1, C))
     _full(out, "out", x.dtype, (T, C))
     given = isinstance(final_state, torch.Tensor)
@@ -375,7 +388,7 @@ def conv_fwd(x, weight, bias=None, state=None, cu_seqlens=None, *, num_seqs: int
     for o in (out, sT if given else None):
         if o is not None:
             _apart(o, x, state, *(t for t in (out, sT) if t is not o))
-    _launch(lib.kda_conv_fwd, lib, x.device, (ctypes.byref(d), _p(x), _p(weight), _p(bias), _p(state), _p(cu_seqlens),
+    _launch(lib.kda_conv_fwd, lib, x.device, (ref, _p(x), _p(weight), _p(bias), _p(state), _p(cu_seqlens),
                                               _p(y), _p(sT)))
     return y, sT
 
@@ -389,7 +402,7 @@ def conv_bwd(x, weight, dy, bias=None, state=None, cu_seqlens=None, dstate_T=Non
     lib = load_library()
     T, C = _rank(x, "x", 2)
     N = _seqs(cu_seqlens, num_seqs, T)
-    d, W = _conv_dims(x, weight, bias, N, activation, _given(dy, "dy"))
+    d, ref, W = _conv_dims(x, weight, bias, N, activation, _given(dy, "dy"))
     _full(state, "state", x.dtype, (N, W - 1, C))
     _full(dstate_T, "dstate_T", x.dtype, (N, W - 1, C))
     _same_device(x, weight=weight, dy=dy, bias=bias, state=state, cu_seqlens=cu_seqlens, dstate_T=dstate_T,
@@ -399,8 +412,7 @@ def conv_bwd(x, weight, dy, bias=None, state=None, cu_seqlens=None, dstate_T=Non
     dw = _new(weight)
     db = torch.empty((C,), dtype=torch.float32, device=dev)
     ds = torch.empty((N, W - 1, C), dtype=x.dtype, device=dev) if initial_state_grad else None
-    ref = ctypes.byref(d)
-    ws = _workspace(lib, "kda_conv_bwd_workspace_size", d, (), workspace, dev)
+    ws = _workspace("kda_conv_bwd_workspace_size", d, (), workspace, dev)
     _launch(lib.kda_conv_bwd, lib, dev, (ref, _p(x), _p(weight), _p(bias), _p(state), _p(cu_seqlens), _p(dy),
                                          _p(dstate_T), _p(dx), _p(dw), _p(db), _p(ds), _p(ws), ws.numel()))
     return {"dx": dx, "dweight": dw, "dbias": db, "dstate": ds}
@@ -417,7 +429,7 @@ def conv_step(x, weight, state, bias=None, *, activation: str | None = "silu", o
     state_out is given; returns (y, state after)."""
     lib = load_library()
     N, C = _rank(x, "x", 2)
-    d, W = _conv_dims(x, weight, bias, N, activation)
+    d, ref, W = _conv_dims(x, weight, bias, N, activation)
     _full(_given(state, "state"), "state", x.dtype, (N, W - 1, C))
     _full(state_out, "state_out", x.dtype, (N, W - 1, C))
     _full(out, "out", x.dtype, (N, C))
@@ -428,7 +440,7 @@ def conv_step(x, weight, state, bias=None, *, activation: str | None = "silu", o
         _apart(out, x, state, state_out)
     if state_out is not None and state_out is not state:
         _apart(state_out, x, *(() if state_out.data_ptr() == state.data_ptr() else (state,)))
-    _launch(lib.kda_conv_step, lib, x.device, (ctypes.byref(d), _p(x), _p(weight), _p(bias), _p(state), _p(so), _p(y)))
+    _launch(lib.kda_conv_step, lib, x.device, (ref, _p(x), _p(weight), _p(bias), _p(state), _p(so), _p(y)))
     return y, so
 
 
@@ -443,7 +455,7 @@ def _norm_gate_dims(x, weight, gate, activation, eps, dy=None):
     xs = _tokens(x, "x", x.dtype, shape)
     gs = 0 if gate is None else _tokens(gate, "gate", x.dtype, shape)
     ds = 0 if dy is None else _tokens(dy, "dy", x.dtype, shape)
-    return _NormGateDims(T, H, D, _code(x), _ACT[activation], float(eps), 0, xs, gs, ds)
+    return _dims(_NormGateDims, T, H, D, _code(x), _ACT[activation], float(eps), 0, xs, gs, ds)
 
 
 def norm_gate_fwd(x, weight=None, gate=None, *, activation: str = "sigmoid", eps: float = 1e-6, out=None):
@@ -453,13 +465,13 @@ def norm_gate_fwd(x, weight=None, gate=None, *, activation: str = "sigmoid", eps
     activation "sigmoid" or "silu" of the gate; returns y [T, H, D].  out may be x.  A
     norm over the whole width is H = 1."""
     lib = load_library()
-    d = _norm_gate_dims(x, weight, gate, activation, eps)
+    d, ref = _norm_gate_dims(x, weight, gate, activation, eps)
     _full(out, "out", x.dtype, x.shape)
     _same_device(x, weight=weight, gate=gate, out=out)
     y = _new(x) if out is None else out
     if out is not None:
         _apart(out, gate, *(() if out.data_ptr() == x.data_ptr() and x.is_contiguous() else (x,)))
-    _launch(lib.kda_norm_gate_fwd, lib, x.device, (ctypes.byref(d), _p(x), _p(weight), _p(gate), _p(y)))
+    _launch(lib.kda_norm_gate_fwd, lib, x.device, (ref, _p(x), _p(weight), _p(gate), _p(y)))
     return y
 
 
@@ -468,14 +480,13 @@ def norm_gate_bwd(x, weight, dy, gate=None, *, activation: str = "sigmoid", eps:
     "dgate" None without a gate) and "dweight" [D] fp32 (None without a weight).
     workspace: at least norm_gate_bwd_workspace_size bytes (with a weight)."""
     lib = load_library()
-    d = _norm_gate_dims(x, weight, gate, activation, eps, _given(dy, "dy"))
+    d, ref = _norm_gate_dims(x, weight, gate, activation, eps, _given(dy, "dy"))
     _same_device(x, weight=weight, dy=dy, gate=gate, workspace=workspace)
     dev = x.device
     dx = _new(x)
     dg = None if gate is None else _new(x)
     dw = None if weight is None else torch.empty(x.shape[2], dtype=torch.float32, device=dev)
-    ref = ctypes.byref(d)
-    ws = None if dw is None else _workspace(lib, "kda_norm_gate_bwd_workspace_size", d, (), workspace, dev)
+    ws = None if dw is None else _workspace("kda_norm_gate_bwd_workspace_size", d, (), workspace, dev)
     _launch(lib.kda_norm_gate_bwd, lib, dev, (ref, _p(x), _p(weight), _p(gate), _p(dy), _p(dx), _p(dg), _p(dw),
                                               _p(ws), 0 if ws is None else ws.numel()))
     return {"dx": dx, "dgate": dg, "dweight": dw}
@@ -498,7 +509,7 @@ def _res_norm_dims(x, res, weight, channel_scale, scale, eps, rname, dy=None, dr
     rs = _tokens(res, rname, res.dtype, shape)
     ds = 0 if dy is None else _tokens(dy, "dy", like.dtype, shape)
     drs = 0 if dres is None else _tokens(dres, "dresidual_out", res.dtype, shape)
-    return _ResNormDims(shape[0], D, code, rcode, float(eps), float(scale), 0, xs, rs, ds, drs), like
+    return *_dims(_ResNormDims, shape[0], D, code, rcode, float(eps), float(scale), 0, xs, rs, ds, drs), like
 
 
 def residual_norm_fwd(x, residual, weight, *, scale: float = 1.0, channel_scale=None, eps: float = 1e-6, out=None,
@@ -511,7 +522,7 @@ def residual_norm_fwd(x, residual, weight, *, scale: float = 1.0, channel_scale=
     sum before its rounding.  residual_out may be residual."""
     lib = load_library()
     _rank(x, "x", 2)
-    d, _ = _res_norm_dims(x, residual, weight, channel_scale, scale, eps, "residual")
+    d, ref, _ = _res_norm_dims(x, residual, weight, channel_scale, scale, eps, "residual")
     _full(out, "out", x.dtype, x.shape)
     _full(residual_out, "residual_out", residual.dtype, x.shape)
     _same_device(x, residual=residual, weight=weight, channel_scale=channel_scale, out=out, residual_out=residual_out)
@@ -522,7 +533,7 @@ def residual_norm_fwd(x, residual, weight, *, scale: float = 1.0, channel_scale=
     if residual_out is not None:
         same = residual_out.data_ptr() == residual.data_ptr() and residual.is_contiguous()
         _apart(residual_out, x, *(() if same else (residual,)))
-    _launch(lib.kda_residual_norm_fwd, lib, x.device, (ctypes.byref(d), _p(x), _p(residual), _p(weight),
+    _launch(lib.kda_residual_norm_fwd, lib, x.device, (ref, _p(x), _p(residual), _p(weight),
                                                        _p(channel_scale), _p(r), _p(y)))
     return y, r
 
@@ -537,7 +548,7 @@ def residual_norm_bwd(x, residual_out, weight, dy, dresidual_out=None, *, scale:
     lib = load_library()
     if x is None and channel_scale is not None:
         raise TypeError("x is needed for the derivative of channel_scale")
-    d, like = _res_norm_dims(x, residual_out, weight, channel_scale, scale, eps, "residual_out", _given(dy, "dy"),
+    d, ref, like = _res_norm_dims(x, residual_out, weight, channel_scale, scale, eps, "residual_out", _given(dy, "dy"),
                              dresidual_out)
     _same_device(residual_out, x=x, weight=weight, channel_scale=channel_scale, dy=dy, dresidual_out=dresidual_out,
                  workspace=workspace)
@@ -546,8 +557,7 @@ def residual_norm_bwd(x, residual_out, weight, dy, dresidual_out=None, *, scale:
     dr = _new(residual_out)
     dw = torch.empty(shape[1], dtype=torch.float32, device=dev)
     dc = None if channel_scale is None else torch.empty(shape[1], dtype=torch.float32, device=dev)
-    ref = ctypes.byref(d)
-    ws = _workspace(lib, "kda_residual_norm_bwd_workspace_size", d, (), workspace, dev)
+    ws = _workspace("kda_residual_norm_bwd_workspace_size", d, (), workspace, dev)
     _launch(lib.kda_residual_norm_bwd, lib, dev, (ref, _p(x), _p(residual_out), _p(weight), _p(channel_scale), _p(dy),
                                                   _p(dresidual_out), _p(dx), _p(dr), _p(dw), _p(dc), _p(ws),
                                                   ws.numel()))
@@ -557,4 +567,5 @@ def residual_norm_bwd(x, residual_out, weight, dy, dresidual_out=None, *, scale:
 def residual_norm_bwd_workspace_size(x):
     """Bytes of workspace residual_norm_bwd needs for x's shape and dtype."""
     T, D = _rank(x, "x", 2)
-    return _size("kda_residual_norm_bwd_workspace_size", _ResNormDims(T, D, _code(x), _code(x), 0.0, 1.0, 0, 0, 0, 0, 0))
+    d = _ResNormDims(T, D, _code(x), _code(x), 0.0, 1.0, 0, 0, 0, 0, 0)
+    return _size("kda_residual_norm_bwd_workspace_size", d)
