@@ -7,9 +7,9 @@
 //   gradient at h, with d = dy w:
 //     dh = dres + r (d - n mean(d n)),  dx = c dh,  dw = sum dy n,  dcs = scale sum dh x
 //
-// All are one pass over HBM: each row is read once into registers, its sums are
-// formed over the G lanes (or the whole workgroup) that hold it, and the
-// outputs leave from the same registers.  mean(d n) = r mean(d x), so both of
+// All are one pass over HBM, which bounds them (5.2 to 5.9 TB/s on large inputs): each
+// row is read once into registers, its sums are formed over the G lanes (or the
+// whole workgroup) that hold it, and the outputs leave from the same registers.  mean(d n) = r mean(d x), so both of
 // the backward's sums are formed before r is known and share one reduction.
 #include "kda_block.hpp"
 #include "kda_rows.hpp"
@@ -17,9 +17,10 @@
 namespace kda {
 namespace {
 
-constexpr int BT = 256;
+// Threads of a workgroup whose rows take G lanes: 256, or one row's G.
+constexpr int threads_of(int g) { return g > 256 ? g : 256; }
 
-// Sums of A values over the lanes of a row: G lanes of a wavefront, or (G = BT)
+// Sums of A values over the lanes of a row: G lanes of a wavefront, or (G >= 256)
 // the whole workgroup through LDS.
 template <int G, int A>
 __device__ __forceinline__ void row_sum(float (&v)[A], float* lds) {
@@ -27,7 +28,7 @@ __device__ __forceinline__ void row_sum(float (&v)[A], float* lds) {
 #pragma unroll
         for (int i = 0; i < A; ++i) v[i] = lanes_sum<G>(v[i]);
     } else {
-        constexpr int NW = BT / WAVE;
+        constexpr int NW = G / WAVE;
         const int wv = threadIdx.x / WAVE;
         __syncthreads();  // the previous row's sums have been read
 #pragma unroll
@@ -59,11 +60,11 @@ template <int V, int G> struct Cols {
     }
 };
 
-// A workgroup's partial column sums: each of its BT / G row groups holds acc for
+// A workgroup's partial column sums: each of its row groups holds acc for
 // the same columns; summed in group order and written to out[0 .. D).
 template <int G, int VPT, int V>
 __device__ __forceinline__ void block_partial(const float (&acc)[VPT][V], float* lds, float* out, int D) {
-    constexpr int RPB = BT / G, W_ = G * VPT * V;
+    constexpr int BT = threads_of(G), RPB = BT / G, W_ = G * VPT * V;
     const int g = threadIdx.x % G, rg = threadIdx.x / G;
     __syncthreads();
 #pragma unroll
@@ -99,8 +100,8 @@ template <int GATE> __device__ __forceinline__ float gate_slope(float g, float s
 }
 
 template <typename T, int V, int G, int VPT, int GATE>
-__global__ __launch_bounds__(BT) void norm_gate_fwd_kernel(NormGateArgs a) {
-    constexpr int RPB = BT / G;
+__global__ __launch_bounds__(threads_of(G)) void norm_gate_fwd_kernel(NormGateArgs a) {
+    constexpr int BT = threads_of(G), RPB = BT / G;
     __shared__ float lds[BT / WAVE];
     const int g = threadIdx.x % G, D = a.width;
     const float invD = 1.f / (float)D;
@@ -147,8 +148,8 @@ __global__ __launch_bounds__(BT) void norm_gate_fwd_kernel(NormGateArgs a) {
 }
 
 template <typename T, int V, int G, int VPT, int GATE>
-__global__ __launch_bounds__(BT) void norm_gate_bwd_kernel(NormGateArgs a) {
-    constexpr int RPB = BT / G;
+__global__ __launch_bounds__(threads_of(G)) void norm_gate_bwd_kernel(NormGateArgs a) {
+    constexpr int BT = threads_of(G), RPB = BT / G;
     __shared__ float lds[RPB > 1 ? RPB * G * VPT * V : 2 * BT / WAVE];
     const int g = threadIdx.x % G, D = a.width;
     const float invD = 1.f / (float)D;
@@ -212,8 +213,8 @@ __global__ __launch_bounds__(BT) void norm_gate_bwd_kernel(NormGateArgs a) {
 }
 
 template <typename T, typename R, int V, int G, int VPT>
-__global__ __launch_bounds__(BT) void res_norm_fwd_kernel(ResNormArgs a) {
-    constexpr int RPB = BT / G;
+__global__ __launch_bounds__(threads_of(G)) void res_norm_fwd_kernel(ResNormArgs a) {
+    constexpr int BT = threads_of(G), RPB = BT / G;
     __shared__ float lds[BT / WAVE];
     const int g = threadIdx.x % G, D = a.width;
     const float invD = 1.f / (float)D;
@@ -258,8 +259,8 @@ __global__ __launch_bounds__(BT) void res_norm_fwd_kernel(ResNormArgs a) {
 }
 
 template <typename T, typename R, int V, int G, int VPT>
-__global__ __launch_bounds__(BT) void res_norm_bwd_kernel(ResNormArgs a) {
-    constexpr int RPB = BT / G;
+__global__ __launch_bounds__(threads_of(G)) void res_norm_bwd_kernel(ResNormArgs a) {
+    constexpr int BT = threads_of(G), RPB = BT / G;
     __shared__ float lds[RPB > 1 ? RPB * G * VPT * V : 2 * BT / WAVE];
     const int g = threadIdx.x % G, D = a.width;
     const float invD = 1.f / (float)D;
@@ -369,8 +370,8 @@ RowShape row_shape(int nv) {
     if (nv <= 128) return {64, 2};
     if (nv <= 256) return {256, 1};
     if (nv <= 512) return {256, 2};
-    if (nv <= 1024) return {256, 4};
-    return {256, 8};
+    if (nv <= 1024) return {512, 2};
+    return {512, 4};
 }
 // Elements per lane and access: 16 bytes of the row's type, single elements in
 // rows shorter than that.
@@ -379,15 +380,26 @@ int vec_of(int dtype, int width) {
     return width >= v ? v : 1;
 }
 
-int blocks_for(int dtype, int width, int64_t rows, int most) {
+int vecs_of(int dtype, int width) {
     const int v = vec_of(dtype, width);
-    const RowShape s = row_shape((width + v - 1) / v);
-    const int64_t rpb = BT / s.g, b = (rows + rpb - 1) / rpb;
+    return (width + v - 1) / v;
+}
+
+// Workgroups of `rows` rows of nv vectors, at most `most`.
+int blocks_for(int nv, int64_t rows, int most) {
+    const RowShape s = row_shape(nv);
+    const int64_t rpb = threads_of(s.g) / s.g, b = (rows + rpb - 1) / rpb;
     return (int)(b < most ? b : most);
 }
 
 constexpr int FWD_BLOCKS = 1 << 20;  // one row group each up to here
-constexpr int BWD_BLOCKS = 1024;     // four workgroups per compute unit; each writes one partial row
+// The backward's workgroups, a whole number for each of the 256 compute units
+// each of which leaves a partial row:
+// fewer where rows are long.  Of 256, 512, 768 and 1024, measured in bf16:
+//   gated norm, 32768 x 32 rows of 128: 477, 285, 246, 255 us;  20000 rows of 4096: 228, 163, 168, 188
+//   residual norm, 20000 rows of 1000 (fp32): 130, 79, 81, 84;  16384 rows of 4096: 229, 237, 257, 250
+int ng_blocks(int nv) { return nv > 256 ? 512 : 768; }
+int rn_blocks(int nv) { return nv > 256 ? 256 : 512; }
 
 #define KDA_ROW_CASES(RUN, V)                                                                                  \
     switch (s.g * 16 + s.vpt) {                                                                                \
@@ -403,15 +415,15 @@ constexpr int BWD_BLOCKS = 1024;     // four workgroups per compute unit; each w
         case 64 * 16 + 2: RUN(V, 64, 2); break;                                                                \
         case 256 * 16 + 1: RUN(V, 256, 1); break;                                                              \
         case 256 * 16 + 2: RUN(V, 256, 2); break;                                                              \
-        case 256 * 16 + 4: RUN(V, 256, 4); break;                                                              \
-        default: if constexpr (V == 4) { RUN(V, 256, 8); }                                                     \
+        case 512 * 16 + 2: RUN(V, 512, 2); break;                                                              \
+        default: if constexpr (V == 4) { RUN(V, 512, 4); }                                                     \
     }
 
 template <typename T, int V>
 void norm_gate_launch(const NormGateArgs& a, bool backward, int blocks, RowShape s, hipStream_t st) {
 #define RUN_NG1(V_, G, VPT, GATE)                                                                                    \
-    if (backward) hipLaunchKernelGGL((norm_gate_bwd_kernel<T, V_, G, VPT, GATE>), dim3(blocks), dim3(BT), 0, st, a); \
-    else hipLaunchKernelGGL((norm_gate_fwd_kernel<T, V_, G, VPT, GATE>), dim3(blocks), dim3(BT), 0, st, a)
+    if (backward) hipLaunchKernelGGL((norm_gate_bwd_kernel<T, V_, G, VPT, GATE>), dim3(blocks), dim3(threads_of(G)), 0, st, a); \
+    else hipLaunchKernelGGL((norm_gate_fwd_kernel<T, V_, G, VPT, GATE>), dim3(blocks), dim3(threads_of(G)), 0, st, a)
 #define RUN_NG(V_, G, VPT)                               \
     if (!a.gate) { RUN_NG1(V_, G, VPT, GATE_NONE); }     \
     else if (a.silu) { RUN_NG1(V_, G, VPT, GATE_SILU); } \
@@ -422,8 +434,8 @@ void norm_gate_launch(const NormGateArgs& a, bool backward, int blocks, RowShape
 template <typename T, typename R, int V>
 void res_norm_launch(const ResNormArgs& a, bool backward, int blocks, RowShape s, hipStream_t st) {
 #define RUN_RN(V_, G, VPT)                                                                                       \
-    if (backward) hipLaunchKernelGGL((res_norm_bwd_kernel<T, R, V_, G, VPT>), dim3(blocks), dim3(BT), 0, st, a); \
-    else hipLaunchKernelGGL((res_norm_fwd_kernel<T, R, V_, G, VPT>), dim3(blocks), dim3(BT), 0, st, a)
+    if (backward) hipLaunchKernelGGL((res_norm_bwd_kernel<T, R, V_, G, VPT>), dim3(blocks), dim3(threads_of(G)), 0, st, a); \
+    else hipLaunchKernelGGL((res_norm_fwd_kernel<T, R, V_, G, VPT>), dim3(blocks), dim3(threads_of(G)), 0, st, a)
     KDA_ROW_CASES(RUN_RN, V)
 }
 
@@ -436,12 +448,16 @@ hipError_t launch_colsum(const float* part, int rows, int64_t cols, int64_t spli
     return hipGetLastError();
 }
 
-int norm_gate_blocks(int dtype, int width, int64_t rows) { return blocks_for(dtype, width, rows, BWD_BLOCKS); }
+int norm_gate_blocks(int dtype, int width, int64_t rows) {
+    const int nv = vecs_of(dtype, width);
+    return blocks_for(nv, rows, ng_blocks(nv));
+}
 
 hipError_t launch_norm_gate(const NormGateArgs& a, bool backward, hipStream_t st) {
     const int v = vec_of(a.dtype, a.width);
-    const RowShape s = row_shape((a.width + v - 1) / v);
-    const int blocks = blocks_for(a.dtype, a.width, a.rows, backward ? BWD_BLOCKS : FWD_BLOCKS);
+    const int nv = vecs_of(a.dtype, a.width);
+    const RowShape s = row_shape(nv);
+    const int blocks = blocks_for(nv, a.rows, backward ? ng_blocks(nv) : FWD_BLOCKS);
     if (a.dtype == 1 && v == 1) norm_gate_launch<bf16, 1>(a, backward, blocks, s, st);
     else if (a.dtype == 1) norm_gate_launch<bf16, 8>(a, backward, blocks, s, st);
     else if (v == 1) norm_gate_launch<float, 1>(a, backward, blocks, s, st);
@@ -449,12 +465,16 @@ hipError_t launch_norm_gate(const NormGateArgs& a, bool backward, hipStream_t st
     return hipGetLastError();
 }
 
-int res_norm_blocks(int dtype, int width, int64_t rows) { return blocks_for(dtype, width, rows, BWD_BLOCKS); }
+int res_norm_blocks(int dtype, int width, int64_t rows) {
+    const int nv = vecs_of(dtype, width);
+    return blocks_for(nv, rows, rn_blocks(nv));
+}
 
 hipError_t launch_res_norm(const ResNormArgs& a, bool backward, hipStream_t st) {
     const int v = vec_of(a.dtype, a.width);
-    const RowShape s = row_shape((a.width + v - 1) / v);
-    const int blocks = blocks_for(a.dtype, a.width, a.rows, backward ? BWD_BLOCKS : FWD_BLOCKS);
+    const int nv = vecs_of(a.dtype, a.width);
+    const RowShape s = row_shape(nv);
+    const int blocks = blocks_for(nv, a.rows, backward ? rn_blocks(nv) : FWD_BLOCKS);
     if (v == 1) {
         if (a.dtype == 1 && a.rdtype == 1) res_norm_launch<bf16, bf16, 1>(a, backward, blocks, s, st);
         else if (a.dtype == 1) res_norm_launch<bf16, float, 1>(a, backward, blocks, s, st);
