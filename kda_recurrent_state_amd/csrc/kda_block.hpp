@@ -85,7 +85,7 @@ struct LinScanArgs {
     int64_t xs, ls, ds;
     int32_t dtype;
 };
-constexpr int LINSCAN_TILE = 128;
+constexpr int LINSCAN_TILE = 128;  // tokens of the shortest tiles
 constexpr int LINSCAN_LINE = 16;  // words of a 128-byte line
 // The chain between tiles: one word per tile and channel, and a counter per block
 // of 64 channels or more.

@@ -3,9 +3,10 @@
 //   h_t = a_t h_{t-1} + x_t,  a_t = e^{log a_t},  y_t = h_t            per channel
 //   g_t = dy_t + a_{t+1} g_{t+1},  dx_t = g_t,  dlog a_t = g_t a_t h_{t-1}
 //
-// HBM-bound, so x and log a are read once.  The packed axis is cut into tiles of
-// 128 tokens whatever the sequences' edges; a workgroup holds one tile of 64 V
-// channels, each of its eight wavefronts 16 tokens in registers.  A run of tokens
+// HBM-bound (2 x 32768 x 4096 bf16: 409 us, 5.3 TB/s), so x and log a are read once.
+// The packed axis is cut into tiles of 128 or 256 tokens whatever the sequences'
+// edges; a workgroup holds one tile of 64 V channels, each of its wavefronts 16
+// tokens in registers.  A run of tokens
 // maps the state before it to P h + E (P the product of its a, E its end from a
 // zero state), or, if a sequence starts in it, to E alone: that case is marked
 // by P = -1 and chosen, never multiplied, so that nothing of an earlier
@@ -29,10 +30,8 @@
 namespace kda {
 namespace {
 
-constexpr int TT = LINSCAN_TILE;       // tokens per tile
-constexpr int NW = 8, BT = NW * WAVE;  // wavefronts of a workgroup
-constexpr int TW = TT / NW;            // tokens per wavefront
-constexpr int SW = 64 / TW;            // wavefronts between two rows of states
+constexpr int TW = 16;       // tokens per wavefront; a workgroup's NW wavefronts hold a tile
+constexpr int SW = 64 / TW;  // wavefronts between two rows of states
 constexpr uint32_t EMPTY = 0xffffffffu;  // P of a word not yet published
 constexpr uint32_t KNOWN = 0xbf800000u;  // P = -1: E is the state itself
 // Polls before a wait is given up (seconds; reached only if the workspace is
@@ -60,9 +59,9 @@ __device__ __forceinline__ uint64_t read_word(const uint64_t* word) {
 // The nearest LB are read together; after that a poll reads only the farthest
 // again, whose state is the first to become known, and what was not there yet.
 // Forwards LB = 4 keeps a wide chain ahead of the memory (2 x 32768 x 4096: 409 us;
-// LB = 2: 415, 8: 416, 1: 473); narrow ones (fewer than 32 column blocks), which
-// wait for each other more than for memory, take 8 (4096 x 2048: 21 us, 4: 23, 16:
-// 27; 60000 x 64: 38, 4: 46).  Backwards 4, in float32 2 for its registers.
+// LB = 2: 415, 8: 416, 1: 473); narrow ones take 8 (in tiles of 128, 4096 x 2048:
+// 21 us, 4: 23, 16: 27; 60000 x 64: 38, 4: 46).  Backwards 4, in float32 2 for its
+// registers.
 template <int LB>  // words of the chain read at once
 __device__ __forceinline__ float look_back(const uint64_t* word, int64_t step, int behind) {
     const int far = (behind < LB ? behind : LB) - 1;
@@ -237,7 +236,7 @@ __device__ __forceinline__ void run_backward(const LinScanArgs& p, const Seqs& s
 __device__ __forceinline__ void empty_seqs(const Seqs& sq, const float* from, float* to, int C, int block, int blocks) {
     for (int n = block; n < sq.N; n += blocks) {
         if (sq.start(n + 1) > sq.start(n)) continue;
-        for (int c = threadIdx.x; c < C; c += BT) to[(int64_t)n * C + c] = from ? from[(int64_t)n * C + c] : 0.f;
+        for (int c = threadIdx.x; c < C; c += (int)blockDim.x) to[(int64_t)n * C + c] = from ? from[(int64_t)n * C + c] : 0.f;
     }
 }
 
@@ -265,7 +264,7 @@ __device__ __forceinline__ void take_tile(uint64_t* tickets, int cblocks, int* l
 // The tile's (P, E) from its wavefronts', the state handed to it, and its own
 // published: thread j < 64 V does channel j of the workgroup.  In: sp, se; out:
 // sh, the state handed to the tile.  BACK: from the last wavefront to the first.
-template <int V, bool BACK, int LB>
+template <int V, int NW, bool BACK, int LB>
 __device__ __forceinline__ void chain(const LinScanArgs& p, const float (&sp)[NW][WAVE * V],
                                       const float (&se)[NW][WAVE * V], float (&sh)[WAVE * V], int cb, int tile,
                                       int tiles) {
@@ -289,8 +288,8 @@ __device__ __forceinline__ void chain(const LinScanArgs& p, const float (&sp)[NW
 }
 
 // OUT: y and hT too, else the states alone.
-template <typename T, int V, bool OUT, int LB>
-__global__ __launch_bounds__(BT) void linscan_fwd_kernel(LinScanArgs p, int tiles, int cblocks, uint64_t* tickets) {
+template <typename T, int V, int NW, bool OUT, int LB>
+__global__ __launch_bounds__(NW* WAVE) void linscan_fwd_kernel(LinScanArgs p, int tiles, int cblocks, uint64_t* tickets) {
     __shared__ float sp[NW][WAVE * V], se[NW][WAVE * V], sh[WAVE * V];
     __shared__ int s_tile;
     const Seqs sq{p.cu, p.N, p.T, p.eq};
@@ -304,7 +303,7 @@ __global__ __launch_bounds__(BT) void linscan_fwd_kernel(LinScanArgs p, int tile
     if (tile >= tiles) return;
     const int lane = threadIdx.x % WAVE, wv = __builtin_amdgcn_readfirstlane(threadIdx.x / WAVE);
     const int c = column<V>((cb * WAVE + lane) * V, p.C);  // lanes past the row's end: its last, once more
-    const int t0 = tile * TT + wv * TW;
+    const int t0 = (tile * NW + wv) * TW;
     Pack<float, V> la[TW];
     Pack<T, V> x[TW];
     load_rows<V>(p.la, p.ls, t0, p.T, c, la);
@@ -317,7 +316,7 @@ __global__ __launch_bounds__(BT) void linscan_fwd_kernel(LinScanArgs p, int tile
 #pragma unroll
     for (int v = 0; v < V; ++v) sp[wv][lane * V + v] = P[v], se[wv][lane * V + v] = E[v];
     __syncthreads();
-    chain<V, false, LB>(p, sp, se, sh, cb, tile, tiles);
+    chain<V, NW, false, LB>(p, sp, se, sh, cb, tile, tiles);
     __syncthreads();
 #pragma unroll
     for (int v = 0; v < V; ++v) h[v] = sh[lane * V + v];
@@ -338,8 +337,8 @@ __global__ __launch_bounds__(BT) void linscan_fwd_kernel(LinScanArgs p, int tile
     }
 }
 
-template <typename T, int V>
-__global__ __launch_bounds__(BT, 4) void linscan_bwd_kernel(LinScanArgs p, int tiles, int cblocks, uint64_t* tickets) {
+template <typename T, int V, int NW>
+__global__ __launch_bounds__(NW* WAVE, 4) void linscan_bwd_kernel(LinScanArgs p, int tiles, int cblocks, uint64_t* tickets) {
     __shared__ float sp[NW][WAVE * V], se[NW][WAVE * V], rp[NW][WAVE * V], re[NW][WAVE * V], sh[WAVE * V];
     __shared__ int s_tile;
     const Seqs sq{p.cu, p.N, p.T, p.eq};
@@ -354,14 +353,14 @@ __global__ __launch_bounds__(BT, 4) void linscan_bwd_kernel(LinScanArgs p, int t
     if (tile < 0) return;
     const int lane = threadIdx.x % WAVE, wv = __builtin_amdgcn_readfirstlane(threadIdx.x / WAVE);
     const int c = column<V>((cb * WAVE + lane) * V, p.C);  // lanes past the row's end: its last, once more
-    const int t0 = tile * TT + wv * TW;
+    const int t0 = (tile * NW + wv) * TW;
     Pack<float, V> la[TW];
     Pack<T, V> x[TW], dy[TW];
     load_rows<V>(p.la, p.ls, t0, p.T, c, la);
     load_rows<V>((const T*)p.dy, p.ds, t0, p.T, c, dy);
     load_rows<V>((const T*)p.x, p.xs, t0, p.T, c, x);
     // the state before the 64 tokens that this wavefront's belong to
-    const int row = (tile * TT + wv / SW * SW * TW) / (SW * TW), rows = (p.T + SW * TW - 1) / (SW * TW);
+    const int row = (tile * NW + wv) / SW, rows = (p.T + SW * TW - 1) / (SW * TW);
     float h[V], g[V];
     get_v<V>(load_v<V>(p.states + (int64_t)(row < rows ? row : rows - 1) * p.C + c), h);
     const Edges ed = edges_of(sq, t0, sq.end());
@@ -376,7 +375,7 @@ __global__ __launch_bounds__(BT, 4) void linscan_bwd_kernel(LinScanArgs p, int t
 #pragma unroll
     for (int v = 0; v < V; ++v) sp[wv][lane * V + v] = P[v], se[wv][lane * V + v] = E[v];
     __syncthreads();
-    chain<V, true, sizeof(T) == 4 ? 2 : 4>(p, rp, re, sh, cb, tile, tiles);
+    chain<V, NW, true, sizeof(T) == 4 ? 2 : 4>(p, rp, re, sh, cb, tile, tiles);
     // the state before every token of the run
     for (int w = wv / SW * SW; w < wv; ++w)
 #pragma unroll
@@ -443,13 +442,21 @@ __global__ __launch_bounds__(BS) void linscan_step_kernel(LinScanArgs p) {
     }
 }
 
-int tiles_of(int T) { return (T + TT - 1) / TT; }
 int empty_blocks(int N) { return N < 64 ? N : 64; }
 
+// A chain is narrow below 32 column blocks.  Its tiles wait for each other more
+// than for memory, so they are longer: 256 tokens on 16 wavefronts.  In a wide one
+// 128 on 8 leave room for two workgroups on a compute unit, one loading while
+// the other waits or stores.  Measured, 256 against 128: 2 x 32768 x 4096 bf16
+// 489 us against 409, 24571 x 4096 fp32 239 against 214; 24571 x 1000 fp32 71
+// against 75, 4096 x 2048 bf16 19.6 against 21.0, 60000 x 64 26 against 38.  (Tiles
+// of 64: 466, 227; 82, 24.7, 64.)
+template <int V> bool narrow(int C) { return C < 32 * WAVE * V; }
+
 // Clears the chain (more than one tile) and gives the launch its grid.
-template <int V, typename K>
+template <int V, int NW, typename K>
 hipError_t run_chain(K kernel, const LinScanArgs& a, bool empties, hipStream_t st) {
-    const int tiles = tiles_of(a.T), cblocks = (a.C + WAVE * V - 1) / (WAVE * V);
+    const int tiles = (a.T + NW * TW - 1) / (NW * TW), cblocks = (a.C + WAVE * V - 1) / (WAVE * V);
     const int64_t blocks = (int64_t)tiles * cblocks + (empties ? empty_blocks(a.N) : 0);
     if (blocks == 0) return hipSuccess;
     uint64_t* tickets = nullptr;
@@ -459,7 +466,7 @@ hipError_t run_chain(K kernel, const LinScanArgs& a, bool empties, hipStream_t s
         hipLaunchKernelGGL(linscan_clear_kernel, dim3((unsigned)((words + counters + 511) / 512)), dim3(256), 0, st,
                            a.word, words, counters);
     }
-    hipLaunchKernelGGL(kernel, dim3((unsigned)blocks), dim3(BT), 0, st, a, tiles, cblocks, tickets);
+    hipLaunchKernelGGL(kernel, dim3((unsigned)blocks), dim3(NW * WAVE), 0, st, a, tiles, cblocks, tickets);
     return hipGetLastError();
 }
 
@@ -467,12 +474,19 @@ template <typename T, int V, bool OUT>
 hipError_t fwd(const LinScanArgs& a, hipStream_t st) {
     const bool empties = OUT && a.hT;
     if constexpr (V > 1)
-        if (a.C >= 32 * WAVE * V) return run_chain<V>(linscan_fwd_kernel<T, V, OUT, 4>, a, empties, st);
-    return run_chain<V>(linscan_fwd_kernel<T, V, OUT, 8>, a, empties, st);
+        if (!narrow<V>(a.C)) return run_chain<V, 8>(linscan_fwd_kernel<T, V, 8, OUT, 4>, a, empties, st);
+    return run_chain<V, 16>(linscan_fwd_kernel<T, V, 16, OUT, 8>, a, empties, st);
 }
 template <typename T, int V>
 hipError_t fwd(const LinScanArgs& a, bool out, hipStream_t st) {
     return out ? fwd<T, V, true>(a, st) : fwd<T, V, false>(a, st);
+}
+template <typename T, int V>
+hipError_t bwd(const LinScanArgs& a, hipStream_t st) {
+    const bool empties = a.hT != nullptr;
+    if constexpr (V > 1)
+        if (!narrow<V>(a.C)) return run_chain<V, 8>(linscan_bwd_kernel<T, V, 8>, a, empties, st);
+    return run_chain<V, 16>(linscan_bwd_kernel<T, V, 16>, a, empties, st);
 }
 
 }  // namespace
@@ -483,12 +497,8 @@ hipError_t launch_linscan_fwd(const LinScanArgs& a, bool out, hipStream_t st) {
 }
 
 hipError_t launch_linscan_bwd(const LinScanArgs& a, hipStream_t st) {
-    const bool empties = a.hT != nullptr;
-    if (a.C < 2)
-        return a.dtype == 1 ? run_chain<1>(linscan_bwd_kernel<bf16, 1>, a, empties, st)
-                            : run_chain<1>(linscan_bwd_kernel<float, 1>, a, empties, st);
-    return a.dtype == 1 ? run_chain<2>(linscan_bwd_kernel<bf16, 2>, a, empties, st)
-                        : run_chain<2>(linscan_bwd_kernel<float, 2>, a, empties, st);
+    if (a.C < 2) return a.dtype == 1 ? bwd<bf16, 1>(a, st) : bwd<float, 1>(a, st);
+    return a.dtype == 1 ? bwd<bf16, 2>(a, st) : bwd<float, 2>(a, st);
 }
 
 hipError_t launch_linscan_step(const LinScanArgs& a, hipStream_t st) {
