@@ -47,7 +47,7 @@ struct ResNormArgs {
     int32_t dtype, rdtype;
 };
 hipError_t launch_res_norm(const ResNormArgs& a, bool backward, hipStream_t st);
-int res_norm_blocks(int dtype, int width, int64_t rows);
+int res_norm_blocks(const ResNormArgs& a);  // workgroups (partial rows) of the backward
 
 struct ConvArgs {
     const void* x;

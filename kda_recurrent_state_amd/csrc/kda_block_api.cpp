@@ -207,8 +207,14 @@ int plan_res_norm(const kda_residual_norm_dims_t* d, kda::ResNormArgs* a) {
 }
 
 // the larger of the backward's two layouts (with and without dchannel_scale)
-size_t res_norm_workspace(const kda::ResNormArgs& a) {
-    return round256((size_t)kda::res_norm_blocks(a.dtype, a.width, a.rows) * a.width * 2 * 4);
+size_t res_norm_workspace(kda::ResNormArgs a) {
+    size_t most = 0;
+    for (int dcs = 0; dcs < 2; ++dcs) {
+        a.want_dcs = dcs;
+        const size_t bytes = (size_t)kda::res_norm_blocks(a) * a.width * (dcs + 1) * 4;
+        if (bytes > most) most = bytes;
+    }
+    return round256(most);
 }
 
 }  // namespace
@@ -481,7 +487,7 @@ int kda_residual_norm_bwd(const kda_residual_norm_dims_t* d, const void* x, cons
     a.want_dcs = dchannel_scale != nullptr;
     if (a.rows > 0) KDA_TRY(hip_status(kda::launch_res_norm(a, true, (hipStream_t)stream), "residual norm gradient"));
     if (!sums) return ok();
-    return hip_status(kda::launch_colsum(a.part, kda::res_norm_blocks(a.dtype, a.width, a.rows),
+    return hip_status(kda::launch_colsum(a.part, kda::res_norm_blocks(a),
                                          (int64_t)a.width * (a.want_dcs ? 2 : 1), a.width, dweight, dchannel_scale,
                                          (hipStream_t)stream),
                       "residual norm gradient");

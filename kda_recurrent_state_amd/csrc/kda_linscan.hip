@@ -40,12 +40,12 @@ constexpr int MAX_POLLS = 1 << 21;
 
 // One run of tokens followed by another: (p, e) <- (p2, e2) after (p, e).  Fused
 // multiply-adds by name: a state folded in by a waiting workgroup has to have the
-// bits of the one that its owner publishes.
+// bits of the one that its owner publishes.  (-1 times a chosen 0 leaves e2 as it is.)
 __device__ __forceinline__ void then(float& p, float& e, float p2, float e2) {
-    e = p2 < 0.f ? e2 : fmaf(p2, e, e2);
+    e = fmaf(p2, p2 < 0.f ? 0.f : e, e2);
     p = p2 < 0.f ? -1.f : p < 0.f ? -1.f : p2 * p;
 }
-__device__ __forceinline__ float apply(float p, float e, float h) { return p < 0.f ? e : fmaf(p, h, e); }
+__device__ __forceinline__ float apply(float p, float e, float h) { return fmaf(p, p < 0.f ? 0.f : h, e); }
 
 __device__ __forceinline__ void publish(uint64_t* word, float p, float e) {
     const uint32_t pb = p == p ? __float_as_uint(p) : 0x7fc00000u;  // no NaN reads as EMPTY

@@ -359,7 +359,11 @@ __global__ __launch_bounds__(CSW* CSR) void colsum_kernel(const float* part, int
     }
 }
 
-// Lanes and vectors per lane of a row of nv vectors.
+// Lanes and vectors per lane of a row of nv vectors: a wavefront or part of it up to
+// two vectors a lane, longer rows a workgroup.  Measured, bf16, 64e6 values, forward and
+// gradient in us: rows of 1024 as here 92 and 128, over 256 lanes 92 and 223; 2048
+// here 93 and 132, a wavefront with four a lane 92 and 132; 4096 here 94, over 512
+// lanes 92; 8192 here 97 and 137, 256 lanes with four 95 and 149.
 struct RowShape { int g, vpt; };
 RowShape row_shape(int nv) {
     if (nv <= 4) return {4, 1};
@@ -393,13 +397,19 @@ int blocks_for(int nv, int64_t rows, int most) {
 }
 
 constexpr int FWD_BLOCKS = 1 << 20;  // one row group each up to here
-// The backward's workgroups, a whole number for each of the 256 compute units
-// each of which leaves a partial row:
-// fewer where rows are long.  Of 256, 512, 768 and 1024, measured in bf16:
-//   gated norm, 32768 x 32 rows of 128: 477, 285, 246, 255 us;  20000 rows of 4096: 228, 163, 168, 188
-//   residual norm, 20000 rows of 1000 (fp32): 130, 79, 81, 84;  16384 rows of 4096: 229, 237, 257, 250
+// The backward's workgroups, a whole number for each of the 256 compute units,
+// each of which leaves a partial row: as few as keep enough loads in flight.  Of
+// 256, 512, 768 and 1024 took, in us,
+//   gated norm, bf16:     32768 x 32 rows of 128: 477, 285, 246, 255;  30000 of 2048: 275, 159, 127, 122
+//                         20000 of 4096: 228, 163, 168, 188
+//   residual norm, loads  24 KB a row (bf16, 4096): 155, 132, 144, 135;  40 KB: 217, 200, 216, 205
+//                         48 KB (fp32 stream, 4096): 230, 238, 258, 251;  (bf16, 8192): 136, 142, 149, 155
+//                         64 KB: 166, 180, 195, 207;  rows of 1000, fp32: 130, 79, 81, 84
 int ng_blocks(int nv) { return nv > 256 ? 512 : 768; }
-int rn_blocks(int nv) { return nv > 256 ? 256 : 512; }
+int rn_blocks(const ResNormArgs& a) {
+    const int e = a.dtype == 1 ? 2 : 4, er = a.rdtype == 1 ? 2 : 4;
+    return a.width * (2 * er + e + (a.want_dcs ? e : 0)) >= 48 * 1024 ? 256 : 512;
+}
 
 #define KDA_ROW_CASES(RUN, V)                                                                                  \
     switch (s.g * 16 + s.vpt) {                                                                                \
@@ -465,16 +475,13 @@ hipError_t launch_norm_gate(const NormGateArgs& a, bool backward, hipStream_t st
     return hipGetLastError();
 }
 
-int res_norm_blocks(int dtype, int width, int64_t rows) {
-    const int nv = vecs_of(dtype, width);
-    return blocks_for(nv, rows, rn_blocks(nv));
-}
+int res_norm_blocks(const ResNormArgs& a) { return blocks_for(vecs_of(a.dtype, a.width), a.rows, rn_blocks(a)); }
 
 hipError_t launch_res_norm(const ResNormArgs& a, bool backward, hipStream_t st) {
     const int v = vec_of(a.dtype, a.width);
     const int nv = vecs_of(a.dtype, a.width);
     const RowShape s = row_shape(nv);
-    const int blocks = blocks_for(nv, a.rows, backward ? rn_blocks(nv) : FWD_BLOCKS);
+    const int blocks = backward ? res_norm_blocks(a) : blocks_for(nv, a.rows, FWD_BLOCKS);
     if (v == 1) {
         if (a.dtype == 1 && a.rdtype == 1) res_norm_launch<bf16, bf16, 1>(a, backward, blocks, s, st);
         else if (a.dtype == 1) res_norm_launch<bf16, float, 1>(a, backward, blocks, s, st);
