@@ -66,7 +66,7 @@ struct ConvArgs {
 };
 hipError_t launch_conv_fwd(const ConvArgs& a, hipStream_t st);
 hipError_t launch_conv_bwd(const ConvArgs& a, hipStream_t st);
-int conv_bwd_parts(int dtype, int T, int N, int C, int W);  // partial rows of the backward
+int conv_bwd_parts(int T, int N, int C);  // partial rows of the backward
 hipError_t launch_conv_step(const ConvArgs& a, hipStream_t st);
 
 struct LinScanArgs {

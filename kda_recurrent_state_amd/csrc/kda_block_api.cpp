@@ -138,7 +138,7 @@ int plan_conv(const kda_conv_dims_t* d, kda::ConvArgs* a) {
 }
 
 size_t conv_bwd_workspace(const kda::ConvArgs& a) {
-    return round256((size_t)kda::conv_bwd_parts(a.dtype, a.T, a.N, a.C, a.W) * a.C * (a.W + 1) * 4);
+    return round256((size_t)kda::conv_bwd_parts(a.T, a.N, a.C) * a.C * (a.W + 1) * 4);
 }
 
 // ---------------------------------------------------------------- norms
@@ -359,7 +359,7 @@ int kda_conv_bwd(const kda_conv_dims_t* d, const void* x, const float* weight, c
     a.part = static_cast<float*>(workspace);
     if (a.N > 0) KDA_TRY(hip_status(kda::launch_conv_bwd(a, (hipStream_t)stream), "convolution gradient"));
     if (!dweight && !dbias) return ok();
-    return hip_status(kda::launch_colsum(a.part, kda::conv_bwd_parts(a.dtype, a.T, a.N, a.C, a.W), (int64_t)a.C * (a.W + 1),
+    return hip_status(kda::launch_colsum(a.part, kda::conv_bwd_parts(a.T, a.N, a.C), (int64_t)a.C * (a.W + 1),
                                          (int64_t)a.C * a.W, dweight, dbias, (hipStream_t)stream),
                       "convolution gradient");
 }

@@ -8,7 +8,8 @@
 //   dx_s = sum_{k < W} w[W-1-k] dz_{s+k},   dw[W-1-k] = sum_s x_s dz_{s+k},   db = sum_t dz_t,
 // plus the derivative of the outgoing state for the rows that form it.
 //
-// HBM-bound: a thread owns V adjacent channels of a strip of consecutive tokens
+// HBM-bound (forward 65501 x 4096 bf16: 5.6 TB/s; the backward, 4.7 TB/s, issues 29 vector
+// instructions an element as well): a thread owns V adjacent channels of a strip of consecutive tokens
 // and slides the W-token window along it in registers, so every row is read
 // once and the strip's W - 1 leading rows (backward: 2 (W - 1)) once more,
 // from cache.  Groups of tokens are loaded together ahead of their use.
@@ -60,9 +61,11 @@ __device__ __forceinline__ void get_if(bool there, const Pack<T, V>& r, float (&
 template <int V, int W>
 __device__ __forceinline__ void load_weight(const ConvArgs& a, int c, float (&w)[V][W], float (&b)[V]) {
     const float* wp = a.weight + (int64_t)c * W;
-    if constexpr (V == 1) {
+    if constexpr (V * W % 4 != 0) {
 #pragma unroll
-        for (int j = 0; j < W; ++j) w[0][j] = wp[j];
+        for (int i = 0; i < V; ++i)
+#pragma unroll
+            for (int j = 0; j < W; ++j) w[i][j] = wp[i * W + j];
     } else {
         const Pack<float, V * W> wr = load_v<V * W>(wp);
 #pragma unroll
@@ -401,7 +404,7 @@ struct ConvShape { int G, L, cblocks, strips; };
 ConvShape conv_shape(int V, int C) {
     ConvShape s;
     const int ncv = (C + V - 1) / V;
-    s.G = 64;
+    s.G = 64;  // fewer in narrow rows (65536 x 64: 11 us with 8 lanes a row, 20 with 64)
     while (s.G > 8 && s.G / 2 >= ncv) s.G /= 2;
     s.cblocks = (ncv + s.G - 1) / s.G;
     s.L = s.strips = 0;
@@ -412,13 +415,13 @@ void set_strips(ConvShape* s, int T, int64_t L) {
     s->L = (int)L;
     s->strips = (int)((T + spb * L - 1) / (spb * L));
 }
-// Forward: strips of up to 32 tokens, shorter ones where that leaves fewer than
-// 2048 workgroups.
+// Forward: strips of up to 16 tokens (65501 x 4096 bf16: 194 us; 8: 195, 32: 202, 64:
+// 207), shorter ones where that leaves fewer than 2048 workgroups.
 ConvShape fwd_shape(int V, int T, int C) {
     ConvShape s = conv_shape(V, C);
     int L = 8;
     const int64_t spb = BT / s.G;
-    while (L < 32 && (T + spb * L - 1) / (spb * L) * s.cblocks > 2048) L *= 2;
+    while (L < 16 && (T + spb * L - 1) / (spb * L) * s.cblocks > 2048) L *= 2;
     set_strips(&s, T, L);
     return s;
 }
@@ -438,12 +441,12 @@ ConvShape bwd_shape(int V, int T, int C) {
 }
 
 int state_blocks(int N) { return N < 32 ? N : 32; }
-// Channels per lane.  Forward: 16 bytes.  Backward: 4, but 2 for bf16 with four
-// taps, whose windows and sums leave too few wavefronts otherwise (32768 x 4096:
-// 190 us against 200; with two taps 30000 x 1536: 98 against 88, and float32 with
-// four 20011 x 2000: 142 against 132).  Single channels in rows shorter than that.
+// Channels per lane.  Forward: 16 bytes (65501 x 4096 bf16: 194 us; four channels 199).
+// Backward: 2, whose windows and sums leave more wavefronts than 4 (30000 x 1536 with
+// three taps: 73 us against 80; 3000 x 1024 with four: 19 against 24; 32768 x 4096: 178
+// against 176; fp32, 20011 x 2000: 116 against 118).  Single channels in rows shorter than that.
 int fwd_vec(int dtype, int C) { return dtype == 1 ? (C >= 8 ? 8 : 1) : (C >= 4 ? 4 : 1); }
-constexpr int bwd_vec(int dtype, int C, int W) { return C < 4 ? 1 : dtype == 1 && W == 4 ? 2 : 4; }
+int bwd_vec(int C) { return C >= 2 ? 2 : 1; }
 
 // f(taps, SiLU or not) for the call's.
 template <typename F> void by_taps(const ConvArgs& a, F f) {
@@ -491,16 +494,13 @@ template <typename T, int V> hipError_t bwd_launch(const ConvArgs& a, hipStream_
     by_taps(a, [&](auto w, auto silu) {
         constexpr int W = decltype(w)::value;
         constexpr bool SILU = decltype(silu)::value;
-        if constexpr (V == 1 || V == bwd_vec(sizeof(T) == 2, 4, W)) {  // the widths that bwd_vec gives this V
-            if constexpr (V > 1)
-                if (s.G == WAVE) {
-                    hipLaunchKernelGGL((conv_bwd_kernel<T, V, W, SILU, true>), grid, dim3(BT), 0, st, a, s.G, s.L,
-                                       s.cblocks, extra);
-                    return;
-                }
-            hipLaunchKernelGGL((conv_bwd_kernel<T, V, W, SILU, false>), grid, dim3(BT), 0, st, a, s.G, s.L, s.cblocks,
-                               extra);
-        }
+        if constexpr (V > 1)
+            if (s.G == WAVE) {
+                hipLaunchKernelGGL((conv_bwd_kernel<T, V, W, SILU, true>), grid, dim3(BT), 0, st, a, s.G, s.L, s.cblocks,
+                                   extra);
+                return;
+            }
+        hipLaunchKernelGGL((conv_bwd_kernel<T, V, W, SILU, false>), grid, dim3(BT), 0, st, a, s.G, s.L, s.cblocks, extra);
     });
     return hipGetLastError();
 }
@@ -522,15 +522,12 @@ hipError_t launch_conv_fwd(const ConvArgs& a, hipStream_t st) {
     return v == 1 ? fwd_launch<float, 1>(a, st) : fwd_launch<float, 4>(a, st);
 }
 
-int conv_bwd_parts(int dtype, int T, int N, int C, int W) {
-    return bwd_shape(bwd_vec(dtype, C, W), T, C).strips + state_blocks(N);
-}
+int conv_bwd_parts(int T, int N, int C) { return bwd_shape(bwd_vec(C), T, C).strips + state_blocks(N); }
 
 hipError_t launch_conv_bwd(const ConvArgs& a, hipStream_t st) {
-    const int v = bwd_vec(a.dtype, a.C, a.W);
-    if (a.dtype == 1)
-        return v == 1 ? bwd_launch<bf16, 1>(a, st) : v == 2 ? bwd_launch<bf16, 2>(a, st) : bwd_launch<bf16, 4>(a, st);
-    return v == 1 ? bwd_launch<float, 1>(a, st) : bwd_launch<float, 4>(a, st);
+    const int v = bwd_vec(a.C);
+    if (a.dtype == 1) return v == 1 ? bwd_launch<bf16, 1>(a, st) : bwd_launch<bf16, 2>(a, st);
+    return v == 1 ? bwd_launch<float, 1>(a, st) : bwd_launch<float, 2>(a, st);
 }
 
 hipError_t launch_conv_step(const ConvArgs& a, hipStream_t st) {
