@@ -102,14 +102,17 @@ def _tokens(t, name, dtype, shape):
         raise ValueError(f"{name} must have shape {tuple(shape)} (got {tuple(t.shape)})")
     if t.is_contiguous():
         return 0
+    stride = t.stride()
+    if len(stride) == 2 and stride[1] == 1 and stride[0] >= shape[1]:  # the usual slice
+        return stride[0] if shape[0] > 1 else 0
     inner = 1
-    for size, stride in zip(reversed(shape[1:]), reversed(t.stride()[1:])):
-        if size > 1 and stride != inner:
-            raise ValueError(f"{name} must be contiguous within a token (strides {t.stride()})")
+    for size, step in zip(reversed(shape[1:]), reversed(stride[1:])):
+        if size > 1 and step != inner:
+            raise ValueError(f"{name} must be contiguous within a token (strides {stride})")
         inner *= size
-    if shape[0] > 1 and t.stride(0) < inner:
-        raise ValueError(f"{name}'s tokens must not overlap (strides {t.stride()})")
-    return t.stride(0) if shape[0] > 1 else 0
+    if shape[0] > 1 and stride[0] < inner:
+        raise ValueError(f"{name}'s tokens must not overlap (strides {stride})")
+    return stride[0] if shape[0] > 1 else 0
 
 
 def _full(t, name, dtype, shape):
@@ -170,7 +173,7 @@ def _same_device(ref, **tensors):
 def _extent(t):
     lo = t.data_ptr()
     if t.is_contiguous():
-        return lo, lo + t.numel() * t.element_size()
+        return lo, lo + t.nbytes
     return lo, lo + (1 + sum((n - 1) * d for n, d in zip(t.shape, t.stride()))) * t.element_size()
 
 
@@ -238,12 +241,12 @@ def _size(name, dims, *more):
 # ------------------------------------------------------------------ diagonal recurrence
 
 def _scan_dims(x, log_a, N, dy=None):
-    T, C = _rank(x, "x", 2)
+    shape = x.shape
     code = _code(x)
-    xs = _tokens(x, "x", x.dtype, (T, C))
-    ls = _tokens(log_a, "log_a", torch.float32, (T, C))
-    ds = 0 if dy is None else _tokens(dy, "dy", x.dtype, (T, C))
-    return _dims(_ScanDims, N, C, T, code, 0, xs, ls, ds)
+    xs = 0 if x.is_contiguous() else _tokens(x, "x", x.dtype, shape)
+    ls = _tokens(log_a, "log_a", torch.float32, shape)
+    ds = 0 if dy is None else _tokens(dy, "dy", x.dtype, shape)
+    return _dims(_ScanDims, N, shape[1], shape[0], code, 0, xs, ls, ds)
 
 
 def _scan(x, log_a, h0, cu_seqlens, num_seqs, out, final_state, states, workspace):
@@ -350,15 +353,14 @@ def scan_step(x, log_a, h, *, out=None, h_out=None):
 # ------------------------------------------------------------------ short convolution
 
 def _conv_dims(x, weight, bias, N, activation, dy=None):
-    T, C = _rank(x, "x", 2)
+    T, C = x.shape
     code = _code(x)
-    _rank(weight, "weight", 2)
-    W = weight.shape[1]
+    W = _rank(weight, "weight", 2)[1]
     _full(weight, "weight", torch.float32, (C, W))
     _full(bias, "bias", torch.float32, (C,))
     if activation not in (None, "silu"):
         raise ValueError(f"activation must be None or 'silu' (got {activation!r})")
-    xs = _tokens(x, "x", x.dtype, (T, C))
+    xs = 0 if x.is_contiguous() else _tokens(x, "x", x.dtype, (T, C))
     ds = 0 if dy is None else _tokens(dy, "dy", x.dtype, (T, C))
     return *_dims(_ConvDims, N, C, T, code, W, _ACT[activation], 0, xs, ds), W
 
@@ -452,7 +454,7 @@ def _norm_gate_dims(x, weight, gate, activation, eps, dy=None):
     if activation not in ("silu", "sigmoid"):
         raise ValueError(f"activation must be 'silu' or 'sigmoid' (got {activation!r})")
     _full(weight, "weight", torch.float32, (D,))
-    xs = _tokens(x, "x", x.dtype, shape)
+    xs = 0 if x.is_contiguous() else _tokens(x, "x", x.dtype, shape)
     gs = 0 if gate is None else _tokens(gate, "gate", x.dtype, shape)
     ds = 0 if dy is None else _tokens(dy, "dy", x.dtype, shape)
     return _dims(_NormGateDims, T, H, D, _code(x), _ACT[activation], float(eps), 0, xs, gs, ds)
