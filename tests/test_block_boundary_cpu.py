@@ -162,6 +162,16 @@ def test_refusals(lib, fn, change, given, expect):
     assert st == expect, (st, lib.kda_last_error())
 
 
+@pytest.mark.parametrize("fn", ["kda_scan_fwd", "kda_scan_bwd"])
+def test_scan_larger_than_a_launch_is_refused(lib, fn):
+    """ceil(T / 128) ceil(C / 64) workgroups of 512 threads, fewer than 2^32 - 64 * 512 threads in all."""
+    first = (0xFFFFFFFF // 512 - 64) * 128 + 1
+    for dims in (dict(total_tokens=first, channels=1), dict(total_tokens=first, channels=64),
+                 dict(total_tokens=0x7FFF0000, channels=1), dict(total_tokens=first // 64, channels=64 * 65)):
+        assert call(lib, fn, scan_dims(num_seqs=1, **dims)) == INVALID
+        assert "too large" in lib.kda_last_error().decode()
+
+
 def test_workspace_sizes(lib):
     n = ctypes.c_size_t(0)
     for T in (1, 64, 128, 129, 1000):
