@@ -8,7 +8,7 @@
 //   dx_s = sum_{k < W} w[W-1-k] dz_{s+k},   dw[W-1-k] = sum_s x_s dz_{s+k},   db = sum_t dz_t,
 // plus the derivative of the outgoing state for the rows that form it.
 //
-// HBM-bound (forward 65501 x 4096 bf16: 5.6 TB/s; the backward, 4.7 TB/s, issues 29 vector
+// HBM-bound (forward 65501 x 4096 bf16: 6.0 TB/s; the backward, 5.0 TB/s, issues 29 vector
 // instructions an element as well): a thread owns V adjacent channels of a strip of consecutive tokens
 // and slides the W-token window along it in registers, so every row is read
 // once and the strip's W - 1 leading rows (backward: 2 (W - 1)) once more,
@@ -91,7 +91,7 @@ __device__ __forceinline__ void next_seq(const Seqs& sq, int u, int& n, int& beg
     if (end <= u) end = u + 1;  // and one token at a time
 }
 
-template <typename T, int V, int W, bool SILU, bool UNI>
+template <typename T, int V, int W, bool SILU, bool UNI, bool PAST>
 __global__ __launch_bounds__(BT) void conv_fwd_kernel(ConvArgs a, int G, int L, int cblocks, int state_blocks) {
     const Seqs sq{a.cu, a.N, a.T, a.eq};
     const int cl = threadIdx.x % G, spb = BT / G;
@@ -152,7 +152,7 @@ __global__ __launch_bounds__(BT) void conv_fwd_kernel(ConvArgs a, int G, int L, 
         store_nt<V>((T*)a.y + (int64_t)u * a.C + tp.c, z);
     };
 
-    auto row = [&](int u) { return load_v<V>(tp.x + (int64_t)(u < a.T ? u : a.T - 1) * a.xs + tp.c); };
+    auto row = [&](int u) { return load_c<PAST, V>(tp.x + (int64_t)(u < a.T ? u : a.T - 1) * a.xs + tp.c); };
     while (t < stop) {
         if (t + GRP <= stop && t + GRP <= end) {
             Pack<T, V> xv[GRP];
@@ -188,7 +188,7 @@ template <bool SILU> __device__ __forceinline__ float dz_of(float dy, float z) {
 // The first state_blocks rows of workgroups form the rows of dstate, the others
 // walk strips of tokens.  Both add the products x_s dz_{s+k} of the rows they own to their
 // workgroup's partial dweight.
-template <typename T, int V, int W, bool SILU, bool UNI>
+template <typename T, int V, int W, bool SILU, bool UNI, bool PAST>
 __global__ __launch_bounds__(BT) void conv_bwd_kernel(ConvArgs a, int G, int L, int cblocks, int state_blocks) {
     __shared__ float lds[BT * V];
     const Seqs sq{a.cu, a.N, a.T, a.eq};
@@ -277,7 +277,8 @@ __global__ __launch_bounds__(BT) void conv_bwd_kernel(ConvArgs a, int G, int L, 
                 if (!have) {
                     Pack<T, V> r[2 * (W - 1)], d[W - 1];  // x rows from t - W + 1, dy rows from t
 #pragma unroll
-                    for (int k = 0; k < 2 * (W - 1); ++k) r[k] = load_v<V>(tp.x + (int64_t)(t - (W - 1) + k) * a.xs + tp.c);
+                    for (int k = 0; k < 2 * (W - 1); ++k)
+                        r[k] = load_v<V>(tp.x + (int64_t)(t - (W - 1) + k) * a.xs + tp.c);
 #pragma unroll
                     for (int k = 0; k < W - 1; ++k) d[k] = load_v<V>(dyp + (int64_t)(t + k) * a.ds + tp.c);
 #pragma unroll
@@ -296,8 +297,8 @@ __global__ __launch_bounds__(BT) void conv_bwd_kernel(ConvArgs a, int G, int L, 
                 Pack<T, V> xv[GRB], dv[GRB];
 #pragma unroll
                 for (int i = 0; i < GRB; ++i) {
-                    xv[i] = load_v<V>(tp.x + (int64_t)(t + W - 1 + i) * a.xs + tp.c);
-                    dv[i] = load_v<V>(dyp + (int64_t)(t + W - 1 + i) * a.ds + tp.c);
+                    xv[i] = load_c<PAST, V>(tp.x + (int64_t)(t + W - 1 + i) * a.xs + tp.c);
+                    dv[i] = load_c<PAST, V>(dyp + (int64_t)(t + W - 1 + i) * a.ds + tp.c);
                 }
 #pragma unroll
                 for (int g = 0; g < GRB; ++g) {  // token t + g; the newest row is t + g + W - 1
@@ -415,8 +416,8 @@ void set_strips(ConvShape* s, int T, int64_t L) {
     s->L = (int)L;
     s->strips = (int)((T + spb * L - 1) / (spb * L));
 }
-// Forward: strips of up to 16 tokens (65501 x 4096 bf16: 194 us; 8: 195, 32: 202, 64:
-// 207), shorter ones where that leaves fewer than 2048 workgroups.
+// Forward: strips of up to 16 tokens (65501 x 4096 bf16: 185 us; 8: 194, 32: 189, 64:
+// 199), shorter ones where that leaves fewer than 2048 workgroups.
 ConvShape fwd_shape(int V, int T, int C) {
     ConvShape s = conv_shape(V, C);
     int L = 8;
@@ -441,10 +442,10 @@ ConvShape bwd_shape(int V, int T, int C) {
 }
 
 int state_blocks(int N) { return N < 32 ? N : 32; }
-// Channels per lane.  Forward: 16 bytes (65501 x 4096 bf16: 194 us; four channels 199).
+// Channels per lane.  Forward: 16 bytes (65501 x 4096 bf16: 185 us; four channels 192).
 // Backward: 2, whose windows and sums leave more wavefronts than 4 (30000 x 1536 with
-// three taps: 73 us against 80; 3000 x 1024 with four: 19 against 24; 32768 x 4096: 178
-// against 176; fp32, 20011 x 2000: 116 against 118).  Single channels in rows shorter than that.
+// three taps: 72 us against 78; 3000 x 1024 with four: 20 against 24; 32768 x 4096: 170
+// against 169; fp32, 20011 x 2000: 118 against 115).  Single channels in rows shorter than that.
 int fwd_vec(int dtype, int C) { return dtype == 1 ? (C >= 8 ? 8 : 1) : (C >= 4 ? 4 : 1); }
 int bwd_vec(int C) { return C >= 2 ? 2 : 1; }
 
@@ -466,42 +467,34 @@ bool grid_of(const ConvShape& s, int extra, dim3* grid) {
     return blocks <= 0xffffffffll / BT;
 }
 
+#define KDA_CONV_LAUNCH(KERNEL, ...) \
+    hipLaunchKernelGGL((KERNEL<T, V, W, SILU, __VA_ARGS__>), grid, dim3(BT), 0, st, a, s.G, s.L, s.cblocks, extra)
+#define KDA_CONV_CASES(KERNEL, PAST)                                           \
+    by_taps(a, [&](auto w, auto silu) {                                        \
+        constexpr int W = decltype(w)::value;                                  \
+        constexpr bool SILU = decltype(silu)::value, WIDE = V > 1;             \
+        if (!WIDE || s.G < WAVE) KDA_CONV_LAUNCH(KERNEL, false, false);        \
+        else if (PAST) KDA_CONV_LAUNCH(KERNEL, WIDE, WIDE);                    \
+        else KDA_CONV_LAUNCH(KERNEL, WIDE, false);                             \
+    })
 template <typename T, int V> hipError_t fwd_launch(const ConvArgs& a, hipStream_t st) {
     const ConvShape s = fwd_shape(V, a.T, a.C);
     const int extra = a.state_T ? state_blocks(a.N) : 0;
+    const int64_t size = (int64_t)a.T * a.C * sizeof(T);
     dim3 grid;
     if (!grid_of(s, extra, &grid)) return hipErrorInvalidConfiguration;
     if (grid.x == 0) return hipSuccess;
-    by_taps(a, [&](auto w, auto silu) {
-        constexpr int W = decltype(w)::value;
-        constexpr bool SILU = decltype(silu)::value;
-        if constexpr (V > 1)
-            if (s.G == WAVE) {
-                hipLaunchKernelGGL((conv_fwd_kernel<T, V, W, SILU, true>), grid, dim3(BT), 0, st, a, s.G, s.L, s.cblocks,
-                                   extra);
-                return;
-            }
-        hipLaunchKernelGGL((conv_fwd_kernel<T, V, W, SILU, false>), grid, dim3(BT), 0, st, a, s.G, s.L, s.cblocks, extra);
-    });
+    KDA_CONV_CASES(conv_fwd_kernel, past_cache(size));
     return hipGetLastError();
 }
 
 template <typename T, int V> hipError_t bwd_launch(const ConvArgs& a, hipStream_t st) {
     const ConvShape s = bwd_shape(V, a.T, a.C);
     const int extra = state_blocks(a.N);
+    const int64_t size = (int64_t)a.T * a.C * sizeof(T);
     dim3 grid;
     if (!grid_of(s, extra, &grid)) return hipErrorInvalidConfiguration;
-    by_taps(a, [&](auto w, auto silu) {
-        constexpr int W = decltype(w)::value;
-        constexpr bool SILU = decltype(silu)::value;
-        if constexpr (V > 1)
-            if (s.G == WAVE) {
-                hipLaunchKernelGGL((conv_bwd_kernel<T, V, W, SILU, true>), grid, dim3(BT), 0, st, a, s.G, s.L, s.cblocks,
-                                   extra);
-                return;
-            }
-        hipLaunchKernelGGL((conv_bwd_kernel<T, V, W, SILU, false>), grid, dim3(BT), 0, st, a, s.G, s.L, s.cblocks, extra);
-    });
+    KDA_CONV_CASES(conv_bwd_kernel, past_cache(2 * size));
     return hipGetLastError();
 }
 

@@ -7,7 +7,7 @@
 //   gradient at h, with d = dy w:
 //     dh = dres + r (d - n mean(d n)),  dx = c dh,  dw = sum dy n,  dcs = scale sum dh x
 //
-// All are one pass over HBM, which bounds them (5.2 to 5.9 TB/s on large inputs): each
+// All are one pass over HBM, which bounds them (5.4 to 6.0 TB/s on large inputs): each
 // row is read once into registers, its sums are formed over the G lanes (or the
 // whole workgroup) that hold it, and the outputs leave from the same registers.  mean(d n) = r mean(d x), so both of
 // the backward's sums are formed before r is known and share one reduction.
@@ -99,7 +99,7 @@ template <int GATE> __device__ __forceinline__ float gate_slope(float g, float s
     return GATE == GATE_SILU ? s * (1.f + g * (1.f - s)) : s * (1.f - s);
 }
 
-template <typename T, int V, int G, int VPT, int GATE>
+template <typename T, int V, int G, int VPT, int GATE, bool PAST>
 __global__ __launch_bounds__(threads_of(G)) void norm_gate_fwd_kernel(NormGateArgs a) {
     constexpr int BT = threads_of(G), RPB = BT / G;
     __shared__ float lds[BT / WAVE];
@@ -114,10 +114,10 @@ __global__ __launch_bounds__(threads_of(G)) void norm_gate_fwd_kernel(NormGateAr
         Pack<T, V> xr[VPT], gr[VPT];
         Pack<float, V> wr[VPT];
 #pragma unroll
-        for (int j = 0; j < VPT; ++j) xr[j] = load_v<V>(xp + Cols<V, G>(j, g, D).c);
+        for (int j = 0; j < VPT; ++j) xr[j] = load_c<PAST, V>(xp + Cols<V, G>(j, g, D).c);
         if (GATE)
 #pragma unroll
-            for (int j = 0; j < VPT; ++j) gr[j] = load_v<V>(gp + Cols<V, G>(j, g, D).c);
+            for (int j = 0; j < VPT; ++j) gr[j] = load_c<PAST, V>(gp + Cols<V, G>(j, g, D).c);
         if (a.weight)
 #pragma unroll
             for (int j = 0; j < VPT; ++j) wr[j] = load_v<V>(a.weight + Cols<V, G>(j, g, D).c);
@@ -142,12 +142,12 @@ __global__ __launch_bounds__(threads_of(G)) void norm_gate_fwd_kernel(NormGateAr
             if (GATE)
 #pragma unroll
                 for (int i = 0; i < V; ++i) y[i] *= gate_act<GATE>(gr[j][i], sigmoid_f(gr[j][i]));
-            if (cl.live) store_v<V>((T*)a.y + r * D + cl.c, y);
+            if (cl.live) store_c<PAST, V>((T*)a.y + r * D + cl.c, y);
         }
     }
 }
 
-template <typename T, int V, int G, int VPT, int GATE>
+template <typename T, int V, int G, int VPT, int GATE, bool PAST>
 __global__ __launch_bounds__(threads_of(G)) void norm_gate_bwd_kernel(NormGateArgs a) {
     constexpr int BT = threads_of(G), RPB = BT / G;
     __shared__ float lds[RPB > 1 ? RPB * G * VPT * V : 2 * BT / WAVE];
@@ -170,12 +170,12 @@ __global__ __launch_bounds__(threads_of(G)) void norm_gate_bwd_kernel(NormGateAr
 #pragma unroll
         for (int j = 0; j < VPT; ++j) {
             const int c = Cols<V, G>(j, g, D).c;
-            xr[j] = load_v<V>(xp + c);
-            dr[j] = load_v<V>(dp + c);
+            xr[j] = load_c<PAST, V>(xp + c);
+            dr[j] = load_c<PAST, V>(dp + c);
         }
         if (GATE)
 #pragma unroll
-            for (int j = 0; j < VPT; ++j) gr[j] = load_v<V>(gp + Cols<V, G>(j, g, D).c);
+            for (int j = 0; j < VPT; ++j) gr[j] = load_c<PAST, V>(gp + Cols<V, G>(j, g, D).c);
         float sg[VPT][V], sm[2] = {0.f, 0.f};  // sg: the gate's logistic value
 #pragma unroll
         for (int j = 0; j < VPT; ++j) {
@@ -204,15 +204,15 @@ __global__ __launch_bounds__(threads_of(G)) void norm_gate_bwd_kernel(NormGateAr
                 dw[j][i] += dy * act * n;
             }
             if (cl.live) {
-                store_v<V>((T*)a.y + r * D + cl.c, dx);
-                if (GATE) store_v<V>((T*)a.dgate + r * D + cl.c, dg);
+                store_c<PAST, V>((T*)a.y + r * D + cl.c, dx);
+                if (GATE) store_c<PAST, V>((T*)a.dgate + r * D + cl.c, dg);
             }
         }
     }
     if (a.part) block_partial<G, VPT, V>(dw, lds, a.part + (int64_t)blockIdx.x * D, D);
 }
 
-template <typename T, typename R, int V, int G, int VPT>
+template <typename T, typename R, int V, int G, int VPT, bool PAST>
 __global__ __launch_bounds__(threads_of(G)) void res_norm_fwd_kernel(ResNormArgs a) {
     constexpr int BT = threads_of(G), RPB = BT / G;
     __shared__ float lds[BT / WAVE];
@@ -225,10 +225,11 @@ __global__ __launch_bounds__(threads_of(G)) void res_norm_fwd_kernel(ResNormArgs
 #pragma unroll
         for (int j = 0; j < VPT; ++j) {
             const int c = Cols<V, G>(j, g, D).c;
-            rr[j] = load_v<V>((const R*)a.res + r * a.rs + c);
-            xr[j] = load_v<V>((const T*)a.x + r * a.xs + c);
-            wr[j] = load_v<V>(a.weight + c);
+            rr[j] = load_c<PAST, V>((const R*)a.res + r * a.rs + c);
+            xr[j] = load_c<PAST, V>((const T*)a.x + r * a.xs + c);
         }
+#pragma unroll
+        for (int j = 0; j < VPT; ++j) wr[j] = load_v<V>(a.weight + Cols<V, G>(j, g, D).c);
         if (a.cscale)
 #pragma unroll
             for (int j = 0; j < VPT; ++j) cr[j] = load_v<V>(a.cscale + Cols<V, G>(j, g, D).c);
@@ -251,14 +252,14 @@ __global__ __launch_bounds__(threads_of(G)) void res_norm_fwd_kernel(ResNormArgs
 #pragma unroll
             for (int i = 0; i < V; ++i) y[i] = h[j][i] * rn * wr[j][i];
             if (cl.live) {
-                store_v<V>((R*)a.res_out + r * D + cl.c, h[j]);
-                store_v<V>((T*)a.y + r * D + cl.c, y);
+                store_c<PAST, V>((R*)a.res_out + r * D + cl.c, h[j]);
+                store_c<PAST, V>((T*)a.y + r * D + cl.c, y);
             }
         }
     }
 }
 
-template <typename T, typename R, int V, int G, int VPT>
+template <typename T, typename R, int V, int G, int VPT, bool PAST>
 __global__ __launch_bounds__(threads_of(G)) void res_norm_bwd_kernel(ResNormArgs a) {
     constexpr int BT = threads_of(G), RPB = BT / G;
     __shared__ float lds[RPB > 1 ? RPB * G * VPT * V : 2 * BT / WAVE];
@@ -279,15 +280,15 @@ __global__ __launch_bounds__(threads_of(G)) void res_norm_bwd_kernel(ResNormArgs
 #pragma unroll
         for (int j = 0; j < VPT; ++j) {
             const int c = Cols<V, G>(j, g, D).c;
-            hr[j] = load_v<V>((const R*)a.res + r * a.rs + c);
-            dr[j] = load_v<V>((const T*)a.dy + r * a.ds + c);
+            hr[j] = load_c<PAST, V>((const R*)a.res + r * a.rs + c);
+            dr[j] = load_c<PAST, V>((const T*)a.dy + r * a.ds + c);
         }
         if (a.dres)
 #pragma unroll
-            for (int j = 0; j < VPT; ++j) rr[j] = load_v<V>((const R*)a.dres + r * a.drs + Cols<V, G>(j, g, D).c);
+            for (int j = 0; j < VPT; ++j) rr[j] = load_c<PAST, V>((const R*)a.dres + r * a.drs + Cols<V, G>(j, g, D).c);
         if (a.want_dcs)
 #pragma unroll
-            for (int j = 0; j < VPT; ++j) xr[j] = load_v<V>((const T*)a.x + r * a.xs + Cols<V, G>(j, g, D).c);
+            for (int j = 0; j < VPT; ++j) xr[j] = load_c<PAST, V>((const T*)a.x + r * a.xs + Cols<V, G>(j, g, D).c);
         float sm[2] = {0.f, 0.f};
 #pragma unroll
         for (int j = 0; j < VPT; ++j) {
@@ -314,8 +315,8 @@ __global__ __launch_bounds__(threads_of(G)) void res_norm_bwd_kernel(ResNormArgs
                 if (a.want_dcs) dcs[j][i] += a.scale * dh[i] * xr[j][i];
             }
             if (cl.live) {
-                store_v<V>((R*)a.res_out + r * D + cl.c, dh);
-                store_v<V>((T*)a.y + r * D + cl.c, dx);
+                store_c<PAST, V>((R*)a.res_out + r * D + cl.c, dh);
+                store_c<PAST, V>((T*)a.y + r * D + cl.c, dx);
             }
         }
     }
@@ -360,7 +361,7 @@ __global__ __launch_bounds__(CSW* CSR) void colsum_kernel(const float* part, int
 }
 
 // Lanes and vectors per lane of a row of nv vectors: a wavefront or part of it up to
-// two vectors a lane, longer rows a workgroup.  Measured, bf16, 64e6 values, forward and
+// two vectors a lane, longer rows a workgroup.  Measured (through the caches), bf16, 64e6 values, forward and
 // gradient in us: rows of 1024 as here 92 and 128, over 256 lanes 92 and 223; 2048
 // here 93 and 132, a wavefront with four a lane 92 and 132; 4096 here 94, over 512
 // lanes 92; 8192 here 97 and 137, 256 lanes with four 95 and 149.
@@ -400,11 +401,11 @@ constexpr int FWD_BLOCKS = 1 << 20;  // one row group each up to here
 // The backward's workgroups, a whole number for each of the 256 compute units,
 // each of which leaves a partial row: as few as keep enough loads in flight.  Of
 // 256, 512, 768 and 1024 took, in us,
-//   gated norm, bf16:     32768 x 32 rows of 128: 477, 285, 246, 255;  30000 of 2048: 275, 159, 127, 122
-//                         20000 of 4096: 228, 163, 168, 188
-//   residual norm, loads  24 KB a row (bf16, 4096): 155, 132, 144, 135;  40 KB: 217, 200, 216, 205
-//                         48 KB (fp32 stream, 4096): 230, 238, 258, 251;  (bf16, 8192): 136, 142, 149, 155
-//                         64 KB: 166, 180, 195, 207;  rows of 1000, fp32: 130, 79, 81, 84
+//   gated norm, bf16:     32768 x 32 rows of 128: 463, 280, 237, 241;  30000 of 2048: 268, 155, 123, 118
+//                         20000 of 4096: 233, 158, 155, 178;  8192 of 8192: 142, 148, 153, 159
+//   residual norm, loads  24 KB a row (bf16, 16384 of 4096): 152, 121, 136, 125;  40 KB: 210, 189, 205, 195
+//                         48 KB (fp32 stream, 16384 of 4096): 229, 225, 249, 241;  (bf16, 8192 of 8192): 137,
+//                         142, 149, 156;  64 KB: 165, 178, 193, 205;  fp32, 20000 rows of 1000: 125, 75, 77, 82
 int ng_blocks(int nv) { return nv > 256 ? 512 : 768; }
 int rn_blocks(const ResNormArgs& a) {
     const int e = a.dtype == 1 ? 2 : 4, er = a.rdtype == 1 ? 2 : 4;
@@ -429,24 +430,36 @@ int rn_blocks(const ResNormArgs& a) {
         default: if constexpr (V == 4) { RUN(V, 512, 4); }                                                     \
     }
 
-template <typename T, int V>
+#define KDA_LAUNCH(KERNEL, G, ...) \
+    hipLaunchKernelGGL((KERNEL<__VA_ARGS__>), dim3(blocks), dim3(threads_of(G)), 0, st, a)
+template <typename T, int V, bool PAST>
 void norm_gate_launch(const NormGateArgs& a, bool backward, int blocks, RowShape s, hipStream_t st) {
-#define RUN_NG1(V_, G, VPT, GATE)                                                                                    \
-    if (backward) hipLaunchKernelGGL((norm_gate_bwd_kernel<T, V_, G, VPT, GATE>), dim3(blocks), dim3(threads_of(G)), 0, st, a); \
-    else hipLaunchKernelGGL((norm_gate_fwd_kernel<T, V_, G, VPT, GATE>), dim3(blocks), dim3(threads_of(G)), 0, st, a)
+#define RUN_NG1(V_, G, VPT, GATE)                                                   \
+    if (backward) KDA_LAUNCH(norm_gate_bwd_kernel, G, T, V_, G, VPT, GATE, PAST);   \
+    else KDA_LAUNCH(norm_gate_fwd_kernel, G, T, V_, G, VPT, GATE, PAST)
 #define RUN_NG(V_, G, VPT)                               \
     if (!a.gate) { RUN_NG1(V_, G, VPT, GATE_NONE); }     \
     else if (a.silu) { RUN_NG1(V_, G, VPT, GATE_SILU); } \
     else { RUN_NG1(V_, G, VPT, GATE_SIGMOID); }
     KDA_ROW_CASES(RUN_NG, V)
 }
+template <typename T, int V>
+void norm_gate_launch(const NormGateArgs& a, bool backward, int blocks, RowShape s, bool past, hipStream_t st) {
+    if (V > 1 && past) norm_gate_launch<T, V, (V > 1)>(a, backward, blocks, s, st);
+    else norm_gate_launch<T, V, false>(a, backward, blocks, s, st);
+}
 
-template <typename T, typename R, int V>
+template <typename T, typename R, int V, bool PAST>
 void res_norm_launch(const ResNormArgs& a, bool backward, int blocks, RowShape s, hipStream_t st) {
-#define RUN_RN(V_, G, VPT)                                                                                       \
-    if (backward) hipLaunchKernelGGL((res_norm_bwd_kernel<T, R, V_, G, VPT>), dim3(blocks), dim3(threads_of(G)), 0, st, a); \
-    else hipLaunchKernelGGL((res_norm_fwd_kernel<T, R, V_, G, VPT>), dim3(blocks), dim3(threads_of(G)), 0, st, a)
+#define RUN_RN(V_, G, VPT)                                                      \
+    if (backward) KDA_LAUNCH(res_norm_bwd_kernel, G, T, R, V_, G, VPT, PAST);   \
+    else KDA_LAUNCH(res_norm_fwd_kernel, G, T, R, V_, G, VPT, PAST)
     KDA_ROW_CASES(RUN_RN, V)
+}
+template <typename T, typename R, int V>
+void res_norm_launch(const ResNormArgs& a, bool backward, int blocks, RowShape s, bool past, hipStream_t st) {
+    if (V > 1 && past) res_norm_launch<T, R, V, (V > 1)>(a, backward, blocks, s, st);
+    else res_norm_launch<T, R, V, false>(a, backward, blocks, s, st);
 }
 
 }  // namespace
@@ -468,10 +481,12 @@ hipError_t launch_norm_gate(const NormGateArgs& a, bool backward, hipStream_t st
     const int nv = vecs_of(a.dtype, a.width);
     const RowShape s = row_shape(nv);
     const int blocks = blocks_for(nv, a.rows, backward ? ng_blocks(nv) : FWD_BLOCKS);
-    if (a.dtype == 1 && v == 1) norm_gate_launch<bf16, 1>(a, backward, blocks, s, st);
-    else if (a.dtype == 1) norm_gate_launch<bf16, 8>(a, backward, blocks, s, st);
-    else if (v == 1) norm_gate_launch<float, 1>(a, backward, blocks, s, st);
-    else norm_gate_launch<float, 4>(a, backward, blocks, s, st);
+    const int64_t size = a.rows * a.width * (a.dtype == 1 ? 2 : 4);  // of a tensor
+    const bool past = past_cache(size * (1 + backward + (a.gate != nullptr)));
+    if (a.dtype == 1 && v == 1) norm_gate_launch<bf16, 1>(a, backward, blocks, s, past, st);
+    else if (a.dtype == 1) norm_gate_launch<bf16, 8>(a, backward, blocks, s, past, st);
+    else if (v == 1) norm_gate_launch<float, 1>(a, backward, blocks, s, past, st);
+    else norm_gate_launch<float, 4>(a, backward, blocks, s, past, st);
     return hipGetLastError();
 }
 
@@ -482,14 +497,16 @@ hipError_t launch_res_norm(const ResNormArgs& a, bool backward, hipStream_t st) 
     const int nv = vecs_of(a.dtype, a.width);
     const RowShape s = row_shape(nv);
     const int blocks = backward ? res_norm_blocks(a) : blocks_for(nv, a.rows, FWD_BLOCKS);
+    const int64_t n = a.rows * a.width, size = n * (a.dtype == 1 ? 2 : 4), rsize = n * (a.rdtype == 1 ? 2 : 4);
+    const bool past = past_cache(size + rsize + (backward && a.dres ? rsize : 0) + (backward && a.want_dcs ? size : 0));
     if (v == 1) {
-        if (a.dtype == 1 && a.rdtype == 1) res_norm_launch<bf16, bf16, 1>(a, backward, blocks, s, st);
-        else if (a.dtype == 1) res_norm_launch<bf16, float, 1>(a, backward, blocks, s, st);
-        else res_norm_launch<float, float, 1>(a, backward, blocks, s, st);
+        if (a.dtype == 1 && a.rdtype == 1) res_norm_launch<bf16, bf16, 1>(a, backward, blocks, s, past, st);
+        else if (a.dtype == 1) res_norm_launch<bf16, float, 1>(a, backward, blocks, s, past, st);
+        else res_norm_launch<float, float, 1>(a, backward, blocks, s, past, st);
     } else {
-        if (a.dtype == 1 && a.rdtype == 1) res_norm_launch<bf16, bf16, 8>(a, backward, blocks, s, st);
-        else if (a.dtype == 1) res_norm_launch<bf16, float, 8>(a, backward, blocks, s, st);
-        else res_norm_launch<float, float, 4>(a, backward, blocks, s, st);
+        if (a.dtype == 1 && a.rdtype == 1) res_norm_launch<bf16, bf16, 8>(a, backward, blocks, s, past, st);
+        else if (a.dtype == 1) res_norm_launch<bf16, float, 8>(a, backward, blocks, s, past, st);
+        else res_norm_launch<float, float, 4>(a, backward, blocks, s, past, st);
     }
     return hipGetLastError();
 }

@@ -63,6 +63,26 @@ template <int V, typename T> __device__ __forceinline__ void store_nt(T* p, cons
     }
 }
 
+// Inputs that fill half of the 256 MiB last-level cache or more are read past it, and
+// the call's outputs written past it: they would only push each other out.  Smaller
+// ones may be there from whoever wrote them.  Measured, us through the cache and past
+// it (three sets of inputs and outputs in turn), by the MiB of inputs:
+//   convolution, bf16: 64: 25 and 30, 96: 41 and 41, 128: 55 and 53, 192: 78 and 74, 512:
+//     193 and 185; its gradient, 96: 43 and 45, 128: 57 and 56, 512: 178 and 169
+//   gated norm: fp32, 37: 10.7 and 12.2; bf16, 64: 19.5 and 19.2, 128: 38 and 34, 512: 135
+//     and 126; its gradient, 192: 68 and 63, 768: 248 and 240
+//   residual norm, gradient, bf16, 384: 133 and 118
+inline bool past_cache(int64_t in_bytes) { return in_bytes >= 128ll << 20; }
+// (An access of two halves touches each line twice, which has to stay cached in between.)
+template <bool PAST, int V, typename T> __device__ __forceinline__ Pack<T, V> load_c(const T* p) {
+    if constexpr (PAST && V * sizeof(T) <= 16) return load_nt<V>(p);
+    else return load_v<V>(p);
+}
+template <bool PAST, int V, typename T> __device__ __forceinline__ void store_c(T* p, const float (&v)[V]) {
+    if constexpr (PAST && V * sizeof(T) <= 16) store_nt<V>(p, v);
+    else store_v<V>(p, v);
+}
+
 // First column of the lane whose columns start at c, in a row of C >= V.
 template <int V> __device__ __forceinline__ int column(int c, int C) { return c + V <= C ? c : C - V; }
 

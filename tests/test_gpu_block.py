@@ -777,3 +777,84 @@ def test_a_recurrent_block_prefill_then_steps(dtype):
         assert rel(y.view(N, C), full[:, t].cpu().double()) <= step
     assert torch.equal(cs, cs_full)
     assert rel(hT, hT_full.cpu().double()) <= step
+
+
+def pieces(f, cuts, *tensors):
+    """f of the tensors' rows from each cut to the next, joined."""
+    got = [f(*(t[a:b] for t in tensors)) for a, b in zip(cuts, cuts[1:])]
+    return [torch.cat(col) for col in zip(*got)]
+
+
+def sums_match(got, parts, terms):
+    """Column sums of one call against the sum of several: the same terms, added in float32 by
+    at most 512 additions one after the other (a lane's rows, its workgroup's, the
+    workgroups'), so each sum is off by at most 512 * 2^-24 of its terms' magnitudes."""
+    diff = (got.double() - sum(p.double() for p in parts)).abs()
+    assert (diff <= 2 * 512 * 2.0 ** -24 * terms).all()  # the call's and, of their own terms, the parts'
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+def test_norms_larger_than_the_cache(dtype):
+    """Inputs of more than 128 MiB are read past the last-level cache by kernels of their own,
+    their quarters are not: the rows have to come out the same."""
+    T, D = (30000, 2501) if dtype is BF else (17000, 2051)
+    cuts = [0, T // 4, T // 2, 3 * (T // 4), T]
+    torch.manual_seed(5)
+    x, g, dy = (torch.randn(T, 1, D, device=DEV, dtype=dtype) for _ in range(3))
+    w = torch.rand(D, device=DEV) + 0.5
+    assert 128 << 20 <= 2 * x.nbytes and 3 * x[:cuts[1]].nbytes < 128 << 20
+    y = kda.norm_gate_fwd(x, w, g)
+    (yh,) = pieces(lambda a, b: [kda.norm_gate_fwd(a, w, b)], cuts, x, g)
+    assert torch.equal(y, yh)
+    inplace = x.clone()
+    assert torch.equal(kda.norm_gate_fwd(inplace, w, g, out=inplace), y)
+    G = kda.norm_gate_bwd(x, w, dy, g)
+    dx, dg, dw = pieces(lambda a, b, c: list(kda.norm_gate_bwd(a, w, b, c).values()), cuts, x, dy, g)
+    assert torch.equal(G["dx"], dx) and torch.equal(G["dgate"], dg)
+    n = x.float() * torch.rsqrt(x.float().square().mean(-1, keepdim=True) + 1e-6)
+    terms = (n * dy.float()).abs().double().sum((0, 1)) * 1.01  # a logistic gate is below 1
+    sums_match(G["dweight"], dw.view(4, D), terms)
+    x, res, dy = x[:, 0], g[:, 0], dy[:, 0]
+    y, r = kda.residual_norm_fwd(x, res, w, scale=0.5)
+    (yh, rh) = pieces(lambda a, b: kda.residual_norm_fwd(a, b, w, scale=0.5), cuts, x, res)
+    assert torch.equal(y, yh) and torch.equal(r, rh)
+    G = kda.residual_norm_bwd(None, r, w, dy, scale=0.5)
+    (dx, dr) = pieces(lambda a, b: list(kda.residual_norm_bwd(None, a, w, b, scale=0.5).values())[:2], cuts, r, dy)
+    assert torch.equal(G["dx"], dx) and torch.equal(G["dresidual"], dr)
+
+
+@pytest.mark.parametrize("C", [2501, 2504])
+@pytest.mark.parametrize("dtype", DTYPES)
+def test_conv_larger_than_the_cache(dtype, C):
+    """The same for the convolution: two sequences in one call against each by itself."""
+    T = 30000 if dtype is BF else 15000
+    cut = T // 2 + 1
+    torch.manual_seed(6)
+    x, dy = (torch.randn(T, C, device=DEV, dtype=dtype) for _ in range(2))
+    w, b = torch.randn(C, 4, device=DEV) * 0.5, torch.randn(C, device=DEV)
+    assert 128 << 20 <= x.nbytes and x[:cut].nbytes < 128 << 20
+    cu = torch.tensor([0, cut, T], dtype=torch.int32, device=DEV)
+    y, st = kda.conv_fwd(x, w, b, None, cu)
+    (yh, sh) = pieces(lambda a: kda.conv_fwd(a, w, b), [0, cut, T], x)
+    assert torch.equal(y, yh) and torch.equal(st, sh)
+    G = kda.conv_bwd(x, w, dy, b, None, cu)
+    # against the definition around the sequences' ends and inside them
+    for beg, end in ((0, cut), (cut, T)):
+        for lo in (beg, (beg + end) // 2, end - 24):
+            hi = lo + 24
+            first, last = max(lo - 3, beg), min(hi + 3, end)
+            st = x[first - 3:first] if first > beg else torch.zeros_like(x[:3])
+            f8 = [t.cpu().double() for t in (x[first:last], w, b, st[None])]
+            val, bnd = R.conv_grad(*f8, [0, last - first], True, dy[first:last].cpu().double(), torch.zeros(1, 3, C, dtype=F8))
+            sl = slice(lo - first, hi - first)
+            R.check(G["dx"][lo:hi], val["dx"][sl], bnd["dx"][sl], "dx")
+    # away from the ends (by more than a strip) every row is formed by the same operations
+    for lo, hi in ((0, cut // 2), (cut // 2, cut), (cut, 3 * T // 4), (3 * T // 4, T)):
+        st = x[lo - 3:lo][None].contiguous() if lo not in (0, cut) else None
+        dx = kda.conv_bwd(x[lo:hi], w, dy[lo:hi], b, st)["dx"]
+        assert 2 * dx.nbytes < 128 << 20 and torch.equal(G["dx"][lo + 512:hi - 512], dx[512:-512])
+    parts = [kda.conv_bwd(x[s], w, dy[s], b) for s in (slice(0, cut), slice(cut, T))]
+    # |dz| <= 1.1 |dy| for SiLU, and sum |x dz| <= the product of the columns' norms
+    nx, nd = x.double().square().sum(0).sqrt(), 1.1 * dy.double().square().sum(0).sqrt()
+    sums_match(G["dweight"], [t["dweight"] for t in parts], (nx * nd)[:, None] * 1.01)
+    sums_match(G["dbias"], [t["dbias"] for t in parts], 1.1 * dy.double().abs().sum(0) * 1.01)
