@@ -8,7 +8,7 @@
 //   dx_s = sum_{k < W} w[W-1-k] dz_{s+k},   dw[W-1-k] = sum_s x_s dz_{s+k},   db = sum_t dz_t,
 // plus the derivative of the outgoing state for the rows that form it.
 //
-// HBM-bound (forward 65501 x 4096 bf16: 6.0 TB/s; the backward, 5.0 TB/s, issues 29 vector
+// HBM-bound (forward 65501 x 4096 bf16: 5.8 TB/s; the backward, 4.9 TB/s, issues 29 vector
 // instructions an element as well): a thread owns V adjacent channels of a strip of consecutive tokens
 // and slides the W-token window along it in registers, so every row is read
 // once and the strip's W - 1 leading rows (backward: 2 (W - 1)) once more,

@@ -7,10 +7,11 @@
 //   gradient at h, with d = dy w:
 //     dh = dres + r (d - n mean(d n)),  dx = c dh,  dw = sum dy n,  dcs = scale sum dh x
 //
-// All are one pass over HBM, which bounds them (5.4 to 6.0 TB/s on large inputs): each
+// All are one pass over HBM, which bounds them (5.5 to 6 TB/s on large inputs): each
 // row is read once into registers, its sums are formed over the G lanes (or the
-// whole workgroup) that hold it, and the outputs leave from the same registers.  mean(d n) = r mean(d x), so both of
-// the backward's sums are formed before r is known and share one reduction.
+// whole workgroup) that hold it, and the outputs leave from the same registers.
+// mean(d n) = r mean(d x), so both of the backward's sums are formed before r is
+// known and share one reduction.
 #include "kda_block.hpp"
 #include "kda_rows.hpp"
 
@@ -361,7 +362,7 @@ __global__ __launch_bounds__(CSW* CSR) void colsum_kernel(const float* part, int
 }
 
 // Lanes and vectors per lane of a row of nv vectors: a wavefront or part of it up to
-// two vectors a lane, longer rows a workgroup.  Measured (through the caches), bf16, 64e6 values, forward and
+// two vectors a lane, longer rows a workgroup.  Measured through the cache, bf16, 64e6 values, forward and
 // gradient in us: rows of 1024 as here 92 and 128, over 256 lanes 92 and 223; 2048
 // here 93 and 132, a wavefront with four a lane 92 and 132; 4096 here 94, over 512
 // lanes 92; 8192 here 97 and 137, 256 lanes with four 95 and 149.
