@@ -96,8 +96,11 @@ enum { GATE_NONE, GATE_SIGMOID, GATE_SILU };
 template <int GATE> __device__ __forceinline__ float gate_act(float g, float s) {
     return GATE == GATE_SILU ? g * s : GATE == GATE_SIGMOID ? s : 1.f;
 }
+// The logistic slope is as small as the smaller of s and 1 - s, and as right: for g > 0 the
+// difference would lose it (all of it from g = 17 on), e^-g s is the same number.  SiLU's
+// slope is near 1 there, which 1 - s is as right as it has to be for.
 template <int GATE> __device__ __forceinline__ float gate_slope(float g, float s) {
-    return GATE == GATE_SILU ? s * (1.f + g * (1.f - s)) : s * (1.f - s);
+    return GATE == GATE_SILU ? s * (1.f + g * (1.f - s)) : s * (g > 0.f ? __expf(-g) * s : 1.f - s);
 }
 
 template <typename T, int V, int G, int VPT, int GATE, bool PAST>

@@ -433,6 +433,31 @@ def test_norm_gate_against_reference(D, act, dtype):
 
 
 @pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("act", ["sigmoid", "silu"])
+def test_norm_gate_far_gates(act, dtype):
+    """A gate far from zero: its slope, small as it is, is right relative to its own size.
+
+    In units of u = 2^-24, with e = exp(-|g|) within 1.25 |g| + 3 (the argument's product, the
+    rounded constant log2 e, the instruction): the logistic value is within 1.25 |g| + 6, the
+    smaller of it and its complement within 1.25 |g| + 7 of itself, so their product is
+    within 4 |g| + 24 of itself; SiLU's slope s (1 + g (1 - s)) within as many of
+    s (1 + |g| (1 - s)).  The other factors, dy n w, are within 64."""
+    log(f"norm_gate far gates {act} {dtype}")
+    far = [1, 4, 8, 12, 14, 16, 17, 18, 20, 30, 60]
+    gates = torch.tensor([0.0] + [float(s * v) for v in far for s in (1, -1)])
+    r = rnd(34)
+    T, H, D = 6, 2, gates.numel()
+    x, w, dy = r(T, H, D).to(dtype), 1 + 0.3 * r(D), r(T, H, D).to(dtype)
+    gt = gates.expand(T, H, D).contiguous().to(dtype)
+    x8, w8, g8, dy8 = (t.double() for t in (x, w, gt, dy))
+    got = kda.norm_gate_bwd(dev(x), dev(w), dev(dy), dev(gt), activation=act)["dgate"]
+    n = x8 / torch.sqrt((x8 * x8).mean(-1, keepdim=True) + 1e-6)
+    s, c = 1 / (1 + torch.exp(-g8)), 1 / (1 + torch.exp(g8))
+    slope, size = (s * c, s * c) if act == "sigmoid" else (s * (1 + g8 * c), s * (1 + g8.abs() * c))
+    R.check(got, dy8 * n * w8 * slope, (4 * g8.abs() + 24 + 64) * (dy8 * n * w8).abs() * size, "dgate")
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
 def test_norm_gate_without_weight_many_rows(dtype):
     log(f"norm_gate rows {dtype}")
     r = rnd(32)
