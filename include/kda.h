@@ -445,8 +445,8 @@ typedef struct {
  *   workspace  kda_scan_workspace_size bytes (0: may be NULL).  Calls that share
  *              a workspace must be ordered on one stream: two at once give
  *              wrong values (NaN where one waits for a state in vain).
- * Refused, as larger than one launch: ceil(T / 128) ceil(C / 64) >= 8388544 (T of
- * 1.07e9 in rows of up to 64 channels; wide rows run out of memory first).
+ * Refused, as larger than one launch: ceil(T / 128) ceil(C / 64) >= 8388479 (T above
+ * 1073725184 in rows of up to 64 channels; wide rows run out of memory first).
  */
 KDA_API int kda_scan_fwd(const kda_scan_dims_t* dims, const void* x, const float* log_a, const float* h0,
                          const int32_t* cu_seqlens, void* y, float* h_T, float* states, void* workspace,

@@ -93,6 +93,32 @@ inline size_t linscan_chain_bytes(int64_t T, int64_t C) {
     const size_t tiles = (size_t)((T + LINSCAN_TILE - 1) / LINSCAN_TILE);
     return tiles > 1 ? (tiles * C + (C + 63) / 64 * LINSCAN_LINE) * 8 : 0;
 }
+// The launch for T tokens of C channels: vec channels a lane, waves wavefronts of 16
+// tokens to a tile, tiles x cblocks workgroups, and up to LINSCAN_EMPTY more for empty
+// sequences.
+constexpr int LINSCAN_EMPTY = 64;
+struct LinScanShape { int vec, waves, tiles, cblocks; };
+inline LinScanShape linscan_shape(int32_t T, int32_t C) {
+    LinScanShape s;
+    s.vec = C < 2 ? 1 : 2;
+    // A chain is narrow below 32 column blocks.  Its tiles wait for each other more
+    // than for memory, so they are longer: 256 tokens on 16 wavefronts.  In a wide one
+    // 128 on 8 leave room for two workgroups on a compute unit, one loading while
+    // the other waits or stores.  Measured, 256 against 128: 2 x 32768 x 4096 bf16
+    // 489 us against 409, 24571 x 4096 fp32 239 against 214; 24571 x 1000 fp32 71
+    // against 75, 4096 x 2048 bf16 19.6 against 21.0, 60000 x 64 26 against 38.  (Tiles
+    // of 64: 466, 227; 82, 24.7, 64.)
+    s.waves = s.vec == 1 || C < 32 * 64 * s.vec ? 16 : 8;
+    s.tiles = (T + s.waves * 16 - 1) / (s.waves * 16);
+    s.cblocks = (C + 64 * s.vec - 1) / (64 * s.vec);
+    return s;
+}
+// Whether such a launch stays below 2^32 threads.  One column block of tiles of 256
+// is the tightest: n = ceil(T / 128) makes ceil(n / 2) + 64 workgroups of 1024 threads, at
+// most 512 n + 66048.  Every other shape has fewer threads for its n column blocks of 64.
+inline bool linscan_fits(int64_t T, int64_t C) {
+    return (T + LINSCAN_TILE - 1) / LINSCAN_TILE * ((C + 63) / 64) < (1ll << 32) / 512 - 129;
+}
 hipError_t launch_linscan_fwd(const LinScanArgs& a, bool out, hipStream_t st);  // out: y, hT; states where given
 hipError_t launch_linscan_bwd(const LinScanArgs& a, hipStream_t st);            // dx, dla, dh0 from states
 hipError_t launch_linscan_step(const LinScanArgs& a, hipStream_t st);

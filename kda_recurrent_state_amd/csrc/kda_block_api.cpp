@@ -109,10 +109,8 @@ size_t scan_workspace(const kda::LinScanArgs& a, int backward) {
     return scan_chain_bytes(a) + (backward ? round256(states) : 0);
 }
 
-// Workgroups of a launch: 512 threads each, fewer than 2^32 in all.
 int check_scan_size(const kda::LinScanArgs& a) {
-    const int64_t tiles = ((int64_t)a.T + kda::LINSCAN_TILE - 1) / kda::LINSCAN_TILE, blocks = (a.C + 63) / 64;
-    if (tiles * blocks > kMaxThreads / 512 - 64)
+    if (!kda::linscan_fits(a.T, a.C))
         return fail(KDA_ERR_INVALID_ARGUMENT, "total_tokens x channels = %d x %d is too large", a.T, a.C);
     return KDA_OK;
 }

@@ -30,7 +30,7 @@
 namespace kda {
 namespace {
 
-constexpr int TW = 16;       // tokens per wavefront; a workgroup's NW wavefronts hold a tile
+constexpr int TW = 16;       // tokens per wavefront; a workgroup's NW wavefronts hold a tile (linscan_shape)
 constexpr int SW = 64 / TW;  // wavefronts between two rows of states
 constexpr uint32_t EMPTY = 0xffffffffu;  // P of a word not yet published
 constexpr uint32_t KNOWN = 0xbf800000u;  // P = -1: E is the state itself
@@ -444,63 +444,55 @@ __global__ __launch_bounds__(BS) void linscan_step_kernel(LinScanArgs p) {
     }
 }
 
-int empty_blocks(int N) { return N < 64 ? N : 64; }
-
-// A chain is narrow below 32 column blocks.  Its tiles wait for each other more
-// than for memory, so they are longer: 256 tokens on 16 wavefronts.  In a wide one
-// 128 on 8 leave room for two workgroups on a compute unit, one loading while
-// the other waits or stores.  Measured, 256 against 128: 2 x 32768 x 4096 bf16
-// 489 us against 409, 24571 x 4096 fp32 239 against 214; 24571 x 1000 fp32 71
-// against 75, 4096 x 2048 bf16 19.6 against 21.0, 60000 x 64 26 against 38.  (Tiles
-// of 64: 466, 227; 82, 24.7, 64.)
-template <int V> bool narrow(int C) { return C < 32 * WAVE * V; }
+int empty_blocks(int N) { return N < LINSCAN_EMPTY ? N : LINSCAN_EMPTY; }
 
 // Clears the chain (more than one tile) and gives the launch its grid.
-template <int V, int NW, typename K>
-hipError_t run_chain(K kernel, const LinScanArgs& a, bool empties, hipStream_t st) {
-    const int tiles = (a.T + NW * TW - 1) / (NW * TW), cblocks = (a.C + WAVE * V - 1) / (WAVE * V);
-    const int64_t blocks = (int64_t)tiles * cblocks + (empties ? empty_blocks(a.N) : 0);
+template <typename K>
+hipError_t run_chain(K kernel, const LinScanArgs& a, const LinScanShape& s, bool empties, hipStream_t st) {
+    const int64_t blocks = (int64_t)s.tiles * s.cblocks + (empties ? empty_blocks(a.N) : 0);
     if (blocks == 0) return hipSuccess;
     uint64_t* tickets = nullptr;
-    if (tiles > 1) {
-        const int64_t words = (int64_t)tiles * a.C, counters = (int64_t)cblocks * LINSCAN_LINE;
+    if (s.tiles > 1) {
+        const int64_t words = (int64_t)s.tiles * a.C, counters = (int64_t)s.cblocks * LINSCAN_LINE;
         tickets = a.word + words;
         hipLaunchKernelGGL(linscan_clear_kernel, dim3((unsigned)((words + counters + 511) / 512)), dim3(256), 0, st,
                            a.word, words, counters);
     }
-    hipLaunchKernelGGL(kernel, dim3((unsigned)blocks), dim3(NW * WAVE), 0, st, a, tiles, cblocks, tickets);
+    hipLaunchKernelGGL(kernel, dim3((unsigned)blocks), dim3(s.waves * WAVE), 0, st, a, s.tiles, s.cblocks, tickets);
     return hipGetLastError();
 }
 
 template <typename T, int V, bool OUT>
-hipError_t fwd(const LinScanArgs& a, hipStream_t st) {
+hipError_t fwd(const LinScanArgs& a, const LinScanShape& s, hipStream_t st) {
     const bool empties = OUT && a.hT;
     if constexpr (V > 1)
-        if (!narrow<V>(a.C)) return run_chain<V, 8>(linscan_fwd_kernel<T, V, 8, OUT, 4>, a, empties, st);
-    return run_chain<V, 16>(linscan_fwd_kernel<T, V, 16, OUT, 8>, a, empties, st);
+        if (s.waves == 8) return run_chain(linscan_fwd_kernel<T, V, 8, OUT, 4>, a, s, empties, st);
+    return run_chain(linscan_fwd_kernel<T, V, 16, OUT, 8>, a, s, empties, st);
 }
 template <typename T, int V>
-hipError_t fwd(const LinScanArgs& a, bool out, hipStream_t st) {
-    return out ? fwd<T, V, true>(a, st) : fwd<T, V, false>(a, st);
+hipError_t fwd(const LinScanArgs& a, const LinScanShape& s, bool out, hipStream_t st) {
+    return out ? fwd<T, V, true>(a, s, st) : fwd<T, V, false>(a, s, st);
 }
 template <typename T, int V>
-hipError_t bwd(const LinScanArgs& a, hipStream_t st) {
+hipError_t bwd(const LinScanArgs& a, const LinScanShape& s, hipStream_t st) {
     const bool empties = a.hT != nullptr;
     if constexpr (V > 1)
-        if (!narrow<V>(a.C)) return run_chain<V, 8>(linscan_bwd_kernel<T, V, 8>, a, empties, st);
-    return run_chain<V, 16>(linscan_bwd_kernel<T, V, 16>, a, empties, st);
+        if (s.waves == 8) return run_chain(linscan_bwd_kernel<T, V, 8>, a, s, empties, st);
+    return run_chain(linscan_bwd_kernel<T, V, 16>, a, s, empties, st);
 }
 
 }  // namespace
 
 hipError_t launch_linscan_fwd(const LinScanArgs& a, bool out, hipStream_t st) {
-    if (a.C < 2) return a.dtype == 1 ? fwd<bf16, 1>(a, out, st) : fwd<float, 1>(a, out, st);
-    return a.dtype == 1 ? fwd<bf16, 2>(a, out, st) : fwd<float, 2>(a, out, st);
+    const LinScanShape s = linscan_shape(a.T, a.C);
+    if (s.vec == 1) return a.dtype == 1 ? fwd<bf16, 1>(a, s, out, st) : fwd<float, 1>(a, s, out, st);
+    return a.dtype == 1 ? fwd<bf16, 2>(a, s, out, st) : fwd<float, 2>(a, s, out, st);
 }
 
 hipError_t launch_linscan_bwd(const LinScanArgs& a, hipStream_t st) {
-    if (a.C < 2) return a.dtype == 1 ? bwd<bf16, 1>(a, st) : bwd<float, 1>(a, st);
-    return a.dtype == 1 ? bwd<bf16, 2>(a, st) : bwd<float, 2>(a, st);
+    const LinScanShape s = linscan_shape(a.T, a.C);
+    if (s.vec == 1) return a.dtype == 1 ? bwd<bf16, 1>(a, s, st) : bwd<float, 1>(a, s, st);
+    return a.dtype == 1 ? bwd<bf16, 2>(a, s, st) : bwd<float, 2>(a, s, st);
 }
 
 hipError_t launch_linscan_step(const LinScanArgs& a, hipStream_t st) {
