@@ -16,11 +16,12 @@
 // (P, E), takes the state before the tile from the nearest tile behind whose
 // state is known, folding in the (P, E) of those between, publishes its own end
 // state as (-1, h), and only then walks its tokens.  A pair is one 64-bit word,
-// written and read whole at agent scope, so no other ordering is needed; the
-// fold runs oldest to newest with the same operations that formed the published
-// states, so the result does not depend on which of them were there.  Tiles
-// are taken in the order of a ticket counter: a workgroup waits only for tiles
-// whose workgroups have started, so every wait ends.
+// read and written whole at agent scope, so no other ordering is needed, and
+// written by the thread that owns the channel alone, so that a known state
+// stays known.  The fold runs oldest to newest with the same operations that
+// formed the published states, so the result does not depend on which of them
+// were there.  Tiles are taken in the order of a ticket counter: a workgroup
+// waits only for tiles whose workgroups have started, so every wait ends.
 //
 // The backward runs the same way from the end, with c_t = a_t g_t as what a
 // token hands to the one before it, and takes the forward states from `states`.
@@ -272,19 +273,19 @@ __device__ __forceinline__ void chain(const LinScanArgs& p, const float (&sp)[NW
                                       int tiles) {
     const int j = threadIdx.x;
     if (j >= WAVE * V) return;
-    const int c = column<V>((cb * WAVE + j / V) * V, p.C) + j % V;
+    const ChainColumn k = chain_column<V>(cb, j, p.C);
     float P = sp[BACK ? NW - 1 : 0][j], E = se[BACK ? NW - 1 : 0][j];
 #pragma unroll
     for (int w = 1; w < NW; ++w) then(P, E, sp[BACK ? NW - 1 - w : w][j], se[BACK ? NW - 1 - w : w][j]);
     const int behind = BACK ? tiles - 1 - tile : tile;
-    uint64_t* word = p.word + (int64_t)tile * p.C + c;
+    uint64_t* word = p.word + (int64_t)tile * p.C + k.c;
     float h = 0.f;
     if (tiles > 1) {
         if (behind > 0) {
-            publish(word, P, E);
+            if (k.owner) publish(word, P, E);
             h = look_back<LB>(BACK ? word + p.C : word - p.C, BACK ? (int64_t)p.C : -(int64_t)p.C, behind);
         }
-        if (P >= 0.f || behind == 0 || P != P) publish(word, -1.f, apply(P, E, h));
+        if (k.owner && (P >= 0.f || behind == 0 || P != P)) publish(word, -1.f, apply(P, E, h));
     }
     sh[j] = h;
 }

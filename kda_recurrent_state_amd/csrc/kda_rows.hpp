@@ -84,7 +84,16 @@ template <bool PAST, int V, typename T> __device__ __forceinline__ void store_c(
 }
 
 // First column of the lane whose columns start at c, in a row of C >= V.
-template <int V> __device__ __forceinline__ int column(int c, int C) { return c + V <= C ? c : C - V; }
+template <int V> __host__ __device__ __forceinline__ int column(int c, int C) { return c + V <= C ? c : C - V; }
+
+// The channel of thread j of a block of 64 V columns, and whether it is the thread's own:
+// a lane that was moved back from the row's end, or that lies past it, carries channels
+// of other lanes' too.
+struct ChainColumn { int c; bool owner; };
+template <int V> __host__ __device__ __forceinline__ ChainColumn chain_column(int cb, int j, int C) {
+    const int at = (cb * 64 + j / V) * V, c = column<V>(at, C) + j % V;
+    return {c, c >= at};
+}
 
 // Sequences of a packed axis of T tokens: offsets cu[0..N] on the device, or
 // (cu null) N sequences of eq tokens each.  Offsets are clamped to [0, T], so

@@ -1,4 +1,5 @@
-"""The sizes at which the scan's launch would be too large (host only)."""
+"""The scan's launch, on the host: the sizes at which it would be too large, and which of its
+threads publish a channel's state."""
 import os
 
 import pytest
@@ -22,11 +23,21 @@ def test_room_for_the_empty_sequences(fn, T, C):
     assert "too large" in lib.kda_last_error().decode()
 
 
-def test_accepted_sizes_fit_a_launch(tmp_path):
+def host_check(name, tmp_path):
     if not os.path.exists(HIPCC):
         pytest.skip("hipcc not available")
-    exe = str(tmp_path / "scan_launch_check")
+    exe = str(tmp_path / name)
     _run([HIPCC, "-x", "hip", "-O1", "-std=c++17", "--offload-arch=gfx950", "-Xclang", "-target-feature", "-Xclang",
           "-packed-fp32-ops", "-I" + os.path.join(ROOT, "kda_recurrent_state_amd", "csrc"),
-          os.path.join(SAN, "scan_launch_check.cpp"), "-o", exe])
-    assert "scan launch check ok" in _run([exe]).stdout
+          os.path.join(SAN, name + ".cpp"), "-o", exe])
+    return _run([exe]).stdout
+
+
+def test_accepted_sizes_fit_a_launch(tmp_path):
+    assert "scan launch check ok" in host_check("scan_launch_check", tmp_path)
+
+
+def test_one_publisher_for_each_channel(tmp_path):
+    """In rows of odd length a block's end lane moves back by a column, which its neighbour
+    (of the next workgroup's wavefront, or of another) owns: only that one publishes it."""
+    assert "scan owner check ok" in host_check("scan_owner_check", tmp_path)
