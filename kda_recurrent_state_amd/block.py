@@ -199,7 +199,12 @@ def _p(t):
     return None if t is None else t.data_ptr()
 
 
-_raw_stream = torch._C._cuda_getCurrentRawStream  # current_stream(device).cuda_stream without the objects (1.9 us)
+def _stream_of(i):
+    return torch.cuda.current_stream(i).cuda_stream
+
+
+# the same without the objects (1.9 us less) where torch has it
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", _stream_of)
 
 
 def _launch(fn, lib, device, args):
