@@ -10,7 +10,9 @@ each with its gradient (``*_bwd``) and, where it keeps a state, one token per
 sequence (``*_step``).  Tensors are bf16 or fp32; parameters (weight, bias,
 channel_scale), log_a and the recurrence's states are fp32.  Inputs may be
 slices of a fused projection: everything but the token stride must be
-contiguous.  Outputs are contiguous, and allocated here unless given.
+contiguous.  Outputs are contiguous, and allocated here unless given; one that is
+given, or a given workspace's bytes, must not overlap another tensor of the call
+(but for the updates in place that a call names).
 Packed sequences are given as for ``chunk_fwd``; tokens at or past
 ``cu_seqlens[-1]`` are left alone, and so are their rows of the outputs.
 """
@@ -179,12 +181,15 @@ def _extent(t):
 
 def _apart(out, *inputs):
     """Refuses an output whose memory overlaps an input's."""
-    a, b = _extent(out)
-    for t in inputs:
+    _bytes_apart("an output", *_extent(out), inputs)
+
+
+def _bytes_apart(what, a, b, tensors):
+    for t in tensors:
         if t is not None:
             lo, hi = _extent(t)
             if a < hi and lo < b and lo < hi and a < b:
-                raise ValueError("an output overlaps another tensor of the call")
+                raise ValueError(f"{what} overlaps another tensor of the call")
 
 
 def _new(like):
@@ -229,13 +234,17 @@ def _needed(name, kind, fields, more):
     return need.value
 
 
-def _workspace(name, dims, more, workspace, device):
-    """The caller's workspace, or one of the size that the entry point `name` says."""
+def _workspace(name, dims, more, workspace, device, *tensors):
+    """The caller's workspace, whose bytes that the call uses are none of its tensors', or
+    one of the size that the entry point `name` says."""
+    need = _needed(name, type(dims), bytes(dims), more)
     if workspace is None:
-        return torch.empty(_needed(name, type(dims), bytes(dims), more), dtype=torch.uint8, device=device)
+        return torch.empty(need, dtype=torch.uint8, device=device)
     if not isinstance(workspace, torch.Tensor) or workspace.dtype is not torch.uint8 or workspace.dim() != 1 \
             or not workspace.is_contiguous():
         raise TypeError("workspace must be a contiguous 1-D uint8 tensor")
+    at = workspace.data_ptr()
+    _bytes_apart("the workspace", at, at + min(need, workspace.numel()), tensors)
     return workspace
 
 
@@ -271,8 +280,8 @@ def _scan(x, log_a, h0, cu_seqlens, num_seqs, out, final_state, states, workspac
     hT = final_state if given else torch.empty((N, C), dtype=torch.float32, device=x.device) if final_state else None
     for o in (out, hT if given else None, states):
         if o is not None:
-            _apart(o, x, log_a, h0, *(t for t in (out, hT, states) if t is not o))
-    ws = _workspace("kda_scan_workspace_size", d, (0,), workspace, x.device)
+            _apart(o, x, log_a, h0, cu_seqlens, *(t for t in (out, hT, states) if t is not o))
+    ws = _workspace("kda_scan_workspace_size", d, (0,), workspace, x.device, x, log_a, h0, cu_seqlens, out, hT, states)
     _launch(lib.kda_scan_fwd, lib, x.device, (ref, _p(x), _p(log_a), _p(h0), _p(cu_seqlens), _p(y), _p(hT),
                                               _p(states), _p(ws), ws.numel()))
     return y, hT
@@ -323,7 +332,7 @@ def scan_bwd(x, log_a, dy, h0=None, cu_seqlens=None, dh_T=None, *, num_seqs: int
     dx = _new(x)
     dla = _new(log_a)
     dh0 = torch.empty((N, C), dtype=torch.float32, device=dev) if initial_state_grad else None
-    ws = _workspace("kda_scan_workspace_size", d, (1,), workspace, dev)
+    ws = _workspace("kda_scan_workspace_size", d, (1,), workspace, dev, x, log_a, dy, h0, cu_seqlens, dh_T, states)
     _launch(lib.kda_scan_bwd, lib, dev, (ref, _p(x), _p(log_a), _p(h0), _p(cu_seqlens), _p(states), _p(dy), _p(dh_T),
                                          _p(dx), _p(dla), _p(dh0), _p(ws), ws.numel()))
     return {"dx": dx, "dlog_a": dla, "dh0": dh0}
@@ -394,7 +403,7 @@ def conv_fwd(x, weight, bias=None, state=None, cu_seqlens=None, *, num_seqs: int
     sT = final_state if given else torch.empty((N, W - 1, C), dtype=x.dtype, device=x.device) if final_state else None
     for o in (out, sT if given else None):
         if o is not None:
-            _apart(o, x, state, *(t for t in (out, sT) if t is not o))
+            _apart(o, x, weight, bias, state, cu_seqlens, *(t for t in (out, sT) if t is not o))
     _launch(lib.kda_conv_fwd, lib, x.device, (ref, _p(x), _p(weight), _p(bias), _p(state), _p(cu_seqlens),
                                               _p(y), _p(sT)))
     return y, sT
@@ -419,7 +428,8 @@ def conv_bwd(x, weight, dy, bias=None, state=None, cu_seqlens=None, dstate_T=Non
     dw = _new(weight)
     db = torch.empty((C,), dtype=torch.float32, device=dev)
     ds = torch.empty((N, W - 1, C), dtype=x.dtype, device=dev) if initial_state_grad else None
-    ws = _workspace("kda_conv_bwd_workspace_size", d, (), workspace, dev)
+    ws = _workspace("kda_conv_bwd_workspace_size", d, (), workspace, dev, x, weight, dy, bias, state, cu_seqlens,
+                    dstate_T)
     _launch(lib.kda_conv_bwd, lib, dev, (ref, _p(x), _p(weight), _p(bias), _p(state), _p(cu_seqlens), _p(dy),
                                          _p(dstate_T), _p(dx), _p(dw), _p(db), _p(ds), _p(ws), ws.numel()))
     return {"dx": dx, "dweight": dw, "dbias": db, "dstate": ds}
@@ -444,9 +454,9 @@ def conv_step(x, weight, state, bias=None, *, activation: str | None = "silu", o
     so = state if state_out is None else state_out
     y = _new(x) if out is None else out
     if out is not None:
-        _apart(out, x, state, state_out)
+        _apart(out, x, weight, bias, state, state_out)
     if state_out is not None and state_out is not state:
-        _apart(state_out, x, *(() if state_out.data_ptr() == state.data_ptr() else (state,)))
+        _apart(state_out, x, weight, bias, *(() if state_out.data_ptr() == state.data_ptr() else (state,)))
     _launch(lib.kda_conv_step, lib, x.device, (ref, _p(x), _p(weight), _p(bias), _p(state), _p(so), _p(y)))
     return y, so
 
@@ -477,7 +487,7 @@ def norm_gate_fwd(x, weight=None, gate=None, *, activation: str = "sigmoid", eps
     _same_device(x, weight=weight, gate=gate, out=out)
     y = _new(x) if out is None else out
     if out is not None:
-        _apart(out, gate, *(() if out.data_ptr() == x.data_ptr() and x.is_contiguous() else (x,)))
+        _apart(out, weight, gate, *(() if out.data_ptr() == x.data_ptr() and x.is_contiguous() else (x,)))
     _launch(lib.kda_norm_gate_fwd, lib, x.device, (ref, _p(x), _p(weight), _p(gate), _p(y)))
     return y
 
@@ -493,7 +503,8 @@ def norm_gate_bwd(x, weight, dy, gate=None, *, activation: str = "sigmoid", eps:
     dx = _new(x)
     dg = None if gate is None else _new(x)
     dw = None if weight is None else torch.empty(x.shape[2], dtype=torch.float32, device=dev)
-    ws = None if dw is None else _workspace("kda_norm_gate_bwd_workspace_size", d, (), workspace, dev)
+    ws = None if dw is None else _workspace("kda_norm_gate_bwd_workspace_size", d, (), workspace, dev, x, weight, dy,
+                                            gate)
     _launch(lib.kda_norm_gate_bwd, lib, dev, (ref, _p(x), _p(weight), _p(gate), _p(dy), _p(dx), _p(dg), _p(dw),
                                               _p(ws), 0 if ws is None else ws.numel()))
     return {"dx": dx, "dgate": dg, "dweight": dw}
@@ -536,10 +547,10 @@ def residual_norm_fwd(x, residual, weight, *, scale: float = 1.0, channel_scale=
     y = _new(x) if out is None else out
     r = _new(residual) if residual_out is None else residual_out
     if out is not None:
-        _apart(out, x, residual, residual_out)
+        _apart(out, x, residual, weight, channel_scale, residual_out)
     if residual_out is not None:
         same = residual_out.data_ptr() == residual.data_ptr() and residual.is_contiguous()
-        _apart(residual_out, x, *(() if same else (residual,)))
+        _apart(residual_out, x, weight, channel_scale, *(() if same else (residual,)))
     _launch(lib.kda_residual_norm_fwd, lib, x.device, (ref, _p(x), _p(residual), _p(weight),
                                                        _p(channel_scale), _p(r), _p(y)))
     return y, r
@@ -564,7 +575,8 @@ def residual_norm_bwd(x, residual_out, weight, dy, dresidual_out=None, *, scale:
     dr = _new(residual_out)
     dw = torch.empty(shape[1], dtype=torch.float32, device=dev)
     dc = None if channel_scale is None else torch.empty(shape[1], dtype=torch.float32, device=dev)
-    ws = _workspace("kda_residual_norm_bwd_workspace_size", d, (), workspace, dev)
+    ws = _workspace("kda_residual_norm_bwd_workspace_size", d, (), workspace, dev, x, residual_out, weight,
+                    channel_scale, dy, dresidual_out)
     _launch(lib.kda_residual_norm_bwd, lib, dev, (ref, _p(x), _p(residual_out), _p(weight), _p(channel_scale), _p(dy),
                                                   _p(dresidual_out), _p(dx), _p(dr), _p(dw), _p(dc), _p(ws),
                                                   ws.numel()))
