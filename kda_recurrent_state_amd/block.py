@@ -172,24 +172,28 @@ def _same_device(ref, **tensors):
             _named_devices(ref, **tensors)
 
 
-def _extent(t):
-    lo = t.data_ptr()
+def _touches(t, a, b):
+    """Whether t, contiguous within its tokens, has a byte in [a, b)."""
+    lo, size = t.data_ptr(), t.nbytes
+    if not size or a >= b:
+        return False
     if t.is_contiguous():
-        return lo, lo + t.nbytes
-    return lo, lo + (1 + sum((n - 1) * d for n, d in zip(t.shape, t.stride()))) * t.element_size()
+        return a < lo + size and lo < b
+    tokens, step = t.shape[0], t.stride(0) * t.element_size()
+    first = max(0, (a - lo - size // tokens) // step + 1)  # the first token that ends behind a
+    return first < tokens and lo + first * step < b
 
 
 def _apart(out, *inputs):
     """Refuses an output whose memory overlaps an input's."""
-    _bytes_apart("an output", *_extent(out), inputs)
+    at = out.data_ptr()
+    _bytes_apart("an output", at, at + out.nbytes, inputs)
 
 
 def _bytes_apart(what, a, b, tensors):
     for t in tensors:
-        if t is not None:
-            lo, hi = _extent(t)
-            if a < hi and lo < b and lo < hi and a < b:
-                raise ValueError(f"{what} overlaps another tensor of the call")
+        if t is not None and _touches(t, a, b):
+            raise ValueError(f"{what} overlaps another tensor of the call")
 
 
 def _new(like):

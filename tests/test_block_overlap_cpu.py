@@ -101,3 +101,53 @@ def test_a_workspace_is_the_bytes_that_are_needed(launched):
     assert launched == ["kda_scan_fwd"]
     with pytest.raises(ValueError, match="overlaps"):
         kda.scan_fwd(pool[need - 4:-4].view(F32).view(T, C), la, workspace=pool)
+
+
+def rows(buf, every, count):
+    return buf[::every][:count]
+
+
+def test_an_output_between_an_inputs_tokens(launched):
+    """Tokens far apart leave room for other tensors: only their own bytes count."""
+    buf = f(9, C)
+    x, out, la = rows(buf, 4, 2), buf[1:3], f(2, C)  # tokens 0 and 4; rows 1 and 2
+    kda.scan_fwd(x, la, out=out)
+    kda.scan_step(x, la, f(2, C), out=buf[2:4])
+    kda.norm_gate_fwd(x.view(2, 1, C), f(C), out=buf[5:7].view(2, 1, C))
+    kda.residual_norm_fwd(la, x, f(C), out=buf[1:3], residual_out=buf[5:7])
+    assert len(launched) == 4
+    for at in (0, 3, 4):
+        with pytest.raises(ValueError, match="overlaps"):
+            kda.scan_fwd(x, la, out=buf[at:at + 2])
+    flat = buf.view(-1)
+    for at in (1, C - 1, 3 * C - C + 1, 5 * C - 1):  # by an element, at either end of either token
+        with pytest.raises(ValueError, match="overlaps"):
+            kda.scan_fwd(x, la, out=flat[at:at + 2 * C].view(2, C))
+    kda.scan_fwd(x, la, out=flat[C:3 * C].view(2, C))
+    kda.scan_fwd(x, la, out=flat[2 * C:4 * C].view(2, C))
+    kda.scan_fwd(x, la, out=flat[5 * C:7 * C].view(2, C))
+    assert len(launched) == 7
+    # a slice of a fused projection: every gap is shorter than the output, wherever it lies
+    wide = f(T, 3 * C)
+    for at in range(0, wide.numel() - T * C + 1, 37):
+        with pytest.raises(ValueError, match="overlaps"):
+            kda.scan_fwd(wide[:, C:2 * C], f(T, C), out=wide.view(-1)[at:at + T * C].view(T, C))
+    assert len(launched) == 7
+
+
+@pytest.mark.parametrize("seed", range(4))
+def test_touching_is_sharing_a_byte(seed):
+    """Against the bytes themselves, for token tensors of two and three dimensions."""
+    g = torch.Generator().manual_seed(seed)
+    pick = lambda lo, hi: int(torch.randint(lo, hi, (1,), generator=g))
+    buf = torch.zeros(600)
+    base = buf.data_ptr()
+    for _ in range(2000):
+        n, h, c = pick(0, 5), pick(1, 3), pick(1, 6)
+        step, at = pick(h * c, h * c + 40), pick(0, 40)
+        t = torch.as_strided(buf, (n, h, c), (step, c, 1), at)
+        t = t if pick(0, 2) else torch.as_strided(buf, (n, h * c), (step, 1), at)
+        mine = {at + r * step + i for r in range(n) for i in range(h * c)}
+        a = pick(0, 300)
+        b = a + pick(0, 30)
+        assert block._touches(t, base + 4 * a, base + 4 * b) == bool(mine & set(range(a, b)))
