@@ -78,10 +78,18 @@ def _declare(lib):
     lib.kda_scan_workspace_size.argtypes = [ctypes.POINTER(_ScanDims), ctypes.c_int, ctypes.POINTER(Z)]
 
 
+def _struct(kind, *fields):
+    """A dims structure; ctypes itself takes an integer modulo its field's size."""
+    for (name, of), v in zip(kind._fields_, fields):
+        if of is _i32 and not -1 << 31 <= v < 1 << 31:
+            raise ValueError(f"{name} = {v} does not fit 32 bits")
+    return kind(*fields)
+
+
 @lru_cache(maxsize=4096)
 def _dims(kind, *fields):
     """A dims structure (only ever read) and a reference to it."""
-    d = kind(*fields)
+    d = _struct(kind, *fields)
     return d, ctypes.byref(d)
 
 
@@ -345,7 +353,8 @@ def scan_bwd(x, log_a, dy, h0=None, cu_seqlens=None, dh_T=None, *, num_seqs: int
 def scan_workspace_size(x, *, num_seqs: int = 1, backward: bool = False):
     """Bytes of workspace scan_fwd (or, backward=True, scan_bwd) needs for x's shape."""
     T, C = _rank(x, "x", 2)
-    return _size("kda_scan_workspace_size", _ScanDims(int(num_seqs), C, T, _code(x), 0, 0, 0, 0), int(bool(backward)))
+    return _size("kda_scan_workspace_size", _struct(_ScanDims, int(num_seqs), C, T, _code(x), 0, 0, 0, 0),
+                 int(bool(backward)))
 
 
 def scan_step(x, log_a, h, *, out=None, h_out=None):
@@ -442,7 +451,8 @@ def conv_bwd(x, weight, dy, bias=None, state=None, cu_seqlens=None, dstate_T=Non
 def conv_bwd_workspace_size(x, width: int, *, num_seqs: int = 1):
     """Bytes of workspace conv_bwd needs for x's shape and `width` taps."""
     T, C = _rank(x, "x", 2)
-    return _size("kda_conv_bwd_workspace_size", _ConvDims(int(num_seqs), C, T, _code(x), int(width), 0, 0, 0, 0))
+    return _size("kda_conv_bwd_workspace_size",
+                 _struct(_ConvDims, int(num_seqs), C, T, _code(x), int(width), 0, 0, 0, 0))
 
 
 def conv_step(x, weight, state, bias=None, *, activation: str | None = "silu", out=None, state_out=None):
@@ -517,7 +527,8 @@ def norm_gate_bwd(x, weight, dy, gate=None, *, activation: str = "sigmoid", eps:
 def norm_gate_bwd_workspace_size(x):
     """Bytes of workspace norm_gate_bwd needs for x's shape."""
     T, H, D = _rank(x, "x", 3)
-    return _size("kda_norm_gate_bwd_workspace_size", _NormGateDims(T, H, D, _code(x), 2, 0.0, 0, 0, 0, 0))
+    return _size("kda_norm_gate_bwd_workspace_size",
+                 _struct(_NormGateDims, T, H, D, _code(x), 2, 0.0, 0, 0, 0, 0))
 
 
 def _res_norm_dims(x, res, weight, channel_scale, scale, eps, rname, dy=None, dres=None):
@@ -590,5 +601,5 @@ def residual_norm_bwd(x, residual_out, weight, dy, dresidual_out=None, *, scale:
 def residual_norm_bwd_workspace_size(x):
     """Bytes of workspace residual_norm_bwd needs for x's shape and dtype."""
     T, D = _rank(x, "x", 2)
-    d = _ResNormDims(T, D, _code(x), _code(x), 0.0, 1.0, 0, 0, 0, 0, 0)
+    d = _struct(_ResNormDims, T, D, _code(x), _code(x), 0.0, 1.0, 0, 0, 0, 0, 0)
     return _size("kda_residual_norm_bwd_workspace_size", d)
