@@ -411,6 +411,9 @@ KDA_API int kda_decode_step_ex(const kda_dims_t* dims, const kda_prologue_t* pro
  *   - Outputs must not overlap inputs or each other except where said.
  *   - Sums, norms and states are held in fp32; an output is rounded once.
  *     Reductions run in a fixed order: a call repeats bit for bit.
+ *   - A norm's squares are fp32 as well: a row's sum of squares has to stay below
+ *     3.4e38, and its mean square + eps above 1.2e-38 (a gradient overflows below
+ *     a quarter of that).
  * ------------------------------------------------------------------------- */
 
 /*

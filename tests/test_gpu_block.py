@@ -457,6 +457,33 @@ def test_norm_gate_far_gates(act, dtype):
     R.check(got, dy8 * n * w8 * slope, (4 * g8.abs() + 24 + 64) * (dy8 * n * w8).abs() * size, "dgate")
 
 
+@pytest.mark.parametrize("D", [1, 40, 256, 8192])
+@pytest.mark.parametrize("end", ["least", "most"])
+def test_norms_at_the_ends_of_their_range(end, D):
+    """Rows whose mean square is 1.3e-38, and whose sum of squares is 3e38: the bounds hold.  (Squares
+    below 1.2e-38 are off by up to 2^-150 instead of their 2^-24: 5e-8 of the mean's 1.3e-38 each, so
+    the mean by less than one u more.)"""
+    log(f"norm range {end} D={D}")
+    r = rnd(35)
+    T, eps = 5, 0.0
+    x8 = r(T, 1, D).double()
+    x8 = x8 / (x8 * x8).mean(-1, keepdim=True).sqrt()
+    x = (x8 * ((1.3e-38 if end == "least" else 3e38 / D) ** 0.5)).float()
+    w, dy = 1 + 0.3 * r(D), r(T, 1, D)
+    yv, yb = R.norm_gate(x.double(), w.double(), None, None, eps)
+    R.check(kda.norm_gate_fwd(dev(x), dev(w), eps=eps), yv, yb, "y")
+    val, bnd = R.norm_gate_grad(x.double(), w.double(), None, None, eps, dy.double())
+    g = kda.norm_gate_bwd(dev(x), dev(w), dev(dy), eps=eps)
+    for k in val:
+        R.check(g[k], val[k], bnd[k], k)
+    zero = torch.zeros(T, D)
+    val, bnd = R.residual_norm_grad(zero.double(), x[:, 0].double(), w.double(), 1.0, None, eps, dy[:, 0].double(),
+                                    zero.double())
+    g = kda.residual_norm_bwd(None, dev(x[:, 0].contiguous()), dev(w), dev(dy[:, 0].contiguous()), eps=eps)
+    for k in val:
+        R.check(g[k], val[k], bnd[k], k)
+
+
 @pytest.mark.parametrize("dtype", DTYPES)
 def test_norm_gate_without_weight_many_rows(dtype):
     log(f"norm_gate rows {dtype}")
