@@ -104,10 +104,12 @@ inline LinScanShape linscan_shape(int32_t T, int32_t C) {
     // A chain is narrow below 32 column blocks.  Its tiles wait for each other more
     // than for memory, so they are longer: 256 tokens on 16 wavefronts.  In a wide one
     // 128 on 8 leave room for two workgroups on a compute unit, one loading while
-    // the other waits or stores.  Measured, 256 against 128: 2 x 32768 x 4096 bf16
-    // 489 us against 409, 24571 x 4096 fp32 239 against 214; 24571 x 1000 fp32 71
-    // against 75, 4096 x 2048 bf16 19.6 against 21.0, 60000 x 64 26 against 38.  (Tiles
-    // of 64: 466, 227; 82, 24.7, 64.)
+    // the other waits or stores.  Measured in a graph, 256 against 128, us: 60000 x 64
+    // in one sequence 44 and 75, in 64 sequences 19.4 and 22.9, 4096 x 2048 bf16 20.6 and
+    // 22.4, 24571 x 1000 fp32 72 and 75; 2 x 32768 x 4096 bf16 482 and 412, 24571 x 4096
+    // fp32 239 and 219.  Between them the length counts as well, which the rule leaves
+    // out: 4096 x 3584 bf16 33.3 and 33.6 and its gradient in fp32 90 and 95, but
+    // 32768 x 3584 237 and 192, 668 and 592, and 32768 x 2048 137 and 120, 379 and 358.
     s.waves = s.vec == 1 || C < 32 * 64 * s.vec ? 16 : 8;
     s.tiles = (T + s.waves * 16 - 1) / (s.waves * 16);
     s.cblocks = (C + 64 * s.vec - 1) / (64 * s.vec);

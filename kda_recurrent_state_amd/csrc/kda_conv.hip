@@ -416,8 +416,8 @@ void set_strips(ConvShape* s, int T, int64_t L) {
     s->L = (int)L;
     s->strips = (int)((T + spb * L - 1) / (spb * L));
 }
-// Forward: strips of up to 16 tokens (65501 x 4096 bf16: 185 us; 8: 194, 32: 189, 64:
-// 199), shorter ones where that leaves fewer than 2048 workgroups.
+// Forward: strips of 16 tokens (65501 x 4096 bf16: 185 us; 8: 194, 32: 189, 64: 199), or
+// of 8 where those make no more than 2048 workgroups.
 ConvShape fwd_shape(int V, int T, int C) {
     ConvShape s = conv_shape(V, C);
     int L = 8;

@@ -3,7 +3,8 @@
 //   h_t = a_t h_{t-1} + x_t,  a_t = e^{log a_t},  y_t = h_t            per channel
 //   g_t = dy_t + a_{t+1} g_{t+1},  dx_t = g_t,  dlog a_t = g_t a_t h_{t-1}
 //
-// HBM-bound (2 x 32768 x 4096 bf16: 409 us, 5.3 TB/s), so x and log a are read once.
+// HBM-bound (2 x 32768 x 4096 bf16: 409 us, 5.25 TB/s of the bytes that have to move), so x and
+// log a are read once.
 // The packed axis is cut into tiles of 128 or 256 tokens whatever the sequences'
 // edges; a workgroup holds one tile of 64 V channels, each of its wavefronts 16
 // tokens in registers.  A run of tokens
@@ -62,9 +63,9 @@ __device__ __forceinline__ uint64_t read_word(const uint64_t* word) {
 // The nearest LB are read together; after that a poll reads only the farthest
 // again, whose state is the first to become known, and what was not there yet.
 // Forwards LB = 4 keeps a wide chain ahead of the memory (2 x 32768 x 4096: 409 us;
-// LB = 2: 415, 8: 416, 1: 473); narrow ones take 8 (in tiles of 128, 4096 x 2048:
-// 21 us, 4: 23, 16: 27; 60000 x 64: 38, 4: 46).  Backwards 4, in float32 2 for its
-// registers.
+// LB = 2: 415, 8: 416, 1: 473); narrow ones take 8 (60000 x 64 in one sequence: 44 us,
+// 4: 56, 16: 39; 4096 x 2048: 20.6, 21.4, 21.1; 24571 x 1000 fp32: 72, 70, 76).
+// Backwards 4, in float32 2 for its registers.
 template <int LB>  // words of the chain read at once
 __device__ __forceinline__ float look_back(const uint64_t* word, int64_t step, int behind) {
     const int far = (behind < LB ? behind : LB) - 1;
@@ -147,7 +148,9 @@ __device__ __forceinline__ void load_rows(const T* base, int64_t stride, int t0,
     }
 }
 
-// e^{log a}; tokens that do not exist keep the state (a = 1, and x = 0 below).
+// e^{log a}, by the exponential instruction: within (|log a| + 3) 2^-24, which an exact one
+// would take a dozen instructions per element to make 2^-24.  Tokens that do not exist keep
+// the state (a = 1, and x = 0 below).
 template <int V>
 __device__ __forceinline__ void decays(const Pack<float, V> (&la)[TW], int count, float (&a)[TW][V]) {
 #pragma unroll

@@ -332,7 +332,10 @@ __global__ __launch_bounds__(threads_of(G)) void res_norm_bwd_kernel(ResNormArgs
 }
 
 // Column sums of a [rows][cols] matrix: 16 columns per workgroup, 64 row lanes
-// each, so that a narrow matrix still spreads over the rows.
+// each, so that a narrow matrix still spreads over the rows.  In float32 as the partial
+// rows are: a sum over a million rows of 128 is a chain of at most 114 additions (86 rows of a
+// group, 16 groups of a workgroup, 12 partial rows) and a tree, so within 121 2^-24 of its
+// terms' magnitudes.
 constexpr int CSW = 16, CSR = 64;
 __global__ __launch_bounds__(CSW* CSR) void colsum_kernel(const float* part, int rows, int64_t cols, int64_t split,
                                                           float* out, float* out2) {
@@ -405,11 +408,14 @@ constexpr int FWD_BLOCKS = 1 << 20;  // one row group each up to here
 // The backward's workgroups, a whole number for each of the 256 compute units,
 // each of which leaves a partial row: as few as keep enough loads in flight.  Of
 // 256, 512, 768 and 1024 took, in us,
-//   gated norm, bf16:     32768 x 32 rows of 128: 463, 280, 237, 241;  30000 of 2048: 268, 155, 123, 118
-//                         20000 of 4096: 233, 158, 155, 178;  8192 of 8192: 142, 148, 153, 159
+//   gated norm, bf16:     32768 x 32 rows of 128: 473, 284, 239, 243;  30000 of 2048: 272, 157, 125, 117
+//                         20000 of 4096: 243, 167, 159, 180;  8192 of 8192: 150, 154, 160, 164
 //   residual norm, loads  24 KB a row (bf16, 16384 of 4096): 152, 121, 136, 125;  40 KB: 210, 189, 205, 195
 //                         48 KB (fp32 stream, 16384 of 4096): 229, 225, 249, 241;  (bf16, 8192 of 8192): 137,
 //                         142, 149, 156;  64 KB: 165, 178, 193, 205;  fp32, 20000 rows of 1000: 125, 75, 77, 82
+// Both rules split where the figures do, and lie between rows that want either: the gated
+// norm's 4096 columns lose 5 % by 512 where its 8192 gain 4 %, the residual norm's two rows
+// of 48 KB lose 2 % and gain 4 % by 256.
 int ng_blocks(int nv) { return nv > 256 ? 512 : 768; }
 int rn_blocks(const ResNormArgs& a) {
     const int e = a.dtype == 1 ? 2 : 4, er = a.rdtype == 1 ? 2 : 4;

@@ -70,8 +70,13 @@ template <int V, typename T> __device__ __forceinline__ void store_nt(T* p, cons
 //   convolution, bf16: 64: 25 and 30, 96: 41 and 41, 128: 55 and 53, 192: 78 and 74, 512:
 //     193 and 185; its gradient, 96: 43 and 45, 128: 57 and 56, 512: 178 and 169
 //   gated norm: fp32, 37: 10.7 and 12.2; bf16, 64: 19.5 and 19.2, 128: 38 and 34, 512: 135
-//     and 126; its gradient, 192: 68 and 63, 768: 248 and 240
+//     and 126; its gradient, 192: 68 and 65, 768: 249 and 240
 //   residual norm, gradient, bf16, 384: 133 and 118
+// The convolution and the scan write past it at every size.  With the call that reads the
+// output behind them in a graph, ordinary stores took, us against these: convolution, then
+// scan, by the MiB of the output, 16: 29.5 and 28.6, 64: 89 and 92; convolution, then
+// norm, 8: 13.5 and 12.8, 64: 54 and 57; scan, then norm, 8: 21.1 and 20.2, 32: 53.7 and 52.1,
+// 64: 87.2 and 88.0.
 inline bool past_cache(int64_t in_bytes) { return in_bytes >= 128ll << 20; }
 // (An access of two halves touches each line twice, which has to stay cached in between.)
 template <bool PAST, int V, typename T> __device__ __forceinline__ Pack<T, V> load_c(const T* p) {
@@ -138,6 +143,7 @@ __device__ __forceinline__ int wave_find(const Seqs& sq, int t) {
     return lo;
 }
 
+// By the exponential and reciprocal instructions: within (|z| + 6) 2^-24 of itself.
 __device__ __forceinline__ float sigmoid_f(float z) { return __builtin_amdgcn_rcpf(1.f + __expf(-z)); }
 
 // Sum over the G (a power of two up to 64) consecutive lanes of a group.
