@@ -479,11 +479,12 @@ KDA_API int kda_scan_workspace_size(const kda_scan_dims_t* dims, int backward, s
 KDA_API int kda_scan_step(const kda_scan_dims_t* dims, const void* x, const float* log_a, const float* h_in,
                           float* h_out, void* y, void* stream);
 
-/* Activation of kda_conv and of kda_norm_gate's gate. */
+/* Activation of kda_conv, of kda_norm_gate's gate and of kda_glu's. */
 typedef enum {
     KDA_ACT_NONE = 0,     /* kda_conv only */
     KDA_ACT_SILU = 1,     /* z / (1 + e^-z) */
-    KDA_ACT_SIGMOID = 2   /* 1 / (1 + e^-z); kda_norm_gate only */
+    KDA_ACT_SIGMOID = 2,  /* 1 / (1 + e^-z); kda_norm_gate and kda_glu only */
+    KDA_ACT_GELU = 3      /* z Phi(z), Phi the normal distribution function; kda_glu only */
 } kda_act_t;
 
 /*
@@ -606,6 +607,162 @@ KDA_API int kda_residual_norm_bwd(const kda_residual_norm_dims_t* dims, const vo
                                   const void* dresidual_out, void* dx, void* dresidual, float* dweight,
                                   float* dchannel_scale, void* workspace, size_t workspace_bytes, void* stream);
 KDA_API int kda_residual_norm_bwd_workspace_size(const kda_residual_norm_dims_t* dims, size_t* bytes);
+
+/* -------------------------------------------------------------------------
+ * Selective state space scan: per head a state of K rows and P columns,
+ *     d_t = softplus(dt_t + dt_bias),  a_t = exp(d_t A),
+ *     h_t = a_t h_{t-1} + d_t B_t^T x_t,   y_t = C_t h_t + D x_t,
+ * with one decay per token and head, and B and C shared by the heads of a group
+ * (head h belongs to group h / (heads / groups)).  The conventions are those of the
+ * operators above; the states have the layout of the state layer's, [K, P] per head.
+ *   - A is <= 0 and d >= 0 (not checked); any decay is exact to rounding.
+ *   - bf16 inputs are multiplied exactly and summed in fp32; fp32 inputs as sums
+ *     of three bf16 parts, to 2^-24 of a product.
+ *   - Inputs are finite.  A non-finite value stays in its own sequence; it may reach
+ *     outputs up to 63 tokens before it.
+ * ------------------------------------------------------------------------- */
+typedef struct {
+    int32_t num_seqs;      /* N */
+    int32_t heads;         /* H: 1 to 65536 */
+    int64_t total_tokens;  /* T (steps: T == N) */
+    int32_t groups;        /* G: divides H */
+    int32_t state;         /* K: 1 to 256 */
+    int32_t width;         /* P: 1 to 8192 */
+    int32_t dtype;         /* kda_dtype_t of x, B, C, y, dy and their derivatives; everything else: float32 */
+    int32_t softplus;      /* 1: d = softplus(dt + dt_bias); 0: d = dt + dt_bias */
+    int32_t reserved;      /* 0 */
+    int64_t x_stride, dt_stride, b_stride, c_stride, dy_stride;  /* token strides of the inputs, 0 = contiguous */
+} kda_ssm_dims_t;
+
+/*
+ *   x          [T, H, P] dtype;  B, C [T, G, K] dtype;  dt [T, H] float32
+ *   A          [H] float32;  D [H] float32, or NULL for zeros;  dt_bias [H] float32, or NULL for zeros
+ *   h0         [N, H, K, P] float32 initial states, or NULL for zeros
+ *   cu_seqlens as for kda_chunk_fwd (NULL: N sequences of T / N tokens)
+ *   y          [T, H, P] dtype
+ *   h_T        [N, H, K, P] float32 final states, or NULL to skip (an empty sequence's is its h0); not h0
+ *   workspace  kda_ssm_workspace_size bytes (0: may be NULL).  Calls that share a workspace
+ *              must be ordered on one stream.
+ * Refused, as larger than one launch: more than 2^24 workgroups, which takes more than ten
+ * million sequences or chunks of tokens.
+ */
+KDA_API int kda_ssm_fwd(const kda_ssm_dims_t* dims, const void* x, const float* dt, const float* A, const void* B,
+                        const void* C, const float* D, const float* dt_bias, const float* h0,
+                        const int32_t* cu_seqlens, void* y, float* h_T, void* workspace, size_t workspace_bytes,
+                        void* stream);
+
+/*
+ * Gradient of kda_ssm_fwd for upstream derivatives dy [T, H, P] dtype and dh_T
+ * [N, H, K, P] float32 (NULL for zeros).  The forward inputs are passed again; its states are
+ * computed again.
+ *   dx [T, H, P], dB and dC [T, G, K] (summed over the group's heads): dtype
+ *   ddt [T, H] float32, the derivative of the raw dt
+ *   dA, dD, ddt_bias [H] float32 (each NULL to skip);  dh0 [N, H, K, P] float32 (NULL to skip)
+ */
+KDA_API int kda_ssm_bwd(const kda_ssm_dims_t* dims, const void* x, const float* dt, const float* A, const void* B,
+                        const void* C, const float* D, const float* dt_bias, const float* h0,
+                        const int32_t* cu_seqlens, const void* dy, const float* dh_T, void* dx, float* ddt, float* dA,
+                        void* dB, void* dC, float* dD, float* ddt_bias, float* dh0, void* workspace,
+                        size_t workspace_bytes, void* stream);
+
+/* Workspace of kda_ssm_fwd (backward = 0) or kda_ssm_bwd (1). */
+KDA_API int kda_ssm_workspace_size(const kda_ssm_dims_t* dims, int backward, size_t* bytes);
+
+/* One token per sequence: y [N, H, P] and the state after it, from x [N, H, P], B, C [N, G, K], dt [N, H]
+ * and h_in [N, H, K, P]; h_out may equal h_in. */
+KDA_API int kda_ssm_step(const kda_ssm_dims_t* dims, const void* x, const float* dt, const float* A, const void* B,
+                         const void* C, const float* D, const float* dt_bias, const float* h_in, float* h_out, void* y,
+                         void* stream);
+
+/*
+ * The same behind the layer's short convolution: xbc [N, H P + 2 G K] dtype holds the
+ * projections of x, B and C, whose convolution (kda_conv_step's, with conv_width taps and
+ * conv_activation) is not rounded before the scan takes it.  conv_weight [channels, conv_width]
+ * and conv_bias [channels] float32 (NULL for zeros); conv_state_in and conv_state_out
+ * [N, conv_width - 1, channels] dtype, which may be equal.  dims' b_stride and c_stride are not
+ * read; x_stride is xbc's.
+ */
+KDA_API int kda_ssm_conv_step(const kda_ssm_dims_t* dims, int conv_width, int conv_activation, const void* xbc,
+                              const float* conv_weight, const float* conv_bias, const void* conv_state_in,
+                              void* conv_state_out, const float* dt, const float* A, const float* D,
+                              const float* dt_bias, const float* h_in, float* h_out, void* y, void* workspace,
+                              size_t workspace_bytes, void* stream);
+KDA_API int kda_ssm_conv_step_workspace_size(const kda_ssm_dims_t* dims, size_t* bytes);
+
+/* -------------------------------------------------------------------------
+ * State cache: recurrent states (of the state layer, its snapshots or the state space scan)
+ * kept in 8 bits.  A state is `rows` rows of `width` float32 values.  A row has one scale,
+ * max |x| times 1/127 (int8) or 1/448 (e4m3), that factor and the product rounded to float32,
+ * and its codes are the nearest of the format's values to the exact quotients x / scale, ties to
+ * even.  A row of zeros (or one so small
+ * that its scale is zero) has scale and codes zero; a row with an infinity or a NaN reads
+ * back as NaN.
+ * ------------------------------------------------------------------------- */
+typedef enum { KDA_CACHE_I8 = 0, KDA_CACHE_E4M3 = 1 } kda_cache_format_t;
+
+typedef struct {
+    int32_t states;    /* R: states of the call, up to 8388607 */
+    int32_t slots;     /* S: slots of the cache */
+    int64_t rows;      /* rows of a state (for [H, K, P]: H K), up to 2^40 */
+    int32_t width;     /* values of a row: 1 to 8192 */
+    int32_t format;    /* kda_cache_format_t */
+    int32_t reserved;  /* 0 */
+} kda_state_cache_dims_t;
+
+/*
+ *   states  [R, rows, width] float32
+ *   slots   [R] int32 on the device, or NULL for slot r of state r (R <= S then).  A slot
+ *           outside [0, S) is skipped; where two states have one slot, the later stays.
+ *   codes   [S, rows, width] 8-bit;  scales [S, rows] float32.  Other slots are left as they were.
+ */
+KDA_API int kda_state_cache_write(const kda_state_cache_dims_t* dims, const float* states, const int32_t* slots,
+                                  void* codes, float* scales, void* stream);
+
+/* states[r] = code x scale of slot slots[r]; zeros where the slot is outside [0, S). */
+KDA_API int kda_state_cache_read(const kda_state_cache_dims_t* dims, const void* codes, const float* scales,
+                                 const int32_t* slots, float* states, void* stream);
+
+/* -------------------------------------------------------------------------
+ * Gated half of a feed-forward block: both projections, the activation and their product,
+ *     g = x Wg^T,  u = x Wu^T,  h = act(g) u,
+ * and its gradient.  Sums are fp32.  bf16 inputs are multiplied exactly; dg and du (the
+ * derivatives of g and u) are rounded to bf16 before the products that take them.  float32 inputs
+ * are multiplied as sums of three bf16 parts, to 2^-24 of a product.
+ * ------------------------------------------------------------------------- */
+typedef struct {
+    int64_t tokens;      /* T: 0 to 2147418112 */
+    int32_t width;       /* D: 1 to 1048576 */
+    int32_t hidden;      /* F: 1 to 1048576 */
+    int32_t dtype;       /* kda_dtype_t of x, the weights, h, dh and their derivatives */
+    int32_t activation;  /* KDA_ACT_SILU, KDA_ACT_SIGMOID or KDA_ACT_GELU */
+    int64_t x_stride, dh_stride;  /* token strides of the inputs, 0 = D and F */
+} kda_glu_dims_t;
+
+/*
+ *   x               [T, D] dtype
+ *   w_gate, w_up    [F, D] dtype (two halves of one [2 F, D] tensor, or tensors of their own)
+ *   h               [T, F] dtype
+ *   saved           [2, T, F] float32, or NULL: g and u, for kda_glu_bwd
+ *   workspace       kda_glu_workspace_size bytes (0: may be NULL); calls that share one must be
+ *                   ordered on one stream
+ * More than 64 tokens are read in place where x and the weights are bf16 at 16-byte addresses and
+ * strides, with D a multiple of 64; other inputs are copied into the workspace first.
+ */
+KDA_API int kda_glu_fwd(const kda_glu_dims_t* dims, const void* x, const void* w_gate, const void* w_up, void* h,
+                        float* saved, void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * Gradient of kda_glu_fwd for dh [T, F]: dx [T, D] (NULL to skip), dw_gate and dw_up [F, D], all dtype.
+ * saved: as kda_glu_fwd wrote it for the same inputs, or NULL to compute g and u again.
+ */
+KDA_API int kda_glu_bwd(const kda_glu_dims_t* dims, const void* x, const void* w_gate, const void* w_up,
+                        const float* saved, const void* dh, void* dx, void* dw_gate, void* dw_up, void* workspace,
+                        size_t workspace_bytes, void* stream);
+
+/* Workspace of kda_glu_fwd (backward = 0) or kda_glu_bwd (1; enough with and without dx and saved) for
+ * these inputs, whose addresses are looked at and whose values are not. */
+KDA_API int kda_glu_workspace_size(const kda_glu_dims_t* dims, const void* x, const void* w_gate, const void* w_up,
+                                   int backward, size_t* bytes);
 
 /* Static text for a status code. */
 KDA_API const char* kda_status_string(int status);

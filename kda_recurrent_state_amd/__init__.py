@@ -137,7 +137,8 @@ def load_library(build_if_missing: bool = True):
             lib.kda_last_error.restype = ctypes.c_char_p
             lib.kda_last_error.argtypes = []
             lib.kda_version.restype = ctypes.c_int
-            block._declare(lib)
+            for part in (block, statespace, state_cache, feedforward):
+                part._declare(lib)
             _lib = lib
         return _lib
 
@@ -549,3 +550,12 @@ from . import block  # noqa: E402
 from .block import *  # noqa: E402,F401,F403
 
 __all__ += block.__all__
+# the selective state space scan
+from . import statespace  # noqa: E402
+from .statespace import *  # noqa: E402,F401,F403
+# states kept in 8 bits
+from . import state_cache  # noqa: E402
+from .state_cache import *  # noqa: E402,F401,F403
+# the gated half of a feed-forward block
+from . import feedforward  # noqa: E402
+from .feedforward import *  # noqa: E402,F401,F403

@@ -16,7 +16,9 @@ CSRC = os.path.join(HERE, "csrc")
 BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libkda.so")
 SOURCES = ["kda_api.cpp", "kda_decode.hip", "kda_chunk.hip", "kda_prep.hip", "kda_prep2.hip", "kda_scan.hip",
-           "kda_bwd.hip", "kda_bwd_pro.hip", "kda_block_api.cpp", "kda_norm.hip", "kda_conv.hip", "kda_linscan.hip"]
+           "kda_bwd.hip", "kda_bwd_pro.hip", "kda_block_api.cpp", "kda_norm.hip", "kda_conv.hip", "kda_linscan.hip",
+           "kda_ssm_api.cpp", "kda_ssm.hip", "kda_state_cache_api.cpp", "kda_state_cache.hip",
+           "kda_glu_api.cpp", "kda_glu.hip"]
 ARCH = "gfx950"
 FLAGS = ["-O3", "-std=c++17", "-fPIC", f"--offload-arch={ARCH}", "-ffp-contract=fast",
          "-Xclang", "-target-feature", "-Xclang", "-packed-fp32-ops",
@@ -28,7 +30,9 @@ FLAGS = ["-O3", "-std=c++17", "-fPIC", f"--offload-arch={ARCH}", "-ffp-contract=
 EXTRA = {"kda_scan.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form"],
          # the gradient pass holds a state and its derivative per wavefront; in this
          # form it fits without spilling to scratch memory at dk = dv = 128
-         "kda_bwd.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form"]}
+         "kda_bwd.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form"],
+         # the same for a state block that is split into parts every chunk
+         "kda_ssm.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form"]}
 
 
 def _hipcc() -> str:

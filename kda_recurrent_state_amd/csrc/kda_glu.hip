@@ -1,0 +1,751 @@
+// kda_glu.hip -- the gated half of a feed-forward block and its gradient:
+//   g = x Wg^T, u = x Wu^T, h = act(g) u                         (x [T, D], W [F, D])
+//   dg = dh u act'(g), du = dh act(g), dx = dg Wg + du Wu, dWg = dg^T x, dWu = du^T x.
+// Three products of matrices on the matrix cores, with what surrounds them in their epilogues.
+//
+// bf16 operands are read where they lie.  fp32 operands are first split into three bf16 planes whose sum they
+// are (24 bits), and the product runs over the six pairs of planes above 2^-24, smallest first, into
+// the same accumulators: about four times the rate that fp32 matrix instructions would have.
+#include "kda_glu.hpp"
+
+#include "kda_rows.hpp"
+
+namespace kda {
+namespace {
+
+typedef short s16x4 __attribute__((ext_vector_type(4)));
+
+// ---------------------------------------------------------------- activations
+
+// act(z) and its slope.  sigmoid(-z) is formed by itself: 1 - sigmoid(z) would lose it for large z.
+template <int ACT> __device__ __forceinline__ void activation(float z, float& a, float& slope) {
+    if constexpr (ACT == GLU_GELU) {
+        const float cdf = 0.5f * erfcf(-0.70710678118654752f * z);
+        a = z * cdf;
+        slope = cdf + z * 0.39894228040143268f * __expf(-0.5f * z * z);
+    } else {
+        const float e = __expf(-fabsf(z)), big = __builtin_amdgcn_rcpf(1.f + e), small = e * big;
+        const float s = z >= 0.f ? big : small, sn = z >= 0.f ? small : big;
+        if constexpr (ACT == GLU_SILU) {
+            a = z * s;
+            slope = s * (1.f + z * sn);
+        } else {
+            a = s;
+            slope = s * sn;
+        }
+    }
+}
+template <int ACT> __device__ __forceinline__ float gated(float g, float u) {
+    float a, slope;
+    activation<ACT>(g, a, slope);
+    return a * u;
+}
+
+// ---------------------------------------------------------------- tiled product
+//
+// out[m][n] = sum over segments s and k of A_s[m][k] B_s[n][k].  An operand is either stored with k
+// contiguous (KR false: [rows][k]) or with k along the rows (KR true: [k][rows]); k is a multiple of 64 in the
+// first form, and there are a multiple of 64 columns in the second.  Rows past the last are the last again, and their
+// results are not stored; k rows past the last meet zeros of the other operand.
+
+constexpr int BK = 64;
+constexpr int MAX_SEGS = 12;
+
+struct Segment { const bf16 *a, *b, *b2; };
+struct GemmArgs {
+    Segment seg[MAX_SEGS];
+    int64_t lda, ldb;          // elements between rows
+    int64_t M, N;              // rows of A and B (of each of the two B where there are two)
+    int64_t kA, kB, colsA, colsB;  // k rows that exist, and their columns, a multiple of 64 (KR)
+    int32_t segs, ksteps;      // steps of BK in a segment
+    int32_t mt, nt, split;     // tiles, shares of the sum
+    int32_t halves;            // outputs: seg[0..segs) and seg[segs..2 segs)
+    // epilogue
+    void* out;
+    void* out2;
+    float* part;
+    const void* dh;
+    float* saved;
+    bf16 *dg, *du;
+    int64_t ldo, hs, plane, T, Tpad;
+    int32_t F, Fpad;
+};
+
+template <bool KR> struct Operand;
+// [rows][k]: a row of 64 k is 128 bytes in LDS, its 16-byte pieces exchanged by the row's number so that 8
+// neighbouring rows' pieces of the same k lie in different banks.
+template <> struct Operand<false> {
+    template <int ROWS, int THREADS> static constexpr int loads() { return ROWS * 8 / THREADS; }
+    static __device__ __forceinline__ int source(int at, int64_t rows_left, int64_t ld, int) {
+        const int row = at / 8, piece = (at & 7) ^ (row & 7);
+        const int64_t r = row < rows_left ? row : rows_left - 1;
+        return (int)(r * ld * 2) + piece * 16;
+    }
+    static __device__ __forceinline__ bf16x8 frag(const char* tile, int row0, int ks, int lane, int) {
+        const int row = row0 + (lane & 15), piece = (ks * 4 + (lane >> 4)) ^ (row & 7);
+        return *reinterpret_cast<const bf16x8*>(tile + row * 128 + piece * 16);
+    }
+};
+// [k][rows]: a k row of R columns is 2 R bytes, its 32-byte pieces (16 columns) exchanged so that the 8 k rows that
+// half a wavefront reads at once lie in different banks.
+template <> struct Operand<true> {
+    template <int ROWS, int THREADS> static constexpr int loads() { return ROWS * 8 / THREADS; }
+    static __device__ __forceinline__ int turn(int k) { return (k & 3) | ((k >> 3) & 1) << 2; }
+    static __device__ __forceinline__ int source(int at, int64_t rows_left, int64_t ld, int rows) {
+        const int per = rows / 8, k = at / per, slot = at % per;
+        const int c = ((((slot >> 1) ^ turn(k)) << 1) | (slot & 1)) * 8;
+        const int64_t col = c + 8 <= rows_left ? c : rows_left - 8;
+        return (int)(k * ld * 2 + col * 2);
+    }
+    static __device__ __forceinline__ bf16x8 frag(const char* tile, int row0, int ks, int lane, int rows) {
+        typedef __attribute__((address_space(3))) s16x4* lds;
+        const int i = lane & 15, q = lane >> 4, k = ks * 32 + 8 * q + (i >> 2);
+        const char* p = tile + k * rows * 2 + (((row0 >> 4) ^ turn(k)) * 32) + (i & 3) * 8;
+        const bf16x4 lo = __builtin_bit_cast(bf16x4, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds)(p)));
+        const bf16x4 hi = __builtin_bit_cast(bf16x4, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds)(p + 4 * rows * 2)));
+        return __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
+    }
+};
+
+__device__ __forceinline__ void copy16(const char* base, int offset, char* lds) {
+    __builtin_amdgcn_global_load_lds((const void*)(base + offset), (__attribute__((address_space(3))) void*)lds, 16, 0, 0);
+}
+
+// The copies issued by this wavefront are done but for the last LEFT, and so are those of every other
+// wavefront of the workgroup, and their reads of LDS.
+template <int LEFT> __device__ __forceinline__ void wait_copies() {
+    static_assert(LEFT < 64, "the counter's range");
+    asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"(LEFT) : "memory");
+}
+
+// Epilogues: 4 neighbouring columns n .. n + 3 of row m, stored where they exist.
+template <typename T> __device__ __forceinline__ void store_row(T* row, int64_t n, int64_t N, f32x4 v) {
+    float f[4] = {v[0], v[1], v[2], v[3]};
+    if (n + 4 <= N) store_v<4>(row + n, f);
+    else
+        for (int i = 0; i < 4; ++i)
+            if (n + i < N) row[n + i] = from_f32<T>(f[i]);
+}
+// dg and du go to planes of [Tpad][Fpad], zero where a token or column does not exist.
+template <int NP> __device__ __forceinline__ void store_planes(bf16* p, int64_t plane, float (&v)[4]) {
+#pragma unroll
+    for (int n = 0; n < NP; ++n) {
+        bf16x4 b;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            b[i] = (bf16)v[i];
+            v[i] -= (float)b[i];
+        }
+        *reinterpret_cast<bf16x4*>(p + n * plane) = b;
+    }
+}
+template <typename DT, int ACT>
+__device__ __forceinline__ void store_dgu(const GemmArgs& g, int64_t t, int64_t f, const float (&gv)[4], const float (&uv)[4]) {
+    if (t >= g.Tpad || f >= g.Fpad) return;
+    float dg[4], du[4];
+    zero_v(dg);
+    zero_v(du);
+    if (t < g.T && f < g.F) {
+        float d[4];
+        zero_v(d);
+        const DT* row = (const DT*)g.dh + t * g.hs;
+        if (f + 4 <= g.F) get_v(load_v<4>(row + f), d);
+        else
+            for (int i = 0; i < 4; ++i)
+                if (f + i < g.F) d[i] = to_f32(row[f + i]);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            float a, slope;
+            activation<ACT>(gv[i], a, slope);
+            const bool in = f + i < g.F;
+            dg[i] = in ? d[i] * uv[i] * slope : 0.f;
+            du[i] = in ? d[i] * a : 0.f;
+        }
+    }
+    constexpr int NP = sizeof(DT) == 2 ? 1 : 3;
+    store_planes<NP>(g.dg + t * g.Fpad + f, g.plane, dg);
+    store_planes<NP>(g.du + t * g.Fpad + f, g.plane, du);
+}
+
+enum { EPI_OUT, EPI_H, EPI_DGU };
+
+// BM x BN results a workgroup of WM x WN wavefronts, STAGES tiles of both operands in LDS: while one is
+// multiplied the next ones arrive.  With two B (EPI_H, EPI_DGU) the first half of BN is of one and
+// the second of the other, so that a lane holds both results of a column.
+template <typename DT, int BM, int BN, int WM, int WN, int STAGES, bool AKR, bool BKR, int EPI, int ACT>
+__global__ void __launch_bounds__(WM* WN * 64, WM* WN / 4) glu_gemm_kernel(GemmArgs g) {
+    constexpr bool DUAL = EPI != EPI_OUT;
+    constexpr int THREADS = WM * WN * 64, TM = BM / WM / 16, TN = BN / WN / 16;
+    constexpr int LA = BM * 8 / THREADS, LB = BN * 8 / THREADS, STAGE = (BM + BN) * BK * 2;
+    constexpr int BH = DUAL ? BN / 2 : BN;  // columns of one B in a tile
+    extern __shared__ __attribute__((aligned(1024))) char smem[];
+    const int tid = threadIdx.x, lane = tid % 64, wave = __builtin_amdgcn_readfirstlane(tid / 64);
+    const int wm = wave / WN, wn = wave % WN;
+
+    // Every eighth workgroup runs on the same die: a die takes a run of neighbouring tiles, which share
+    // operands in its cache, in strips of 8 tiles along m.
+    int64_t b = blockIdx.x;
+    const int64_t tiles = (int64_t)g.mt * g.nt, total = tiles * g.split * g.halves;
+    {
+        const int64_t per = (total + 7) / 8;
+        b = (b & 7) * per + (b >> 3);
+        if ((int64_t)(blockIdx.x >> 3) >= per || b >= total) return;
+    }
+    const int share = (int)(b / tiles % g.split), half = (int)(b / tiles / g.split);
+    const int64_t tile = b % tiles;
+    const int64_t strip = tile / (8 * g.nt), in = tile % (8 * g.nt);
+    const int tall = (int)(g.mt - strip * 8 < 8 ? g.mt - strip * 8 : 8);
+    const int64_t m0 = (strip * 8 + in % tall) * BM, n0 = in / tall * BH;
+
+    int offa[LA], offb[LB];
+#pragma unroll
+    for (int i = 0; i < LA; ++i) offa[i] = Operand<AKR>::source(i * THREADS + tid, (AKR ? g.colsA : g.M) - m0, g.lda, BM);
+#pragma unroll
+    for (int i = 0; i < LB; ++i) {
+        const int at = i * THREADS + tid;
+        if (DUAL) offb[i] = Operand<false>::source(at % (BH * 8), g.N - n0, g.ldb, BH);
+        else offb[i] = Operand<BKR>::source(at, (BKR ? g.colsB : g.N) - n0, g.ldb, BN);
+    }
+    const int all = g.segs * g.ksteps, k0 = (int)((int64_t)share * all / g.split), k1 = (int)((int64_t)(share + 1) * all / g.split);
+
+    auto fetch = [&](int step) {
+        const int s = step / g.ksteps, kk = step % g.ksteps;
+        const Segment sg = g.seg[half * g.segs + s];
+        char* at = smem + step % STAGES * STAGE + wave * 1024;
+        const char* pa = (const char*)(sg.a + (AKR ? (int64_t)kk * BK * g.lda + m0 : m0 * g.lda + (int64_t)kk * BK));
+        const char* pb = (const char*)(sg.b + (BKR ? (int64_t)kk * BK * g.ldb + n0 : n0 * g.ldb + (int64_t)kk * BK));
+        const int la = AKR ? (int)(g.kA - (int64_t)kk * BK) : BK, lb = BKR ? (int)(g.kB - (int64_t)kk * BK) : BK;
+#pragma unroll
+        for (int i = 0; i < LA; ++i) {
+            int o = offa[i];
+            if (AKR && la < BK) {
+                const int k = (i * THREADS + tid) / (BM / 8);
+                if (k >= la) o -= (int)((k - la + 1) * g.lda * 2);
+            }
+            copy16(pa, o, at + i * THREADS * 16);
+        }
+        const char* pb2 = DUAL ? (const char*)(sg.b2 + n0 * g.ldb + (int64_t)kk * BK) : pb;
+#pragma unroll
+        for (int i = 0; i < LB; ++i) {
+            int o = offb[i];
+            if (BKR && lb < BK) {
+                const int k = (i * THREADS + tid) / (BN / 8);
+                if (k >= lb) o -= (int)((k - lb + 1) * g.ldb * 2);
+            }
+            copy16(DUAL && i * THREADS >= BH * 8 ? pb2 : pb, o, at + BM * BK * 2 + i * THREADS * 16);
+        }
+    };
+
+    f32x4 acc[TM][TN];
+#pragma unroll
+    for (int i = 0; i < TM; ++i)
+#pragma unroll
+        for (int j = 0; j < TN; ++j) acc[i][j] = zero4();
+
+    constexpr int AHEAD = STAGES - 1;
+#pragma unroll
+    for (int s = 0; s < AHEAD; ++s)
+        if (k0 + s < k1) fetch(k0 + s);
+    for (int k = k0; k < k1; ++k) {
+        // the copies of step k have arrived (up to AHEAD - 1 later steps may be on their way), and every
+        // wavefront has read step k - 1, whose place the next copies take
+        constexpr int LEFT = (AHEAD - 1) * (LA + LB);
+        if (k + AHEAD - 1 < k1) wait_copies<LEFT>(); else wait_copies<0>();
+        if (k + AHEAD < k1) fetch(k + AHEAD);
+        const char* ta = smem + k % STAGES * STAGE;
+        const char* tb = ta + BM * BK * 2;
+#pragma unroll
+        for (int ks = 0; ks < 2; ++ks) {
+            bf16x8 fb[TN], fa[TM];
+#pragma unroll
+            for (int j = 0; j < TN; ++j) {
+                const int row = DUAL ? (j >= TN / 2 ? BH : 0) + wn * (BH / WN) + j % (TN / 2) * 16 : wn * (BN / WN) + j * 16;
+                fb[j] = Operand<BKR>::frag(tb, row, ks, lane, BN);
+            }
+#pragma unroll
+            for (int i = 0; i < TM; ++i) fa[i] = Operand<AKR>::frag(ta, wm * (BM / WM) + i * 16, ks, lane, BM);
+#pragma unroll
+            for (int i = 0; i < TM; ++i)
+#pragma unroll
+                for (int j = 0; j < TN; ++j)
+                    acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(fb[j], fa[i], acc[i][j], 0, 0, 0);
+        }
+    }
+
+    // a lane holds columns 4 (lane / 16) .. + 3 of row lane % 16 of each 16 x 16 tile
+#pragma unroll
+    for (int i = 0; i < TM; ++i) {
+        const int64_t m = m0 + wm * (BM / WM) + i * 16 + (lane & 15);
+        if constexpr (DUAL) {
+#pragma unroll
+            for (int j = 0; j < TN / 2; ++j) {
+                const int64_t n = n0 + wn * (BH / WN) + j * 16 + 4 * (lane >> 4);
+                const f32x4 gv = acc[i][j], uv = acc[i][j + TN / 2];
+                if constexpr (EPI == EPI_H) {
+                    if (m < g.M && n < g.N) {
+                        f32x4 h;
+#pragma unroll
+                        for (int r = 0; r < 4; ++r) h[r] = gated<ACT>(gv[r], uv[r]);
+                        store_row((DT*)g.out + m * g.N, n, g.N, h);
+                        if (g.saved) {
+                            store_row(g.saved + m * g.N, n, g.N, gv);
+                            store_row(g.saved + (g.T + m) * g.N, n, g.N, uv);
+                        }
+                    }
+                } else {
+                    const float ga[4] = {gv[0], gv[1], gv[2], gv[3]}, ua[4] = {uv[0], uv[1], uv[2], uv[3]};
+                    store_dgu<DT, ACT>(g, m, n, ga, ua);
+                }
+            }
+        } else {
+#pragma unroll
+            for (int j = 0; j < TN; ++j) {
+                const int64_t n = n0 + wn * (BN / WN) + j * 16 + 4 * (lane >> 4);
+                if (m >= g.M || n >= g.N) continue;
+                if (g.split > 1) store_row(g.part + ((int64_t)(half * g.split + share) * g.M + m) * g.N, n, g.N, acc[i][j]);
+                else store_row((DT*)(half ? g.out2 : g.out) + m * g.N, n, g.N, acc[i][j]);
+            }
+        }
+    }
+}
+
+// out = sum of the shares, in order.
+template <typename DT> __global__ void __launch_bounds__(256) glu_shares_kernel(const float* part, int split, int64_t n, DT* out) {
+    for (int64_t i = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 4; i < n; i += (int64_t)gridDim.x * 1024) {
+        if (i + 4 <= n) {
+            f32x4 s = zero4();
+            for (int k = 0; k < split; ++k) {
+                const Pack<float, 4> p = load_v<4>(part + k * n + i);
+#pragma unroll
+                for (int r = 0; r < 4; ++r) s[r] += p[r];
+            }
+            float f[4] = {s[0], s[1], s[2], s[3]};
+            store_v<4>(out + i, f);
+        } else {
+            for (int64_t j = i; j < n; ++j) {
+                float s = 0.f;
+                for (int k = 0; k < split; ++k) s += part[k * n + j];
+                out[j] = from_f32<DT>(s);
+            }
+        }
+    }
+}
+
+// [rows][cols] as NP planes of [rows][pad] bf16, zero past the columns.
+template <typename DT, int NP>
+__global__ void __launch_bounds__(256) glu_pack_kernel(const DT* src, int64_t stride, int64_t rows, int cols, int pad,
+                                                       int64_t plane, bf16* dst) {
+    const int per = pad / 4;
+    for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < rows * per; i += (int64_t)gridDim.x * 256) {
+        const int64_t r = i / per;
+        const int c = (int)(i % per) * 4;
+        float v[4];
+        zero_v(v);
+        if (c + 4 <= cols) get_v(load_v<4>(src + r * stride + c), v);
+        else
+            for (int k = 0; k < 4; ++k)
+                if (c + k < cols) v[k] = to_f32(src[r * stride + c + k]);
+        store_planes<NP>(dst + r * pad + c, plane, v);
+    }
+}
+
+// dg and du from the products that the forward kept.
+template <typename DT, int ACT> __global__ void __launch_bounds__(256) glu_saved_kernel(GemmArgs g) {
+    const int per = g.Fpad / 4;
+    for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < g.Tpad * per; i += (int64_t)gridDim.x * 256) {
+        const int64_t t = i / per;
+        const int f = (int)(i % per) * 4;
+        float gv[4], uv[4];
+        zero_v(gv);
+        zero_v(uv);
+        if (t < g.T && f < g.F) {
+            const float *pg = g.saved + t * g.F + f, *pu = g.saved + (g.T + t) * g.F + f;
+            if (f + 4 <= g.F) {
+                get_v(load_nt<4>(pg), gv);
+                get_v(load_nt<4>(pu), uv);
+            } else {
+                for (int k = 0; k < 4; ++k)
+                    if (f + k < g.F) {
+                        gv[k] = pg[k];
+                        uv[k] = pu[k];
+                    }
+            }
+        }
+        store_dgu<DT, ACT>(g, t, f, gv, uv);
+    }
+}
+
+// ---------------------------------------------------------------- few tokens
+//
+// Up to 64 tokens: the weights are what there is to read.  A workgroup takes 16 columns of both
+// weights, its wavefronts a part of the sum each; weights come straight from memory into the operand's
+// registers, x from the cache.
+template <typename DT> struct Direct;
+template <> struct Direct<bf16> {
+    static constexpr int NP = 1;
+    static __device__ __forceinline__ void split(const Pack<bf16, 8>& p, bf16x8 (&o)[1]) { o[0] = p.part[0]; }
+};
+template <> struct Direct<float> {
+    static constexpr int NP = 3;
+    static __device__ __forceinline__ void split(const Pack<float, 8>& p, bf16x8 (&o)[3]) {
+        float v[8];
+        get_v(p, v);
+#pragma unroll
+        for (int n = 0; n < 3; ++n)
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                o[n][i] = (bf16)v[i];
+                v[i] -= (float)o[n][i];
+            }
+    }
+};
+
+template <typename DT, int TT, int ACT>
+__global__ void __launch_bounds__(256) glu_few_kernel(GluArgs a) {
+    constexpr int NP = Direct<DT>::NP, U = sizeof(DT) == 2 ? (TT > 2 ? 4 : 8) : 2;
+    const int lane = threadIdx.x % 64, wave = threadIdx.x / 64, l15 = lane & 15, q = lane >> 4;
+    const int f0 = blockIdx.x * 16, f = min(f0 + l15, a.F - 1);
+    const DT *wg = (const DT*)a.wg + (int64_t)f * a.D, *wu = (const DT*)a.wu + (int64_t)f * a.D;
+    const DT* xr[TT];
+#pragma unroll
+    for (int t = 0; t < TT; ++t) xr[t] = (const DT*)a.x + (int64_t)min((int64_t)(t * 16 + l15), a.T - 1) * a.xs;
+    f32x4 ag[TT], au[TT];
+#pragma unroll
+    for (int t = 0; t < TT; ++t) ag[t] = au[t] = zero4();
+    const int steps = (a.D + 31) / 32, s0 = steps * wave / 4, s1 = steps * (wave + 1) / 4;
+    auto get = [&](const DT* row, int k) {
+        if (k + 8 <= a.D) return load_v<8>(row + k);
+        Pack<DT, 8> p;
+        for (int i = 0; i < 8; ++i)
+            p.part[i / Pack<DT, 8>::N][i % Pack<DT, 8>::N] = k + i < a.D ? row[k + i] : from_f32<DT>(0.f);
+        return p;
+    };
+    for (int s = s0; s < s1; s += U) {
+        Pack<DT, 8> pg[U], pu[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int k = min(s + u, s1 - 1) * 32 + 8 * q;
+            pg[u] = get(wg, k);
+            pu[u] = get(wu, k);
+        }
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            if (s + u >= s1) break;
+            bf16x8 g[NP], w[NP];
+            Direct<DT>::split(pg[u], g);
+            Direct<DT>::split(pu[u], w);
+#pragma unroll
+            for (int t = 0; t < TT; ++t) {
+                bf16x8 x[NP];
+                Direct<DT>::split(get(xr[t], (s + u) * 32 + 8 * q), x);
+#pragma unroll
+                for (int i = 0; i < NP; ++i)
+#pragma unroll
+                    for (int j = 0; j < NP; ++j)
+                        if (i + j <= 2) {
+                            ag[t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(g[i], x[j], ag[t], 0, 0, 0);
+                            au[t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(w[i], x[j], au[t], 0, 0, 0);
+                        }
+            }
+        }
+    }
+    __shared__ f32x4 part[3][2][TT][64];
+    if (wave > 0) {
+#pragma unroll
+        for (int t = 0; t < TT; ++t) {
+            part[wave - 1][0][t][lane] = ag[t];
+            part[wave - 1][1][t][lane] = au[t];
+        }
+    }
+    __syncthreads();
+    if (wave > 0) return;
+#pragma unroll
+    for (int t = 0; t < TT; ++t) {
+#pragma unroll
+        for (int w = 0; w < 3; ++w) {
+            ag[t] += part[w][0][t][lane];
+            au[t] += part[w][1][t][lane];
+        }
+        const int64_t m = t * 16 + l15;
+        const int n = f0 + 4 * q;
+        if (m >= a.T || n >= a.F) continue;
+        f32x4 h;
+#pragma unroll
+        for (int r = 0; r < 4; ++r) h[r] = gated<ACT>(ag[t][r], au[t][r]);
+        store_row((DT*)a.h + m * a.F, n, a.F, h);
+        if (a.saved) {
+            store_row(a.saved + m * a.F, n, a.F, ag[t]);
+            store_row(a.saved + (a.T + m) * a.F, n, a.F, au[t]);
+        }
+    }
+}
+
+// ---------------------------------------------------------------- launches
+
+int64_t up(int64_t x, int64_t to) { return (x + to - 1) / to * to; }
+size_t up256(int64_t x) { return (size_t)up(x, 256); }
+int planes(const GluArgs& a) { return a.dtype == 1 ? 1 : 3; }
+
+// The six pairs of planes above 2^-24, smallest first.
+constexpr int PAIRS[6][2] = {{1, 1}, {0, 2}, {2, 0}, {0, 1}, {1, 0}, {0, 0}};
+
+struct Mat { const bf16* p; int64_t ld, plane; };  // an operand, or its planes
+
+// Tile shape and shares of a product of M x N results over `steps` steps.
+struct Shape { bool big; int mt, nt, split; };
+Shape shape_of(int64_t M, int64_t N, bool dual, int halves, int steps, bool may_split) {
+    auto tiles = [&](int bm, int bn) {
+        return ((M + bm - 1) / bm) * ((N + (dual ? bn / 2 : bn) - 1) / (dual ? bn / 2 : bn)) * halves;
+    };
+    Shape s;
+    s.big = tiles(256, 256) >= 192;
+    const int bm = s.big ? 256 : 128, bn = bm;
+    s.mt = (int)((M + bm - 1) / bm);
+    s.nt = (int)((N + (dual ? bn / 2 : bn) - 1) / (dual ? bn / 2 : bn));
+    s.split = 1;
+    if (may_split && !s.big) {
+        const int64_t t = tiles(bm, bn) > 0 ? tiles(bm, bn) : 1, want = (512 + t - 1) / t, most = steps / 8 > 0 ? steps / 8 : 1;
+        s.split = (int)(want < most ? want : most);
+    }
+    return s;
+}
+
+template <typename DT, bool AKR, bool BKR, int EPI, int ACT>
+hipError_t run_gemm(GemmArgs g, const Shape& s, hipStream_t st) {
+    g.mt = s.mt;
+    g.nt = s.nt;
+    g.split = s.split;
+    const int64_t total = (int64_t)s.mt * s.nt * s.split * g.halves, blocks = (total + 7) / 8 * 8;
+    hipError_t e;
+    if (s.big) {
+        constexpr int lds = 2 * 512 * BK * 2;
+        auto* k = glu_gemm_kernel<DT, 256, 256, 2, 4, 2, AKR, BKR, EPI, ACT>;
+        e = hipFuncSetAttribute((const void*)k, hipFuncAttributeMaxDynamicSharedMemorySize, lds);
+        if (e != hipSuccess) return e;
+        hipLaunchKernelGGL(k, dim3((unsigned)blocks), dim3(512), lds, st, g);
+    } else {
+        constexpr int lds = 2 * 256 * BK * 2;
+        auto* k = glu_gemm_kernel<DT, 128, 128, 2, 2, 2, AKR, BKR, EPI, ACT>;
+        hipLaunchKernelGGL(k, dim3((unsigned)blocks), dim3(256), lds, st, g);
+    }
+    return hipGetLastError();
+}
+
+template <typename DT> hipError_t sum_shares(const float* part, int split, int64_t n, void* out, hipStream_t st) {
+    const int64_t blocks = (n / 4 + 256) / 256;
+    hipLaunchKernelGGL(glu_shares_kernel<DT>, dim3((unsigned)(blocks < 4096 ? blocks : 4096)), dim3(256), 0, st, part, split, n,
+                       (DT*)out);
+    return hipGetLastError();
+}
+
+template <typename DT>
+hipError_t pack(const void* src, int64_t stride, int64_t rows, int cols, int pad, bf16* dst, hipStream_t st) {
+    constexpr int NP = sizeof(DT) == 2 ? 1 : 3;
+    const int64_t blocks = (rows * (pad / 4) + 255) / 256;
+    hipLaunchKernelGGL((glu_pack_kernel<DT, NP>), dim3((unsigned)(blocks < 8192 ? blocks : 8192)), dim3(256), 0, st,
+                       (const DT*)src, stride, rows, cols, pad, rows * pad, dst);
+    return hipGetLastError();
+}
+
+#define GLU_TRY(call)                            \
+    do {                                         \
+        const hipError_t e_ = (call);            \
+        if (e_ != hipSuccess) return e_;         \
+    } while (0)
+
+// The workspace's arrays, in order.
+struct Work {
+    size_t size = 0;
+    bf16 *x = nullptr, *wg = nullptr, *wu = nullptr, *dg = nullptr, *du = nullptr;
+    float* part = nullptr;
+};
+int pad_of(const GluArgs& a) { return (int)up(a.D, BK); }
+Shape dx_shape(const GluArgs& a) {
+    const int np = planes(a);
+    return shape_of(a.T, a.D, false, 1, (int)(up(a.F, BK) / BK) * 2 * (np == 1 ? 1 : 6), true);
+}
+Shape dw_shape(const GluArgs& a) {
+    const int np = planes(a);
+    return shape_of(a.F, a.D, false, 2, (int)(up(a.T, BK) / BK) * (np == 1 ? 1 : 6), true);
+}
+Work work_of(const GluArgs& a, bool backward, bool input_grad, uint8_t* base) {
+    Work w;
+    auto take = [&](int64_t bytes) {
+        uint8_t* p = base + w.size;
+        w.size += up256(bytes);
+        return p;
+    };
+    const int64_t np = planes(a), pad = pad_of(a);
+    if (!backward && a.T <= GLU_FEW) return w;
+    if (!a.x_plain) w.x = (bf16*)take(a.T * pad * np * 2);
+    if (!a.w_plain) {
+        w.wg = (bf16*)take(a.F * pad * np * 2);
+        w.wu = (bf16*)take(a.F * pad * np * 2);
+    }
+    if (backward) {
+        const int64_t one = up(a.T, BK) * up(a.F, BK) * np * 2;
+        w.dg = (bf16*)take(one);
+        w.du = (bf16*)take(one);
+        const Shape sx = dx_shape(a), sw = dw_shape(a);
+        const int64_t px = input_grad && sx.split > 1 ? sx.split * a.T * a.D * 4 : 0;
+        const int64_t pw = sw.split > 1 ? 2ll * sw.split * a.F * a.D * 4 : 0;
+        if (px > 0 || pw > 0) w.part = (float*)take(px > pw ? px : pw);
+    }
+    return w;
+}
+
+struct Inputs { Mat x, wg, wu; };
+template <typename DT> hipError_t inputs(const GluArgs& a, const Work& w, Inputs* in, hipStream_t st) {
+    const int pad = pad_of(a);
+    in->x = a.x_plain ? Mat{(const bf16*)a.x, a.xs, 0} : Mat{w.x, pad, a.T * pad};
+    in->wg = a.w_plain ? Mat{(const bf16*)a.wg, a.D, 0} : Mat{w.wg, pad, (int64_t)a.F * pad};
+    in->wu = a.w_plain ? Mat{(const bf16*)a.wu, a.D, 0} : Mat{w.wu, pad, (int64_t)a.F * pad};
+    if (a.T == 0) return hipSuccess;
+    if (!a.x_plain) GLU_TRY((pack<DT>(a.x, a.xs, a.T, a.D, pad, w.x, st)));
+    if (!a.w_plain) {
+        GLU_TRY((pack<DT>(a.wg, a.D, a.F, a.D, pad, w.wg, st)));
+        GLU_TRY((pack<DT>(a.wu, a.D, a.F, a.D, pad, w.wu, st)));
+    }
+    return hipSuccess;
+}
+
+// x against both weights, with EPI
+template <typename DT, int EPI, int ACT> hipError_t products(const GluArgs& a, const Inputs& in, GemmArgs g, hipStream_t st) {
+    const int np = planes(a), n = np == 1 ? 1 : 6;
+    for (int i = 0; i < n; ++i) {
+        const int pa = np == 1 ? 0 : PAIRS[i][0], pb = np == 1 ? 0 : PAIRS[i][1];
+        g.seg[i] = {in.x.p + pa * in.x.plane, in.wg.p + pb * in.wg.plane, in.wu.p + pb * in.wu.plane};
+    }
+    g.segs = n;
+    g.ksteps = pad_of(a) / BK;
+    g.lda = in.x.ld;
+    g.ldb = in.wg.ld;
+    g.M = a.T;
+    g.N = a.F;
+    g.halves = 1;
+    return run_gemm<DT, false, false, EPI, ACT>(g, shape_of(a.T, a.F, true, 1, 0, false), st);
+}
+
+template <typename DT, int ACT> hipError_t few(const GluArgs& a, hipStream_t st) {
+    const dim3 grid((a.F + 15) / 16);
+    if (a.T <= 16) hipLaunchKernelGGL((glu_few_kernel<DT, 1, ACT>), grid, dim3(256), 0, st, a);
+    else if (a.T <= 32) hipLaunchKernelGGL((glu_few_kernel<DT, 2, ACT>), grid, dim3(256), 0, st, a);
+    else hipLaunchKernelGGL((glu_few_kernel<DT, 4, ACT>), grid, dim3(256), 0, st, a);
+    return hipGetLastError();
+}
+
+template <typename DT, int ACT> hipError_t forward(const GluArgs& a, hipStream_t st) {
+    if (a.T <= GLU_FEW) return few<DT, ACT>(a, st);
+    const Work w = work_of(a, false, false, a.ws);
+    Inputs in;
+    GLU_TRY((inputs<DT>(a, w, &in, st)));
+    GemmArgs g = {};
+    g.out = a.h;
+    g.saved = a.saved;
+    g.T = a.T;
+    return products<DT, EPI_H, ACT>(a, in, g, st);
+}
+
+template <typename DT, int ACT> hipError_t backward(const GluArgs& a, hipStream_t st) {
+    const Work w = work_of(a, true, a.dx != nullptr, a.ws);
+    Inputs in;
+    GLU_TRY((inputs<DT>(a, w, &in, st)));
+    const int np = planes(a), n = np == 1 ? 1 : 6;
+    GemmArgs g = {};
+    g.T = a.T;
+    g.Tpad = up(a.T, BK);
+    g.F = a.F;
+    g.Fpad = (int)up(a.F, BK);
+    g.plane = g.Tpad * g.Fpad;
+    g.dh = a.dh;
+    g.hs = a.hs;
+    g.dg = w.dg;
+    g.du = w.du;
+    g.saved = a.saved;
+    if (a.T == 0) {
+        // nothing but the weights' gradients, which are zero
+    } else if (a.saved) {
+        const int64_t blocks = (g.plane / 4 + 255) / 256;
+        hipLaunchKernelGGL((glu_saved_kernel<DT, ACT>), dim3((unsigned)(blocks < 16384 ? blocks : 16384)), dim3(256), 0, st, g);
+        GLU_TRY(hipGetLastError());
+    } else {
+        GLU_TRY((products<DT, EPI_DGU, ACT>(a, in, g, st)));
+    }
+    if (a.dx && a.T > 0) {
+        GemmArgs p = {};
+        for (int i = 0; i < n; ++i) {
+            const int pa = np == 1 ? 0 : PAIRS[i][0], pb = np == 1 ? 0 : PAIRS[i][1];
+            p.seg[2 * i] = {w.dg + pa * g.plane, in.wg.p + pb * in.wg.plane, nullptr};
+            p.seg[2 * i + 1] = {w.du + pa * g.plane, in.wu.p + pb * in.wu.plane, nullptr};
+        }
+        p.segs = 2 * n;
+        p.ksteps = g.Fpad / BK;
+        p.lda = g.Fpad;
+        p.ldb = in.wg.ld;
+        p.M = a.T;
+        p.N = a.D;
+            p.kB = a.F;
+        p.colsB = pad_of(a);
+        p.halves = 1;
+        p.out = a.dx;
+        p.part = w.part;
+        const Shape s = dx_shape(a);
+        GLU_TRY((run_gemm<DT, false, true, EPI_OUT, 0>(p, s, st)));
+        if (s.split > 1) GLU_TRY((sum_shares<DT>(w.part, s.split, a.T * a.D, a.dx, st)));
+    }
+    GemmArgs p = {};
+    for (int i = 0; i < n; ++i) {
+        const int pa = np == 1 ? 0 : PAIRS[i][0], pb = np == 1 ? 0 : PAIRS[i][1];
+        p.seg[i] = {w.dg + pa * g.plane, in.x.p + pb * in.x.plane, nullptr};
+        p.seg[n + i] = {w.du + pa * g.plane, in.x.p + pb * in.x.plane, nullptr};
+    }
+    p.segs = n;
+    p.ksteps = (int)(g.Tpad / BK);
+    p.lda = g.Fpad;
+    p.ldb = in.x.ld;
+    p.M = a.F;
+    p.N = a.D;
+    p.kA = g.Tpad;
+    p.kB = a.T;
+    p.colsA = g.Fpad;
+    p.colsB = pad_of(a);
+    p.halves = 2;
+    p.out = a.dwg;
+    p.out2 = a.dwu;
+    p.part = w.part;
+    const Shape s = dw_shape(a);
+    GLU_TRY((run_gemm<DT, true, true, EPI_OUT, 0>(p, s, st)));
+    if (s.split > 1) {
+        const int64_t one = (int64_t)a.F * a.D;
+        GLU_TRY((sum_shares<DT>(w.part, s.split, one, a.dwg, st)));
+        GLU_TRY((sum_shares<DT>(w.part + s.split * one, s.split, one, a.dwu, st)));
+    }
+    return hipSuccess;
+}
+
+template <typename DT> hipError_t by_act(const GluArgs& a, bool bwd, hipStream_t st) {
+    switch (a.act) {
+        case GLU_SILU: return bwd ? backward<DT, GLU_SILU>(a, st) : forward<DT, GLU_SILU>(a, st);
+        case GLU_SIGMOID: return bwd ? backward<DT, GLU_SIGMOID>(a, st) : forward<DT, GLU_SIGMOID>(a, st);
+        default: return bwd ? backward<DT, GLU_GELU>(a, st) : forward<DT, GLU_GELU>(a, st);
+    }
+}
+
+}  // namespace
+
+size_t glu_fwd_workspace(const GluArgs& a) { return work_of(a, false, false, nullptr).size; }
+size_t glu_bwd_workspace(const GluArgs& a, bool input_grad) { return work_of(a, true, input_grad, nullptr).size; }
+int64_t glu_blocks(const GluArgs& a) {
+    const int64_t t = (a.T + 127) / 128, d = ((int64_t)a.D + 127) / 128, f = ((int64_t)a.F + 63) / 64;
+    const int64_t h = t * f, dx = t * d * dx_shape(a).split, dw = f * d * 2 * dw_shape(a).split;
+    return (h > dx ? h > dw ? h : dw : dx > dw ? dx : dw) + 8;
+}
+
+hipError_t launch_glu_fwd(const GluArgs& a, hipStream_t st) {
+    return a.dtype == 1 ? by_act<bf16>(a, false, st) : by_act<float>(a, false, st);
+}
+hipError_t launch_glu_bwd(const GluArgs& a, hipStream_t st) {
+    return a.dtype == 1 ? by_act<bf16>(a, true, st) : by_act<float>(a, true, st);
+}
+
+}  // namespace kda

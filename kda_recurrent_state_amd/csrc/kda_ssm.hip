@@ -1,0 +1,1130 @@
+// kda_ssm.hip -- selective state space scan: chunked walk over packed sequences.
+//
+// Per head, with d_t = softplus(dt_t + bias), l_t = d_t A log2(e) and a_t = 2^{l_t}:
+//   h_t = a_t h_{t-1} + d_t B_t^T x_t,   y_t = C_t h_t + D x_t,   h [K, P].
+// Inside a chunk of Q tokens, with c_t the running sum of l:
+//   y_t   = 2^{c_t} C_t h + sum_{s <= t} (C_t . B_s) 2^{c_t - c_s} d_s x_s + D x_t
+//   h'    = 2^{c_Q} h + sum_s 2^{c_Q - c_s} d_s B_s^T x_s.
+// The gradient with respect to x' = d x walks the chunks from the end, with the chunk's tokens
+// reversed, r_t = c_Q - c_t in place of c_t and (B, C, x) replaced by (C, B, dy):
+//   dx'_s = 2^{r_s} B_s g + sum_{t >= s} (B_s . C_t) 2^{r_s - r_t} dy_t
+//   g'    = 2^{c_Q} g + sum_t 2^{c_Q - r_t} C_t^T dy_t,
+// the same map with other names, so one kernel does both.
+//
+// Exponents: c_t - c_s is the difference of two sums that may be large while it is small, so the
+// sums are formed in fp64 and held as a multiple of 2^-8 and a rest; both differences are exact or
+// nearly so.  No exponent is positive, so nothing overflows whatever the decay; l is held above
+// -300, below which 2^l is zero for every state that fp32 holds.
+//
+// Matrix cores take bf16 operands.  bf16 inputs go in as they are; what is computed in fp32 (the
+// masked products, the state, decayed inputs) goes in as a sum of 2 or 3 bf16 parts, each the
+// rounding of what the parts before it left: two hold a value to 2^-18, three to 2^-26 of itself.
+// Two for what ends in a bf16 output, three for the states and wherever inputs are fp32 (those
+// are split as they are staged; products of parts below 2^-24 are left out).
+#include "kda_ssm.hpp"
+
+#include "kda_rows.hpp"
+
+namespace kda {
+namespace {
+
+constexpr int WAVES = 4;
+constexpr int NT = WAVES * WAVE;
+constexpr float LOG2E = 1.4426950408889634f;
+
+template <typename DT> struct Cfg;
+template <> struct Cfg<bf16> { static constexpr int QT = 4, NP = 1, MP = 2, HP = 2; };
+template <> struct Cfg<float> { static constexpr int QT = 2, NP = 3, MP = 3, HP = 3; };
+
+typedef short s16x4 __attribute__((ext_vector_type(4)));
+
+// The sum of N bf16 parts that stands for v.
+template <int N> struct Parts { bf16x8 p[N]; };
+template <int N> __device__ __forceinline__ Parts<N> split8(const float (&in)[8]) {
+    Parts<N> o;
+    float v[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = in[i];
+#pragma unroll
+    for (int n = 0; n < N; ++n) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) o.p[n][i] = (bf16)v[i];
+        if (n + 1 < N) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) v[i] -= (float)o.p[n][i];
+        }
+    }
+    return o;
+}
+
+// acc += A B over the parts of both, without the products below 2^-24.
+template <int NA, int NB>
+__device__ __forceinline__ f32x4 mma_parts(const Parts<NA>& a, const Parts<NB>& b, f32x4 acc) {
+#pragma unroll
+    for (int i = 0; i < NA; ++i)
+#pragma unroll
+        for (int j = 0; j < NB; ++j)
+            if (i + j <= 2) acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a.p[i], b.p[j], acc, 0, 0, 0);
+    return acc;
+}
+
+// Operands of 32 contraction indices.  In the "paired" order lane group q = lane / 16 holds indices
+// 4 q .. 4 q + 3 and 16 + 4 q .. 16 + 4 q + 3: the order in which two accumulator tiles, one
+// above the other, hold their rows, so that they can be fed back without leaving the registers.
+__device__ __forceinline__ bf16x8 join(bf16x4 a, bf16x4 b) {
+    return __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7);
+}
+// rows: the lane's row of a matrix whose contraction index is contiguous
+__device__ __forceinline__ bf16x8 row_paired(const bf16* row, int lane) {
+    const bf16* p = row + 4 * (lane >> 4);
+    return join(*reinterpret_cast<const bf16x4*>(p), *reinterpret_cast<const bf16x4*>(p + 16));
+}
+__device__ __forceinline__ bf16x8 row_natural(const bf16* row, int lane) {
+    return *reinterpret_cast<const bf16x8*>(row + 8 * (lane >> 4));
+}
+// a matrix stored with its contraction index along the rows: each group of 16 lanes reads 4 rows of 16
+// columns and gets them transposed, 4 contraction indices of column lane % 16
+__device__ __forceinline__ bf16x4 tr4(const bf16* m, int ld, int k0, int lane) {
+    typedef __attribute__((address_space(3))) s16x4* lds;
+    const bf16* p = m + (k0 + ((lane & 15) >> 2)) * ld + 4 * (lane & 3);
+    return __builtin_bit_cast(bf16x4, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds)(p)));
+}
+__device__ __forceinline__ bf16x8 col_paired(const bf16* m, int ld, int lane) {
+    const int k = 4 * (lane >> 4);
+    return join(tr4(m, ld, k, lane), tr4(m, ld, k + 16, lane));
+}
+__device__ __forceinline__ bf16x8 col_natural(const bf16* m, int ld, int lane) {
+    const int k = 8 * (lane >> 4);
+    return join(tr4(m, ld, k, lane), tr4(m, ld, k + 4, lane));
+}
+
+// ROWS rows of up to COLS columns on their way from global memory to LDS, zero where a row or
+// column does not exist: loads first, then (split into NP planes) the stores.
+template <typename DT, int ROWS, int COLS, int THREADS> struct Stage {
+    static constexpr int NP = Cfg<DT>::NP, PER = COLS / 8, ALL = ROWS * PER, CNT = (ALL + THREADS - 1) / THREADS;
+    Pack<DT, 8> v[CNT];
+    // row r is token first + r * dir, r < n
+    __device__ __forceinline__ void load(const DT* src, int64_t stride, int cols, int first, int dir, int n, int tid) {
+#pragma unroll
+        for (int i = 0; i < CNT; ++i) {
+            const int at = i * THREADS + tid, r = at / PER, c = at % PER * 8;
+            float z[8];
+            zero_v(z);
+            set(v[i], z);
+            if (r < n && c < cols && at < ALL) {
+                const DT* p = src + (int64_t)(first + r * dir) * stride + c;
+                if (c + 8 <= cols) {
+                    v[i] = load_v<8>(p);
+                } else {
+                    for (int k = 0; k < 8; ++k)
+                        if (c + k < cols) z[k] = to_f32(p[k]);
+                    set(v[i], z);
+                }
+            }
+        }
+    }
+    __device__ __forceinline__ void store(bf16* dst, int ld, int plane, int tid) const {
+#pragma unroll
+        for (int i = 0; i < CNT; ++i) {
+            const int at = i * THREADS + tid, r = at / PER, c = at % PER * 8;
+            if (ALL % THREADS != 0 && at >= ALL) continue;
+            float f[8];
+            get_v(v[i], f);
+            const Parts<NP> s = split8<NP>(f);
+#pragma unroll
+            for (int n = 0; n < NP; ++n) *reinterpret_cast<bf16x8*>(dst + n * plane + r * ld + c) = s.p[n];
+        }
+    }
+    static __device__ __forceinline__ void set(Pack<DT, 8>& p, const float (&f)[8]) {
+#pragma unroll
+        for (int k = 0; k < 8; ++k) p.part[k / Pack<DT, 8>::N][k % Pack<DT, 8>::N] = from_f32<DT>(f[k]);
+    }
+};
+
+__device__ __forceinline__ float softplus_f(float z) { return fmaxf(z, 0.f) + log1pf(expf(-fabsf(z))); }
+
+__device__ __forceinline__ double lanes_scan(double v, int lane) {
+#pragma unroll
+    for (int d = 1; d < WAVE; d <<= 1) {
+        const double t = __shfl_up(v, d);
+        if (lane >= d) v += t;
+    }
+    return v;
+}
+
+// The decays of a chunk, one token a lane: c (or r, reversed) as hi + lo, the weight of a
+// token as a source, and its derivatives' factors.
+template <int Q> struct Decays {
+    float hi[Q], lo[Q], src[Q], scale[Q], from[Q], to[Q];
+    // src: weight of the token's product (d, reversed 1); scale: of its result (1, reversed d);
+    // from: 2^{c}; to: 2^{total - c} (src not included)
+};
+template <int Q>
+__device__ __forceinline__ double decays(Decays<Q>& w, const SsmArgs& a, int h, int first, int dir, int n, bool rev, int lane) {
+    float d = 0.f;
+    double l = 0.0;
+    if (lane < n) {
+        const float z = a.dt[(int64_t)(first + lane * dir) * a.dts + h] + (a.bias ? a.bias[h] : 0.f);
+        d = a.softplus ? softplus_f(z) : z;
+        l = fmax((double)d * (double)a.A[h] * 1.4426950408889634, -300.0);
+    }
+    const double incl = lanes_scan(l, lane), c = rev ? incl - l : incl;
+    const double total = __shfl(incl, WAVE - 1);
+    if (lane < Q) {
+        const double hi = rint(c * 256.0) * (1.0 / 256.0);
+        w.hi[lane] = (float)hi;
+        w.lo[lane] = (float)(c - hi);
+        w.src[lane] = lane < n ? (rev ? 1.f : d) : 0.f;
+        w.scale[lane] = rev ? d : 1.f;
+        w.from[lane] = exp2f((float)c);
+        w.to[lane] = exp2f((float)(total - c));
+    }
+    return total;
+}
+
+// The n-th piece of `every` tokens of each sequence has the slot start / every + sequence + n: slots
+// rise with the sequence, and a sequence of L tokens has room for ceil(L / every) of them.
+struct Piece { int seq, n, start, len; bool live; };
+__device__ __forceinline__ Piece find_piece(const Seqs& sq, int slot, int every) {
+    const int lane = threadIdx.x % WAVE;
+    int lo = 0, hi = sq.N;
+    while (hi - lo > 1) {
+        const int step = (hi - lo + WAVE - 1) / WAVE, n = lo + (lane + 1) * step;
+        const bool in = n < hi;
+        const int below = __popcll(__ballot(in && sq.start(in ? n : lo) / every + (in ? n : lo) <= slot));
+        lo += below * step;
+        hi = hi - lo < step ? hi : lo + step;
+    }
+    Piece p;
+    p.seq = lo;
+    p.start = sq.start(lo);
+    p.len = max(sq.start(lo + 1) - p.start, 0);
+    p.n = slot - (p.start / every + lo);
+    p.live = p.n >= 0 && (p.n == 0 || (int64_t)p.n * every < p.len);
+    return p;
+}
+
+// A launch's workgroups by (slot, group) and by four units of the group.  Workgroups of a
+// (slot, group) read the same B and C; every eighth workgroup runs on the same die, so they are
+// given numbers 8 apart.
+struct Place { int slot, group, quad; bool live; };
+__device__ __forceinline__ Place place_of(int b, int64_t slots, int G, int quads) {
+    const int64_t pair = (b & 7) + 8ll * ((b >> 3) / quads);
+    Place p;
+    p.quad = (b >> 3) % quads;
+    p.slot = (int)(pair / G);
+    p.group = (int)(pair % G);
+    p.live = p.slot < slots;
+    return p;
+}
+int64_t place_blocks(int64_t slots, int G, int quads) { return (slots * G + 7) / 8 * 8 * quads; }
+
+constexpr int OUT = 1, EMIT = 2, ENDS = 4;
+
+// One wavefront per unit walks the chunks of a segment, its state in accumulator tiles [k][p].
+// OUT: writes the results; EMIT: the state before every chunk; ENDS: starts from zero and
+// writes the segment's own state and decay (not for a sequence's last segment).
+template <typename DT, int KT, int PT, int MODE>
+__global__ void __launch_bounds__(NT, 2) ssm_walk_kernel(SsmArgs a, const DT* val, const DT* key, const DT* query,
+                                                         int64_t vs, int64_t ks, int64_t qs, const float* first_state,
+                                                         float* last_state, float* emit, int rev, int64_t slots,
+                                                         int quads) {
+    using C_ = Cfg<DT>;
+    constexpr int QT = C_::QT, Q = QT * 16, NP = C_::NP, MP = C_::MP, HP = C_::HP;
+    constexpr int LDK = KT * 16 + 8, LDP = PT * 16 + 8, PLK = Q * LDK, PLP = Q * LDP;
+    extern __shared__ __attribute__((aligned(16))) char smem[];
+    bf16* skey = reinterpret_cast<bf16*>(smem);
+    bf16* squery = skey + NP * PLK;
+    bf16* sval_all = (MODE & OUT) ? squery + NP * PLK : squery;
+    Decays<Q>* sdec = reinterpret_cast<Decays<Q>*>(sval_all + WAVES * NP * PLP);
+
+    const int tid = threadIdx.x, lane = tid % WAVE, wave = __builtin_amdgcn_readfirstlane(tid / WAVE);
+    const int l15 = lane & 15, q4 = lane >> 4;
+    const Place at = place_of(blockIdx.x, slots, a.G, quads);
+    if (!at.live) return;
+    const Seqs sq{a.cu, a.N, a.T, a.eq};
+    const Piece pc = find_piece(sq, at.slot, a.seg);
+    if (!pc.live) return;
+    const int per = a.H / a.G, units = per * a.blocks, unit_in = at.quad * WAVES + wave;
+    const bool mine = unit_in < units;
+    const int unit = at.group * units + (mine ? unit_in : 0);
+    const int h = unit / a.blocks, p0 = unit % a.blocks * (PT * 16);
+    const int segs = max((pc.len + a.seg - 1) / a.seg, 1);
+    const bool is_last = pc.n == (rev ? 0 : segs - 1), is_first = pc.n == (rev ? segs - 1 : 0);
+    if ((MODE & ENDS) && is_last) return;
+    const int t0 = pc.n * a.seg, t1 = min(t0 + a.seg, pc.len), chunks = (t1 - t0 + Q - 1) / Q;
+    const int64_t frag = ((int64_t)at.slot * a.H * a.blocks + unit) * (KT * PT * WAVE) + lane;
+
+    bf16* sval = sval_all + wave * NP * PLP;
+    Decays<Q>& dec = sdec[wave];
+    f32x4 st[KT][PT];
+#pragma unroll
+    for (int k = 0; k < KT; ++k)
+#pragma unroll
+        for (int p = 0; p < PT; ++p) st[k][p] = zero4();
+    if (!(MODE & ENDS) && mine) {
+        if (!is_first) {
+            const f32x4* e = reinterpret_cast<const f32x4*>(a.ends);
+#pragma unroll
+            for (int k = 0; k < KT; ++k)
+#pragma unroll
+                for (int p = 0; p < PT; ++p) st[k][p] = e[frag + (k * PT + p) * WAVE];
+        } else if (first_state) {
+            const float* f = first_state + ((int64_t)pc.seq * a.H + h) * a.K * a.P;
+#pragma unroll
+            for (int k = 0; k < KT; ++k)
+#pragma unroll
+                for (int p = 0; p < PT; ++p)
+#pragma unroll
+                    for (int r = 0; r < 4; ++r) {
+                        const int kk = 16 * k + 4 * q4 + r, pp = p0 + 16 * p + l15;
+                        if (kk < a.K && pp < a.P) st[k][p][r] = f[(int64_t)kk * a.P + pp];
+                    }
+        }
+    }
+    const float dskip = (MODE & OUT) && a.D && mine ? a.D[h] : 0.f;
+    double log_decay = 0.0;
+
+    for (int ci = 0; ci < chunks; ++ci) {
+        const int cc = rev ? chunks - 1 - ci : ci;
+        const int c0 = pc.start + t0 + cc * Q, n = min(Q, pc.start + t1 - c0);
+        const int first = rev ? c0 + n - 1 : c0, dir = rev ? -1 : 1;
+        if (ci) __syncthreads();  // the last chunk's tiles are read
+        float total;
+        {
+            Stage<DT, Q, KT * 16, NT> bk, bq;
+            Stage<DT, Q, PT * 16, WAVE> bv;
+            bk.load(key + (int64_t)at.group * a.K, ks, a.K, first, dir, n, tid);
+            if (MODE & OUT) bq.load(query + (int64_t)at.group * a.K, qs, a.K, first, dir, n, tid);
+            bv.load(val + (int64_t)h * a.P + p0, vs, min(a.P - p0, PT * 16), first, dir, n, lane);
+            const double lt = decays<Q>(dec, a, h, first, dir, n, rev, lane);
+            log_decay += lt;
+            total = exp2f((float)lt);
+            bk.store(skey, LDK, PLK, tid);
+            if (MODE & OUT) bq.store(squery, LDK, PLK, tid);
+            bv.store(sval, LDP, PLP, lane);
+        }
+        __syncthreads();
+        if (!mine) continue;
+
+        if (MODE & EMIT) {
+            const int64_t cslot = pc.start / Q + pc.seq + (t0 / Q + cc);
+            float* e = emit + (cslot * a.H * a.blocks + unit) * (KT * 16 * PT * 16);
+#pragma unroll
+            for (int k = 0; k < KT; ++k)
+#pragma unroll
+                for (int p = 0; p < PT; ++p)
+#pragma unroll
+                    for (int r = 0; r < 4; ++r) e[(16 * k + 4 * q4 + r) * (PT * 16) + 16 * p + l15] = st[k][p][r];
+        }
+
+        if constexpr ((MODE & OUT) != 0) {
+            // results transposed, [p][t]: a lane holds 4 neighbouring columns of token 16 j + l15
+            f32x4 acc[QT][PT];
+#pragma unroll
+            for (int j = 0; j < QT; ++j)
+#pragma unroll
+                for (int p = 0; p < PT; ++p) acc[j][p] = zero4();
+#pragma unroll
+            for (int kk = 0; kk < KT / 2; ++kk) {
+                Parts<NP> qf[QT];
+#pragma unroll
+                for (int j = 0; j < QT; ++j)
+#pragma unroll
+                    for (int m = 0; m < NP; ++m)
+                        qf[j].p[m] = row_paired(squery + m * PLK + (16 * j + l15) * LDK + 32 * kk, lane);
+#pragma unroll
+                for (int p = 0; p < PT; ++p) {
+                    float v[8];
+#pragma unroll
+                    for (int r = 0; r < 4; ++r) {
+                        v[r] = st[2 * kk][p][r];
+                        v[4 + r] = st[2 * kk + 1][p][r];
+                    }
+                    const Parts<HP> hf = split8<HP>(v);
+#pragma unroll
+                    for (int j = 0; j < QT; ++j) acc[j][p] = mma_parts(hf, qf[j], acc[j][p]);
+                }
+            }
+#pragma unroll
+            for (int j = 0; j < QT; ++j) {
+                const int t = 16 * j + l15;
+                const float from = dec.from[t];
+#pragma unroll
+                for (int p = 0; p < PT; ++p) acc[j][p] *= from;
+                Parts<NP> qf[KT / 2];
+#pragma unroll
+                for (int kk = 0; kk < KT / 2; ++kk)
+#pragma unroll
+                    for (int m = 0; m < NP; ++m)
+                        qf[kk].p[m] = row_paired(squery + m * PLK + t * LDK + 32 * kk, lane);
+                const float hi = dec.hi[t], lo = dec.lo[t];
+#pragma unroll
+                for (int i2 = 0; i2 <= j / 2; ++i2) {
+                    float m8[8];
+#pragma unroll
+                    for (int half = 0; half < 2; ++half) {
+                        const int i = 2 * i2 + half;
+                        if (i > j) {
+#pragma unroll
+                            for (int r = 0; r < 4; ++r) m8[4 * half + r] = 0.f;
+                            continue;
+                        }
+                        f32x4 s = zero4();
+#pragma unroll
+                        for (int kk = 0; kk < KT / 2; ++kk) {
+                            Parts<NP> kf;
+#pragma unroll
+                            for (int m = 0; m < NP; ++m)
+                                kf.p[m] = row_paired(skey + m * PLK + (16 * i + l15) * LDK + 32 * kk, lane);
+                            s = mma_parts(kf, qf[kk], s);
+                        }
+                        const f32x4 shi = *reinterpret_cast<const f32x4*>(&dec.hi[16 * i + 4 * q4]);
+                        const f32x4 slo = *reinterpret_cast<const f32x4*>(&dec.lo[16 * i + 4 * q4]);
+                        const f32x4 src = *reinterpret_cast<const f32x4*>(&dec.src[16 * i + 4 * q4]);
+#pragma unroll
+                        for (int r = 0; r < 4; ++r) {
+                            const float e = __builtin_amdgcn_exp2f((hi - shi[r]) + (lo - slo[r]));
+                            const float v = s[r] * (e * src[r]);
+                            m8[4 * half + r] = i < j || 4 * q4 + r <= l15 ? v : 0.f;
+                        }
+                    }
+                    const Parts<MP> mf = split8<MP>(m8);
+#pragma unroll
+                    for (int p = 0; p < PT; ++p) {
+                        Parts<NP> vf;
+#pragma unroll
+                        for (int m = 0; m < NP; ++m)
+                            vf.p[m] = col_paired(sval + m * PLP + 32 * i2 * LDP + 16 * p, LDP, lane);
+                        acc[j][p] = mma_parts(vf, mf, acc[j][p]);
+                    }
+                }
+                if (t < n) {
+                    const float scale = dec.scale[t];
+                    DT* out = reinterpret_cast<DT*>(a.y) + ((int64_t)(first + t * dir) * a.H + h) * a.P + p0;
+#pragma unroll
+                    for (int p = 0; p < PT; ++p) {
+                        const int c = 16 * p + 4 * q4;
+                        float o[4];
+                        zero_v(o);
+#pragma unroll
+                        for (int m = NP - 1; m >= 0; --m) {
+                            const bf16x4 v = *reinterpret_cast<const bf16x4*>(sval + m * PLP + t * LDP + c);
+#pragma unroll
+                            for (int r = 0; r < 4; ++r) o[r] += (float)v[r];
+                        }
+#pragma unroll
+                        for (int r = 0; r < 4; ++r) o[r] = scale * acc[j][p][r] + dskip * o[r];
+                        if (p0 + c + 4 <= a.P) {
+                            store_v<4>(out + c, o);
+                        } else {
+#pragma unroll
+                            for (int r = 0; r < 4; ++r)
+                                if (p0 + c + r < a.P) out[c + r] = from_f32<DT>(o[r]);
+                        }
+                    }
+                }
+            }
+        }
+
+        // the state behind the chunk
+#pragma unroll
+        for (int k = 0; k < KT; ++k)
+#pragma unroll
+            for (int p = 0; p < PT; ++p) st[k][p] *= total;
+#pragma unroll
+        for (int i2 = 0; i2 < QT / 2; ++i2) {
+            const int s0 = 32 * i2 + 4 * q4;
+            float w[8];
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+                w[r] = dec.to[s0 + r] * dec.src[s0 + r];
+                w[4 + r] = dec.to[s0 + 16 + r] * dec.src[s0 + 16 + r];
+            }
+            Parts<3> xf[PT];
+#pragma unroll
+            for (int p = 0; p < PT; ++p) {
+                float v[8];
+                zero_v(v);
+#pragma unroll
+                for (int m = NP - 1; m >= 0; --m) {
+                    const bf16x8 b = col_paired(sval + m * PLP + 32 * i2 * LDP + 16 * p, LDP, lane);
+#pragma unroll
+                    for (int r = 0; r < 8; ++r) v[r] += (float)b[r];
+                }
+#pragma unroll
+                for (int r = 0; r < 8; ++r) v[r] *= w[r];
+                xf[p] = split8<3>(v);
+            }
+#pragma unroll
+            for (int k = 0; k < KT; ++k) {
+                Parts<NP> kf;
+#pragma unroll
+                for (int m = 0; m < NP; ++m) kf.p[m] = col_paired(skey + m * PLK + 32 * i2 * LDK + 16 * k, LDK, lane);
+#pragma unroll
+                for (int p = 0; p < PT; ++p) st[k][p] = mma_parts(kf, xf[p], st[k][p]);
+            }
+        }
+    }
+    if (!mine) return;
+    if (MODE & ENDS) {
+        f32x4* e = reinterpret_cast<f32x4*>(a.ends);
+#pragma unroll
+        for (int k = 0; k < KT; ++k)
+#pragma unroll
+            for (int p = 0; p < PT; ++p) e[frag + (k * PT + p) * WAVE] = st[k][p];
+        if (lane == 0 && p0 == 0) a.decay[(int64_t)at.slot * a.H + h] = exp2f((float)log_decay);
+    } else if (is_last && last_state) {
+        float* f = last_state + ((int64_t)pc.seq * a.H + h) * a.K * a.P;
+#pragma unroll
+        for (int k = 0; k < KT; ++k)
+#pragma unroll
+            for (int p = 0; p < PT; ++p)
+#pragma unroll
+                for (int r = 0; r < 4; ++r) {
+                    const int kk = 16 * k + 4 * q4 + r, pp = p0 + 16 * p + l15;
+                    if (kk < a.K && pp < a.P) f[(int64_t)kk * a.P + pp] = st[k][p][r];
+                }
+    }
+}
+
+// Joins the segments of a sequence: ends[slot] holds what the segment adds from a zero state and becomes
+// the state it starts from.  Four elements a thread.
+__global__ void __launch_bounds__(NT) ssm_join_kernel(SsmArgs a, const float* first_state, int rev, int per_unit,
+                                                      int pieces) {
+    const int64_t units = (int64_t)a.H * a.blocks;
+    for (int64_t b = blockIdx.x; b < a.N * units * pieces; b += gridDim.x) {
+    const int piece = (int)(b % pieces), unit = (int)(b / pieces % units), seq = (int)(b / pieces / units);
+    const Seqs sq{a.cu, a.N, a.T, a.eq};
+    const int start = sq.start(seq), len = sq.start(seq + 1) - start;
+    const int segs = (max(len, 0) + a.seg - 1) / a.seg;
+    const int e = piece * NT + threadIdx.x;
+    if (segs < 2 || e >= per_unit) continue;
+    const int h = unit / a.blocks, tiles = a.cols / 16;
+    const int lane = e % WAVE, tile = e / WAVE;
+    f32x4 cur = zero4();
+    if (first_state) {
+        const int k0 = 16 * (tile / tiles) + 4 * (lane >> 4), p = unit % a.blocks * a.cols + 16 * (tile % tiles) + (lane & 15);
+#pragma unroll
+        for (int r = 0; r < 4; ++r)
+            if (k0 + r < a.K && p < a.P) cur[r] = first_state[(((int64_t)seq * a.H + h) * a.K + k0 + r) * a.P + p];
+    }
+    const int64_t slot = start / a.seg + seq;
+    f32x4* ends = reinterpret_cast<f32x4*>(a.ends);
+    auto at = [&](int j) { return ((slot + (rev ? segs - 1 - j : j)) * units + unit) * per_unit + e; };
+    auto dec = [&](int j) { return a.decay[(slot + (rev ? segs - 1 - j : j)) * a.H + h]; };
+    f32x4 nxt = ends[at(0)];
+    float nd = dec(0);
+    for (int j = 0; j + 1 < segs; ++j) {
+        const f32x4 own = nxt;
+        const float d = nd;
+        if (j + 2 < segs) {
+            nxt = ends[at(j + 1)];
+            nd = dec(j + 1);
+        }
+        cur = cur * d + own;
+        ends[at(j + 1)] = cur;
+    }
+    }
+}
+
+// The gradient that needs the states from both sides, a workgroup per chunk and share of a group's
+// units.  With M[t][s] = (C_t . B_s) 2^{c_t - c_s} and E[t][s] = dy_t . x_s, s <= t, h the state
+// before the chunk and g the derivative behind it:
+//   dC_t = sum_s (E 2^{..} d_s)[t][s] B_s + 2^{c_t} dy_t h^T
+//   dB_s = sum_t (E 2^{..} d_s)[t][s] C_t + d_s 2^{c_Q - c_s} x_s g^T
+//   d(d_s) = sum_t (M E)[t][s] + 2^{c_Q - c_s} B_s . (x_s g^T)      (without the decays)
+//   dl_t = sum of d_s (M E)[r][s] over r >= t > s + sum_{r >= t} 2^{c_r} C_r . (dy_r h^T)
+//          + sum_{s < t} d_s 2^{c_Q - c_s} B_s . (x_s g^T) + 2^{c_Q} h . g
+// dB and dC are summed over the group's heads in registers.  The wavefronts share a unit: each forms
+// 16 rows of M, E and their products (in LDS as bf16 parts), then a quarter of the columns of
+// dB and dC, so no sum crosses wavefronts but those of single numbers a token.
+template <typename DT, int KT, int PT>
+__global__ void __launch_bounds__(NT, 2) ssm_grad_kernel(SsmArgs a, int64_t slots, int quads) {
+    using C_ = Cfg<DT>;
+    constexpr int QT = C_::QT, Q = QT * 16, NP = C_::NP, MP = C_::MP;
+    constexpr int LDK = KT * 16 + 8, LDP = PT * 16 + 8, LDQ = Q + 8, PLK = Q * LDK, PLP = Q * LDP, PLQ = Q * LDQ;
+    constexpr int KW = KT < WAVES ? 1 : KT / WAVES;  // column tiles of a wavefront
+    struct Sums { float row[Q], col[WAVES][Q], ui[WAVES][Q], vi[WAVES][Q], xy[Q], hg[WAVES]; };
+    extern __shared__ __attribute__((aligned(16))) char smem[];
+    bf16* sb = reinterpret_cast<bf16*>(smem);
+    bf16* sc = sb + NP * PLK;
+    bf16* sx = sc + NP * PLK;
+    bf16* sdy = sx + NP * PLP;
+    bf16* sds = sdy + NP * PLP;
+    Decays<Q>& dec = *reinterpret_cast<Decays<Q>*>(sds + MP * PLQ);
+    Sums& sum = *reinterpret_cast<Sums*>(&dec + 1);
+
+    const int tid = threadIdx.x, lane = tid % WAVE, wave = __builtin_amdgcn_readfirstlane(tid / WAVE);
+    const int l15 = lane & 15, q4 = lane >> 4;
+    const Place at = place_of(blockIdx.x, slots, a.G, quads);
+    if (!at.live) return;
+    const Seqs sq{a.cu, a.N, a.T, a.eq};
+    const Piece pc = find_piece(sq, at.slot, Q);
+    if (!pc.live || pc.len == 0) return;
+    const int c0 = pc.start + pc.n * Q, n = min(Q, pc.len - pc.n * Q);
+    const int units = a.H / a.G * a.blocks;
+    const int u0 = (int)((int64_t)at.quad * units / quads), u1 = (int)((int64_t)(at.quad + 1) * units / quads);
+    const int64_t all_units = (int64_t)a.H * a.blocks;
+
+    {
+        Stage<DT, Q, KT * 16, NT> bk, bq;
+        bk.load((const DT*)a.B + (int64_t)at.group * a.K, a.bs, a.K, c0, 1, n, tid);
+        bq.load((const DT*)a.C + (int64_t)at.group * a.K, a.cs, a.K, c0, 1, n, tid);
+        bk.store(sb, LDK, PLK, tid);
+        bq.store(sc, LDK, PLK, tid);
+    }
+    f32x4 dB[QT][KW], dC[QT][KW];
+#pragma unroll
+    for (int j = 0; j < QT; ++j)
+#pragma unroll
+        for (int k = 0; k < KW; ++k) dB[j][k] = dC[j][k] = zero4();
+
+    for (int un = u0; un < u1; ++un) {
+        const int unit = at.group * units + un, h = unit / a.blocks, p0 = unit % a.blocks * (PT * 16);
+        const int cols = min(a.P - p0, PT * 16);
+        if (un > u0) __syncthreads();
+        float total = 0.f;
+        {
+            Stage<DT, Q, PT * 16, NT> bx, by;
+            bx.load((const DT*)a.x + (int64_t)h * a.P + p0, a.xs, cols, c0, 1, n, tid);
+            by.load((const DT*)a.dy + (int64_t)h * a.P + p0, a.dys, cols, c0, 1, n, tid);
+            if (wave == 0) total = exp2f((float)decays<Q>(dec, a, h, c0, 1, n, false, lane));
+            bx.store(sx, LDP, PLP, tid);
+            by.store(sdy, LDP, PLP, tid);
+        }
+        __syncthreads();
+
+        // rows t of tile `wave` against every s up to them, transposed: a lane holds 4 s of one t
+        if (wave < QT) {
+            const int j = wave, t = 16 * j + l15;
+            Parts<NP> cf[KT / 2], yf[PT / 2];
+#pragma unroll
+            for (int kk = 0; kk < KT / 2; ++kk)
+#pragma unroll
+                for (int m = 0; m < NP; ++m) cf[kk].p[m] = row_natural(sc + m * PLK + t * LDK + 32 * kk, lane);
+#pragma unroll
+            for (int pp = 0; pp < PT / 2; ++pp)
+#pragma unroll
+                for (int m = 0; m < NP; ++m) yf[pp].p[m] = row_natural(sdy + m * PLP + t * LDP + 32 * pp, lane);
+            const float hi = dec.hi[t], lo = dec.lo[t];
+            float row = 0.f;
+#pragma unroll
+            for (int i = 0; i < QT; ++i) {
+                f32x4 ds = zero4(), z = zero4();
+                if (i <= j) {
+                    f32x4 s = zero4(), e = zero4();
+#pragma unroll
+                    for (int kk = 0; kk < KT / 2; ++kk) {
+                        Parts<NP> f;
+#pragma unroll
+                        for (int m = 0; m < NP; ++m)
+                            f.p[m] = row_natural(sb + m * PLK + (16 * i + l15) * LDK + 32 * kk, lane);
+                        s = mma_parts(f, cf[kk], s);
+                    }
+#pragma unroll
+                    for (int pp = 0; pp < PT / 2; ++pp) {
+                        Parts<NP> f;
+#pragma unroll
+                        for (int m = 0; m < NP; ++m)
+                            f.p[m] = row_natural(sx + m * PLP + (16 * i + l15) * LDP + 32 * pp, lane);
+                        e = mma_parts(f, yf[pp], e);
+                    }
+                    const f32x4 shi = *reinterpret_cast<const f32x4*>(&dec.hi[16 * i + 4 * q4]);
+                    const f32x4 slo = *reinterpret_cast<const f32x4*>(&dec.lo[16 * i + 4 * q4]);
+                    const f32x4 src = *reinterpret_cast<const f32x4*>(&dec.src[16 * i + 4 * q4]);
+#pragma unroll
+                    for (int r = 0; r < 4; ++r) {
+                        const bool in = i < j || 4 * q4 + r <= l15;
+                        const float le = in ? __builtin_amdgcn_exp2f((hi - shi[r]) + (lo - slo[r])) * e[r] : 0.f;
+                        ds[r] = le * src[r];
+                        z[r] = le * s[r];
+                        row += z[r] * src[r];
+                        if (i == j && 4 * q4 + r == l15) sum.xy[t] = e[r];
+                    }
+                }
+                // sums over the tile's 16 tokens t; the next wavefronts' tiles add theirs
+#pragma unroll
+                for (int r = 0; r < 4; ++r) {
+                    const float c = lanes_sum<16>(z[r]);
+                    if (l15 == 0) sum.col[j][16 * i + 4 * q4 + r] = c;
+                }
+                if (i <= (j | 1)) {  // the tile above the diagonal that a product over 32 tokens meets is zero
+                    float v[4] = {ds[0], ds[1], ds[2], ds[3]};
+#pragma unroll
+                    for (int m = 0; m < MP; ++m) {
+                        bf16x4 b;
+#pragma unroll
+                        for (int r = 0; r < 4; ++r) {
+                            b[r] = (bf16)v[r];
+                            v[r] -= (float)b[r];
+                        }
+                        *reinterpret_cast<bf16x4*>(sds + m * PLQ + t * LDQ + 16 * i + 4 * q4) = b;
+                    }
+                }
+            }
+            row += __shfl_xor(row, 16);
+            row += __shfl_xor(row, 32);
+            if (q4 == 0) sum.row[t] = row;
+        }
+        __syncthreads();
+
+        // the wavefront's columns of dB and dC
+        f32x4 ui[QT], vi[QT];
+        float hg = 0.f;
+#pragma unroll
+        for (int j = 0; j < QT; ++j) ui[j] = vi[j] = zero4();
+        if (wave * KW < KT) {
+            const int64_t cslot = pc.start / Q + pc.seq + pc.n;
+            const int64_t state = (cslot * all_units + unit) * (KT * 16 * PT * 16);
+#pragma unroll
+            for (int k = 0; k < KW; ++k) {
+                const int kt = wave * KW + k, kc = 16 * kt + l15;
+                Parts<3> hf[PT / 2], gf[PT / 2];
+#pragma unroll
+                for (int pp = 0; pp < PT / 2; ++pp) {
+                    const int64_t o = state + (int64_t)kc * (PT * 16) + 32 * pp + 8 * q4;
+                    const Pack<float, 8> hv = load_v<8>(a.hs + o), gv = load_v<8>(a.gs + o);
+                    float hx[8], gx[8];
+                    get_v(hv, hx);
+                    get_v(gv, gx);
+#pragma unroll
+                    for (int r = 0; r < 8; ++r) hg += hx[r] * gx[r];
+                    hf[pp] = split8<3>(hx);
+                    gf[pp] = split8<3>(gx);
+                }
+#pragma unroll
+                for (int j = 0; j < QT; ++j) {
+                    f32x4 tc = zero4(), tb = zero4();
+#pragma unroll
+                    for (int pp = 0; pp < PT / 2; ++pp) {
+                        Parts<NP> f, x;
+#pragma unroll
+                        for (int m = 0; m < NP; ++m) {
+                            f.p[m] = row_natural(sdy + m * PLP + (16 * j + l15) * LDP + 32 * pp, lane);
+                            x.p[m] = row_natural(sx + m * PLP + (16 * j + l15) * LDP + 32 * pp, lane);
+                        }
+                        tc = mma_parts(f, hf[pp], tc);
+                        tb = mma_parts(x, gf[pp], tb);
+                    }
+                    const int t = 16 * j + 4 * q4;
+                    const f32x4 from = *reinterpret_cast<const f32x4*>(&dec.from[t]);
+                    const f32x4 to = *reinterpret_cast<const f32x4*>(&dec.to[t]);
+                    const f32x4 src = *reinterpret_cast<const f32x4*>(&dec.src[t]);
+#pragma unroll
+                    for (int r = 0; r < 4; ++r) {
+                        float cv = 0.f, bv = 0.f;
+#pragma unroll
+                        for (int m = NP - 1; m >= 0; --m) {
+                            cv += (float)sc[m * PLK + (t + r) * LDK + kc];
+                            bv += (float)sb[m * PLK + (t + r) * LDK + kc];
+                        }
+                        const float c = tc[r] * from[r], b = tb[r] * to[r];
+                        ui[j][r] += cv * c;
+                        vi[j][r] += bv * b;
+                        dC[j][k][r] += c;
+                        dB[j][k][r] += b * src[r];
+                    }
+                }
+#pragma unroll
+                for (int i2 = 0; i2 < QT / 2; ++i2) {
+                    Parts<NP> bf, cf;
+#pragma unroll
+                    for (int m = 0; m < NP; ++m) {
+                        bf.p[m] = col_natural(sb + m * PLK + 32 * i2 * LDK + 16 * kt, LDK, lane);
+                        cf.p[m] = col_natural(sc + m * PLK + 32 * i2 * LDK + 16 * kt, LDK, lane);
+                    }
+#pragma unroll
+                    for (int j = 0; j < QT; ++j) {
+                        Parts<MP> f;
+                        if (i2 <= j / 2) {
+#pragma unroll
+                            for (int m = 0; m < MP; ++m)
+                                f.p[m] = row_natural(sds + m * PLQ + (16 * j + l15) * LDQ + 32 * i2, lane);
+                            dC[j][k] = mma_parts(f, bf, dC[j][k]);
+                        }
+                        if (i2 >= j / 2) {
+#pragma unroll
+                            for (int m = 0; m < MP; ++m)
+                                f.p[m] = col_natural(sds + m * PLQ + 32 * i2 * LDQ + 16 * j, LDQ, lane);
+                            dB[j][k] = mma_parts(f, cf, dB[j][k]);
+                        }
+                    }
+                }
+            }
+        }
+#pragma unroll
+        for (int j = 0; j < QT; ++j)
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+                const float u = lanes_sum<16>(ui[j][r]), v = lanes_sum<16>(vi[j][r]);
+                if (l15 == 0) {
+                    sum.ui[wave][16 * j + 4 * q4 + r] = u;
+                    sum.vi[wave][16 * j + 4 * q4 + r] = v;
+                }
+            }
+        hg = lanes_sum<WAVE>(hg);
+        if (lane == 0) sum.hg[wave] = hg;
+        __syncthreads();
+
+        if (wave == 0) {
+            double rows = 0.0, cols_ = 0.0, outs = 0.0;
+            float dd = 0.f, xy = 0.f;
+            if (lane < n) {
+                float c = 0.f, u = 0.f, v = 0.f;
+#pragma unroll
+                for (int w = 0; w < WAVES; ++w) {
+                    if (w < QT) c += sum.col[w][lane];
+                    u += sum.ui[w][lane];
+                    v += sum.vi[w][lane];
+                }
+                const float d = dec.src[lane];
+                rows = (double)sum.row[lane] + u;
+                cols_ = (double)c * d;
+                outs = (double)v * d;
+                dd = c + v;
+                xy = sum.xy[lane];
+            }
+            const double through = (double)total * ((sum.hg[0] + sum.hg[1]) + (sum.hg[2] + sum.hg[3]));
+            const double net = lanes_scan(rows - cols_, lane), before = lanes_scan(outs, lane) - outs;
+            const double dl = __shfl(net, WAVE - 1) - net + (rows - cols_) + before + through;
+            if (lane < n) {
+                float* o = a.tok + ((int64_t)(c0 + lane) * all_units + unit) * 3;
+                o[0] = (float)dl;
+                o[1] = dd;
+                o[2] = xy;
+            }
+        }
+    }
+
+    if (wave * KW >= KT) return;
+#pragma unroll
+    for (int j = 0; j < QT; ++j)
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+            const int t = 16 * j + 4 * q4 + r;
+            if (t >= n) continue;
+#pragma unroll
+            for (int k = 0; k < KW; ++k) {
+                const int kc = 16 * (wave * KW + k) + l15;
+                if (kc >= a.K) continue;
+                const int64_t o = ((int64_t)(c0 + t) * a.G + at.group) * a.K + kc;
+                if (quads == 1) {
+                    ((DT*)a.dB)[o] = from_f32<DT>(dB[j][k][r]);
+                    ((DT*)a.dC)[o] = from_f32<DT>(dC[j][k][r]);
+                } else {
+                    const int64_t all = (int64_t)a.T * a.G * a.K, p = (int64_t)at.quad * 2 * all + o;
+                    a.part[p] = dB[j][k][r];
+                    a.part[p + all] = dC[j][k][r];
+                }
+            }
+        }
+}
+
+// dB and dC from the shares' sums.
+template <typename DT> __global__ void __launch_bounds__(NT) ssm_shares_kernel(SsmArgs a) {
+    const Seqs sq{a.cu, a.N, a.T, a.eq};
+    const int64_t all = (int64_t)a.T * a.G * a.K, live = (int64_t)sq.end() * a.G * a.K;
+    for (int64_t i = (int64_t)blockIdx.x * NT + threadIdx.x; i < live; i += (int64_t)gridDim.x * NT) {
+        float b = 0.f, c = 0.f;
+        for (int s = 0; s < a.split; ++s) {
+            b += a.part[(int64_t)s * 2 * all + i];
+            c += a.part[(int64_t)s * 2 * all + all + i];
+        }
+        ((DT*)a.dB)[i] = from_f32<DT>(b);
+        ((DT*)a.dC)[i] = from_f32<DT>(c);
+    }
+}
+
+// ddt from the units' numbers, and partial sums of dA, dD and dbias over the workgroup's tokens: a lane is a
+// head, a wavefront every fourth token.
+__global__ void __launch_bounds__(NT) ssm_tokens_kernel(SsmArgs a, int tokens) {
+    const Seqs sq{a.cu, a.N, a.T, a.eq};
+    const int lane = threadIdx.x % WAVE, wave = threadIdx.x / WAVE;
+    const int64_t t0 = (int64_t)blockIdx.x * tokens, t1 = min(t0 + tokens, (int64_t)sq.end());
+    const int h = blockIdx.y * WAVE + lane;
+    __shared__ double part[WAVES][3][WAVE];
+    double dA = 0.0, dD = 0.0, db = 0.0;
+    if (h < a.H) {
+        const float A = a.A[h], bias = a.bias ? a.bias[h] : 0.f;
+        for (int64_t t = t0 + wave; t < t1; t += WAVES) {
+            const float* u = a.tok + (t * a.H + h) * a.blocks * 3;
+            double dl = 0.0, dd = 0.0, xy = 0.0;
+            for (int b = 0; b < a.blocks; ++b) {
+                dl += u[3 * b];
+                dd += u[3 * b + 1];
+                xy += u[3 * b + 2];
+            }
+            const float z = a.dt[t * a.dts + h] + bias;
+            const float d = a.softplus ? softplus_f(z) : z;
+            // the slope of softplus is the logistic function
+            const double s = a.softplus ? 1.0 / (1.0 + exp(-(double)z)) : 1.0;
+            const double dz = (dl * A + dd) * s;
+            a.ddt[t * a.H + h] = (float)dz;
+            dA += dl * d;
+            dD += xy;
+            db += dz;
+        }
+    }
+    part[wave][0][lane] = dA;
+    part[wave][1][lane] = dD;
+    part[wave][2][lane] = db;
+    __syncthreads();
+    if (wave < 3 && h < a.H) {
+        double s = 0.0;
+        for (int w = 0; w < WAVES; ++w) s += part[w][wave][lane];
+        a.sums[((int64_t)blockIdx.x * 3 + wave) * a.H + h] = (float)s;
+    }
+}
+
+// Last sums of dA, dD and dbias: a wavefront per value.
+__global__ void __launch_bounds__(NT) ssm_sums_kernel(SsmArgs a, int rows) {
+    const int lane = threadIdx.x % WAVE;
+    const int64_t i = (int64_t)blockIdx.x * WAVES + threadIdx.x / WAVE;
+    if (i >= 3ll * a.H) return;
+    const int which = (int)(i / a.H), h = (int)(i % a.H);
+    float* out = which == 0 ? a.dA : which == 1 ? a.dD : a.dbias;
+    if (!out) return;
+    double s = 0.0;
+    for (int r = lane; r < rows; r += WAVE) s += a.sums[((int64_t)r * 3 + which) * a.H + h];
+#pragma unroll
+    for (int m = 1; m < WAVE; m <<= 1) s += __shfl_xor(s, m);
+    if (lane == 0) out[h] = (float)s;
+}
+
+// ---------------------------------------------------------------- one token per sequence
+
+// z = act(bias + sum_j w_j x_{W-1-j}) in fp32, and the taps moved on by a token.
+template <typename DT> __global__ void __launch_bounds__(NT) ssm_conv_kernel(SsmConvArgs a) {
+    const int64_t i = (int64_t)blockIdx.x * NT + threadIdx.x;
+    if (i >= (int64_t)a.N * a.C) return;
+    const int64_t n = i / a.C;
+    const int c = (int)(i % a.C);
+    const DT* in = (const DT*)a.state_in + n * (a.W - 1) * a.C + c;
+    DT* out = (DT*)a.state_out + n * (a.W - 1) * a.C + c;
+    const DT x = ((const DT*)a.x)[n * a.xs + c];
+    const float* w = a.weight + (int64_t)c * a.W;
+    DT s[3];
+    for (int j = 0; j < a.W - 1; ++j) s[j] = in[(int64_t)j * a.C];
+    float z = a.bias ? a.bias[c] : 0.f;
+    for (int j = 0; j < a.W - 1; ++j) z += w[j] * to_f32(s[j]);
+    z += w[a.W - 1] * to_f32(x);
+    if (a.silu) z *= sigmoid_f(z);
+    for (int j = 0; j + 1 < a.W - 1; ++j) out[(int64_t)j * a.C] = s[j + 1];
+    out[(int64_t)(a.W - 2) * a.C] = x;
+    a.z[i] = z;
+}
+
+// A workgroup per (sequence, head, COLS columns): the state is read and written once, V neighbouring
+// columns and K / ROWS rows a thread.
+template <typename TI, typename TO, int V>
+__global__ void __launch_bounds__(NT) ssm_step_kernel(SsmStepArgs a, int lanes_log2, int cblocks) {
+    const int cb = blockIdx.x % cblocks;
+    const int64_t nh = blockIdx.x / cblocks;
+    const int64_t n = nh / a.H;
+    const int h = (int)(nh % a.H), g = h / (a.H / a.G);
+    const int lanes = 1 << lanes_log2, cl = threadIdx.x & (lanes - 1), r0 = threadIdx.x >> lanes_log2, rs = NT >> lanes_log2;
+    const int p = (cb * lanes + cl) * V;
+    const bool in = p < a.P;
+    const float z = a.dt[n * a.dts + h] + (a.bias ? a.bias[h] : 0.f);
+    const float d = a.softplus ? softplus_f(z) : z;
+    const float decay = expf(d * a.A[h]);
+    const TI* B = (const TI*)a.B + n * a.bs + (int64_t)g * a.K;
+    const TI* C = (const TI*)a.C + n * a.cs + (int64_t)g * a.K;
+    float x[V], y[V];
+    zero_v(x);
+    zero_v(y);
+    if (in) get_v(load_v<V>((const TI*)a.x + n * a.xs + (int64_t)h * a.P + p), x);
+    float xd[V];
+#pragma unroll
+    for (int v = 0; v < V; ++v) xd[v] = d * x[v];
+    const float* hin = a.h_in + nh * a.K * a.P + p;
+    float* hout = a.h_out + nh * a.K * a.P + p;
+    constexpr int U = 8;
+    if (in) {
+        for (int k0 = r0; k0 < a.K; k0 += U * rs) {
+            Pack<float, V> s[U];
+            float b[U], c[U];
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                const int k = k0 + u * rs;
+                if (k < a.K) {
+                    s[u] = load_nt<V>(hin + (int64_t)k * a.P);
+                    b[u] = to_f32(B[k]);
+                    c[u] = to_f32(C[k]);
+                }
+            }
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                const int k = k0 + u * rs;
+                if (k >= a.K) break;
+                float o[V];
+#pragma unroll
+                for (int v = 0; v < V; ++v) {
+                    o[v] = decay * s[u][v] + b[u] * xd[v];
+                    y[v] += c[u] * o[v];
+                }
+                store_nt<V>(hout + (int64_t)k * a.P, o);
+            }
+        }
+    }
+    __shared__ float part[NT * V];
+#pragma unroll
+    for (int v = 0; v < V; ++v) part[threadIdx.x * V + v] = y[v];
+    __syncthreads();
+    if (r0 == 0 && in) {
+        for (int r = 1; r < rs; ++r)
+#pragma unroll
+            for (int v = 0; v < V; ++v) y[v] += part[(r * lanes + cl) * V + v];
+        const float dk = a.D ? a.D[h] : 0.f;
+#pragma unroll
+        for (int v = 0; v < V; ++v) y[v] += dk * x[v];
+        store_v<V>((TO*)a.y + nh * a.P + p, y);
+    }
+}
+
+// ---------------------------------------------------------------- launches
+
+template <typename DT, int KT, int PT, int MODE> constexpr int walk_lds() {
+    constexpr int Q = Cfg<DT>::QT * 16, NP = Cfg<DT>::NP;
+    return ((MODE & OUT ? 2 : 1) * NP * Q * (KT * 16 + 8) + WAVES * NP * Q * (PT * 16 + 8)) * 2 +
+           WAVES * (int)sizeof(Decays<Q>);
+}
+template <typename DT, int KT, int PT> constexpr int grad_lds() {
+    constexpr int Q = Cfg<DT>::QT * 16, NP = Cfg<DT>::NP;
+    return (2 * NP * Q * (KT * 16 + 8) + 2 * NP * Q * (PT * 16 + 8) + Cfg<DT>::MP * Q * (Q + 8)) * 2 +
+           (int)sizeof(Decays<Q>) + (Q * (2 + 3 * WAVES) + WAVES) * 4;
+}
+
+template <typename F> hipError_t allow_lds(F* kernel, int bytes) {
+    return bytes > 65536 ? hipFuncSetAttribute(reinterpret_cast<const void*>(kernel),
+                                               hipFuncAttributeMaxDynamicSharedMemorySize, bytes)
+                         : hipSuccess;
+}
+
+struct Roles {
+    const void *val, *key, *query;
+    int64_t vs, ks, qs;
+    const float* first;
+    float* last;
+    float* emit;
+    int rev;
+};
+
+template <typename DT, int KT, int PT, int MODE>
+hipError_t walk(const SsmArgs& a, const Roles& r, hipStream_t st) {
+    const int64_t slots = ssm_slots(a, a.seg);
+    const int quads = (a.H / a.G * a.blocks + WAVES - 1) / WAVES;
+    constexpr int lds = walk_lds<DT, KT, PT, MODE>();
+    static_assert(lds <= 160 * 1024, "a chunk's tiles fit a compute unit");
+    auto* kernel = ssm_walk_kernel<DT, KT, PT, MODE>;
+    const hipError_t e = allow_lds(kernel, lds);
+    if (e != hipSuccess) return e;
+    hipLaunchKernelGGL(kernel, dim3((unsigned)place_blocks(slots, a.G, quads)), dim3(NT), lds, st, a, (const DT*)r.val,
+                       (const DT*)r.key, (const DT*)r.query, r.vs, r.ks, r.qs, r.first, r.last, r.emit, r.rev, slots, quads);
+    return hipGetLastError();
+}
+
+bool segmented(const SsmArgs& a) { return a.cu ? a.seg < a.T : a.seg < a.eq; }
+
+#define SSM_TRY(call)                                do {                                                 const hipError_t e_ = (call);                    if (e_ != hipSuccess) return e_;             } while (0)
+
+// The states that the segments start from, then the walk proper.
+template <typename DT, int KT, int PT, int MODE>
+hipError_t whole_walk(const SsmArgs& a, const Roles& r, hipStream_t st) {
+    if (segmented(a)) {
+        SSM_TRY((walk<DT, KT, PT, ENDS>(a, r, st)));
+        const int per_unit = KT * PT * WAVE, pieces = (per_unit + NT - 1) / NT;
+        const int64_t blocks = ssm_units(a) * a.N * pieces;
+        hipLaunchKernelGGL(ssm_join_kernel, dim3((unsigned)(blocks < 1 << 20 ? blocks : 1 << 20)), dim3(NT), 0, st, a, r.first,
+                           r.rev, per_unit, pieces);
+        SSM_TRY(hipGetLastError());
+    }
+    return walk<DT, KT, PT, MODE>(a, r, st);
+}
+
+template <typename DT, int KT, int PT> hipError_t forward(const SsmArgs& a, hipStream_t st) {
+    const Roles r{a.x, a.B, a.C, a.xs, a.bs, a.cs, a.h0, a.hT, nullptr, 0};
+    return whole_walk<DT, KT, PT, OUT>(a, r, st);
+}
+
+template <typename DT, int KT, int PT> hipError_t backward(const SsmArgs& a, hipStream_t st) {
+    if (a.N > 0) {
+        const Roles f{a.x, a.B, a.C, a.xs, a.bs, a.cs, a.h0, nullptr, a.hs, 0};
+        SSM_TRY((whole_walk<DT, KT, PT, EMIT>(a, f, st)));
+        const Roles b{a.dy, a.C, a.B, a.dys, a.cs, a.bs, a.dhT, a.dh0, a.gs, 1};
+        SSM_TRY((whole_walk<DT, KT, PT, OUT | EMIT>(a, b, st)));
+    }
+    if (a.T > 0) {
+        const int64_t slots = ssm_slots(a, a.chunk);
+        constexpr int lds = grad_lds<DT, KT, PT>();
+        static_assert(lds <= 160 * 1024, "a chunk's tiles fit a compute unit");
+        auto* kernel = ssm_grad_kernel<DT, KT, PT>;
+        SSM_TRY(allow_lds(kernel, lds));
+        hipLaunchKernelGGL(kernel, dim3((unsigned)place_blocks(slots, a.G, a.split)), dim3(NT), lds, st, a, slots, a.split);
+        SSM_TRY(hipGetLastError());
+        if (a.split > 1) {
+            const int64_t all = (int64_t)a.T * a.G * a.K, blocks = (all + NT - 1) / NT;
+            hipLaunchKernelGGL(ssm_shares_kernel<DT>, dim3((unsigned)(blocks < 4096 ? blocks : 4096)), dim3(NT), 0, st, a);
+            SSM_TRY(hipGetLastError());
+        }
+    }
+    const int tokens = (a.T + SSM_SUM_ROWS - 1) / SSM_SUM_ROWS < 16 ? 16 : (a.T + SSM_SUM_ROWS - 1) / SSM_SUM_ROWS;
+    const int rows = (a.T + tokens - 1) / tokens;
+    if (rows > 0) {
+        hipLaunchKernelGGL(ssm_tokens_kernel, dim3(rows, (a.H + WAVE - 1) / WAVE), dim3(NT), 0, st, a, tokens);
+        SSM_TRY(hipGetLastError());
+    }
+    if (!a.dA && !a.dD && !a.dbias) return hipSuccess;
+    hipLaunchKernelGGL(ssm_sums_kernel, dim3((3 * a.H + WAVES - 1) / WAVES), dim3(NT), 0, st, a, rows);
+    return hipGetLastError();
+}
+
+template <typename DT> hipError_t by_state(const SsmArgs& a, bool bwd, hipStream_t st) {
+    switch (a.rows) {
+        case 32: return bwd ? backward<DT, 2, 4>(a, st) : forward<DT, 2, 4>(a, st);
+        case 64: return bwd ? backward<DT, 4, 4>(a, st) : forward<DT, 4, 4>(a, st);
+        case 128: return bwd ? backward<DT, 8, 4>(a, st) : forward<DT, 8, 4>(a, st);
+        default: return bwd ? backward<DT, 16, 2>(a, st) : forward<DT, 16, 2>(a, st);
+    }
+}
+
+}  // namespace
+
+hipError_t launch_ssm_fwd(const SsmArgs& a, hipStream_t st) {
+    return a.dtype == 1 ? by_state<bf16>(a, false, st) : by_state<float>(a, false, st);
+}
+hipError_t launch_ssm_bwd(const SsmArgs& a, hipStream_t st) {
+    return a.dtype == 1 ? by_state<bf16>(a, true, st) : by_state<float>(a, true, st);
+}
+
+hipError_t launch_ssm_conv(const SsmConvArgs& a, hipStream_t st) {
+    const int64_t blocks = ((int64_t)a.N * a.C + NT - 1) / NT;
+    if (a.dtype == 1) hipLaunchKernelGGL(ssm_conv_kernel<bf16>, dim3((unsigned)blocks), dim3(NT), 0, st, a);
+    else hipLaunchKernelGGL(ssm_conv_kernel<float>, dim3((unsigned)blocks), dim3(NT), 0, st, a);
+    return hipGetLastError();
+}
+
+namespace {
+template <typename TI, typename TO> hipError_t step(const SsmStepArgs& a, hipStream_t st) {
+    // rows of whole float4 in four columns a lane; narrow blocks of columns where the heads do not fill the GPU
+    const bool four = a.P % 4 == 0;
+    const int wide = four ? (a.P + 3) / 4 : a.P;
+    int log2 = 0;
+    while ((1 << log2) < wide && log2 < 6) ++log2;
+    const int64_t heads = (int64_t)a.N * a.H;
+    while (log2 > 3 && heads * ((wide + (1 << log2) - 1) >> log2) < 512) --log2;
+    const int cblocks = (wide + (1 << log2) - 1) >> log2;
+    const dim3 grid((unsigned)(heads * cblocks));
+    if (four) hipLaunchKernelGGL((ssm_step_kernel<TI, TO, 4>), grid, dim3(NT), 0, st, a, log2, cblocks);
+    else hipLaunchKernelGGL((ssm_step_kernel<TI, TO, 1>), grid, dim3(NT), 0, st, a, log2, cblocks);
+    return hipGetLastError();
+}
+}  // namespace
+
+hipError_t launch_ssm_step(const SsmStepArgs& a, hipStream_t st) {
+    if (a.dtype != 1) return step<float, float>(a, st);
+    return a.f32_in ? step<float, bf16>(a, st) : step<bf16, bf16>(a, st);
+}
+
+}  // namespace kda

@@ -1,0 +1,70 @@
+// kda_ssm.hpp -- sizes and host-side launchers of the selective state space scan.
+#pragma once
+
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+namespace kda {
+
+// The state [K, P] of a head is held by wavefronts in blocks of all K rows and up to
+// SSM_COLS columns (half of that above 128 rows, where the block would not fit a wavefront's
+// registers): a "unit" is a head's block of columns.  Columns do not meet in the
+// recurrence, so units are independent.
+constexpr int SSM_COLS = 64;
+constexpr int SSM_MAX_STATE = 256;
+inline int ssm_cols(int K) { return K > 128 ? SSM_COLS / 2 : SSM_COLS; }
+inline int ssm_rows(int K) { return K <= 32 ? 32 : K <= 64 ? 64 : K <= 128 ? 128 : 256; }
+inline int ssm_chunk(int dtype) { return dtype == 1 ? 64 : 32; }  // tokens of a chunk (1: bf16)
+
+struct SsmArgs {
+    const void *x, *B, *C, *dy;
+    const float *dt, *A, *D, *bias, *h0, *dhT;  // D, bias, h0, dhT may be null
+    const int32_t* cu;                           // device, may be null
+    void *y, *dB, *dC;                           // y: forward output; backward: dx
+    float *hT, *ddt, *dA, *dD, *dbias, *dh0;     // each may be null but ddt
+    int32_t N, T, eq, H, G, K, P;
+    int64_t xs, dts, bs, cs, dys;                // token strides
+    int32_t dtype, softplus;
+    // plan
+    int32_t chunk, rows, cols, blocks;           // tokens of a chunk, padded K, columns and column blocks of a unit
+    int32_t seg;                                 // tokens of a segment (a multiple of chunk)
+    int32_t split;                               // shares of a group's units in the gradient
+    // workspace
+    float *ends, *decay;                         // a segment's own state at its end / the state it starts from; its decay
+    float *hs, *gs;                              // states before every chunk, derivatives behind it
+    float *part;                                 // partial dB, dC of the shares
+    float *tok;                                  // per token and unit: derivative of the log decay, of dt, x dy
+    float *sums;                                 // partial dA, dD, dbias
+};
+
+inline int64_t ssm_units(const SsmArgs& a) { return (int64_t)a.H * a.blocks; }
+inline int64_t ssm_slots(const SsmArgs& a, int every) { return a.T / every + a.N; }
+inline int64_t ssm_unit_state(const SsmArgs& a) { return (int64_t)a.rows * a.cols; }
+constexpr int SSM_SUM_ROWS = 256;
+
+hipError_t launch_ssm_fwd(const SsmArgs& a, hipStream_t st);
+hipError_t launch_ssm_bwd(const SsmArgs& a, hipStream_t st);
+
+struct SsmStepArgs {
+    const void *x, *B, *C;      // in: dtype; with a convolution all three lie in conv's float output
+    const float *dt, *A, *D, *bias, *h_in;
+    float* h_out;
+    void* y;
+    int32_t N, H, G, K, P;
+    int64_t xs, dts, bs, cs;
+    int32_t dtype, softplus, f32_in;
+};
+hipError_t launch_ssm_step(const SsmStepArgs& a, hipStream_t st);
+
+struct SsmConvArgs {
+    const void* x;
+    const float *weight, *bias;  // bias may be null
+    const void* state_in;
+    void* state_out;
+    float* z;                    // [N, C]
+    int32_t N, C, W, dtype, silu;
+    int64_t xs;
+};
+hipError_t launch_ssm_conv(const SsmConvArgs& a, hipStream_t st);
+
+}  // namespace kda
