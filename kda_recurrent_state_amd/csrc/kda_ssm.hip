@@ -36,6 +36,7 @@ template <typename DT> struct Cfg;
 template <> struct Cfg<bf16> { static constexpr int QT = 4, NP = 1, MP = 2, HP = 2; };
 template <> struct Cfg<float> { static constexpr int QT = 2, NP = 3, MP = 3, HP = 3; };
 
+template <int V> struct Int { static constexpr int value = V; };
 typedef short s16x4 __attribute__((ext_vector_type(4)));
 
 // The sum of N bf16 parts that stands for v.
@@ -99,26 +100,39 @@ __device__ __forceinline__ bf16x8 col_natural(const bf16* m, int ld, int lane) {
 }
 
 // ROWS rows of up to COLS columns on their way from global memory to LDS, zero where a row or
-// column does not exist: loads first, then (split into NP planes) the stores.
+// column does not exist: loads first, then (split into NP planes) the stores.  Where every column
+// exists (the usual case) no lane branches: rows past the last read the last and are replaced by zeros.
 template <typename DT, int ROWS, int COLS, int THREADS> struct Stage {
     static constexpr int NP = Cfg<DT>::NP, PER = COLS / 8, ALL = ROWS * PER, CNT = (ALL + THREADS - 1) / THREADS;
     Pack<DT, 8> v[CNT];
-    // row r is token first + r * dir, r < n
+    // row r is token first + r * dir, r < n (n > 0)
     __device__ __forceinline__ void load(const DT* src, int64_t stride, int cols, int first, int dir, int n, int tid) {
+        if (cols == COLS) {
+            const DT* base = src + (int64_t)first * stride;
+            const int step = (int)stride * dir;
+#pragma unroll
+            for (int i = 0; i < CNT; ++i) {
+                const int at = i * THREADS + tid, r = min(at / PER, n - 1), c = at % PER * 8;
+                if (ALL % THREADS == 0 || at < ALL) v[i] = load_v<8>(base + ((int64_t)r * step + c));
+            }
+            if (n < ROWS) {
+#pragma unroll
+                for (int i = 0; i < CNT; ++i)
+                    if ((i * THREADS + tid) / PER >= n) clear(v[i]);
+            }
+            return;
+        }
 #pragma unroll
         for (int i = 0; i < CNT; ++i) {
             const int at = i * THREADS + tid, r = at / PER, c = at % PER * 8;
-            float z[8];
-            zero_v(z);
-            set(v[i], z);
+            clear(v[i]);
             if (r < n && c < cols && at < ALL) {
                 const DT* p = src + (int64_t)(first + r * dir) * stride + c;
                 if (c + 8 <= cols) {
                     v[i] = load_v<8>(p);
                 } else {
                     for (int k = 0; k < 8; ++k)
-                        if (c + k < cols) z[k] = to_f32(p[k]);
-                    set(v[i], z);
+                        if (c + k < cols) v[i].part[k / Pack<DT, 8>::N][k % Pack<DT, 8>::N] = p[k];
                 }
             }
         }
@@ -128,16 +142,21 @@ template <typename DT, int ROWS, int COLS, int THREADS> struct Stage {
         for (int i = 0; i < CNT; ++i) {
             const int at = i * THREADS + tid, r = at / PER, c = at % PER * 8;
             if (ALL % THREADS != 0 && at >= ALL) continue;
-            float f[8];
-            get_v(v[i], f);
-            const Parts<NP> s = split8<NP>(f);
+            bf16* p = dst + r * ld + c;
+            if constexpr (NP == 1) {
+                *reinterpret_cast<bf16x8*>(p) = __builtin_bit_cast(bf16x8, v[i]);
+            } else {
+                float f[8];
+                get_v(v[i], f);
+                const Parts<NP> s = split8<NP>(f);
 #pragma unroll
-            for (int n = 0; n < NP; ++n) *reinterpret_cast<bf16x8*>(dst + n * plane + r * ld + c) = s.p[n];
+                for (int n = 0; n < NP; ++n) *reinterpret_cast<bf16x8*>(p + n * plane) = s.p[n];
+            }
         }
     }
-    static __device__ __forceinline__ void set(Pack<DT, 8>& p, const float (&f)[8]) {
+    static __device__ __forceinline__ void clear(Pack<DT, 8>& p) {
 #pragma unroll
-        for (int k = 0; k < 8; ++k) p.part[k / Pack<DT, 8>::N][k % Pack<DT, 8>::N] = from_f32<DT>(f[k]);
+        for (int k = 0; k < 8; ++k) p.part[k / Pack<DT, 8>::N][k % Pack<DT, 8>::N] = from_f32<DT>(0.f);
     }
 };
 
@@ -182,6 +201,17 @@ __device__ __forceinline__ double decays(Decays<Q>& w, const SsmArgs& a, int h, 
     return total;
 }
 
+// Sum over the 16 lanes of a group by rotations inside the group: no trip through LDS.
+__device__ __forceinline__ float sum16(float x) {
+    auto turned = [](float v, auto ctrl) {
+        return __builtin_bit_cast(float, __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, v), decltype(ctrl)::value, 15, 15, true));
+    };
+    x += turned(x, Int<0x128>());
+    x += turned(x, Int<0x124>());
+    x += turned(x, Int<0x122>());
+    return x + turned(x, Int<0x121>());
+}
+
 // The n-th piece of `every` tokens of each sequence has the slot start / every + sequence + n: slots
 // rise with the sequence, and a sequence of L tokens has room for ceil(L / every) of them.
 struct Piece { int seq, n, start, len; bool live; };
@@ -195,11 +225,13 @@ __device__ __forceinline__ Piece find_piece(const Seqs& sq, int slot, int every)
         lo += below * step;
         hi = hi - lo < step ? hi : lo + step;
     }
+    // the same in every lane: kept in scalar registers, and so is every address that comes of them
+    auto uniform = [](int v) { return __builtin_amdgcn_readfirstlane(v); };
     Piece p;
-    p.seq = lo;
-    p.start = sq.start(lo);
-    p.len = max(sq.start(lo + 1) - p.start, 0);
-    p.n = slot - (p.start / every + lo);
+    p.seq = uniform(lo);
+    p.start = uniform(sq.start(p.seq));
+    p.len = max(uniform(sq.start(p.seq + 1)) - p.start, 0);
+    p.n = slot - (p.start / every + p.seq);
     p.live = p.n >= 0 && (p.n == 0 || (int64_t)p.n * every < p.len);
     return p;
 }
@@ -220,6 +252,13 @@ __device__ __forceinline__ Place place_of(int b, int64_t slots, int G, int quads
 int64_t place_blocks(int64_t slots, int G, int quads) { return (slots * G + 7) / 8 * 8 * quads; }
 
 constexpr int OUT = 1, EMIT = 2, ENDS = 4;
+
+// A value the compiler takes for a new one.  Addresses that depend on it are formed where they are used
+// and not kept in registers through the walk, where the state leaves no room for them.
+__device__ __forceinline__ int renewed(int v) {
+    asm volatile("" : "+v"(v));
+    return v;
+}
 
 // One wavefront per unit walks the chunks of a segment, its state in accumulator tiles [k][p].
 // OUT: writes the results; EMIT: the state before every chunk; ENDS: starts from zero and
@@ -292,6 +331,7 @@ __global__ void __launch_bounds__(NT, 2) ssm_walk_kernel(SsmArgs a, const DT* va
         if (ci) __syncthreads();  // the last chunk's tiles are read
         float total;
         {
+            const int tid = renewed(threadIdx.x), lane = tid % WAVE;
             Stage<DT, Q, KT * 16, NT> bk, bq;
             Stage<DT, Q, PT * 16, WAVE> bv;
             bk.load(key + (int64_t)at.group * a.K, ks, a.K, first, dir, n, tid);
@@ -310,12 +350,13 @@ __global__ void __launch_bounds__(NT, 2) ssm_walk_kernel(SsmArgs a, const DT* va
         if (MODE & EMIT) {
             const int64_t cslot = pc.start / Q + pc.seq + (t0 / Q + cc);
             float* e = emit + (cslot * a.H * a.blocks + unit) * (KT * 16 * PT * 16);
+            const int own = renewed(4 * q4 * (PT * 16) + l15);
 #pragma unroll
             for (int k = 0; k < KT; ++k)
 #pragma unroll
                 for (int p = 0; p < PT; ++p)
 #pragma unroll
-                    for (int r = 0; r < 4; ++r) e[(16 * k + 4 * q4 + r) * (PT * 16) + 16 * p + l15] = st[k][p][r];
+                    for (int r = 0; r < 4; ++r) e[own + (16 * k + r) * (PT * 16) + 16 * p] = st[k][p][r];
         }
 
         if constexpr ((MODE & OUT) != 0) {
@@ -348,6 +389,8 @@ __global__ void __launch_bounds__(NT, 2) ssm_walk_kernel(SsmArgs a, const DT* va
             }
 #pragma unroll
             for (int j = 0; j < QT; ++j) {
+                // operands are read again for each tile of tokens: kept from tile to tile they would push the state out
+                const int lane = renewed(threadIdx.x) % WAVE, l15 = lane & 15, q4 = lane >> 4;
                 const int t = 16 * j + l15;
                 const float from = dec.from[t];
 #pragma unroll
@@ -401,7 +444,8 @@ __global__ void __launch_bounds__(NT, 2) ssm_walk_kernel(SsmArgs a, const DT* va
                 }
                 if (t < n) {
                     const float scale = dec.scale[t];
-                    DT* out = reinterpret_cast<DT*>(a.y) + ((int64_t)(first + t * dir) * a.H + h) * a.P + p0;
+                    DT* out = reinterpret_cast<DT*>(a.y) + ((int64_t)first * a.H + h) * a.P + p0 +
+                              (int64_t)t * dir * a.H * a.P;
 #pragma unroll
                     for (int p = 0; p < PT; ++p) {
                         const int c = 16 * p + 4 * q4;
@@ -580,19 +624,37 @@ __global__ void __launch_bounds__(NT, 2) ssm_grad_kernel(SsmArgs a, int64_t slot
 #pragma unroll
         for (int k = 0; k < KW; ++k) dB[j][k] = dC[j][k] = zero4();
 
-    for (int un = u0; un < u1; ++un) {
+    Stage<DT, Q, PT * 16, NT> bx, by;  // the next unit's, on their way
+    auto fetch = [&](int un, int tid) {
         const int unit = at.group * units + un, h = unit / a.blocks, p0 = unit % a.blocks * (PT * 16);
         const int cols = min(a.P - p0, PT * 16);
-        if (un > u0) __syncthreads();
+        bx.load((const DT*)a.x + (int64_t)h * a.P + p0, a.xs, cols, c0, 1, n, tid);
+        by.load((const DT*)a.dy + (int64_t)h * a.P + p0, a.dys, cols, c0, 1, n, tid);
+    };
+    fetch(u0, tid);
+    for (int un = u0; un < u1; ++un) {
+        const int unit = at.group * units + un, h = unit / a.blocks;
         float total = 0.f;
+        // The last unit's products are read (its third barrier); the states are on their way through the first phase.
         {
-            Stage<DT, Q, PT * 16, NT> bx, by;
-            bx.load((const DT*)a.x + (int64_t)h * a.P + p0, a.xs, cols, c0, 1, n, tid);
-            by.load((const DT*)a.dy + (int64_t)h * a.P + p0, a.dys, cols, c0, 1, n, tid);
+            const int tid = renewed(threadIdx.x), lane = tid % WAVE;
             if (wave == 0) total = exp2f((float)decays<Q>(dec, a, h, c0, 1, n, false, lane));
             bx.store(sx, LDP, PLP, tid);
             by.store(sdy, LDP, PLP, tid);
+            if (un + 1 < u1) fetch(un + 1, tid);
         }
+        Pack<float, 8> hv[PT / 2], gv[PT / 2];
+        auto states = [&](int k) {
+            const int64_t cslot = pc.start / Q + pc.seq + pc.n;
+            const int64_t state = (cslot * all_units + unit) * (KT * 16 * PT * 16) + (wave * KW + k) * 16 * (PT * 16);
+            const int lane = renewed(threadIdx.x) % WAVE, own = (lane & 15) * (PT * 16) + 8 * (lane >> 4);
+#pragma unroll
+            for (int pp = 0; pp < PT / 2; ++pp) {
+                hv[pp] = load_v<8>(a.hs + state + (own + 32 * pp));
+                gv[pp] = load_v<8>(a.gs + state + (own + 32 * pp));
+            }
+        };
+        if (wave * KW < KT) states(0);
         __syncthreads();
 
         // rows t of tile `wave` against every s up to them, transposed: a lane holds 4 s of one t
@@ -646,7 +708,7 @@ __global__ void __launch_bounds__(NT, 2) ssm_grad_kernel(SsmArgs a, int64_t slot
                 // sums over the tile's 16 tokens t; the next wavefronts' tiles add theirs
 #pragma unroll
                 for (int r = 0; r < 4; ++r) {
-                    const float c = lanes_sum<16>(z[r]);
+                    const float c = sum16(z[r]);
                     if (l15 == 0) sum.col[j][16 * i + 4 * q4 + r] = c;
                 }
                 if (i <= (j | 1)) {  // the tile above the diagonal that a product over 32 tokens meets is zero
@@ -670,29 +732,24 @@ __global__ void __launch_bounds__(NT, 2) ssm_grad_kernel(SsmArgs a, int64_t slot
         __syncthreads();
 
         // the wavefront's columns of dB and dC
-        f32x4 ui[QT], vi[QT];
         float hg = 0.f;
-#pragma unroll
-        for (int j = 0; j < QT; ++j) ui[j] = vi[j] = zero4();
         if (wave * KW < KT) {
-            const int64_t cslot = pc.start / Q + pc.seq + pc.n;
-            const int64_t state = (cslot * all_units + unit) * (KT * 16 * PT * 16);
 #pragma unroll
             for (int k = 0; k < KW; ++k) {
-                const int kt = wave * KW + k, kc = 16 * kt + l15;
+                const int lane = renewed(threadIdx.x) % WAVE, l15 = lane & 15, q4 = lane >> 4;
+                const int kt = wave * KW + k;
                 Parts<3> hf[PT / 2], gf[PT / 2];
 #pragma unroll
                 for (int pp = 0; pp < PT / 2; ++pp) {
-                    const int64_t o = state + (int64_t)kc * (PT * 16) + 32 * pp + 8 * q4;
-                    const Pack<float, 8> hv = load_v<8>(a.hs + o), gv = load_v<8>(a.gs + o);
                     float hx[8], gx[8];
-                    get_v(hv, hx);
-                    get_v(gv, gx);
+                    get_v(hv[pp], hx);
+                    get_v(gv[pp], gx);
 #pragma unroll
                     for (int r = 0; r < 8; ++r) hg += hx[r] * gx[r];
                     hf[pp] = split8<3>(hx);
                     gf[pp] = split8<3>(gx);
                 }
+                if (k + 1 < KW) states(k + 1);
 #pragma unroll
                 for (int j = 0; j < QT; ++j) {
                     f32x4 tc = zero4(), tb = zero4();
@@ -711,19 +768,27 @@ __global__ void __launch_bounds__(NT, 2) ssm_grad_kernel(SsmArgs a, int64_t slot
                     const f32x4 from = *reinterpret_cast<const f32x4*>(&dec.from[t]);
                     const f32x4 to = *reinterpret_cast<const f32x4*>(&dec.to[t]);
                     const f32x4 src = *reinterpret_cast<const f32x4*>(&dec.src[t]);
+                    f32x4 cv = zero4(), bv = zero4();
+#pragma unroll
+                    for (int m = NP - 1; m >= 0; --m) {
+                        const bf16x4 c = tr4(sc + m * PLK + 16 * kt, LDK, t, lane), b = tr4(sb + m * PLK + 16 * kt, LDK, t, lane);
+#pragma unroll
+                        for (int r = 0; r < 4; ++r) {
+                            cv[r] += (float)c[r];
+                            bv[r] += (float)b[r];
+                        }
+                    }
 #pragma unroll
                     for (int r = 0; r < 4; ++r) {
-                        float cv = 0.f, bv = 0.f;
-#pragma unroll
-                        for (int m = NP - 1; m >= 0; --m) {
-                            cv += (float)sc[m * PLK + (t + r) * LDK + kc];
-                            bv += (float)sb[m * PLK + (t + r) * LDK + kc];
-                        }
                         const float c = tc[r] * from[r], b = tb[r] * to[r];
-                        ui[j][r] += cv * c;
-                        vi[j][r] += bv * b;
                         dC[j][k][r] += c;
                         dB[j][k][r] += b * src[r];
+                        // the wavefront's columns so far, in its own row
+                        const float u = sum16(cv[r] * c), v = sum16(bv[r] * b);
+                        if (l15 == 0) {
+                            sum.ui[wave][t + r] = k ? sum.ui[wave][t + r] + u : u;
+                            sum.vi[wave][t + r] = k ? sum.vi[wave][t + r] + v : v;
+                        }
                     }
                 }
 #pragma unroll
@@ -753,16 +818,6 @@ __global__ void __launch_bounds__(NT, 2) ssm_grad_kernel(SsmArgs a, int64_t slot
                 }
             }
         }
-#pragma unroll
-        for (int j = 0; j < QT; ++j)
-#pragma unroll
-            for (int r = 0; r < 4; ++r) {
-                const float u = lanes_sum<16>(ui[j][r]), v = lanes_sum<16>(vi[j][r]);
-                if (l15 == 0) {
-                    sum.ui[wave][16 * j + 4 * q4 + r] = u;
-                    sum.vi[wave][16 * j + 4 * q4 + r] = v;
-                }
-            }
         hg = lanes_sum<WAVE>(hg);
         if (lane == 0) sum.hg[wave] = hg;
         __syncthreads();
@@ -775,8 +830,10 @@ __global__ void __launch_bounds__(NT, 2) ssm_grad_kernel(SsmArgs a, int64_t slot
 #pragma unroll
                 for (int w = 0; w < WAVES; ++w) {
                     if (w < QT) c += sum.col[w][lane];
-                    u += sum.ui[w][lane];
-                    v += sum.vi[w][lane];
+                    if (w * KW < KT) {
+                        u += sum.ui[w][lane];
+                        v += sum.vi[w][lane];
+                    }
                 }
                 const float d = dec.src[lane];
                 rows = (double)sum.row[lane] + u;
