@@ -33,27 +33,44 @@ constexpr int NT = WAVES * WAVE;
 constexpr float LOG2E = 1.4426950408889634f;
 
 template <typename DT> struct Cfg;
-template <> struct Cfg<bf16> { static constexpr int QT = 4, NP = 1, MP = 2, HP = 2; };
+// QT: 16-token tiles of a chunk; parts of inputs (NP), of the masked products (MP), of the state where it is an
+// operand of a result (HP)
+template <> struct Cfg<bf16> { static constexpr int QT = 4, NP = 1, MP = 1, HP = 1; };
 template <> struct Cfg<float> { static constexpr int QT = 2, NP = 3, MP = 3, HP = 3; };
 
 template <int V> struct Int { static constexpr int value = V; };
 typedef short s16x4 __attribute__((ext_vector_type(4)));
 
+typedef float f32x2 __attribute__((ext_vector_type(2)));
+typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+
+// Two values as bf16 in one register, one instruction; and back, exactly.
+__device__ __forceinline__ uint32_t pack2(float a, float b) {
+    return __builtin_bit_cast(uint32_t, __builtin_convertvector((f32x2{a, b}), bf16x2));
+}
+__device__ __forceinline__ float low_of(uint32_t v) { return __uint_as_float(v << 16); }
+__device__ __forceinline__ float high_of(uint32_t v) { return __uint_as_float(v & 0xffff0000u); }
+
 // The sum of N bf16 parts that stands for v.
 template <int N> struct Parts { bf16x8 p[N]; };
 template <int N> __device__ __forceinline__ Parts<N> split8(const float (&in)[8]) {
+    typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
     Parts<N> o;
     float v[8];
 #pragma unroll
     for (int i = 0; i < 8; ++i) v[i] = in[i];
 #pragma unroll
     for (int n = 0; n < N; ++n) {
+        u32x4 w;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) o.p[n][i] = (bf16)v[i];
-        if (n + 1 < N) {
-#pragma unroll
-            for (int i = 0; i < 8; ++i) v[i] -= (float)o.p[n][i];
+        for (int i = 0; i < 4; ++i) {
+            w[i] = pack2(v[2 * i], v[2 * i + 1]);
+            if (n + 1 < N) {
+                v[2 * i] -= low_of(w[i]);
+                v[2 * i + 1] -= high_of(w[i]);
+            }
         }
+        o.p[n] = __builtin_bit_cast(bf16x8, w);
     }
     return o;
 }
@@ -174,9 +191,9 @@ __device__ __forceinline__ double lanes_scan(double v, int lane) {
 // The decays of a chunk, one token a lane: c (or r, reversed) as hi + lo, the weight of a
 // token as a source, and its derivatives' factors.
 template <int Q> struct Decays {
-    float hi[Q], lo[Q], src[Q], scale[Q], from[Q], to[Q];
+    float hi[Q], lo[Q], src[Q], scale[Q], from[Q], to[Q], c[Q], less[Q];
     // src: weight of the token's product (d, reversed 1); scale: of its result (1, reversed d);
-    // from: 2^{c}; to: 2^{total - c} (src not included)
+    // from: 2^{c}; to: 2^{total - c} (src not included); c; less: c - log2(src)
 };
 template <int Q>
 __device__ __forceinline__ double decays(Decays<Q>& w, const SsmArgs& a, int h, int first, int dir, int n, bool rev, int lane) {
@@ -195,6 +212,8 @@ __device__ __forceinline__ double decays(Decays<Q>& w, const SsmArgs& a, int h, 
         w.lo[lane] = (float)(c - hi);
         w.src[lane] = lane < n ? (rev ? 1.f : d) : 0.f;
         w.scale[lane] = rev ? d : 1.f;
+        w.c[lane] = (float)c;
+        w.less[lane] = (float)(c - (double)__log2f(w.src[lane]));
         w.from[lane] = exp2f((float)c);
         w.to[lane] = exp2f((float)(total - c));
     }
@@ -401,7 +420,7 @@ __global__ void __launch_bounds__(NT, 2) ssm_walk_kernel(SsmArgs a, const DT* va
 #pragma unroll
                     for (int m = 0; m < NP; ++m)
                         qf[kk].p[m] = row_paired(squery + m * PLK + t * LDK + 32 * kk, lane);
-                const float hi = dec.hi[t], lo = dec.lo[t];
+                const float ct = dec.c[t], hi = dec.hi[t], lo = dec.lo[t];
 #pragma unroll
                 for (int i2 = 0; i2 <= j / 2; ++i2) {
                     float m8[8];
@@ -422,14 +441,22 @@ __global__ void __launch_bounds__(NT, 2) ssm_walk_kernel(SsmArgs a, const DT* va
                                 kf.p[m] = row_paired(skey + m * PLK + (16 * i + l15) * LDK + 32 * kk, lane);
                             s = mma_parts(kf, qf[kk], s);
                         }
-                        const f32x4 shi = *reinterpret_cast<const f32x4*>(&dec.hi[16 * i + 4 * q4]);
-                        const f32x4 slo = *reinterpret_cast<const f32x4*>(&dec.lo[16 * i + 4 * q4]);
-                        const f32x4 src = *reinterpret_cast<const f32x4*>(&dec.src[16 * i + 4 * q4]);
+                        if constexpr (NP == 1) {
+                            const f32x4 less = *reinterpret_cast<const f32x4*>(&dec.less[16 * i + 4 * q4]);
 #pragma unroll
-                        for (int r = 0; r < 4; ++r) {
-                            const float e = __builtin_amdgcn_exp2f((hi - shi[r]) + (lo - slo[r]));
-                            const float v = s[r] * (e * src[r]);
-                            m8[4 * half + r] = i < j || 4 * q4 + r <= l15 ? v : 0.f;
+                            for (int r = 0; r < 4; ++r) {
+                                const float v = s[r] * __builtin_amdgcn_exp2f(ct - less[r]);
+                                m8[4 * half + r] = i < j || 4 * q4 + r <= l15 ? v : 0.f;
+                            }
+                        } else {
+                            const f32x4 shi = *reinterpret_cast<const f32x4*>(&dec.hi[16 * i + 4 * q4]);
+                            const f32x4 slo = *reinterpret_cast<const f32x4*>(&dec.lo[16 * i + 4 * q4]);
+                            const f32x4 src = *reinterpret_cast<const f32x4*>(&dec.src[16 * i + 4 * q4]);
+#pragma unroll
+                            for (int r = 0; r < 4; ++r) {
+                                const float v = s[r] * (__builtin_amdgcn_exp2f((hi - shi[r]) + (lo - slo[r])) * src[r]);
+                                m8[4 * half + r] = i < j || 4 * q4 + r <= l15 ? v : 0.f;
+                            }
                         }
                     }
                     const Parts<MP> mf = split8<MP>(m8);
@@ -453,9 +480,10 @@ __global__ void __launch_bounds__(NT, 2) ssm_walk_kernel(SsmArgs a, const DT* va
                         zero_v(o);
 #pragma unroll
                         for (int m = NP - 1; m >= 0; --m) {
-                            const bf16x4 v = *reinterpret_cast<const bf16x4*>(sval + m * PLP + t * LDP + c);
+                            const uint2 v = *reinterpret_cast<const uint2*>(sval + m * PLP + t * LDP + c);
+                            const float f[4] = {low_of(v.x), high_of(v.x), low_of(v.y), high_of(v.y)};
 #pragma unroll
-                            for (int r = 0; r < 4; ++r) o[r] += (float)v[r];
+                            for (int r = 0; r < 4; ++r) o[r] = m + 1 < NP ? o[r] + f[r] : f[r];
                         }
 #pragma unroll
                         for (int r = 0; r < 4; ++r) o[r] = scale * acc[j][p][r] + dskip * o[r];
@@ -494,7 +522,7 @@ __global__ void __launch_bounds__(NT, 2) ssm_walk_kernel(SsmArgs a, const DT* va
                 for (int m = NP - 1; m >= 0; --m) {
                     const bf16x8 b = col_paired(sval + m * PLP + 32 * i2 * LDP + 16 * p, LDP, lane);
 #pragma unroll
-                    for (int r = 0; r < 8; ++r) v[r] += (float)b[r];
+                    for (int r = 0; r < 8; ++r) v[r] = m + 1 < NP ? v[r] + (float)b[r] : (float)b[r];
                 }
 #pragma unroll
                 for (int r = 0; r < 8; ++r) v[r] *= w[r];
@@ -774,8 +802,8 @@ __global__ void __launch_bounds__(NT, 2) ssm_grad_kernel(SsmArgs a, int64_t slot
                         const bf16x4 c = tr4(sc + m * PLK + 16 * kt, LDK, t, lane), b = tr4(sb + m * PLK + 16 * kt, LDK, t, lane);
 #pragma unroll
                         for (int r = 0; r < 4; ++r) {
-                            cv[r] += (float)c[r];
-                            bv[r] += (float)b[r];
+                            cv[r] = m + 1 < NP ? cv[r] + (float)c[r] : (float)c[r];
+                            bv[r] = m + 1 < NP ? bv[r] + (float)b[r] : (float)b[r];
                         }
                     }
 #pragma unroll

@@ -9,8 +9,12 @@ term's absolute value.  What may be off, relative to a term:
                  exponential, of which a term meets 4 (into its chunk's end, chunks and segments between,
                  into its own): (10 |L| + 16) u.  As L e^-L <= 0.74 e^-(L / 2), the part with L is at most
                  7.4 u times the same sum with half the decay.
-  parts          a value in two bf16 parts is held to 2^-18 = 64 u, in three to 2^-26; products of parts below
-                 2^-24 left out: 4 u.  A bf16 result meets up to two roundings to two parts: 128 u.
+  parts          a value in three bf16 parts is held to 2^-26; products of parts below 2^-24 left out: 4 u.
+  bf16 results   y and dx are sums of products with the masked weights (C . B) decay d, and with the state; both
+                 are held in fp32 and rounded once to bf16 as operands, as dB's and dC's weights are.
+                 Each term of the sum has one of them as a factor, so it is off by at most half a
+                 step of bf16, 2^-8 = 2^16 u, relative: 2^16 mag in all, whatever the number of terms.  States,
+                 dt, A, D and h0's gradients do not pass such a rounding.
   sums           one rounding an addition.  A chunk adds 32 products in each of 6 instructions to a state
                  tile: 192 roundings in a chunk of 32 tokens (fp32), the same in 64 (bf16): at most 6 u a
                  token.  A result adds K state rows (6 products each in fp32) and a chunk's 64 tokens;
@@ -43,8 +47,11 @@ def ssm(x, dt, A, B, C, D, h0, cu):
     return (torch.stack(ys) if ys else torch.zeros(0, H, P, dtype=F8)), torch.stack(hs)
 
 
-def ssm_bounds(x, z, A, B, C, D, bias, h0, cu, soft=True):
-    """Values and bounds of y and h_T."""
+BF_OPERAND = 2.0 ** 16  # half a step of bf16 in units of u
+
+
+def ssm_bounds(x, z, A, B, C, D, bias, h0, cu, soft=True, dtype=torch.float32):
+    """Values and bounds of y and h_T; dtype is that of x."""
     d = softplus(z + bias) if soft else z + bias
     y, h = ssm(x, d, A, B, C, D, h0, cu)
     K, T = B.shape[2], max([b - a for a, b in zip(cu[:-1], cu[1:])] + [0])
@@ -52,7 +59,9 @@ def ssm_bounds(x, z, A, B, C, D, bias, h0, cu, soft=True):
     full = ssm(m[0], d, A, m[1], m[2], m[3], m[4], cu)
     half = ssm(m[0], d, A / 2, m[1], m[2], m[3], m[4], cu)
     R = 224 + 8 * (6 * K + 64) + 6 * T
-    return {"y": y, "h": h}, {"y": R * full[0] + 8 * half[0], "h": R * full[1] + 8 * half[1]}
+    return {"y": y, "h": h}, {"y": R * full[0] + 8 * half[0], "h": R * full[1] + 8 * half[1]} \
+        if dtype == torch.float32 else \
+        {"y": (R + BF_OPERAND) * full[0] + 8 * half[0], "h": R * full[1] + 8 * half[1]}
 
 
 def _grads(x, z, A, B, C, D, bias, h0, cu, dy, dhT, soft, scale=1.0):
@@ -103,7 +112,7 @@ def ssm_grad_mag(x, z, A, B, C, D, bias, h0, cu, dy, dhT, soft, scale=1.0):
             "dD": (x * dy).sum((0, 2)), "ddt_bias": ddt.sum(0), "dh0": out["dh0"]}
 
 
-def ssm_grad_bounds(x, z, A, B, C, D, bias, h0, cu, dy, dhT, soft=True):
+def ssm_grad_bounds(x, z, A, B, C, D, bias, h0, cu, dy, dhT, soft=True, dtype=torch.float32):
     val = _grads(x, z, A, B, C, D, bias, h0, cu, dy, dhT, soft)
     full = ssm_grad_mag(x, z, A, B, C, D, bias, h0, cu, dy, dhT, soft)
     half = ssm_grad_mag(x, z, A, B, C, D, bias, h0, cu, dy, dhT, soft, 0.5)
@@ -115,6 +124,8 @@ def ssm_grad_bounds(x, z, A, B, C, D, bias, h0, cu, dy, dhT, soft=True):
     bound = {}
     for k in val:
         bound[k] = R * full[k] + 16 * half[k]
+        if dtype != torch.float32 and k in ("dx", "dB", "dC"):
+            bound[k] = bound[k] + BF_OPERAND * full[k]
     # The derivative of a log decay is a sum over pairs of tokens around it, formed as running sums of the chunk's
     # row and column sums, in which every other pair cancels: the same products are in both, but the additions
     # and factors behind them (64 + 16 roundings of a row's, of a column's sum) are not.

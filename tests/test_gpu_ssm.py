@@ -28,6 +28,14 @@ def make(lengths, size, dtype, seed, fast=False):
     return v, r(T, H, P).to(dtype), r(N, H, K, P) * 0.2
 
 
+def bounds(v, lengths, **kw):
+    return M.ssm_bounds(*cpu8(v), bounds_of(lengths), dtype=v["x"].dtype, **kw)
+
+
+def grad_bounds(v, lengths, dy, dhT, **kw):
+    return M.ssm_grad_bounds(*cpu8(v), bounds_of(lengths), dy.double(), dhT.double(), dtype=v["x"].dtype, **kw)
+
+
 def cpu8(v):
     return [v[k].double() for k in ("x", "dt", "A", "B", "C", "D", "dt_bias", "h0")]
 
@@ -61,7 +69,7 @@ def test_forward(lens, size, dtype):
     lengths = LENS[lens]
     log(f"ssm forward {lens} {size} {dtype}")
     v, _, _ = make(lengths, size, dtype, 3)
-    val, bnd = M.ssm_bounds(*cpu8(v), bounds_of(lengths))
+    val, bnd = bounds(v, lengths)
     d = dev(v)
     y, h = call(d, cud(lengths))
     w = [M.check(y, val["y"], bnd["y"], "y"), M.check(h, val["h"], bnd["h"], "h_T")]
@@ -78,7 +86,7 @@ def test_gradient(lens, size, dtype):
     lengths = LENS[lens]
     log(f"ssm gradient {lens} {size} {dtype}")
     v, dy, dhT = make(lengths, size, dtype, 4)
-    val, bnd = M.ssm_grad_bounds(*cpu8(v), bounds_of(lengths), dy.double(), dhT.double())
+    val, bnd = grad_bounds(v, lengths, dy, dhT)
     d, dyd, dhd = dev(v), dy.to(DEV), dhT.to(DEV)
     got = grad(d, dyd, cud(lengths), dhd)
     w = {k: M.check(got[k], val[k], bnd[k], k) for k in val}
@@ -100,12 +108,11 @@ def test_any_decay(dtype):
     v["dt"][30:90, 1] = 7.0      # a long steep stretch, then mild tokens
     v["dt"][::3, 2] = 0.0
     v["dt"][100, 3] = 5.0
-    args = cpu8(v)
-    val, bnd = M.ssm_bounds(*args, bounds_of(lengths), soft=False)
+    val, bnd = bounds(v, lengths, soft=False)
     d, cu = dev(v), cud(lengths)
     y, h = call(d, cu, softplus=False)
     M.check(y, val["y"], bnd["y"], "y"), M.check(h, val["h"], bnd["h"], "h_T")
-    val, bnd = M.ssm_grad_bounds(*args, bounds_of(lengths), dy.double(), dhT.double(), soft=False)
+    val, bnd = grad_bounds(v, lengths, dy, dhT, soft=False)
     got = grad(d, dy.to(DEV), cu, dhT.to(DEV), softplus=False)
     for k in val:
         M.check(got[k], val[k], bnd[k], k)
@@ -115,7 +122,7 @@ def test_optional_arguments():
     lengths, size = [70, 20], (4, 2, 16, 24)
     v, dy, dhT = make(lengths, size, F4, 6)
     zero = dict(v, D=torch.zeros(4), dt_bias=torch.zeros(4), h0=torch.zeros_like(v["h0"]))
-    val, bnd = M.ssm_bounds(*cpu8(zero), bounds_of(lengths))
+    val, bnd = bounds(zero, lengths)
     d, cu = dev(dict(v, dt_bias=v["dt_bias"])), cud(lengths)
     none = dict(d, D=None, dt_bias=None, h0=None)
     y, h = call(none, cu)
