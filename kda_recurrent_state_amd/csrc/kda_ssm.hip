@@ -30,7 +30,7 @@ namespace {
 
 constexpr int WAVES = 4;
 constexpr int NT = WAVES * WAVE;
-constexpr float LOG2E = 1.4426950408889634f;
+constexpr int WALK = 32;  // tokens of a chunk of the walk
 
 template <typename DT> struct Cfg;
 // QT: 16-token tiles of a chunk; parts of inputs (NP), of the masked products (MP), of the state where it is an
@@ -122,29 +122,31 @@ __device__ __forceinline__ bf16x8 col_natural(const bf16* m, int ld, int lane) {
 template <typename DT, int ROWS, int COLS, int THREADS> struct Stage {
     static constexpr int NP = Cfg<DT>::NP, PER = COLS / 8, ALL = ROWS * PER, CNT = (ALL + THREADS - 1) / THREADS;
     Pack<DT, 8> v[CNT];
-    // row r is token first + r * dir, r < n (n > 0)
-    __device__ __forceinline__ void load(const DT* src, int64_t stride, int cols, int first, int dir, int n, int tid) {
-        if (cols == COLS) {
-            const DT* base = src + (int64_t)first * stride;
-            const int step = (int)stride * dir;
+    // Row r is token t0 + r (reversed: the last of the n from t0 on minus r), r < n, n > 0.  Everything but tid is
+    // uniform: offsets of lanes are 32 bits from a scalar address, where the stride allows it.
+    __device__ __forceinline__ void load(const DT* src, int64_t stride, int cols, int t0, bool rev, int n, unsigned tid) {
+        if (cols == COLS && stride < 1 << 22) {
+            const char* base = reinterpret_cast<const char*>(src + (int64_t)t0 * stride);
 #pragma unroll
             for (int i = 0; i < CNT; ++i) {
-                const int at = i * THREADS + tid, r = min(at / PER, n - 1), c = at % PER * 8;
-                if (ALL % THREADS == 0 || at < ALL) v[i] = load_v<8>(base + ((int64_t)r * step + c));
+                const unsigned at = i * THREADS + tid, row = at / PER, c = at % PER * 8;
+                const unsigned r = rev ? max((int)(n - 1 - row), 0) : min((int)row, n - 1);
+                if (ALL % THREADS == 0 || at < ALL)
+                    v[i] = load_v<8>(reinterpret_cast<const DT*>(base + (__umul24(r, (unsigned)stride) + c) * (unsigned)sizeof(DT)));
             }
             if (n < ROWS) {
 #pragma unroll
                 for (int i = 0; i < CNT; ++i)
-                    if ((i * THREADS + tid) / PER >= n) clear(v[i]);
+                    if ((int)((i * THREADS + tid) / PER) >= n) clear(v[i]);
             }
             return;
         }
 #pragma unroll
         for (int i = 0; i < CNT; ++i) {
-            const int at = i * THREADS + tid, r = at / PER, c = at % PER * 8;
+            const int at = i * THREADS + (int)tid, r = at / PER, c = at % PER * 8;
             clear(v[i]);
             if (r < n && c < cols && at < ALL) {
-                const DT* p = src + (int64_t)(first + r * dir) * stride + c;
+                const DT* p = src + (int64_t)(rev ? t0 + n - 1 - r : t0 + r) * stride + c;
                 if (c + 8 <= cols) {
                     v[i] = load_v<8>(p);
                 } else {
@@ -154,12 +156,30 @@ template <typename DT, int ROWS, int COLS, int THREADS> struct Stage {
             }
         }
     }
-    __device__ __forceinline__ void store(bf16* dst, int ld, int plane, int tid) const {
+    __device__ __forceinline__ void store(bf16* dst, int ld, int plane, unsigned tid) const {
 #pragma unroll
         for (int i = 0; i < CNT; ++i) {
-            const int at = i * THREADS + tid, r = at / PER, c = at % PER * 8;
+            const unsigned at = i * THREADS + tid, r = at / PER, c = at % PER * 8;
             if (ALL % THREADS != 0 && at >= ALL) continue;
             bf16* p = dst + r * ld + c;
+            if constexpr (NP == 1) {
+                *reinterpret_cast<bf16x8*>(p) = __builtin_bit_cast(bf16x8, v[i]);
+            } else {
+                float f[8];
+                get_v(v[i], f);
+                const Parts<NP> s = split8<NP>(f);
+#pragma unroll
+                for (int n = 0; n < NP; ++n) *reinterpret_cast<bf16x8*>(p + n * plane) = s.p[n];
+            }
+        }
+    }
+    // the same with the byte of piece p of row r from `place`; plane in bytes
+    template <typename F> __device__ __forceinline__ void store_to(char* dst, int plane, unsigned tid, F place) const {
+#pragma unroll
+        for (int i = 0; i < CNT; ++i) {
+            const unsigned at = i * THREADS + tid;
+            if (ALL % THREADS != 0 && at >= ALL) continue;
+            char* p = dst + place(at / PER, at % PER);
             if constexpr (NP == 1) {
                 *reinterpret_cast<bf16x8*>(p) = __builtin_bit_cast(bf16x8, v[i]);
             } else {
@@ -188,32 +208,26 @@ __device__ __forceinline__ double lanes_scan(double v, int lane) {
     return v;
 }
 
-// The decays of a chunk, one token a lane: c (or r, reversed) as hi + lo, the weight of a
-// token as a source, and its derivatives' factors.
+// The decays of a chunk, one token a lane: c as hi + lo and what comes of it.
 template <int Q> struct Decays {
-    float hi[Q], lo[Q], src[Q], scale[Q], from[Q], to[Q], c[Q], less[Q];
-    // src: weight of the token's product (d, reversed 1); scale: of its result (1, reversed d);
-    // from: 2^{c}; to: 2^{total - c} (src not included); c; less: c - log2(src)
+    float hi[Q], lo[Q], src[Q], from[Q], to[Q];
+    // src: d; from: 2^{c}; to: 2^{total - c}
 };
 template <int Q>
-__device__ __forceinline__ double decays(Decays<Q>& w, const SsmArgs& a, int h, int first, int dir, int n, bool rev, int lane) {
+__device__ __forceinline__ double decays(Decays<Q>& w, const SsmArgs& a, int h, int first, int n, int lane) {
     float d = 0.f;
     double l = 0.0;
     if (lane < n) {
-        const float z = a.dt[(int64_t)(first + lane * dir) * a.dts + h] + (a.bias ? a.bias[h] : 0.f);
+        const float z = a.dt[(int64_t)(first + lane) * a.dts + h] + (a.bias ? a.bias[h] : 0.f);
         d = a.softplus ? softplus_f(z) : z;
         l = fmax((double)d * (double)a.A[h] * 1.4426950408889634, -300.0);
     }
-    const double incl = lanes_scan(l, lane), c = rev ? incl - l : incl;
-    const double total = __shfl(incl, WAVE - 1);
+    const double c = lanes_scan(l, lane), total = __shfl(c, WAVE - 1);
     if (lane < Q) {
         const double hi = rint(c * 256.0) * (1.0 / 256.0);
         w.hi[lane] = (float)hi;
         w.lo[lane] = (float)(c - hi);
-        w.src[lane] = lane < n ? (rev ? 1.f : d) : 0.f;
-        w.scale[lane] = rev ? d : 1.f;
-        w.c[lane] = (float)c;
-        w.less[lane] = (float)(c - (double)__log2f(w.src[lane]));
+        w.src[lane] = d;
         w.from[lane] = exp2f((float)c);
         w.to[lane] = exp2f((float)(total - c));
     }
@@ -259,12 +273,13 @@ __device__ __forceinline__ Piece find_piece(const Seqs& sq, int slot, int every)
 // (slot, group) read the same B and C; every eighth workgroup runs on the same die, so they are
 // given numbers 8 apart.
 struct Place { int slot, group, quad; bool live; };
-__device__ __forceinline__ Place place_of(int b, int64_t slots, int G, int quads) {
-    const int64_t pair = (b & 7) + 8ll * ((b >> 3) / quads);
+__device__ __forceinline__ Place place_of(unsigned b, int slots, int G, int quads) {
+    auto uniform = [](unsigned v) { return (int)__builtin_amdgcn_readfirstlane(v); };
+    const unsigned pair = (b & 7) + 8 * ((b >> 3) / (unsigned)quads);
     Place p;
-    p.quad = (b >> 3) % quads;
-    p.slot = (int)(pair / G);
-    p.group = (int)(pair % G);
+    p.quad = uniform((b >> 3) % (unsigned)quads);
+    p.slot = uniform(pair / (unsigned)G);
+    p.group = uniform(pair % (unsigned)G);
     p.live = p.slot < slots;
     return p;
 }
@@ -274,47 +289,136 @@ constexpr int OUT = 1, EMIT = 2, ENDS = 4;
 
 // A value the compiler takes for a new one.  Addresses that depend on it are formed where they are used
 // and not kept in registers through the walk, where the state leaves no room for them.
-__device__ __forceinline__ int renewed(int v) {
+__device__ __forceinline__ unsigned renewed(unsigned v) {
     asm volatile("" : "+v"(v));
     return v;
 }
 
-// One wavefront per unit walks the chunks of a segment, its state in accumulator tiles [k][p].
-// OUT: writes the results; EMIT: the state before every chunk; ENDS: starts from zero and
-// writes the segment's own state and decay (not for a sequence's last segment).
-template <typename DT, int KT, int PT, int MODE>
-__global__ void __launch_bounds__(NT, 2) ssm_walk_kernel(SsmArgs a, const DT* val, const DT* key, const DT* query,
-                                                         int64_t vs, int64_t ks, int64_t qs, const float* first_state,
-                                                         float* last_state, float* emit, int rev, int64_t slots,
-                                                         int quads) {
-    using C_ = Cfg<DT>;
-    constexpr int QT = C_::QT, Q = QT * 16, NP = C_::NP, MP = C_::MP, HP = C_::HP;
-    constexpr int LDK = KT * 16 + 8, LDP = PT * 16 + 8, PLK = Q * LDK, PLP = Q * LDP;
-    extern __shared__ __attribute__((aligned(16))) char smem[];
-    bf16* skey = reinterpret_cast<bf16*>(smem);
-    bf16* squery = skey + NP * PLK;
-    bf16* sval_all = (MODE & OUT) ? squery + NP * PLK : squery;
-    Decays<Q>* sdec = reinterpret_cast<Decays<Q>*>(sval_all + WAVES * NP * PLP);
+// ROWS rows of COLS bf16 in LDS, their 16-byte pieces exchanged by the row's number so that neither a column of
+// pieces (16 rows at once) nor a block of 8 rows by 16 columns (half a transposing read) meets in a bank.
+template <int COLS> struct Tile {
+    static constexpr int ROW = COLS * 2, PIECES = COLS / 8;
+    static __device__ __forceinline__ int turn(int row) {
+        if constexpr (PIECES >= 16) return (row & 7) << 1 | ((row >> 3) & 1);
+        else if constexpr (PIECES == 8) return ((row >> 1) & 3) << 1 | ((row >> 3) & 1);
+        else if constexpr (PIECES == 4) return ((row >> 2) & 1) << 1 | ((row >> 3) & 1);
+        else return (row >> 3) & 1;
+    }
+    // byte of piece p of a row
+    static __device__ __forceinline__ int at(int row, int p) { return row * ROW + (p ^ turn(row)) * 16; }
+    // 32 contraction indices of a row in the paired order
+    static __device__ __forceinline__ bf16x8 row_paired(const char* m, int row, int k32, int lane) {
+        const int q = lane >> 4;
+        return join(*reinterpret_cast<const bf16x4*>(m + at(row, 4 * k32 + (q >> 1)) + (q & 1) * 8),
+                    *reinterpret_cast<const bf16x4*>(m + at(row, 4 * k32 + 2 + (q >> 1)) + (q & 1) * 8));
+    }
+    // 32 rows as contraction indices of 16 columns in the paired order
+    static __device__ __forceinline__ bf16x8 col_paired(const char* m, int c16, int lane) {
+        typedef __attribute__((address_space(3))) s16x4* lds;
+        const int i = lane & 15, row = 4 * (lane >> 4) + (i >> 2);
+        const char* p = m + at(row, 2 * c16 + ((i & 3) >> 1)) + (i & 1) * 8;  // row + 16 has the same turn
+        return join(__builtin_bit_cast(bf16x4, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds)(p))),
+                    __builtin_bit_cast(bf16x4, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds)(p + 16 * ROW))));
+    }
+};
 
-    const int tid = threadIdx.x, lane = tid % WAVE, wave = __builtin_amdgcn_readfirstlane(tid / WAVE);
+// The waits before this barrier are those for LDS only: loads from memory stay on their way.
+__device__ __forceinline__ void lds_barrier() { asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory"); }
+
+// The decays of a chunk of the walk, for the wavefronts of a head.
+struct WalkDecays {
+    float from[WALK], into[WALK], scale[WALK], c[WALK], less[WALK];
+    // from: 2^{c}; into: 2^{total - c} src; scale: weight of a token's result (1, reversed d); less: c - log2(src),
+    // src the weight of its product (d, reversed 1)
+    float total, pad[3];  // 2^{total}
+};
+struct ExactDecays {  // fp32 only: c as hi + lo
+    float hi[WALK], lo[WALK], src[WALK];
+};
+
+// Two chunks at once, 32 tokens each, a token a lane; returns the sum of both chunks' log decays.
+template <bool EXACT>
+__device__ __forceinline__ double walk_decays(WalkDecays& w, ExactDecays* x, float z, float A, int softplus, bool in,
+                                              bool rev, int lane) {
+    const int u = lane & (WALK - 1);
+    const float d = in ? (softplus ? softplus_f(z) : z) : 0.f;
+    const double l = in ? fmax((double)d * (double)A * 1.4426950408889634, -300.0) : 0.0;
+    double incl = l;
+#pragma unroll
+    for (int m = 1; m < WALK; m <<= 1) {
+        const double t = __shfl_up(incl, m, WALK);
+        if (u >= m) incl += t;
+    }
+    const double c = rev ? incl - l : incl, total = __shfl(incl, WALK - 1, WALK);
+    const float src = in ? (rev ? 1.f : d) : 0.f;
+    w.from[u] = exp2f((float)c);
+    w.into[u] = exp2f((float)(total - c)) * src;
+    w.scale[u] = rev ? d : 1.f;
+    w.c[u] = (float)c;
+    w.less[u] = (float)(c - (double)__log2f(src));
+    if (u == 0) w.total = exp2f((float)total);
+    if (EXACT) {
+        const double hi = rint(c * 256.0) * (1.0 / 256.0);
+        x->hi[u] = (float)hi;
+        x->lo[u] = (float)(c - hi);
+        x->src[u] = src;
+    }
+    return total + __shfl_xor(total, WALK);
+}
+
+// One wavefront per unit walks the chunks of a segment, its state in accumulator tiles [k][p].
+// OUT: writes the results; EMIT: the state before every chunk of a.chunk tokens; ENDS: starts from zero and
+// writes the segment's own state and decay (not for a sequence's last segment).
+//
+// A unit is narrow, 64 registers of state, so that three wavefronts share a SIMD: with twice the columns two did,
+// and waited for LDS most of their time (2 x 32768 tokens of 32 heads: 560 us against NEW_US).  The wavefronts of a
+// workgroup that have the same head form the masked products once between them, in LDS.  Chunks of 32 tokens;
+// with bf16 inputs the next chunk's rows are on their way in registers while one is multiplied.
+template <typename DT, int KT, int PT, int MODE>
+__global__ void __launch_bounds__(NT, sizeof(DT) == 2 ? 3 : 2)
+ssm_walk_kernel(SsmArgs a, const DT* val, const DT* key, const DT* query, int64_t vs, int64_t ks, int64_t qs,
+                const float* first_state, float* last_state, float* emit, int rev, int slots, int quads) {
+    using C_ = Cfg<DT>;
+    using TK = Tile<KT * 16>;
+    using TP = Tile<PT * 16>;
+    constexpr int Q = WALK, NP = C_::NP, MP = C_::MP, HP = C_::HP;
+    constexpr bool AHEAD = NP == 1;
+    constexpr int PLK = Q * TK::ROW, PLP = Q * TP::ROW, PLM = Q * Q * 2;  // bytes of a plane
+    constexpr int KEYS = NP * PLK, QUERIES = (MODE & OUT) ? KEYS : 0, VALS = NP * PLP, MASKED = (MODE & OUT) ? MP * PLM : 0;
+    extern __shared__ __attribute__((aligned(16))) char smem[];
+    char* const skey = smem;
+    char* const squery = skey + KEYS;
+    char* const svals = squery + QUERIES;
+    char* const smasked = svals + WAVES * VALS;
+    WalkDecays* const sdec = reinterpret_cast<WalkDecays*>(smasked + WAVES * MASKED);  // [head][chunk & 3]
+    ExactDecays* const sexact = reinterpret_cast<ExactDecays*>(sdec + 4 * WAVES);
+
+    const int lane = threadIdx.x % WAVE, wave = __builtin_amdgcn_readfirstlane(threadIdx.x / WAVE);
     const int l15 = lane & 15, q4 = lane >> 4;
     const Place at = place_of(blockIdx.x, slots, a.G, quads);
     if (!at.live) return;
     const Seqs sq{a.cu, a.N, a.T, a.eq};
     const Piece pc = find_piece(sq, at.slot, a.seg);
     if (!pc.live) return;
-    const int per = a.H / a.G, units = per * a.blocks, unit_in = at.quad * WAVES + wave;
+    const int per = a.H / a.G, units = per * a.wblocks, unit_in = at.quad * WAVES + wave;
     const bool mine = unit_in < units;
     const int unit = at.group * units + (mine ? unit_in : 0);
-    const int h = unit / a.blocks, p0 = unit % a.blocks * (PT * 16);
+    const int h = unit / a.wblocks, block = unit % a.wblocks, p0 = block * (PT * 16);
+    // the workgroup's wavefronts with this head: `team` of them from `lead` on, this one the who-th
+    const int lead = mine ? max(wave - block, 0) : wave, who = wave - lead;
+    const int team = mine ? min(min(lead + a.wblocks - (block - who), WAVES), units - at.quad * WAVES) - lead : 1;
+    const bool decides = mine && who == team - 1;  // forms the head's decays
+    const int share = team == 1 ? 7 : team == 2 ? (who ? 2 : 5) : who < 3 ? 1 << who : 0;  // of the masked products' tiles
     const int segs = max((pc.len + a.seg - 1) / a.seg, 1);
     const bool is_last = pc.n == (rev ? 0 : segs - 1), is_first = pc.n == (rev ? segs - 1 : 0);
     if ((MODE & ENDS) && is_last) return;
     const int t0 = pc.n * a.seg, t1 = min(t0 + a.seg, pc.len), chunks = (t1 - t0 + Q - 1) / Q;
-    const int64_t frag = ((int64_t)at.slot * a.H * a.blocks + unit) * (KT * PT * WAVE) + lane;
+    const int64_t frag = ((int64_t)at.slot * a.H * a.wblocks + unit) * (KT * PT * WAVE) + lane;
 
-    bf16* sval = sval_all + wave * NP * PLP;
-    Decays<Q>& dec = sdec[wave];
+    char* const sval = svals + wave * VALS;
+    char* const sm = smasked + lead * MASKED;
+    WalkDecays* const dec = sdec + 4 * lead;
+    ExactDecays* const exact = sexact + 4 * lead;
     f32x4 st[KT][PT];
 #pragma unroll
     for (int k = 0; k < KT; ++k)
@@ -336,206 +440,253 @@ __global__ void __launch_bounds__(NT, 2) ssm_walk_kernel(SsmArgs a, const DT* va
 #pragma unroll
                     for (int r = 0; r < 4; ++r) {
                         const int kk = 16 * k + 4 * q4 + r, pp = p0 + 16 * p + l15;
-                        if (kk < a.K && pp < a.P) st[k][p][r] = f[(int64_t)kk * a.P + pp];
+                        if (kk < a.K && pp < a.P) st[k][p][r] = f[kk * a.P + pp];
                     }
         }
     }
+    if (MODE & OUT) {  // the tile above the diagonal stays zero
+        for (int i = threadIdx.x * 16; i < WAVES * MASKED; i += NT * 16) *reinterpret_cast<f32x4*>(smasked + i) = zero4();
+    }
     const float dskip = (MODE & OUT) && a.D && mine ? a.D[h] : 0.f;
+    const float A = a.A[h], bias = a.bias ? a.bias[h] : 0.f;
     double log_decay = 0.0;
 
+    // chunk ci in the order of the walk: its first token in that order, and how many it has
+    struct Chunk { int index, t0, first, n; };
+    auto chunk_at = [&](int ci) {
+        Chunk c;
+        c.index = rev ? chunks - 1 - ci : ci;
+        c.t0 = pc.start + t0 + c.index * Q;
+        c.n = min(Q, pc.start + t1 - c.t0);
+        c.first = rev ? c.t0 + c.n - 1 : c.t0;
+        return c;
+    };
+    const int dir = rev ? -1 : 1;
+    // dt of chunks ci and ci + 1, a token a lane
+    auto steps_of = [&](int ci) {
+        const Chunk c = chunk_at(ci + (lane >> 5));
+        const bool in = ci + (lane >> 5) < chunks && (lane & 31) < c.n;
+        return in ? a.dt[(int64_t)(c.first + (lane & 31) * dir) * a.dts + h] : 0.f;
+    };
+    auto decays_of = [&](int ci, float raw) {
+        const Chunk c = chunk_at(ci + (lane >> 5));
+        const bool in = ci + (lane >> 5) < chunks && (lane & 31) < c.n;
+        const int to = (ci & 2) + (lane >> 5);
+        log_decay += walk_decays<NP != 1>(dec[to], &exact[to], raw + bias, A, a.softplus, in, rev, lane);
+    };
+
+    Stage<DT, Q, KT * 16, NT> bk, bq;
+    Stage<DT, Q, PT * 16, WAVE> bv;
+    auto load = [&](const Chunk& c) {
+        const unsigned tid = renewed(threadIdx.x);
+        bk.load(key + (int64_t)at.group * a.K, ks, a.K, c.t0, rev, c.n, tid);
+        if (MODE & OUT) bq.load(query + (int64_t)at.group * a.K, qs, a.K, c.t0, rev, c.n, tid);
+        bv.load(val + (int64_t)h * a.P + p0, vs, min(a.P - p0, PT * 16), c.t0, rev, c.n, tid % WAVE);
+    };
+    auto store = [&]() {
+        const unsigned tid = renewed(threadIdx.x);
+        bk.store_to(skey, PLK, tid, [](int r, int p) { return TK::at(r, p); });
+        if (MODE & OUT) bq.store_to(squery, PLK, tid, [](int r, int p) { return TK::at(r, p); });
+        bv.store_to(sval, PLP, tid % WAVE, [](int r, int p) { return TP::at(r, p); });
+    };
+    float raw = 0.f;
+    if (chunks > 0) {
+        if (AHEAD) load(chunk_at(0));
+        if (decides) {
+            raw = steps_of(0);
+            decays_of(0, raw);
+        }
+    }
+
     for (int ci = 0; ci < chunks; ++ci) {
-        const int cc = rev ? chunks - 1 - ci : ci;
-        const int c0 = pc.start + t0 + cc * Q, n = min(Q, pc.start + t1 - c0);
-        const int first = rev ? c0 + n - 1 : c0, dir = rev ? -1 : 1;
-        if (ci) __syncthreads();  // the last chunk's tiles are read
-        float total;
-        {
-            const int tid = renewed(threadIdx.x), lane = tid % WAVE;
-            Stage<DT, Q, KT * 16, NT> bk, bq;
-            Stage<DT, Q, PT * 16, WAVE> bv;
-            bk.load(key + (int64_t)at.group * a.K, ks, a.K, first, dir, n, tid);
-            if (MODE & OUT) bq.load(query + (int64_t)at.group * a.K, qs, a.K, first, dir, n, tid);
-            bv.load(val + (int64_t)h * a.P + p0, vs, min(a.P - p0, PT * 16), first, dir, n, lane);
-            const double lt = decays<Q>(dec, a, h, first, dir, n, rev, lane);
-            log_decay += lt;
-            total = exp2f((float)lt);
-            bk.store(skey, LDK, PLK, tid);
-            if (MODE & OUT) bq.store(squery, LDK, PLK, tid);
-            bv.store(sval, LDP, PLP, lane);
-        }
-        __syncthreads();
-        if (!mine) continue;
+        const Chunk c = chunk_at(ci);
+        const int first = c.first, n = c.n;
+        if (!AHEAD) load(c);
+        if (ci) lds_barrier();  // the last chunk's tiles are read
+        store();
+        lds_barrier();
+        if (AHEAD && ci + 1 < chunks) load(chunk_at(ci + 1));
+        if (decides && !(ci & 1)) raw = steps_of(ci + 2);
+        const WalkDecays& w = dec[ci & 3];
 
-        if (MODE & EMIT) {
-            const int64_t cslot = pc.start / Q + pc.seq + (t0 / Q + cc);
-            float* e = emit + (cslot * a.H * a.blocks + unit) * (KT * 16 * PT * 16);
-            const int own = renewed(4 * q4 * (PT * 16) + l15);
+        if ((MODE & EMIT) && mine) {
+            const int ev = a.chunk / Q;
+            if (rev ? c.index % ev == ev - 1 || ci == 0 : c.index % ev == 0) {
+                const int64_t cslot = pc.start / a.chunk + pc.seq + (t0 / a.chunk + c.index / ev);
+                const int wide = a.blocks * a.cols;
+                float* e = emit + (cslot * a.H + h) * ((int64_t)KT * 16 * wide) + p0;
+                const int own = renewed(4 * q4 * wide + l15);
 #pragma unroll
-            for (int k = 0; k < KT; ++k)
+                for (int k = 0; k < KT; ++k)
 #pragma unroll
-                for (int p = 0; p < PT; ++p)
+                    for (int r = 0; r < 4; ++r)
 #pragma unroll
-                    for (int r = 0; r < 4; ++r) e[own + (16 * k + r) * (PT * 16) + 16 * p] = st[k][p][r];
+                        for (int p = 0; p < PT; ++p) e[own + (16 * k + r) * wide + 16 * p] = st[k][p][r];
+            }
         }
 
+        f32x4 acc[2][PT];  // results transposed, [p][t]: a lane holds 4 neighbouring columns of token 16 j + l15
         if constexpr ((MODE & OUT) != 0) {
-            // results transposed, [p][t]: a lane holds 4 neighbouring columns of token 16 j + l15
-            f32x4 acc[QT][PT];
+            if (mine) {
+                // this wavefront's share of the masked products' three tiles
 #pragma unroll
-            for (int j = 0; j < QT; ++j)
+                for (int x = 0; x < 3; ++x) {
+                    constexpr int J[3] = {1, 1, 0}, I[3] = {0, 1, 0};
+                    if (!(share & 1 << x)) continue;
+                    const int lane = renewed(threadIdx.x) % WAVE, l15 = lane & 15, q4 = lane >> 4;
+                    const int t = 16 * J[x] + l15, s0 = 16 * I[x] + 4 * q4;
+                    f32x4 s = zero4();
 #pragma unroll
-                for (int p = 0; p < PT; ++p) acc[j][p] = zero4();
+                    for (int kk = 0; kk < KT / 2; ++kk) {
+                        Parts<NP> qf, kf;
 #pragma unroll
-            for (int kk = 0; kk < KT / 2; ++kk) {
-                Parts<NP> qf[QT];
-#pragma unroll
-                for (int j = 0; j < QT; ++j)
-#pragma unroll
-                    for (int m = 0; m < NP; ++m)
-                        qf[j].p[m] = row_paired(squery + m * PLK + (16 * j + l15) * LDK + 32 * kk, lane);
-#pragma unroll
-                for (int p = 0; p < PT; ++p) {
-                    float v[8];
-#pragma unroll
-                    for (int r = 0; r < 4; ++r) {
-                        v[r] = st[2 * kk][p][r];
-                        v[4 + r] = st[2 * kk + 1][p][r];
+                        for (int m = 0; m < NP; ++m) {
+                            qf.p[m] = TK::row_paired(squery + m * PLK, t, kk, lane);
+                            kf.p[m] = TK::row_paired(skey + m * PLK, 16 * I[x] + l15, kk, lane);
+                        }
+                        s = mma_parts(kf, qf, s);
                     }
-                    const Parts<HP> hf = split8<HP>(v);
+                    float v[4];
+                    if constexpr (NP == 1) {
+                        const f32x4 less = *reinterpret_cast<const f32x4*>(&w.less[s0]);
+                        const float ct = w.c[t];
 #pragma unroll
-                    for (int j = 0; j < QT; ++j) acc[j][p] = mma_parts(hf, qf[j], acc[j][p]);
+                        for (int r = 0; r < 4; ++r) v[r] = s[r] * __builtin_amdgcn_exp2f(ct - less[r]);
+                    } else {
+                        const ExactDecays& x_ = exact[ci & 3];
+                        const f32x4 hi = *reinterpret_cast<const f32x4*>(&x_.hi[s0]);
+                        const f32x4 lo = *reinterpret_cast<const f32x4*>(&x_.lo[s0]);
+                        const f32x4 src = *reinterpret_cast<const f32x4*>(&x_.src[s0]);
+#pragma unroll
+                        for (int r = 0; r < 4; ++r)
+                            v[r] = s[r] * (__builtin_amdgcn_exp2f((x_.hi[t] - hi[r]) + (x_.lo[t] - lo[r])) * src[r]);
+                    }
+                    if (I[x] == J[x]) {
+#pragma unroll
+                        for (int r = 0; r < 4; ++r) v[r] = 4 * q4 + r <= l15 ? v[r] : 0.f;
+                    }
+                    char* to = sm + t * (Q * 2) + ((q4 ^ ((t >> 1) & 3)) * 16) + I[x] * 8;
+#pragma unroll
+                    for (int m = 0; m < MP; ++m) {
+                        const uint32_t a0 = pack2(v[0], v[1]), a1 = pack2(v[2], v[3]);
+                        *reinterpret_cast<uint2*>(to + m * PLM) = make_uint2(a0, a1);
+                        v[0] -= low_of(a0);
+                        v[1] -= high_of(a0);
+                        v[2] -= low_of(a1);
+                        v[3] -= high_of(a1);
+                    }
+                }
+                // the state's part of the results
+                const int lane = renewed(threadIdx.x) % WAVE, l15 = lane & 15;
+#pragma unroll
+                for (int kk = 0; kk < KT / 2; ++kk) {
+                    Parts<NP> qf[2];
+#pragma unroll
+                    for (int j = 0; j < 2; ++j)
+#pragma unroll
+                        for (int m = 0; m < NP; ++m) qf[j].p[m] = TK::row_paired(squery + m * PLK, 16 * j + l15, kk, lane);
+#pragma unroll
+                    for (int p = 0; p < PT; ++p) {
+                        float v[8];
+#pragma unroll
+                        for (int r = 0; r < 4; ++r) {
+                            v[r] = st[2 * kk][p][r];
+                            v[4 + r] = st[2 * kk + 1][p][r];
+                        }
+                        const Parts<HP> hf = split8<HP>(v);
+#pragma unroll
+                        for (int j = 0; j < 2; ++j) acc[j][p] = mma_parts(hf, qf[j], kk ? acc[j][p] : zero4());
+                    }
                 }
             }
+            lds_barrier();  // the masked products are there
+        }
+        if (mine) {
+            Parts<NP> vf[PT];
 #pragma unroll
-            for (int j = 0; j < QT; ++j) {
-                // operands are read again for each tile of tokens: kept from tile to tile they would push the state out
+            for (int p = 0; p < PT; ++p)
+#pragma unroll
+                for (int m = 0; m < NP; ++m) vf[p].p[m] = TP::col_paired(sval + m * PLP, p, lane);
+            if constexpr ((MODE & OUT) != 0) {
                 const int lane = renewed(threadIdx.x) % WAVE, l15 = lane & 15, q4 = lane >> 4;
-                const int t = 16 * j + l15;
-                const float from = dec.from[t];
 #pragma unroll
-                for (int p = 0; p < PT; ++p) acc[j][p] *= from;
-                Parts<NP> qf[KT / 2];
+                for (int j = 0; j < 2; ++j) {
+                    const int t = 16 * j + l15;
+                    const float from = w.from[t], scale = w.scale[t];
+                    Parts<MP> mf;
 #pragma unroll
-                for (int kk = 0; kk < KT / 2; ++kk)
-#pragma unroll
-                    for (int m = 0; m < NP; ++m)
-                        qf[kk].p[m] = row_paired(squery + m * PLK + t * LDK + 32 * kk, lane);
-                const float ct = dec.c[t], hi = dec.hi[t], lo = dec.lo[t];
-#pragma unroll
-                for (int i2 = 0; i2 <= j / 2; ++i2) {
-                    float m8[8];
-#pragma unroll
-                    for (int half = 0; half < 2; ++half) {
-                        const int i = 2 * i2 + half;
-                        if (i > j) {
-#pragma unroll
-                            for (int r = 0; r < 4; ++r) m8[4 * half + r] = 0.f;
-                            continue;
-                        }
-                        f32x4 s = zero4();
-#pragma unroll
-                        for (int kk = 0; kk < KT / 2; ++kk) {
-                            Parts<NP> kf;
-#pragma unroll
-                            for (int m = 0; m < NP; ++m)
-                                kf.p[m] = row_paired(skey + m * PLK + (16 * i + l15) * LDK + 32 * kk, lane);
-                            s = mma_parts(kf, qf[kk], s);
-                        }
-                        if constexpr (NP == 1) {
-                            const f32x4 less = *reinterpret_cast<const f32x4*>(&dec.less[16 * i + 4 * q4]);
-#pragma unroll
-                            for (int r = 0; r < 4; ++r) {
-                                const float v = s[r] * __builtin_amdgcn_exp2f(ct - less[r]);
-                                m8[4 * half + r] = i < j || 4 * q4 + r <= l15 ? v : 0.f;
-                            }
-                        } else {
-                            const f32x4 shi = *reinterpret_cast<const f32x4*>(&dec.hi[16 * i + 4 * q4]);
-                            const f32x4 slo = *reinterpret_cast<const f32x4*>(&dec.lo[16 * i + 4 * q4]);
-                            const f32x4 src = *reinterpret_cast<const f32x4*>(&dec.src[16 * i + 4 * q4]);
-#pragma unroll
-                            for (int r = 0; r < 4; ++r) {
-                                const float v = s[r] * (__builtin_amdgcn_exp2f((hi - shi[r]) + (lo - slo[r])) * src[r]);
-                                m8[4 * half + r] = i < j || 4 * q4 + r <= l15 ? v : 0.f;
-                            }
-                        }
-                    }
-                    const Parts<MP> mf = split8<MP>(m8);
+                    for (int m = 0; m < MP; ++m)
+                        mf.p[m] = *reinterpret_cast<const bf16x8*>(sm + m * PLM + t * (Q * 2) + ((q4 ^ ((t >> 1) & 3)) * 16));
+                    DT* out = reinterpret_cast<DT*>(a.y) + ((int64_t)first * a.H + h) * a.P + p0 + (int64_t)t * dir * a.H * a.P;
 #pragma unroll
                     for (int p = 0; p < PT; ++p) {
-                        Parts<NP> vf;
-#pragma unroll
-                        for (int m = 0; m < NP; ++m)
-                            vf.p[m] = col_paired(sval + m * PLP + 32 * i2 * LDP + 16 * p, LDP, lane);
-                        acc[j][p] = mma_parts(vf, mf, acc[j][p]);
-                    }
-                }
-                if (t < n) {
-                    const float scale = dec.scale[t];
-                    DT* out = reinterpret_cast<DT*>(a.y) + ((int64_t)first * a.H + h) * a.P + p0 +
-                              (int64_t)t * dir * a.H * a.P;
-#pragma unroll
-                    for (int p = 0; p < PT; ++p) {
-                        const int c = 16 * p + 4 * q4;
+                        acc[j][p] = mma_parts(vf[p], mf, acc[j][p] * from);
+                        const int col = 16 * p + 4 * q4;
                         float o[4];
                         zero_v(o);
 #pragma unroll
                         for (int m = NP - 1; m >= 0; --m) {
-                            const uint2 v = *reinterpret_cast<const uint2*>(sval + m * PLP + t * LDP + c);
+                            const uint2 v = *reinterpret_cast<const uint2*>(sval + m * PLP + TP::at(t, 2 * p + (q4 >> 1)) + (q4 & 1) * 8);
                             const float f[4] = {low_of(v.x), high_of(v.x), low_of(v.y), high_of(v.y)};
 #pragma unroll
                             for (int r = 0; r < 4; ++r) o[r] = m + 1 < NP ? o[r] + f[r] : f[r];
                         }
 #pragma unroll
                         for (int r = 0; r < 4; ++r) o[r] = scale * acc[j][p][r] + dskip * o[r];
-                        if (p0 + c + 4 <= a.P) {
-                            store_v<4>(out + c, o);
-                        } else {
+                        if (t < n) {
+                            if (p0 + col + 4 <= a.P) {
+                                store_v<4>(out + col, o);
+                            } else {
 #pragma unroll
-                            for (int r = 0; r < 4; ++r)
-                                if (p0 + c + r < a.P) out[c + r] = from_f32<DT>(o[r]);
+                                for (int r = 0; r < 4; ++r)
+                                    if (p0 + col + r < a.P) out[col + r] = from_f32<DT>(o[r]);
+                            }
                         }
                     }
                 }
             }
-        }
-
-        // the state behind the chunk
-#pragma unroll
-        for (int k = 0; k < KT; ++k)
-#pragma unroll
-            for (int p = 0; p < PT; ++p) st[k][p] *= total;
-#pragma unroll
-        for (int i2 = 0; i2 < QT / 2; ++i2) {
-            const int s0 = 32 * i2 + 4 * q4;
-            float w[8];
-#pragma unroll
-            for (int r = 0; r < 4; ++r) {
-                w[r] = dec.to[s0 + r] * dec.src[s0 + r];
-                w[4 + r] = dec.to[s0 + 16 + r] * dec.src[s0 + 16 + r];
-            }
+            // the state behind the chunk
+            const int lane = renewed(threadIdx.x) % WAVE, q4 = lane >> 4;
+            const float total = w.total;
+            const f32x4 w0 = *reinterpret_cast<const f32x4*>(&w.into[4 * q4]), w1 = *reinterpret_cast<const f32x4*>(&w.into[16 + 4 * q4]);
             Parts<3> xf[PT];
 #pragma unroll
             for (int p = 0; p < PT; ++p) {
                 float v[8];
-                zero_v(v);
 #pragma unroll
-                for (int m = NP - 1; m >= 0; --m) {
-                    const bf16x8 b = col_paired(sval + m * PLP + 32 * i2 * LDP + 16 * p, LDP, lane);
+                for (int r = 0; r < 8; ++r) {
+                    v[r] = (float)vf[p].p[NP - 1][r];
 #pragma unroll
-                    for (int r = 0; r < 8; ++r) v[r] = m + 1 < NP ? v[r] + (float)b[r] : (float)b[r];
+                    for (int m = NP - 2; m >= 0; --m) v[r] += (float)vf[p].p[m][r];
+                    v[r] *= r < 4 ? w0[r] : w1[r - 4];
                 }
-#pragma unroll
-                for (int r = 0; r < 8; ++r) v[r] *= w[r];
                 xf[p] = split8<3>(v);
             }
+            // products that add to one tile wait for each other: two tiles' rows side by side, a part at a time
 #pragma unroll
-            for (int k = 0; k < KT; ++k) {
-                Parts<NP> kf;
+            for (int k = 0; k < KT; k += 2) {
+                Parts<NP> kf[2];
 #pragma unroll
-                for (int m = 0; m < NP; ++m) kf.p[m] = col_paired(skey + m * PLK + 32 * i2 * LDK + 16 * k, LDK, lane);
+                for (int i = 0; i < 2; ++i)
 #pragma unroll
-                for (int p = 0; p < PT; ++p) st[k][p] = mma_parts(kf, xf[p], st[k][p]);
+                    for (int m = 0; m < NP; ++m) kf[i].p[m] = TK::col_paired(skey + m * PLK, k + i, lane);
+#pragma unroll
+                for (int i = 0; i < 2; ++i)
+#pragma unroll
+                    for (int p = 0; p < PT; ++p) st[k + i][p] *= total;
+#pragma unroll
+                for (int m = 0; m < NP; ++m)
+#pragma unroll
+                    for (int x = 0; x < 3; ++x)
+                        if (m + x <= 2) {
+#pragma unroll
+                            for (int i = 0; i < 2; ++i)
+#pragma unroll
+                                for (int p = 0; p < PT; ++p)
+                                    st[k + i][p] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(kf[i].p[m], xf[p].p[x], st[k + i][p], 0, 0, 0);
+                        }
             }
+            if (decides && (ci & 1) && ci + 1 < chunks) decays_of(ci + 1, raw);
         }
     }
     if (!mine) return;
@@ -545,7 +696,7 @@ __global__ void __launch_bounds__(NT, 2) ssm_walk_kernel(SsmArgs a, const DT* va
         for (int k = 0; k < KT; ++k)
 #pragma unroll
             for (int p = 0; p < PT; ++p) e[frag + (k * PT + p) * WAVE] = st[k][p];
-        if (lane == 0 && p0 == 0) a.decay[(int64_t)at.slot * a.H + h] = exp2f((float)log_decay);
+        if (lane == 0 && decides && block == who) a.decay[(int64_t)at.slot * a.H + h] = exp2f((float)log_decay);
     } else if (is_last && last_state) {
         float* f = last_state + ((int64_t)pc.seq * a.H + h) * a.K * a.P;
 #pragma unroll
@@ -555,7 +706,7 @@ __global__ void __launch_bounds__(NT, 2) ssm_walk_kernel(SsmArgs a, const DT* va
 #pragma unroll
                 for (int r = 0; r < 4; ++r) {
                     const int kk = 16 * k + 4 * q4 + r, pp = p0 + 16 * p + l15;
-                    if (kk < a.K && pp < a.P) f[(int64_t)kk * a.P + pp] = st[k][p][r];
+                    if (kk < a.K && pp < a.P) f[kk * a.P + pp] = st[k][p][r];
                 }
     }
 }
@@ -564,7 +715,7 @@ __global__ void __launch_bounds__(NT, 2) ssm_walk_kernel(SsmArgs a, const DT* va
 // the state it starts from.  Four elements a thread.
 __global__ void __launch_bounds__(NT) ssm_join_kernel(SsmArgs a, const float* first_state, int rev, int per_unit,
                                                       int pieces) {
-    const int64_t units = (int64_t)a.H * a.blocks;
+    const int64_t units = (int64_t)a.H * a.wblocks;
     for (int64_t b = blockIdx.x; b < a.N * units * pieces; b += gridDim.x) {
     const int piece = (int)(b % pieces), unit = (int)(b / pieces % units), seq = (int)(b / pieces / units);
     const Seqs sq{a.cu, a.N, a.T, a.eq};
@@ -572,11 +723,11 @@ __global__ void __launch_bounds__(NT) ssm_join_kernel(SsmArgs a, const float* fi
     const int segs = (max(len, 0) + a.seg - 1) / a.seg;
     const int e = piece * NT + threadIdx.x;
     if (segs < 2 || e >= per_unit) continue;
-    const int h = unit / a.blocks, tiles = a.cols / 16;
+    const int h = unit / a.wblocks, tiles = a.wcols / 16;
     const int lane = e % WAVE, tile = e / WAVE;
     f32x4 cur = zero4();
     if (first_state) {
-        const int k0 = 16 * (tile / tiles) + 4 * (lane >> 4), p = unit % a.blocks * a.cols + 16 * (tile % tiles) + (lane & 15);
+        const int k0 = 16 * (tile / tiles) + 4 * (lane >> 4), p = unit % a.wblocks * a.wcols + 16 * (tile % tiles) + (lane & 15);
 #pragma unroll
         for (int r = 0; r < 4; ++r)
             if (k0 + r < a.K && p < a.P) cur[r] = first_state[(((int64_t)seq * a.H + h) * a.K + k0 + r) * a.P + p];
@@ -612,7 +763,7 @@ __global__ void __launch_bounds__(NT) ssm_join_kernel(SsmArgs a, const float* fi
 // 16 rows of M, E and their products (in LDS as bf16 parts), then a quarter of the columns of
 // dB and dC, so no sum crosses wavefronts but those of single numbers a token.
 template <typename DT, int KT, int PT>
-__global__ void __launch_bounds__(NT, 2) ssm_grad_kernel(SsmArgs a, int64_t slots, int quads) {
+__global__ void __launch_bounds__(NT, 2) ssm_grad_kernel(SsmArgs a, int slots, int quads) {
     using C_ = Cfg<DT>;
     constexpr int QT = C_::QT, Q = QT * 16, NP = C_::NP, MP = C_::MP;
     constexpr int LDK = KT * 16 + 8, LDP = PT * 16 + 8, LDQ = Q + 8, PLK = Q * LDK, PLP = Q * LDP, PLQ = Q * LDQ;
@@ -641,8 +792,8 @@ __global__ void __launch_bounds__(NT, 2) ssm_grad_kernel(SsmArgs a, int64_t slot
 
     {
         Stage<DT, Q, KT * 16, NT> bk, bq;
-        bk.load((const DT*)a.B + (int64_t)at.group * a.K, a.bs, a.K, c0, 1, n, tid);
-        bq.load((const DT*)a.C + (int64_t)at.group * a.K, a.cs, a.K, c0, 1, n, tid);
+        bk.load((const DT*)a.B + (int64_t)at.group * a.K, a.bs, a.K, c0, false, n, tid);
+        bq.load((const DT*)a.C + (int64_t)at.group * a.K, a.cs, a.K, c0, false, n, tid);
         bk.store(sb, LDK, PLK, tid);
         bq.store(sc, LDK, PLK, tid);
     }
@@ -653,11 +804,11 @@ __global__ void __launch_bounds__(NT, 2) ssm_grad_kernel(SsmArgs a, int64_t slot
         for (int k = 0; k < KW; ++k) dB[j][k] = dC[j][k] = zero4();
 
     Stage<DT, Q, PT * 16, NT> bx, by;  // the next unit's, on their way
-    auto fetch = [&](int un, int tid) {
+    auto fetch = [&](int un, unsigned tid) {
         const int unit = at.group * units + un, h = unit / a.blocks, p0 = unit % a.blocks * (PT * 16);
         const int cols = min(a.P - p0, PT * 16);
-        bx.load((const DT*)a.x + (int64_t)h * a.P + p0, a.xs, cols, c0, 1, n, tid);
-        by.load((const DT*)a.dy + (int64_t)h * a.P + p0, a.dys, cols, c0, 1, n, tid);
+        bx.load((const DT*)a.x + (int64_t)h * a.P + p0, a.xs, cols, c0, false, n, tid);
+        by.load((const DT*)a.dy + (int64_t)h * a.P + p0, a.dys, cols, c0, false, n, tid);
     };
     fetch(u0, tid);
     for (int un = u0; un < u1; ++un) {
@@ -665,8 +816,8 @@ __global__ void __launch_bounds__(NT, 2) ssm_grad_kernel(SsmArgs a, int64_t slot
         float total = 0.f;
         // The last unit's products are read (its third barrier); the states are on their way through the first phase.
         {
-            const int tid = renewed(threadIdx.x), lane = tid % WAVE;
-            if (wave == 0) total = exp2f((float)decays<Q>(dec, a, h, c0, 1, n, false, lane));
+            const unsigned tid = renewed(threadIdx.x), lane = tid % WAVE;
+            if (wave == 0) total = exp2f((float)decays<Q>(dec, a, h, c0, n, lane));
             bx.store(sx, LDP, PLP, tid);
             by.store(sdy, LDP, PLP, tid);
             if (un + 1 < u1) fetch(un + 1, tid);
@@ -674,12 +825,22 @@ __global__ void __launch_bounds__(NT, 2) ssm_grad_kernel(SsmArgs a, int64_t slot
         Pack<float, 8> hv[PT / 2], gv[PT / 2];
         auto states = [&](int k) {
             const int64_t cslot = pc.start / Q + pc.seq + pc.n;
-            const int64_t state = (cslot * all_units + unit) * (KT * 16 * PT * 16) + (wave * KW + k) * 16 * (PT * 16);
-            const int lane = renewed(threadIdx.x) % WAVE, own = (lane & 15) * (PT * 16) + 8 * (lane >> 4);
+            const int wide = a.blocks * (PT * 16);
+            const int64_t state = (cslot * a.H + h) * ((int64_t)KT * 16 * wide) + (wave * KW + k) * 16 * wide + unit % a.blocks * (PT * 16);
+            const int left = a.wblocks * a.wcols - unit % a.blocks * (PT * 16);
+            const int lane = renewed(threadIdx.x) % WAVE, own = (lane & 15) * wide + 8 * (lane >> 4);
 #pragma unroll
             for (int pp = 0; pp < PT / 2; ++pp) {
                 hv[pp] = load_v<8>(a.hs + state + (own + 32 * pp));
                 gv[pp] = load_v<8>(a.gs + state + (own + 32 * pp));
+            }
+            if (left < PT * 16) {  // columns that no unit of the walk has written
+#pragma unroll
+                for (int pp = 0; pp < PT / 2; ++pp)
+                    if (32 * pp + 8 * (lane >> 4) >= left) {
+                        hv[pp] = Pack<float, 8>{};
+                        gv[pp] = Pack<float, 8>{};
+                    }
             }
         };
         if (wave * KW < KT) states(0);
@@ -1071,9 +1232,9 @@ __global__ void __launch_bounds__(NT) ssm_step_kernel(SsmStepArgs a, int lanes_l
 // ---------------------------------------------------------------- launches
 
 template <typename DT, int KT, int PT, int MODE> constexpr int walk_lds() {
-    constexpr int Q = Cfg<DT>::QT * 16, NP = Cfg<DT>::NP;
-    return ((MODE & OUT ? 2 : 1) * NP * Q * (KT * 16 + 8) + WAVES * NP * Q * (PT * 16 + 8)) * 2 +
-           WAVES * (int)sizeof(Decays<Q>);
+    constexpr int NP = Cfg<DT>::NP;
+    return NP * WALK * ((MODE & OUT ? 2 : 1) * KT * 32 + WAVES * PT * 32) + (MODE & OUT ? WAVES * Cfg<DT>::MP * WALK * WALK * 2 : 0) +
+           4 * WAVES * ((int)sizeof(WalkDecays) + (NP == 1 ? 0 : (int)sizeof(ExactDecays)));
 }
 template <typename DT, int KT, int PT> constexpr int grad_lds() {
     constexpr int Q = Cfg<DT>::QT * 16, NP = Cfg<DT>::NP;
@@ -1099,14 +1260,14 @@ struct Roles {
 template <typename DT, int KT, int PT, int MODE>
 hipError_t walk(const SsmArgs& a, const Roles& r, hipStream_t st) {
     const int64_t slots = ssm_slots(a, a.seg);
-    const int quads = (a.H / a.G * a.blocks + WAVES - 1) / WAVES;
+    const int quads = (a.H / a.G * a.wblocks + WAVES - 1) / WAVES;
     constexpr int lds = walk_lds<DT, KT, PT, MODE>();
     static_assert(lds <= 160 * 1024, "a chunk's tiles fit a compute unit");
     auto* kernel = ssm_walk_kernel<DT, KT, PT, MODE>;
     const hipError_t e = allow_lds(kernel, lds);
     if (e != hipSuccess) return e;
     hipLaunchKernelGGL(kernel, dim3((unsigned)place_blocks(slots, a.G, quads)), dim3(NT), lds, st, a, (const DT*)r.val,
-                       (const DT*)r.key, (const DT*)r.query, r.vs, r.ks, r.qs, r.first, r.last, r.emit, r.rev, slots, quads);
+                       (const DT*)r.key, (const DT*)r.query, r.vs, r.ks, r.qs, r.first, r.last, r.emit, r.rev, (int)slots, quads);
     return hipGetLastError();
 }
 
@@ -1120,7 +1281,7 @@ hipError_t whole_walk(const SsmArgs& a, const Roles& r, hipStream_t st) {
     if (segmented(a)) {
         SSM_TRY((walk<DT, KT, PT, ENDS>(a, r, st)));
         const int per_unit = KT * PT * WAVE, pieces = (per_unit + NT - 1) / NT;
-        const int64_t blocks = ssm_units(a) * a.N * pieces;
+        const int64_t blocks = (int64_t)a.H * a.wblocks * a.N * pieces;
         hipLaunchKernelGGL(ssm_join_kernel, dim3((unsigned)(blocks < 1 << 20 ? blocks : 1 << 20)), dim3(NT), 0, st, a, r.first,
                            r.rev, per_unit, pieces);
         SSM_TRY(hipGetLastError());
@@ -1129,16 +1290,18 @@ hipError_t whole_walk(const SsmArgs& a, const Roles& r, hipStream_t st) {
 }
 
 template <typename DT, int KT, int PT> hipError_t forward(const SsmArgs& a, hipStream_t st) {
+    constexpr int WT = PT / 2;
     const Roles r{a.x, a.B, a.C, a.xs, a.bs, a.cs, a.h0, a.hT, nullptr, 0};
-    return whole_walk<DT, KT, PT, OUT>(a, r, st);
+    return whole_walk<DT, KT, WT, OUT>(a, r, st);
 }
 
 template <typename DT, int KT, int PT> hipError_t backward(const SsmArgs& a, hipStream_t st) {
+    constexpr int WT = PT / 2;
     if (a.N > 0) {
         const Roles f{a.x, a.B, a.C, a.xs, a.bs, a.cs, a.h0, nullptr, a.hs, 0};
-        SSM_TRY((whole_walk<DT, KT, PT, EMIT>(a, f, st)));
+        SSM_TRY((whole_walk<DT, KT, WT, EMIT>(a, f, st)));
         const Roles b{a.dy, a.C, a.B, a.dys, a.cs, a.bs, a.dhT, a.dh0, a.gs, 1};
-        SSM_TRY((whole_walk<DT, KT, PT, OUT | EMIT>(a, b, st)));
+        SSM_TRY((whole_walk<DT, KT, WT, OUT | EMIT>(a, b, st)));
     }
     if (a.T > 0) {
         const int64_t slots = ssm_slots(a, a.chunk);
@@ -1146,7 +1309,7 @@ template <typename DT, int KT, int PT> hipError_t backward(const SsmArgs& a, hip
         static_assert(lds <= 160 * 1024, "a chunk's tiles fit a compute unit");
         auto* kernel = ssm_grad_kernel<DT, KT, PT>;
         SSM_TRY(allow_lds(kernel, lds));
-        hipLaunchKernelGGL(kernel, dim3((unsigned)place_blocks(slots, a.G, a.split)), dim3(NT), lds, st, a, slots, a.split);
+        hipLaunchKernelGGL(kernel, dim3((unsigned)place_blocks(slots, a.G, a.split)), dim3(NT), lds, st, a, (int)slots, a.split);
         SSM_TRY(hipGetLastError());
         if (a.split > 1) {
             const int64_t all = (int64_t)a.T * a.G * a.K, blocks = (all + NT - 1) / NT;

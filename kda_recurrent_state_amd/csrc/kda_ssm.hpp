@@ -6,15 +6,13 @@
 
 namespace kda {
 
-// The state [K, P] of a head is held by wavefronts in blocks of all K rows and up to
-// SSM_COLS columns (half of that above 128 rows, where the block would not fit a wavefront's
-// registers): a "unit" is a head's block of columns.  Columns do not meet in the
-// recurrence, so units are independent.
-constexpr int SSM_COLS = 64;
+// A head's state [K, P] is taken in blocks of all K rows and some columns: columns do not meet in the recurrence.
+// The walk along the tokens holds one in a wavefront's registers, 32 columns (16 above 128 rows); the
+// gradient, which reads the states, takes twice as many at a time.  A head's block of columns is a "unit".
 constexpr int SSM_MAX_STATE = 256;
-inline int ssm_cols(int K) { return K > 128 ? SSM_COLS / 2 : SSM_COLS; }
+inline int ssm_cols(int K) { return K > 128 ? 32 : 64; }
 inline int ssm_rows(int K) { return K <= 32 ? 32 : K <= 64 ? 64 : K <= 128 ? 128 : 256; }
-inline int ssm_chunk(int dtype) { return dtype == 1 ? 64 : 32; }  // tokens of a chunk (1: bf16)
+inline int ssm_chunk(int dtype) { return dtype == 1 ? 64 : 32; }  // tokens of the gradient's chunk (1: bf16)
 
 struct SsmArgs {
     const void *x, *B, *C, *dy;
@@ -26,7 +24,8 @@ struct SsmArgs {
     int64_t xs, dts, bs, cs, dys;                // token strides
     int32_t dtype, softplus;
     // plan
-    int32_t chunk, rows, cols, blocks;           // tokens of a chunk, padded K, columns and column blocks of a unit
+    int32_t chunk, rows;                         // tokens of a chunk, padded K
+    int32_t cols, blocks, wcols, wblocks;        // columns of a block, blocks of a head: of the gradient, of the walk
     int32_t seg;                                 // tokens of a segment (a multiple of chunk)
     int32_t split;                               // shares of a group's units in the gradient
     // workspace
@@ -39,7 +38,7 @@ struct SsmArgs {
 
 inline int64_t ssm_units(const SsmArgs& a) { return (int64_t)a.H * a.blocks; }
 inline int64_t ssm_slots(const SsmArgs& a, int every) { return a.T / every + a.N; }
-inline int64_t ssm_unit_state(const SsmArgs& a) { return (int64_t)a.rows * a.cols; }
+inline int64_t ssm_unit_state(const SsmArgs& a) { return (int64_t)a.rows * a.cols; }  // of the gradient's units
 constexpr int SSM_SUM_ROWS = 256;
 
 hipError_t launch_ssm_fwd(const SsmArgs& a, hipStream_t st);

@@ -16,6 +16,7 @@ namespace {
 constexpr int kMaxHeads = 65536;
 constexpr int kMaxHeadWidth = 8192;
 constexpr int64_t kMaxBlocks = 0xffffff;  // workgroups of 256 threads in one launch
+constexpr int64_t kWalkGroups = 768;
 constexpr int kWaves = 4;                 // units of a workgroup of the walk
 
 int64_t round_up(int64_t x, int64_t to) { return (x + to - 1) / to * to; }
@@ -57,9 +58,11 @@ int plan(const kda_ssm_dims_t* d, kda::SsmArgs* a) {
     a->rows = kda::ssm_rows(a->K);
     a->cols = kda::ssm_cols(a->K);
     a->blocks = (a->P + a->cols - 1) / a->cols;
-    // Segments: enough workgroups for two on every compute unit.
-    const int64_t quads = ((int64_t)a->H / a->G * a->blocks + kWaves - 1) / kWaves;
-    const int64_t want = 512 / (quads * a->G) > 0 ? 512 / (quads * a->G) : 1;
+    a->wcols = a->cols / 2;
+    a->wblocks = (a->P + a->wcols - 1) / a->wcols;
+    // Segments: enough workgroups for three on every compute unit.
+    const int64_t quads = ((int64_t)a->H / a->G * a->wblocks + kWaves - 1) / kWaves;
+    const int64_t want = kWalkGroups / (quads * a->G) > 0 ? kWalkGroups / (quads * a->G) : 1;
     const int64_t seg = round_up((a->T + want - 1) / want, a->chunk);
     a->seg = (int32_t)(seg < 2 * a->chunk ? 2 * a->chunk : seg);
     const int64_t pairs = kda::ssm_slots(*a, a->chunk) * a->G, units = (int64_t)a->H / a->G * a->blocks;
@@ -79,7 +82,7 @@ size_t layout(kda::SsmArgs* a, int backward, uint8_t* base) {
     const int64_t state = kda::ssm_unit_state(*a), units = kda::ssm_units(*a);
     if (a->seg < a->T) {
         const int64_t slots = kda::ssm_slots(*a, a->seg);
-        a->ends = take(slots * units * state);
+        a->ends = take(slots * a->H * a->wblocks * a->rows * a->wcols);
         a->decay = take(slots * a->H);
     }
     if (backward) {
@@ -95,7 +98,7 @@ size_t layout(kda::SsmArgs* a, int backward, uint8_t* base) {
 
 // One launch holds 2^32 threads.
 int check_size(const kda::SsmArgs& a, int backward) {
-    const int64_t quads = ((int64_t)a.H / a.G * a.blocks + kWaves - 1) / kWaves;
+    const int64_t quads = ((int64_t)a.H / a.G * a.wblocks + kWaves - 1) / kWaves;
     const int64_t walk = (kda::ssm_slots(a, a.seg) * a.G + 8) * quads;
     const int64_t grad = backward ? (kda::ssm_slots(a, a.chunk) * a.G + 8) * a.split : 0;
     if (walk > kMaxBlocks || grad > kMaxBlocks)
