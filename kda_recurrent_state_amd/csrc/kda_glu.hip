@@ -48,7 +48,8 @@ template <int ACT> __device__ __forceinline__ float gated(float g, float u) {
 // first form, and there are a multiple of 64 columns in the second.  Rows past the last are the last again, and their
 // results are not stored; k rows past the last meet zeros of the other operand.
 
-constexpr int BK = 64;
+constexpr int BK = 32;    // k of a stage: one matrix instruction's
+constexpr int PAD = 64;   // what k and padded columns are a multiple of
 constexpr int MAX_SEGS = 12;
 
 struct Segment { const bf16 *a, *b, *b2; };
@@ -72,24 +73,22 @@ struct GemmArgs {
 };
 
 template <bool KR> struct Operand;
-// [rows][k]: a row of 64 k is 128 bytes in LDS, its 16-byte pieces exchanged by the row's number so that 8
+// [rows][k]: a row of 32 k is 64 bytes in LDS, its 16-byte pieces exchanged by the row's number so that 16
 // neighbouring rows' pieces of the same k lie in different banks.
 template <> struct Operand<false> {
-    template <int ROWS, int THREADS> static constexpr int loads() { return ROWS * 8 / THREADS; }
     static __device__ __forceinline__ int source(int at, int64_t rows_left, int64_t ld, int) {
-        const int row = at / 8, piece = (at & 7) ^ (row & 7);
+        const int row = at / 4, piece = (at & 3) ^ ((row >> 2) & 3);
         const int64_t r = row < rows_left ? row : rows_left - 1;
         return (int)(r * ld * 2) + piece * 16;
     }
-    static __device__ __forceinline__ bf16x8 frag(const char* tile, int row0, int ks, int lane, int) {
-        const int row = row0 + (lane & 15), piece = (ks * 4 + (lane >> 4)) ^ (row & 7);
-        return *reinterpret_cast<const bf16x8*>(tile + row * 128 + piece * 16);
+    static __device__ __forceinline__ bf16x8 frag(const char* tile, int row0, int lane, int) {
+        const int row = row0 + (lane & 15), piece = (lane >> 4) ^ ((row >> 2) & 3);
+        return *reinterpret_cast<const bf16x8*>(tile + row * 64 + piece * 16);
     }
 };
 // [k][rows]: a k row of R columns is 2 R bytes, its 32-byte pieces (16 columns) exchanged so that the 8 k rows that
 // half a wavefront reads at once lie in different banks.
 template <> struct Operand<true> {
-    template <int ROWS, int THREADS> static constexpr int loads() { return ROWS * 8 / THREADS; }
     static __device__ __forceinline__ int turn(int k) { return (k & 3) | ((k >> 3) & 1) << 2; }
     static __device__ __forceinline__ int source(int at, int64_t rows_left, int64_t ld, int rows) {
         const int per = rows / 8, k = at / per, slot = at % per;
@@ -97,9 +96,9 @@ template <> struct Operand<true> {
         const int64_t col = c + 8 <= rows_left ? c : rows_left - 8;
         return (int)(k * ld * 2 + col * 2);
     }
-    static __device__ __forceinline__ bf16x8 frag(const char* tile, int row0, int ks, int lane, int rows) {
+    static __device__ __forceinline__ bf16x8 frag(const char* tile, int row0, int lane, int rows) {
         typedef __attribute__((address_space(3))) s16x4* lds;
-        const int i = lane & 15, q = lane >> 4, k = ks * 32 + 8 * q + (i >> 2);
+        const int i = lane & 15, q = lane >> 4, k = 8 * q + (i >> 2);
         const char* p = tile + k * rows * 2 + (((row0 >> 4) ^ turn(k)) * 32) + (i & 3) * 8;
         const bf16x4 lo = __builtin_bit_cast(bf16x4, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds)(p)));
         const bf16x4 hi = __builtin_bit_cast(bf16x4, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds)(p + 4 * rows * 2)));
@@ -169,14 +168,16 @@ __device__ __forceinline__ void store_dgu(const GemmArgs& g, int64_t t, int64_t 
 
 enum { EPI_OUT, EPI_H, EPI_DGU };
 
-// BM x BN results a workgroup of WM x WN wavefronts, STAGES tiles of both operands in LDS: while one is
-// multiplied the next ones arrive.  With two B (EPI_H, EPI_DGU) the first half of BN is of one and
-// the second of the other, so that a lane holds both results of a column.
+// BM x BN results a workgroup of WM x WN wavefronts.  Both operands come in stages of 32 k, STAGES of them in LDS:
+// while a stage is multiplied out of registers, the next is read from LDS into others and the ones after it
+// arrive, so that a copy has STAGES - 1 stages' time.  One barrier a stage: behind it the next stage's copies are
+// complete and the stage before it, read by everyone, takes the next copies.  With two B (EPI_H, EPI_DGU) the
+// first half of BN is of one and the second of the other, so that a lane holds both results of a column.
 template <typename DT, int BM, int BN, int WM, int WN, int STAGES, bool AKR, bool BKR, int EPI, int ACT>
-__global__ void __launch_bounds__(WM* WN * 64, WM* WN / 4) glu_gemm_kernel(GemmArgs g) {
+__global__ void __launch_bounds__(WM* WN * 64, 2) glu_gemm_kernel(GemmArgs g) {
     constexpr bool DUAL = EPI != EPI_OUT;
     constexpr int THREADS = WM * WN * 64, TM = BM / WM / 16, TN = BN / WN / 16;
-    constexpr int LA = BM * 8 / THREADS, LB = BN * 8 / THREADS, STAGE = (BM + BN) * BK * 2;
+    constexpr int LA = BM * 4 / THREADS, LB = BN * 4 / THREADS, STAGE = (BM + BN) * BK * 2;
     constexpr int BH = DUAL ? BN / 2 : BN;  // columns of one B in a tile
     extern __shared__ __attribute__((aligned(1024))) char smem[];
     const int tid = threadIdx.x, lane = tid % 64, wave = __builtin_amdgcn_readfirstlane(tid / 64);
@@ -184,18 +185,15 @@ __global__ void __launch_bounds__(WM* WN * 64, WM* WN / 4) glu_gemm_kernel(GemmA
 
     // Every eighth workgroup runs on the same die: a die takes a run of neighbouring tiles, which share
     // operands in its cache, in strips of 8 tiles along m.
-    int64_t b = blockIdx.x;
-    const int64_t tiles = (int64_t)g.mt * g.nt, total = tiles * g.split * g.halves;
-    {
-        const int64_t per = (total + 7) / 8;
-        b = (b & 7) * per + (b >> 3);
-        if ((int64_t)(blockIdx.x >> 3) >= per || b >= total) return;
-    }
-    const int share = (int)(b / tiles % g.split), half = (int)(b / tiles / g.split);
-    const int64_t tile = b % tiles;
-    const int64_t strip = tile / (8 * g.nt), in = tile % (8 * g.nt);
-    const int tall = (int)(g.mt - strip * 8 < 8 ? g.mt - strip * 8 : 8);
-    const int64_t m0 = (strip * 8 + in % tall) * BM, n0 = in / tall * BH;
+    auto uniform = [](unsigned v) { return (int)__builtin_amdgcn_readfirstlane(v); };
+    const unsigned tiles = (unsigned)g.mt * g.nt, total = tiles * g.split * g.halves, run = (total + 7) / 8;
+    const unsigned b = (blockIdx.x & 7) * run + (blockIdx.x >> 3);
+    if ((blockIdx.x >> 3) >= run || b >= total) return;
+    const int half = uniform(b / tiles / g.split), share = uniform(b / tiles % g.split), tile = uniform(b % tiles);
+    const int strip = uniform((unsigned)tile / (8u * g.nt)), in = tile - strip * 8 * g.nt;
+    const int tall = min(g.mt - strip * 8, 8);
+    const int ntile = uniform((unsigned)in / (unsigned)tall), mtile = strip * 8 + (in - ntile * tall);
+    const int64_t m0 = (int64_t)mtile * BM, n0 = (int64_t)ntile * BH;
 
     int offa[LA], offb[LB];
 #pragma unroll
@@ -203,36 +201,56 @@ __global__ void __launch_bounds__(WM* WN * 64, WM* WN / 4) glu_gemm_kernel(GemmA
 #pragma unroll
     for (int i = 0; i < LB; ++i) {
         const int at = i * THREADS + tid;
-        if (DUAL) offb[i] = Operand<false>::source(at % (BH * 8), g.N - n0, g.ldb, BH);
+        if (DUAL) offb[i] = Operand<false>::source(at % (BH * 4), g.N - n0, g.ldb, BH);
         else offb[i] = Operand<BKR>::source(at, (BKR ? g.colsB : g.N) - n0, g.ldb, BN);
     }
-    const int all = g.segs * g.ksteps, k0 = (int)((int64_t)share * all / g.split), k1 = (int)((int64_t)(share + 1) * all / g.split);
+    // this share's stages, an even number from an even one on
+    const int all = g.segs * g.ksteps / 2, k0 = (int)((int64_t)share * all / g.split) * 2;
+    const int stages = (int)((int64_t)(share + 1) * all / g.split) * 2 - k0;
 
-    auto fetch = [&](int step) {
-        const int s = step / g.ksteps, kk = step % g.ksteps;
-        const Segment sg = g.seg[half * g.segs + s];
-        char* at = smem + step % STAGES * STAGE + wave * 1024;
-        const char* pa = (const char*)(sg.a + (AKR ? (int64_t)kk * BK * g.lda + m0 : m0 * g.lda + (int64_t)kk * BK));
-        const char* pb = (const char*)(sg.b + (BKR ? (int64_t)kk * BK * g.ldb + n0 : n0 * g.ldb + (int64_t)kk * BK));
-        const int la = AKR ? (int)(g.kA - (int64_t)kk * BK) : BK, lb = BKR ? (int)(g.kB - (int64_t)kk * BK) : BK;
+    // What is fetched next: its operands' addresses, moved on by a stage each time and looked up where a segment
+    // begins, and its place in LDS.
+    int fs = uniform((unsigned)k0 / (unsigned)max(g.ksteps, 1)), fk = k0 - fs * g.ksteps, fslot = 0;
+    const char *pa = nullptr, *pb = nullptr, *pb2 = nullptr;
+    const int64_t stepa = (AKR ? g.lda : 1) * BK * 2, stepb = (BKR ? g.ldb : 1) * BK * 2;
+    auto segment = [&]() {
+        const Segment sg = g.seg[half * g.segs + fs];
+        pa = (const char*)(sg.a + (AKR ? m0 : m0 * g.lda)) + fk * stepa;
+        pb = (const char*)(sg.b + (BKR ? n0 : n0 * g.ldb)) + fk * stepb;
+        if (DUAL) pb2 = (const char*)(sg.b2 + n0 * g.ldb) + fk * stepb;
+    };
+    auto fetch = [&]() {
+        char* at = smem + fslot * STAGE + wave * 1024;
+        const int64_t k = (int64_t)fk * BK;
+        if ((AKR && g.kA - k < BK) || (BKR && g.kB - k < BK)) {
+            // k rows past the last are the last again; the stage may lie behind it whole
+            const int la = AKR ? (int)(g.kA - k) : BK, lb = BKR ? (int)(g.kB - k) : BK;
 #pragma unroll
-        for (int i = 0; i < LA; ++i) {
-            int o = offa[i];
-            if (AKR && la < BK) {
-                const int k = (i * THREADS + tid) / (BM / 8);
-                if (k >= la) o -= (int)((k - la + 1) * g.lda * 2);
+            for (int i = 0; i < LA; ++i) {
+                const int row = (i * THREADS + tid) / (BM / 8);
+                copy16(pa, offa[i] - (AKR && row >= la ? (int)((row - la + 1) * g.lda * 2) : 0), at + i * THREADS * 16);
             }
-            copy16(pa, o, at + i * THREADS * 16);
+#pragma unroll
+            for (int i = 0; i < LB; ++i) {
+                const int row = (i * THREADS + tid) / (BN / 8);
+                copy16(pb, offb[i] - (BKR && row >= lb ? (int)((row - lb + 1) * g.ldb * 2) : 0),
+                       at + BM * BK * 2 + i * THREADS * 16);
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < LA; ++i) copy16(pa, offa[i], at + i * THREADS * 16);
+#pragma unroll
+            for (int i = 0; i < LB; ++i)
+                copy16(DUAL && i * THREADS >= BH * 4 ? pb2 : pb, offb[i], at + BM * BK * 2 + i * THREADS * 16);
         }
-        const char* pb2 = DUAL ? (const char*)(sg.b2 + n0 * g.ldb + (int64_t)kk * BK) : pb;
-#pragma unroll
-        for (int i = 0; i < LB; ++i) {
-            int o = offb[i];
-            if (BKR && lb < BK) {
-                const int k = (i * THREADS + tid) / (BN / 8);
-                if (k >= lb) o -= (int)((k - lb + 1) * g.ldb * 2);
-            }
-            copy16(DUAL && i * THREADS >= BH * 8 ? pb2 : pb, o, at + BM * BK * 2 + i * THREADS * 16);
+        if (++fslot == STAGES) fslot = 0;
+        pa += stepa;
+        pb += stepb;
+        if (DUAL) pb2 += stepb;
+        if (++fk == g.ksteps) {
+            fk = 0;
+            ++fs;
+            if (fs < g.segs) segment();
         }
     };
 
@@ -241,34 +259,56 @@ __global__ void __launch_bounds__(WM* WN * 64, WM* WN / 4) glu_gemm_kernel(GemmA
     for (int i = 0; i < TM; ++i)
 #pragma unroll
         for (int j = 0; j < TN; ++j) acc[i][j] = zero4();
-
-    constexpr int AHEAD = STAGES - 1;
-#pragma unroll
-    for (int s = 0; s < AHEAD; ++s)
-        if (k0 + s < k1) fetch(k0 + s);
-    for (int k = k0; k < k1; ++k) {
-        // the copies of step k have arrived (up to AHEAD - 1 later steps may be on their way), and every
-        // wavefront has read step k - 1, whose place the next copies take
-        constexpr int LEFT = (AHEAD - 1) * (LA + LB);
-        if (k + AHEAD - 1 < k1) wait_copies<LEFT>(); else wait_copies<0>();
-        if (k + AHEAD < k1) fetch(k + AHEAD);
-        const char* ta = smem + k % STAGES * STAGE;
+    bf16x8 fa[2][TM], fb[2][TN];
+    int rslot = 0;
+    auto read = [&](bf16x8 (&xa)[TM], bf16x8 (&xb)[TN]) {
+        const char* ta = smem + rslot * STAGE;
         const char* tb = ta + BM * BK * 2;
 #pragma unroll
-        for (int ks = 0; ks < 2; ++ks) {
-            bf16x8 fb[TN], fa[TM];
+        for (int j = 0; j < TN; ++j) {
+            const int row = DUAL ? (j >= TN / 2 ? BH : 0) + wn * (BH / WN) + j % (TN / 2) * 16 : wn * (BN / WN) + j * 16;
+            xb[j] = Operand<BKR>::frag(tb, row, lane, BN);
+        }
 #pragma unroll
-            for (int j = 0; j < TN; ++j) {
-                const int row = DUAL ? (j >= TN / 2 ? BH : 0) + wn * (BH / WN) + j % (TN / 2) * 16 : wn * (BN / WN) + j * 16;
-                fb[j] = Operand<BKR>::frag(tb, row, ks, lane, BN);
-            }
+        for (int i = 0; i < TM; ++i) xa[i] = Operand<AKR>::frag(ta, wm * (BM / WM) + i * 16, lane, BM);
+        if (++rslot == STAGES) rslot = 0;
+    };
+    auto multiply = [&](const bf16x8 (&xa)[TM], const bf16x8 (&xb)[TN]) {
 #pragma unroll
-            for (int i = 0; i < TM; ++i) fa[i] = Operand<AKR>::frag(ta, wm * (BM / WM) + i * 16, ks, lane, BM);
+        for (int i = 0; i < TM; ++i)
 #pragma unroll
-            for (int i = 0; i < TM; ++i)
+            for (int j = 0; j < TN; ++j) acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(xb[j], xa[i], acc[i][j], 0, 0, 0);
+    };
+    // stage j is in one set of registers, stage j + 1 goes to the other
+    auto steady = [&](const bf16x8 (&xa)[TM], const bf16x8 (&xb)[TN], bf16x8 (&ya)[TM], bf16x8 (&yb)[TN]) {
+        wait_copies<(STAGES - 2) * (LA + LB)>();
+        read(ya, yb);
+        fetch();
+        multiply(xa, xb);
+    };
+    auto last = [&](int j, const bf16x8 (&xa)[TM], const bf16x8 (&xb)[TN], bf16x8 (&ya)[TM], bf16x8 (&yb)[TN]) {
+        if (j + 1 < stages) {
+            wait_copies<0>();
+            read(ya, yb);
+            if (j + STAGES < stages) fetch();
+        }
+        multiply(xa, xb);
+    };
+    if (stages > 0) {
+        segment();
 #pragma unroll
-                for (int j = 0; j < TN; ++j)
-                    acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(fb[j], fa[i], acc[i][j], 0, 0, 0);
+        for (int s = 0; s < STAGES; ++s)
+            if (s < stages) fetch();
+        if (stages >= STAGES) wait_copies<(STAGES - 1) * (LA + LB)>(); else wait_copies<0>();
+        read(fa[0], fb[0]);
+        int j = 0;
+        for (; j + 1 + STAGES < stages; j += 2) {
+            steady(fa[0], fb[0], fa[1], fb[1]);
+            steady(fa[1], fb[1], fa[0], fb[0]);
+        }
+        for (; j < stages; j += 2) {
+            last(j, fa[0], fb[0], fa[1], fb[1]);
+            last(j + 1, fa[1], fb[1], fa[0], fb[0]);
         }
     }
 
@@ -491,6 +531,8 @@ constexpr int PAIRS[6][2] = {{1, 1}, {0, 2}, {2, 0}, {0, 1}, {1, 0}, {0, 0}};
 
 struct Mat { const bf16* p; int64_t ld, plane; };  // an operand, or its planes
 
+constexpr int BIG_STAGES = 5, SMALL_STAGES = 4;
+
 // Tile shape and shares of a product of M x N results over `steps` steps.
 struct Shape { bool big; int mt, nt, split; };
 Shape shape_of(int64_t M, int64_t N, bool dual, int halves, int steps, bool may_split) {
@@ -504,7 +546,7 @@ Shape shape_of(int64_t M, int64_t N, bool dual, int halves, int steps, bool may_
     s.nt = (int)((N + (dual ? bn / 2 : bn) - 1) / (dual ? bn / 2 : bn));
     s.split = 1;
     if (may_split && !s.big) {
-        const int64_t t = tiles(bm, bn) > 0 ? tiles(bm, bn) : 1, want = (512 + t - 1) / t, most = steps / 8 > 0 ? steps / 8 : 1;
+        const int64_t t = tiles(bm, bn) > 0 ? tiles(bm, bn) : 1, want = (512 + t - 1) / t, most = steps / 16 > 0 ? steps / 16 : 1;
         s.split = (int)(want < most ? want : most);
     }
     return s;
@@ -518,14 +560,14 @@ hipError_t run_gemm(GemmArgs g, const Shape& s, hipStream_t st) {
     const int64_t total = (int64_t)s.mt * s.nt * s.split * g.halves, blocks = (total + 7) / 8 * 8;
     hipError_t e;
     if (s.big) {
-        constexpr int lds = 2 * 512 * BK * 2;
-        auto* k = glu_gemm_kernel<DT, 256, 256, 2, 4, 2, AKR, BKR, EPI, ACT>;
+        constexpr int lds = BIG_STAGES * 512 * BK * 2;
+        auto* k = glu_gemm_kernel<DT, 256, 256, 2, 4, BIG_STAGES, AKR, BKR, EPI, ACT>;
         e = hipFuncSetAttribute((const void*)k, hipFuncAttributeMaxDynamicSharedMemorySize, lds);
         if (e != hipSuccess) return e;
         hipLaunchKernelGGL(k, dim3((unsigned)blocks), dim3(512), lds, st, g);
     } else {
-        constexpr int lds = 2 * 256 * BK * 2;
-        auto* k = glu_gemm_kernel<DT, 128, 128, 2, 2, 2, AKR, BKR, EPI, ACT>;
+        constexpr int lds = SMALL_STAGES * 256 * BK * 2;
+        auto* k = glu_gemm_kernel<DT, 128, 128, 2, 2, SMALL_STAGES, AKR, BKR, EPI, ACT>;
         hipLaunchKernelGGL(k, dim3((unsigned)blocks), dim3(256), lds, st, g);
     }
     return hipGetLastError();
@@ -559,14 +601,14 @@ struct Work {
     bf16 *x = nullptr, *wg = nullptr, *wu = nullptr, *dg = nullptr, *du = nullptr;
     float* part = nullptr;
 };
-int pad_of(const GluArgs& a) { return (int)up(a.D, BK); }
+int pad_of(const GluArgs& a) { return (int)up(a.D, PAD); }
 Shape dx_shape(const GluArgs& a) {
     const int np = planes(a);
-    return shape_of(a.T, a.D, false, 1, (int)(up(a.F, BK) / BK) * 2 * (np == 1 ? 1 : 6), true);
+    return shape_of(a.T, a.D, false, 1, (int)(up(a.F, PAD) / BK) * 2 * (np == 1 ? 1 : 6), true);
 }
 Shape dw_shape(const GluArgs& a) {
     const int np = planes(a);
-    return shape_of(a.F, a.D, false, 2, (int)(up(a.T, BK) / BK) * (np == 1 ? 1 : 6), true);
+    return shape_of(a.F, a.D, false, 2, (int)(up(a.T, PAD) / BK) * (np == 1 ? 1 : 6), true);
 }
 Work work_of(const GluArgs& a, bool backward, bool input_grad, uint8_t* base) {
     Work w;
@@ -583,7 +625,7 @@ Work work_of(const GluArgs& a, bool backward, bool input_grad, uint8_t* base) {
         w.wu = (bf16*)take(a.F * pad * np * 2);
     }
     if (backward) {
-        const int64_t one = up(a.T, BK) * up(a.F, BK) * np * 2;
+        const int64_t one = up(a.T, PAD) * up(a.F, PAD) * np * 2;
         w.dg = (bf16*)take(one);
         w.du = (bf16*)take(one);
         const Shape sx = dx_shape(a), sw = dw_shape(a);
@@ -653,9 +695,9 @@ template <typename DT, int ACT> hipError_t backward(const GluArgs& a, hipStream_
     const int np = planes(a), n = np == 1 ? 1 : 6;
     GemmArgs g = {};
     g.T = a.T;
-    g.Tpad = up(a.T, BK);
+    g.Tpad = up(a.T, PAD);
     g.F = a.F;
-    g.Fpad = (int)up(a.F, BK);
+    g.Fpad = (int)up(a.F, PAD);
     g.plane = g.Tpad * g.Fpad;
     g.dh = a.dh;
     g.hs = a.hs;
