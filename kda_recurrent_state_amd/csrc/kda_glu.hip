@@ -48,7 +48,7 @@ template <int ACT> __device__ __forceinline__ float gated(float g, float u) {
 // first form, and there are a multiple of 64 columns in the second.  Rows past the last are the last again, and their
 // results are not stored; k rows past the last meet zeros of the other operand.
 
-constexpr int BK = 32;    // k of a stage: one matrix instruction's
+constexpr int KI = 32;    // k of a matrix instruction
 constexpr int PAD = 64;   // what k and padded columns are a multiple of
 constexpr int MAX_SEGS = 12;
 
@@ -58,7 +58,7 @@ struct GemmArgs {
     int64_t lda, ldb;          // elements between rows
     int64_t M, N;              // rows of A and B (of each of the two B where there are two)
     int64_t kA, kB, colsA, colsB;  // k rows that exist, and their columns, a multiple of 64 (KR)
-    int32_t segs, ksteps;      // steps of BK in a segment
+    int32_t segs, ksteps;      // stages of a segment
     int32_t mt, nt, split;     // tiles, shares of the sum
     int32_t halves;            // outputs: seg[0..segs) and seg[segs..2 segs)
     // epilogue
@@ -72,23 +72,27 @@ struct GemmArgs {
     int32_t F, Fpad;
 };
 
-template <bool KR> struct Operand;
-// [rows][k]: a row of 32 k is 64 bytes in LDS, its 16-byte pieces exchanged by the row's number so that 16
+template <int V> struct Int { static constexpr int value = V; };
+
+template <bool KR, int BK> struct Operand;
+// [rows][k]: a row of BK k is 64 or 128 bytes in LDS, its 16-byte pieces exchanged by the row's number so that
 // neighbouring rows' pieces of the same k lie in different banks.
-template <> struct Operand<false> {
+template <int BK> struct Operand<false, BK> {
+    static constexpr int P = BK / 8;
+    static __device__ __forceinline__ int turn(int row) { return P == 8 ? row & 7 : (row >> 2) & 3; }
     static __device__ __forceinline__ int source(int at, int64_t rows_left, int64_t ld, int) {
-        const int row = at / 4, piece = (at & 3) ^ ((row >> 2) & 3);
+        const int row = at / P, piece = (at % P) ^ turn(row);
         const int64_t r = row < rows_left ? row : rows_left - 1;
         return (int)(r * ld * 2) + piece * 16;
     }
-    static __device__ __forceinline__ bf16x8 frag(const char* tile, int row0, int lane, int) {
-        const int row = row0 + (lane & 15), piece = (lane >> 4) ^ ((row >> 2) & 3);
-        return *reinterpret_cast<const bf16x8*>(tile + row * 64 + piece * 16);
+    static __device__ __forceinline__ bf16x8 frag(const char* tile, int row0, int part, int lane, int) {
+        const int row = row0 + (lane & 15), piece = (part * 4 + (lane >> 4)) ^ turn(row);
+        return *reinterpret_cast<const bf16x8*>(tile + row * (BK * 2) + piece * 16);
     }
 };
 // [k][rows]: a k row of R columns is 2 R bytes, its 32-byte pieces (16 columns) exchanged so that the 8 k rows that
 // half a wavefront reads at once lie in different banks.
-template <> struct Operand<true> {
+template <int BK> struct Operand<true, BK> {
     static __device__ __forceinline__ int turn(int k) { return (k & 3) | ((k >> 3) & 1) << 2; }
     static __device__ __forceinline__ int source(int at, int64_t rows_left, int64_t ld, int rows) {
         const int per = rows / 8, k = at / per, slot = at % per;
@@ -96,9 +100,9 @@ template <> struct Operand<true> {
         const int64_t col = c + 8 <= rows_left ? c : rows_left - 8;
         return (int)(k * ld * 2 + col * 2);
     }
-    static __device__ __forceinline__ bf16x8 frag(const char* tile, int row0, int lane, int rows) {
+    static __device__ __forceinline__ bf16x8 frag(const char* tile, int row0, int part, int lane, int rows) {
         typedef __attribute__((address_space(3))) s16x4* lds;
-        const int i = lane & 15, q = lane >> 4, k = 8 * q + (i >> 2);
+        const int i = lane & 15, q = lane >> 4, k = part * KI + 8 * q + (i >> 2);
         const char* p = tile + k * rows * 2 + (((row0 >> 4) ^ turn(k)) * 32) + (i & 3) * 8;
         const bf16x4 lo = __builtin_bit_cast(bf16x4, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds)(p)));
         const bf16x4 hi = __builtin_bit_cast(bf16x4, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds)(p + 4 * rows * 2)));
@@ -106,7 +110,7 @@ template <> struct Operand<true> {
     }
 };
 
-__device__ __forceinline__ void copy16(const char* base, int offset, char* lds) {
+__device__ __forceinline__ void copy16(const char* base, int64_t offset, char* lds) {
     __builtin_amdgcn_global_load_lds((const void*)(base + offset), (__attribute__((address_space(3))) void*)lds, 16, 0, 0);
 }
 
@@ -168,16 +172,18 @@ __device__ __forceinline__ void store_dgu(const GemmArgs& g, int64_t t, int64_t 
 
 enum { EPI_OUT, EPI_H, EPI_DGU };
 
-// BM x BN results a workgroup of WM x WN wavefronts.  Both operands come in stages of 32 k, STAGES of them in LDS:
-// while a stage is multiplied out of registers, the next is read from LDS into others and the ones after it
-// arrive, so that a copy has STAGES - 1 stages' time.  One barrier a stage: behind it the next stage's copies are
-// complete and the stage before it, read by everyone, takes the next copies.  With two B (EPI_H, EPI_DGU) the
+// BM x BN results a workgroup of WM x WN wavefronts.  Both operands come in stages of BK k, STAGES of them in LDS.
+// The next 32 k are read from LDS into registers while 32 are multiplied out of others, and the stages after
+// this one are on their way.  One barrier a stage, where its last 32 k are in everyone's registers: behind it
+// the next stage's copies are complete, and this one's place takes new ones.  With two B (EPI_H, EPI_DGU) the
 // first half of BN is of one and the second of the other, so that a lane holds both results of a column.
-template <typename DT, int BM, int BN, int WM, int WN, int STAGES, bool AKR, bool BKR, int EPI, int ACT>
+template <typename DT, int BM, int BN, int BK, int WM, int WN, int STAGES, bool AKR, bool BKR, int EPI, int ACT>
 __global__ void __launch_bounds__(WM* WN * 64, 2) glu_gemm_kernel(GemmArgs g) {
     constexpr bool DUAL = EPI != EPI_OUT;
     constexpr int THREADS = WM * WN * 64, TM = BM / WM / 16, TN = BN / WN / 16;
-    constexpr int LA = BM * 4 / THREADS, LB = BN * 4 / THREADS, STAGE = (BM + BN) * BK * 2;
+    constexpr int P = BK / 8, LA = BM * P / THREADS, LB = BN * P / THREADS, STAGE = (BM + BN) * BK * 2, PARTS = BK / KI;
+    using OA = Operand<AKR, BK>;
+    using OB = Operand<BKR, BK>;
     constexpr int BH = DUAL ? BN / 2 : BN;  // columns of one B in a tile
     extern __shared__ __attribute__((aligned(1024))) char smem[];
     const int tid = threadIdx.x, lane = tid % 64, wave = __builtin_amdgcn_readfirstlane(tid / 64);
@@ -197,16 +203,17 @@ __global__ void __launch_bounds__(WM* WN * 64, 2) glu_gemm_kernel(GemmArgs g) {
 
     int offa[LA], offb[LB];
 #pragma unroll
-    for (int i = 0; i < LA; ++i) offa[i] = Operand<AKR>::source(i * THREADS + tid, (AKR ? g.colsA : g.M) - m0, g.lda, BM);
+    for (int i = 0; i < LA; ++i) offa[i] = OA::source(i * THREADS + tid, (AKR ? g.colsA : g.M) - m0, g.lda, BM);
 #pragma unroll
     for (int i = 0; i < LB; ++i) {
         const int at = i * THREADS + tid;
-        if (DUAL) offb[i] = Operand<false>::source(at % (BH * 4), g.N - n0, g.ldb, BH);
-        else offb[i] = Operand<BKR>::source(at, (BKR ? g.colsB : g.N) - n0, g.ldb, BN);
+        if (DUAL) offb[i] = OB::source(at % (BH * P), g.N - n0, g.ldb, BH);
+        else offb[i] = OB::source(at, (BKR ? g.colsB : g.N) - n0, g.ldb, BN);
     }
-    // this share's stages, an even number from an even one on
-    const int all = g.segs * g.ksteps / 2, k0 = (int)((int64_t)share * all / g.split) * 2;
-    const int stages = (int)((int64_t)(share + 1) * all / g.split) * 2 - k0;
+    // this share's stages, whole pairs of 32 k
+    constexpr int PAIR = 2 / PARTS;
+    const int all = g.segs * g.ksteps / PAIR, k0 = (int)((int64_t)share * all / g.split) * PAIR;
+    const int stages = (int)((int64_t)(share + 1) * all / g.split) * PAIR - k0;
 
     // What is fetched next: its operands' addresses, moved on by a stage each time and looked up where a segment
     // begins, and its place in LDS.
@@ -238,10 +245,10 @@ __global__ void __launch_bounds__(WM* WN * 64, 2) glu_gemm_kernel(GemmArgs g) {
             }
         } else {
 #pragma unroll
-            for (int i = 0; i < LA; ++i) copy16(pa, offa[i], at + i * THREADS * 16);
+            for (int i = 0; i < LA; ++i) copy16(pa, (unsigned)offa[i], at + i * THREADS * 16);
 #pragma unroll
             for (int i = 0; i < LB; ++i)
-                copy16(DUAL && i * THREADS >= BH * 4 ? pb2 : pb, offb[i], at + BM * BK * 2 + i * THREADS * 16);
+                copy16(DUAL && i * THREADS >= BH * P ? pb2 : pb, (unsigned)offb[i], at + BM * BK * 2 + i * THREADS * 16);
         }
         if (++fslot == STAGES) fslot = 0;
         pa += stepa;
@@ -261,17 +268,17 @@ __global__ void __launch_bounds__(WM* WN * 64, 2) glu_gemm_kernel(GemmArgs g) {
         for (int j = 0; j < TN; ++j) acc[i][j] = zero4();
     bf16x8 fa[2][TM], fb[2][TN];
     int rslot = 0;
-    auto read = [&](bf16x8 (&xa)[TM], bf16x8 (&xb)[TN]) {
+    auto read = [&](int part, bf16x8 (&xa)[TM], bf16x8 (&xb)[TN]) {
         const char* ta = smem + rslot * STAGE;
         const char* tb = ta + BM * BK * 2;
 #pragma unroll
         for (int j = 0; j < TN; ++j) {
             const int row = DUAL ? (j >= TN / 2 ? BH : 0) + wn * (BH / WN) + j % (TN / 2) * 16 : wn * (BN / WN) + j * 16;
-            xb[j] = Operand<BKR>::frag(tb, row, lane, BN);
+            xb[j] = OB::frag(tb, row, part, lane, BN);
         }
 #pragma unroll
-        for (int i = 0; i < TM; ++i) xa[i] = Operand<AKR>::frag(ta, wm * (BM / WM) + i * 16, lane, BM);
-        if (++rslot == STAGES) rslot = 0;
+        for (int i = 0; i < TM; ++i) xa[i] = OA::frag(ta, wm * (BM / WM) + i * 16, part, lane, BM);
+        if (part == PARTS - 1 && ++rslot == STAGES) rslot = 0;
     };
     auto multiply = [&](const bf16x8 (&xa)[TM], const bf16x8 (&xb)[TN]) {
 #pragma unroll
@@ -279,36 +286,38 @@ __global__ void __launch_bounds__(WM* WN * 64, 2) glu_gemm_kernel(GemmArgs g) {
 #pragma unroll
             for (int j = 0; j < TN; ++j) acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(xb[j], xa[i], acc[i][j], 0, 0, 0);
     };
-    // stage j is in one set of registers, stage j + 1 goes to the other
-    auto steady = [&](const bf16x8 (&xa)[TM], const bf16x8 (&xb)[TN], bf16x8 (&ya)[TM], bf16x8 (&yb)[TN]) {
-        wait_copies<(STAGES - 2) * (LA + LB)>();
-        read(ya, yb);
-        fetch();
-        multiply(xa, xb);
+    // the first 32 k of the next stage, of which at most LEFT copies are still on their way behind it
+    auto next = [&](auto left, bool more, bf16x8 (&xa)[TM], bf16x8 (&xb)[TN]) {
+        wait_copies<decltype(left)::value>();
+        read(0, xa, xb);
+        if (more) fetch();
     };
-    auto last = [&](int j, const bf16x8 (&xa)[TM], const bf16x8 (&xb)[TN], bf16x8 (&ya)[TM], bf16x8 (&yb)[TN]) {
-        if (j + 1 < stages) {
-            wait_copies<0>();
-            read(ya, yb);
-            if (j + STAGES < stages) fetch();
-        }
-        multiply(xa, xb);
-    };
+    constexpr int LEFT = (STAGES - 2) * (LA + LB);
     if (stages > 0) {
         segment();
 #pragma unroll
         for (int s = 0; s < STAGES; ++s)
             if (s < stages) fetch();
         if (stages >= STAGES) wait_copies<(STAGES - 1) * (LA + LB)>(); else wait_copies<0>();
-        read(fa[0], fb[0]);
+        read(0, fa[0], fb[0]);
         int j = 0;
-        for (; j + 1 + STAGES < stages; j += 2) {
-            steady(fa[0], fb[0], fa[1], fb[1]);
-            steady(fa[1], fb[1], fa[0], fb[0]);
+        // the next stages exist: no conditions in the loop
+        for (; j + PAIR - 1 + STAGES < stages; j += PAIR) {
+            if constexpr (PARTS == 1) next(Int<LEFT>(), true, fa[1], fb[1]);
+            else read(1, fa[1], fb[1]);
+            multiply(fa[0], fb[0]);
+            next(Int<LEFT>(), true, fa[0], fb[0]);
+            multiply(fa[1], fb[1]);
         }
-        for (; j < stages; j += 2) {
-            last(j, fa[0], fb[0], fa[1], fb[1]);
-            last(j + 1, fa[1], fb[1], fa[0], fb[0]);
+        for (; j < stages; j += PAIR) {
+            if constexpr (PARTS == 1) {
+                if (j + 1 < stages) next(Int<0>(), j + STAGES < stages, fa[1], fb[1]);
+            } else {
+                read(1, fa[1], fb[1]);
+            }
+            multiply(fa[0], fb[0]);
+            if (j + PAIR < stages) next(Int<0>(), j + PAIR - 1 + STAGES < stages, fa[0], fb[0]);
+            multiply(fa[1], fb[1]);
         }
     }
 
@@ -531,7 +540,6 @@ constexpr int PAIRS[6][2] = {{1, 1}, {0, 2}, {2, 0}, {0, 1}, {1, 0}, {0, 0}};
 
 struct Mat { const bf16* p; int64_t ld, plane; };  // an operand, or its planes
 
-constexpr int BIG_STAGES = 5, SMALL_STAGES = 4;
 
 // Tile shape and shares of a product of M x N results over `steps` steps.
 struct Shape { bool big; int mt, nt, split; };
@@ -552,25 +560,35 @@ Shape shape_of(int64_t M, int64_t N, bool dual, int halves, int steps, bool may_
     return s;
 }
 
+template <typename DT, int SIDE, int BK, int STAGES, bool AKR, bool BKR, int EPI, int ACT>
+hipError_t launch_gemm(GemmArgs g, int64_t blocks, hipStream_t st) {
+    constexpr int lds = STAGES * 2 * SIDE * BK * 2, WN = SIDE / 64;
+    static_assert(lds <= 160 * 1024, "the stages fit a compute unit");
+    auto* k = glu_gemm_kernel<DT, SIDE, SIDE, BK, 2, WN, STAGES, AKR, BKR, EPI, ACT>;
+    if (lds > 65536) {
+        const hipError_t e = hipFuncSetAttribute((const void*)k, hipFuncAttributeMaxDynamicSharedMemorySize, lds);
+        if (e != hipSuccess) return e;
+    }
+    g.ksteps /= BK;
+    hipLaunchKernelGGL(k, dim3((unsigned)blocks), dim3(2 * WN * 64), lds, st, g);
+    return hipGetLastError();
+}
+
+// (g.ksteps: k of a segment)
 template <typename DT, bool AKR, bool BKR, int EPI, int ACT>
 hipError_t run_gemm(GemmArgs g, const Shape& s, hipStream_t st) {
     g.mt = s.mt;
     g.nt = s.nt;
     g.split = s.split;
     const int64_t total = (int64_t)s.mt * s.nt * s.split * g.halves, blocks = (total + 7) / 8 * 8;
-    hipError_t e;
-    if (s.big) {
-        constexpr int lds = BIG_STAGES * 512 * BK * 2;
-        auto* k = glu_gemm_kernel<DT, 256, 256, 2, 4, BIG_STAGES, AKR, BKR, EPI, ACT>;
-        e = hipFuncSetAttribute((const void*)k, hipFuncAttributeMaxDynamicSharedMemorySize, lds);
-        if (e != hipSuccess) return e;
-        hipLaunchKernelGGL(k, dim3((unsigned)blocks), dim3(512), lds, st, g);
-    } else {
-        constexpr int lds = SMALL_STAGES * 256 * BK * 2;
-        auto* k = glu_gemm_kernel<DT, 128, 128, 2, 2, SMALL_STAGES, AKR, BKR, EPI, ACT>;
-        hipLaunchKernelGGL(k, dim3((unsigned)blocks), dim3(256), lds, st, g);
-    }
-    return hipGetLastError();
+    // Stages of 64 k where both operands have k contiguous: their rows are then read in whole cache lines
+    // (8192 x 4096 x 20480: 1160 us; of 32, half lines, 1314).  An operand with k along the rows is read in whole
+    // lines either way, and five stages of 32 have more time to arrive than two of 64: 1154 us against 1672
+    // for both such (dW), 1171 against 1184 for one (dx).  Small tiles: 64 (777 x 1000 x 2731 fp32, three
+    // products: 82, 91, 75 us; of 32: 103, 104, 86).
+    constexpr int BK = AKR || BKR ? 32 : 64;
+    if (s.big) return launch_gemm<DT, 256, BK, BK == 32 ? 5 : 2, AKR, BKR, EPI, ACT>(g, blocks, st);
+    return launch_gemm<DT, 128, 64, 2, AKR, BKR, EPI, ACT>(g, blocks, st);
 }
 
 template <typename DT> hipError_t sum_shares(const float* part, int split, int64_t n, void* out, hipStream_t st) {
@@ -604,11 +622,11 @@ struct Work {
 int pad_of(const GluArgs& a) { return (int)up(a.D, PAD); }
 Shape dx_shape(const GluArgs& a) {
     const int np = planes(a);
-    return shape_of(a.T, a.D, false, 1, (int)(up(a.F, PAD) / BK) * 2 * (np == 1 ? 1 : 6), true);
+    return shape_of(a.T, a.D, false, 1, (int)(up(a.F, PAD) / KI) * 2 * (np == 1 ? 1 : 6), true);
 }
 Shape dw_shape(const GluArgs& a) {
     const int np = planes(a);
-    return shape_of(a.F, a.D, false, 2, (int)(up(a.T, PAD) / BK) * (np == 1 ? 1 : 6), true);
+    return shape_of(a.F, a.D, false, 2, (int)(up(a.T, PAD) / KI) * (np == 1 ? 1 : 6), true);
 }
 Work work_of(const GluArgs& a, bool backward, bool input_grad, uint8_t* base) {
     Work w;
@@ -659,7 +677,7 @@ template <typename DT, int EPI, int ACT> hipError_t products(const GluArgs& a, c
         g.seg[i] = {in.x.p + pa * in.x.plane, in.wg.p + pb * in.wg.plane, in.wu.p + pb * in.wu.plane};
     }
     g.segs = n;
-    g.ksteps = pad_of(a) / BK;
+    g.ksteps = pad_of(a);
     g.lda = in.x.ld;
     g.ldb = in.wg.ld;
     g.M = a.T;
@@ -721,7 +739,7 @@ template <typename DT, int ACT> hipError_t backward(const GluArgs& a, hipStream_
             p.seg[2 * i + 1] = {w.du + pa * g.plane, in.wu.p + pb * in.wu.plane, nullptr};
         }
         p.segs = 2 * n;
-        p.ksteps = g.Fpad / BK;
+        p.ksteps = g.Fpad;
         p.lda = g.Fpad;
         p.ldb = in.wg.ld;
         p.M = a.T;
@@ -742,7 +760,7 @@ template <typename DT, int ACT> hipError_t backward(const GluArgs& a, hipStream_
         p.seg[n + i] = {w.du + pa * g.plane, in.x.p + pb * in.x.plane, nullptr};
     }
     p.segs = n;
-    p.ksteps = (int)(g.Tpad / BK);
+    p.ksteps = (int)g.Tpad;
     p.lda = g.Fpad;
     p.ldb = in.x.ld;
     p.M = a.F;
