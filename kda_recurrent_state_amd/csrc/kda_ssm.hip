@@ -210,11 +210,11 @@ __device__ __forceinline__ double lanes_scan(double v, int lane) {
 
 // The decays of a chunk, one token a lane: c as hi + lo and what comes of it.
 template <int Q> struct Decays {
-    float hi[Q], lo[Q], src[Q], from[Q], to[Q];
+    float hi[Q], lo[Q], src[Q], from[Q], to[Q], total, pad[15];  // total: 2^{total}
     // src: d; from: 2^{c}; to: 2^{total - c}
 };
 template <int Q>
-__device__ __forceinline__ double decays(Decays<Q>& w, const SsmArgs& a, int h, int first, int n, int lane) {
+__device__ __forceinline__ void decays(Decays<Q>& w, const SsmArgs& a, int h, int first, int n, int lane) {
     float d = 0.f;
     double l = 0.0;
     if (lane < n) {
@@ -230,8 +230,8 @@ __device__ __forceinline__ double decays(Decays<Q>& w, const SsmArgs& a, int h, 
         w.src[lane] = d;
         w.from[lane] = exp2f((float)c);
         w.to[lane] = exp2f((float)(total - c));
+        if (lane == 0) w.total = exp2f((float)total);
     }
-    return total;
 }
 
 // Sum over the 16 lanes of a group by rotations inside the group: no trip through LDS.
@@ -751,6 +751,23 @@ __global__ void __launch_bounds__(NT) ssm_join_kernel(SsmArgs a, const float* fi
     }
 }
 
+template <int Q> struct GradSums { float row[WAVES][Q], col[WAVES][Q], ui[WAVES][Q], vi[WAVES][Q], xy[Q], hg[WAVES]; };
+
+// The decays of every chunk and head, for the gradient: a wavefront each.
+template <typename DT>
+__global__ void __launch_bounds__(NT) ssm_decay_kernel(SsmArgs a, int slots) {
+    constexpr int Q = Cfg<DT>::QT * 16;
+    const int lane = threadIdx.x % WAVE;
+    const int64_t i = (int64_t)blockIdx.x * WAVES + threadIdx.x / WAVE;
+    if (i >= (int64_t)slots * a.H) return;
+    const int slot = __builtin_amdgcn_readfirstlane((int)(i / a.H)), h = __builtin_amdgcn_readfirstlane((int)(i % a.H));
+    const Seqs sq{a.cu, a.N, a.T, a.eq};
+    const Piece pc = find_piece(sq, slot, Q);
+    if (!pc.live || pc.len == 0) return;
+    const int c0 = pc.start + pc.n * Q, n = min(Q, pc.len - pc.n * Q);
+    decays<Q>(reinterpret_cast<Decays<Q>*>(a.dec)[i], a, h, c0, n, lane);
+}
+
 // The gradient that needs the states from both sides, a workgroup per chunk and share of a group's
 // units.  With M[t][s] = (C_t . B_s) 2^{c_t - c_s} and E[t][s] = dy_t . x_s, s <= t, h the state
 // before the chunk and g the derivative behind it:
@@ -759,16 +776,17 @@ __global__ void __launch_bounds__(NT) ssm_join_kernel(SsmArgs a, const float* fi
 //   d(d_s) = sum_t (M E)[t][s] + 2^{c_Q - c_s} B_s . (x_s g^T)      (without the decays)
 //   dl_t = sum of d_s (M E)[r][s] over r >= t > s + sum_{r >= t} 2^{c_r} C_r . (dy_r h^T)
 //          + sum_{s < t} d_s 2^{c_Q - c_s} B_s . (x_s g^T) + 2^{c_Q} h . g
-// dB and dC are summed over the group's heads in registers.  The wavefronts share a unit: each forms
-// 16 rows of M, E and their products (in LDS as bf16 parts), then a quarter of the columns of
-// dB and dC, so no sum crosses wavefronts but those of single numbers a token.
+// dB and dC are summed over the group's heads in registers.  The wavefronts share a unit: each forms up to
+// three 16 x 16 tiles of E and its products (in LDS as bf16 parts; C . B, the same for all heads, stays in
+// registers), then a quarter of the columns of dB and dC, so no sum crosses wavefronts but those of single
+// numbers a token, which ssm_tokens_kernel puts together.
 template <typename DT, int KT, int PT>
 __global__ void __launch_bounds__(NT, 2) ssm_grad_kernel(SsmArgs a, int slots, int quads) {
     using C_ = Cfg<DT>;
     constexpr int QT = C_::QT, Q = QT * 16, NP = C_::NP, MP = C_::MP;
     constexpr int LDK = KT * 16 + 8, LDP = PT * 16 + 8, LDQ = Q + 8, PLK = Q * LDK, PLP = Q * LDP, PLQ = Q * LDQ;
     constexpr int KW = KT < WAVES ? 1 : KT / WAVES;  // column tiles of a wavefront
-    struct Sums { float row[Q], col[WAVES][Q], ui[WAVES][Q], vi[WAVES][Q], xy[Q], hg[WAVES]; };
+    using Sums = GradSums<Q>;
     extern __shared__ __attribute__((aligned(16))) char smem[];
     bf16* sb = reinterpret_cast<bf16*>(smem);
     bf16* sc = sb + NP * PLK;
@@ -790,12 +808,53 @@ __global__ void __launch_bounds__(NT, 2) ssm_grad_kernel(SsmArgs a, int slots, i
     const int u0 = (int)((int64_t)at.quad * units / quads), u1 = (int)((int64_t)(at.quad + 1) * units / quads);
     const int64_t all_units = (int64_t)a.H * a.blocks;
 
+    Stage<DT, Q, PT * 16, NT> bx, by;  // the next unit's, on their way
+    float nd[5];
+    auto fetch = [&](int un, unsigned tid) {
+        const int unit = at.group * units + un, h = unit / a.blocks, p0 = unit % a.blocks * (PT * 16);
+        const int cols = min(a.P - p0, PT * 16);
+        bx.load((const DT*)a.x + (int64_t)h * a.P + p0, a.xs, cols, c0, false, n, tid);
+        by.load((const DT*)a.dy + (int64_t)h * a.P + p0, a.dys, cols, c0, false, n, tid);
+        if (tid < Q) {
+            const float* d = reinterpret_cast<const float*>(&reinterpret_cast<const Decays<Q>*>(a.dec)[(int64_t)at.slot * a.H + h]);
+#pragma unroll
+            for (int i = 0; i < 5; ++i) nd[i] = d[i * Q + tid];
+        }
+    };
     {
         Stage<DT, Q, KT * 16, NT> bk, bq;
         bk.load((const DT*)a.B + (int64_t)at.group * a.K, a.bs, a.K, c0, false, n, tid);
         bq.load((const DT*)a.C + (int64_t)at.group * a.K, a.cs, a.K, c0, false, n, tid);
+        fetch(u0, tid);
         bk.store(sb, LDK, PLK, tid);
         bq.store(sc, LDK, PLK, tid);
+        // what no tile writes stays zero: products above the diagonal, sums that a wavefront has no part in
+        for (int i = tid; i < MP * PLQ / 2; i += NT) reinterpret_cast<uint32_t*>(sds)[i] = 0;
+        for (int i = tid; i < (int)(sizeof(Sums) / 4); i += NT) reinterpret_cast<uint32_t*>(&sum)[i] = 0;
+    }
+    __syncthreads();
+
+    // the wavefront's tiles (rows j, columns i), no two with the same columns
+    constexpr int NTILE = QT == 4 ? 3 : 1;
+    const int tiles = QT == 4 ? (wave == 0 || wave == 3 ? 2 : 3) : (wave < 3 ? 1 : 0);
+    auto tile_j = [&](int x) { return QT == 4 ? (wave == 0 ? 3 : wave == 1 ? (x < 2 ? 3 : 0) : wave == 2 ? 2 : 1) : (wave < 2 ? 1 : 0); };
+    auto tile_i = [&](int x) { return QT == 4 ? (wave == 1 ? (x < 2 ? 2 + x : 0) : x) : (wave == 1 ? 1 : 0); };
+    f32x4 cb[NTILE];  // C . B
+#pragma unroll
+    for (int x = 0; x < NTILE; ++x) {
+        cb[x] = zero4();
+        if (x >= tiles) continue;
+        const int t = 16 * tile_j(x) + l15, s = 16 * tile_i(x) + l15;
+#pragma unroll
+        for (int kk = 0; kk < KT / 2; ++kk) {
+            Parts<NP> f, c;
+#pragma unroll
+            for (int m = 0; m < NP; ++m) {
+                f.p[m] = row_natural(sb + m * PLK + s * LDK + 32 * kk, lane);
+                c.p[m] = row_natural(sc + m * PLK + t * LDK + 32 * kk, lane);
+            }
+            cb[x] = mma_parts(f, c, cb[x]);
+        }
     }
     f32x4 dB[QT][KW], dC[QT][KW];
 #pragma unroll
@@ -803,23 +862,18 @@ __global__ void __launch_bounds__(NT, 2) ssm_grad_kernel(SsmArgs a, int slots, i
 #pragma unroll
         for (int k = 0; k < KW; ++k) dB[j][k] = dC[j][k] = zero4();
 
-    Stage<DT, Q, PT * 16, NT> bx, by;  // the next unit's, on their way
-    auto fetch = [&](int un, unsigned tid) {
-        const int unit = at.group * units + un, h = unit / a.blocks, p0 = unit % a.blocks * (PT * 16);
-        const int cols = min(a.P - p0, PT * 16);
-        bx.load((const DT*)a.x + (int64_t)h * a.P + p0, a.xs, cols, c0, false, n, tid);
-        by.load((const DT*)a.dy + (int64_t)h * a.P + p0, a.dys, cols, c0, false, n, tid);
-    };
-    fetch(u0, tid);
     for (int un = u0; un < u1; ++un) {
         const int unit = at.group * units + un, h = unit / a.blocks;
-        float total = 0.f;
         // The last unit's products are read (its third barrier); the states are on their way through the first phase.
         {
-            const unsigned tid = renewed(threadIdx.x), lane = tid % WAVE;
-            if (wave == 0) total = exp2f((float)decays<Q>(dec, a, h, c0, n, lane));
+            const unsigned tid = renewed(threadIdx.x);
             bx.store(sx, LDP, PLP, tid);
             by.store(sdy, LDP, PLP, tid);
+            if (tid < Q) {
+                float* d = reinterpret_cast<float*>(&dec);
+#pragma unroll
+                for (int i = 0; i < 5; ++i) d[i * Q + tid] = nd[i];
+            }
             if (un + 1 < u1) fetch(un + 1, tid);
         }
         Pack<float, 8> hv[PT / 2], gv[PT / 2];
@@ -828,16 +882,17 @@ __global__ void __launch_bounds__(NT, 2) ssm_grad_kernel(SsmArgs a, int slots, i
             const int wide = a.blocks * (PT * 16);
             const int64_t state = (cslot * a.H + h) * ((int64_t)KT * 16 * wide) + (wave * KW + k) * 16 * wide + unit % a.blocks * (PT * 16);
             const int left = a.wblocks * a.wcols - unit % a.blocks * (PT * 16);
-            const int lane = renewed(threadIdx.x) % WAVE, own = (lane & 15) * wide + 8 * (lane >> 4);
+            const unsigned lane = renewed(threadIdx.x) % WAVE, own = (lane & 15) * wide + 8 * (lane >> 4);
+            const float *ph = a.hs + state, *pg = a.gs + state;
 #pragma unroll
             for (int pp = 0; pp < PT / 2; ++pp) {
-                hv[pp] = load_v<8>(a.hs + state + (own + 32 * pp));
-                gv[pp] = load_v<8>(a.gs + state + (own + 32 * pp));
+                hv[pp] = load_v<8>(ph + (own + 32 * pp));
+                gv[pp] = load_v<8>(pg + (own + 32 * pp));
             }
             if (left < PT * 16) {  // columns that no unit of the walk has written
 #pragma unroll
                 for (int pp = 0; pp < PT / 2; ++pp)
-                    if (32 * pp + 8 * (lane >> 4) >= left) {
+                    if ((int)(32 * pp + 8 * (lane >> 4)) >= left) {
                         hv[pp] = Pack<float, 8>{};
                         gv[pp] = Pack<float, 8>{};
                     }
@@ -846,77 +901,55 @@ __global__ void __launch_bounds__(NT, 2) ssm_grad_kernel(SsmArgs a, int slots, i
         if (wave * KW < KT) states(0);
         __syncthreads();
 
-        // rows t of tile `wave` against every s up to them, transposed: a lane holds 4 s of one t
-        if (wave < QT) {
-            const int j = wave, t = 16 * j + l15;
-            Parts<NP> cf[KT / 2], yf[PT / 2];
+        // tiles of E, transposed: a lane holds 4 s of one t
 #pragma unroll
-            for (int kk = 0; kk < KT / 2; ++kk)
+        for (int x = 0; x < NTILE; ++x) {
+            if (x >= tiles) continue;
+            const int j = tile_j(x), i = tile_i(x);
+            const int lane = renewed(threadIdx.x) % WAVE, l15 = lane & 15, q4 = lane >> 4;
+            const int t = 16 * j + l15, s0 = 16 * i + 4 * q4;
+            f32x4 e = zero4();
 #pragma unroll
-                for (int m = 0; m < NP; ++m) cf[kk].p[m] = row_natural(sc + m * PLK + t * LDK + 32 * kk, lane);
+            for (int pp = 0; pp < PT / 2; ++pp) {
+                Parts<NP> f, y;
 #pragma unroll
-            for (int pp = 0; pp < PT / 2; ++pp)
-#pragma unroll
-                for (int m = 0; m < NP; ++m) yf[pp].p[m] = row_natural(sdy + m * PLP + t * LDP + 32 * pp, lane);
+                for (int m = 0; m < NP; ++m) {
+                    f.p[m] = row_natural(sx + m * PLP + (16 * i + l15) * LDP + 32 * pp, lane);
+                    y.p[m] = row_natural(sdy + m * PLP + t * LDP + 32 * pp, lane);
+                }
+                e = mma_parts(f, y, e);
+            }
             const float hi = dec.hi[t], lo = dec.lo[t];
-            float row = 0.f;
+            const f32x4 shi = *reinterpret_cast<const f32x4*>(&dec.hi[s0]);
+            const f32x4 slo = *reinterpret_cast<const f32x4*>(&dec.lo[s0]);
+            const f32x4 src = *reinterpret_cast<const f32x4*>(&dec.src[s0]);
+            float row = 0.f, v[4];
 #pragma unroll
-            for (int i = 0; i < QT; ++i) {
-                f32x4 ds = zero4(), z = zero4();
-                if (i <= j) {
-                    f32x4 s = zero4(), e = zero4();
+            for (int r = 0; r < 4; ++r) {
+                const bool in = i < j || 4 * q4 + r <= l15;
+                const float le = in ? __builtin_amdgcn_exp2f((hi - shi[r]) + (lo - slo[r])) * e[r] : 0.f;
+                v[r] = le * src[r];
+                const float z = le * cb[x][r];
+                row += z * src[r];
+                if (i == j && 4 * q4 + r == l15) sum.xy[t] = e[r];
+                const float c = sum16(z);  // over the tile's 16 tokens t
+                if (l15 == 0) sum.col[wave][s0 + r] = c;
+            }
 #pragma unroll
-                    for (int kk = 0; kk < KT / 2; ++kk) {
-                        Parts<NP> f;
-#pragma unroll
-                        for (int m = 0; m < NP; ++m)
-                            f.p[m] = row_natural(sb + m * PLK + (16 * i + l15) * LDK + 32 * kk, lane);
-                        s = mma_parts(f, cf[kk], s);
-                    }
-#pragma unroll
-                    for (int pp = 0; pp < PT / 2; ++pp) {
-                        Parts<NP> f;
-#pragma unroll
-                        for (int m = 0; m < NP; ++m)
-                            f.p[m] = row_natural(sx + m * PLP + (16 * i + l15) * LDP + 32 * pp, lane);
-                        e = mma_parts(f, yf[pp], e);
-                    }
-                    const f32x4 shi = *reinterpret_cast<const f32x4*>(&dec.hi[16 * i + 4 * q4]);
-                    const f32x4 slo = *reinterpret_cast<const f32x4*>(&dec.lo[16 * i + 4 * q4]);
-                    const f32x4 src = *reinterpret_cast<const f32x4*>(&dec.src[16 * i + 4 * q4]);
-#pragma unroll
-                    for (int r = 0; r < 4; ++r) {
-                        const bool in = i < j || 4 * q4 + r <= l15;
-                        const float le = in ? __builtin_amdgcn_exp2f((hi - shi[r]) + (lo - slo[r])) * e[r] : 0.f;
-                        ds[r] = le * src[r];
-                        z[r] = le * s[r];
-                        row += z[r] * src[r];
-                        if (i == j && 4 * q4 + r == l15) sum.xy[t] = e[r];
-                    }
-                }
-                // sums over the tile's 16 tokens t; the next wavefronts' tiles add theirs
-#pragma unroll
-                for (int r = 0; r < 4; ++r) {
-                    const float c = sum16(z[r]);
-                    if (l15 == 0) sum.col[j][16 * i + 4 * q4 + r] = c;
-                }
-                if (i <= (j | 1)) {  // the tile above the diagonal that a product over 32 tokens meets is zero
-                    float v[4] = {ds[0], ds[1], ds[2], ds[3]};
-#pragma unroll
-                    for (int m = 0; m < MP; ++m) {
-                        bf16x4 b;
-#pragma unroll
-                        for (int r = 0; r < 4; ++r) {
-                            b[r] = (bf16)v[r];
-                            v[r] -= (float)b[r];
-                        }
-                        *reinterpret_cast<bf16x4*>(sds + m * PLQ + t * LDQ + 16 * i + 4 * q4) = b;
-                    }
+            for (int m = 0; m < MP; ++m) {
+                const uint32_t a0 = pack2(v[0], v[1]), a1 = pack2(v[2], v[3]);
+                *reinterpret_cast<uint2*>(sds + m * PLQ + t * LDQ + s0) = make_uint2(a0, a1);
+                if (m + 1 < MP) {
+                    v[0] -= low_of(a0);
+                    v[1] -= high_of(a0);
+                    v[2] -= low_of(a1);
+                    v[3] -= high_of(a1);
                 }
             }
             row += __shfl_xor(row, 16);
             row += __shfl_xor(row, 32);
-            if (q4 == 0) sum.row[t] = row;
+            // tiles of the same rows follow each other
+            if (q4 == 0) sum.row[wave][t] = x > 0 && tile_j(x) == tile_j(x - 1) ? sum.row[wave][t] + row : row;
         }
         __syncthreads();
 
@@ -1011,35 +1044,22 @@ __global__ void __launch_bounds__(NT, 2) ssm_grad_kernel(SsmArgs a, int slots, i
         if (lane == 0) sum.hg[wave] = hg;
         __syncthreads();
 
-        if (wave == 0) {
-            double rows = 0.0, cols_ = 0.0, outs = 0.0;
-            float dd = 0.f, xy = 0.f;
-            if (lane < n) {
-                float c = 0.f, u = 0.f, v = 0.f;
+        if (threadIdx.x < Q) {
+            const int t = threadIdx.x;
+            float row = 0.f, col = 0.f, ui = 0.f, vi = 0.f;
 #pragma unroll
-                for (int w = 0; w < WAVES; ++w) {
-                    if (w < QT) c += sum.col[w][lane];
-                    if (w * KW < KT) {
-                        u += sum.ui[w][lane];
-                        v += sum.vi[w][lane];
-                    }
-                }
-                const float d = dec.src[lane];
-                rows = (double)sum.row[lane] + u;
-                cols_ = (double)c * d;
-                outs = (double)v * d;
-                dd = c + v;
-                xy = sum.xy[lane];
+            for (int w = 0; w < WAVES; ++w) {
+                row += sum.row[w][t];
+                col += sum.col[w][t];
+                ui += sum.ui[w][t];
+                vi += sum.vi[w][t];
             }
-            const double through = (double)total * ((sum.hg[0] + sum.hg[1]) + (sum.hg[2] + sum.hg[3]));
-            const double net = lanes_scan(rows - cols_, lane), before = lanes_scan(outs, lane) - outs;
-            const double dl = __shfl(net, WAVE - 1) - net + (rows - cols_) + before + through;
-            if (lane < n) {
-                float* o = a.tok + ((int64_t)(c0 + lane) * all_units + unit) * 3;
-                o[0] = (float)dl;
-                o[1] = dd;
-                o[2] = xy;
-            }
+            float* o = a.tok + ((int64_t)at.slot * all_units + unit) * (5 * Q) + t;
+            o[0] = row + ui;
+            o[Q] = col;
+            o[2 * Q] = vi;
+            o[3 * Q] = sum.xy[t];
+            if (t == 0) o[4 * Q] = (sum.hg[0] + sum.hg[1]) + (sum.hg[2] + sum.hg[3]);
         }
     }
 
@@ -1082,45 +1102,58 @@ template <typename DT> __global__ void __launch_bounds__(NT) ssm_shares_kernel(S
     }
 }
 
-// ddt from the units' numbers, and partial sums of dA, dD and dbias over the workgroup's tokens: a lane is a
-// head, a wavefront every fourth token.
-__global__ void __launch_bounds__(NT) ssm_tokens_kernel(SsmArgs a, int tokens) {
+// A wavefront per chunk and head: the units' numbers put together, ddt, and the chunk's parts of dA, dD and dbias.
+template <typename DT>
+__global__ void __launch_bounds__(NT) ssm_tokens_kernel(SsmArgs a, int slots) {
+    constexpr int Q = Cfg<DT>::QT * 16;
+    const int lane = threadIdx.x % WAVE;
+    const int64_t i = (int64_t)blockIdx.x * WAVES + threadIdx.x / WAVE;
+    if (i >= (int64_t)slots * a.H) return;
+    const int slot = __builtin_amdgcn_readfirstlane((int)(i / a.H)), h = __builtin_amdgcn_readfirstlane((int)(i % a.H));
     const Seqs sq{a.cu, a.N, a.T, a.eq};
-    const int lane = threadIdx.x % WAVE, wave = threadIdx.x / WAVE;
-    const int64_t t0 = (int64_t)blockIdx.x * tokens, t1 = min(t0 + tokens, (int64_t)sq.end());
-    const int h = blockIdx.y * WAVE + lane;
-    __shared__ double part[WAVES][3][WAVE];
-    double dA = 0.0, dD = 0.0, db = 0.0;
-    if (h < a.H) {
-        const float A = a.A[h], bias = a.bias ? a.bias[h] : 0.f;
-        for (int64_t t = t0 + wave; t < t1; t += WAVES) {
-            const float* u = a.tok + (t * a.H + h) * a.blocks * 3;
-            double dl = 0.0, dd = 0.0, xy = 0.0;
-            for (int b = 0; b < a.blocks; ++b) {
-                dl += u[3 * b];
-                dd += u[3 * b + 1];
-                xy += u[3 * b + 2];
-            }
-            const float z = a.dt[t * a.dts + h] + bias;
-            const float d = a.softplus ? softplus_f(z) : z;
-            // the slope of softplus is the logistic function
-            const double s = a.softplus ? 1.0 / (1.0 + exp(-(double)z)) : 1.0;
-            const double dz = (dl * A + dd) * s;
-            a.ddt[t * a.H + h] = (float)dz;
-            dA += dl * d;
-            dD += xy;
-            db += dz;
+    const Piece pc = find_piece(sq, slot, Q);
+    float* sums = a.sums + (int64_t)slot * 3 * a.H + h;
+    if (!pc.live || pc.len == 0) {
+        if (lane < 3) sums[lane * a.H] = 0.f;
+        return;
+    }
+    const int c0 = pc.start + pc.n * Q, n = min(Q, pc.len - pc.n * Q);
+    const Decays<Q>& dec = reinterpret_cast<const Decays<Q>*>(a.dec)[i];
+    const float* tok = a.tok + i * a.blocks * (5 * Q);
+    double rows = 0.0, cols = 0.0, outs = 0.0, dd = 0.0, xy = 0.0, hg = 0.0, d = 0.0;
+    for (int b = 0; b < a.blocks; ++b) hg += tok[(int64_t)b * 5 * Q + 4 * Q];
+    if (lane < n) {
+        double c = 0.0, v = 0.0;
+        for (int b = 0; b < a.blocks; ++b) {
+            const float* u = tok + (int64_t)b * 5 * Q + lane;
+            rows += u[0];
+            c += u[Q];
+            v += u[2 * Q];
+            xy += u[3 * Q];
         }
+        d = dec.src[lane];
+        cols = c * d;
+        outs = v * d;
+        dd = c + v;
     }
-    part[wave][0][lane] = dA;
-    part[wave][1][lane] = dD;
-    part[wave][2][lane] = db;
-    __syncthreads();
-    if (wave < 3 && h < a.H) {
-        double s = 0.0;
-        for (int w = 0; w < WAVES; ++w) s += part[w][wave][lane];
-        a.sums[((int64_t)blockIdx.x * 3 + wave) * a.H + h] = (float)s;
+    const double through = (double)dec.total * hg;
+    const double net = lanes_scan(rows - cols, lane), before = lanes_scan(outs, lane) - outs;
+    const double dl = __shfl(net, WAVE - 1) - net + (rows - cols) + before + through;
+    double dz = 0.0;
+    if (lane < n) {
+        const float z = a.dt[(int64_t)(c0 + lane) * a.dts + h] + (a.bias ? a.bias[h] : 0.f);
+        // the slope of softplus is the logistic function
+        dz = (dl * a.A[h] + dd) * (a.softplus ? 1.0 / (1.0 + exp(-(double)z)) : 1.0);
+        a.ddt[(int64_t)(c0 + lane) * a.H + h] = (float)dz;
     }
+    double dA = lane < n ? dl * d : 0.0;
+#pragma unroll
+    for (int m = 1; m < WAVE; m <<= 1) {
+        dA += __shfl_xor(dA, m);
+        xy += __shfl_xor(xy, m);
+        dz += __shfl_xor(dz, m);
+    }
+    if (lane < 3) sums[lane * a.H] = (float)(lane == 0 ? dA : lane == 1 ? xy : dz);
 }
 
 // Last sums of dA, dD and dbias: a wavefront per value.
@@ -1239,7 +1272,7 @@ template <typename DT, int KT, int PT, int MODE> constexpr int walk_lds() {
 template <typename DT, int KT, int PT> constexpr int grad_lds() {
     constexpr int Q = Cfg<DT>::QT * 16, NP = Cfg<DT>::NP;
     return (2 * NP * Q * (KT * 16 + 8) + 2 * NP * Q * (PT * 16 + 8) + Cfg<DT>::MP * Q * (Q + 8)) * 2 +
-           (int)sizeof(Decays<Q>) + (Q * (2 + 3 * WAVES) + WAVES) * 4;
+           (int)sizeof(Decays<Q>) + (int)sizeof(GradSums<Q>);
 }
 
 template <typename F> hipError_t allow_lds(F* kernel, int bytes) {
@@ -1303,8 +1336,11 @@ template <typename DT, int KT, int PT> hipError_t backward(const SsmArgs& a, hip
         const Roles b{a.dy, a.C, a.B, a.dys, a.cs, a.bs, a.dhT, a.dh0, a.gs, 1};
         SSM_TRY((whole_walk<DT, KT, WT, OUT | EMIT>(a, b, st)));
     }
+    const int64_t slots = ssm_slots(a, a.chunk);
     if (a.T > 0) {
-        const int64_t slots = ssm_slots(a, a.chunk);
+        const dim3 each((unsigned)((slots * a.H + WAVES - 1) / WAVES));
+        hipLaunchKernelGGL(ssm_decay_kernel<DT>, each, dim3(NT), 0, st, a, (int)slots);
+        SSM_TRY(hipGetLastError());
         constexpr int lds = grad_lds<DT, KT, PT>();
         static_assert(lds <= 160 * 1024, "a chunk's tiles fit a compute unit");
         auto* kernel = ssm_grad_kernel<DT, KT, PT>;
@@ -1316,15 +1352,11 @@ template <typename DT, int KT, int PT> hipError_t backward(const SsmArgs& a, hip
             hipLaunchKernelGGL(ssm_shares_kernel<DT>, dim3((unsigned)(blocks < 4096 ? blocks : 4096)), dim3(NT), 0, st, a);
             SSM_TRY(hipGetLastError());
         }
-    }
-    const int tokens = (a.T + SSM_SUM_ROWS - 1) / SSM_SUM_ROWS < 16 ? 16 : (a.T + SSM_SUM_ROWS - 1) / SSM_SUM_ROWS;
-    const int rows = (a.T + tokens - 1) / tokens;
-    if (rows > 0) {
-        hipLaunchKernelGGL(ssm_tokens_kernel, dim3(rows, (a.H + WAVE - 1) / WAVE), dim3(NT), 0, st, a, tokens);
+        hipLaunchKernelGGL(ssm_tokens_kernel<DT>, each, dim3(NT), 0, st, a, (int)slots);
         SSM_TRY(hipGetLastError());
     }
     if (!a.dA && !a.dD && !a.dbias) return hipSuccess;
-    hipLaunchKernelGGL(ssm_sums_kernel, dim3((3 * a.H + WAVES - 1) / WAVES), dim3(NT), 0, st, a, rows);
+    hipLaunchKernelGGL(ssm_sums_kernel, dim3((3 * a.H + WAVES - 1) / WAVES), dim3(NT), 0, st, a, a.T > 0 ? (int)slots : 0);
     return hipGetLastError();
 }
 

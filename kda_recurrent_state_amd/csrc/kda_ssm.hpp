@@ -32,14 +32,15 @@ struct SsmArgs {
     float *ends, *decay;                         // a segment's own state at its end / the state it starts from; its decay
     float *hs, *gs;                              // states before every chunk, derivatives behind it
     float *part;                                 // partial dB, dC of the shares
-    float *tok;                                  // per token and unit: derivative of the log decay, of dt, x dy
-    float *sums;                                 // partial dA, dD, dbias
+    float *dec;                                  // decays of every chunk and head
+    float *tok;                                  // numbers of every chunk's tokens and unit
+    float *sums;                                 // every chunk's parts of dA, dD, dbias
 };
 
 inline int64_t ssm_units(const SsmArgs& a) { return (int64_t)a.H * a.blocks; }
 inline int64_t ssm_slots(const SsmArgs& a, int every) { return a.T / every + a.N; }
 inline int64_t ssm_unit_state(const SsmArgs& a) { return (int64_t)a.rows * a.cols; }  // of the gradient's units
-constexpr int SSM_SUM_ROWS = 256;
+inline int64_t ssm_decay_floats(const SsmArgs& a) { return 5ll * a.chunk + 16; }
 
 hipError_t launch_ssm_fwd(const SsmArgs& a, hipStream_t st);
 hipError_t launch_ssm_bwd(const SsmArgs& a, hipStream_t st);

@@ -90,8 +90,9 @@ size_t layout(kda::SsmArgs* a, int backward, uint8_t* base) {
         a->hs = take(slots * units * state);
         a->gs = take(slots * units * state);
         if (a->split > 1) a->part = take((int64_t)a->split * 2 * a->T * a->G * a->K);
-        a->tok = take((int64_t)a->T * units * 3);
-        a->sums = take((int64_t)kda::SSM_SUM_ROWS * 3 * a->H);
+        a->dec = take(slots * a->H * kda::ssm_decay_floats(*a));
+        a->tok = take(slots * units * 5 * a->chunk);
+        a->sums = take(slots * 3 * a->H);
     }
     return at;
 }
@@ -101,7 +102,8 @@ int check_size(const kda::SsmArgs& a, int backward) {
     const int64_t quads = ((int64_t)a.H / a.G * a.wblocks + kWaves - 1) / kWaves;
     const int64_t walk = (kda::ssm_slots(a, a.seg) * a.G + 8) * quads;
     const int64_t grad = backward ? (kda::ssm_slots(a, a.chunk) * a.G + 8) * a.split : 0;
-    if (walk > kMaxBlocks || grad > kMaxBlocks)
+    const int64_t waves = backward ? kda::ssm_slots(a, a.chunk) * a.H / 4 + 1 : 0;
+    if (walk > kMaxBlocks || grad > kMaxBlocks || waves > kMaxBlocks)
         return fail(KDA_ERR_INVALID_ARGUMENT, "num_seqs, total_tokens and heads = %d, %d and %d are too large for one launch",
                     a.N, a.T, a.H);
     return KDA_OK;
