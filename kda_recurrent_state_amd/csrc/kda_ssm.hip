@@ -234,15 +234,19 @@ __device__ __forceinline__ void decays(Decays<Q>& w, const SsmArgs& a, int h, in
     }
 }
 
-// Sum over the 16 lanes of a group by rotations inside the group: no trip through LDS.
-__device__ __forceinline__ float sum16(float x) {
-    auto turned = [](float v, auto ctrl) {
-        return __builtin_bit_cast(float, __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, v), decltype(ctrl)::value, 15, 15, true));
-    };
-    x += turned(x, Int<0x128>());
-    x += turned(x, Int<0x124>());
-    x += turned(x, Int<0x122>());
-    return x + turned(x, Int<0x121>());
+// Sums of four values over the 16 lanes of a group, the n-th in every lane with lane % 4 == n: neighbours
+// exchange what they give up, so that 5 additions do what 16 would.  No trip through LDS.
+template <int CTRL> __device__ __forceinline__ float lane_of(float v) {
+    const int i = __builtin_bit_cast(int, v);
+    return __builtin_bit_cast(float, __builtin_amdgcn_update_dpp(i, i, CTRL, 15, 15, false));
+}
+__device__ __forceinline__ float sums16(f32x4 v, int lane) {
+    const bool odd = lane & 1, high = lane & 2;
+    const float a = (odd ? v[1] : v[0]) + lane_of<0xb1>(odd ? v[0] : v[1]);
+    const float b = (odd ? v[3] : v[2]) + lane_of<0xb1>(odd ? v[2] : v[3]);
+    float s = (high ? b : a) + lane_of<0x4e>(high ? a : b);
+    s += lane_of<0x124>(s);
+    return s + lane_of<0x128>(s);
 }
 
 // The n-th piece of `every` tokens of each sequence has the slot start / every + sequence + n: slots
@@ -924,6 +928,7 @@ __global__ void __launch_bounds__(NT, 2) ssm_grad_kernel(SsmArgs a, int slots, i
             const f32x4 slo = *reinterpret_cast<const f32x4*>(&dec.lo[s0]);
             const f32x4 src = *reinterpret_cast<const f32x4*>(&dec.src[s0]);
             float row = 0.f, v[4];
+            f32x4 zs;
 #pragma unroll
             for (int r = 0; r < 4; ++r) {
                 const bool in = i < j || 4 * q4 + r <= l15;
@@ -932,9 +937,10 @@ __global__ void __launch_bounds__(NT, 2) ssm_grad_kernel(SsmArgs a, int slots, i
                 const float z = le * cb[x][r];
                 row += z * src[r];
                 if (i == j && 4 * q4 + r == l15) sum.xy[t] = e[r];
-                const float c = sum16(z);  // over the tile's 16 tokens t
-                if (l15 == 0) sum.col[wave][s0 + r] = c;
+                zs[r] = z;
             }
+            const float c = sums16(zs, lane);  // over the tile's 16 tokens t
+            if (l15 < 4) sum.col[wave][s0 + l15] = c;
 #pragma unroll
             for (int m = 0; m < MP; ++m) {
                 const uint32_t a0 = pack2(v[0], v[1]), a1 = pack2(v[2], v[3]);
@@ -969,49 +975,60 @@ __global__ void __launch_bounds__(NT, 2) ssm_grad_kernel(SsmArgs a, int slots, i
 #pragma unroll
                     for (int r = 0; r < 8; ++r) hg += hx[r] * gx[r];
                     hf[pp] = split8<3>(hx);
+                }
+                // sums over the wavefront's columns go to its own row: lane n of 4 holds row n's
+                auto add = [&](float (&to)[Q], int t, f32x4 v) {
+                    const float u = sums16(v, lane);
+                    if (l15 < 4) to[t + l15] = k ? to[t + l15] + u : u;
+                };
+#pragma unroll
+                for (int j = 0; j < QT; ++j) {
+                    const int t = 16 * j + 4 * q4;
+                    f32x4 tc = zero4(), cv = zero4();
+#pragma unroll
+                    for (int pp = 0; pp < PT / 2; ++pp) {
+                        Parts<NP> f;
+#pragma unroll
+                        for (int m = 0; m < NP; ++m) f.p[m] = row_natural(sdy + m * PLP + (16 * j + l15) * LDP + 32 * pp, lane);
+                        tc = mma_parts(f, hf[pp], tc);
+                    }
+                    tc *= *reinterpret_cast<const f32x4*>(&dec.from[t]);
+                    dC[j][k] += tc;
+#pragma unroll
+                    for (int m = NP - 1; m >= 0; --m) {
+                        const bf16x4 c = tr4(sc + m * PLK + 16 * kt, LDK, t, lane);
+#pragma unroll
+                        for (int r = 0; r < 4; ++r) cv[r] = m + 1 < NP ? cv[r] + (float)c[r] : (float)c[r];
+                    }
+                    add(sum.ui[wave], t, cv * tc);
+                }
+#pragma unroll
+                for (int pp = 0; pp < PT / 2; ++pp) {
+                    float gx[8];
+                    get_v(gv[pp], gx);
                     gf[pp] = split8<3>(gx);
                 }
                 if (k + 1 < KW) states(k + 1);
 #pragma unroll
                 for (int j = 0; j < QT; ++j) {
-                    f32x4 tc = zero4(), tb = zero4();
+                    const int t = 16 * j + 4 * q4;
+                    f32x4 tb = zero4(), bv = zero4();
 #pragma unroll
                     for (int pp = 0; pp < PT / 2; ++pp) {
-                        Parts<NP> f, x;
+                        Parts<NP> x;
 #pragma unroll
-                        for (int m = 0; m < NP; ++m) {
-                            f.p[m] = row_natural(sdy + m * PLP + (16 * j + l15) * LDP + 32 * pp, lane);
-                            x.p[m] = row_natural(sx + m * PLP + (16 * j + l15) * LDP + 32 * pp, lane);
-                        }
-                        tc = mma_parts(f, hf[pp], tc);
+                        for (int m = 0; m < NP; ++m) x.p[m] = row_natural(sx + m * PLP + (16 * j + l15) * LDP + 32 * pp, lane);
                         tb = mma_parts(x, gf[pp], tb);
                     }
-                    const int t = 16 * j + 4 * q4;
-                    const f32x4 from = *reinterpret_cast<const f32x4*>(&dec.from[t]);
-                    const f32x4 to = *reinterpret_cast<const f32x4*>(&dec.to[t]);
-                    const f32x4 src = *reinterpret_cast<const f32x4*>(&dec.src[t]);
-                    f32x4 cv = zero4(), bv = zero4();
+                    tb *= *reinterpret_cast<const f32x4*>(&dec.to[t]);
+                    dB[j][k] += tb * *reinterpret_cast<const f32x4*>(&dec.src[t]);
 #pragma unroll
                     for (int m = NP - 1; m >= 0; --m) {
-                        const bf16x4 c = tr4(sc + m * PLK + 16 * kt, LDK, t, lane), b = tr4(sb + m * PLK + 16 * kt, LDK, t, lane);
+                        const bf16x4 b = tr4(sb + m * PLK + 16 * kt, LDK, t, lane);
 #pragma unroll
-                        for (int r = 0; r < 4; ++r) {
-                            cv[r] = m + 1 < NP ? cv[r] + (float)c[r] : (float)c[r];
-                            bv[r] = m + 1 < NP ? bv[r] + (float)b[r] : (float)b[r];
-                        }
+                        for (int r = 0; r < 4; ++r) bv[r] = m + 1 < NP ? bv[r] + (float)b[r] : (float)b[r];
                     }
-#pragma unroll
-                    for (int r = 0; r < 4; ++r) {
-                        const float c = tc[r] * from[r], b = tb[r] * to[r];
-                        dC[j][k][r] += c;
-                        dB[j][k][r] += b * src[r];
-                        // the wavefront's columns so far, in its own row
-                        const float u = sum16(cv[r] * c), v = sum16(bv[r] * b);
-                        if (l15 == 0) {
-                            sum.ui[wave][t + r] = k ? sum.ui[wave][t + r] + u : u;
-                            sum.vi[wave][t + r] = k ? sum.vi[wave][t + r] + v : v;
-                        }
-                    }
+                    add(sum.vi[wave], t, bv * tb);
                 }
 #pragma unroll
                 for (int i2 = 0; i2 < QT / 2; ++i2) {
