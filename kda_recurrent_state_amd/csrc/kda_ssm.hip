@@ -191,6 +191,29 @@ template <typename DT, int ROWS, int COLS, int THREADS> struct Stage {
             }
         }
     }
+    // the same into rows in the paired order
+    template <typename TILE> __device__ __forceinline__ void store_paired(char* dst, int plane, unsigned tid) const {
+#pragma unroll
+        for (int i = 0; i < CNT; ++i) {
+            const unsigned at = i * THREADS + tid;
+            if (ALL % THREADS != 0 && at >= ALL) continue;
+            const int r = at / PER, p = at % PER;
+            Parts<NP> s;
+            if constexpr (NP == 1) {
+                s.p[0] = __builtin_bit_cast(bf16x8, v[i]);
+            } else {
+                float f[8];
+                get_v(v[i], f);
+                s = split8<NP>(f);
+            }
+#pragma unroll
+            for (int n = 0; n < NP; ++n) {
+                char* to = dst + n * plane + TILE::half(p) * 8;
+                *reinterpret_cast<bf16x4*>(to + TILE::at(r, TILE::place(p))) = __builtin_shufflevector(s.p[n], s.p[n], 0, 1, 2, 3);
+                *reinterpret_cast<bf16x4*>(to + TILE::at(r, TILE::place(p) + 1)) = __builtin_shufflevector(s.p[n], s.p[n], 4, 5, 6, 7);
+            }
+        }
+    }
     static __device__ __forceinline__ void clear(Pack<DT, 8>& p) {
 #pragma unroll
         for (int k = 0; k < 8; ++k) p.part[k / Pack<DT, 8>::N][k % Pack<DT, 8>::N] = from_f32<DT>(0.f);
@@ -316,6 +339,13 @@ template <int COLS> struct Tile {
         return join(*reinterpret_cast<const bf16x4*>(m + at(row, 4 * k32 + (q >> 1)) + (q & 1) * 8),
                     *reinterpret_cast<const bf16x4*>(m + at(row, 4 * k32 + 2 + (q >> 1)) + (q & 1) * 8));
     }
+    // the same of a row that is stored in the paired order: piece p's two halves go to half(p) of pieces place(p) and
+    // place(p) + 1
+    static __device__ __forceinline__ int place(int p) { return (p & ~3) + 2 * (p & 1); }
+    static __device__ __forceinline__ int half(int p) { return (p >> 1) & 1; }
+    static __device__ __forceinline__ bf16x8 row_stored(const char* m, int row, int k32, int lane) {
+        return *reinterpret_cast<const bf16x8*>(m + at(row, 4 * k32 + (lane >> 4)));
+    }
     // 32 rows as contraction indices of 16 columns in the paired order
     static __device__ __forceinline__ bf16x8 col_paired(const char* m, int c16, int lane) {
         typedef __attribute__((address_space(3))) s16x4* lds;
@@ -334,16 +364,17 @@ struct WalkDecays {
     float from[WALK], into[WALK], scale[WALK], c[WALK], less[WALK];
     // from: 2^{c}; into: 2^{total - c} src; scale: weight of a token's result (1, reversed d); less: c - log2(src),
     // src the weight of its product (d, reversed 1)
-    float total, pad[3];  // 2^{total}
+    float total, pad[3];  // 2^{total} (BEHIND: the log decay of the chunks behind this one)
 };
 struct ExactDecays {  // fp32 only: c as hi + lo
     float hi[WALK], lo[WALK], src[WALK];
 };
 
 // Two chunks at once, 32 tokens each, a token a lane; returns the sum of both chunks' log decays.
-template <bool EXACT>
+// BEHIND: `into` is the weight at the end of the segment, `behind` the log decay of the chunks behind these.
+template <bool EXACT, bool BEHIND>
 __device__ __forceinline__ double walk_decays(WalkDecays& w, ExactDecays* x, float z, float A, int softplus, bool in,
-                                              bool rev, int lane) {
+                                              bool rev, double behind, int lane) {
     const int u = lane & (WALK - 1);
     const float d = in ? (softplus ? softplus_f(z) : z) : 0.f;
     const double l = in ? fmax((double)d * (double)A * 1.4426950408889634, -300.0) : 0.0;
@@ -355,6 +386,13 @@ __device__ __forceinline__ double walk_decays(WalkDecays& w, ExactDecays* x, flo
     }
     const double c = rev ? incl - l : incl, total = __shfl(incl, WALK - 1, WALK);
     const float src = in ? (rev ? 1.f : d) : 0.f;
+    if (BEHIND) {
+        const double other = __shfl(total, 0);
+        behind += lane >= WALK ? other : 0.0;
+        w.into[u] = exp2f((float)(behind + (total - c))) * src;
+        if (u == 0) w.total = (float)behind;
+        return total + __shfl_xor(total, WALK);
+    }
     w.from[u] = exp2f((float)c);
     w.into[u] = exp2f((float)(total - c)) * src;
     w.scale[u] = rev ? d : 1.f;
@@ -413,6 +451,13 @@ ssm_walk_kernel(SsmArgs a, const DT* val, const DT* key, const DT* query, int64_
     const int team = mine ? min(min(lead + a.wblocks - (block - who), WAVES), units - at.quad * WAVES) - lead : 1;
     const bool decides = mine && who == team - 1;  // forms the head's decays
     const int share = team == 1 ? 7 : team == 2 ? (who ? 2 : 5) : who < 3 ? 1 << who : 0;  // of the masked products' tiles
+    // the leads of the workgroup's heads
+    int leads = 0;
+#pragma unroll
+    for (int o = 0; o < WAVES; ++o) {
+        const int u = at.quad * WAVES + o;
+        if (u < units && (o == 0 || u % a.wblocks == 0)) leads |= 1 << o;
+    }
     const int segs = max((pc.len + a.seg - 1) / a.seg, 1);
     const bool is_last = pc.n == (rev ? 0 : segs - 1), is_first = pc.n == (rev ? segs - 1 : 0);
     if ((MODE & ENDS) && is_last) return;
@@ -455,11 +500,13 @@ ssm_walk_kernel(SsmArgs a, const DT* val, const DT* key, const DT* query, int64_
     const float A = a.A[h], bias = a.bias ? a.bias[h] : 0.f;
     double log_decay = 0.0;
 
-    // chunk ci in the order of the walk: its first token in that order, and how many it has
+    // Chunk ci in the order of the walk: its first token in that order, and how many it has.  What a segment adds is
+    // the sum of its tokens' products, each with the decay from there to the segment's end, so ENDS takes the chunks
+    // from the end: weights come whole and the state is never scaled.
     struct Chunk { int index, t0, first, n; };
     auto chunk_at = [&](int ci) {
         Chunk c;
-        c.index = rev ? chunks - 1 - ci : ci;
+        c.index = (rev != 0) != ((MODE & ENDS) != 0) ? chunks - 1 - ci : ci;
         c.t0 = pc.start + t0 + c.index * Q;
         c.n = min(Q, pc.start + t1 - c.t0);
         c.first = rev ? c.t0 + c.n - 1 : c.t0;
@@ -476,7 +523,7 @@ ssm_walk_kernel(SsmArgs a, const DT* val, const DT* key, const DT* query, int64_
         const Chunk c = chunk_at(ci + (lane >> 5));
         const bool in = ci + (lane >> 5) < chunks && (lane & 31) < c.n;
         const int to = (ci & 2) + (lane >> 5);
-        log_decay += walk_decays<NP != 1>(dec[to], &exact[to], raw + bias, A, a.softplus, in, rev, lane);
+        log_decay += walk_decays<NP != 1, (MODE & ENDS) != 0>(dec[to], &exact[to], raw + bias, A, a.softplus, in, rev, log_decay, lane);
     };
 
     Stage<DT, Q, KT * 16, NT> bk, bq;
@@ -490,7 +537,7 @@ ssm_walk_kernel(SsmArgs a, const DT* val, const DT* key, const DT* query, int64_
     auto store = [&]() {
         const unsigned tid = renewed(threadIdx.x);
         bk.store_to(skey, PLK, tid, [](int r, int p) { return TK::at(r, p); });
-        if (MODE & OUT) bq.store_to(squery, PLK, tid, [](int r, int p) { return TK::at(r, p); });
+        if (MODE & OUT) bq.template store_paired<TK>(squery, PLK, tid);
         bv.store_to(sval, PLP, tid % WAVE, [](int r, int p) { return TP::at(r, p); });
     };
     float raw = 0.f;
@@ -504,7 +551,7 @@ ssm_walk_kernel(SsmArgs a, const DT* val, const DT* key, const DT* query, int64_
 
     for (int ci = 0; ci < chunks; ++ci) {
         const Chunk c = chunk_at(ci);
-        const int first = c.first, n = c.n;
+        const int n = c.n;
         if (!AHEAD) load(c);
         if (ci) lds_barrier();  // the last chunk's tiles are read
         store();
@@ -512,6 +559,15 @@ ssm_walk_kernel(SsmArgs a, const DT* val, const DT* key, const DT* query, int64_
         if (AHEAD && ci + 1 < chunks) load(chunk_at(ci + 1));
         if (decides && !(ci & 1)) raw = steps_of(ci + 2);
         const WalkDecays& w = dec[ci & 3];
+        if (MODE & ENDS) {
+            // Past 2^-150 every weight of this chunk and of those before it is zero in fp32: the sum is done, for
+            // the workgroup where it is for each of its heads.
+            float most = -INFINITY;
+#pragma unroll
+            for (int o = 0; o < WAVES; ++o)
+                if (leads & 1 << o) most = fmaxf(most, sdec[4 * o + (ci & 3)].total);
+            if (most < -152.f) break;
+        }
 
         if ((MODE & EMIT) && mine) {
             const int ev = a.chunk / Q;
@@ -545,7 +601,7 @@ ssm_walk_kernel(SsmArgs a, const DT* val, const DT* key, const DT* query, int64_
                         Parts<NP> qf, kf;
 #pragma unroll
                         for (int m = 0; m < NP; ++m) {
-                            qf.p[m] = TK::row_paired(squery + m * PLK, t, kk, lane);
+                            qf.p[m] = TK::row_stored(squery + m * PLK, t, kk, lane);
                             kf.p[m] = TK::row_paired(skey + m * PLK, 16 * I[x] + l15, kk, lane);
                         }
                         s = mma_parts(kf, qf, s);
@@ -588,7 +644,7 @@ ssm_walk_kernel(SsmArgs a, const DT* val, const DT* key, const DT* query, int64_
 #pragma unroll
                     for (int j = 0; j < 2; ++j)
 #pragma unroll
-                        for (int m = 0; m < NP; ++m) qf[j].p[m] = TK::row_paired(squery + m * PLK, 16 * j + l15, kk, lane);
+                        for (int m = 0; m < NP; ++m) qf[j].p[m] = TK::row_stored(squery + m * PLK, 16 * j + l15, kk, lane);
 #pragma unroll
                     for (int p = 0; p < PT; ++p) {
                         float v[8];
@@ -613,6 +669,9 @@ ssm_walk_kernel(SsmArgs a, const DT* val, const DT* key, const DT* query, int64_
                 for (int m = 0; m < NP; ++m) vf[p].p[m] = TP::col_paired(sval + m * PLP, p, lane);
             if constexpr ((MODE & OUT) != 0) {
                 const int lane = renewed(threadIdx.x) % WAVE, l15 = lane & 15, q4 = lane >> 4;
+                const int token = a.H * a.P;
+                DT* const out = reinterpret_cast<DT*>(a.y) + ((int64_t)c.t0 * a.H + h) * a.P + p0;
+                const bool whole = n == Q && p0 + PT * 16 <= a.P && token < 1 << 22;  // no conditions by lane
 #pragma unroll
                 for (int j = 0; j < 2; ++j) {
                     const int t = 16 * j + l15;
@@ -621,10 +680,11 @@ ssm_walk_kernel(SsmArgs a, const DT* val, const DT* key, const DT* query, int64_
 #pragma unroll
                     for (int m = 0; m < MP; ++m)
                         mf.p[m] = *reinterpret_cast<const bf16x8*>(sm + m * PLM + t * (Q * 2) + ((q4 ^ ((t >> 1) & 3)) * 16));
-                    DT* out = reinterpret_cast<DT*>(a.y) + ((int64_t)first * a.H + h) * a.P + p0 + (int64_t)t * dir * a.H * a.P;
+                    const unsigned row = rev ? n - 1 - t : t;
 #pragma unroll
                     for (int p = 0; p < PT; ++p) {
                         acc[j][p] = mma_parts(vf[p], mf, acc[j][p] * from);
+                        if (rev) acc[j][p] *= scale;
                         const int col = 16 * p + 4 * q4;
                         float o[4];
                         zero_v(o);
@@ -636,14 +696,17 @@ ssm_walk_kernel(SsmArgs a, const DT* val, const DT* key, const DT* query, int64_
                             for (int r = 0; r < 4; ++r) o[r] = m + 1 < NP ? o[r] + f[r] : f[r];
                         }
 #pragma unroll
-                        for (int r = 0; r < 4; ++r) o[r] = scale * acc[j][p][r] + dskip * o[r];
-                        if (t < n) {
+                        for (int r = 0; r < 4; ++r) o[r] = acc[j][p][r] + dskip * o[r];
+                        if (whole) {
+                            store_v<4>(reinterpret_cast<DT*>(reinterpret_cast<char*>(out) + (__umul24(row, (unsigned)token) + col) * (unsigned)sizeof(DT)), o);
+                        } else if (t < n) {
+                            DT* to = out + (int64_t)row * token + col;
                             if (p0 + col + 4 <= a.P) {
-                                store_v<4>(out + col, o);
+                                store_v<4>(to, o);
                             } else {
 #pragma unroll
                                 for (int r = 0; r < 4; ++r)
-                                    if (p0 + col + r < a.P) out[col + r] = from_f32<DT>(o[r]);
+                                    if (p0 + col + r < a.P) to[r] = from_f32<DT>(o[r]);
                             }
                         }
                     }
@@ -677,7 +740,8 @@ ssm_walk_kernel(SsmArgs a, const DT* val, const DT* key, const DT* query, int64_
 #pragma unroll
                 for (int i = 0; i < 2; ++i)
 #pragma unroll
-                    for (int p = 0; p < PT; ++p) st[k + i][p] *= total;
+                    for (int p = 0; p < PT; ++p)
+                        if (!(MODE & ENDS)) st[k + i][p] *= total;
 #pragma unroll
                 for (int m = 0; m < NP; ++m)
 #pragma unroll
