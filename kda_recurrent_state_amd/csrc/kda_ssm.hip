@@ -149,9 +149,13 @@ template <typename DT, int ROWS, int COLS, int THREADS> struct Stage {
                 const DT* p = src + (int64_t)(rev ? t0 + n - 1 - r : t0 + r) * stride + c;
                 if (c + 8 <= cols) {
                     v[i] = load_v<8>(p);
-                } else {
+                } else {  // one by one, and none waits for another: elements past the row are its last, then zero
+                    DT e[8];
+#pragma unroll
+                    for (int k = 0; k < 8; ++k) e[k] = p[min(k, cols - 1 - c)];
+#pragma unroll
                     for (int k = 0; k < 8; ++k)
-                        if (c + k < cols) v[i].part[k / Pack<DT, 8>::N][k % Pack<DT, 8>::N] = p[k];
+                        v[i].part[k / Pack<DT, 8>::N][k % Pack<DT, 8>::N] = c + k < cols ? e[k] : from_f32<DT>(0.f);
                 }
             }
         }
@@ -413,7 +417,7 @@ __device__ __forceinline__ double walk_decays(WalkDecays& w, ExactDecays* x, flo
 // writes the segment's own state and decay (not for a sequence's last segment).
 //
 // A unit is narrow, 64 registers of state, so that three wavefronts share a SIMD: with twice the columns two did,
-// and waited for LDS most of their time (2 x 32768 tokens of 32 heads: 560 us against NEW_US).  The wavefronts of a
+// and waited for LDS and each other (with two of this size on a SIMD 764 us against 589, 2 x 32768 tokens of 32 heads).  The wavefronts of a
 // workgroup that have the same head form the masked products once between them, in LDS.  Chunks of 32 tokens;
 // with bf16 inputs the next chunk's rows are on their way in registers while one is multiplied.
 template <typename DT, int KT, int PT, int MODE>

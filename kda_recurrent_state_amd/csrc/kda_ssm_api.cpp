@@ -60,7 +60,9 @@ int plan(const kda_ssm_dims_t* d, kda::SsmArgs* a) {
     a->blocks = (a->P + a->cols - 1) / a->cols;
     a->wcols = a->cols / 2;
     a->wblocks = (a->P + a->wcols - 1) / a->wcols;
-    // Segments: enough workgroups for three on every compute unit.
+    // Segments: enough workgroups for three on every compute unit, all that fit, so that they run in one round.  Measured
+    // with workgroups for 512, 768, 1024 and 1536, us: 2 x 32768 tokens of 32 heads 920, 786, 897, 823; gradient of
+    // 2 x 8192 1049, 999, 1079, 1060; 16384 tokens of 32 heads of 64 119, 115, 111, 127; one of 4096 65 each.
     const int64_t quads = ((int64_t)a->H / a->G * a->wblocks + kWaves - 1) / kWaves;
     const int64_t want = kWalkGroups / (quads * a->G) > 0 ? kWalkGroups / (quads * a->G) : 1;
     const int64_t seg = round_up((a->T + want - 1) / want, a->chunk);
