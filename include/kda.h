@@ -618,8 +618,8 @@ KDA_API int kda_residual_norm_bwd_workspace_size(const kda_residual_norm_dims_t*
  *   - A is <= 0 and d >= 0 (not checked); any decay is exact to rounding.
  *   - bf16 inputs are multiplied exactly and summed in fp32; fp32 inputs as sums
  *     of three bf16 parts, to 2^-24 of a product.
- *   - Inputs are finite.  A non-finite value stays in its own sequence; it may reach
- *     outputs up to 63 tokens before it.
+ *   - Inputs are finite.  A non-finite value stays in its own sequence.  It may reach outputs up to
+ *     63 tokens before it, and be lost behind decays whose product is zero in float32.
  * ------------------------------------------------------------------------- */
 typedef struct {
     int32_t num_seqs;      /* N */
@@ -643,8 +643,8 @@ typedef struct {
  *   h_T        [N, H, K, P] float32 final states, or NULL to skip (an empty sequence's is its h0); not h0
  *   workspace  kda_ssm_workspace_size bytes (0: may be NULL).  Calls that share a workspace
  *              must be ordered on one stream.
- * Refused, as larger than one launch: more than 2^24 workgroups, which takes more than ten
- * million sequences or chunks of tokens.
+ * Refused, as larger than one launch: more than 2^24 workgroups, which takes millions of
+ * sequences or chunks of tokens.
  */
 KDA_API int kda_ssm_fwd(const kda_ssm_dims_t* dims, const void* x, const float* dt, const float* A, const void* B,
                         const void* C, const float* D, const float* dt_bias, const float* h0,
@@ -701,7 +701,7 @@ KDA_API int kda_ssm_conv_step_workspace_size(const kda_ssm_dims_t* dims, size_t*
 typedef enum { KDA_CACHE_I8 = 0, KDA_CACHE_E4M3 = 1 } kda_cache_format_t;
 
 typedef struct {
-    int32_t states;    /* R: states of the call, up to 8388607 */
+    int32_t states;    /* R: states of the call, up to 2^20; states or slots x rows x width up to 2^60 */
     int32_t slots;     /* S: slots of the cache */
     int64_t rows;      /* rows of a state (for [H, K, P]: H K), up to 2^40 */
     int32_t width;     /* values of a row: 1 to 8192 */

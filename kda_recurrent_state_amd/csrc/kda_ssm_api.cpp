@@ -3,6 +3,7 @@
 // here allocates device memory or keeps state.
 #include <hip/hip_runtime.h>
 
+#include <math.h>
 #include <stdint.h>
 
 #include "../../include/kda.h"
@@ -77,11 +78,11 @@ int plan(const kda_ssm_dims_t* d, kda::SsmArgs* a) {
 size_t layout(kda::SsmArgs* a, int backward, uint8_t* base) {
     size_t at = 0;
     auto take = [&](int64_t floats) {
-        float* p = reinterpret_cast<float*>(base + at);
+        float* p = base ? reinterpret_cast<float*>(base + at) : nullptr;
         at += round256((size_t)floats * 4);
         return p;
     };
-    const int64_t state = kda::ssm_unit_state(*a), units = kda::ssm_units(*a);
+    const int64_t units = kda::ssm_units(*a);
     if (a->seg < a->T) {
         const int64_t slots = kda::ssm_slots(*a, a->seg);
         a->ends = take(slots * a->H * a->wblocks * a->rows * a->wcols);
@@ -89,8 +90,8 @@ size_t layout(kda::SsmArgs* a, int backward, uint8_t* base) {
     }
     if (backward) {
         const int64_t slots = kda::ssm_slots(*a, a->chunk);
-        a->hs = take(slots * units * state);
-        a->gs = take(slots * units * state);
+        a->hs = take(slots * units * kda::ssm_unit_state(*a));
+        a->gs = take(slots * units * kda::ssm_unit_state(*a));
         if (a->split > 1) a->part = take((int64_t)a->split * 2 * a->T * a->G * a->K);
         a->dec = take(slots * a->H * kda::ssm_decay_floats(*a));
         a->tok = take(slots * units * 5 * a->chunk);
@@ -99,13 +100,14 @@ size_t layout(kda::SsmArgs* a, int backward, uint8_t* base) {
     return at;
 }
 
-// One launch holds 2^32 threads.
+// A launch holds 2^32 threads, and the states of a gradient's chunks less than 2^60 bytes.  In double, which holds every
+// product of the sizes' limits.
 int check_size(const kda::SsmArgs& a, int backward) {
-    const int64_t quads = ((int64_t)a.H / a.G * a.wblocks + kWaves - 1) / kWaves;
-    const int64_t walk = (kda::ssm_slots(a, a.seg) * a.G + 8) * quads;
-    const int64_t grad = backward ? (kda::ssm_slots(a, a.chunk) * a.G + 8) * a.split : 0;
-    const int64_t waves = backward ? kda::ssm_slots(a, a.chunk) * a.H / 4 + 1 : 0;
-    if (walk > kMaxBlocks || grad > kMaxBlocks || waves > kMaxBlocks)
+    const double quads = ((int64_t)a.H / a.G * a.wblocks + kWaves - 1) / kWaves, chunks = kda::ssm_slots(a, a.chunk);
+    const double walk = ((double)kda::ssm_slots(a, a.seg) * a.G + 8) * quads;
+    const double grad = backward ? fmax((chunks * a.G + 8) * a.split, chunks * a.H / 4 + 1) : 0;
+    const double states = backward ? chunks * a.H * a.blocks * a.rows * a.cols * 8 : 0;
+    if (walk > kMaxBlocks || grad > kMaxBlocks || states > 1e18)
         return fail(KDA_ERR_INVALID_ARGUMENT, "num_seqs, total_tokens and heads = %d, %d and %d are too large for one launch",
                     a.N, a.T, a.H);
     return KDA_OK;
@@ -131,6 +133,7 @@ int kda_ssm_workspace_size(const kda_ssm_dims_t* d, int backward, size_t* bytes)
     if (!bytes) return fail(KDA_ERR_INVALID_ARGUMENT, "bytes is NULL");
     kda::SsmArgs a;
     KDA_TRY(plan(d, &a));
+    KDA_TRY(check_size(a, backward));
     *bytes = layout(&a, backward, nullptr);
     return ok();
 }

@@ -12,17 +12,23 @@ using namespace kda::checks;
 
 namespace {
 
+// A write looks through the slots of the states behind each of its own: 2^20 states look at 2^39 slots.
+constexpr int kMaxStates = 1 << 20;
+
 int check(const kda_state_cache_dims_t* d, const void* values, const char* name, const void* codes, const float* scales,
           const int32_t* slots, kda::StateCacheArgs* a) {
     if (!d) return fail(KDA_ERR_INVALID_ARGUMENT, "dims is NULL");
     if (d->states < 0) return fail(KDA_ERR_INVALID_ARGUMENT, "states = %d < 0", d->states);
-    if (d->states > 0x7fffff) return fail(KDA_ERR_INVALID_ARGUMENT, "states = %d: at most %d", d->states, 0x7fffff);
+    if (d->states > kMaxStates) return fail(KDA_ERR_INVALID_ARGUMENT, "states = %d: at most %d", d->states, kMaxStates);
     if (d->slots < 0) return fail(KDA_ERR_INVALID_ARGUMENT, "slots = %d < 0", d->slots);
     if (d->rows < 0 || d->rows > (int64_t)1 << 40)
         return fail(KDA_ERR_INVALID_ARGUMENT, "rows = %lld: must be 0 to 2^40", (long long)d->rows);
     if (d->width < 1) return fail(KDA_ERR_INVALID_ARGUMENT, "width = %d < 1", d->width);
     if (d->width > kda::STATE_CACHE_MAX_WIDTH)
         return fail(KDA_ERR_UNSUPPORTED, "width = %d: at most %d", d->width, kda::STATE_CACHE_MAX_WIDTH);
+    if ((double)d->rows * d->width * (d->states > d->slots ? d->states : d->slots) > 0x1p60)
+        return fail(KDA_ERR_INVALID_ARGUMENT, "states, slots, rows and width = %d, %d, %lld and %d are too large", d->states,
+                    d->slots, (long long)d->rows, d->width);
     if (d->format != KDA_CACHE_I8 && d->format != KDA_CACHE_E4M3)
         return fail(KDA_ERR_INVALID_ARGUMENT, "format = %d is not KDA_CACHE_I8 or KDA_CACHE_E4M3", d->format);
     if (d->reserved != 0) return fail(KDA_ERR_INVALID_ARGUMENT, "reserved = %d is not 0", d->reserved);
