@@ -375,10 +375,11 @@ struct ExactDecays {  // fp32 only: c as hi + lo
 };
 
 // Two chunks at once, 32 tokens each, a token a lane; returns the sum of both chunks' log decays.
-// BEHIND: `into` is the weight at the end of the segment, `behind` the log decay of the chunks behind these.
+// BEHIND: `into` is the weight at the end of the segment, `behind` the log decay of the chunks behind these; `sign` is the
+// sign of the sum it goes to.  Otherwise the state changes its sign with every chunk, and is negative before odd ones.
 template <bool EXACT, bool BEHIND>
 __device__ __forceinline__ double walk_decays(WalkDecays& w, ExactDecays* x, float z, float A, int softplus, bool in,
-                                              bool rev, double behind, int lane) {
+                                              bool rev, double behind, float sign, int lane) {
     const int u = lane & (WALK - 1);
     const float d = in ? (softplus ? softplus_f(z) : z) : 0.f;
     const double l = in ? fmax((double)d * (double)A * 1.4426950408889634, -300.0) : 0.0;
@@ -393,16 +394,17 @@ __device__ __forceinline__ double walk_decays(WalkDecays& w, ExactDecays* x, flo
     if (BEHIND) {
         const double other = __shfl(total, 0);
         behind += lane >= WALK ? other : 0.0;
-        w.into[u] = exp2f((float)(behind + (total - c))) * src;
+        w.into[u] = exp2f((float)(behind + (total - c))) * (src * sign);
         if (u == 0) w.total = (float)behind;
         return total + __shfl_xor(total, WALK);
     }
-    w.from[u] = exp2f((float)c);
-    w.into[u] = exp2f((float)(total - c)) * src;
+    const float odd = lane >= WALK ? -1.f : 1.f;
+    w.from[u] = exp2f((float)c) * odd;
+    w.into[u] = exp2f((float)(total - c)) * (src * -odd);
     w.scale[u] = rev ? d : 1.f;
     w.c[u] = (float)c;
     w.less[u] = (float)(c - (double)__log2f(src));
-    if (u == 0) w.total = exp2f((float)total);
+    if (u == 0) w.total = -exp2f((float)total);
     if (EXACT) {
         const double hi = rint(c * 256.0) * (1.0 / 256.0);
         x->hi[u] = (float)hi;
@@ -517,6 +519,17 @@ ssm_walk_kernel(SsmArgs a, const DT* val, const DT* key, const DT* query, int64_
         return c;
     };
     const int dir = rev ? -1 : 1;
+    // A matrix instruction's additions are off towards one side, by a tenth of a unit in the last place, in every element
+    // alike: little, but sums over the whole state gather it (dA).  So the state is held with the other sign half of the
+    // time, where it is scaled anyway in every other chunk, in ENDS over the first half of the chunks.
+    const int turn = chunks / 2;
+    auto negate = [&]() {
+#pragma unroll
+        for (int k = 0; k < KT; ++k)
+#pragma unroll
+            for (int p = 0; p < PT; ++p) st[k][p] = -st[k][p];
+    };
+    bool positive = turn == 0;  // ENDS
     // dt of chunks ci and ci + 1, a token a lane
     auto steps_of = [&](int ci) {
         const Chunk c = chunk_at(ci + (lane >> 5));
@@ -527,7 +540,8 @@ ssm_walk_kernel(SsmArgs a, const DT* val, const DT* key, const DT* query, int64_
         const Chunk c = chunk_at(ci + (lane >> 5));
         const bool in = ci + (lane >> 5) < chunks && (lane & 31) < c.n;
         const int to = (ci & 2) + (lane >> 5);
-        log_decay += walk_decays<NP != 1, (MODE & ENDS) != 0>(dec[to], &exact[to], raw + bias, A, a.softplus, in, rev, log_decay, lane);
+        const float sign = ci + (lane >> 5) < turn ? -1.f : 1.f;
+        log_decay += walk_decays<NP != 1, (MODE & ENDS) != 0>(dec[to], &exact[to], raw + bias, A, a.softplus, in, rev, log_decay, sign, lane);
     };
 
     Stage<DT, Q, KT * 16, NT> bk, bq;
@@ -571,6 +585,10 @@ ssm_walk_kernel(SsmArgs a, const DT* val, const DT* key, const DT* query, int64_
             for (int o = 0; o < WAVES; ++o)
                 if (leads & 1 << o) most = fmaxf(most, sdec[4 * o + (ci & 3)].total);
             if (most < -152.f) break;
+            if (ci == turn && turn) {
+                negate();
+                positive = true;
+            }
         }
 
         if ((MODE & EMIT) && mine) {
@@ -580,12 +598,13 @@ ssm_walk_kernel(SsmArgs a, const DT* val, const DT* key, const DT* query, int64_
                 const int wide = a.blocks * a.cols;
                 float* e = emit + (cslot * a.H + h) * ((int64_t)KT * 16 * wide) + p0;
                 const int own = renewed(4 * q4 * wide + l15);
+                const float sign = ci & 1 ? -1.f : 1.f;
 #pragma unroll
                 for (int k = 0; k < KT; ++k)
 #pragma unroll
                     for (int r = 0; r < 4; ++r)
 #pragma unroll
-                        for (int p = 0; p < PT; ++p) e[own + (16 * k + r) * wide + 16 * p] = st[k][p][r];
+                        for (int p = 0; p < PT; ++p) e[own + (16 * k + r) * wide + 16 * p] = st[k][p][r] * sign;
             }
         }
 
@@ -763,6 +782,7 @@ ssm_walk_kernel(SsmArgs a, const DT* val, const DT* key, const DT* query, int64_
     }
     if (!mine) return;
     if (MODE & ENDS) {
+        if (!positive) negate();
         f32x4* e = reinterpret_cast<f32x4*>(a.ends);
 #pragma unroll
         for (int k = 0; k < KT; ++k)
@@ -770,6 +790,7 @@ ssm_walk_kernel(SsmArgs a, const DT* val, const DT* key, const DT* query, int64_
             for (int p = 0; p < PT; ++p) e[frag + (k * PT + p) * WAVE] = st[k][p];
         if (lane == 0 && decides && block == who) a.decay[(int64_t)at.slot * a.H + h] = exp2f((float)log_decay);
     } else if (is_last && last_state) {
+        if (chunks & 1) negate();
         float* f = last_state + ((int64_t)pc.seq * a.H + h) * a.K * a.P;
 #pragma unroll
         for (int k = 0; k < KT; ++k)
@@ -823,7 +844,11 @@ __global__ void __launch_bounds__(NT) ssm_join_kernel(SsmArgs a, const float* fi
     }
 }
 
-template <int Q> struct GradSums { float row[WAVES][Q], col[WAVES][Q], ui[WAVES][Q], vi[WAVES][Q], xy[Q], hg[WAVES]; };
+// row, col: of the products of two tiles, col also of a tile's with itself; near: a tile's own part of the derivative of
+// its tokens' log decays; far: row of the tiles (3, 0) and (2, 0)
+template <int Q> struct GradSums {
+    float row[WAVES][Q], col[WAVES][Q], ui[WAVES][Q], vi[WAVES][Q], own[Q], near[Q + 1], far[2][16], xy[Q], hg[WAVES];
+};
 
 // The decays of every chunk and head, for the gradient: a wavefront each.
 template <typename DT>
@@ -996,16 +1021,33 @@ __global__ void __launch_bounds__(NT, 2) ssm_grad_kernel(SsmArgs a, int slots, i
             const f32x4 slo = *reinterpret_cast<const f32x4*>(&dec.lo[s0]);
             const f32x4 src = *reinterpret_cast<const f32x4*>(&dec.src[s0]);
             float row = 0.f, v[4];
-            f32x4 zs;
+            f32x4 zs, before;
 #pragma unroll
             for (int r = 0; r < 4; ++r) {
                 const bool in = i < j || 4 * q4 + r <= l15;
                 const float le = in ? __builtin_amdgcn_exp2f((hi - shi[r]) + (lo - slo[r])) * e[r] : 0.f;
                 v[r] = le * src[r];
-                const float z = le * cb[x][r];
+                float z = le * cb[x][r];
+                if (i == j && 4 * q4 + r == l15) {
+                    // a token's own product: in the derivative of its step, in no decay's
+                    sum.xy[t] = e[r];
+                    sum.own[t] = z;
+                    z = 0.f;
+                }
                 row += z * src[r];
-                if (i == j && 4 * q4 + r == l15) sum.xy[t] = e[r];
+                before[r] = row;
                 zs[r] = z;
+            }
+            if (i == j) {
+                // token j + 1's decay is in the products of rows behind j with columns up to j: running sums over the
+                // columns, added over the rows
+                const float one = __shfl_up(row, 16), pair = row + (q4 >= 1 ? one : 0.f);
+                const float two = __shfl_up(pair, 32), up = __shfl_up(pair + (q4 >= 2 ? two : 0.f), 16);
+                const float left = q4 >= 1 ? up : 0.f;
+#pragma unroll
+                for (int r = 0; r < 4; ++r) before[r] = 4 * q4 + r < l15 ? left + before[r] : 0.f;
+                const float o = sums16(before, lane);
+                if (l15 < 4) sum.near[s0 + l15 + 1] = o;
             }
             const float c = sums16(zs, lane);  // over the tile's 16 tokens t
             if (l15 < 4) sum.col[wave][s0 + l15] = c;
@@ -1020,10 +1062,14 @@ __global__ void __launch_bounds__(NT, 2) ssm_grad_kernel(SsmArgs a, int slots, i
                     v[3] -= high_of(a1);
                 }
             }
+            if (i == j) continue;
             row += __shfl_xor(row, 16);
             row += __shfl_xor(row, 32);
-            // tiles of the same rows follow each other
-            if (q4 == 0) sum.row[wave][t] = x > 0 && tile_j(x) == tile_j(x - 1) ? sum.row[wave][t] + row : row;
+            if (q4 == 0) {
+                // tiles of the same rows follow each other
+                sum.row[wave][t] = x > 0 && tile_j(x) == tile_j(x - 1) ? sum.row[wave][t] + row : row;
+                if (QT == 4 && x == 0 && i == 0 && j > 1) sum.far[j == 2][l15] = row;
+            }
         }
         __syncthreads();
 
@@ -1130,21 +1176,32 @@ __global__ void __launch_bounds__(NT, 2) ssm_grad_kernel(SsmArgs a, int slots, i
         __syncthreads();
 
         if (threadIdx.x < Q) {
-            const int t = threadIdx.x;
+            const int t = threadIdx.x, tile = t / 16;
+            const int same = QT == 4 ? (tile == 1 ? 3 : tile == 2 ? 2 : 1) : 2 - tile;  // the wavefront of the tile's products with itself
             float row = 0.f, col = 0.f, ui = 0.f, vi = 0.f;
 #pragma unroll
             for (int w = 0; w < WAVES; ++w) {
                 row += sum.row[w][t];
-                col += sum.col[w][t];
+                if (w != same) col += sum.col[w][t];
                 ui += sum.ui[w][t];
                 vi += sum.vi[w][t];
             }
-            float* o = a.tok + ((int64_t)at.slot * all_units + unit) * (5 * Q) + t;
-            o[0] = row + ui;
-            o[Q] = col;
-            o[2 * Q] = vi;
-            o[3 * Q] = sum.xy[t];
-            if (t == 0) o[4 * Q] = (sum.hg[0] + sum.hg[1]) + (sum.hg[2] + sum.hg[3]);
+            // products of later tiles with earlier ones pass the whole of a tile between them
+            float between = 0.f;
+            if (QT == 4) {
+                between = tile == 1 ? sum.far[0][t & 15] + sum.far[1][t & 15] : tile == 2 ? sum.row[0][t + 16] : 0.f;
+#pragma unroll
+                for (int m = 1; m < 16; m <<= 1) between += __shfl_xor(between, m);
+            }
+            float* o = a.tok + ((int64_t)at.slot * all_units + unit) * ssm_token_floats(Q) + t;
+            o[0] = ui;
+            o[Q] = vi;
+            o[2 * Q] = row;
+            o[3 * Q] = col;
+            o[4 * Q] = sum.near[t] + between;
+            o[5 * Q] = sum.own[t] + sum.col[same][t];
+            o[6 * Q] = sum.xy[t];
+            if (t == 0) o[7 * Q] = (sum.hg[0] + sum.hg[1]) + (sum.hg[2] + sum.hg[3]);
         }
     }
 
@@ -1204,26 +1261,39 @@ __global__ void __launch_bounds__(NT) ssm_tokens_kernel(SsmArgs a, int slots) {
     }
     const int c0 = pc.start + pc.n * Q, n = min(Q, pc.len - pc.n * Q);
     const Decays<Q>& dec = reinterpret_cast<const Decays<Q>*>(a.dec)[i];
-    const float* tok = a.tok + i * a.blocks * (5 * Q);
-    double rows = 0.0, cols = 0.0, outs = 0.0, dd = 0.0, xy = 0.0, hg = 0.0, d = 0.0;
-    for (int b = 0; b < a.blocks; ++b) hg += tok[(int64_t)b * 5 * Q + 4 * Q];
+    const float* tok = a.tok + i * a.blocks * ssm_token_floats(Q);
+    double in = 0.0, out = 0.0, later = 0.0, sooner = 0.0, own = 0.0, dd = 0.0, xy = 0.0, hg = 0.0, d = 0.0;
+    for (int b = 0; b < a.blocks; ++b) hg += tok[(int64_t)b * ssm_token_floats(Q) + 7 * Q];
     if (lane < n) {
-        double c = 0.0, v = 0.0;
         for (int b = 0; b < a.blocks; ++b) {
-            const float* u = tok + (int64_t)b * 5 * Q + lane;
-            rows += u[0];
-            c += u[Q];
-            v += u[2 * Q];
-            xy += u[3 * Q];
+            const float* u = tok + (int64_t)b * ssm_token_floats(Q) + lane;
+            in += u[0];
+            out += u[Q];
+            later += u[2 * Q];
+            sooner += u[3 * Q];
+            own += u[4 * Q];
+            dd += u[5 * Q];
+            xy += u[6 * Q];
         }
         d = dec.src[lane];
-        cols = c * d;
-        outs = v * d;
-        dd = c + v;
+        dd += out + sooner;
+        out *= d;
+        sooner *= d;
     }
-    const double through = (double)dec.total * hg;
-    const double net = lanes_scan(rows - cols, lane), before = lanes_scan(outs, lane) - outs;
-    const double dl = __shfl(net, WAVE - 1) - net + (rows - cols) + before + through;
+    // A log decay is in every product of a token not before it with one before it.  Each sum here is one of such products
+    // only, with none that another takes away again: what enters (state before the chunk) with this or later tokens, what
+    // leaves with earlier ones, this tile's rows from here on with earlier tiles, its columns before with later ones.
+    double dl = own + (double)dec.total * hg;
+    const double first = lanes_scan(in, lane), last = lanes_scan(out, lane);
+    dl += __shfl(first, WAVE - 1) - first + in + (last - out);
+    const double mine = sooner;
+#pragma unroll
+    for (int m = 1; m < 16; m <<= 1) {
+        const double r = __shfl_down(later, m, 16), c = __shfl_up(sooner, m, 16);
+        if ((lane & 15) + m < 16) later += r;
+        if ((lane & 15) >= m) sooner += c;
+    }
+    dl += later + (sooner - mine);
     double dz = 0.0;
     if (lane < n) {
         const float z = a.dt[(int64_t)(c0 + lane) * a.dts + h] + (a.bias ? a.bias[h] : 0.f);

@@ -40,6 +40,7 @@ struct SsmArgs {
 inline int64_t ssm_units(const SsmArgs& a) { return (int64_t)a.H * a.blocks; }
 inline int64_t ssm_slots(const SsmArgs& a, int every) { return (int64_t)a.T / every + a.N; }
 inline int64_t ssm_unit_state(const SsmArgs& a) { return (int64_t)a.rows * a.cols; }  // of the gradient's units
+constexpr int ssm_token_floats(int chunk) { return 7 * chunk + 16; }  // of a chunk and unit
 inline int64_t ssm_decay_floats(const SsmArgs& a) { return 5ll * a.chunk + 16; }
 
 hipError_t launch_ssm_fwd(const SsmArgs& a, hipStream_t st);

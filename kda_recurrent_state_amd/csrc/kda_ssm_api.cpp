@@ -94,7 +94,7 @@ size_t layout(kda::SsmArgs* a, int backward, uint8_t* base) {
         a->gs = take(slots * units * kda::ssm_unit_state(*a));
         if (a->split > 1) a->part = take((int64_t)a->split * 2 * a->T * a->G * a->K);
         a->dec = take(slots * a->H * kda::ssm_decay_floats(*a));
-        a->tok = take(slots * units * 5 * a->chunk);
+        a->tok = take(slots * units * kda::ssm_token_floats(a->chunk));
         a->sums = take(slots * 3 * a->H);
     }
     return at;
