@@ -200,7 +200,7 @@ def _apart(out, *inputs):
 
 def _bytes_apart(what, a, b, tensors):
     for t in tensors:
-        if t is not None and _touches(t, a, b):
+        if t is not None and t.data_ptr() < b and _touches(t, a, b):
             raise ValueError(f"{what} overlaps another tensor of the call")
 
 

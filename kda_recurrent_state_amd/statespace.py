@@ -179,8 +179,9 @@ def ssm_conv_step(xbc, conv_weight, conv_state, dt, A, h, D=None, dt_bias=None, 
     _tokens(dt, "dt", torch.float32, (N, H))
     _full(conv_weight, "conv_weight", torch.float32, (channels, W))
     _full(conv_bias, "conv_bias", torch.float32, (channels,))
-    for t, name in ((_given(conv_state, "conv_state"), "conv_state"), (conv_state_out, "conv_state_out")):
-        _full(t, name, xbc.dtype, (N, W - 1, channels))
+    states = (N, W - 1, channels)
+    _full(_given(conv_state, "conv_state"), "conv_state", xbc.dtype, states)
+    _full(conv_state_out, "conv_state_out", xbc.dtype, states)
     _full(_given(A, "A"), "A", torch.float32, (H,))
     _full(D, "D", torch.float32, (H,))
     _full(dt_bias, "dt_bias", torch.float32, (H,))
