@@ -548,7 +548,11 @@ Shape shape_of(int64_t M, int64_t N, bool dual, int halves, int steps, bool may_
         return ((M + bm - 1) / bm) * ((N + (dual ? bn / 2 : bn) - 1) / (dual ? bn / 2 : bn)) * halves;
     };
     Shape s;
-    s.big = tiles(256, 256) >= 192;
+    // A tile of 256 x 256 has half the reads of four of 128 x 128, but one has a compute unit to itself: taken where its
+    // last round of workgroups is full enough, three quarters over all rounds.  bf16 forward, big and small, us:
+    // 256 tiles 55, 67; 320 173, 156; 352 95, 94; 396 77, 86; 640 276, 305; 88 47, 34.
+    const int64_t big = tiles(256, 256), rounds = (big + 255) / 256;
+    s.big = rounds > 0 && big * 4 >= rounds * 256 * 3;
     const int bm = s.big ? 256 : 128, bn = bm;
     s.mt = (int)((M + bm - 1) / bm);
     s.nt = (int)((N + (dual ? bn / 2 : bn) - 1) / (dual ? bn / 2 : bn));
@@ -628,6 +632,13 @@ Shape dw_shape(const GluArgs& a) {
     const int np = planes(a);
     return shape_of(a.F, a.D, false, 2, (int)(up(a.T, PAD) / KI) * (np == 1 ? 1 : 6), true);
 }
+// Few tokens or tiles.  Inputs that tiles can read as they lie: tiles from 33 tokens on, where there are 96 of
+// them.  bf16 forward of 33 and 64 tokens, few or tiles, us: 4096 x 10240 56, 68 or 45, 46; 2048 x 8192 26, 30 or 25, 25; 4096 x
+// 5632 41, 47 or 43, 44; 2048 x 2816 15, 17 or 21, 21.  Others are packed for tiles, and fp32 has six products:
+// 64 tokens 1000 x 2731 bf16 10 or 28, fp32 23 or 81; 4096 x 10240 fp32 191 or 508.
+bool is_few(const GluArgs& a) {
+    return a.T <= (a.x_plain && a.w_plain && a.F > 95 * 64 ? GLU_FEW / 2 : GLU_FEW);
+}
 Work work_of(const GluArgs& a, bool backward, bool input_grad, uint8_t* base) {
     Work w;
     auto take = [&](int64_t bytes) {
@@ -636,7 +647,7 @@ Work work_of(const GluArgs& a, bool backward, bool input_grad, uint8_t* base) {
         return p;
     };
     const int64_t np = planes(a), pad = pad_of(a);
-    if (!backward && a.T <= GLU_FEW) return w;
+    if (!backward && is_few(a)) return w;
     if (!a.x_plain) w.x = (bf16*)take(a.T * pad * np * 2);
     if (!a.w_plain) {
         w.wg = (bf16*)take(a.F * pad * np * 2);
@@ -695,7 +706,7 @@ template <typename DT, int ACT> hipError_t few(const GluArgs& a, hipStream_t st)
 }
 
 template <typename DT, int ACT> hipError_t forward(const GluArgs& a, hipStream_t st) {
-    if (a.T <= GLU_FEW) return few<DT, ACT>(a, st);
+    if (is_few(a)) return few<DT, ACT>(a, st);
     const Work w = work_of(a, false, false, a.ws);
     Inputs in;
     GLU_TRY((inputs<DT>(a, w, &in, st)));
