@@ -54,7 +54,8 @@ def test_against_definition(size, act, dtype):
     log("  share of the allowed error: " + " ".join(f"{v:.3f}" for v in w))
 
 
-@pytest.mark.parametrize("size", [(2000, 256, 4096), (5000, 1088, 1000), (4096, 512, 8192)], ids=str)
+@pytest.mark.parametrize("size", [(2000, 256, 4096), (5000, 1088, 1000), (4096, 512, 8192), (4090, 4096, 72), (4090, 4000, 40),
+                                  (100, 4096, 2040), (65, 4000, 2040), (50, 192, 6144)], ids=str)
 def test_large_tiles(size):
     """The large tiles' shapes, in whole numbers: sums below 2^24 are exact in any order, so the weights' gradients and
     the products are too."""
