@@ -16,11 +16,19 @@
 // nearly so.  No exponent is positive, so nothing overflows whatever the decay; l is held above
 // -300, below which 2^l is zero for every state that fp32 holds.
 //
-// Matrix cores take bf16 operands.  bf16 inputs go in as they are; what is computed in fp32 (the
-// masked products, the state, decayed inputs) goes in as a sum of 2 or 3 bf16 parts, each the
-// rounding of what the parts before it left: two hold a value to 2^-18, three to 2^-26 of itself.
-// Two for what ends in a bf16 output, three for the states and wherever inputs are fp32 (those
-// are split as they are staged; products of parts below 2^-24 are left out).
+// Matrix cores take bf16 operands.  bf16 inputs go in as they are; what is computed in fp32 and is an operand again goes in as
+// a sum of bf16 parts, each the rounding of what the parts before it left: three hold a value to 2^-26 of itself.
+//   - states, and what the derivatives of dt, A and h0 are sums of: three parts;
+//   - y, dx, dB and dC with bf16 inputs: the masked products and (in y and dx) the state are rounded to bf16 once.  Every
+//     term of such a result has one of them as a factor, so the result is off by at most 2^-8 of the
+//     sum of its terms' magnitudes, about what its own rounding costs (measured against 64 bits 1.8e-3, rounding alone 1.7e-3;
+//     with two parts y took 1080 us where it takes 846, 2 x 32768 tokens);
+//   - fp32 inputs: everything in three parts, split as it is staged; products of parts below 2^-24 are left out.
+//
+// Per call: the segments' own states (ENDS), their join, and the walk proper.  The gradient does this twice, forwards for the
+// states before every chunk (EMIT) and backwards for dx and the derivatives behind every chunk, and then
+// has a kernel over chunks for what needs both.  2 x 32768 tokens of 32 heads of 128 x 128, bf16: 735 us (ENDS 185, join 18,
+// OUT 535); gradient of 2 x 8192: 985 us (below).
 #include "kda_ssm.hpp"
 
 #include "kda_rows.hpp"
@@ -418,6 +426,11 @@ __device__ __forceinline__ double walk_decays(WalkDecays& w, ExactDecays* x, flo
 // OUT: writes the results; EMIT: the state before every chunk of a.chunk tokens; ENDS: starts from zero and
 // writes the segment's own state and decay (not for a sequence's last segment).
 //
+// What bounds it: instruction issue.  For 65536 tokens of 32 heads OUT issues 177e6 vector and 19e6 matrix instructions, 288
+// and 121 us on 1024 SIMDs at 2.4 GHz (4 and 16 cycles each), and takes 535; the two hardly overlap.  It moves
+// 1.15 GB, 2.2 TB/s.  ENDS 42e6 and 7e6: 68 and 44 us of 185.  Vector instructions are the splitting of the state and the decayed rows into parts (3 instructions a pair and
+// part), the scaling of the state, and a sixth the masked products.
+//
 // A unit is narrow, 64 registers of state, so that three wavefronts share a SIMD: with twice the columns two did,
 // and waited for LDS and each other (with two of this size on a SIMD 764 us against 589, 2 x 32768 tokens of 32 heads).  The wavefronts of a
 // workgroup that have the same head form the masked products once between them, in LDS.  Chunks of 32 tokens;
@@ -805,7 +818,8 @@ ssm_walk_kernel(SsmArgs a, const DT* val, const DT* key, const DT* query, int64_
 }
 
 // Joins the segments of a sequence: ends[slot] holds what the segment adds from a zero state and becomes
-// the state it starts from.  Four elements a thread.
+// the state it starts from.  Four elements a thread, the next segment's on their way.  One read and one write of the segments'
+// states (92 MB in 18 us, 2 x 32768 tokens in 22 segments, 5.1 TB/s).
 __global__ void __launch_bounds__(NT) ssm_join_kernel(SsmArgs a, const float* first_state, int rev, int per_unit,
                                                       int pieces) {
     const int64_t units = (int64_t)a.H * a.wblocks;
@@ -877,6 +891,11 @@ __global__ void __launch_bounds__(NT) ssm_decay_kernel(SsmArgs a, int slots) {
 // three 16 x 16 tiles of E and its products (in LDS as bf16 parts; C . B, the same for all heads, stays in
 // registers), then a quarter of the columns of dB and dC, so no sum crosses wavefronts but those of single
 // numbers a token, which ssm_tokens_kernel puts together.
+//
+// 2 x 8192 tokens of 32 heads of 128 x 128, bf16: 415 us of 985 (walks 220 and 140, ENDS 2 x 73, joins 2 x 16, tokens 16,
+// decays 9, sums 4).  Vector issue 179 us (110e6 instructions), matrix 54, LDS 107 (66e6 cycles on 256 compute units), and
+// it reads 1.4 GB, most of it the chunks' states, 3.4 TB/s: no one resource, but the phases of a unit behind each other at
+// two wavefronts a SIMD.
 template <typename DT, int KT, int PT>
 __global__ void __launch_bounds__(NT, 2) ssm_grad_kernel(SsmArgs a, int slots, int quads) {
     using C_ = Cfg<DT>;
@@ -1349,6 +1368,9 @@ template <typename DT> __global__ void __launch_bounds__(NT) ssm_conv_kernel(Ssm
     a.z[i] = z;
 }
 
+// 256 sequences of 32 heads of 128 x 128: 189 us, 1.06 GB at 5.6 TB/s, bound by memory.  The convolution before it is a
+// kernel of its own (10 us there): in this one every head of a group would convolve the group's B and C again, and its
+// states move on in place under the other heads' reads.
 // A workgroup per (sequence, head, COLS columns): the state is read and written once, V neighbouring
 // columns and K / ROWS rows a thread.
 template <typename TI, typename TO, int V>
