@@ -17,8 +17,10 @@ Shapes (tokens of all sequences packed along the first axis):
     fp32 (o has the same dtype); log_a, beta and states are fp32.
 
 The operators that a token-mixing block runs around the layer (short
-convolution, diagonal recurrence, gated and residual norms) are in ``block.py``
-and exported here as well.
+convolution, diagonal recurrence, gated and residual norms) are in ``block.py``,
+the selective state space scan in ``statespace.py``, the gated feed-forward
+products in ``feedforward.py`` and states kept in 8 bits in ``state_cache.py``;
+all are exported here as well.
 """
 from __future__ import annotations
 
