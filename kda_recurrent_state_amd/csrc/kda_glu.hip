@@ -433,9 +433,9 @@ template <typename DT, int ACT> __global__ void __launch_bounds__(256) glu_saved
 
 // ---------------------------------------------------------------- few tokens
 //
-// Few tokens: the weights are what there is to read.  4 tokens of 4096 x 10240 bf16: 168 MB in 34.5 us, 4.9 TB/s.  A workgroup takes 16 columns of both
-// weights, its wavefronts a part of the sum each; weights come straight from memory into the operand's
-// registers, x from the cache.
+// Few tokens: the weights are what there is to read.  4 tokens of 4096 x 10240 bf16: 168 MB in 34.5 us, 4.9 TB/s.
+// A workgroup takes 16 columns of both weights, its wavefronts a part of the sum each; weights come straight from
+// memory into the operand's registers, x from the cache.
 template <typename DT> struct Direct;
 template <> struct Direct<bf16> {
     static constexpr int NP = 1;
@@ -762,7 +762,7 @@ template <typename DT, int ACT> hipError_t backward(const GluArgs& a, hipStream_
         p.ldb = in.wg.ld;
         p.M = a.T;
         p.N = a.D;
-            p.kB = a.F;
+        p.kB = a.F;
         p.colsB = pad_of(a);
         p.halves = 1;
         p.out = a.dx;

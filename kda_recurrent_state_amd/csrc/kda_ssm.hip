@@ -1483,7 +1483,11 @@ hipError_t walk(const SsmArgs& a, const Roles& r, hipStream_t st) {
 
 bool segmented(const SsmArgs& a) { return a.cu ? a.seg < a.T : a.seg < a.eq; }
 
-#define SSM_TRY(call)                                do {                                                 const hipError_t e_ = (call);                    if (e_ != hipSuccess) return e_;             } while (0)
+#define SSM_TRY(call)                     \
+    do {                                  \
+        const hipError_t e_ = (call);     \
+        if (e_ != hipSuccess) return e_;  \
+    } while (0)
 
 // The states that the segments start from, then the walk proper.
 template <typename DT, int KT, int PT, int MODE>
