@@ -435,6 +435,11 @@ __device__ __forceinline__ double walk_decays(WalkDecays& w, ExactDecays* x, flo
 // and waited for LDS and each other (with two of this size on a SIMD 764 us against 589, 2 x 32768 tokens of 32 heads).  The wavefronts of a
 // workgroup that have the same head form the masked products once between them, in LDS.  Chunks of 32 tokens;
 // with bf16 inputs the next chunk's rows are on their way in registers while one is multiplied.
+//
+// Heads of a workgroup, whose first unit's number in the group is a multiple of four: two of two blocks each, and any more blocks leave
+// room for parts of two.  So two workgroups in fp32 share a compute unit (K <= 64: 70 KB, with room for four heads 90).
+__host__ __device__ constexpr int walk_heads(int blocks) { return blocks == 1 ? WAVES : 2; }
+
 template <typename DT, int KT, int PT, int MODE>
 __global__ void __launch_bounds__(NT, sizeof(DT) == 2 ? 3 : 2)
 ssm_walk_kernel(SsmArgs a, const DT* val, const DT* key, const DT* query, int64_t vs, int64_t ks, int64_t qs,
@@ -451,8 +456,9 @@ ssm_walk_kernel(SsmArgs a, const DT* val, const DT* key, const DT* query, int64_
     char* const squery = skey + KEYS;
     char* const svals = squery + QUERIES;
     char* const smasked = svals + WAVES * VALS;
-    WalkDecays* const sdec = reinterpret_cast<WalkDecays*>(smasked + WAVES * MASKED);  // [head][chunk & 3]
-    ExactDecays* const sexact = reinterpret_cast<ExactDecays*>(sdec + 4 * WAVES);
+    const int heads = walk_heads(a.wblocks);  // that a workgroup may have
+    WalkDecays* const sdec = reinterpret_cast<WalkDecays*>(smasked + heads * MASKED);  // [head][chunk & 3]
+    ExactDecays* const sexact = reinterpret_cast<ExactDecays*>(sdec + 4 * heads);
 
     const int lane = threadIdx.x % WAVE, wave = __builtin_amdgcn_readfirstlane(threadIdx.x / WAVE);
     const int l15 = lane & 15, q4 = lane >> 4;
@@ -484,9 +490,10 @@ ssm_walk_kernel(SsmArgs a, const DT* val, const DT* key, const DT* query, int64_
     const int64_t frag = ((int64_t)at.slot * a.H * a.wblocks + unit) * (KT * PT * WAVE) + lane;
 
     char* const sval = svals + wave * VALS;
-    char* const sm = smasked + lead * MASKED;
-    WalkDecays* const dec = sdec + 4 * lead;
-    ExactDecays* const exact = sexact + 4 * lead;
+    const int own = mine ? __builtin_popcount(leads & ((1 << lead) - 1)) : 0;  // the head's number in the workgroup
+    char* const sm = smasked + own * MASKED;
+    WalkDecays* const dec = sdec + 4 * own;
+    ExactDecays* const exact = sexact + 4 * own;
     f32x4 st[KT][PT];
 #pragma unroll
     for (int k = 0; k < KT; ++k)
@@ -513,7 +520,7 @@ ssm_walk_kernel(SsmArgs a, const DT* val, const DT* key, const DT* query, int64_
         }
     }
     if (MODE & OUT) {  // the tile above the diagonal stays zero
-        for (int i = threadIdx.x * 16; i < WAVES * MASKED; i += NT * 16) *reinterpret_cast<f32x4*>(smasked + i) = zero4();
+        for (int i = threadIdx.x * 16; i < heads * MASKED; i += NT * 16) *reinterpret_cast<f32x4*>(smasked + i) = zero4();
     }
     const float dskip = (MODE & OUT) && a.D && mine ? a.D[h] : 0.f;
     const float A = a.A[h], bias = a.bias ? a.bias[h] : 0.f;
@@ -596,7 +603,7 @@ ssm_walk_kernel(SsmArgs a, const DT* val, const DT* key, const DT* query, int64_
             float most = -INFINITY;
 #pragma unroll
             for (int o = 0; o < WAVES; ++o)
-                if (leads & 1 << o) most = fmaxf(most, sdec[4 * o + (ci & 3)].total);
+                if (o < __builtin_popcount(leads)) most = fmaxf(most, sdec[4 * o + (ci & 3)].total);
             if (most < -152.f) break;
             if (ci == turn && turn) {
                 negate();
@@ -1441,10 +1448,11 @@ __global__ void __launch_bounds__(NT) ssm_step_kernel(SsmStepArgs a, int lanes_l
 
 // ---------------------------------------------------------------- launches
 
-template <typename DT, int KT, int PT, int MODE> constexpr int walk_lds() {
+template <typename DT, int KT, int PT, int MODE> constexpr int walk_lds(int heads) {
     constexpr int NP = Cfg<DT>::NP;
-    return NP * WALK * ((MODE & OUT ? 2 : 1) * KT * 32 + WAVES * PT * 32) + (MODE & OUT ? WAVES * Cfg<DT>::MP * WALK * WALK * 2 : 0) +
-           4 * WAVES * ((int)sizeof(WalkDecays) + (NP == 1 ? 0 : (int)sizeof(ExactDecays)));
+    return NP * WALK * ((MODE & OUT ? 2 : 1) * KT * 32 + WAVES * PT * 32) +
+           heads * ((MODE & OUT ? Cfg<DT>::MP * WALK * WALK * 2 : 0) +
+                    4 * ((int)sizeof(WalkDecays) + (NP == 1 ? 0 : (int)sizeof(ExactDecays))));
 }
 template <typename DT, int KT, int PT> constexpr int grad_lds() {
     constexpr int Q = Cfg<DT>::QT * 16, NP = Cfg<DT>::NP;
@@ -1471,8 +1479,8 @@ template <typename DT, int KT, int PT, int MODE>
 hipError_t walk(const SsmArgs& a, const Roles& r, hipStream_t st) {
     const int64_t slots = ssm_slots(a, a.seg);
     const int quads = (a.H / a.G * a.wblocks + WAVES - 1) / WAVES;
-    constexpr int lds = walk_lds<DT, KT, PT, MODE>();
-    static_assert(lds <= 160 * 1024, "a chunk's tiles fit a compute unit");
+    static_assert(walk_lds<DT, KT, PT, MODE>(WAVES) <= 160 * 1024, "a chunk's tiles fit a compute unit");
+    const int lds = walk_lds<DT, KT, PT, MODE>(walk_heads(a.wblocks));
     auto* kernel = ssm_walk_kernel<DT, KT, PT, MODE>;
     const hipError_t e = allow_lds(kernel, lds);
     if (e != hipSuccess) return e;
