@@ -326,6 +326,16 @@ int64_t place_blocks(int64_t slots, int G, int quads) { return (slots * G + 7) /
 
 constexpr int OUT = 1, EMIT = 2, ENDS = 4;
 
+// What a walk takes and gives: the values, keys and queries (x, B, C; reversed dy, C, B) and their token strides, the
+// states before the first token and behind the last, those before every chunk, and its segments' own states and decays.
+struct Role {
+    const void *val, *key, *query;
+    int64_t vs, ks, qs;
+    const float* first;
+    float *last, *emit, *ends, *decay;
+    int rev;
+};
+
 // A value the compiler takes for a new one.  Addresses that depend on it are formed where they are used
 // and not kept in registers through the walk, where the state leaves no room for them.
 __device__ __forceinline__ unsigned renewed(unsigned v) {
@@ -442,13 +452,18 @@ __host__ __device__ constexpr int walk_heads(int blocks) { return blocks == 1 ? 
 
 template <typename DT, int KT, int PT, int MODE>
 __global__ void __launch_bounds__(NT, sizeof(DT) == 2 ? 3 : 2)
-ssm_walk_kernel(SsmArgs a, const DT* val, const DT* key, const DT* query, int64_t vs, int64_t ks, int64_t qs,
-                const float* first_state, float* last_state, float* emit, int rev, int slots, int quads) {
+ssm_walk_kernel(SsmArgs a, Role one, Role two, int slots, int quads) {
     using C_ = Cfg<DT>;
     using TK = Tile<KT * 16>;
     using TP = Tile<PT * 16>;
     constexpr int Q = WALK, NP = C_::NP, MP = C_::MP, HP = C_::HP;
     constexpr bool AHEAD = NP == 1;
+    const Role& role = (MODE & ENDS) && blockIdx.y ? two : one;
+    const DT *const val = (const DT*)role.val, *const key = (const DT*)role.key, *const query = (const DT*)role.query;
+    const int64_t vs = role.vs, ks = role.ks, qs = role.qs;
+    const float* const first_state = role.first;
+    float *const last_state = role.last, *const emit = role.emit;
+    const int rev = role.rev;
     constexpr int PLK = Q * TK::ROW, PLP = Q * TP::ROW, PLM = Q * Q * 2;  // bytes of a plane
     constexpr int KEYS = NP * PLK, QUERIES = (MODE & OUT) ? KEYS : 0, VALS = NP * PLP, MASKED = (MODE & OUT) ? MP * PLM : 0;
     extern __shared__ __attribute__((aligned(16))) char smem[];
@@ -501,7 +516,7 @@ ssm_walk_kernel(SsmArgs a, const DT* val, const DT* key, const DT* query, int64_
         for (int p = 0; p < PT; ++p) st[k][p] = zero4();
     if (!(MODE & ENDS) && mine) {
         if (!is_first) {
-            const f32x4* e = reinterpret_cast<const f32x4*>(a.ends);
+            const f32x4* e = reinterpret_cast<const f32x4*>(role.ends);
 #pragma unroll
             for (int k = 0; k < KT; ++k)
 #pragma unroll
@@ -803,12 +818,12 @@ ssm_walk_kernel(SsmArgs a, const DT* val, const DT* key, const DT* query, int64_
     if (!mine) return;
     if (MODE & ENDS) {
         if (!positive) negate();
-        f32x4* e = reinterpret_cast<f32x4*>(a.ends);
+        f32x4* e = reinterpret_cast<f32x4*>(role.ends);
 #pragma unroll
         for (int k = 0; k < KT; ++k)
 #pragma unroll
             for (int p = 0; p < PT; ++p) e[frag + (k * PT + p) * WAVE] = st[k][p];
-        if (lane == 0 && decides && block == who) a.decay[(int64_t)at.slot * a.H + h] = exp2f((float)log_decay);
+        if (lane == 0 && decides && block == who) role.decay[(int64_t)at.slot * a.H + h] = exp2f((float)log_decay);
     } else if (is_last && last_state) {
         if (chunks & 1) negate();
         float* f = last_state + ((int64_t)pc.seq * a.H + h) * a.K * a.P;
@@ -827,8 +842,10 @@ ssm_walk_kernel(SsmArgs a, const DT* val, const DT* key, const DT* query, int64_
 // Joins the segments of a sequence: ends[slot] holds what the segment adds from a zero state and becomes
 // the state it starts from.  Four elements a thread, the next segment's on their way.  One read and one write of the segments'
 // states (92 MB in 18 us, 2 x 32768 tokens in 22 segments, 5.1 TB/s).
-__global__ void __launch_bounds__(NT) ssm_join_kernel(SsmArgs a, const float* first_state, int rev, int per_unit,
-                                                      int pieces) {
+__global__ void __launch_bounds__(NT) ssm_join_kernel(SsmArgs a, Role one, Role two, int per_unit, int pieces) {
+    const Role& role = blockIdx.y ? two : one;
+    const float* const first_state = role.first;
+    const int rev = role.rev;
     const int64_t units = (int64_t)a.H * a.wblocks;
     for (int64_t b = blockIdx.x; b < a.N * units * pieces; b += gridDim.x) {
     const int piece = (int)(b % pieces), unit = (int)(b / pieces % units), seq = (int)(b / pieces / units);
@@ -847,9 +864,9 @@ __global__ void __launch_bounds__(NT) ssm_join_kernel(SsmArgs a, const float* fi
             if (k0 + r < a.K && p < a.P) cur[r] = first_state[(((int64_t)seq * a.H + h) * a.K + k0 + r) * a.P + p];
     }
     const int64_t slot = start / a.seg + seq;
-    f32x4* ends = reinterpret_cast<f32x4*>(a.ends);
+    f32x4* ends = reinterpret_cast<f32x4*>(role.ends);
     auto at = [&](int j) { return ((slot + (rev ? segs - 1 - j : j)) * units + unit) * per_unit + e; };
-    auto dec = [&](int j) { return a.decay[(slot + (rev ? segs - 1 - j : j)) * a.H + h]; };
+    auto dec = [&](int j) { return role.decay[(slot + (rev ? segs - 1 - j : j)) * a.H + h]; };
     f32x4 nxt = ends[at(0)];
     float nd = dec(0);
     for (int j = 0; j + 1 < segs; ++j) {
@@ -1466,17 +1483,8 @@ template <typename F> hipError_t allow_lds(F* kernel, int bytes) {
                          : hipSuccess;
 }
 
-struct Roles {
-    const void *val, *key, *query;
-    int64_t vs, ks, qs;
-    const float* first;
-    float* last;
-    float* emit;
-    int rev;
-};
-
 template <typename DT, int KT, int PT, int MODE>
-hipError_t walk(const SsmArgs& a, const Roles& r, hipStream_t st) {
+hipError_t walk(const SsmArgs& a, const Role& one, const Role* two, hipStream_t st) {
     const int64_t slots = ssm_slots(a, a.seg);
     const int quads = (a.H / a.G * a.wblocks + WAVES - 1) / WAVES;
     static_assert(walk_lds<DT, KT, PT, MODE>(WAVES) <= 160 * 1024, "a chunk's tiles fit a compute unit");
@@ -1484,8 +1492,8 @@ hipError_t walk(const SsmArgs& a, const Roles& r, hipStream_t st) {
     auto* kernel = ssm_walk_kernel<DT, KT, PT, MODE>;
     const hipError_t e = allow_lds(kernel, lds);
     if (e != hipSuccess) return e;
-    hipLaunchKernelGGL(kernel, dim3((unsigned)place_blocks(slots, a.G, quads)), dim3(NT), lds, st, a, (const DT*)r.val,
-                       (const DT*)r.key, (const DT*)r.query, r.vs, r.ks, r.qs, r.first, r.last, r.emit, r.rev, (int)slots, quads);
+    hipLaunchKernelGGL(kernel, dim3((unsigned)place_blocks(slots, a.G, quads), two ? 2 : 1), dim3(NT), lds, st, a, one,
+                       two ? *two : one, (int)slots, quads);
     return hipGetLastError();
 }
 
@@ -1497,33 +1505,32 @@ bool segmented(const SsmArgs& a) { return a.cu ? a.seg < a.T : a.seg < a.eq; }
         if (e_ != hipSuccess) return e_;  \
     } while (0)
 
-// The states that the segments start from, then the walk proper.
-template <typename DT, int KT, int PT, int MODE>
-hipError_t whole_walk(const SsmArgs& a, const Roles& r, hipStream_t st) {
-    if (segmented(a)) {
-        SSM_TRY((walk<DT, KT, PT, ENDS>(a, r, st)));
-        const int per_unit = KT * PT * WAVE, pieces = (per_unit + NT - 1) / NT;
-        const int64_t blocks = (int64_t)a.H * a.wblocks * a.N * pieces;
-        hipLaunchKernelGGL(ssm_join_kernel, dim3((unsigned)(blocks < 1 << 20 ? blocks : 1 << 20)), dim3(NT), 0, st, a, r.first,
-                           r.rev, per_unit, pieces);
-        SSM_TRY(hipGetLastError());
-    }
-    return walk<DT, KT, PT, MODE>(a, r, st);
+// The states that the segments of one walk, or of two at once, start from.
+template <typename DT, int KT, int PT> hipError_t starts(const SsmArgs& a, const Role& one, const Role* two, hipStream_t st) {
+    if (!segmented(a)) return hipSuccess;
+    SSM_TRY((walk<DT, KT, PT, ENDS>(a, one, two, st)));
+    const int per_unit = KT * PT * WAVE, pieces = (per_unit + NT - 1) / NT;
+    const int64_t blocks = (int64_t)a.H * a.wblocks * a.N * pieces;
+    hipLaunchKernelGGL(ssm_join_kernel, dim3((unsigned)(blocks < 1 << 20 ? blocks : 1 << 20), two ? 2 : 1), dim3(NT), 0, st, a,
+                       one, two ? *two : one, per_unit, pieces);
+    return hipGetLastError();
 }
 
 template <typename DT, int KT, int PT> hipError_t forward(const SsmArgs& a, hipStream_t st) {
     constexpr int WT = PT / 2;
-    const Roles r{a.x, a.B, a.C, a.xs, a.bs, a.cs, a.h0, a.hT, nullptr, 0};
-    return whole_walk<DT, KT, WT, OUT>(a, r, st);
+    const Role r{a.x, a.B, a.C, a.xs, a.bs, a.cs, a.h0, a.hT, nullptr, a.ends, a.decay, 0};
+    SSM_TRY((starts<DT, KT, WT>(a, r, nullptr, st)));
+    return walk<DT, KT, WT, OUT>(a, r, nullptr, st);
 }
 
 template <typename DT, int KT, int PT> hipError_t backward(const SsmArgs& a, hipStream_t st) {
     constexpr int WT = PT / 2;
     if (a.N > 0) {
-        const Roles f{a.x, a.B, a.C, a.xs, a.bs, a.cs, a.h0, nullptr, a.hs, 0};
-        SSM_TRY((whole_walk<DT, KT, WT, EMIT>(a, f, st)));
-        const Roles b{a.dy, a.C, a.B, a.dys, a.cs, a.bs, a.dhT, a.dh0, a.gs, 1};
-        SSM_TRY((whole_walk<DT, KT, WT, OUT | EMIT>(a, b, st)));
+        const Role f{a.x, a.B, a.C, a.xs, a.bs, a.cs, a.h0, nullptr, a.hs, a.ends, a.decay, 0};
+        const Role b{a.dy, a.C, a.B, a.dys, a.cs, a.bs, a.dhT, a.dh0, a.gs, a.rends, a.rdecay, 1};
+        SSM_TRY((starts<DT, KT, WT>(a, f, &b, st)));
+        SSM_TRY((walk<DT, KT, WT, EMIT>(a, f, nullptr, st)));
+        SSM_TRY((walk<DT, KT, WT, OUT | EMIT>(a, b, nullptr, st)));
     }
     const int64_t slots = ssm_slots(a, a.chunk);
     if (a.T > 0) {

@@ -30,6 +30,7 @@ struct SsmArgs {
     int32_t split;                               // shares of a group's units in the gradient
     // workspace
     float *ends, *decay;                         // a segment's own state at its end / the state it starts from; its decay
+    float *rends, *rdecay;                       // the same of the gradient's reverse walk
     float *hs, *gs;                              // states before every chunk, derivatives behind it
     float *part;                                 // partial dB, dC of the shares
     float *dec;                                  // decays of every chunk and head

@@ -87,6 +87,10 @@ size_t layout(kda::SsmArgs* a, int backward, uint8_t* base) {
         const int64_t slots = kda::ssm_slots(*a, a->seg);
         a->ends = take(slots * a->H * a->wblocks * a->rows * a->wcols);
         a->decay = take(slots * a->H);
+        if (backward) {
+            a->rends = take(slots * a->H * a->wblocks * a->rows * a->wcols);
+            a->rdecay = take(slots * a->H);
+        }
     }
     if (backward) {
         const int64_t slots = kda::ssm_slots(*a, a->chunk);
@@ -104,7 +108,7 @@ size_t layout(kda::SsmArgs* a, int backward, uint8_t* base) {
 // product of the sizes' limits.
 int check_size(const kda::SsmArgs& a, int backward) {
     const double quads = ((int64_t)a.H / a.G * a.wblocks + kWaves - 1) / kWaves, chunks = kda::ssm_slots(a, a.chunk);
-    const double walk = ((double)kda::ssm_slots(a, a.seg) * a.G + 8) * quads;
+    const double walk = ((double)kda::ssm_slots(a, a.seg) * a.G + 8) * quads * (backward ? 2 : 1);
     const double grad = backward ? fmax((chunks * a.G + 8) * a.split, chunks * a.H / 4 + 1) : 0;
     const double states = backward ? chunks * a.H * a.blocks * a.rows * a.cols * 8 : 0;
     if (walk > kMaxBlocks || grad > kMaxBlocks || states > 1e18)
