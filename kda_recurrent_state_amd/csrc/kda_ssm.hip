@@ -451,14 +451,12 @@ __device__ __forceinline__ double walk_decays(WalkDecays& w, ExactDecays* x, flo
 __host__ __device__ constexpr int walk_heads(int blocks) { return blocks == 1 ? WAVES : 2; }
 
 template <typename DT, int KT, int PT, int MODE>
-__global__ void __launch_bounds__(NT, sizeof(DT) == 2 ? 3 : 2)
-ssm_walk_kernel(SsmArgs a, Role one, Role two, int slots, int quads) {
+__device__ __forceinline__ void walk_segment(const SsmArgs& a, const Role& role, int slots, int quads) {
     using C_ = Cfg<DT>;
     using TK = Tile<KT * 16>;
     using TP = Tile<PT * 16>;
     constexpr int Q = WALK, NP = C_::NP, MP = C_::MP, HP = C_::HP;
     constexpr bool AHEAD = NP == 1;
-    const Role& role = (MODE & ENDS) && blockIdx.y ? two : one;
     const DT *const val = (const DT*)role.val, *const key = (const DT*)role.key, *const query = (const DT*)role.query;
     const int64_t vs = role.vs, ks = role.ks, qs = role.qs;
     const float* const first_state = role.first;
@@ -836,6 +834,19 @@ ssm_walk_kernel(SsmArgs a, Role one, Role two, int slots, int quads) {
                     const int kk = 16 * k + 4 * q4 + r, pp = p0 + 16 * p + l15;
                     if (kk < a.K && pp < a.P) f[kk * a.P + pp] = st[k][p][r];
                 }
+    }
+}
+
+// Two walks of one kind side by side, or (BOTH) the gradient's, which need nothing from each other: the longer first.
+constexpr int BOTH = 8;
+template <typename DT, int KT, int PT, int MODE>
+__global__ void __launch_bounds__(NT, sizeof(DT) == 2 ? 3 : 2)
+ssm_walk_kernel(SsmArgs a, Role one, Role two, int slots, int quads) {
+    if constexpr (MODE == BOTH) {
+        if (blockIdx.y) walk_segment<DT, KT, PT, EMIT>(a, two, slots, quads);
+        else walk_segment<DT, KT, PT, OUT | EMIT>(a, one, slots, quads);
+    } else {
+        walk_segment<DT, KT, PT, MODE>(a, (MODE & ENDS) && blockIdx.y ? two : one, slots, quads);
     }
 }
 
@@ -1487,8 +1498,9 @@ template <typename DT, int KT, int PT, int MODE>
 hipError_t walk(const SsmArgs& a, const Role& one, const Role* two, hipStream_t st) {
     const int64_t slots = ssm_slots(a, a.seg);
     const int quads = (a.H / a.G * a.wblocks + WAVES - 1) / WAVES;
-    static_assert(walk_lds<DT, KT, PT, MODE>(WAVES) <= 160 * 1024, "a chunk's tiles fit a compute unit");
-    const int lds = walk_lds<DT, KT, PT, MODE>(walk_heads(a.wblocks));
+    constexpr int LDS = MODE == BOTH ? OUT : MODE;
+    static_assert(walk_lds<DT, KT, PT, LDS>(WAVES) <= 160 * 1024, "a chunk's tiles fit a compute unit");
+    const int lds = walk_lds<DT, KT, PT, LDS>(walk_heads(a.wblocks));
     auto* kernel = ssm_walk_kernel<DT, KT, PT, MODE>;
     const hipError_t e = allow_lds(kernel, lds);
     if (e != hipSuccess) return e;
@@ -1529,8 +1541,7 @@ template <typename DT, int KT, int PT> hipError_t backward(const SsmArgs& a, hip
         const Role f{a.x, a.B, a.C, a.xs, a.bs, a.cs, a.h0, nullptr, a.hs, a.ends, a.decay, 0};
         const Role b{a.dy, a.C, a.B, a.dys, a.cs, a.bs, a.dhT, a.dh0, a.gs, a.rends, a.rdecay, 1};
         SSM_TRY((starts<DT, KT, WT>(a, f, &b, st)));
-        SSM_TRY((walk<DT, KT, WT, EMIT>(a, f, nullptr, st)));
-        SSM_TRY((walk<DT, KT, WT, OUT | EMIT>(a, b, nullptr, st)));
+        SSM_TRY((walk<DT, KT, WT, BOTH>(a, b, &f, st)));
     }
     const int64_t slots = ssm_slots(a, a.chunk);
     if (a.T > 0) {
