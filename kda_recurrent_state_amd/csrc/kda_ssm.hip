@@ -25,10 +25,10 @@
 //     with two parts y took 1080 us where it takes 846, 2 x 32768 tokens);
 //   - fp32 inputs: everything in three parts, split as it is staged; products of parts below 2^-24 are left out.
 //
-// Per call: the segments' own states (ENDS), their join, and the walk proper.  The gradient does this twice, forwards for the
-// states before every chunk (EMIT) and backwards for dx and the derivatives behind every chunk, and then
-// has a kernel over chunks for what needs both.  2 x 32768 tokens of 32 heads of 128 x 128, bf16: 735 us (ENDS 185, join 18,
-// OUT 535); gradient of 2 x 8192: 985 us (below).
+// Per call: the segments' own states (ENDS), their join, and the walk proper.  The gradient does this in both directions side by
+// side, forwards for the states before every chunk (EMIT) and backwards for dx and the derivatives behind every
+// chunk, and then has a kernel over chunks for what needs both.  2 x 32768 tokens of 32 heads of 128 x 128, bf16: 735 us (ENDS
+// 185, join 18, OUT 535); gradient of 2 x 8192: 980 us (below).
 #include "kda_ssm.hpp"
 
 #include "kda_rows.hpp"
@@ -446,8 +446,9 @@ __device__ __forceinline__ double walk_decays(WalkDecays& w, ExactDecays* x, flo
 // workgroup that have the same head form the masked products once between them, in LDS.  Chunks of 32 tokens;
 // with bf16 inputs the next chunk's rows are on their way in registers while one is multiplied.
 //
-// Heads of a workgroup, whose first unit's number in the group is a multiple of four: two of two blocks each, and any more blocks leave
-// room for parts of two.  So two workgroups in fp32 share a compute unit (K <= 64: 70 KB, with room for four heads 90).
+// Heads of a workgroup, whose first unit's number in the group is a multiple of four: two of two blocks each, and any more
+// blocks leave room for parts of two.  So two workgroups in fp32 share a compute unit (K <= 64: 70 KB, with room for
+// four heads 90; forward and gradient of 6007 tokens of 10 heads of 40 x 50 242 us and 261).
 __host__ __device__ constexpr int walk_heads(int blocks) { return blocks == 1 ? WAVES : 2; }
 
 template <typename DT, int KT, int PT, int MODE>
@@ -837,7 +838,8 @@ __device__ __forceinline__ void walk_segment(const SsmArgs& a, const Role& role,
     }
 }
 
-// Two walks of one kind side by side, or (BOTH) the gradient's, which need nothing from each other: the longer first.
+// Two walks of one kind side by side, or (BOTH) the gradient's, which need nothing from each other: the longer first.  In one
+// launch each the 6007 tokens take 216 us, one after another 242 (ENDS and join together 230); 2 x 8192 979 and 994.
 constexpr int BOTH = 8;
 template <typename DT, int KT, int PT, int MODE>
 __global__ void __launch_bounds__(NT, sizeof(DT) == 2 ? 3 : 2)
@@ -927,8 +929,7 @@ __global__ void __launch_bounds__(NT) ssm_decay_kernel(SsmArgs a, int slots) {
 // registers), then a quarter of the columns of dB and dC, so no sum crosses wavefronts but those of single
 // numbers a token, which ssm_tokens_kernel puts together.
 //
-// 2 x 8192 tokens of 32 heads of 128 x 128, bf16: 415 us of 985 (walks 220 and 140, ENDS 2 x 73, joins 2 x 16, tokens 16,
-// decays 9, sums 4).  Vector issue 179 us (110e6 instructions), matrix 54, LDS 107 (66e6 cycles on 256 compute units), and
+// 2 x 8192 tokens of 32 heads of 128 x 128, bf16: 425 us of 980 (walks 355, ENDS 140, joins 30, tokens 17, decays 9, sums 4).  Vector issue 179 us (110e6 instructions), matrix 54, LDS 107 (66e6 cycles on 256 compute units), and
 // it reads 1.4 GB, most of it the chunks' states, 3.4 TB/s: no one resource, but the phases of a unit behind each other at
 // two wavefronts a SIMD.
 template <typename DT, int KT, int PT>
