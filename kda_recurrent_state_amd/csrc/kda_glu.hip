@@ -364,8 +364,11 @@ __global__ void __launch_bounds__(WM* WN * 64, 2) glu_gemm_kernel(GemmArgs g) {
     }
 }
 
-// out = sum of the shares, in order.  (777 x 1000 x 2731: 6 us of 320.)
-template <typename DT> __global__ void __launch_bounds__(256) glu_shares_kernel(const float* part, int split, int64_t n, DT* out) {
+// One output or two, each the sum of its shares, in order.  (777 x 1000 x 2731: 6 + 7 us of 300.)
+template <typename DT>
+__global__ void __launch_bounds__(256) glu_shares_kernel(const float* part, int split, int64_t n, DT* one, DT* two) {
+    DT* const out = blockIdx.y ? two : one;
+    part += blockIdx.y * split * n;
     for (int64_t i = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 4; i < n; i += (int64_t)gridDim.x * 1024) {
         if (i + 4 <= n) {
             f32x4 s = zero4();
@@ -386,11 +389,18 @@ template <typename DT> __global__ void __launch_bounds__(256) glu_shares_kernel(
     }
 }
 
-// [rows][cols] as NP planes of [rows][pad] bf16, zero past the columns.
-template <typename DT, int NP>
-__global__ void __launch_bounds__(256) glu_pack_kernel(const DT* src, int64_t stride, int64_t rows, int cols, int pad,
-                                                       int64_t plane, bf16* dst) {
-    const int per = pad / 4;
+// Up to three matrices, [rows][cols] each, as NP planes of [rows][pad] bf16, zero past the columns.
+struct PackArgs {
+    const void* src[3];
+    bf16* dst[3];
+    int64_t stride[3], rows[3];
+    int cols, pad;
+};
+template <typename DT, int NP> __global__ void __launch_bounds__(256) glu_pack_kernel(PackArgs a) {
+    const DT* src = (const DT*)a.src[blockIdx.y];
+    bf16* dst = a.dst[blockIdx.y];
+    const int64_t stride = a.stride[blockIdx.y], rows = a.rows[blockIdx.y], plane = rows * a.pad;
+    const int per = a.pad / 4, cols = a.cols;
     for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < rows * per; i += (int64_t)gridDim.x * 256) {
         const int64_t r = i / per;
         const int c = (int)(i % per) * 4;
@@ -400,7 +410,7 @@ __global__ void __launch_bounds__(256) glu_pack_kernel(const DT* src, int64_t st
         else
             for (int k = 0; k < 4; ++k)
                 if (c + k < cols) v[k] = to_f32(src[r * stride + c + k]);
-        store_planes<NP>(dst + r * pad + c, plane, v);
+        store_planes<NP>(dst + r * a.pad + c, plane, v);
     }
 }
 
@@ -602,19 +612,11 @@ hipError_t run_gemm(GemmArgs g, const Shape& s, hipStream_t st) {
     return launch_gemm<DT, 128, 64, 2, AKR, BKR, EPI, ACT>(g, blocks, st);
 }
 
-template <typename DT> hipError_t sum_shares(const float* part, int split, int64_t n, void* out, hipStream_t st) {
-    const int64_t blocks = (n / 4 + 256) / 256;
-    hipLaunchKernelGGL(glu_shares_kernel<DT>, dim3((unsigned)(blocks < 4096 ? blocks : 4096)), dim3(256), 0, st, part, split, n,
-                       (DT*)out);
-    return hipGetLastError();
-}
-
 template <typename DT>
-hipError_t pack(const void* src, int64_t stride, int64_t rows, int cols, int pad, bf16* dst, hipStream_t st) {
-    constexpr int NP = sizeof(DT) == 2 ? 1 : 3;
-    const int64_t blocks = (rows * (pad / 4) + 255) / 256;
-    hipLaunchKernelGGL((glu_pack_kernel<DT, NP>), dim3((unsigned)(blocks < 8192 ? blocks : 8192)), dim3(256), 0, st,
-                       (const DT*)src, stride, rows, cols, pad, rows * pad, dst);
+hipError_t sum_shares(const float* part, int split, int64_t n, void* one, void* two, hipStream_t st) {
+    const int64_t blocks = (n / 4 + 256) / 256;
+    hipLaunchKernelGGL(glu_shares_kernel<DT>, dim3((unsigned)(blocks < 4096 ? blocks : 4096), two ? 2 : 1), dim3(256), 0, st, part,
+                       split, n, (DT*)one, (DT*)two);
     return hipGetLastError();
 }
 
@@ -679,12 +681,28 @@ template <typename DT> hipError_t inputs(const GluArgs& a, const Work& w, Inputs
     in->wg = a.w_plain ? Mat{(const bf16*)a.wg, a.D, 0} : Mat{w.wg, pad, (int64_t)a.F * pad};
     in->wu = a.w_plain ? Mat{(const bf16*)a.wu, a.D, 0} : Mat{w.wu, pad, (int64_t)a.F * pad};
     if (a.T == 0) return hipSuccess;
-    if (!a.x_plain) GLU_TRY((pack<DT>(a.x, a.xs, a.T, a.D, pad, w.x, st)));
+    PackArgs p = {};
+    int n = 0;
+    int64_t most = 0;
+    auto add = [&](const void* src, int64_t stride, int64_t rows, bf16* dst) {
+        p.src[n] = src;
+        p.dst[n] = dst;
+        p.stride[n] = stride;
+        p.rows[n++] = rows;
+        most = rows > most ? rows : most;
+    };
+    if (!a.x_plain) add(a.x, a.xs, a.T, w.x);
     if (!a.w_plain) {
-        GLU_TRY((pack<DT>(a.wg, a.D, a.F, a.D, pad, w.wg, st)));
-        GLU_TRY((pack<DT>(a.wu, a.D, a.F, a.D, pad, w.wu, st)));
+        add(a.wg, a.D, a.F, w.wg);
+        add(a.wu, a.D, a.F, w.wu);
     }
-    return hipSuccess;
+    if (n == 0) return hipSuccess;
+    p.cols = a.D;
+    p.pad = pad;
+    const int64_t blocks = (most * (pad / 4) + 255) / 256;
+    hipLaunchKernelGGL((glu_pack_kernel<DT, sizeof(DT) == 2 ? 1 : 3>), dim3((unsigned)(blocks < 8192 ? blocks : 8192), n),
+                       dim3(256), 0, st, p);
+    return hipGetLastError();
 }
 
 // x against both weights, with EPI
@@ -769,7 +787,7 @@ template <typename DT, int ACT> hipError_t backward(const GluArgs& a, hipStream_
         p.part = w.part;
         const Shape s = dx_shape(a);
         GLU_TRY((run_gemm<DT, false, true, EPI_OUT, 0>(p, s, st)));
-        if (s.split > 1) GLU_TRY((sum_shares<DT>(w.part, s.split, a.T * a.D, a.dx, st)));
+        if (s.split > 1) GLU_TRY((sum_shares<DT>(w.part, s.split, a.T * a.D, a.dx, nullptr, st)));
     }
     GemmArgs p = {};
     for (int i = 0; i < n; ++i) {
@@ -793,11 +811,7 @@ template <typename DT, int ACT> hipError_t backward(const GluArgs& a, hipStream_
     p.part = w.part;
     const Shape s = dw_shape(a);
     GLU_TRY((run_gemm<DT, true, true, EPI_OUT, 0>(p, s, st)));
-    if (s.split > 1) {
-        const int64_t one = (int64_t)a.F * a.D;
-        GLU_TRY((sum_shares<DT>(w.part, s.split, one, a.dwg, st)));
-        GLU_TRY((sum_shares<DT>(w.part + s.split * one, s.split, one, a.dwu, st)));
-    }
+    if (s.split > 1) GLU_TRY((sum_shares<DT>(w.part, s.split, (int64_t)a.F * a.D, a.dwg, a.dwu, st)));
     return hipSuccess;
 }
 
