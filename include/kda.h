@@ -617,9 +617,9 @@ KDA_API int kda_residual_norm_bwd_workspace_size(const kda_residual_norm_dims_t*
  * operators above; the states have the layout of the state layer's, [K, P] per head.
  *   - A is <= 0 and d >= 0 (not checked); any decay is exact to rounding.
  *   - States, and the derivatives of dt, A, D, dt_bias and h0, are sums in fp32 of products to 2^-24.
- *     y, dx, dB and dC of bf16 inputs are sums in fp32 too, of terms with one factor that was rounded to
- *     bf16 (masked products, the state): within 2^-8 of the sum of the terms' magnitudes.  fp32 inputs are
- *     multiplied as sums of three bf16 parts, to 2^-24 of a product.
+ *     y and dx of bf16 inputs are sums in fp32 too, of terms with one factor that was rounded to bf16
+ *     (masked products, the state): within 2^-8 of the sum of the terms' magnitudes; dB and dC within
+ *     2^-18.  fp32 inputs are multiplied as sums of three bf16 parts, to 2^-24 of a product.
  *   - Inputs are finite.  A non-finite value stays in its own sequence.  It may reach outputs up to
  *     63 tokens before it, and be lost behind decays whose product is zero in float32.
  * ------------------------------------------------------------------------- */

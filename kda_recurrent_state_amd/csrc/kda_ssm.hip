@@ -19,16 +19,18 @@
 // Matrix cores take bf16 operands.  bf16 inputs go in as they are; what is computed in fp32 and is an operand again goes in as
 // a sum of bf16 parts, each the rounding of what the parts before it left: three hold a value to 2^-26 of itself.
 //   - states, and what the derivatives of dt, A and h0 are sums of: three parts;
-//   - y, dx, dB and dC with bf16 inputs: the masked products and (in y and dx) the state are rounded to bf16 once.  Every
-//     term of such a result has one of them as a factor, so the result is off by at most 2^-8 of the
-//     sum of its terms' magnitudes, about what its own rounding costs (measured against 64 bits 1.8e-3, rounding alone 1.7e-3;
-//     with two parts y took 1080 us where it takes 846, 2 x 32768 tokens);
+//   - y and dx with bf16 inputs: the masked products and the state are rounded to bf16 once.  Every term of such a
+//     result has one of them as a factor, so the result is off by at most 2^-8 of the sum of its terms' magnitudes,
+//     about what its own rounding costs (measured against 64 bits 1.8e-3 to 2.2e-3, rounding alone 1.7e-3; with two
+//     parts the forward of 2 x 32768 tokens took 1080 us where it took 846 with one);
+//   - dB and dC with bf16 inputs: two parts of the masked products.  They sum heads whose terms cancel: with one part 2.7e-3
+//     against 64 bits where rounding alone is 1.7e-3, and with two 1.7e-3 (gradient of 2 x 8192 980 us and 1025);
 //   - fp32 inputs: everything in three parts, split as it is staged; products of parts below 2^-24 are left out.
 //
 // Per call: the segments' own states (ENDS), their join, and the walk proper.  The gradient does this in both directions side by
 // side, forwards for the states before every chunk (EMIT) and backwards for dx and the derivatives behind every
 // chunk, and then has a kernel over chunks for what needs both.  2 x 32768 tokens of 32 heads of 128 x 128, bf16: 735 us (ENDS
-// 185, join 18, OUT 535); gradient of 2 x 8192: 980 us (below).
+// 185, join 18, OUT 535); gradient of 2 x 8192: 1025 us (below).
 #include "kda_ssm.hpp"
 
 #include "kda_rows.hpp"
@@ -41,10 +43,10 @@ constexpr int NT = WAVES * WAVE;
 constexpr int WALK = 32;  // tokens of a chunk of the walk
 
 template <typename DT> struct Cfg;
-// QT: 16-token tiles of a chunk; parts of inputs (NP), of the masked products (MP), of the state where it is an
-// operand of a result (HP)
-template <> struct Cfg<bf16> { static constexpr int QT = 4, NP = 1, MP = 1, HP = 1; };
-template <> struct Cfg<float> { static constexpr int QT = 2, NP = 3, MP = 3, HP = 3; };
+// QT: 16-token tiles of a chunk; parts of inputs (NP), of the masked products in the walk (MP) and in dB and dC (GP),
+// of the state where it is an operand of a result (HP)
+template <> struct Cfg<bf16> { static constexpr int QT = 4, NP = 1, MP = 1, HP = 1, GP = 2; };
+template <> struct Cfg<float> { static constexpr int QT = 2, NP = 3, MP = 3, HP = 3, GP = 3; };
 
 template <int V> struct Int { static constexpr int value = V; };
 typedef short s16x4 __attribute__((ext_vector_type(4)));
@@ -929,13 +931,13 @@ __global__ void __launch_bounds__(NT) ssm_decay_kernel(SsmArgs a, int slots) {
 // registers), then a quarter of the columns of dB and dC, so no sum crosses wavefronts but those of single
 // numbers a token, which ssm_tokens_kernel puts together.
 //
-// 2 x 8192 tokens of 32 heads of 128 x 128, bf16: 425 us of 980 (walks 355, ENDS 140, joins 30, tokens 17, decays 9, sums 4).  Vector issue 179 us (110e6 instructions), matrix 54, LDS 107 (66e6 cycles on 256 compute units), and
+// 2 x 8192 tokens of 32 heads of 128 x 128, bf16: 470 us of 1025 (walks 355, ENDS 140, joins 30, tokens 17, decays 9, sums 4).  Vector issue 179 us (110e6 instructions), matrix 54, LDS 107 (66e6 cycles on 256 compute units), and
 // it reads 1.4 GB, most of it the chunks' states, 3.4 TB/s: no one resource, but the phases of a unit behind each other at
 // two wavefronts a SIMD.
 template <typename DT, int KT, int PT>
 __global__ void __launch_bounds__(NT, 2) ssm_grad_kernel(SsmArgs a, int slots, int quads) {
     using C_ = Cfg<DT>;
-    constexpr int QT = C_::QT, Q = QT * 16, NP = C_::NP, MP = C_::MP;
+    constexpr int QT = C_::QT, Q = QT * 16, NP = C_::NP, MP = C_::GP;
     constexpr int LDK = KT * 16 + 8, LDP = PT * 16 + 8, LDQ = Q + 8, PLK = Q * LDK, PLP = Q * LDP, PLQ = Q * LDQ;
     constexpr int KW = KT < WAVES ? 1 : KT / WAVES;  // column tiles of a wavefront
     using Sums = GradSums<Q>;
@@ -1485,7 +1487,7 @@ template <typename DT, int KT, int PT, int MODE> constexpr int walk_lds(int head
 }
 template <typename DT, int KT, int PT> constexpr int grad_lds() {
     constexpr int Q = Cfg<DT>::QT * 16, NP = Cfg<DT>::NP;
-    return (2 * NP * Q * (KT * 16 + 8) + 2 * NP * Q * (PT * 16 + 8) + Cfg<DT>::MP * Q * (Q + 8)) * 2 +
+    return (2 * NP * Q * (KT * 16 + 8) + 2 * NP * Q * (PT * 16 + 8) + Cfg<DT>::GP * Q * (Q + 8)) * 2 +
            (int)sizeof(Decays<Q>) + (int)sizeof(GradSums<Q>);
 }
 

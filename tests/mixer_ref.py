@@ -11,10 +11,11 @@ term's absolute value.  What may be off, relative to a term:
                  7.4 u times the same sum with half the decay.
   parts          a value in three bf16 parts is held to 2^-26; products of parts below 2^-24 left out: 4 u.
   bf16 results   y and dx are sums of products with the masked weights (C . B) decay d, and with the state; both
-                 are held in fp32 and rounded once to bf16 as operands, as dB's and dC's weights are.
+                 are held in fp32 and rounded once to bf16 as operands.
                  Each term of the sum has one of them as a factor, so it is off by at most half a
-                 step of bf16, 2^-8 = 2^16 u, relative: 2^16 mag in all, whatever the number of terms.  States,
-                 dt, A, D and h0's gradients do not pass such a rounding.
+                 step of bf16, 2^-8 = 2^16 u, relative: 2^16 mag in all, whatever the number of terms.  dB's and dC's
+                 masked weights go in as two parts, which hold them to 2^-18 = 64 u.  States, dt, A, D and
+                 h0's gradients do not pass such a rounding.
   sums           one rounding an addition.  A chunk adds 32 products in each of 6 instructions to a state
                  tile: 192 roundings in a chunk of 32 tokens (fp32), the same in 64 (bf16): at most 6 u a
                  token.  A result adds K state rows (6 products each in fp32) and a chunk's 64 tokens;
@@ -125,7 +126,7 @@ def ssm_grad_bounds(x, z, A, B, C, D, bias, h0, cu, dy, dhT, soft=True, dtype=to
     for k in val:
         bound[k] = R * full[k] + 16 * half[k]
         if dtype != torch.float32 and k in ("dx", "dB", "dC"):
-            bound[k] = bound[k] + BF_OPERAND * full[k]
+            bound[k] = bound[k] + (BF_OPERAND if k == "dx" else 64) * full[k]
     # The derivative of a log decay is a sum over pairs of tokens around it, formed as running sums of the chunk's
     # row and column sums, in which every other pair cancels: the same products are in both, but the additions
     # and factors behind them (64 + 16 roundings of a row's, of a column's sum) are not.
