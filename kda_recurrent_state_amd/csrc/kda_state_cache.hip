@@ -16,18 +16,6 @@ namespace {
 
 constexpr int NT = 256;
 
-// The quotient x / s, s > 0, as a number on the same side of every border between two codes.  The division is correctly
-// rounded to fp32; where it lands on a border without being one, the sign of the remainder says which side x / s is on.
-// (Every border has at most 12 significant bits, so a quotient with more is none.)
-__device__ __forceinline__ float beside_border(float x, float s) {
-    const float q = x / s;
-    const uint32_t b = __float_as_uint(q);
-    if ((b & 0xfffu) == 0) {
-        const float rest = fmaf(-q, s, x);
-        if (rest != 0.f) return __uint_as_float((rest > 0.f) == (q > 0.f) ? b + 1 : b - 1);
-    }
-    return q;
-}
 __device__ __forceinline__ uint32_t pack_i8(const float (&q)[4]) {  // whole numbers or NaN (a scale that is no number: 0 x scale is NaN)
     uint32_t w = 0;
 #pragma unroll

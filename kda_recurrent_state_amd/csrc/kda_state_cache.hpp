@@ -1,4 +1,4 @@
-// kda_state_cache.hpp -- host-side launcher of the 8-bit state cache.
+// kda_state_cache.hpp -- host-side launcher of the 8-bit state cache, and the quotient that its codes are taken from.
 #pragma once
 
 #include <hip/hip_runtime.h>
@@ -19,5 +19,19 @@ struct StateCacheArgs {
     int32_t width, format;   // 0: int8, 1: e4m3
 };
 hipError_t launch_state_cache(const StateCacheArgs& a, bool write, hipStream_t st);
+
+// The quotient x / s, s > 0, as a number on the same side of every border between two codes.  The division is correctly
+// rounded to fp32; where it lands on a border without being one, the sign of the remainder says which side x / s is on.
+// (Every border has at most 12 significant bits, so a quotient with more is none; nor is zero, to which a quotient
+// below the least fp32 number is rounded.)
+__host__ __device__ inline float beside_border(float x, float s) {
+    const float q = x / s;
+    const uint32_t b = __builtin_bit_cast(uint32_t, q);
+    if ((b & 0xfffu) == 0 && q != 0.f) {
+        const float rest = __builtin_fmaf(-q, s, x);
+        if (rest != 0.f) return __builtin_bit_cast(float, (rest > 0.f) == (q > 0.f) ? b + 1 : b - 1);
+    }
+    return q;
+}
 
 }  // namespace kda
