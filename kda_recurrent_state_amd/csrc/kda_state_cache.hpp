@@ -23,8 +23,13 @@ hipError_t launch_state_cache(const StateCacheArgs& a, bool write, hipStream_t s
 // The quotient x / s, s > 0, as a number on the same side of every border between two codes.  The division is correctly
 // rounded to fp32; where it lands on a border without being one, the sign of the remainder says which side x / s is on.
 // (Every border has at most 12 significant bits, so a quotient with more is none; nor is zero, to which a quotient
-// below the least fp32 number is rounded.)
+// below the least fp32 number is rounded.)  A remainder can be 2^-22 of the scale (a step of s times half a code), which a
+// small scale would leave below fp32's range: it and x, at most 448 of it, are moved up by a power of two.
 __host__ __device__ inline float beside_border(float x, float s) {
+    if (s < 0x1p-60f) {
+        s *= 0x1p64f;
+        x *= 0x1p64f;
+    }
     const float q = x / s;
     const uint32_t b = __builtin_bit_cast(uint32_t, q);
     if ((b & 0xfffu) == 0 && q != 0.f) {

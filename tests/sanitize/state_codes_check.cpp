@@ -46,7 +46,10 @@ static int check(float x, float s, const std::vector<float>& all) {
 
 int main() {
     const std::vector<float> i8 = borders(false), f8 = borders(true);
-    const float scales[] = {0.7f, 1.f, 1.1f, 777.7f, 2.23f, 2.2e7f, 3.3e-5f, 1.9e30f, 2.3e-30f, 7e35f};
+    // the least scales, those around the least normal number, and ordinary ones
+    const float scales[] = {0x1p-149f, 0x1.8p-148f, 0x1p-140f, 0x1.fffffcp-127f, 0x1p-126f, 0x1.000002p-126f, 0x1.aaaaaap-126f,
+                            0x1.23456p-125f, 0x1.fffffep-124f, 0x1.555556p-120f, 0x1.fffffep-61f, 0x1.000002p-60f, 0.7f, 1.f, 1.1f, 777.7f,
+                            2.23f, 2.2e7f, 3.3e-5f, 1.9e30f, 2.3e-30f, 7e35f};
     int bad = 0;
     for (float s : scales) {
         for (const auto* b : {&i8, &f8})

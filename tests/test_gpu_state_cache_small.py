@@ -38,3 +38,23 @@ def test_quotients_that_underflow(fmt):
                     rows.append([most, 0.0, 0.0, 0.0] + quad[k:] + quad[:k])
                 rows.append([most, most * small, tiny, -tiny] + [0.0] * 4)
     same_codes(torch.tensor(rows, dtype=torch.float32), fmt)
+
+
+@pytest.mark.parametrize("fmt", FORMATS)
+def test_borders_of_small_scales(fmt):
+    """Values on and beside the middles between neighbouring codes where the scale is the least number, subnormal or
+    just above, so that the quotient's remainder is below what float32 holds."""
+    log(f"state cache, borders of small scales {fmt}")
+    values, _ = M.formats(fmt)
+    mid = (values[1:] + values[:-1]) / 2
+    rows = []
+    for s in (2.0 ** -149, 2.0 ** -140 + 2.0 ** -149, 2.0 ** -126, 2.0 ** -126 + 2.0 ** -149, 1.7 * 2.0 ** -126, 1.1 * 2.0 ** -125,
+              1.3 * 2.0 ** -120, 1.9 * 2.0 ** -61):
+        most = (values[-1] * s).float()
+        v = (mid * s).float()
+        for step in range(-3, 4):
+            w = v.clone()
+            for _ in range(abs(step)):
+                w = torch.nextafter(w, torch.full_like(w, 1.0 if step > 0 else -1.0))
+            rows.append(torch.cat([w, most[None]]))
+    same_codes(torch.stack(rows), fmt)
