@@ -26,17 +26,13 @@ hipError_t launch_state_cache(const StateCacheArgs& a, bool write, hipStream_t s
 // below the least fp32 number is rounded.)  A remainder can be 2^-22 of the scale (a step of s times half a code), which a
 // small scale would leave below fp32's range: it and x, at most 448 of it, are moved up by a power of two.
 __host__ __device__ inline float beside_border(float x, float s) {
-    if (s < 0x1p-60f) {
-        s *= 0x1p64f;
-        x *= 0x1p64f;
-    }
-    const float q = x / s;
+    const float up = s < 0x1p-60f ? 0x1p64f : 1.f;
+    x *= up;
+    s *= up;
+    const float q = x / s, rest = __builtin_fmaf(-q, s, x);
     const uint32_t b = __builtin_bit_cast(uint32_t, q);
-    if ((b & 0xfffu) == 0 && q != 0.f) {
-        const float rest = __builtin_fmaf(-q, s, x);
-        if (rest != 0.f) return __builtin_bit_cast(float, (rest > 0.f) == (q > 0.f) ? b + 1 : b - 1);
-    }
-    return q;
+    const bool beside = (b & 0xfffu) == 0 && (b << 1) != 0 && rest != 0.f;
+    return __builtin_bit_cast(float, b + (beside ? (rest > 0.f) == (q > 0.f) ? 1u : ~0u : 0u));
 }
 
 }  // namespace kda
