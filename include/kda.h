@@ -621,7 +621,8 @@ KDA_API int kda_residual_norm_bwd_workspace_size(const kda_residual_norm_dims_t*
  *     (masked products, the state): within 2^-8 of the sum of the terms' magnitudes; dB and dC within
  *     2^-18.  fp32 inputs are multiplied as sums of three bf16 parts, to 2^-24 of a product.
  *   - Inputs are finite.  A non-finite value stays in its own sequence.  It may reach outputs up to
- *     63 tokens before it, and be lost behind decays whose product is zero in float32.
+ *     63 tokens before it, and be lost behind decays whose product is zero in float32.  A NaN in a
+ *     head's A, dt_bias or D makes the results of that head NaN that read it, as in single steps.
  * ------------------------------------------------------------------------- */
 typedef struct {
     int32_t num_seqs;      /* N */

@@ -234,6 +234,11 @@ template <typename DT, int ROWS, int COLS, int THREADS> struct Stage {
     }
 };
 
+// d A in units of log 2, held above -300; a NaN stays one.
+__device__ __forceinline__ double log2_decay(float d, float A) {
+    const double l = (double)d * (double)A * 1.4426950408889634;
+    return l < -300.0 ? -300.0 : l;
+}
 __device__ __forceinline__ float softplus_f(float z) { return fmaxf(z, 0.f) + log1pf(expf(-fabsf(z))); }
 
 __device__ __forceinline__ double lanes_scan(double v, int lane) {
@@ -257,7 +262,7 @@ __device__ __forceinline__ void decays(Decays<Q>& w, const SsmArgs& a, int h, in
     if (lane < n) {
         const float z = a.dt[(int64_t)(first + lane) * a.dts + h] + (a.bias ? a.bias[h] : 0.f);
         d = a.softplus ? softplus_f(z) : z;
-        l = fmax((double)d * (double)a.A[h] * 1.4426950408889634, -300.0);
+        l = log2_decay(d, a.A[h]);
     }
     const double c = lanes_scan(l, lane), total = __shfl(c, WAVE - 1);
     if (lane < Q) {
@@ -402,7 +407,7 @@ __device__ __forceinline__ double walk_decays(WalkDecays& w, ExactDecays* x, flo
                                               bool rev, double behind, float sign, int lane) {
     const int u = lane & (WALK - 1);
     const float d = in ? (softplus ? softplus_f(z) : z) : 0.f;
-    const double l = in ? fmax((double)d * (double)A * 1.4426950408889634, -300.0) : 0.0;
+    const double l = in ? log2_decay(d, A) : 0.0;
     double incl = l;
 #pragma unroll
     for (int m = 1; m < WALK; m <<= 1) {
