@@ -390,20 +390,17 @@ __device__ __forceinline__ void lds_barrier() { asm volatile("s_waitcnt lgkmcnt(
 
 // The decays of a chunk of the walk, for the wavefronts of a head.
 struct WalkDecays {
-    float from[WALK], into[WALK], scale[WALK], c[WALK], less[WALK];
-    // from: 2^{c}; into: 2^{total - c} src; scale: weight of a token's result (1, reversed d); less: c - log2(src),
-    // src the weight of its product (d, reversed 1)
+    float from[WALK], into[WALK], scale[WALK], hi[WALK], lo[WALK], less[WALK];
+    // from: 2^{c}; into: 2^{total - c} src, src the weight of a token's product (d, reversed 1); scale: that of its result
+    // (1, reversed d); c is hi + lo; less: lo - log2(src), fp32 inputs: src
     float total, pad[3];  // 2^{total} (BEHIND: the log decay of the chunks behind this one)
-};
-struct ExactDecays {  // fp32 only: c as hi + lo
-    float hi[WALK], lo[WALK], src[WALK];
 };
 
 // Two chunks at once, 32 tokens each, a token a lane; returns the sum of both chunks' log decays.
 // BEHIND: `into` is the weight at the end of the segment, `behind` the log decay of the chunks behind these; `sign` is the
 // sign of the sum it goes to.  Otherwise the state changes its sign with every chunk, and is negative before odd ones.
 template <bool EXACT, bool BEHIND>
-__device__ __forceinline__ double walk_decays(WalkDecays& w, ExactDecays* x, float z, float A, int softplus, bool in,
+__device__ __forceinline__ double walk_decays(WalkDecays& w, float z, float A, int softplus, bool in,
                                               bool rev, double behind, float sign, int lane) {
     const int u = lane & (WALK - 1);
     const float d = in ? (softplus ? softplus_f(z) : z) : 0.f;
@@ -427,15 +424,12 @@ __device__ __forceinline__ double walk_decays(WalkDecays& w, ExactDecays* x, flo
     w.from[u] = exp2f((float)c) * odd;
     w.into[u] = exp2f((float)(total - c)) * (src * -odd);
     w.scale[u] = rev ? d : 1.f;
-    w.c[u] = (float)c;
-    w.less[u] = (float)(c - (double)__log2f(src));
+    const double hi = rint(c * 256.0) * (1.0 / 256.0);
+    const float lo = (float)(c - hi);
+    w.hi[u] = (float)hi;
+    w.lo[u] = lo;
+    w.less[u] = EXACT ? src : lo - __log2f(src);
     if (u == 0) w.total = -exp2f((float)total);
-    if (EXACT) {
-        const double hi = rint(c * 256.0) * (1.0 / 256.0);
-        x->hi[u] = (float)hi;
-        x->lo[u] = (float)(c - hi);
-        x->src[u] = src;
-    }
     return total + __shfl_xor(total, WALK);
 }
 
@@ -479,7 +473,6 @@ __device__ __forceinline__ void walk_segment(const SsmArgs& a, const Role& role,
     char* const smasked = svals + WAVES * VALS;
     const int heads = walk_heads(a.wblocks);  // that a workgroup may have
     WalkDecays* const sdec = reinterpret_cast<WalkDecays*>(smasked + heads * MASKED);  // [head][chunk & 3]
-    ExactDecays* const sexact = reinterpret_cast<ExactDecays*>(sdec + 4 * heads);
 
     const int lane = threadIdx.x % WAVE, wave = __builtin_amdgcn_readfirstlane(threadIdx.x / WAVE);
     const int l15 = lane & 15, q4 = lane >> 4;
@@ -514,7 +507,6 @@ __device__ __forceinline__ void walk_segment(const SsmArgs& a, const Role& role,
     const int own = mine ? __builtin_popcount(leads & ((1 << lead) - 1)) : 0;  // the head's number in the workgroup
     char* const sm = smasked + own * MASKED;
     WalkDecays* const dec = sdec + 4 * own;
-    ExactDecays* const exact = sexact + 4 * own;
     f32x4 st[KT][PT];
 #pragma unroll
     for (int k = 0; k < KT; ++k)
@@ -582,7 +574,7 @@ __device__ __forceinline__ void walk_segment(const SsmArgs& a, const Role& role,
         const bool in = ci + (lane >> 5) < chunks && (lane & 31) < c.n;
         const int to = (ci & 2) + (lane >> 5);
         const float sign = ci + (lane >> 5) < turn ? -1.f : 1.f;
-        log_decay += walk_decays<NP != 1, (MODE & ENDS) != 0>(dec[to], &exact[to], raw + bias, A, a.softplus, in, rev, log_decay, sign, lane);
+        log_decay += walk_decays<NP != 1, (MODE & ENDS) != 0>(dec[to], raw + bias, A, a.softplus, in, rev, log_decay, sign, lane);
     };
 
     Stage<DT, Q, KT * 16, NT> bk, bq;
@@ -671,19 +663,16 @@ __device__ __forceinline__ void walk_segment(const SsmArgs& a, const Role& role,
                         s = mma_parts(kf, qf, s);
                     }
                     float v[4];
+                    const float hi_t = w.hi[t], lo_t = w.lo[t];
+                    const f32x4 hi = *reinterpret_cast<const f32x4*>(&w.hi[s0]), less = *reinterpret_cast<const f32x4*>(&w.less[s0]);
                     if constexpr (NP == 1) {
-                        const f32x4 less = *reinterpret_cast<const f32x4*>(&w.less[s0]);
-                        const float ct = w.c[t];
 #pragma unroll
-                        for (int r = 0; r < 4; ++r) v[r] = s[r] * __builtin_amdgcn_exp2f(ct - less[r]);
+                        for (int r = 0; r < 4; ++r) v[r] = s[r] * __builtin_amdgcn_exp2f((hi_t - hi[r]) + (lo_t - less[r]));
                     } else {
-                        const ExactDecays& x_ = exact[ci & 3];
-                        const f32x4 hi = *reinterpret_cast<const f32x4*>(&x_.hi[s0]);
-                        const f32x4 lo = *reinterpret_cast<const f32x4*>(&x_.lo[s0]);
-                        const f32x4 src = *reinterpret_cast<const f32x4*>(&x_.src[s0]);
+                        const f32x4 lo = *reinterpret_cast<const f32x4*>(&w.lo[s0]);
 #pragma unroll
                         for (int r = 0; r < 4; ++r)
-                            v[r] = s[r] * (__builtin_amdgcn_exp2f((x_.hi[t] - hi[r]) + (x_.lo[t] - lo[r])) * src[r]);
+                            v[r] = s[r] * (__builtin_amdgcn_exp2f((hi_t - hi[r]) + (lo_t - lo[r])) * less[r]);
                     }
                     if (I[x] == J[x]) {
 #pragma unroll
@@ -1488,7 +1477,7 @@ template <typename DT, int KT, int PT, int MODE> constexpr int walk_lds(int head
     constexpr int NP = Cfg<DT>::NP;
     return NP * WALK * ((MODE & OUT ? 2 : 1) * KT * 32 + WAVES * PT * 32) +
            heads * ((MODE & OUT ? Cfg<DT>::MP * WALK * WALK * 2 : 0) +
-                    4 * ((int)sizeof(WalkDecays) + (NP == 1 ? 0 : (int)sizeof(ExactDecays))));
+                    4 * (int)sizeof(WalkDecays));
 }
 template <typename DT, int KT, int PT> constexpr int grad_lds() {
     constexpr int Q = Cfg<DT>::QT * 16, NP = Cfg<DT>::NP;

@@ -3,8 +3,9 @@ import pytest
 import torch
 
 import kda_recurrent_state_amd as kda
+from tests import mixer_ref as M
 from tests.parity import log
-from tests.test_gpu_ssm import BF, DEV, F4, call, cud, dev, grad, make
+from tests.test_gpu_ssm import BF, DEV, F4, call, cpu8, cud, dev, grad, make
 
 pytestmark = pytest.mark.gpu
 
@@ -38,3 +39,29 @@ def test_a_nan_parameter_is_its_heads(lengths, name, dtype):
         ys, _ = kda.ssm_step(bad["x"][:1], bad["dt"][:1], bad["A"], bad["B"][:1], bad["C"][:1], hs, bad["D"], bad["dt_bias"])
         assert torch.isnan(ys[:, 2]).all() and torch.isnan(hs[:, 2]).all()
         assert torch.isfinite(ys[:, keep]).all() and torch.isfinite(hs[:, keep]).all()
+
+
+def steep(H=512, T=96, seed=32):
+    """Decays of 2^-100 and less: sums of log decays in the thousands, whose differences are what the weights are made
+    of.  A token's result is its own weight C d, just above the middle between two bf16 numbers, plus a part of x that puts
+    a weight rounded down just below such a middle again: an exponent off by 2^-11 costs a whole step twice."""
+    g = torch.Generator().manual_seed(seed)
+    r = lambda *s: torch.rand(*s, generator=g)
+    C = (1 + r(T, 1, 1)).to(BF)
+    d = (1 + 2.0 ** -8 + 2e-4 + 2e-4 * r(T, H)) / C.float()[:, 0]
+    return dict(x=torch.ones(T, H, 1, dtype=BF), dt=d, A=-(140 + 60 * r(H)), B=torch.ones(T, 1, 1, dtype=BF), C=C,
+                D=torch.full((H,), 2.0 ** -8 - 2.0 ** -16), dt_bias=torch.zeros(H), h0=torch.zeros(1, H, 1, 1))
+
+
+def test_weights_behind_steep_decays():
+    log("ssm, weights behind steep decays")
+    v = steep()
+    val, bnd = M.ssm_bounds(*cpu8(v), [0, 96], soft=False, dtype=BF)
+    y, h = call(dev(v), softplus=False)
+    M.check(y, val["y"], bnd["y"], "y"), M.check(h, val["h"], bnd["h"], "h_T")
+    # mild tokens behind steep ones, which see each other
+    mild = torch.arange(96) % 32 >= 20
+    v["dt"][mild] *= 2.0 ** -9
+    val, bnd = M.ssm_bounds(*cpu8(v), [0, 96], soft=False, dtype=BF)
+    y, h = call(dev(v), softplus=False)
+    M.check(y, val["y"], bnd["y"], "y"), M.check(h, val["h"], bnd["h"], "h_T")
