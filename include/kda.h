@@ -672,7 +672,7 @@ KDA_API int kda_ssm_bwd(const kda_ssm_dims_t* dims, const void* x, const float* 
 KDA_API int kda_ssm_workspace_size(const kda_ssm_dims_t* dims, int backward, size_t* bytes);
 
 /* One token per sequence: y [N, H, P] and the state after it, from x [N, H, P], B, C [N, G, K], dt [N, H]
- * and h_in [N, H, K, P]; h_out may equal h_in. */
+ * and h_in [N, H, K, P]; h_out may equal h_in, and is refused on any other tensor of the call. */
 KDA_API int kda_ssm_step(const kda_ssm_dims_t* dims, const void* x, const float* dt, const float* A, const void* B,
                          const void* C, const float* D, const float* dt_bias, const float* h_in, float* h_out, void* y,
                          void* stream);
@@ -682,8 +682,8 @@ KDA_API int kda_ssm_step(const kda_ssm_dims_t* dims, const void* x, const float*
  * projections of x, B and C, whose convolution (kda_conv_step's, with conv_width taps and
  * conv_activation) is not rounded before the scan takes it.  conv_weight [channels, conv_width]
  * and conv_bias [channels] float32 (NULL for zeros); conv_state_in and conv_state_out
- * [N, conv_width - 1, channels] dtype, which may be equal.  dims' b_stride and c_stride are not
- * read; x_stride is xbc's.
+ * [N, conv_width - 1, channels] dtype, which may be equal; on any other tensor of the call conv_state_out and
+ * h_out are refused.  dims' b_stride and c_stride are not read; x_stride is xbc's.
  */
 KDA_API int kda_ssm_conv_step(const kda_ssm_dims_t* dims, int conv_width, int conv_activation, const void* xbc,
                               const float* conv_weight, const float* conv_bias, const void* conv_state_in,

@@ -73,6 +73,32 @@ inline int check_workspace(const void* ws, size_t have, size_t need) {
     return KDA_OK;
 }
 
+// A tensor of a call: `tokens` of `bytes` bytes each, `step` bytes from one to the next.
+struct Extent {
+    const char* name;
+    const void* p;  // may be null
+    int64_t tokens, step, bytes;
+};
+inline Extent whole(const char* name, const void* p, int64_t bytes) { return {name, p, 1, bytes, bytes}; }
+
+// Whether the tensor has a byte in [a, b); what lies between its tokens is not its own.
+inline bool touches(const Extent& t, uintptr_t a, uintptr_t b) {
+    const uintptr_t lo = (uintptr_t)t.p;
+    if (!t.p || t.tokens <= 0 || lo >= b) return false;
+    if (lo + (uintptr_t)t.bytes > a) return true;  // the first token
+    const uintptr_t first = (a - lo - (uintptr_t)t.bytes) / (uintptr_t)t.step + 1;  // the first that ends behind a
+    return first < (uintptr_t)t.tokens && lo + first * (uintptr_t)t.step < b;
+}
+
+// An output that lies on a tensor of the call that it may not (others[0 .. count)) is refused.
+inline int check_apart(const char* name, const void* out, int64_t bytes, const Extent* others, int count) {
+    const uintptr_t a = (uintptr_t)out, b = a + (uintptr_t)bytes;
+    for (int i = 0; i < count; ++i)
+        if (others[i].p != nullptr && touches(others[i], a, b))
+            return fail(KDA_ERR_INVALID_ARGUMENT, "%s overlaps %s", name, others[i].name);
+    return KDA_OK;
+}
+
 inline int hip_status(hipError_t e, const char* what) {
     if (e != hipSuccess) return fail(KDA_ERR_HIP, "%s launch: %s", what, hipGetErrorString(e));
     return ok();

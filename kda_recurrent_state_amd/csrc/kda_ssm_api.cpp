@@ -223,6 +223,12 @@ kda::SsmStepArgs step_args(const kda_ssm_dims_t* d, const float* dt, const float
     return a;
 }
 
+int64_t state_bytes(const kda::SsmStepArgs& a) { return (int64_t)a.N * a.H * a.K * a.P * 4; }
+Extent dt_extent(const kda::SsmStepArgs& a) { return {"dt", a.dt, a.N, a.dts * 4, 4ll * a.H}; }
+Extent y_extent(const kda::SsmStepArgs& a) { return whole("y", a.y, (int64_t)a.N * a.H * a.P * esize(a.dtype)); }
+// A state may be updated in place.
+Extent h_in_extent(const kda::SsmStepArgs& a) { return whole("h_in", a.h_in == a.h_out ? nullptr : a.h_in, state_bytes(a)); }
+
 }  // namespace
 
 int kda_ssm_step(const kda_ssm_dims_t* d, const void* x, const float* dt, const float* A, const void* B, const void* C,
@@ -239,6 +245,11 @@ int kda_ssm_step(const kda_ssm_dims_t* d, const void* x, const float* dt, const 
     const char* names[] = {"x", "B", "C"};
     const int align[] = {e, e, e};
     KDA_TRY(check_ptrs(ptrs, names, align, 3));
+    const int64_t state = state_bytes(a), gk = (int64_t)a.G * a.K * e;
+    const Extent others[] = {{"x", x, a.N, a.xs * e, (int64_t)a.H * a.P * e}, {"B", B, a.N, a.bs * e, gk},
+                             {"C", C, a.N, a.cs * e, gk}, dt_extent(a), whole("A", A, 4ll * a.H), whole("D", D, 4ll * a.H),
+                             whole("dt_bias", dt_bias, 4ll * a.H), y_extent(a), h_in_extent(a)};
+    KDA_TRY(check_apart("h_out", h_out, state, others, 9));
     a.x = x; a.B = B; a.C = C;
     return hip_status(kda::launch_ssm_step(a, (hipStream_t)stream), "state space step");
 }
@@ -276,6 +287,16 @@ int kda_ssm_conv_step(const kda_ssm_dims_t* d, int conv_width, int conv_activati
     size_t need = 0;
     kda_ssm_conv_step_workspace_size(d, &need);
     KDA_TRY(check_workspace(workspace, workspace_bytes, need));
+    const int64_t state = state_bytes(a), taps = (int64_t)a.N * (conv_width - 1) * channels * e;
+    const Extent others[] = {{"xbc", xbc, a.N, c.xs * e, channels * e}, whole("conv_weight", conv_weight, channels * conv_width * 4),
+                             whole("conv_bias", conv_bias, channels * 4), dt_extent(a), whole("A", A, 4ll * a.H),
+                             whole("D", D, 4ll * a.H), whole("dt_bias", dt_bias, 4ll * a.H), y_extent(a),
+                             whole("the workspace", workspace, (int64_t)need), h_in_extent(a),
+                             whole("conv_state_in", conv_state_in == conv_state_out ? nullptr : conv_state_in, taps)};
+    KDA_TRY(check_apart("h_out", h_out, state, others, 11));
+    KDA_TRY(check_apart("conv_state_out", conv_state_out, taps, others, 11));
+    const Extent states[] = {whole("h_out", h_out, state)};
+    KDA_TRY(check_apart("conv_state_out", conv_state_out, taps, states, 1));
     float* z = static_cast<float*>(workspace);
     c.x = xbc; c.weight = conv_weight; c.bias = conv_bias; c.state_in = conv_state_in; c.state_out = conv_state_out;
     c.z = z; c.N = a.N; c.C = (int32_t)channels; c.W = conv_width; c.dtype = a.dtype;

@@ -128,7 +128,8 @@ def ssm_workspace_size(x, B, *, num_seqs: int = 1, backward: bool = False):
 
 def ssm_step(x, dt, A, B, C, h, D=None, dt_bias=None, *, softplus: bool = True, out=None, h_out=None):
     """One token per sequence: x [N, H, P], dt [N, H], B, C [N, G, K], h [N, H, K, P] fp32, updated in
-    place unless h_out is given; returns (y [N, H, P], state after)."""
+    place unless h_out is given; returns (y [N, H, P], state after).  A state that is updated in place is
+    refused (KdaError) on any other tensor of the call, as one that is given apart is."""
     lib = load_library()
     N, H, P = _rank(x, "x", 3)
     d, ref, K = _ssm_dims(x, dt, A, B, C, D, dt_bias, N, softplus)
@@ -167,7 +168,8 @@ def ssm_conv_step(xbc, conv_weight, conv_state, dt, A, h, D=None, dt_bias=None, 
     xbc [N, H P + 2 G K] holds the projections of x, B and C in this order; conv_weight
     [channels, W] and conv_bias [channels] fp32 and conv_state [N, W - 1, channels] are as for
     conv_step, h [N, H, K, P] as for ssm_step.  Both states are updated in place unless
-    conv_state_out or h_out is given.  workspace: at least ssm_conv_step_workspace_size
+    conv_state_out or h_out is given, and then refused (KdaError) on each other or another tensor of
+    the call.  workspace: at least ssm_conv_step_workspace_size
     bytes."""
     lib = load_library()
     dims = _conv_step_dims(xbc, dt, h, softplus)
