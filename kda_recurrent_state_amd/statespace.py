@@ -153,6 +153,8 @@ def _conv_step_dims(xbc, dt, h, softplus):
     N, channels = _rank(xbc, "xbc", 2)
     H, K, P = _rank(_given(h, "h"), "h", 4)[1:]
     rest = channels - H * P
+    if K < 1:
+        raise ValueError(f"h must have state rows (got {tuple(h.shape)})")
     if rest <= 0 or rest % (2 * K):
         raise ValueError(f"xbc has {channels} channels, which is not heads x width = {H} x {P} and 2 x groups x {K}")
     xs = _tokens(xbc, "xbc", xbc.dtype, (N, channels))
