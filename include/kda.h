@@ -619,7 +619,9 @@ KDA_API int kda_residual_norm_bwd_workspace_size(const kda_residual_norm_dims_t*
  *   - States, and the derivatives of dt, A, D, dt_bias and h0, are sums in fp32 of products to 2^-24.
  *     y and dx of bf16 inputs are sums in fp32 too, of terms with one factor that was rounded to bf16
  *     (masked products, the state): within 2^-8 of the sum of the terms' magnitudes; dB and dC within
- *     2^-18.  fp32 inputs are multiplied as sums of three bf16 parts, to 2^-24 of a product.
+ *     2^-18.  fp32 inputs are multiplied as sums of three bf16 parts, to 2^-24 of a product and
+ *     2^-134 of a factor, whatever their value.  Beside bf16 inputs, states, h0 and dh_T stay below
+ *     the largest bf16, 3.3895e38, in magnitude.
  *   - Inputs are finite.  A non-finite value stays in its own sequence.  It may reach outputs up to
  *     63 tokens before it, and be lost behind decays whose product is zero in float32.  A NaN in a
  *     head's A, dt_bias or D makes the results of that head NaN that read it, as in single steps.
@@ -730,7 +732,8 @@ KDA_API int kda_state_cache_read(const kda_state_cache_dims_t* dims, const void*
  *     g = x Wg^T,  u = x Wu^T,  h = act(g) u,
  * and its gradient.  Sums are fp32.  bf16 inputs are multiplied exactly; dg and du (the
  * derivatives of g and u) are rounded to bf16 before the products that take them.  float32 inputs
- * are multiplied as sums of three bf16 parts, to 2^-24 of a product.
+ * are multiplied as sums of three bf16 parts, to 2^-24 of a product and 2^-134 of a factor.  Inputs are
+ * finite, of any value: an infinity may come out as NaN.  A NaN in a token of x stays in its row of h.
  * ------------------------------------------------------------------------- */
 typedef struct {
     int64_t tokens;      /* T: 0 to 2147418112 */

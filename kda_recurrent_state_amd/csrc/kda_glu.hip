@@ -136,7 +136,7 @@ template <int NP> __device__ __forceinline__ void store_planes(bf16* p, int64_t 
         bf16x4 b;
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            b[i] = (bf16)v[i];
+            b[i] = (bf16)(NP > 1 && n == 0 ? first_part(v[i]) : v[i]);
             v[i] -= (float)b[i];
         }
         *reinterpret_cast<bf16x4*>(p + n * plane) = b;
@@ -460,7 +460,7 @@ template <> struct Direct<float> {
         for (int n = 0; n < 3; ++n)
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
-                o[n][i] = (bf16)v[i];
+                o[n][i] = (bf16)(n == 0 ? first_part(v[i]) : v[i]);
                 v[i] -= (float)o[n][i];
             }
     }

@@ -143,6 +143,10 @@ __device__ __forceinline__ int wave_find(const Seqs& sq, int t) {
     return lo;
 }
 
+// The first of several bf16 parts of a value is taken of this: a finite value above the largest bf16 would round
+// to infinity, and what it leaves for the other parts would be no number.  (What a NaN leaves is a NaN.)
+__device__ __forceinline__ float first_part(float v) { return __builtin_amdgcn_fmed3f(v, -0x1.fep127f, 0x1.fep127f); }
+
 // By the exponential and reciprocal instructions: within (|z| + 6) 2^-24 of itself.
 __device__ __forceinline__ float sigmoid_f(float z) { return __builtin_amdgcn_rcpf(1.f + __expf(-z)); }
 

@@ -61,9 +61,10 @@ __device__ __forceinline__ uint32_t pack2(float a, float b) {
 __device__ __forceinline__ float low_of(uint32_t v) { return __uint_as_float(v << 16); }
 __device__ __forceinline__ float high_of(uint32_t v) { return __uint_as_float(v & 0xffff0000u); }
 
-// The sum of N bf16 parts that stands for v.
+// The sum of N bf16 parts that stands for v.  WIDE: v may be above the largest bf16 (fp32 inputs, and what is formed of
+// them; with bf16 inputs the 16 values a lane that a chunk's update splits cost 1.3 % of the long forward).
 template <int N> struct Parts { bf16x8 p[N]; };
-template <int N> __device__ __forceinline__ Parts<N> split8(const float (&in)[8]) {
+template <int N, bool WIDE> __device__ __forceinline__ Parts<N> split8(const float (&in)[8]) {
     typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
     Parts<N> o;
     float v[8];
@@ -74,7 +75,7 @@ template <int N> __device__ __forceinline__ Parts<N> split8(const float (&in)[8]
         u32x4 w;
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            w[i] = pack2(v[2 * i], v[2 * i + 1]);
+            w[i] = WIDE && n == 0 ? pack2(first_part(v[2 * i]), first_part(v[2 * i + 1])) : pack2(v[2 * i], v[2 * i + 1]);
             if (n + 1 < N) {
                 v[2 * i] -= low_of(w[i]);
                 v[2 * i + 1] -= high_of(w[i]);
@@ -83,6 +84,13 @@ template <int N> __device__ __forceinline__ Parts<N> split8(const float (&in)[8]
         o.p[n] = __builtin_bit_cast(bf16x8, w);
     }
     return o;
+}
+
+// Part m of four values.
+template <bool WIDE> __device__ __forceinline__ void pack4(const float (&v)[4], int m, uint32_t& a, uint32_t& b) {
+    const bool first = WIDE && m == 0;
+    a = first ? pack2(first_part(v[0]), first_part(v[1])) : pack2(v[0], v[1]);
+    b = first ? pack2(first_part(v[2]), first_part(v[3])) : pack2(v[2], v[3]);
 }
 
 // acc += A B over the parts of both, without the products below 2^-24.
@@ -181,7 +189,7 @@ template <typename DT, int ROWS, int COLS, int THREADS> struct Stage {
             } else {
                 float f[8];
                 get_v(v[i], f);
-                const Parts<NP> s = split8<NP>(f);
+                const Parts<NP> s = split8<NP, true>(f);
 #pragma unroll
                 for (int n = 0; n < NP; ++n) *reinterpret_cast<bf16x8*>(p + n * plane) = s.p[n];
             }
@@ -199,7 +207,7 @@ template <typename DT, int ROWS, int COLS, int THREADS> struct Stage {
             } else {
                 float f[8];
                 get_v(v[i], f);
-                const Parts<NP> s = split8<NP>(f);
+                const Parts<NP> s = split8<NP, true>(f);
 #pragma unroll
                 for (int n = 0; n < NP; ++n) *reinterpret_cast<bf16x8*>(p + n * plane) = s.p[n];
             }
@@ -218,7 +226,7 @@ template <typename DT, int ROWS, int COLS, int THREADS> struct Stage {
             } else {
                 float f[8];
                 get_v(v[i], f);
-                s = split8<NP>(f);
+                s = split8<NP, true>(f);
             }
 #pragma unroll
             for (int n = 0; n < NP; ++n) {
@@ -681,7 +689,8 @@ __device__ __forceinline__ void walk_segment(const SsmArgs& a, const Role& role,
                     char* to = sm + t * (Q * 2) + ((q4 ^ ((t >> 1) & 3)) * 16) + I[x] * 8;
 #pragma unroll
                     for (int m = 0; m < MP; ++m) {
-                        const uint32_t a0 = pack2(v[0], v[1]), a1 = pack2(v[2], v[3]);
+                        uint32_t a0, a1;
+                        pack4<(NP > 1)>(v, m, a0, a1);
                         *reinterpret_cast<uint2*>(to + m * PLM) = make_uint2(a0, a1);
                         v[0] -= low_of(a0);
                         v[1] -= high_of(a0);
@@ -706,7 +715,7 @@ __device__ __forceinline__ void walk_segment(const SsmArgs& a, const Role& role,
                             v[r] = st[2 * kk][p][r];
                             v[4 + r] = st[2 * kk + 1][p][r];
                         }
-                        const Parts<HP> hf = split8<HP>(v);
+                        const Parts<HP> hf = split8<HP, (NP > 1)>(v);
 #pragma unroll
                         for (int j = 0; j < 2; ++j) acc[j][p] = mma_parts(hf, qf[j], kk ? acc[j][p] : zero4());
                     }
@@ -780,7 +789,7 @@ __device__ __forceinline__ void walk_segment(const SsmArgs& a, const Role& role,
                     for (int m = NP - 2; m >= 0; --m) v[r] += (float)vf[p].p[m][r];
                     v[r] *= r < 4 ? w0[r] : w1[r - 4];
                 }
-                xf[p] = split8<3>(v);
+                xf[p] = split8<3, (NP > 1)>(v);
             }
             // products that add to one tile wait for each other: two tiles' rows side by side, a part at a time
 #pragma unroll
@@ -1104,7 +1113,8 @@ __global__ void __launch_bounds__(NT, 2) ssm_grad_kernel(SsmArgs a, int slots, i
             if (l15 < 4) sum.col[wave][s0 + l15] = c;
 #pragma unroll
             for (int m = 0; m < MP; ++m) {
-                const uint32_t a0 = pack2(v[0], v[1]), a1 = pack2(v[2], v[3]);
+                uint32_t a0, a1;
+                pack4<(NP > 1)>(v, m, a0, a1);
                 *reinterpret_cast<uint2*>(sds + m * PLQ + t * LDQ + s0) = make_uint2(a0, a1);
                 if (m + 1 < MP) {
                     v[0] -= low_of(a0);
@@ -1139,7 +1149,7 @@ __global__ void __launch_bounds__(NT, 2) ssm_grad_kernel(SsmArgs a, int slots, i
                     get_v(gv[pp], gx);
 #pragma unroll
                     for (int r = 0; r < 8; ++r) hg += hx[r] * gx[r];
-                    hf[pp] = split8<3>(hx);
+                    hf[pp] = split8<3, (NP > 1)>(hx);
                 }
                 // sums over the wavefront's columns go to its own row: lane n of 4 holds row n's
                 auto add = [&](float (&to)[Q], int t, f32x4 v) {
@@ -1171,7 +1181,7 @@ __global__ void __launch_bounds__(NT, 2) ssm_grad_kernel(SsmArgs a, int slots, i
                 for (int pp = 0; pp < PT / 2; ++pp) {
                     float gx[8];
                     get_v(gv[pp], gx);
-                    gf[pp] = split8<3>(gx);
+                    gf[pp] = split8<3, (NP > 1)>(gx);
                 }
                 if (k + 1 < KW) states(k + 1);
 #pragma unroll
