@@ -555,9 +555,15 @@ __all__ += block.__all__
 # the selective state space scan
 from . import statespace  # noqa: E402
 from .statespace import *  # noqa: E402,F401,F403
+
+__all__ += statespace.__all__
 # states kept in 8 bits
 from . import state_cache  # noqa: E402
 from .state_cache import *  # noqa: E402,F401,F403
+
+__all__ += state_cache.__all__
 # the gated half of a feed-forward block
 from . import feedforward  # noqa: E402
 from .feedforward import *  # noqa: E402,F401,F403
+
+__all__ += feedforward.__all__
