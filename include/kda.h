@@ -648,8 +648,9 @@ typedef struct {
  *   h_T        [N, H, K, P] float32 final states, or NULL to skip (an empty sequence's is its h0); not h0
  *   workspace  kda_ssm_workspace_size bytes (0: may be NULL).  Calls that share a workspace
  *              must be ordered on one stream.
- * Refused, as larger than one launch: more than 2^24 workgroups, which takes millions of
- * sequences or chunks of tokens.
+ * Refused, as larger than one launch: more than 2^24 workgroups.  The walk has one for four blocks of 32
+ * columns (16 where state > 128) of a group's heads, for every sequence and every segment of a long
+ * one, the gradient two: half a million sequences of 32 heads of 128 columns, and half of that.
  */
 KDA_API int kda_ssm_fwd(const kda_ssm_dims_t* dims, const void* x, const float* dt, const float* A, const void* B,
                         const void* C, const float* D, const float* dt_bias, const float* h0,

@@ -5,7 +5,9 @@
 //
 // bf16 operands are read where they lie.  fp32 operands are first split into three bf16 planes whose sum they
 // are (24 bits), and the product runs over the six pairs of planes above 2^-24, smallest first, into
-// the same accumulators: about four times the rate that fp32 matrix instructions would have.
+// the same accumulators.  Six products at the peak of 2.5 PFLOP/s are 2.7 times the fp32 matrix instructions' 157 TFLOP/s;
+// measured are 94 TFLOP/s of fp32 products at 777 x 1000 x 2731, where a library's fp32 product makes 74, and 149 at
+// 1024 x 4096 x 10240 for the library's 144.
 #include "kda_glu.hpp"
 
 #include "kda_rows.hpp"
@@ -181,6 +183,9 @@ enum { EPI_OUT, EPI_H, EPI_DGU };
 // What bounds it, 16384 x 4096 x 10240 bf16 (2.75 TFLOP, one tile of 256 x 256 a compute unit): 2180 us, 1260 TFLOP/s, where
 // the matrix pipes alone take 1092 (168e6 instructions of 16 cycles on 1024 SIMDs at 2.4 GHz), vector issue 426 and LDS 410; a
 // library product of these sizes runs at 1563.  The rest is the wait for a stage: 64 KB for 512 cycles of products.
+// Two library products in bf16 and an elementwise tail (or one product over both weights), us, against this: 128 tokens
+// of 4096 x 10240 70 (54), 68; 512 115 (94), 136; 1024 170 (175), 196; 2048 329 (418), 323; 8192 1043 (1064), 1089;
+// 16384 2048 (2122), 2164.
 // With fp32 the same loop runs over six pairs of planes: 777 x 1000 x 2731 91 us forward, 560 TFLOP/s of bf16 products, 94 of
 // fp32 ones; 301 tiles of 128 on 256 compute units, two to some of them.
 template <typename DT, int BM, int BN, int BK, int WM, int WN, int STAGES, bool AKR, bool BKR, int EPI, int ACT>
@@ -444,6 +449,8 @@ template <typename DT, int ACT> __global__ void __launch_bounds__(256) glu_saved
 // ---------------------------------------------------------------- few tokens
 //
 // Few tokens: the weights are what there is to read.  4 tokens of 4096 x 10240 bf16: 168 MB in 34.5 us, 4.9 TB/s.
+// fp32, 336 MB: 92 us up to 16 tokens, 3.7 TB/s, and 198 for 64 (two library products and a tail: 76 and 134); x is
+// split into its parts again by every workgroup, and its products are six.
 // A workgroup takes 16 columns of both weights, its wavefronts a part of the sum each; weights come straight from
 // memory into the operand's registers, x from the cache.
 template <typename DT> struct Direct;
@@ -574,6 +581,10 @@ Shape shape_of(int64_t M, int64_t N, bool dual, int halves, int steps, bool may_
     s.mt = (int)((M + bm - 1) / bm);
     s.nt = (int)((N + (dual ? bn / 2 : bn) - 1) / (dual ? bn / 2 : bn));
     s.split = 1;
+    // Shares of the sum: two workgroups for every compute unit, rounded up, none shorter than 16 steps.  Whole, this way
+    // and rounded down (one round of workgroups at most), us: 777 x 1000 x 2731 fp32, dx in 56 tiles 397, 97, 65, dW in 352 107,
+    // 110, 107; bf16 70, 29, 23 and 35, 35, 35; 1024 x 1024 x 2816 bf16, 64 tiles 74, 26, 26, 352 34, 43, 33; 2048
+    // tokens, 128 tiles 73, 36, 35, 352 54, 62, 53; 4096 x 512 x 1408 fp32, 128 tiles 212, 77, 79, 88 334, 154, 119.
     if (may_split && !s.big) {
         const int64_t t = tiles(bm, bn) > 0 ? tiles(bm, bn) : 1, want = (512 + t - 1) / t, most = steps / 16 > 0 ? steps / 16 : 1;
         s.split = (int)(want < most ? want : most);
@@ -644,7 +655,8 @@ Shape dw_shape(const GluArgs& a) {
 // Few tokens or tiles.  Inputs that tiles can read as they lie: tiles from 33 tokens on, where there are 96 of
 // them.  bf16 forward of 33 and 64 tokens, few or tiles, us: 4096 x 10240 56, 68 or 45, 46; 2048 x 8192 26, 30 or 25, 25; 4096 x
 // 5632 41, 47 or 43, 44; 2048 x 2816 15, 17 or 21, 21.  Others are packed for tiles, and fp32 has six products:
-// 64 tokens 1000 x 2731 bf16 10 or 28, fp32 23 or 81; 4096 x 10240 fp32 191 or 508.
+// 64 tokens 1000 x 2731 bf16 10 or 28, fp32 23 or 81; 4096 x 10240 fp32 191 or 508.  (Weights in the last-level cache; read
+// from memory, bf16: 4096 x 10240 65, 75 or 65, 66; 2048 x 8192 31, 35 or 34, 35.)
 bool is_few(const GluArgs& a) {
     return a.T <= (a.x_plain && a.w_plain && a.F > 95 * 64 ? GLU_FEW / 2 : GLU_FEW);
 }

@@ -13,7 +13,8 @@
 //
 // Exponents: c_t - c_s is the difference of two sums that may be large while it is small, so the
 // sums are formed in fp64 and held as a multiple of 2^-8 and a rest; both differences are exact or
-// nearly so.  No exponent is positive, so nothing overflows whatever the decay; l is held above
+// nearly so.  (As single fp32 numbers, up to 9600 in a chunk, they put up to 2^-10 ln 2 on a weight; the second part
+// is 2 us of the 750 of 2 x 32768 tokens.)  No exponent is positive, so nothing overflows whatever the decay; l is held above
 // -300, below which 2^l is zero for every state that fp32 holds.
 //
 // Matrix cores take bf16 operands.  bf16 inputs go in as they are; what is computed in fp32 and is an operand again goes in as
