@@ -30,8 +30,8 @@
 //
 // Per call: the segments' own states (ENDS), their join, and the walk proper.  The gradient does this in both directions side by
 // side, forwards for the states before every chunk (EMIT) and backwards for dx and the derivatives behind every
-// chunk, and then has a kernel over chunks for what needs both.  2 x 32768 tokens of 32 heads of 128 x 128, bf16: 735 us (ENDS
-// 185, join 18, OUT 535); gradient of 2 x 8192: 1025 us (below).
+// chunk, and then has a kernel over chunks for what needs both.  2 x 32768 tokens of 32 heads of 128 x 128, bf16: 735 to 753 us
+// by the card (at 735 ENDS 185, join 18, OUT 535); gradient of 2 x 8192: 1025 us (below).
 #include "kda_ssm.hpp"
 
 #include "kda_rows.hpp"
