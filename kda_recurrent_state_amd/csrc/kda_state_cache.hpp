@@ -23,8 +23,9 @@ hipError_t launch_state_cache(const StateCacheArgs& a, bool write, hipStream_t s
 // The quotient x / s, s > 0, as a number on the same side of every border between two codes.  The division is correctly
 // rounded to fp32; where it lands on a border without being one, the sign of the remainder says which side x / s is on.
 // (Every border has at most 12 significant bits, so a quotient with more is none; nor is zero, to which a quotient
-// below the least fp32 number is rounded.)  A remainder can be 2^-22 of the scale (a step of s times half a code), which a
-// small scale would leave below fp32's range: it and x, at most 448 of it, are moved up by a power of two.
+// below the least fp32 number is rounded.)  At a border a remainder is a multiple of the last place of s times that of the
+// border, 2^-33 of the scale at the least, which a small scale would leave below fp32's range: both are moved up by a
+// power of two (x is at most some hundred scales).
 __host__ __device__ inline float beside_border(float x, float s) {
     const float up = s < 0x1p-60f ? 0x1p64f : 1.f;
     x *= up;
